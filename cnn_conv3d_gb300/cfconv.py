@@ -25,6 +25,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 CF_OK, CF_ERR_INVALID_ARG, CF_ERR_UNSUPPORTED, CF_ERR_WORKSPACE, CF_ERR_CUDA, CF_ERR_TIMEOUT = range(6)
 CF_OP_FWD, CF_OP_DGRAD, CF_OP_WGRAD, CF_OP_DGRAD_ROUTED, CF_OP_WGRAD_ROUTED, CF_OP_POOL_BWD, CF_OP_BN = range(7)
 CF_POOL_MAX, CF_POOL_AVG, CF_POOL_NONE = range(3)
+CF_ACT_LRELU, CF_ACT_SILU = range(2)
+CF_DT_BF16, CF_DT_F32 = range(2)
 
 
 class cf_conv_desc(ctypes.Structure):
@@ -37,6 +39,30 @@ class cf_pool_epi(ctypes.Structure):
                 ("pool", ctypes.c_int32)]
 
 
+class cf_gn_desc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("d", ctypes.c_int64), ("h", ctypes.c_int64), ("w", ctypes.c_int64),
+                ("c", ctypes.c_int32), ("groups", ctypes.c_int32), ("pool", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("slope", ctypes.c_float), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("x_pitch", ctypes.c_int64), ("y_pitch", ctypes.c_int64)]
+
+
+class cf_ns_desc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class cf_muon_param(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("w_bf16", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+class cf_muon_hyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("nesterov", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float),
+                ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class CfError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {cf_status_string(status)} ({status})")
@@ -46,6 +72,7 @@ class CfError(RuntimeError):
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _DP = ctypes.POINTER(cf_conv_desc)
 _EP = ctypes.POINTER(cf_pool_epi)
+_GP, _NP, _MP, _HP = (ctypes.POINTER(t) for t in (cf_gn_desc, cf_ns_desc, cf_muon_param, cf_muon_hyper))
 
 _SIGS = {
     "cf_conv3d_fwd": ([_DP, _vp, _vp, _EP, _vp, _vp, _sz, _vp], ctypes.c_int),
@@ -76,6 +103,13 @@ _SIGS = {
                   ctypes.c_int),
     "cf_mse": ([_i64, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
     "cf_adam_step": ([_i64, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _f32, _i64, _vp], ctypes.c_int),
+    "cf_group_norm_workspace_size": ([_GP, _i32], _sz),
+    "cf_group_norm_fwd": ([_GP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_group_norm_bwd": ([_GP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_orthogonalize_workspace_size": ([_NP], _sz),
+    "cf_orthogonalize": ([_NP, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_muon_workspace_size": ([_i32, _MP], _sz),
+    "cf_muon_step": ([_i32, _MP, _HP, _vp, _sz, _vp], ctypes.c_int),
     "cf_workspace_size": ([ctypes.c_int, _DP], _sz),
     "cf_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "cf_last_device_status": ([_vp], ctypes.c_int),
@@ -267,6 +301,52 @@ def cf_adam_step(count, w, w_bf16, g, m, v, lr, beta1, beta2, eps, t, stream=Non
     st = _lib.cf_adam_step(count, _ptr(w), _ptr(w_bf16), _ptr(g), _ptr(m), _ptr(v), float(lr), float(beta1),
                            float(beta2), float(eps), int(t), _stream(stream))
     return _check(st, "cf_adam_step") if check else st
+
+
+def cf_group_norm_workspace_size(desc, backward) -> int:
+    return _lib.cf_group_norm_workspace_size(desc, int(backward))
+
+
+def cf_group_norm_fwd(desc, x, gamma, beta, y, mean, rstd, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_group_norm_fwd(desc, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws),
+                                ws_bytes, _stream(stream))
+    return _check(st, "cf_group_norm_fwd") if check else st
+
+
+def cf_group_norm_bwd(desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, ws=None, ws_bytes=0, stream=None,
+                      check=True):
+    st = _lib.cf_group_norm_bwd(desc, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dx),
+                                _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_group_norm_bwd") if check else st
+
+
+def cf_orthogonalize_workspace_size(desc) -> int:
+    return _lib.cf_orthogonalize_workspace_size(desc)
+
+
+def cf_orthogonalize(desc, g, o, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_orthogonalize(desc, _ptr(g), _ptr(o), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_orthogonalize") if check else st
+
+
+def cf_muon_params(entries):
+    """The array of cf_muon_param for entries (w, w_bf16 or None, g, m, scale); a filter of more than two axes is
+    the matrix of its first axis by the rest.  The array holds addresses: keep the tensors."""
+    out = (cf_muon_param * len(entries))()
+    for p, (w, w16, g, m, scale) in zip(out, entries):
+        rows = w.shape[0]
+        p.w, p.w_bf16, p.g, p.m = _ptr(w), _ptr(w16), _ptr(g), _ptr(m)
+        p.rows, p.cols, p.scale = rows, w.numel() // rows, float(scale)
+    return out
+
+
+def cf_muon_workspace_size(params) -> int:
+    return _lib.cf_muon_workspace_size(len(params), params)
+
+
+def cf_muon_step(params, hyper, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_muon_step(len(params), params, hyper, _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_muon_step") if check else st
 
 
 def cf_last_device_status(stream=None) -> int:

@@ -342,6 +342,114 @@ cf_status cf_adam_step(int64_t count, float* w, uint16_t* w_bf16, const float* g
                        float beta1, float beta2, float eps, int64_t t, void* stream);
 
 /*
+ * Group normalisation between the conv and the activation, channels last, for
+ * volumes whose batch is too small for batch statistics.  Per sample and group
+ * of c/groups channels, over all its voxels (M = d*h*w*c/groups values, biased
+ * variance):
+ *   mean = sum x / M,  rstd = 1 / sqrt(sum (x - mean)^2 / M + eps)
+ *   u = gamma rstd (x - mean) + beta
+ *   y = act(u); pooled: MAX act(first maximum of u over the 2x2x2 window),
+ *       AVG mean of act(u) over the window
+ *   act: LReLU(slope) (slope 1: none, 0: ReLU) or SiLU u / (1 + exp(-u))
+ * Backward, from dy at y's shape and the forward's mean and rstd, with u
+ * recomputed from x (nothing else is stored): du = act'(u) times dy (MAX: at
+ * the window's first maximum in (dd, dh, dw) order, 0 elsewhere; AVG: dy / 8),
+ * xh = (x - mean) rstd, and
+ *   dbeta = sum du,  dgamma = sum du xh            (over n and voxels)
+ *   dx = rstd (gamma du - sum_g(gamma du) / M - xh sum_g(gamma du xh) / M)
+ * LReLU'(0) = slope.  Statistics and sums are fp32 or wider, in an order fixed
+ * by the sizes; u in fp32, y and dx rounded once.
+ *   x, dx : [n][d][h][w] voxels of c values, x_pitch values apart (0: c), so
+ *           that a slice of a wider tensor's channels is taken and written in
+ *           place; y, dy likewise with y_pitch, d/2, h/2, w/2 when pooled.
+ *           bf16 (CF_DT_BF16) or fp32 (CF_DT_F32; unpooled only).
+ *   gamma, beta, dgamma, dbeta [c], mean, rstd [n][groups] fp32.
+ *           gamma NULL is 1, beta NULL is 0; mean and rstd may be NULL in the
+ *           forward (inference), dgamma and dbeta in the backward, dx too.
+ * dx must not overlap x or dy.  Supported: any c that groups divides; d, h, w
+ * even when pooled; MAX with LReLU of slope >= 0.
+ * Workspace: cf_group_norm_workspace_size(desc, 0 forward / 1 backward).
+ */
+enum { CF_ACT_LRELU = 0, CF_ACT_SILU = 1 };
+enum { CF_DT_BF16 = 0, CF_DT_F32 = 1 };
+
+typedef struct {
+    int64_t n, d, h, w;       /* sizes of x */
+    int32_t c, groups;
+    int32_t pool;             /* CF_POOL_* */
+    int32_t act;              /* CF_ACT_* */
+    float slope;              /* of CF_ACT_LRELU */
+    float eps;
+    int32_t dtype;            /* CF_DT_* of x, y, dy, dx */
+    int64_t x_pitch, y_pitch; /* values from a voxel to the next; 0 = c */
+} cf_gn_desc;
+
+size_t cf_group_norm_workspace_size(const cf_gn_desc* desc, int32_t backward);
+cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* gamma, const float* beta, void* y,
+                            float* mean, float* rstd, void* ws, size_t ws_bytes, void* stream);
+cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* gamma, const float* beta,
+                            const float* mean, const float* rstd, const void* dy, void* dx, float* dgamma,
+                            float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Orthogonalised updates.  cf_orthogonalize takes `batch` matrices u of
+ * rows x cols and writes, for each, the Newton-Schulz iterate that drives its
+ * singular values towards 1: with X the matrix (transposed when rows > cols),
+ *   X = u / (|u|_F + eps);  `steps` times: A = X X^T, X = a X + (b A + c A A) X
+ * a polynomial of the singular values, so a zero matrix gives zero.  The usual
+ * coefficients are (3.4445, -4.7750, 2.0315) with 5 steps: values in about
+ * [0.7, 1.2].
+ *   g : [batch][rows][cols] bf16 or fp32 (dtype), o : [batch][rows][cols] bf16.
+ * Products take fp16 operands (11 bits) with fp32 sums, X is carried between
+ * steps in 32 bits, and what the diagonals of A and of the polynomial share is
+ * kept out of the rounding: |o - exact| is about 1e-3 |exact| in the Frobenius
+ * norm before the rounding to bf16.  A matrix with an entry that is not finite
+ * gives NaN throughout.
+ * Supported: 1 <= steps <= 16; rows, cols up to 65536.
+ *
+ * cf_muon_step applies one step of momentum with orthogonalised updates to
+ * `count` weight matrices (a conv filter is the matrix [c_out][27 c_in]):
+ *   m = momentum m + g;  u = nesterov ? g + momentum m : m
+ *   w = (1 - lr weight_decay) w - lr scale O(u);  w_bf16 = w rounded (or NULL)
+ * w, g, m fp32 [rows][cols], caller-owned device tensors; m is updated in
+ * place and starts at zero.  params is a host array, read during the call;
+ * tensors of different entries must not overlap.  count 0 does nothing.
+ * Workspaces: cf_orthogonalize_workspace_size, cf_muon_workspace_size (0 for
+ * arguments the call would refuse).
+ */
+typedef struct {
+    int64_t batch, rows, cols;
+    int32_t dtype; /* CF_DT_* of g */
+    int32_t steps;
+    float a, b, c;
+    float eps;
+} cf_ns_desc;
+
+typedef struct {
+    float* w;
+    uint16_t* w_bf16;
+    const float* g;
+    float* m;
+    int64_t rows, cols;
+    float scale;
+} cf_muon_param;
+
+typedef struct {
+    float lr, momentum, weight_decay;
+    int32_t nesterov;
+    int32_t steps;
+    float a, b, c;
+    float eps;
+} cf_muon_hyper;
+
+size_t cf_orthogonalize_workspace_size(const cf_ns_desc* desc);
+cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, void* ws, size_t ws_bytes,
+                           void* stream);
+size_t cf_muon_workspace_size(int32_t count, const cf_muon_param* params);
+cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon_hyper* hyper, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
  * cf_bias_lrelu_pool_bwd without a workspace argument, for callers that
  * cannot allocate device memory (for example an operator plugged into a host
  * framework that owns all device allocations and hands its plug-ins neither

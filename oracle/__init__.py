@@ -621,3 +621,115 @@ def adam_step(w, g, m, v, lr, t, beta1=0.9, beta2=0.999, eps=1e-8):
 def linear_decay_lr(lr0, step, total_steps, final_frac=0.01):
     """Linear decay from lr0 to final_frac * lr0 over total_steps, then constant."""
     return lr0 * (1.0 - (1.0 - final_frac) * min(step / total_steps, 1.0))
+
+
+# ----------------------------------------------------------------------------
+# Group normalisation (channels last) with the block's activation and pooling,
+# and orthogonalised updates with momentum.
+
+def _act(u, act, slope):
+    return u / (1.0 + np.exp(-u)) if act == "silu" else np.where(u > 0, u, slope * u)
+
+
+def _act_grad(u, act, slope):
+    if act == "silu":
+        s = 1.0 / (1.0 + np.exp(-u))
+        return s * (1.0 + u * (1.0 - s))
+    return np.where(u > 0, 1.0, slope)
+
+
+def _to_windows(t):
+    """[N, D, H, W, C] -> [N, D/2, H/2, W/2, 8, C], a window's voxels in (dd, dh, dw) order."""
+    n, d, h, w, c = t.shape
+    t = t.reshape(n, d // 2, 2, h // 2, 2, w // 2, 2, c).transpose(0, 1, 3, 5, 2, 4, 6, 7)
+    return t.reshape(n, d // 2, h // 2, w // 2, 8, c)
+
+
+def _from_windows(t):
+    n, d, h, w, _, c = t.shape
+    t = t.reshape(n, d, h, w, 2, 2, 2, c).transpose(0, 1, 4, 2, 5, 3, 6, 7)
+    return t.reshape(n, 2 * d, 2 * h, 2 * w, c)
+
+
+def group_norm_stats(x, groups, eps=1e-5):
+    """(mean, rstd), each [N, groups]: biased variance over a sample's voxels and a group's channels."""
+    x = _f64(x)
+    g = x.reshape(x.shape[0], -1, groups, x.shape[-1] // groups)
+    mean = g.mean(axis=(1, 3))
+    var = ((g - mean[:, None, :, None]) ** 2).mean(axis=(1, 3))
+    return mean, 1.0 / np.sqrt(var + eps)
+
+
+def _per_channel(t, c):
+    return np.repeat(t, c // t.shape[1], axis=1)[:, None, None, None, :]
+
+
+def group_norm_pre(x, gamma, beta, mean, rstd):
+    """u, the normalised and scaled x, and xh, the normalised x."""
+    x = _f64(x)
+    xh = (x - _per_channel(mean, x.shape[-1])) * _per_channel(rstd, x.shape[-1])
+    return xh * gamma + beta, xh
+
+
+def group_norm_fwd(x, gamma, beta, groups, pool="none", act="lrelu", slope=0.3, eps=1e-5):
+    """(y, mean, rstd) of x [N, D, H, W, C]; pool "none", "max" (of the normalised values, then the activation) or "avg"
+    (of the activated values) over 2x2x2 windows."""
+    mean, rstd = group_norm_stats(x, groups, eps)
+    u, _ = group_norm_pre(x, gamma, beta, mean, rstd)
+    if pool == "max":
+        return _act(_to_windows(u).max(axis=4), act, slope), mean, rstd
+    y = _act(u, act, slope)
+    return (_to_windows(y).mean(axis=4) if pool == "avg" else y), mean, rstd
+
+
+def group_norm_du(u, dy, pool, act, slope):
+    """The gradient at u of the activation and pooling."""
+    if pool == "max":
+        win = _to_windows(u)
+        first = np.argmax(win, axis=4)  # numpy's argmax is the first maximum
+        du = np.zeros_like(win)
+        top = np.take_along_axis(win, first[..., None, :], 4)
+        np.put_along_axis(du, first[..., None, :], _f64(dy)[..., None, :] * _act_grad(top, act, slope), 4)
+        return _from_windows(du)
+    if pool == "avg":
+        dy = _from_windows(np.repeat(_f64(dy)[..., None, :], 8, axis=4)) / 8.0
+    return _f64(dy) * _act_grad(u, act, slope)
+
+
+def group_norm_bwd(x, gamma, beta, groups, dy, pool="none", act="lrelu", slope=0.3, eps=1e-5, stats=None):
+    """(dx, dgamma, dbeta) of group_norm_fwd; stats: (mean, rstd) to use in place of x's own."""
+    x = _f64(x)
+    n, c = x.shape[0], x.shape[-1]
+    mean, rstd = stats if stats is not None else group_norm_stats(x, groups, eps)
+    u, xh = group_norm_pre(x, gamma, beta, mean, rstd)
+    du = group_norm_du(u, dy, pool, act, slope)
+
+    def group_mean(t):
+        return _per_channel(t.reshape(n, -1, groups, c // groups).mean(axis=(1, 3)), c)
+
+    gdu = gamma * du
+    dx = _per_channel(rstd, c) * (gdu - group_mean(gdu) - xh * group_mean(gdu * xh))
+    return dx, (du * xh).sum(axis=(0, 1, 2, 3)), du.sum(axis=(0, 1, 2, 3))
+
+
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(g, steps=5, coef=NS_COEFFICIENTS, eps=1e-7):
+    """X after `steps` of X = a X + (b A + c A A) X, A = X X^T, from X = g / (|g|_F + eps), in the smaller orientation."""
+    g = _f64(g)
+    a, b, c = coef
+    x = g.T if g.shape[0] > g.shape[1] else g
+    x = x / (np.linalg.norm(x) + eps)
+    for _ in range(steps):
+        gram = x @ x.T
+        x = a * x + (b * gram + c * gram @ gram) @ x
+    return x.T if g.shape[0] > g.shape[1] else x
+
+
+def muon_step(w, g, m, lr, scale, momentum=0.95, nesterov=True, weight_decay=0.0, steps=5, coef=NS_COEFFICIENTS, eps=1e-7):
+    """One momentum step with the orthogonalised update; returns (w, m)."""
+    w, g, m = _f64(w), _f64(g), _f64(m)
+    m = momentum * m + g
+    u = g + momentum * m if nesterov else m
+    return w * (1.0 - lr * weight_decay) - lr * scale * newton_schulz(u, steps, coef, eps), m

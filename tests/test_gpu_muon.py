@@ -1,0 +1,250 @@
+"""Orthogonalisation and the momentum step through the C ABI against the 64-bit oracle.
+
+Tolerance of an orthogonalised matrix, in the Frobenius norm relative to the result: each of the five steps rounds operands to
+11 bits (2^-12 of a value) and a step passes an error on with at most the polynomial's slope 3.45, three roundings a step that
+add in squares over the steps: sqrt(3 * 5) * 3.45 * 2^-12 = 3.3e-3.  A bf16 output adds 2^-9 / sqrt(3) * sqrt(2): 1.6e-3.
+Together at most 5e-3.  An fp32 weight is off by its own rounding and by 3.3e-3 of the update."""
+import numpy as np
+import pytest
+
+from tests.gpu_util import guarded
+
+pytestmark = pytest.mark.gpu
+
+NS_TOL, OUT_TOL = 3.3e-3, 5e-3
+
+
+@pytest.fixture(scope="module")
+def cf():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from cnn_conv3d_gb300 import build
+    build.build()
+    from cnn_conv3d_gb300 import cfconv
+    return cfconv
+
+
+def _f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _matrix(rng, shape, kind):
+    g = rng.normal(size=shape)
+    r = min(min(shape), 16)
+    if kind == "directions":  # few directions and noise, as a gradient summed over voxels
+        g = 0.1 * g + rng.normal(size=(shape[0], r)) @ rng.normal(size=(r, shape[1])) / r
+    elif kind == "decay":  # singular values over four decades
+        u, _, vt = np.linalg.svd(g, full_matrices=False)
+        g = (u * np.logspace(0, -4, min(shape))) @ vt
+    return g
+
+
+def _orth(cf, g, dtype, steps=5, coef=None, eps=1e-7):
+    import torch
+    a, b, c = coef or (3.4445, -4.7750, 2.0315)
+    batch, rows, cols = g.shape
+    t = torch.from_numpy(np.asarray(g, np.float32)).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    desc = cf.cf_ns_desc(batch, rows, cols, cf.CF_DT_BF16 if dtype == "bf16" else cf.CF_DT_F32, steps, a, b, c, eps)
+    size = cf.cf_orthogonalize_workspace_size(desc)
+    assert size > 0
+    o, check = guarded(g.shape, torch.bfloat16, fill=9.0)
+    ws, check_ws = guarded((size,), torch.uint8, fill=0xFF)
+    cf.cf_orthogonalize(desc, t, o, ws, size)
+    torch.cuda.synchronize()
+    check("o")
+    check_ws("workspace")
+    assert cf.cf_last_device_status() == cf.CF_OK
+    return _f64(o), _f64(t)
+
+
+def _check(oracle, o, g, tol=OUT_TOL, **kw):
+    for i in range(len(g)):
+        ref = oracle.newton_schulz(g[i], **kw)
+        assert np.all(np.isfinite(o[i]))
+        rel = np.linalg.norm(o[i] - ref) / np.linalg.norm(ref)
+        assert rel <= tol, (i, rel)
+
+
+SHAPES = [(1, 1), (1, 7), (9, 1), (2, 2), (5, 3), (8, 8), (16, 108), (27, 16), (32, 432), (63, 65), (64, 864), (100, 37), (127, 129),
+          (128, 128), (128, 1728), (129, 300), (130, 4000), (200, 256), (256, 108), (256, 3456), (257, 255), (300, 17), (384, 1000),
+          (512, 512), (1000, 333), (640, 2049), (3, 9001)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("kind,dtype", [("normal", "f32"), ("directions", "bf16"), ("decay", "f32")])
+def test_orthogonalize(cf, oracle_mod, rows, cols, kind, dtype):
+    rng = np.random.default_rng(rows * 10007 + cols)
+    o, g = _orth(cf, _matrix(rng, (rows, cols), kind)[None], dtype)
+    _check(oracle_mod, o, g)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(2, 16, 108), (3, 45, 33), (7, 65, 130), (2, 300, 257), (40, 8, 24), (5, 130, 128)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_batches(cf, oracle_mod, batch, rows, cols, dtype):
+    rng = np.random.default_rng(batch)
+    g = np.stack([_matrix(rng, (rows, cols), "directions") * 10.0 ** (i - 2) for i in range(batch)])
+    o, g = _orth(cf, g, dtype)
+    _check(oracle_mod, o, g)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 8])
+def test_steps_and_coefficients(cf, oracle_mod, steps):
+    rng = np.random.default_rng(3)
+    for shape in ((40, 200), (150, 300), (70, 30)):
+        o, g = _orth(cf, _matrix(rng, shape, "normal")[None], "f32", steps, (1.5, -0.5, 0.0))
+        _check(oracle_mod, o, g, steps=steps, coef=(1.5, -0.5, 0.0))
+
+
+def test_zero_and_extreme_scales(cf, oracle_mod):
+    rng = np.random.default_rng(4)
+    for shape in ((20, 50), (200, 400)):
+        g = np.stack([np.zeros(shape), _matrix(rng, shape, "normal") * 1e-5, _matrix(rng, shape, "normal") * 1e12])
+        o, g = _orth(cf, g, "f32")
+        assert np.all(o[0] == 0)
+        _check(oracle_mod, o[1:], g[1:])
+
+
+def test_large_matrix(cf):
+    """2048 x 4100 against 64-bit products on the GPU."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    g = torch.randn((2048, 16), device="cuda", generator=gen) @ torch.randn((16, 4100), device="cuda", generator=gen) / 16
+    g += 0.1 * torch.randn((2048, 4100), device="cuda", generator=gen)
+    desc = cf.cf_ns_desc(1, 2048, 4100, cf.CF_DT_F32, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    size = cf.cf_orthogonalize_workspace_size(desc)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    o = torch.empty((2048, 4100), dtype=torch.bfloat16, device="cuda")
+    cf.cf_orthogonalize(desc, g, o, ws, size)
+    x = g.double() / g.double().norm()
+    for _ in range(5):
+        a = x @ x.T
+        x = 3.4445 * x + (-4.7750 * a + 2.0315 * a @ a) @ x
+    assert float((o.double() - x).norm() / x.norm()) <= OUT_TOL
+    again = torch.empty_like(o)
+    cf.cf_orthogonalize(desc, g, again, ws, size)
+    torch.cuda.synchronize()
+    assert torch.equal(o, again)
+    assert cf.cf_last_device_status() == cf.CF_OK
+
+
+def test_same_bits_again_and_alone_as_in_a_batch(cf):
+    rng = np.random.default_rng(6)
+    for shape in ((33, 70), (180, 260)):
+        g = np.stack([_matrix(rng, shape, "directions") for _ in range(3)])
+        a, _ = _orth(cf, g, "f32")
+        b, _ = _orth(cf, g, "f32")
+        c, _ = _orth(cf, g[1:2], "f32")
+        assert np.array_equal(a, b) and np.array_equal(a[1], c[0])
+
+
+def test_nan_stays_in_its_matrix(cf, oracle_mod):
+    rng = np.random.default_rng(7)
+    g = np.stack([_matrix(rng, (30, 60), "normal") for _ in range(3)])
+    g[1, 3, 4] = np.nan
+    o, g = _orth(cf, g, "f32")
+    _check(oracle_mod, o[[0, 2]], g[[0, 2]])
+    assert np.all(np.isnan(o[1]))
+
+
+LISTS = [
+    [(16, 108)],
+    [(32, 108), (64, 864), (128, 1728)],
+    [(4, 256), (1, 1), (300, 200), (16, 27), (129, 131)],
+    [(256, 3456), (8, 8), (256, 108), (512, 640), (2, 900), (96, 96), (64, 576)],
+    [(5 + i, 20 + 3 * i) for i in range(40)],
+]
+
+
+@pytest.mark.parametrize("shapes", LISTS, ids=[str(len(s)) for s in LISTS])
+@pytest.mark.parametrize("nesterov,decay", [(True, 0.01), (False, 0.0)])
+def test_muon_step(cf, oracle_mod, shapes, nesterov, decay):
+    import torch
+    rng = np.random.default_rng(len(shapes))
+    lr, mu = 0.02, 0.95
+    entries, host, checks = [], [], []
+    for i, shape in enumerate(shapes):
+        w = rng.normal(size=shape) * np.sqrt(2 / shape[1])
+        m = _matrix(rng, shape, "directions")
+        g = [_matrix(rng, shape, "normal") for _ in range(2)]
+        scale = 0.2 * np.sqrt(max(shape))
+        bufs = []
+        for dt, v in ((torch.float32, w), (torch.bfloat16, w), (torch.float32, g[0]), (torch.float32, m)):
+            t, check = guarded(shape, dt)
+            t.copy_(torch.from_numpy(v))
+            bufs.append(t)
+            checks.append(check)
+        if i % 3 == 2:
+            bufs[1] = None
+        entries.append((*bufs, scale))
+        host.append([_f64(bufs[0]), _f64(bufs[3]), g, scale])
+    params = cf.cf_muon_params(entries)
+    hyper = cf.cf_muon_hyper(lr, mu, decay, int(nesterov), 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    size = cf.cf_muon_workspace_size(params)
+    ws, check = guarded((size,), torch.uint8, fill=0xFF)
+    checks.append(check)
+    for step in range(2):
+        for e, h in zip(entries, host):
+            e[2].copy_(torch.from_numpy(h[2][step]))
+        before = [(_f64(e[0]), _f64(e[3])) for e in entries]
+        cf.cf_muon_step(params, hyper, ws, size)
+        torch.cuda.synchronize()
+        assert cf.cf_last_device_status() == cf.CF_OK
+        for (w, w16, g, m, scale), (w0, m0) in zip(entries, before):
+            rw, rm = oracle_mod.muon_step(w0, _f64(g), m0, lr, scale, mu, nesterov, decay)
+            assert np.all(np.abs(_f64(m) - rm) <= 2.0 ** -22 * (np.abs(mu * m0) + np.abs(_f64(g))))
+            o = (w0 * (1 - lr * decay) - rw) / (lr * scale)
+            off = np.linalg.norm(_f64(w) - rw)
+            assert off <= NS_TOL * lr * scale * np.linalg.norm(o) + 2.0 ** -22 * np.linalg.norm(w0), (w.shape, off)
+            if w16 is not None:
+                assert torch.equal(w16, w.to(torch.bfloat16))
+    for check in checks:
+        check("a tensor of the step")
+
+
+def test_muon_in_a_cuda_graph_and_on_a_stream(cf):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    shapes = [(48, 200), (200, 300)]
+    w0 = [torch.randn(s, device="cuda", generator=gen) for s in shapes]
+    g = [torch.randn(s, device="cuda", generator=gen) for s in shapes]
+
+    def fresh():
+        return [t.clone() for t in w0], [torch.zeros_like(t) for t in w0]
+
+    hyper = cf.cf_muon_hyper(0.01, 0.9, 0.1, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    w, m = fresh()
+    params = cf.cf_muon_params([(a, None, b, c, 1.0) for a, b, c in zip(w, g, m)])
+    size = cf.cf_muon_workspace_size(params)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        cf.cf_muon_step(params, hyper, ws, size)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    w2, m2 = fresh()
+    p2 = cf.cf_muon_params([(a, None, b, c, 1.0) for a, b, c in zip(w2, g, m2)])
+    s.wait_stream(torch.cuda.current_stream())
+    cf.cf_muon_step(p2, hyper, ws, size, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cf.cf_muon_step(p2, hyper, ws, size, torch.cuda.current_stream())
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(w + m, w2 + m2):
+        assert torch.equal(a, b)
+
+
+def test_workspace_too_small(cf):
+    import torch
+    g = torch.randn((40, 50), device="cuda")
+    desc = cf.cf_ns_desc(1, 40, 50, cf.CF_DT_F32, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    size = cf.cf_orthogonalize_workspace_size(desc)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    o = torch.empty((40, 50), dtype=torch.bfloat16, device="cuda")
+    assert cf.cf_orthogonalize(desc, g, o, ws, size - 1, check=False) == cf.CF_ERR_WORKSPACE
+    params = cf.cf_muon_params([(g, None, g.clone(), g.clone(), 1.0)])
+    size = cf.cf_muon_workspace_size(params)
+    hyper = cf.cf_muon_hyper(0.01, 0.9, 0.0, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    assert cf.cf_muon_step(params, hyper, ws, size - 1, check=False) == cf.CF_ERR_WORKSPACE

@@ -1,0 +1,182 @@
+"""Pins of the 64-bit group norm, Newton-Schulz and momentum step that the GPU tests compare with, and the refusals of their
+entry points (no GPU needed).  Each pin compares with something else: closed forms, invariances, finite differences, the
+singular values."""
+import numpy as np
+import pytest
+
+import oracle
+
+
+def _case(seed, shape, groups):
+    rng = np.random.default_rng(seed)
+    c = shape[-1]
+    return rng, rng.normal(size=shape) * 2 + 0.5, rng.normal(1, 0.3, c), rng.normal(0, 0.3, c)
+
+
+def test_group_norm_normalises_each_group():
+    rng, x, _, _ = _case(1, (2, 3, 4, 5, 6), 3)
+    y, mean, rstd = oracle.group_norm_fwd(x, np.ones(6), np.zeros(6), 3, slope=1.0, eps=0.0)
+    for n in range(2):
+        for g in range(3):
+            v = y[n, ..., 2 * g:2 * g + 2]
+            assert abs(v.mean()) < 1e-12 and abs(v.var() - 1) < 1e-12
+    # shift and scale of a group's input change nothing but the statistics
+    y2, _, _ = oracle.group_norm_fwd(3 * x + 7, np.ones(6), np.zeros(6), 3, slope=1.0, eps=0.0)
+    np.testing.assert_allclose(y2, y, atol=1e-12)
+
+
+def test_group_norm_of_one_voxel_is_a_norm_over_the_channels():
+    rng, x, gamma, beta = _case(2, (3, 1, 1, 1, 8), 1)
+    y, _, _ = oracle.group_norm_fwd(x, gamma, beta, 1, slope=1.0)
+    v = x.reshape(3, 8)
+    ref = (v - v.mean(1, keepdims=True)) / np.sqrt(v.var(1, keepdims=True) + 1e-5) * gamma + beta
+    np.testing.assert_allclose(y.reshape(3, 8), ref, rtol=1e-12)
+
+
+def test_group_norm_with_a_group_per_channel_and_one_sample_is_batch_norm():
+    rng, x, gamma, beta = _case(3, (1, 3, 4, 2, 5), 5)
+    u, _, _ = oracle.bn_fwd(x, gamma, beta)
+    y, _, _ = oracle.group_norm_fwd(x, gamma, beta, 5, slope=0.3)
+    np.testing.assert_allclose(y, np.where(u > 0, u, 0.3 * u), atol=1e-12)
+
+
+@pytest.mark.parametrize("pool,act", [("none", "lrelu"), ("none", "silu"), ("max", "lrelu"), ("avg", "lrelu"), ("avg", "silu")])
+def test_group_norm_backward_by_differences(pool, act):
+    rng, x, gamma, beta = _case(4, (2, 2, 4, 2, 6), 2)
+    y, _, _ = oracle.group_norm_fwd(x, gamma, beta, 2, pool, act)
+    dy = rng.normal(size=y.shape)
+    grads = oracle.group_norm_bwd(x, gamma, beta, 2, dy, pool, act)
+
+    def loss(x, gamma, beta):
+        return (oracle.group_norm_fwd(x, gamma, beta, 2, pool, act)[0] * dy).sum()
+
+    args, h = [x, gamma, beta], 1e-6
+    for i, grad in enumerate(grads):
+        v = rng.normal(size=args[i].shape)
+        up, down = list(args), list(args)
+        up[i], down[i] = args[i] + h * v, args[i] - h * v
+        np.testing.assert_allclose((loss(*up) - loss(*down)) / (2 * h), (grad * v).sum(), rtol=1e-6, atol=1e-7)
+
+
+@pytest.mark.parametrize("shape", [(4, 9), (9, 4), (6, 6), (1, 5), (1, 1)])
+def test_newton_schulz_maps_the_singular_values(shape):
+    g = np.random.default_rng(5).normal(size=shape)
+    u, s, vt = np.linalg.svd(g, full_matrices=False)
+    t = s / (np.linalg.norm(g) + 1e-7)
+    for _ in range(5):
+        a, b, c = oracle.NS_COEFFICIENTS
+        t = a * t + b * t ** 3 + c * t ** 5
+    np.testing.assert_allclose(oracle.newton_schulz(g), (u * t) @ vt, atol=1e-10)
+    assert np.array_equal(oracle.newton_schulz(np.zeros(shape)), np.zeros(shape))
+
+
+def test_newton_schulz_is_invariant_to_scale_and_rotation():
+    rng = np.random.default_rng(6)
+    g = rng.normal(size=(5, 12))
+    q, _ = np.linalg.qr(rng.normal(size=(5, 5)))
+    np.testing.assert_allclose(oracle.newton_schulz(1e3 * g, eps=0.0), oracle.newton_schulz(g, eps=0.0), atol=1e-12)
+    np.testing.assert_allclose(oracle.newton_schulz(q @ g), q @ oracle.newton_schulz(g), atol=1e-11)
+
+
+def test_muon_step_closed_forms():
+    rng = np.random.default_rng(7)
+    w, g = rng.normal(size=(4, 7)), rng.normal(size=(4, 7))
+    w1, m1 = oracle.muon_step(w, g, np.zeros_like(w), 0.1, 2.0, momentum=0.9, nesterov=False, weight_decay=0.5)
+    np.testing.assert_allclose(m1, g)
+    np.testing.assert_allclose(w1, 0.95 * w - 0.2 * oracle.newton_schulz(g))
+    w2, m2 = oracle.muon_step(w, g, m1, 0.1, 2.0, momentum=0.9, nesterov=True)
+    np.testing.assert_allclose(m2, 1.9 * g)
+    np.testing.assert_allclose(w2, w - 0.2 * oracle.newton_schulz(g), atol=1e-7)  # any multiple of g has its update
+
+
+# ------------------------------------------------------------------------------------------------------------------ refusals
+@pytest.fixture(scope="module")
+def cf():
+    from cnn_conv3d_gb300 import build
+    build.build()
+    from cnn_conv3d_gb300 import cfconv
+    return cfconv
+
+
+def _gn(cf, **kw):
+    d = dict(n=1, d=4, h=4, w=4, c=8, groups=2, pool=cf.CF_POOL_NONE, act=cf.CF_ACT_LRELU, slope=0.3, eps=1e-5,
+             dtype=cf.CF_DT_BF16, x_pitch=0, y_pitch=0)
+    d.update(kw)
+    return cf.cf_gn_desc(*d.values())
+
+
+def test_group_norm_refusals(cf):
+    bad, un, ws = cf.CF_ERR_INVALID_ARG, cf.CF_ERR_UNSUPPORTED, cf.CF_ERR_WORKSPACE
+
+    def both(desc, x=16, y=32, stat=48):
+        f = cf.cf_group_norm_fwd(desc, x, None, None, y, None, None, check=False)
+        b = cf.cf_group_norm_bwd(desc, x, None, None, stat, stat, y, 64, None, None, check=False)
+        assert f == b
+        return f
+
+    for kw in (dict(n=0), dict(d=0), dict(c=0), dict(groups=0), dict(groups=3), dict(n=70000), dict(pool=5), dict(pool=-1),
+               dict(act=2), dict(dtype=2), dict(eps=-1.0), dict(eps=float("nan")), dict(slope=float("nan")), dict(x_pitch=7),
+               dict(y_pitch=4), dict(x_pitch=-8), dict(h=1 << 21)):
+        assert both(_gn(cf, **kw)) == bad, kw
+        assert cf.cf_group_norm_workspace_size(_gn(cf, **kw), 0) == 0
+    for kw in (dict(pool=cf.CF_POOL_MAX, d=3), dict(pool=cf.CF_POOL_AVG, w=5), dict(pool=cf.CF_POOL_MAX, dtype=cf.CF_DT_F32),
+               dict(pool=cf.CF_POOL_MAX, act=cf.CF_ACT_SILU), dict(pool=cf.CF_POOL_MAX, slope=-0.1)):
+        assert both(_gn(cf, **kw)) == un, kw
+        assert cf.cf_group_norm_workspace_size(_gn(cf, **kw), 1) == 0
+    assert both(None) == bad
+    assert both(_gn(cf), x=None) == bad and both(_gn(cf), y=None) == bad
+    assert both(_gn(cf), x=18) == bad and both(_gn(cf), y=40) == bad
+    assert cf.cf_group_norm_bwd(_gn(cf), 16, None, None, None, 16, 32, 64, None, None, check=False) == bad
+    assert cf.cf_group_norm_fwd(_gn(cf), 16, 20, None, 32, None, None, check=False) == bad
+    assert ws == 3
+
+
+def test_orthogonalize_refusals(cf):
+    def call(batch=1, rows=4, cols=8, dtype=1, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7, g=16, o=32, ws=None):
+        return cf.cf_orthogonalize(cf.cf_ns_desc(batch, rows, cols, dtype, steps, a, b, c, eps), g, o, ws, 0, check=False)
+
+    for kw in (dict(batch=0), dict(rows=0), dict(cols=-1), dict(dtype=3), dict(steps=0), dict(a=float("nan")),
+               dict(b=float("inf")), dict(eps=-1.0), dict(eps=float("nan")), dict(g=None), dict(o=None), dict(g=8), dict(o=33),
+               dict(ws=8)):
+        assert call(**kw) == cf.CF_ERR_INVALID_ARG, kw
+    assert call(rows=70000) == cf.CF_ERR_UNSUPPORTED and call(steps=17) == cf.CF_ERR_UNSUPPORTED
+    assert cf.cf_orthogonalize(None, 16, 32, check=False) == cf.CF_ERR_INVALID_ARG
+    assert call() == cf.CF_ERR_WORKSPACE
+
+
+class _Fake:
+    """Something with an address and a shape, for argument checks that launch nothing."""
+
+    def __init__(self, ptr, *shape):
+        self.ptr, self.shape = ptr, shape
+
+    def data_ptr(self):
+        return self.ptr
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+
+def test_muon_refusals(cf):
+    def entry(w=16, w16=32, g=48, m=64, shape=(4, 8), scale=1.0):
+        return (_Fake(w, *shape), w16, g, m, scale)
+
+    def hyper(lr=1e-3, mu=0.9, wd=0.0, steps=5, a=3.4):
+        return cf.cf_muon_hyper(lr, mu, wd, 1, steps, a, -4.7, 2.0, 1e-7)
+
+    def call(e, h, ws=None):
+        return cf.cf_muon_step(cf.cf_muon_params(e), h, ws, 0, check=False)
+
+    bad = cf.CF_ERR_INVALID_ARG
+    assert call([], hyper()) == cf.CF_OK
+    for e in (entry(w=0), entry(g=None), entry(m=None), entry(w=20), entry(w16=34), entry(m=65), entry(scale=float("nan"))):
+        assert call([entry(), e], hyper()) == bad
+    for h in (hyper(lr=float("nan")), hyper(mu=float("inf")), hyper(wd=float("nan")), hyper(steps=0), hyper(a=float("nan"))):
+        assert call([entry()], h) == bad
+    assert cf.cf_muon_step(cf.cf_muon_params([entry()]), None, check=False) == bad
+    assert call([entry()], hyper(), ws=4) == bad
+    assert call([entry(shape=(70000, 2))], hyper()) == cf.CF_ERR_UNSUPPORTED
+    assert call([entry()], hyper(steps=20)) == cf.CF_ERR_UNSUPPORTED
+    assert call([entry()], hyper()) == cf.CF_ERR_WORKSPACE
+    p = cf.cf_muon_params([(_Fake(16, 8, 3, 3, 3, 4), None, 48, 64, 0.5)])
+    assert (p[0].rows, p[0].cols, p[0].w_bf16, p[0].scale) == (8, 108, None, 0.5)
