@@ -8,8 +8,14 @@ beta2 0.999, eps 1e-8 and a linear learning-rate decay to 0.01x).
 Python only owns buffers (torch allocations) and enqueues library calls; every
 arithmetic step runs in libcfconv3d's kernels.  Conv weights keep an fp32
 master copy that Adam updates; the bf16 copy the conv kernels read is written
-by the same Adam launch.  Dropout draws are inputs (keep masks), set per step
-by the caller (set_masks).
+by the same launch.  Dropout draws are inputs (keep masks), set per step by the
+caller (set_masks).
+
+With optimizer="muon" the weight matrices (conv filters as [c_out][27 c_in], the
+hidden fc layers) take momentum steps with orthogonalised updates, one
+cf_muon_step call for all of them, scaled so that an update has the root mean
+square of 0.2 lr that Adam's typically has; vectors and the output layer stay
+with Adam.
 """
 from __future__ import annotations
 
@@ -21,7 +27,10 @@ from .stack import CosmoStack
 
 class CosmoFlowModel:
     def __init__(self, n: int, spatial: int, channels, specs=None, fc=(2048, 256, 4), slope: float = 0.3,
-                 keep: float = 0.8, device: str = "cuda"):
+                 keep: float = 0.8, device: str = "cuda", optimizer: str = "adam"):
+        if optimizer not in ("adam", "muon"):
+            raise ValueError(f"optimizer {optimizer!r}: adam or muon")
+        self.optimizer = optimizer
         self.n, self.slope, self.keep, self.device = n, float(slope), float(keep), device
         self.stack = CosmoStack(n, spatial, channels, slope, device, backward=True, specs=specs)
         st = self.stack
@@ -46,6 +55,7 @@ class CosmoFlowModel:
         # conv weights' fp32 master copies (set by sync_master after loading)
         self.w32 = [torch.empty(w.shape, dtype=f32, device=device) for w in st.w]
         self._adam = None
+        self._muon = None
         self.t = 0
 
     # ---------------------------------------------------------------- set-up
@@ -65,7 +75,7 @@ class CosmoFlowModel:
         for l in range(st.L):
             out.append((self.w32[l], st.w[l], st.dw[l]))
             out.append((st.b[l], None, st.db[l]))
-            if st.bn(l):
+            if st.normed(l):
                 out.append((st.gamma[l], None, st.dgamma[l]))
         for i in range(len(self.fw)):
             out.append((self.fw[i], None, self.dfw[i]))
@@ -101,10 +111,32 @@ class CosmoFlowModel:
             g = dx if i > 0 else None
         self.stack.backward(self.dfeat, s)
 
-    def update(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, stream=None):
-        """One Adam step of every parameter (step counter t advances)."""
+    def matrices(self):
+        """(fp32 tensor, bf16 copy or None, gradient) of the parameters that optimizer="muon" orthogonalises."""
+        st = self.stack
+        return [(self.w32[l], st.w[l], st.dw[l]) for l in range(st.L)] + \
+            [(self.fw[i], None, self.dfw[i]) for i in range(len(self.fw) - 1)]
+
+    def _muon_update(self, lr, momentum, weight_decay, stream):
+        if self._muon is None:
+            ms = [torch.zeros_like(p) for p, _, _ in self.matrices()]
+            params = cf.cf_muon_params([(p, p16, g, m, 0.2 * max(p.shape[0], p.numel() // p.shape[0]) ** 0.5)
+                                        for (p, p16, g), m in zip(self.matrices(), ms)])
+            size = cf.cf_muon_workspace_size(params)
+            self._muon = (ms, params, torch.empty((max(size, 16),), dtype=torch.uint8, device=self.device), size)
+        _, params, ws, size = self._muon
+        hyper = cf.cf_muon_hyper(lr, momentum, weight_decay, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+        cf.cf_muon_step(params, hyper, ws, size, stream)
+
+    def update(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, stream=None, momentum=0.95, weight_decay=0.0):
+        """One step of every parameter (step counter t advances): Adam, or with optimizer="muon" the orthogonalised
+        momentum step (momentum, weight_decay) of matrices() and Adam for the rest."""
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         ps = self.params()
+        if self.optimizer == "muon":
+            self._muon_update(lr, momentum, weight_decay, s)
+            taken = {p.data_ptr() for p, _, _ in self.matrices()}
+            ps = [t for t in ps if t[0].data_ptr() not in taken]
         if self._adam is None:
             self._adam = [(torch.zeros_like(p), torch.zeros_like(p)) for p, _, _ in ps]
         self.t += 1

@@ -51,16 +51,19 @@ POOL_CODES = {"max": cf.CF_POOL_MAX, "avg": cf.CF_POOL_AVG, "none": cf.CF_POOL_N
 
 
 class CosmoStack:
-    """specs: optional per-block (stride, pool) or (stride, pool, "bn"), stride
-    1 or 2, pool "max", "avg" or "none" (default: stride 1 and max-pooling
-    everywhere, the CosmoFlow-shaped five-block stack); "bn" puts batch
-    normalisation (batch statistics, gamma / beta = self.gamma[l] / self.b[l])
-    between the conv and the activation.  The hybrid-parallelism page's Table I
+    """specs: optional per-block (stride, pool), (stride, pool, "bn") or (stride,
+    pool, "gn"[, groups]), stride 1 or 2, pool "max", "avg" or "none" (default:
+    stride 1 and max-pooling everywhere, the CosmoFlow-shaped five-block stack);
+    "bn" puts batch normalisation (batch statistics, gamma / beta =
+    self.gamma[l] / self.b[l]) between the conv and the activation, "gn" group
+    normalisation (a sample's own statistics over groups of channels, 8 unless
+    given), for batches of a few volumes.  The hybrid-parallelism page's Table I
     model is channels (4, 16, 32, 64, 128, 256, 256, 256) with a stride-2
     fourth conv and no pooling after the last two at width 128."""
 
-    # batch-norm epsilon of blocks with spec (stride, pool, "bn")
+    # epsilon of blocks with spec (stride, pool, "bn") and (stride, pool, "gn")
     bn_eps = 1e-5
+    gn_eps = 1e-5
 
     def __init__(self, n: int, spatial: int, channels, slope: float = 0.3, device: str = "cuda",
                  backward: bool = True, overlap: bool = True, specs=None):
@@ -85,18 +88,21 @@ class CosmoStack:
             self.w.append(torch.empty((co, 3, 3, 3, ci), dtype=bf, device=device))
             self.b.append(torch.zeros((co,), dtype=f32, device=device))
             self.y.append(torch.empty((n, sp, sp, sp, co), dtype=bf, device=device))
-            # argmax codes (max) or sign masks (avg) of the pooled output
-            self.idx.append(torch.empty((n, sp, sp, sp, co), dtype=u8, device=device) if pool != "none" else None)
+            # argmax codes (max) or sign masks (avg) of the pooled output (group
+            # norm's backward finds both again from the conv output)
+            self.idx.append(torch.empty((n, sp, sp, sp, co), dtype=u8, device=device)
+                            if pool != "none" and not self.gn(l) else None)
             s = sp
-        # batch-norm blocks: the stored conv output, the channel sums (sum z,
-        # sum z^2), gamma
+        # normalised blocks: the stored conv output, gamma and the statistics:
+        # batch norm's channel sums (sum z, sum z^2), group norm's (mean, rstd)
         self.zc, self.stats, self.gamma = [None] * self.L, [None] * self.L, [None] * self.L
         for l in range(self.L):
-            if self.bn(l):
+            if self.normed(l):
                 n_, d, h, w = self.odims[l]
                 co = channels[l + 1]
                 self.zc[l] = torch.empty((n_, d, h, w, co), dtype=bf, device=device)
-                self.stats[l] = torch.empty((2 * co,), dtype=f32, device=device)
+                self.stats[l] = torch.empty((2 * co,), dtype=f32, device=device) if self.bn(l) else tuple(
+                    torch.empty((n_, self.groups(l)), dtype=f32, device=device) for _ in range(2))
                 self.gamma[l] = torch.ones((co,), dtype=f32, device=device)
         self.backward_enabled = backward
         # with overlap: the backward-data chain on a high-priority stream (it is the
@@ -107,6 +113,9 @@ class CosmoStack:
         for l in range(self.L):
             if self.bn(l):
                 ws = max(ws, cf.cf_workspace_size(cf.CF_OP_BN, cf.cf_conv_desc(1, 1, 1, 1, 1, channels[l + 1])))
+            elif self.gn(l):
+                for back in range(1 + bool(backward)):
+                    ws = max(ws, cf.cf_group_norm_workspace_size(self.gn_desc(l), back))
         if backward:
             self.dz, self.dw, self.db, self.g = [], [], [], []
             # per-block partial bias sums of each max-pooled block's pool backward,
@@ -131,12 +140,14 @@ class CosmoStack:
                     self.dgamma[l] = self.dsums[l][co:]
                 else:
                     self.db.append(torch.empty((co,), dtype=f32, device=device))
+                    if self.gn(l):
+                        self.dgamma[l] = torch.empty((co,), dtype=f32, device=device)
                 # g[l]: the dgrad output of block l+1: the gradient w.r.t. block l's
                 # pooled pre-activation (max), its output (avg); an unpooled block's
                 # dgrad output is its dZ itself (g[l] aliases dz[l]) unless it is
-                # batch-normalised
+                # normalised
                 pool = self.specs[l][1]
-                if pool == "none" and l < self.L - 1 and not self.bn(l):
+                if pool == "none" and l < self.L - 1 and not self.normed(l):
                     self.g.append(self.dz[l])
                 elif l < self.L - 1 or self.routed(l):
                     self.g.append(torch.empty(tuple(self.y[l].shape), dtype=bf, device=device))
@@ -187,10 +198,25 @@ class CosmoStack:
         """Block l has batch normalisation between its conv and its activation."""
         return len(self.specs[l]) > 2 and self.specs[l][2] == "bn"
 
+    def gn(self, l) -> bool:
+        """Block l has group normalisation between its conv and its activation."""
+        return len(self.specs[l]) > 2 and self.specs[l][2] == "gn"
+
+    def normed(self, l) -> bool:
+        return self.bn(l) or self.gn(l)
+
+    def groups(self, l) -> int:
+        return self.specs[l][3] if len(self.specs[l]) > 3 else 8
+
+    def gn_desc(self, l):
+        n, d, h, w = self.odims[l]
+        return cf.cf_gn_desc(n, d, h, w, self.channels[l + 1], self.groups(l), POOL_CODES[self.specs[l][1]],
+                             cf.CF_ACT_LRELU, self.slope, self.gn_eps, cf.CF_DT_BF16, 0, 0)
+
     def pool_bwd_fused(self, l) -> bool:
         """Block l's max-pool backward runs in block l+1's backward-data epilogue."""
         return (self.fuse_pool_bwd and l < self.L - 1 and self.specs[l][1] == "max" and not self.routed(l)
-                and not self.bn(l) and self.specs[l + 1][0] == 1)
+                and not self.normed(l) and self.specs[l + 1][0] == 1)
 
     def desc(self, l):
         n, d, h, w = self.dims[l]
@@ -198,21 +224,26 @@ class CosmoStack:
 
     def epi(self, l, idx=None):
         """Forward epilogue of block l (bias, slope, codes/masks, pooling kind);
-        None for a batch-normalised block (its conv output is stored plain)."""
-        if self.bn(l):
+        None for a normalised block (its conv output is stored plain)."""
+        if self.normed(l):
             return None
         return (self.b[l], self.slope, self.idx[l] if idx is None else idx, POOL_CODES[self.specs[l][1]])
 
     def _fwd_block(self, l, stream):
         """Block l's forward launches: the conv with its fused epilogue, or, with
         batch normalisation, the plain conv, the channel sums and the
-        normalisation + activation + pooling."""
-        if not self.bn(l):
+        normalisation + activation + pooling; with group normalisation the plain
+        conv and the group norm with activation + pooling."""
+        if not self.normed(l):
             cf.cf_conv3d_fwd(self.desc(l), self.block_input(l), self.w[l], self.epi(l), self.y[l], None, 0, stream)
             return
         n, d, h, w = self.odims[l]
         co = self.channels[l + 1]
         cf.cf_conv3d_fwd(self.desc(l), self.block_input(l), self.w[l], None, self.zc[l], None, 0, stream)
+        if self.gn(l):
+            cf.cf_group_norm_fwd(self.gn_desc(l), self.zc[l], self.gamma[l], self.b[l], self.y[l], *self.stats[l], self.ws,
+                                 self.ws.numel(), stream)
+            return
         cf.cf_bn_stats(n * d * h * w, co, self.zc[l], self.stats[l], self.ws, self.ws.numel(), stream)
         cf.cf_bn_act_pool_fwd(POOL_CODES[self.specs[l][1]], n, d, h, w, co, self.zc[l], self.stats[l], self.gamma[l],
                               self.b[l], self.bn_eps, self.slope, self.y[l], self.idx[l], stream)
@@ -292,8 +323,8 @@ class CosmoStack:
         first = 0
         if x_chunks is not None:
             first = max(1, self._chunked_blocks())
-            if any(self.bn(l) for l in range(first)):
-                first = 0  # batch statistics need the whole batch: no per-sample blocks
+            if any(self.normed(l) for l in range(first)):
+                first = 0  # batch statistics need the whole batch, and a normalised block runs whole
             for n0, n1, ev in x_chunks:
                 main.wait_event(ev)
                 for l in range(first):
@@ -356,6 +387,14 @@ class CosmoStack:
                                                    self.y[l] if top else None, self.idx[l], self.zc[l],
                                                    self.stats[l], self.gamma[l], self.bn_eps, self.slope,
                                                    self.dz[l], self.dsums[l], ws, wsb, main)
+                self._run(f"poolbwd{l + 1}", main, fn, timer)
+                to_host(main, host_out and host_out[1][l], self.db[l])
+            elif self.gn(l):
+                # group norm (with the activation / pooling backward folded in) from
+                # the gradient at the block's output: dZ, dbeta (db[l]), dgamma
+                src = dy if l == self.L - 1 else self.g[l]
+                fn = lambda: cf.cf_group_norm_bwd(self.gn_desc(l), self.zc[l], self.gamma[l], self.b[l], *self.stats[l],
+                                                  src, self.dz[l], self.dgamma[l], self.db[l], ws, wsb, main)
                 self._run(f"poolbwd{l + 1}", main, fn, timer)
                 to_host(main, host_out and host_out[1][l], self.db[l])
             elif l == self.L - 1:
@@ -422,11 +461,12 @@ class CosmoStack:
             if l > 0:
                 below = self.specs[l - 1][1]
                 fused = self.pool_bwd_fused(l - 1)
-                dsum = self.db[l - 1] if (not self.bn(l - 1) and (self.routed(l - 1) or below == "none" or fused)) \
+                dsum = self.db[l - 1] if (not self.normed(l - 1) and (self.routed(l - 1) or below == "none" or fused)) \
                     else None
                 # the lower block's output derivative rides on the input gradient
-                # unless it is average-pooled (its derivative is per voxel, from its masks)
-                x_act = self.block_input(l) if below != "avg" else None
+                # unless it is average-pooled (its derivative is per voxel, from its
+                # masks) or group-normalised (its backward applies it)
+                x_act = self.block_input(l) if below != "avg" and not self.gn(l - 1) else None
                 if fused:
                     fn = lambda: cf.cf_conv3d_dgrad_pool_bwd(desc, self.dz[l], self.w[l], x_act, self.slope,
                                                              self.g[l - 1], self.idx[l - 1], self.dz[l - 1], ws, wsb,
