@@ -19,6 +19,7 @@ enum : int {
     WAIT_MMA_FULL = 0x103,
     WAIT_EPI_TMEM_FULL = 0x104,
     WAIT_DRAIN = 0x105,
+    WAIT_GRID = 0x106,
     WAIT_PROBE = 0x1FF,
 };
 

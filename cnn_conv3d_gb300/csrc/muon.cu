@@ -1,7 +1,38 @@
 // muon.cu -- orthogonalisation of matrices by Newton-Schulz products and the
 // momentum step that uses it, with their entry points.
+//
+// Two launches for all matrices of a call.  ns_input_kernel takes the momentum
+// step and the Frobenius norms' partial sums.  ns_kernel is one cooperative
+// launch of a CTA per SM that runs everything else as phases between grid-wide
+// barriers; a phase's items (tiles of all matrices) are dealt out over the CTAs:
+//   C  X = u / (|u| + eps) in operand form, k x n with k <= n
+//   then for each step
+//   G  partial sums of the Gram matrix X X^T (tiles on and above the diagonal,
+//      the long axis split so that the SMs are filled)
+//   R  A' = X X^T - alpha I, alpha = |X|^2 / k, from the partial sums
+//   S  B' = (b + 2 c alpha) A' + c A' A'     (so b A + c A^2 = beta I + B',
+//                                             beta = b alpha + c alpha^2)
+//   U  X = a X + beta X + B' X; the last step writes the result instead
+//
+// Operands are fp16: X = hi + lo in two of them (22 bits), products take hi
+// alone.  Near the end A is close to I: taking alpha and beta off before
+// rounding keeps the rounding relative to what is left.  Of beta X, the last
+// two steps take hi + lo and the earlier ones hi: there B' X cancels beta X
+// along directions whose singular value is still small, and has hi only.
+// Simulated against 64 bits (operands rounded, sums exact): 2e-4 to 1e-3 of the
+// result, where rounding A and B with their diagonals gives up to 4e-3.
+// X is scaled by a power of two tau so that its entries stay well inside
+// fp16's normal range for every size.
+//
+// Operands live in blocks of 64 x 64 in the order that the tensor cores read
+// from shared memory (128-byte rows, 16-byte chunks XORed by the row), zero
+// where a matrix ends inside a block, so that a tile is fetched by bulk copies
+// without a tensor map and nothing has to be masked.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 #include <cmath>
+#include <vector>
 
 #include "cf_internal.h"
 #include "cf_ptx.cuh"
@@ -9,26 +40,70 @@
 namespace cf {
 namespace {
 
-constexpr int kNormBlocks = 128;
-constexpr float kDown = 0x1p-80f;
-constexpr int kTile = 64, kTileK = 16;
+constexpr int kNormChunks = 256;          // partial sums of a matrix's norm, at most
+constexpr float kDown = 0x1p-80f;         // scale of the sums that stand in for overflowing ones
+constexpr int kMaxMats = 48;              // matrices of one launch
+constexpr int kThreads = 320;             // producer, issuer, eight epilogue warps
+constexpr int kBlk = 64 * 64;             // values of an operand block
+constexpr uint32_t kBlkBytes = kBlk * 2;
+constexpr uint32_t kStageA = 2 * kBlkBytes, kStageB = 4 * kBlkBytes, kStage = kStageA + kStageB;
+constexpr int kStages = 4;
+constexpr uint32_t kSmem = kStages * kStage + 1024;
+constexpr int kTileF = 128 * 128;         // floats of a Gram tile
+constexpr int kSlices = 8;                // items of phase R per tile: 16 columns each
 
-__device__ __forceinline__ float load_f(const void* p, int f32, int64_t i) {
-    return f32 ? static_cast<const float*>(p)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
+struct Mat {
+    const void* g;
+    float* m;
+    float* w;
+    uint16_t* o;
+    int64_t rows, cols;      // as stored
+    int k, n;                // k <= n; transposed when rows > cols
+    int f32, tall;
+    float keep, step;        // w = keep w - step X
+    float tau;
+    int rb, cb;              // operand blocks: X is rb x cb, A' and B' rb x rb
+    int mt, ut;              // 128-row tiles, 256-column tiles of X
+    int splits, per;         // parts of the long axis in phase G, blocks of each
+    int chunks;              // norm partials
+    int64_t chunk;           // values of each
+    int n0, c0, g0, r0, s0, u0;  // first item of each phase
+    __half *xh[2], *xl[2], *ad, *bp;
+    float *part, *norm, *unorm, *alpha;
+};
+
+struct Job {
+    Mat mat[kMaxMats];
+    int count, steps;
+    int nn, nc, ng, nr, ns, nu;  // items of each phase
+    float a, b, c, eps, mu;
+    int nesterov;
+    uint32_t* sync;  // arrivals at the grid barrier, abort flag
+    int* status;
+    uint64_t wait_ns;
+};
+
+__device__ __forceinline__ float load_u(const Mat& M, const Job& J, int64_t i) {
+    float u = M.f32 ? static_cast<const float*>(M.g)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[i]);
+    if (M.m) u = J.nesterov ? fmaf(J.mu, M.m[i], u) : M.m[i];
+    return u;
 }
 
-// u = g (momentum 0 and m NULL), or the momentum step; partial sums of u^2 and of (kDown u)^2, which
-// stands in where the first overflows.
-__global__ void __launch_bounds__(256) ns_input_kernel(const void* __restrict__ g, int f32, float* __restrict__ m, float mu,
-                                                       int64_t count, int nesterov, float* __restrict__ part) {
-    __shared__ float red[8], red2[8];
+// The momentum step of one chunk, and its sums of u^2 and of (kDown u)^2, which stands in where the first overflows.
+__global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ Job J) {
+    __shared__ float red[16];
+    if (blockIdx.x == 0 && threadIdx.x < 2) J.sync[threadIdx.x] = 0;
+    int i = 0;
+    while (i + 1 < J.count && (int)blockIdx.x >= J.mat[i + 1].n0) ++i;
+    const Mat& M = J.mat[i];
+    const int64_t b = (blockIdx.x - M.n0) * M.chunk, e = min(b + M.chunk, M.rows * M.cols);
     float s = 0.f, s2 = 0.f;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < count; i += (int64_t)gridDim.x * blockDim.x) {
-        float u = load_f(g, f32, i);
-        if (m) {
-            const float t = fmaf(mu, m[i], u);
-            m[i] = t;
-            u = nesterov ? fmaf(mu, t, u) : t;
+    for (int64_t j = b + threadIdx.x; j < e; j += 256) {
+        float u = M.f32 ? static_cast<const float*>(M.g)[j] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[j]);
+        if (M.m) {
+            const float t = fmaf(J.mu, M.m[j], u);
+            M.m[j] = t;
+            u = J.nesterov ? fmaf(J.mu, t, u) : t;
         }
         s = fmaf(u, u, s);
         u *= kDown;
@@ -38,95 +113,502 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const void* __restrict__ 
         s += __shfl_down_sync(~0u, s, o);
         s2 += __shfl_down_sync(~0u, s2, o);
     }
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s, red2[threadIdx.x >> 5] = s2;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s, red[8 + (threadIdx.x >> 5)] = s2;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < 8; ++i) s += red[i], s2 += red2[i];
-        part[blockIdx.x] = s;
-        part[kNormBlocks + blockIdx.x] = s2;
+        for (int t = 1; t < 8; ++t) s += red[t], s2 += red[8 + t];
+        M.norm[blockIdx.x - M.n0] = s;
+        M.norm[kNormChunks + blockIdx.x - M.n0] = s2;
     }
 }
 
-// X [k][n] = u / (|u| + eps), transposed where tall.
-__global__ void __launch_bounds__(256) ns_scale_kernel(const void* __restrict__ g, int f32, const float* __restrict__ m, float mu,
-                                                       int64_t rows, int64_t cols, int nesterov,
-                                                       const float* __restrict__ part, float eps, float* __restrict__ X) {
-    float s = 0.f, s2 = 0.f;
-    for (int i = 0; i < kNormBlocks; ++i) s += part[i], s2 += part[kNormBlocks + i];
-    // u / (|u| + eps) as (u pre) inv
-    const float pre = isinf(s) ? kDown : 1.f, inv = 1.f / (sqrtf(isinf(s) ? s2 : s) + eps * pre);
-    const int64_t count = rows * cols;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < count; i += (int64_t)gridDim.x * blockDim.x) {
-        float u = load_f(g, f32, i);
-        if (m) u = nesterov ? fmaf(mu, m[i], u) : m[i];
-        X[rows > cols ? (i % cols) * rows + i / cols : i] = u * pre * inv;
-    }
+// Sum of v[0 .. count) over the block, the same everywhere and in a fixed order; all threads call it.
+__device__ __forceinline__ float block_sum(const float* v, int count, float* red) {
+    float s = 0.f;
+    for (int i = threadIdx.x; i < count; i += kThreads) s += v[i];
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) s += red[i];
+    return s;
 }
 
-// C [M][N] = al D + be (P [M][K] Q), Q [K][N] or, transposed, [N][K].
-__global__ void __launch_bounds__(256) ns_gemm_kernel(const float* __restrict__ P, const float* __restrict__ Q, int q_t,
-                                                      const float* __restrict__ D, float al, float be, int64_t M, int64_t N,
-                                                      int64_t K, float* __restrict__ C) {
-    __shared__ float ps[kTileK][kTile + 1], qs[kTileK][kTile + 1];
-    const int64_t i0 = (int64_t)blockIdx.y * kTile, j0 = (int64_t)blockIdx.x * kTile;
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kTileK) {
-        for (int e = threadIdx.x; e < kTile * kTileK; e += 256) {
-            const int r = e / kTileK, kk = e % kTileK;
-            ps[kk][r] = i0 + r < M && k0 + kk < K ? P[(i0 + r) * K + k0 + kk] : 0.f;
-            if (q_t) {
-                qs[kk][r] = j0 + r < N && k0 + kk < K ? Q[(j0 + r) * K + k0 + kk] : 0.f;
-            } else {
-                const int c = e % kTile, kq = e / kTile;
-                qs[kq][c] = j0 + c < N && k0 + kq < K ? Q[(k0 + kq) * N + j0 + c] : 0.f;
+// Offset in values of element (r, c) of a blocked operand with cb blocks a row.
+__device__ __forceinline__ int64_t blocked(int r, int c, int cb) {
+    return ((int64_t)(r >> 6) * cb + (c >> 6)) * kBlk + (r & 63) * 64 + ((((c & 63) >> 3) ^ (r & 7)) << 3) + (c & 7);
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// fp16 operands, fp32 sums: M x N, A K-major, B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+    return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int abort;
+    float red[16];
+};
+
+// All CTAs of the grid: what any of them wrote before is seen by all after, by bulk copies too.
+__device__ bool grid_sync(const Job& J, uint32_t& target, Shared& sh) {
+    fence_async();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        target += gridDim.x;
+        if (*(volatile int*)&sh.abort) atomicExch(&J.sync[1], 1u);
+        __threadfence();
+        atomicAdd(&J.sync[0], 1u);
+        const uint64_t t0 = globaltimer();
+        uint32_t seen, stop;
+        while (true) {
+            asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(seen) : "l"(&J.sync[0]) : "memory");
+            if (seen >= target) break;
+            asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(stop) : "l"(&J.sync[1]) : "memory");
+            if (stop == 0 && globaltimer() - t0 > J.wait_ns) {
+                atomicCAS(J.status, 0, (int)WAIT_GRID);
+                atomicExch(&J.sync[1], 1u);
+                stop = 1;
+            }
+            if (stop) {
+                sh.abort = 1;
+                break;
             }
         }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kTileK; ++kk) {
-            float p[4], q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = ps[kk][ti + 16 * e], q[e] = qs[kk][tj + 16 * e];
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(p[a], q[b], acc[a][b]);
-        }
-        __syncthreads();
+        asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(stop) : "l"(&J.sync[1]) : "memory");
+        if (stop) sh.abort = 1;
+        fence_async();
     }
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int64_t i = i0 + ti + 16 * a, j = j0 + tj + 16 * b;
-            if (i < M && j < N) C[i * N + j] = be * acc[a][b] + (D ? al * D[i * N + j] : 0.f);
-        }
+    __syncthreads();
+    return sh.abort == 0;
 }
 
-// o = X, or w = keep w - step X with its bf16 copy; X transposed where tall.
-__global__ void __launch_bounds__(256) ns_output_kernel(const float* __restrict__ X, int64_t rows, int64_t cols,
-                                                        uint16_t* __restrict__ o, float* __restrict__ w, float keep, float step) {
-    const int64_t count = rows * cols;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < count; i += (int64_t)gridDim.x * blockDim.x) {
-        float v = X[rows > cols ? (i % cols) * rows + i / cols : i];
-        if (w) {
-            v = keep * w[i] - step * v;
-            w[i] = v;
+enum { PH_G, PH_S, PH_U };
+
+// An item of a product phase: which operand blocks, and how many.
+struct Item {
+    int mat, i, j, split;  // 128-row tile, tile of the other side, part of the long axis
+    int kb0, kb1;          // blocks of the contracted axis
+    int nb;                // 64-column blocks of the tile
+};
+
+template <int PH>
+__device__ __forceinline__ int first_of(const Mat& M) { return PH == PH_G ? M.g0 : PH == PH_S ? M.s0 : M.u0; }
+
+template <int PH>
+__device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
+    while (mat + 1 < J.count && it >= first_of<PH>(J.mat[mat + 1])) ++mat;
+    const Mat& M = J.mat[mat];
+    Item t;
+    t.mat = mat;
+    int e = it - first_of<PH>(M);
+    if (PH == PH_U) {
+        t.i = e % M.mt;
+        t.j = e / M.mt;
+        t.split = 0;
+        t.kb0 = 0;
+        t.kb1 = (M.k + 63) / 64;
+        t.nb = min(4, M.cb - 4 * t.j);
+        return t;
+    }
+    if (PH == PH_G) {
+        t.split = e % M.splits;
+        e /= M.splits;
+        t.kb0 = t.split * M.per;
+        t.kb1 = min(t.kb0 + M.per, M.cb);
+    } else {
+        t.split = 0;
+        t.kb0 = 0;
+        t.kb1 = (M.k + 63) / 64;
+    }
+    int i = 0;
+    while (e >= M.mt - i) {
+        e -= M.mt - i;
+        ++i;
+    }
+    t.i = i;
+    t.j = i + e;
+    t.nb = 2;
+    return t;
+}
+
+struct Pipe {
+    int stage = 0;
+    uint32_t phase = 0, local = 0;
+    uint32_t issued = 0, par = 0;  // per stage: a copy was issued, parity of the last
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
         }
-        if (o) o[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+};
+
+template <int PH>
+__device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8_t* ring, Pipe& P) {
+    const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
+    int mat = 0;
+    for (int it = blockIdx.x; it < total; it += gridDim.x) {
+        const Item t = item_of<PH>(J, it, mat);
+        mat = t.mat;
+        const Mat& M = J.mat[mat];
+        const __half* a = PH == PH_G ? M.xh[cur] : PH == PH_S ? M.ad : M.bp;
+        const int acb = PH == PH_G ? M.cb : M.rb;
+        const bool same = PH != PH_U && t.i == t.j;
+        const uint32_t bytes = kStageA + (same ? 0 : t.nb * kBlkBytes);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+            if (!mbar_wait(&sh.empty[P.stage], P.phase ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_PRODUCER_EMPTY)) return;
+            uint8_t* s = ring + P.stage * kStage;
+            uint64_t* bar = &sh.full[P.stage];
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(s, a + ((int64_t)(2 * t.i) * acb + kb) * kBlk, kBlkBytes, bar);
+            bulk_load(s + kBlkBytes, a + ((int64_t)(2 * t.i + 1) * acb + kb) * kBlk, kBlkBytes, bar);
+            if (PH == PH_U) {
+                bulk_load(s + kStageA, M.xh[cur] + ((int64_t)kb * M.cb + 4 * t.j) * kBlk, t.nb * kBlkBytes, bar);
+            } else if (!same) {
+                bulk_load(s + kStageA, a + ((int64_t)(2 * t.j) * acb + kb) * kBlk, kBlkBytes, bar);
+                bulk_load(s + kStageA + kBlkBytes, a + ((int64_t)(2 * t.j + 1) * acb + kb) * kBlk, kBlkBytes, bar);
+            }
+            P.issued |= 1u << P.stage;
+            P.par = (P.par & ~(1u << P.stage)) | (P.phase << P.stage);
+            P.next();
+        }
+    }
+}
+
+template <int PH>
+__device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, Pipe& P) {
+    const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
+    int mat = 0;
+    for (int it = blockIdx.x; it < total; it += gridDim.x, ++P.local) {
+        const Item t = item_of<PH>(J, it, mat);
+        mat = t.mat;
+        const uint32_t acc = P.local & 1, use = P.local >> 1;
+        if (!mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_TMEM_EMPTY)) return;
+        tc_fence_after();
+        const uint32_t d = sh.tmem + acc * 256;
+        const bool same = PH != PH_U && t.i == t.j;
+        const uint32_t idesc = PH == PH_U ? idesc_f16(128, 64 * t.nb, 1) : idesc_f16(128, 128, 0);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+            if (!mbar_wait(&sh.full[P.stage], P.phase, &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
+            tc_fence_after();
+            const uint32_t as = smem_u32(ring + P.stage * kStage), bs = same ? as : as + kStageA;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t ad = sdesc(as + k * 32, 16, 1024, SWZ_128B);
+                // X as [contracted][columns]: 64-column atoms a block apart, 16 contracted rows a step
+                const uint64_t bd = PH == PH_U ? sdesc(bs + k * 2048, kBlkBytes, 1024, SWZ_128B)
+                                               : sdesc(bs + k * 32, 16, 1024, SWZ_128B);
+                umma_bf16(d, ad, bd, idesc, kb > t.kb0 || k > 0);
+            }
+            umma_commit(&sh.empty[P.stage]);
+            P.next();
+        }
+        umma_commit(&sh.tfull[acc]);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The tile's 32 columns c .. c+31 of row r, from tensor memory, as phase G stores them: four columns of all rows in turn.
+__device__ __forceinline__ float4* tile_at(float* part, int r, int c) {
+    return reinterpret_cast<float4*>(part) + (c >> 2) * 128 + r;
+}
+
+struct StepScalars {
+    float alpha, beta, theta;  // theta: the part of beta that takes hi + lo
+};
+__device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, int step) {
+    StepScalars s;
+    s.alpha = *(volatile const float*)M.alpha;
+    s.beta = s.alpha * fmaf(J.c, s.alpha, J.b);
+    s.theta = step + 2 >= J.steps ? s.beta : 0.f;
+    return s;
+}
+
+template <int PH>
+__device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared& sh, Pipe& P) {
+    const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = (warp - 2) >> 2;
+    const int r = 32 * q + lane;
+    int mat = 0;
+    for (int it = blockIdx.x; it < total; it += gridDim.x, ++P.local) {
+        const Item t = item_of<PH>(J, it, mat);
+        mat = t.mat;
+        const Mat& M = J.mat[mat];
+        const uint32_t acc = P.local & 1, use = P.local >> 1;
+        if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
+        tc_fence_after();
+        const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
+        const int i = 128 * t.i + r;
+        float* part = PH == PH_U ? nullptr
+                                 : M.part + ((int64_t)(PH == PH_G ? it - M.g0 : (it - M.s0) * M.splits)) * kTileF;
+        StepScalars sc{};
+        if (PH != PH_G) sc = scalars_of(J, M, step);
+        float usum = 0.f;
+        for (int ch = half; ch < 2 * t.nb; ch += 2) {
+            uint32_t v[32];
+            tmem_ld32(tm + 32 * ch, v);
+            tmem_ld_wait();
+            const int c = 32 * ch;
+            if (PH == PH_G) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                           __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            } else if (PH == PH_S) {
+                const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 dd = *tile_at(part, r, c + e);
+                    o[e] = fmaf(bb, dd.x, J.c * __uint_as_float(v[e]));
+                    o[e + 1] = fmaf(bb, dd.y, J.c * __uint_as_float(v[e + 1]));
+                    o[e + 2] = fmaf(bb, dd.z, J.c * __uint_as_float(v[e + 2]));
+                    o[e + 3] = fmaf(bb, dd.w, J.c * __uint_as_float(v[e + 3]));
+                }
+                const int j = 128 * t.j + c;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4*>(M.bp + blocked(i, j + e, M.rb)) =
+                        make_uint4(pack_f16(o[e], o[e + 1]), pack_f16(o[e + 2], o[e + 3]), pack_f16(o[e + 4], o[e + 5]),
+                                   pack_f16(o[e + 6], o[e + 7]));
+                if (t.i != t.j) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
+                }
+            } else {
+                const int j = 256 * t.j + c;
+                const bool last = step + 1 == J.steps;
+                const float whi = J.a + sc.beta, wlo = J.a + sc.theta;
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    const int64_t at = blocked(i, j + e, M.cb);
+                    const uint4 h = *reinterpret_cast<const uint4*>(M.xh[cur] + at);
+                    const uint4 l = *reinterpret_cast<const uint4*>(M.xl[cur] + at);
+                    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hw[p]));
+                        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lw[p]));
+                        y[e + 2 * p] = fmaf(whi, fh.x, fmaf(wlo, fl.x, __uint_as_float(v[e + 2 * p])));
+                        y[e + 2 * p + 1] = fmaf(whi, fh.y, fmaf(wlo, fl.y, __uint_as_float(v[e + 2 * p + 1])));
+                    }
+                }
+                if (!last) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t hw[4], lw[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float y0 = y[e + 2 * p], y1 = y[e + 2 * p + 1];
+                            const __half2 h = __floats2half2_rn(y0, y1);
+                            const float2 f = __half22float2(h);
+                            hw[p] = *reinterpret_cast<const uint32_t*>(&h);
+                            lw[p] = pack_f16(y0 - f.x, y1 - f.y);
+                            usum = fmaf(y0, y0, fmaf(y1, y1, usum));
+                        }
+                        const int64_t at = blocked(i, j + e, M.cb);
+                        *reinterpret_cast<uint4*>(M.xh[cur ^ 1] + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                        *reinterpret_cast<uint4*>(M.xl[cur ^ 1] + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                    }
+                } else if (i < M.k) {
+                    const float inv = 1.f / M.tau;
+                    const int64_t base = M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j, st = M.tall ? M.k : 1;
+                    const int cnt = min(32, M.n - j);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e < cnt) {
+                            float x = y[e] * inv;
+                            if (M.w) {
+                                x = M.keep * M.w[base + e * st] - M.step * x;
+                                M.w[base + e * st] = x;
+                            }
+                            if (M.o) M.o[base + e * st] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                        }
+                }
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.tempty[acc]);
+        if (PH == PH_U && step + 1 < J.steps) {
+            for (int o = 16; o; o >>= 1) usum += __shfl_xor_sync(~0u, usum, o);
+            if (lane == 0) M.unorm[8 * (it - M.u0) + warp - 2] = usum;
+        }
+    }
+}
+
+template <int PH>
+__device__ __forceinline__ void product_phase(const Job& J, int cur, int step, Shared& sh, uint8_t* ring, Pipe& P) {
+    const int warp = threadIdx.x >> 5;
+    if (warp == 0) {
+        if ((threadIdx.x & 31) == 0) produce<PH>(J, cur, sh, ring, P);
+    } else if (warp == 1) {
+        if ((threadIdx.x & 31) == 0) issue<PH>(J, sh, ring, P);
+    } else {
+        epilogue<PH>(J, cur, step, sh, P);
+    }
+    __syncwarp();
+}
+
+// X in operand form from u, one 64 x 64 block an item.
+__device__ __forceinline__ void convert_phase(const Job& J, Shared& sh, float* buf) {
+    int mat = 0;
+    for (int it = blockIdx.x; it < J.nc; it += gridDim.x) {
+        while (mat + 1 < J.count && it >= J.mat[mat + 1].c0) ++mat;
+        const Mat& M = J.mat[mat];
+        const float s = block_sum(M.norm, M.chunks, sh.red), s2 = block_sum(M.norm + kNormChunks, M.chunks, sh.red);
+        // u / (|u| + eps) as (u pre) inv
+        const float pre = isinf(s) ? kDown : 1.f, nrm = sqrtf(isinf(s) ? s2 : s), inv = 1.f / (nrm + J.eps * pre);
+        const int e = it - M.c0, bi = e / M.cb, bj = e % M.cb;
+        // stored rows and columns of the block
+        const int64_t sr = M.tall ? 64 * bj : 64 * bi, sc = M.tall ? 64 * bi : 64 * bj;
+        for (int t = threadIdx.x; t < kBlk; t += kThreads) {
+            const int r = t >> 6, c = t & 63;
+            const float u = sr + r < M.rows && sc + c < M.cols ? load_u(M, J, (sr + r) * M.cols + sc + c) : 0.f;
+            buf[M.tall ? c * 65 + r : r * 65 + c] = u * pre * inv * M.tau;
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < kBlk / 8; t += kThreads) {
+            const int r = t >> 3, c = 8 * (t & 7);
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float y0 = buf[r * 65 + c + 2 * p], y1 = buf[r * 65 + c + 2 * p + 1];
+                const __half2 h = __floats2half2_rn(y0, y1);
+                const float2 f = __half22float2(h);
+                hw[p] = *reinterpret_cast<const uint32_t*>(&h);
+                lw[p] = pack_f16(y0 - f.x, y1 - f.y);
+            }
+            const int64_t at = blocked(64 * bi + r, 64 * bj + c, M.cb);
+            *reinterpret_cast<uint4*>(M.xh[0] + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(M.xl[0] + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
+        if (e == 0 && threadIdx.x == 0) M.unorm[0] = (nrm * inv * M.tau) * (nrm * inv * M.tau);  // |X|^2 of step 0
+        __syncthreads();
+    }
+}
+
+// A' of a slice of 16 columns of a Gram tile: the sum of its parts, less alpha on the diagonal, in fp32 (kept in the first
+// part's place) and as an operand, on both sides of the diagonal.
+__device__ __forceinline__ void reduce_phase(const Job& J, int step, Shared& sh) {
+    int mat = 0;
+    for (int it = blockIdx.x; it < J.nr; it += gridDim.x) {
+        while (mat + 1 < J.count && it >= J.mat[mat + 1].r0) ++mat;
+        const Mat& M = J.mat[mat];
+        const float inv2 = 1.f / (M.tau * M.tau);
+        const float alpha = block_sum(M.unorm, step == 0 ? 1 : 8 * M.mt * M.ut, sh.red) * inv2 / (float)M.k;
+        const int e = it - M.r0, tile = e / kSlices, sl = e % kSlices;
+        if (e == 0 && threadIdx.x == 0) *M.alpha = alpha;
+        int ti = 0, f = tile;
+        while (f >= M.mt - ti) {
+            f -= M.mt - ti;
+            ++ti;
+        }
+        const int tj = ti + f;
+        float* part = M.part + (int64_t)tile * M.splits * kTileF;
+        if (threadIdx.x < 256) {
+            const int r = threadIdx.x & 127;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int c = 16 * sl + 8 * p + 4 * (threadIdx.x >> 7);
+                float4 s = *tile_at(part, r, c);
+                for (int w = 1; w < M.splits; ++w) {
+                    const float4 x = *tile_at(part + (int64_t)w * kTileF, r, c);
+                    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+                }
+                const int i = 128 * ti + r, j = 128 * tj + c;
+                float o[4] = {s.x * inv2, s.y * inv2, s.z * inv2, s.w * inv2};
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (i == j + x && i < M.k) o[x] -= alpha;
+                *tile_at(part, r, c) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint2*>(M.ad + blocked(i, j, M.rb)) = make_uint2(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]));
+                if (ti != tj) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) M.ad[blocked(j + x, i, M.rb)] = __float2half_rn(o[x]);
+                }
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ Job J) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sh.tfull[a], 1);
+            mbar_init(&sh.tempty[a], 256);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    Pipe P;
+    uint32_t target = 0;
+    convert_phase(J, sh, reinterpret_cast<float*>(ring));
+    bool ok = grid_sync(J, target, sh);
+    for (int step = 0; ok && step < J.steps; ++step) {
+        const int cur = step & 1;
+        product_phase<PH_G>(J, cur, step, sh, ring, P);
+        if (!(ok = grid_sync(J, target, sh))) break;
+        reduce_phase(J, step, sh);
+        if (!(ok = grid_sync(J, target, sh))) break;
+        product_phase<PH_S>(J, cur, step, sh, ring, P);
+        if (!(ok = grid_sync(J, target, sh))) break;
+        product_phase<PH_U>(J, cur, step, sh, ring, P);
+        if (step + 1 < J.steps) ok = grid_sync(J, target, sh);
+    }
+    // after a wait that gave up: copies and products in flight end before the CTA leaves
+    if (*(volatile int*)&sh.abort) {
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < kStages; ++s)
+                if (P.issued & (1u << s)) mbar_wait_timed(&sh.full[s], (P.par >> s) & 1, J.wait_ns);
+        } else if (threadIdx.x == 32) {
+            umma_commit(&sh.drain);
+            mbar_wait_timed(&sh.drain, 0, J.wait_ns);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 512);
     }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool shape_ok(int64_t rows, int64_t cols) { return rows > 0 && cols > 0; }
 bool shape_supported(int64_t rows, int64_t cols) { return rows <= 65536 && cols <= 65536; }
-
-// Workspace of one matrix: norm partials, X twice, A, B.
-size_t matrix_bytes(int64_t rows, int64_t cols) {
-    const size_t k = (size_t)std::min(rows, cols);
-    return 2 * kNormBlocks * sizeof(float) + 256 + ((size_t)rows * cols * 2 + k * k * 2) * sizeof(float);
-}
 
 struct Poly {
     int steps;
@@ -136,27 +618,111 @@ bool poly_ok(const Poly& p) {
     return p.steps >= 1 && std::isfinite(p.a) && std::isfinite(p.b) && std::isfinite(p.c) && p.eps >= 0.f && std::isfinite(p.eps);
 }
 
-cf_status run_matrix(const LaunchCtx& ctx, const Poly& p, int64_t rows, int64_t cols, const void* g, int f32, float* m, float mu,
-                     int nesterov, uint16_t* o, float* w, float keep, float step, void* ws) {
-    const int64_t k = std::min(rows, cols), n = std::max(rows, cols), count = rows * cols;
-    float* part = static_cast<float*>(ws);
-    float* X = part + 2 * kNormBlocks;
-    float* Y = X + (count + 3) / 4 * 4;
-    float* A = Y + (count + 3) / 4 * 4;
-    float* B = A + (k * k + 3) / 4 * 4;
-    const unsigned blocks = (unsigned)std::min<int64_t>((count + 255) / 256, 4 * ctx.num_sms);
-    ns_input_kernel<<<kNormBlocks, 256, 0, ctx.stream>>>(g, f32, m, mu, count, nesterov, part);
-    ns_scale_kernel<<<blocks, 256, 0, ctx.stream>>>(g, f32, m, mu, rows, cols, nesterov, part, p.eps, X);
-    const dim3 kk((unsigned)((k + kTile - 1) / kTile), (unsigned)((k + kTile - 1) / kTile));
-    const dim3 kn((unsigned)((n + kTile - 1) / kTile), (unsigned)((k + kTile - 1) / kTile));
-    for (int s = 0; s < p.steps; ++s) {
-        ns_gemm_kernel<<<kk, 256, 0, ctx.stream>>>(X, X, 1, nullptr, 0.f, 1.f, k, k, n, A);
-        ns_gemm_kernel<<<kk, 256, 0, ctx.stream>>>(A, A, 0, A, p.b, p.c, k, k, k, B);
-        ns_gemm_kernel<<<kn, 256, 0, ctx.stream>>>(B, X, 0, X, p.a, 1.f, k, n, k, Y);
-        std::swap(X, Y);
+// The workspace is laid out for this many CTAs: the sizes do not depend on the device.
+constexpr int kPlanSms = 152;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Sizes, items and the split of the long axis of matrices that run in one launch.
+void plan_sizes(Mat* mats, int count) {
+    int64_t blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        Mat& M = mats[i];
+        M.tall = M.rows > M.cols;
+        M.k = (int)std::min(M.rows, M.cols), M.n = (int)std::max(M.rows, M.cols);
+        M.mt = (M.k + 127) / 128, M.rb = 2 * M.mt, M.cb = (M.n + 63) / 64, M.ut = (M.cb + 3) / 4;
+        blocks += (int64_t)M.mt * (M.mt + 1) / 2 * M.cb;
     }
-    ns_output_kernel<<<blocks, 256, 0, ctx.stream>>>(X, rows, cols, o, w, keep, step);
+    // a CTA's share of phase G's blocks, at least four to a part (a part costs its sums' round trip through memory)
+    const int64_t share = std::max<int64_t>(4, (blocks + kPlanSms - 1) / kPlanSms);
+    for (int i = 0; i < count; ++i) {
+        Mat& M = mats[i];
+        M.per = (int)std::min<int64_t>(share, M.cb);
+        M.splits = (M.cb + M.per - 1) / M.per;
+        const int64_t total = M.rows * M.cols;
+        M.chunk = std::max<int64_t>(4096, (total + kNormChunks - 1) / kNormChunks);
+        M.chunks = (int)((total + M.chunk - 1) / M.chunk);
+        // entries of X are 1 / sqrt(k n) at first and at most about 1.2 / sqrt(n) in the mean later: a quarter of the former's inverse
+        M.tau = std::exp2(std::floor(std::log2(std::max(4.0, std::sqrt((double)M.k * M.n)) / 4.0)));
+    }
+}
+
+// Places the matrices' buffers at `base` (which may be NULL, to count) and returns their size.
+size_t place(Mat* mats, int count, char* base) {
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        char* p = base + at;
+        at += up256(bytes);
+        return p;
+    };
+    for (int i = 0; i < count; ++i) {
+        Mat& M = mats[i];
+        const size_t xb = (size_t)M.rb * M.cb * kBlkBytes, ab = (size_t)M.rb * M.rb * kBlkBytes;
+        for (int p = 0; p < 2; ++p) {
+            M.xh[p] = reinterpret_cast<__half*>(take(xb));
+            M.xl[p] = reinterpret_cast<__half*>(take(xb));
+        }
+        M.ad = reinterpret_cast<__half*>(take(ab));
+        M.bp = reinterpret_cast<__half*>(take(ab));
+        M.part = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * M.splits * kTileF * sizeof(float)));
+        M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
+        M.unorm = reinterpret_cast<float*>(take((size_t)M.mt * M.ut * 8 * sizeof(float)));
+        M.alpha = reinterpret_cast<float*>(take(sizeof(float)));
+    }
+    return at;
+}
+
+size_t workspace_of(std::vector<Mat>& mats) {
+    size_t most = 0;
+    for (size_t b = 0; b < mats.size(); b += kMaxMats) {
+        const int count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
+        plan_sizes(&mats[b], count);
+        most = std::max(most, place(&mats[b], count, nullptr));
+    }
+    return most;
+}
+
+cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws) {
+    if (cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess) return CF_ERR_CUDA;
+    for (size_t b = 0; b < mats.size(); b += kMaxMats) {
+        Job J{};
+        J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
+        plan_sizes(&mats[b], J.count);
+        place(&mats[b], J.count, static_cast<char*>(ws));
+        for (int i = 0; i < J.count; ++i) {
+            Mat& M = J.mat[i] = mats[b + i];
+            M.n0 = J.nn, M.c0 = J.nc, M.g0 = J.ng, M.r0 = J.nr, M.s0 = J.ns, M.u0 = J.nu;
+            const int tiles = M.mt * (M.mt + 1) / 2;
+            J.nn += M.chunks;
+            J.nc += M.rb * M.cb;
+            J.ng += tiles * M.splits;
+            J.nr += tiles * kSlices;
+            J.ns += tiles;
+            J.nu += M.mt * M.ut;
+        }
+        J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.mu = mu, J.nesterov = nesterov;
+        J.sync = static_cast<uint32_t*>(ws);
+        J.status = ctx.status;
+        J.wait_ns = ctx.wait_ns;
+        ns_input_kernel<<<J.nn, 256, 0, ctx.stream>>>(J);
+        void* args[] = {&J};
+        if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(ns_kernel), dim3(ctx.num_sms), dim3(kThreads), args, kSmem,
+                                        ctx.stream) != cudaSuccess)
+            return CF_ERR_CUDA;
+    }
     return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
+}
+
+std::vector<Mat> batch_of(const cf_ns_desc* d, const void* g, uint16_t* o) {
+    std::vector<Mat> mats((size_t)d->batch);
+    const int f32 = d->dtype == CF_DT_F32;
+    const int64_t count = d->rows * d->cols;
+    for (int64_t i = 0; i < d->batch; ++i) {
+        mats[i].rows = d->rows, mats[i].cols = d->cols, mats[i].f32 = f32;
+        mats[i].g = static_cast<const char*>(g) + i * count * (f32 ? 4 : 2);
+        mats[i].o = o + i * count;
+    }
+    return mats;
 }
 
 }  // namespace
@@ -175,24 +741,19 @@ static cf_status ns_check(const cf_ns_desc* d) {
 }
 
 size_t cf_orthogonalize_workspace_size(const cf_ns_desc* desc) {
-    return ns_check(desc) == CF_OK ? matrix_bytes(desc->rows, desc->cols) : 0;
+    if (ns_check(desc) != CF_OK) return 0;
+    std::vector<Mat> mats = batch_of(desc, nullptr, nullptr);
+    return workspace_of(mats);
 }
 
 cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, void* ws, size_t ws_bytes, void* stream) {
     if (const cf_status st = ns_check(desc); st != CF_OK) return st;
     if (g == nullptr || o == nullptr || !aligned16(g) || !aligned16(o) || !aligned16(ws)) return CF_ERR_INVALID_ARG;
-    if (ws == nullptr || ws_bytes < cf_orthogonalize_workspace_size(desc)) return CF_ERR_WORKSPACE;
+    std::vector<Mat> mats = batch_of(desc, g, o);
+    if (ws == nullptr || ws_bytes < workspace_of(mats)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    const int f32 = desc->dtype == CF_DT_F32;
-    const int64_t count = desc->rows * desc->cols;
-    for (int64_t i = 0; i < desc->batch; ++i) {
-        const cf_status st = run_matrix(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, desc->rows, desc->cols,
-                                        static_cast<const char*>(g) + i * count * (f32 ? 4 : 2), f32, nullptr, 0.f, 0,
-                                        o + i * count, nullptr, 0.f, 0.f, ws);
-        if (st != CF_OK) return st;
-    }
-    return CF_OK;
+    return run(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, 0.f, 0, mats, ws);
 }
 
 static cf_status muon_check(int32_t count, const cf_muon_param* p) {
@@ -209,11 +770,20 @@ static cf_status muon_check(int32_t count, const cf_muon_param* p) {
     return CF_OK;
 }
 
+static std::vector<Mat> list_of(int32_t count, const cf_muon_param* p) {
+    std::vector<Mat> mats((size_t)count);
+    for (int32_t i = 0; i < count; ++i) {
+        Mat& M = mats[i];
+        M.g = p[i].g, M.m = p[i].m, M.w = p[i].w, M.o = p[i].w_bf16;
+        M.rows = p[i].rows, M.cols = p[i].cols, M.f32 = 1;
+    }
+    return mats;
+}
+
 size_t cf_muon_workspace_size(int32_t count, const cf_muon_param* params) {
-    if (muon_check(count, params) != CF_OK) return 0;
-    size_t most = 0;
-    for (int32_t i = 0; i < count; ++i) most = std::max(most, matrix_bytes(params[i].rows, params[i].cols));
-    return most;
+    if (count == 0 || muon_check(count, params) != CF_OK) return 0;
+    std::vector<Mat> mats = list_of(count, params);
+    return workspace_of(mats);
 }
 
 cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon_hyper* h, void* ws, size_t ws_bytes,
@@ -226,16 +796,15 @@ cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon
     if (!aligned16(ws)) return CF_ERR_INVALID_ARG;
     if (h->steps > 16) return CF_ERR_UNSUPPORTED;
     if (count == 0) return CF_OK;
-    if (ws == nullptr || ws_bytes < cf_muon_workspace_size(count, params)) return CF_ERR_WORKSPACE;
+    std::vector<Mat> mats = list_of(count, params);
+    if (ws == nullptr || ws_bytes < workspace_of(mats)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
     for (int32_t i = 0; i < count; ++i) {
-        const cf_muon_param& q = params[i];
-        const cf_status st = run_matrix(ctx, p, q.rows, q.cols, q.g, 1, q.m, h->momentum, h->nesterov != 0, q.w_bf16, q.w,
-                                        1.f - h->lr * h->weight_decay, h->lr * q.scale, ws);
-        if (st != CF_OK) return st;
+        mats[i].keep = 1.f - h->lr * h->weight_decay;
+        mats[i].step = h->lr * params[i].scale;
     }
-    return CF_OK;
+    return run(ctx, p, h->momentum, h->nesterov != 0, mats, ws);
 }
 
 }  // extern "C"
