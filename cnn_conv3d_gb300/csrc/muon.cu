@@ -46,11 +46,10 @@ constexpr int kMaxMats = 48;              // matrices of one launch
 constexpr int kThreads = 320;             // producer, issuer, eight epilogue warps
 constexpr int kBlk = 64 * 64;             // values of an operand block
 constexpr uint32_t kBlkBytes = kBlk * 2;
-constexpr uint32_t kStageA = 2 * kBlkBytes, kStageB = 4 * kBlkBytes, kStage = kStageA + kStageB;
-constexpr int kStages = 4;
+constexpr uint32_t kStageA = 4 * kBlkBytes, kStageB = 4 * kBlkBytes, kStage = kStageA + kStageB;
+constexpr int kStages = 3;
 constexpr uint32_t kSmem = kStages * kStage + 1024;
 constexpr int kTileF = 128 * 128;         // floats of a Gram tile
-constexpr int kSlices = 8;                // items of phase R per tile: 16 columns each
 
 struct Mat {
     const void* g;
@@ -62,14 +61,16 @@ struct Mat {
     int f32, tall;
     float keep, step;        // w = keep w - step X
     float tau;
+    int vec;                 // rows of the result start at 16 bytes
+    int mr;                  // a tile of phases G and U has mr * 128 rows
     int rb, cb;              // operand blocks: X is rb x cb, A' and B' rb x rb
-    int mt, ut;              // 128-row tiles, 256-column tiles of X
+    int mt, gt, ut;          // 128-row tiles, mr * 128-row tiles, 256-column tiles of X
     int splits, per;         // parts of the long axis in phase G, blocks of each
     int chunks;              // norm partials
     int64_t chunk;           // values of each
     int n0, c0, g0, r0, s0, u0;  // first item of each phase
     __half *xh[2], *xl[2], *ad, *bp;
-    float *part, *norm, *unorm, *alpha;
+    float *d, *part, *norm, *unorm, *alpha;
 };
 
 struct Job {
@@ -197,10 +198,20 @@ enum { PH_G, PH_S, PH_U };
 
 // An item of a product phase: which operand blocks, and how many.
 struct Item {
-    int mat, i, j, split;  // 128-row tile, tile of the other side, part of the long axis
+    int mat, i, j, split;  // tile, tile of the other side, part of the long axis
     int kb0, kb1;          // blocks of the contracted axis
-    int nb;                // 64-column blocks of the tile
+    int mr, nb;            // 128-row parts and 64-column blocks of the tile
 };
+
+// Tile e of those on and above the diagonal of t x t tiles, row by row.
+__device__ __forceinline__ void upper_tile(int e, int t, int& i, int& j) {
+    i = 0;
+    while (e >= t - i) {
+        e -= t - i;
+        ++i;
+    }
+    j = i + e;
+}
 
 template <int PH>
 __device__ __forceinline__ int first_of(const Mat& M) { return PH == PH_G ? M.g0 : PH == PH_S ? M.s0 : M.u0; }
@@ -212,12 +223,13 @@ __device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
     Item t;
     t.mat = mat;
     int e = it - first_of<PH>(M);
+    t.split = 0;
+    t.kb0 = 0;
+    t.kb1 = (M.k + 63) / 64;
+    t.mr = PH == PH_S ? 1 : M.mr;
     if (PH == PH_U) {
-        t.i = e % M.mt;
-        t.j = e / M.mt;
-        t.split = 0;
-        t.kb0 = 0;
-        t.kb1 = (M.k + 63) / 64;
+        t.i = e % M.gt;
+        t.j = e / M.gt;
         t.nb = min(4, M.cb - 4 * t.j);
         return t;
     }
@@ -226,19 +238,9 @@ __device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
         e /= M.splits;
         t.kb0 = t.split * M.per;
         t.kb1 = min(t.kb0 + M.per, M.cb);
-    } else {
-        t.split = 0;
-        t.kb0 = 0;
-        t.kb1 = (M.k + 63) / 64;
     }
-    int i = 0;
-    while (e >= M.mt - i) {
-        e -= M.mt - i;
-        ++i;
-    }
-    t.i = i;
-    t.j = i + e;
-    t.nb = 2;
+    upper_tile(e, PH == PH_G ? M.gt : M.mt, t.i, t.j);
+    t.nb = 2 * t.mr;
     return t;
 }
 
@@ -265,19 +267,20 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
         const __half* a = PH == PH_G ? M.xh[cur] : PH == PH_S ? M.ad : M.bp;
         const int acb = PH == PH_G ? M.cb : M.rb;
         const bool same = PH != PH_U && t.i == t.j;
-        const uint32_t bytes = kStageA + (same ? 0 : t.nb * kBlkBytes);
+        const int ab = 2 * t.mr;
+        const uint32_t bytes = (ab + (same ? 0 : t.nb)) * kBlkBytes;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
             if (!mbar_wait(&sh.empty[P.stage], P.phase ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_PRODUCER_EMPTY)) return;
             uint8_t* s = ring + P.stage * kStage;
             uint64_t* bar = &sh.full[P.stage];
             mbar_arrive_expect_tx(bar, bytes);
-            bulk_load(s, a + ((int64_t)(2 * t.i) * acb + kb) * kBlk, kBlkBytes, bar);
-            bulk_load(s + kBlkBytes, a + ((int64_t)(2 * t.i + 1) * acb + kb) * kBlk, kBlkBytes, bar);
+            for (int q = 0; q < ab; ++q)
+                bulk_load(s + q * kBlkBytes, a + ((int64_t)(ab * t.i + q) * acb + kb) * kBlk, kBlkBytes, bar);
             if (PH == PH_U) {
                 bulk_load(s + kStageA, M.xh[cur] + ((int64_t)kb * M.cb + 4 * t.j) * kBlk, t.nb * kBlkBytes, bar);
             } else if (!same) {
-                bulk_load(s + kStageA, a + ((int64_t)(2 * t.j) * acb + kb) * kBlk, kBlkBytes, bar);
-                bulk_load(s + kStageA + kBlkBytes, a + ((int64_t)(2 * t.j + 1) * acb + kb) * kBlk, kBlkBytes, bar);
+                for (int q = 0; q < ab; ++q)
+                    bulk_load(s + kStageA + q * kBlkBytes, a + ((int64_t)(ab * t.j + q) * acb + kb) * kBlk, kBlkBytes, bar);
             }
             P.issued |= 1u << P.stage;
             P.par = (P.par & ~(1u << P.stage)) | (P.phase << P.stage);
@@ -290,31 +293,36 @@ template <int PH>
 __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, Pipe& P) {
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
     int mat = 0;
-    for (int it = blockIdx.x; it < total; it += gridDim.x, ++P.local) {
+    for (int it = blockIdx.x; it < total; it += gridDim.x) {
         const Item t = item_of<PH>(J, it, mat);
         mat = t.mat;
-        const uint32_t acc = P.local & 1, use = P.local >> 1;
-        if (!mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_TMEM_EMPTY)) return;
+        uint32_t d[2];
+        for (int h = 0; h < t.mr; ++h) {
+            const uint32_t acc = (P.local + h) & 1, use = (P.local + h) >> 1;
+            if (!mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_TMEM_EMPTY)) return;
+            d[h] = sh.tmem + acc * 256;
+        }
         tc_fence_after();
-        const uint32_t d = sh.tmem + acc * 256;
         const bool same = PH != PH_U && t.i == t.j;
-        const uint32_t idesc = PH == PH_U ? idesc_f16(128, 64 * t.nb, 1) : idesc_f16(128, 128, 0);
+        const uint32_t idesc = idesc_f16(128, 64 * t.nb, PH == PH_U);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
             if (!mbar_wait(&sh.full[P.stage], P.phase, &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
             tc_fence_after();
             const uint32_t as = smem_u32(ring + P.stage * kStage), bs = same ? as : as + kStageA;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint64_t ad = sdesc(as + k * 32, 16, 1024, SWZ_128B);
                 // X as [contracted][columns]: 64-column atoms a block apart, 16 contracted rows a step
                 const uint64_t bd = PH == PH_U ? sdesc(bs + k * 2048, kBlkBytes, 1024, SWZ_128B)
                                                : sdesc(bs + k * 32, 16, 1024, SWZ_128B);
-                umma_bf16(d, ad, bd, idesc, kb > t.kb0 || k > 0);
+                umma_bf16(d[0], sdesc(as + k * 32, 16, 1024, SWZ_128B), bd, idesc, kb > t.kb0 || k > 0);
+                if (PH != PH_S && t.mr == 2)
+                    umma_bf16(d[1], sdesc(as + 2 * kBlkBytes + k * 32, 16, 1024, SWZ_128B), bd, idesc, kb > t.kb0 || k > 0);
             }
             umma_commit(&sh.empty[P.stage]);
             P.next();
         }
-        umma_commit(&sh.tfull[acc]);
+        for (int h = 0; h < t.mr; ++h) umma_commit(&sh.tfull[(P.local + h) & 1]);
+        P.local += t.mr;
     }
 }
 
@@ -339,115 +347,185 @@ __device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, in
     return s;
 }
 
+// hi and lo of X at row i, columns j .. j+31.
+struct XRow {
+    uint4 h[4], l[4];
+};
+__device__ __forceinline__ void load_x(const Mat& M, int cur, int i, int j, XRow& x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t at = blocked(i, j + 8 * e, M.cb);
+        x.h[e] = *reinterpret_cast<const uint4*>(M.xh[cur] + at);
+        x.l[e] = *reinterpret_cast<const uint4*>(M.xl[cur] + at);
+    }
+}
+__device__ __forceinline__ void split_f16(const float* y, uint4& hi, uint4& lo) {
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const __half2 h = __floats2half2_rn(y[2 * p], y[2 * p + 1]);
+        const float2 f = __half22float2(h);
+        hw[p] = *reinterpret_cast<const uint32_t*>(&h);
+        lw[p] = pack_f16(y[2 * p] - f.x, y[2 * p + 1] - f.y);
+    }
+    hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return pack_bf16x2(a, b); }
+
+// The result at row i, columns j .. j+31, from the last iterate (scaled by tau).
+__device__ __forceinline__ void write_result(const Mat& M, int i, int j, float (&y)[32]) {
+    const float inv = 1.f / M.tau;
+    const int cnt = min(32, M.n - j);
+    if (M.vec && cnt == 32) {
+        const int64_t base = (int64_t)i * M.n + j;
+        if (M.w) {
+            float4 w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const float4*>(M.w + base + 4 * e);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[e].x = y[4 * e] = M.keep * w[e].x - M.step * (y[4 * e] * inv);
+                w[e].y = y[4 * e + 1] = M.keep * w[e].y - M.step * (y[4 * e + 1] * inv);
+                w[e].z = y[4 * e + 2] = M.keep * w[e].z - M.step * (y[4 * e + 2] * inv);
+                w[e].w = y[4 * e + 3] = M.keep * w[e].w - M.step * (y[4 * e + 3] * inv);
+                *reinterpret_cast<float4*>(M.w + base + 4 * e) = w[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] *= inv;
+        }
+        if (M.o) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(M.o + base + e) =
+                    make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]), pack_bf16(y[e + 4], y[e + 5]),
+                               pack_bf16(y[e + 6], y[e + 7]));
+        }
+        return;
+    }
+    // transposed: the lanes' rows are consecutive values; else a ragged end or rows that start anywhere
+    const int64_t base = M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j, st = M.tall ? M.k : 1;
+    if (M.w) {
+        float w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w[e] = e < cnt ? M.w[base + e * st] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            y[e] = M.keep * w[e] - M.step * (y[e] * inv);
+            if (e < cnt) M.w[base + e * st] = y[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] *= inv;
+    }
+    if (M.o) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e < cnt) M.o[base + e * st] = __bfloat16_as_ushort(__float2bfloat16_rn(y[e]));
+    }
+}
+
 template <int PH>
 __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared& sh, Pipe& P) {
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = (warp - 2) >> 2;
     const int r = 32 * q + lane;
     int mat = 0;
-    for (int it = blockIdx.x; it < total; it += gridDim.x, ++P.local) {
+    for (int it = blockIdx.x; it < total; it += gridDim.x) {
         const Item t = item_of<PH>(J, it, mat);
         mat = t.mat;
         const Mat& M = J.mat[mat];
-        const uint32_t acc = P.local & 1, use = P.local >> 1;
-        if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
-        tc_fence_after();
-        const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
-        const int i = 128 * t.i + r;
-        float* part = PH == PH_U ? nullptr
-                                 : M.part + ((int64_t)(PH == PH_G ? it - M.g0 : (it - M.s0) * M.splits)) * kTileF;
         StepScalars sc{};
         if (PH != PH_G) sc = scalars_of(J, M, step);
-        float usum = 0.f;
-        for (int ch = half; ch < 2 * t.nb; ch += 2) {
-            uint32_t v[32];
-            tmem_ld32(tm + 32 * ch, v);
-            tmem_ld_wait();
-            const int c = 32 * ch;
-            if (PH == PH_G) {
+        for (int hh = 0; hh < t.mr; ++hh, ++P.local) {
+            const uint32_t acc = P.local & 1, use = P.local >> 1;
+            const int i = 128 * (t.mr * t.i + hh) + r;
+            const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
+            XRow x;
+            if (PH == PH_U) load_x(M, cur, i, 256 * t.j + 32 * half, x);
+            if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
+            tc_fence_after();
+            float usum = 0.f;
+            for (int ch = half; ch < 2 * t.nb; ch += 2) {
+                uint32_t v[32];
+                tmem_ld32(tm + 32 * ch, v);
+                const int c = 32 * ch;
+                if (PH == PH_G) {
+                    // 128 columns at a time, as phase R takes them
+                    float* part = M.part + ((int64_t)(it - M.g0) * t.mr * t.mr + hh * t.mr) * kTileF;
+                    tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                                                           __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-            } else if (PH == PH_S) {
-                const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
-                float o[32];
+                    for (int e = 0; e < 32; e += 4)
+                        *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                               __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                } else if (PH == PH_S) {
+                    const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
+                    float* dt = M.d + (int64_t)(it - M.s0) * kTileF;
+                    float4 dd[8];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 dd = *tile_at(part, r, c + e);
-                    o[e] = fmaf(bb, dd.x, J.c * __uint_as_float(v[e]));
-                    o[e + 1] = fmaf(bb, dd.y, J.c * __uint_as_float(v[e + 1]));
-                    o[e + 2] = fmaf(bb, dd.z, J.c * __uint_as_float(v[e + 2]));
-                    o[e + 3] = fmaf(bb, dd.w, J.c * __uint_as_float(v[e + 3]));
-                }
-                const int j = 128 * t.j + c;
+                    for (int e = 0; e < 8; ++e) dd[e] = *tile_at(dt, r, c + 4 * e);
+                    tmem_ld_wait();
+                    float o[32];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4*>(M.bp + blocked(i, j + e, M.rb)) =
-                        make_uint4(pack_f16(o[e], o[e + 1]), pack_f16(o[e + 2], o[e + 3]), pack_f16(o[e + 4], o[e + 5]),
-                                   pack_f16(o[e + 6], o[e + 7]));
-                if (t.i != t.j) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
-                }
-            } else {
-                const int j = 256 * t.j + c;
-                const bool last = step + 1 == J.steps;
-                const float whi = J.a + sc.beta, wlo = J.a + sc.theta;
-                float y[32];
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    const int64_t at = blocked(i, j + e, M.cb);
-                    const uint4 h = *reinterpret_cast<const uint4*>(M.xh[cur] + at);
-                    const uint4 l = *reinterpret_cast<const uint4*>(M.xl[cur] + at);
-                    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hw[p]));
-                        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lw[p]));
-                        y[e + 2 * p] = fmaf(whi, fh.x, fmaf(wlo, fl.x, __uint_as_float(v[e + 2 * p])));
-                        y[e + 2 * p + 1] = fmaf(whi, fh.y, fmaf(wlo, fl.y, __uint_as_float(v[e + 2 * p + 1])));
+                    for (int e = 0; e < 8; ++e) {
+                        o[4 * e] = fmaf(bb, dd[e].x, J.c * __uint_as_float(v[4 * e]));
+                        o[4 * e + 1] = fmaf(bb, dd[e].y, J.c * __uint_as_float(v[4 * e + 1]));
+                        o[4 * e + 2] = fmaf(bb, dd[e].z, J.c * __uint_as_float(v[4 * e + 2]));
+                        o[4 * e + 3] = fmaf(bb, dd[e].w, J.c * __uint_as_float(v[4 * e + 3]));
                     }
-                }
-                if (!last) {
+                    const int j = 128 * t.j + c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t hw[4], lw[4];
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(M.bp + blocked(i, j + e, M.rb)) =
+                            make_uint4(pack_f16(o[e], o[e + 1]), pack_f16(o[e + 2], o[e + 3]), pack_f16(o[e + 4], o[e + 5]),
+                                       pack_f16(o[e + 6], o[e + 7]));
+                    if (t.i != t.j) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
+                    }
+                } else {
+                    const int j = 256 * t.j + c;
+                    const float whi = J.a + sc.beta, wlo = J.a + sc.theta;
+                    const XRow now = x;
+                    if (ch + 2 < 2 * t.nb) load_x(M, cur, i, j + 64, x);
+                    tmem_ld_wait();
+                    float y[32];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t hw[4] = {now.h[e].x, now.h[e].y, now.h[e].z, now.h[e].w};
+                        const uint32_t lw[4] = {now.l[e].x, now.l[e].y, now.l[e].z, now.l[e].w};
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            const float y0 = y[e + 2 * p], y1 = y[e + 2 * p + 1];
-                            const __half2 h = __floats2half2_rn(y0, y1);
-                            const float2 f = __half22float2(h);
-                            hw[p] = *reinterpret_cast<const uint32_t*>(&h);
-                            lw[p] = pack_f16(y0 - f.x, y1 - f.y);
-                            usum = fmaf(y0, y0, fmaf(y1, y1, usum));
+                            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hw[p]));
+                            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lw[p]));
+                            const int f = 8 * e + 2 * p;
+                            y[f] = fmaf(whi, fh.x, fmaf(wlo, fl.x, __uint_as_float(v[f])));
+                            y[f + 1] = fmaf(whi, fh.y, fmaf(wlo, fl.y, __uint_as_float(v[f + 1])));
                         }
-                        const int64_t at = blocked(i, j + e, M.cb);
-                        *reinterpret_cast<uint4*>(M.xh[cur ^ 1] + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                        *reinterpret_cast<uint4*>(M.xl[cur ^ 1] + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
                     }
-                } else if (i < M.k) {
-                    const float inv = 1.f / M.tau;
-                    const int64_t base = M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j, st = M.tall ? M.k : 1;
-                    const int cnt = min(32, M.n - j);
+                    if (step + 1 < J.steps) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e < cnt) {
-                            float x = y[e] * inv;
-                            if (M.w) {
-                                x = M.keep * M.w[base + e * st] - M.step * x;
-                                M.w[base + e * st] = x;
-                            }
-                            if (M.o) M.o[base + e * st] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                        for (int e = 0; e < 4; ++e) {
+                            uint4 hi, lo;
+                            split_f16(&y[8 * e], hi, lo);
+                            const int64_t at = blocked(i, j + 8 * e, M.cb);
+                            *reinterpret_cast<uint4*>(M.xh[cur ^ 1] + at) = hi;
+                            *reinterpret_cast<uint4*>(M.xl[cur ^ 1] + at) = lo;
                         }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) usum = fmaf(y[e], y[e], usum);
+                    } else if (i < M.k) {
+                        write_result(M, i, j, y);
+                    }
                 }
             }
-        }
-        tc_fence_before();
-        mbar_arrive(&sh.tempty[acc]);
-        if (PH == PH_U && step + 1 < J.steps) {
-            for (int o = 16; o; o >>= 1) usum += __shfl_xor_sync(~0u, usum, o);
-            if (lane == 0) M.unorm[8 * (it - M.u0) + warp - 2] = usum;
+            tc_fence_before();
+            mbar_arrive(&sh.tempty[acc]);
+            if (PH == PH_U && step + 1 < J.steps) {
+                for (int o = 16; o; o >>= 1) usum += __shfl_xor_sync(~0u, usum, o);
+                if (lane == 0) M.unorm[8 * ((it - M.u0) * t.mr + hh) + warp - 2] = usum;
+            }
         }
     }
 }
@@ -465,82 +543,111 @@ __device__ __forceinline__ void product_phase(const Job& J, int cur, int step, S
     __syncwarp();
 }
 
-// X in operand form from u, one 64 x 64 block an item.
-__device__ __forceinline__ void convert_phase(const Job& J, Shared& sh, float* buf) {
-    int mat = 0;
+// X in operand form from u: a thread makes eight values of a row at a time, with its lanes along the stored rows.
+__device__ __forceinline__ void convert_phase(const Job& J, Shared& sh) {
+    constexpr int kUnits = kBlk / 8;
+    int mat = 0, have = -1;
+    float pre = 0.f, inv = 0.f;
     for (int it = blockIdx.x; it < J.nc; it += gridDim.x) {
         while (mat + 1 < J.count && it >= J.mat[mat + 1].c0) ++mat;
         const Mat& M = J.mat[mat];
-        const float s = block_sum(M.norm, M.chunks, sh.red), s2 = block_sum(M.norm + kNormChunks, M.chunks, sh.red);
-        // u / (|u| + eps) as (u pre) inv
-        const float pre = isinf(s) ? kDown : 1.f, nrm = sqrtf(isinf(s) ? s2 : s), inv = 1.f / (nrm + J.eps * pre);
+        if (mat != have) {
+            const float s = block_sum(M.norm, M.chunks, sh.red), s2 = block_sum(M.norm + kNormChunks, M.chunks, sh.red);
+            const float nrm = sqrtf(isinf(s) ? s2 : s);
+            // tau u / (|u| + eps) as (u pre) inv
+            pre = isinf(s) ? kDown : 1.f;
+            inv = M.tau / (nrm + J.eps * pre);
+            if (it == M.c0 && threadIdx.x == 0) M.unorm[0] = (nrm * inv) * (nrm * inv);  // |X|^2 of step 0
+            have = mat;
+        }
         const int e = it - M.c0, bi = e / M.cb, bj = e % M.cb;
-        // stored rows and columns of the block
-        const int64_t sr = M.tall ? 64 * bj : 64 * bi, sc = M.tall ? 64 * bi : 64 * bj;
-        for (int t = threadIdx.x; t < kBlk; t += kThreads) {
-            const int r = t >> 6, c = t & 63;
-            const float u = sr + r < M.rows && sc + c < M.cols ? load_u(M, J, (sr + r) * M.cols + sc + c) : 0.f;
-            buf[M.tall ? c * 65 + r : r * 65 + c] = u * pre * inv * M.tau;
-        }
-        __syncthreads();
-        for (int t = threadIdx.x; t < kBlk / 8; t += kThreads) {
-            const int r = t >> 3, c = 8 * (t & 7);
-            uint32_t hw[4], lw[4];
+        for (int t = threadIdx.x; t < kUnits; t += kThreads) {
+            const int r = M.tall ? t & 63 : t >> 3, c = 8 * (M.tall ? t >> 6 : t & 7);
+            const int i = 64 * bi + r, j = 64 * bj + c;
+            float y[8];
+            if (M.vec && j < M.n && i < M.k) {  // rows of a multiple of eight values
+                const int64_t at = (int64_t)i * M.n + j;
+                if (M.f32) {
+                    const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(M.g) + at);
+                    const float4 p = g[0], q = g[1];
+                    y[0] = p.x, y[1] = p.y, y[2] = p.z, y[3] = p.w, y[4] = q.x, y[5] = q.y, y[6] = q.z, y[7] = q.w;
+                    if (M.m) {
+                        const float4* m = reinterpret_cast<const float4*>(M.m + at);
+                        const float4 mp = m[0], mq = m[1];
+                        const float f[8] = {mp.x, mp.y, mp.z, mp.w, mq.x, mq.y, mq.z, mq.w};
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float y0 = buf[r * 65 + c + 2 * p], y1 = buf[r * 65 + c + 2 * p + 1];
-                const __half2 h = __floats2half2_rn(y0, y1);
-                const float2 f = __half22float2(h);
-                hw[p] = *reinterpret_cast<const uint32_t*>(&h);
-                lw[p] = pack_f16(y0 - f.x, y1 - f.y);
+                        for (int x = 0; x < 8; ++x) y[x] = J.nesterov ? fmaf(J.mu, f[x], y[x]) : f[x];
+                    }
+                } else {
+                    const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(M.g) + at);
+                    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) y[2 * x] = __uint_as_float(w[x] << 16), y[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    y[x] = i < M.k && j + x < M.n ? load_u(M, J, M.tall ? (int64_t)(j + x) * M.k + i : (int64_t)i * M.n + j + x) : 0.f;
             }
-            const int64_t at = blocked(64 * bi + r, 64 * bj + c, M.cb);
-            *reinterpret_cast<uint4*>(M.xh[0] + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-            *reinterpret_cast<uint4*>(M.xl[0] + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
+            uint4 hi, lo;
+            split_f16(y, hi, lo);
+            const int64_t at = blocked(i, j, M.cb);
+            *reinterpret_cast<uint4*>(M.xh[0] + at) = hi;
+            *reinterpret_cast<uint4*>(M.xl[0] + at) = lo;
         }
-        if (e == 0 && threadIdx.x == 0) M.unorm[0] = (nrm * inv * M.tau) * (nrm * inv * M.tau);  // |X|^2 of step 0
-        __syncthreads();
     }
 }
 
-// A' of a slice of 16 columns of a Gram tile: the sum of its parts, less alpha on the diagonal, in fp32 (kept in the first
-// part's place) and as an operand, on both sides of the diagonal.
+// A' of a slice of 16 columns and 128 rows of a Gram tile: the sum of its parts, less alpha on the diagonal, in fp32 and as an
+// operand, on both sides of the diagonal.
 __device__ __forceinline__ void reduce_phase(const Job& J, int step, Shared& sh) {
-    int mat = 0;
+    int mat = 0, have = -1;
+    float alpha = 0.f;
     for (int it = blockIdx.x; it < J.nr; it += gridDim.x) {
         while (mat + 1 < J.count && it >= J.mat[mat + 1].r0) ++mat;
         const Mat& M = J.mat[mat];
         const float inv2 = 1.f / (M.tau * M.tau);
-        const float alpha = block_sum(M.unorm, step == 0 ? 1 : 8 * M.mt * M.ut, sh.red) * inv2 / (float)M.k;
-        const int e = it - M.r0, tile = e / kSlices, sl = e % kSlices;
-        if (e == 0 && threadIdx.x == 0) *M.alpha = alpha;
-        int ti = 0, f = tile;
-        while (f >= M.mt - ti) {
-            f -= M.mt - ti;
-            ++ti;
+        if (mat != have) {
+            alpha = block_sum(M.unorm, step == 0 ? 1 : 8 * M.mt * M.ut, sh.red) * inv2 / (float)M.k;
+            have = mat;
         }
-        const int tj = ti + f;
-        float* part = M.part + (int64_t)tile * M.splits * kTileF;
+        const int slices = 8 * M.mr * M.mr;
+        const int e = it - M.r0, sl = e % slices;
+        if (e == 0 && threadIdx.x == 0) *M.alpha = alpha;
+        int gi, gj;
+        upper_tile(e / slices, M.gt, gi, gj);
+        const int sub = sl / 8;  // 128 x 128 part of the tile
+        const int ti = M.mr * gi + sub / M.mr, tj = M.mr * gj + sub % M.mr;
+        if (ti > tj) continue;
+        const int64_t apart = (int64_t)M.mr * M.mr * kTileF;
+        float* part = M.part + (int64_t)(e / slices) * M.splits * apart + sub * kTileF;
+        float* d = M.d + (int64_t)(ti * M.mt - ti * (ti - 1) / 2 + tj - ti) * kTileF;
         if (threadIdx.x < 256) {
-            const int r = threadIdx.x & 127;
+            const int r = threadIdx.x & 127, c = 16 * (sl % 8) + 4 * (threadIdx.x >> 7);
+            float4 s = *tile_at(part, r, c), u = *tile_at(part, r, c + 8);
+#pragma unroll 4
+            for (int w = 1; w < M.splits; ++w) {
+                const float4 x = *tile_at(part + w * apart, r, c), z = *tile_at(part + w * apart, r, c + 8);
+                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+                u.x += z.x, u.y += z.y, u.z += z.z, u.w += z.w;
+            }
+            float o[8] = {s.x, s.y, s.z, s.w, u.x, u.y, u.z, u.w};
+            const int i = 128 * ti + r, j = 128 * tj + c;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                o[x] *= inv2;
+                if (i == j + x + (x & 4) && i < M.k) o[x] -= alpha;
+            }
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const int c = 16 * sl + 8 * p + 4 * (threadIdx.x >> 7);
-                float4 s = *tile_at(part, r, c);
-                for (int w = 1; w < M.splits; ++w) {
-                    const float4 x = *tile_at(part + (int64_t)w * kTileF, r, c);
-                    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-                }
-                const int i = 128 * ti + r, j = 128 * tj + c;
-                float o[4] = {s.x * inv2, s.y * inv2, s.z * inv2, s.w * inv2};
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (i == j + x && i < M.k) o[x] -= alpha;
-                *tile_at(part, r, c) = make_float4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint2*>(M.ad + blocked(i, j, M.rb)) = make_uint2(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]));
+                const float* f = o + 4 * p;
+                *tile_at(d, r, c + 8 * p) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<uint2*>(M.ad + blocked(i, j + 8 * p, M.rb)) = make_uint2(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]));
                 if (ti != tj) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) M.ad[blocked(j + x, i, M.rb)] = __float2half_rn(o[x]);
+                    for (int x = 0; x < 4; ++x) M.ad[blocked(j + 8 * p + x, i, M.rb)] = __float2half_rn(f[x]);
                 }
             }
         }
@@ -575,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
 
     Pipe P;
     uint32_t target = 0;
-    convert_phase(J, sh, reinterpret_cast<float*>(ring));
+    convert_phase(J, sh);
     bool ok = grid_sync(J, target, sh);
     for (int step = 0; ok && step < J.steps; ++step) {
         const int cur = step & 1;
@@ -625,13 +732,21 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Sizes, items and the split of the long axis of matrices that run in one launch.
 void plan_sizes(Mat* mats, int count) {
-    int64_t blocks = 0;
+    int64_t blocks = 0, tiles = 0;
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
         M.tall = M.rows > M.cols;
         M.k = (int)std::min(M.rows, M.cols), M.n = (int)std::max(M.rows, M.cols);
-        M.mt = (M.k + 127) / 128, M.rb = 2 * M.mt, M.cb = (M.n + 63) / 64, M.ut = (M.cb + 3) / 4;
-        blocks += (int64_t)M.mt * (M.mt + 1) / 2 * M.cb;
+        M.vec = !M.tall && M.n % 8 == 0;
+        M.cb = (M.n + 63) / 64, M.ut = (M.cb + 3) / 4;
+        tiles += (int64_t)((M.k + 127) / 128) * M.ut;
+    }
+    for (int i = 0; i < count; ++i) {
+        Mat& M = mats[i];
+        // 256-row tiles fetch a third less for a product than 128-row ones, but there are half as many
+        M.mr = tiles >= 2 * kPlanSms && M.k > 256 ? 2 : 1;
+        M.gt = (M.k + 128 * M.mr - 1) / (128 * M.mr), M.mt = M.mr * M.gt, M.rb = 2 * M.mt;
+        blocks += (int64_t)M.gt * (M.gt + 1) / 2 * M.cb;
     }
     // a CTA's share of phase G's blocks, at least four to a part (a part costs its sums' round trip through memory)
     const int64_t share = std::max<int64_t>(4, (blocks + kPlanSms - 1) / kPlanSms);
@@ -664,7 +779,8 @@ size_t place(Mat* mats, int count, char* base) {
         }
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
-        M.part = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * M.splits * kTileF * sizeof(float)));
+        M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
+        M.part = reinterpret_cast<float*>(take((size_t)M.gt * (M.gt + 1) / 2 * M.splits * M.mr * M.mr * kTileF * sizeof(float)));
         M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
         M.unorm = reinterpret_cast<float*>(take((size_t)M.mt * M.ut * 8 * sizeof(float)));
         M.alpha = reinterpret_cast<float*>(take(sizeof(float)));
@@ -692,13 +808,13 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         for (int i = 0; i < J.count; ++i) {
             Mat& M = J.mat[i] = mats[b + i];
             M.n0 = J.nn, M.c0 = J.nc, M.g0 = J.ng, M.r0 = J.nr, M.s0 = J.ns, M.u0 = J.nu;
-            const int tiles = M.mt * (M.mt + 1) / 2;
+            const int tiles = M.gt * (M.gt + 1) / 2;
             J.nn += M.chunks;
             J.nc += M.rb * M.cb;
             J.ng += tiles * M.splits;
-            J.nr += tiles * kSlices;
-            J.ns += tiles;
-            J.nu += M.mt * M.ut;
+            J.nr += tiles * 8 * M.mr * M.mr;
+            J.ns += M.mt * (M.mt + 1) / 2;
+            J.nu += M.gt * M.ut;
         }
         J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.mu = mu, J.nesterov = nesterov;
         J.sync = static_cast<uint32_t*>(ws);
