@@ -14,11 +14,11 @@
 //                                             beta = b alpha + c alpha^2)
 //   U  X = a X + beta X + B' X; the last step writes the result instead
 //
-// Operands are fp16: X = hi + lo in two of them (22 bits), products take hi
-// alone.  Near the end A is close to I: taking alpha and beta off before
-// rounding keeps the rounding relative to what is left.  Of beta X, the last
-// two steps take hi + lo and the earlier ones hi: there B' X cancels beta X
-// along directions whose singular value is still small, and has hi only.
+// Operands are fp16, X beside its operand form in fp32.  Near the end A is
+// close to I: taking alpha and beta off before rounding keeps the rounding
+// relative to what is left.  Of beta X, the last two steps take X and the
+// earlier ones its operand: there B' X cancels beta X along directions whose
+// singular value is still small, and has the operand only.
 // Simulated against 64 bits (operands rounded, sums exact): 2e-4 to 1e-3 of the
 // result, where rounding A and B with their diagonals gives up to 4e-3.
 // X is scaled by a power of two tau so that its entries stay well inside
@@ -69,8 +69,8 @@ struct Mat {
     int chunks;              // norm partials
     int64_t chunk;           // values of each
     int n0, c0, g0, r0, s0, u0;  // first item of each phase
-    __half *xh[2], *xl[2], *ad, *bp;
-    float *d, *part, *norm, *unorm, *alpha;
+    __half *xh[2], *ad, *bp;
+    float *x, *d, *part, *norm, *unorm, *alpha;
 };
 
 struct Job {
@@ -331,13 +331,16 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The tile's 32 columns c .. c+31 of row r, from tensor memory, as phase G stores them: four columns of all rows in turn.
-__device__ __forceinline__ float4* tile_at(float* part, int r, int c) {
-    return reinterpret_cast<float4*>(part) + (c >> 2) * 128 + r;
+// Columns c .. c+3 of row r of a 128-row tile in fp32: four columns of all rows in turn, so that lanes that own rows (as
+// tensor memory is read) access consecutive 16 bytes.
+__device__ __forceinline__ float4* tile_at(float* tile, int r, int c) {
+    return reinterpret_cast<float4*>(tile) + (c >> 2) * 128 + r;
 }
+// The 128-row tile of X in fp32 that row i is in.
+__device__ __forceinline__ float* x_tile(const Mat& M, int i) { return M.x + (int64_t)(i >> 7) * M.cb * 64 * 128; }
 
 struct StepScalars {
-    float alpha, beta, theta;  // theta: the part of beta that takes hi + lo
+    float alpha, beta, theta;  // theta: the part of beta that takes X in fp32
 };
 __device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, int step) {
     StepScalars s;
@@ -347,29 +350,25 @@ __device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, in
     return s;
 }
 
-// hi and lo of X at row i, columns j .. j+31.
-struct XRow {
-    uint4 h[4], l[4];
-};
-__device__ __forceinline__ void load_x(const Mat& M, int cur, int i, int j, XRow& x) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int64_t at = blocked(i, j + 8 * e, M.cb);
-        x.h[e] = *reinterpret_cast<const uint4*>(M.xh[cur] + at);
-        x.l[e] = *reinterpret_cast<const uint4*>(M.xl[cur] + at);
-    }
+__device__ __forceinline__ uint4 pack8_f16(const float* y) {
+    return make_uint4(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
 }
-__device__ __forceinline__ void split_f16(const float* y, uint4& hi, uint4& lo) {
-    uint32_t hw[4], lw[4];
+// 32 values of row i, columns j .. j+31, into a blocked operand: two 32-byte stores of two chunks each, which the XOR keeps
+// side by side.
+__device__ __forceinline__ void store_row32(__half* op, int i, int j, int cb, const float (&y)[32]) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const __half2 h = __floats2half2_rn(y[2 * p], y[2 * p + 1]);
-        const float2 f = __half22float2(h);
-        hw[p] = *reinterpret_cast<const uint32_t*>(&h);
-        lw[p] = pack_f16(y[2 * p] - f.x, y[2 * p + 1] - f.y);
+    for (int e = 0; e < 32; e += 16) {
+        uint4 p = pack8_f16(&y[e]), q = pack8_f16(&y[e + 8]);
+        if (i & 1) {
+            const uint4 t = p;
+            p = q;
+            q = t;
+        }
+        __half* at = op + (blocked(i, j + e, cb) & ~(int64_t)15);
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(p.x), "r"(p.y), "r"(p.z), "r"(p.w),
+                     "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                     : "memory");
     }
-    hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-    lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return pack_bf16x2(a, b); }
 
@@ -442,8 +441,12 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
             const uint32_t acc = P.local & 1, use = P.local >> 1;
             const int i = 128 * (t.mr * t.i + hh) + r;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
-            XRow x;
-            if (PH == PH_U) load_x(M, cur, i, 256 * t.j + 32 * half, x);
+            float4 x[8];
+            float* xt = PH == PH_U ? x_tile(M, i) : nullptr;
+            if (PH == PH_U) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = *tile_at(xt, r, 256 * t.j + 32 * half + 4 * e);
+            }
             if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
             tc_fence_after();
             float usum = 0.f;
@@ -475,44 +478,30 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
                         o[4 * e + 3] = fmaf(bb, dd[e].w, J.c * __uint_as_float(v[4 * e + 3]));
                     }
                     const int j = 128 * t.j + c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(M.bp + blocked(i, j + e, M.rb)) =
-                            make_uint4(pack_f16(o[e], o[e + 1]), pack_f16(o[e + 2], o[e + 3]), pack_f16(o[e + 4], o[e + 5]),
-                                       pack_f16(o[e + 6], o[e + 7]));
+                    store_row32(M.bp, i, j, M.rb, o);
                     if (t.i != t.j) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
                     }
                 } else {
                     const int j = 256 * t.j + c;
-                    const float whi = J.a + sc.beta, wlo = J.a + sc.theta;
-                    const XRow now = x;
-                    if (ch + 2 < 2 * t.nb) load_x(M, cur, i, j + 64, x);
-                    tmem_ld_wait();
+                    const float wx = J.a + sc.theta, wh = sc.beta - sc.theta;
                     float y[32];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t hw[4] = {now.h[e].x, now.h[e].y, now.h[e].z, now.h[e].w};
-                        const uint32_t lw[4] = {now.l[e].x, now.l[e].y, now.l[e].z, now.l[e].w};
+                    for (int e = 0; e < 8; ++e) y[4 * e] = x[e].x, y[4 * e + 1] = x[e].y, y[4 * e + 2] = x[e].z, y[4 * e + 3] = x[e].w;
+                    if (ch + 2 < 2 * t.nb) {
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hw[p]));
-                            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lw[p]));
-                            const int f = 8 * e + 2 * p;
-                            y[f] = fmaf(whi, fh.x, fmaf(wlo, fl.x, __uint_as_float(v[f])));
-                            y[f + 1] = fmaf(whi, fh.y, fmaf(wlo, fl.y, __uint_as_float(v[f + 1])));
-                        }
+                        for (int e = 0; e < 8; ++e) x[e] = *tile_at(xt, r, j + 64 + 4 * e);
                     }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        y[e] = fmaf(wx, y[e], fmaf(wh, __half2float(__float2half_rn(y[e])), __uint_as_float(v[e])));
                     if (step + 1 < J.steps) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint4 hi, lo;
-                            split_f16(&y[8 * e], hi, lo);
-                            const int64_t at = blocked(i, j + 8 * e, M.cb);
-                            *reinterpret_cast<uint4*>(M.xh[cur ^ 1] + at) = hi;
-                            *reinterpret_cast<uint4*>(M.xl[cur ^ 1] + at) = lo;
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            *tile_at(xt, r, j + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                        store_row32(M.xh[cur ^ 1], i, j, M.cb, y);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) usum = fmaf(y[e], y[e], usum);
                     } else if (i < M.k) {
@@ -591,11 +580,10 @@ __device__ __forceinline__ void convert_phase(const Job& J, Shared& sh) {
             }
 #pragma unroll
             for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
-            uint4 hi, lo;
-            split_f16(y, hi, lo);
-            const int64_t at = blocked(i, j, M.cb);
-            *reinterpret_cast<uint4*>(M.xh[0] + at) = hi;
-            *reinterpret_cast<uint4*>(M.xl[0] + at) = lo;
+            *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = pack8_f16(y);
+            float* xt = x_tile(M, i);
+            *tile_at(xt, i & 127, j) = make_float4(y[0], y[1], y[2], y[3]);
+            *tile_at(xt, i & 127, j + 4) = make_float4(y[4], y[5], y[6], y[7]);
         }
     }
 }
@@ -773,10 +761,8 @@ size_t place(Mat* mats, int count, char* base) {
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
         const size_t xb = (size_t)M.rb * M.cb * kBlkBytes, ab = (size_t)M.rb * M.rb * kBlkBytes;
-        for (int p = 0; p < 2; ++p) {
-            M.xh[p] = reinterpret_cast<__half*>(take(xb));
-            M.xl[p] = reinterpret_cast<__half*>(take(xb));
-        }
+        for (int p = 0; p < 2; ++p) M.xh[p] = reinterpret_cast<__half*>(take(xb));
+        M.x = reinterpret_cast<float*>(take(2 * xb));
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
