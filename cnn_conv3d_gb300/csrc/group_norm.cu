@@ -1,26 +1,40 @@
 // group_norm.cu -- group normalisation of NDHWC volumes with the block's
 // activation and pooling, forward and backward, and their entry points.
 //
-// Forward and backward each are: per-chunk channel sums, their reduction to
-// what a group needs, and one pass that writes the output.
+// Each direction is a pass that sums over row chunks, a small kernel that adds
+// the chunks up and makes the coefficients, and a pass that writes the output.
+// Memory bounds both passes: a chunk is a few rows of every thread and one
+// block's work, so that many blocks are resident and the ends of some lie under
+// the loads of others.  The output pass goes backwards: what the sums read
+// last, and L2 still has, it reads first.
+#include <cuda_bf16.h>
+
 #include <algorithm>
 
 #include "cf_internal.h"
 #include "cf_ptx.cuh"
+#include "fastdiv.cuh"
 
 namespace cf {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
 struct GnArgs {
-    int64_t n, d, h, w, s;  // s = d*h*w
-    int c, groups, cg;
+    int64_t s;               // voxels of a sample
     int64_t xp, yp;
+    int n, d, h, w, c, groups, cg;
+    int tiles, tile;         // column tiles of `tile` vectors (the last may be narrower)
     float slope, eps;
-    int chunks;      // chunks of rows a sample is cut into
-    int64_t rows;    // rows (voxels, or pooled windows) of a chunk
-    int64_t total;   // rows of a sample
+    int chunks;              // row chunks of a sample, in both passes
+    int srows, rows;         // voxels of a chunk in the statistics pass; voxels or windows of a chunk elsewhere
+    int64_t total;           // voxels or windows of a sample
+    FastDiv w2, h2, tdiv, cdiv;  // pooled extents, tile, chunks
+    float2* part;            // sums of a chunk
+    float4* coef;            // [n][c]: (a, mean, beta, rstd)
+    float2* lin;             // [n][c]: the backward's (k0, k1)
+    float2* chan;            // [n][c]: the backward's channel sums of a sample
 };
 
 template <typename T>
@@ -36,308 +50,698 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ uint16_t from_f<uint16_t>(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
+// V values of a voxel, as loaded.
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Pack {
     T v[V];
 };
 template <typename T, int V>
-__device__ __forceinline__ void load(const T* p, float (&f)[V]) {
-    const Pack<T, V> t = *reinterpret_cast<const Pack<T, V>*>(p);
+__device__ __forceinline__ Pack<T, V> load(const T* p) {
+    return *reinterpret_cast<const Pack<T, V>*>(p);
+}
+// Element by element, two at a time where the vector allows it.
+template <int V>
+__device__ __forceinline__ void vsub(float (&o)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = to_f<T>(t.v[e]);
+        for (int e = 0; e < V; e += 2) {
+            const float2 t = __fadd2_rn(make_float2(a[e], a[e + 1]), make_float2(-b[e], -b[e + 1]));
+            o[e] = t.x, o[e + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = a[e] - b[e];
+    }
+}
+template <int V>
+__device__ __forceinline__ void vadd(float (&o)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 t = __fadd2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+            o[e] = t.x, o[e + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = a[e] + b[e];
+    }
+}
+template <int V>
+__device__ __forceinline__ void vfma(float (&o)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 t = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
+            o[e] = t.x, o[e + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(a[e], b[e], c[e]);
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Pack<T, V>& t, float (&f)[V]) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&t);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = to_f<T>(t.v[e]);
+    }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&f)[V]) {
     Pack<T, V> t;
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&t);
 #pragma unroll
-    for (int e = 0; e < V; ++e) t.v[e] = from_f<T>(f[e]);
+        for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) t.v[e] = from_f<T>(f[e]);
+    }
     *reinterpret_cast<Pack<T, V>*>(p) = t;
 }
 
-template <int ACT>
+// 1 / (1 + exp(-u)): to the last bits for fp32 outputs, by the fast exponential and division (relative error about
+// 1e-6 at |u| of 10) where the result is rounded to bf16.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float u) {
+    if (sizeof(T) == 4) return 1.f / (1.f + expf(-u));
+    return __fdividef(1.f, 1.f + __expf(-u));
+}
+template <typename T, int ACT>
 __device__ __forceinline__ float act_of(float u, float slope) {
-    if (ACT == CF_ACT_SILU) return u / (1.f + expf(-u));
+    if (ACT == CF_ACT_SILU) return u * sigmoid<T>(u);
     return u > 0.f ? u : slope * u;
 }
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ float act_grad(float u, float slope) {
     if (ACT == CF_ACT_SILU) {
-        const float e = 1.f / (1.f + expf(-u));
-        return e * (1.f + u * (1.f - e));
+        const float e = sigmoid<T>(u);
+        return e * fmaf(u, 1.f - e, 1.f);
     }
     return u > 0.f ? 1.f : slope;
 }
 
-// The x offset (in values) of voxel k of row r of a sample: a voxel, or voxel k of a pooled window.
-template <int POOL>
-__device__ __forceinline__ int64_t voxel_of(const GnArgs& A, int64_t n, int64_t r, int k) {
-    if (POOL == CF_POOL_NONE) return (n * A.s + r) * A.xp;
-    const int64_t w2 = A.w / 2, h2 = A.h / 2;
-    const int64_t pw = r % w2, q = r / w2, ph = q % h2, pd = q / h2;
-    return (n * A.s + ((2 * pd + (k >> 2)) * A.h + 2 * ph + ((k >> 1) & 1)) * A.w + 2 * pw + (k & 1)) * A.xp;
+// Where a block works: its sample, columns and rows, and where a thread stands in them.
+template <int V>
+struct Place {
+    int sample, chunk, tile;
+    int64_t r0;               // first row
+    int rows, cols, lanes, col, lane, c0, left;  // left: rows of the thread
+    __device__ __forceinline__ Place(const GnArgs& A, int block, int per, int64_t total) {
+        sample = (int)A.cdiv.div(block);
+        chunk = block - sample * A.chunks;
+        tile = blockIdx.y;
+        r0 = (int64_t)chunk * per;
+        rows = (int)min((int64_t)per, total - r0);
+        if (A.tiles == 1) {
+            cols = A.tile;
+            lane = (int)A.tdiv.div(threadIdx.x);
+        } else {
+            cols = min(A.c / V - tile * A.tile, A.tile);
+            lane = threadIdx.x / cols;
+        }
+        lanes = kThreads / cols;
+        col = threadIdx.x - lane * cols;
+        c0 = (tile * A.tile + col) * V;
+        left = lane < lanes && rows > lane ? (int)((uint32_t)(rows - lane + lanes - 1) / (uint32_t)lanes) : 0;
+    }
+};
+
+// The offset in x (in values) of a window's first voxel, and of the others from it.
+__device__ __forceinline__ int64_t window_at(const GnArgs& A, int64_t row) {
+    const uint32_t m = (uint32_t)row, q = A.w2.div(m), pw = m - q * A.w2.d, pd = A.h2.div(q), ph = q - pd * A.h2.d;
+    return (((int64_t)(2 * pd) * A.h + 2 * ph) * A.w + 2 * pw) * A.xp;
+}
+struct Window {
+    int64_t d, h, w;
+    __device__ __forceinline__ Window(const GnArgs& A) : d(A.xp * A.w * A.h), h(A.xp * A.w), w(A.xp) {}
+    __device__ __forceinline__ int64_t at(int k) const { return (k & 4 ? d : 0) + (k & 2 ? h : 0) + (k & 1 ? w : 0); }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
 }
 
-// Channel means and sums of squared deviations of one chunk (part[n][chunk][c] float2).
+// How a block adds up per group: a thread joins `span` neighbouring values of its vector, which are of one group, to a unit;
+// a group is `units` units, a warp takes its units times the row lanes.
+template <int V>
+struct Span {
+    int span, per, units;  // per: units of a vector
+    __device__ __forceinline__ Span(const GnArgs& A) {
+        span = A.cg % V == 0 ? V : V % A.cg == 0 ? A.cg : 1;
+        per = V / span;
+        units = A.cg / span;
+    }
+};
+// Calls f(entry, row lane) for the entries of group g that the block's column tile has, shared out over a warp; an entry is
+// at [unit of the vector][thread].  Returns their number of units.
+template <int V, typename F>
+__device__ __forceinline__ int group_entries(const GnArgs& A, const Place<V>& P, const Span<V>& sp, int g, F f) {
+    const int at0 = P.tile * A.tile * sp.per, wide = P.cols * sp.per;  // units
+    const int qa = max(g * sp.units - at0, 0), qb = min((g + 1) * sp.units - at0, wide);
+    const int lane = threadIdx.x & 31;
+    int lp = 32, sh = 5;  // lanes of the warp that take row lanes; the others take further units
+    while (lp > P.lanes) lp >>= 1, --sh;
+    for (int q = qa + (lane >> sh); q < qb; q += 32 >> sh) {
+        const int col = sp.per == 1 ? q : q / sp.per, slot = q - col * sp.per;
+        for (int l = lane & (lp - 1); l < P.lanes; l += lp) f(slot * kThreads + l * P.cols + col, l);
+    }
+    return qb - qa;
+}
+
+// Mean and sum of squared deviations of each group over a chunk: part[sample][chunk][tile][group].  A thread sums about its
+// first row: a chunk has at most 32 rows for it, and no more than that factor can be lost in the rounding where the first
+// row is far off.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_stats_kernel(GnArgs A, const T* __restrict__ x, float2* __restrict__ part) {
+__global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, const T* __restrict__ x) {
     __shared__ float sm[kThreads * V], sq[kThreads * V];
-    const int cols = min(A.c / V - (int)blockIdx.y * kThreads, kThreads), lanes = kThreads / cols;
-    const int col = threadIdx.x % cols, lane = threadIdx.x / cols;
-    const int64_t n = blockIdx.z, r0 = blockIdx.x * A.rows, r1 = min(r0 + A.rows, A.total);
-    const int c0 = ((int)blockIdx.y * kThreads + col) * V;
+    const Place<V> P(A, blockIdx.x, A.srows, A.s);
     float k[V], s[V], q[V];
-    int64_t cnt = 0;
 #pragma unroll
     for (int e = 0; e < V; ++e) k[e] = s[e] = q[e] = 0.f;
-    if (lane < lanes)
-        for (int64_t r = r0 + lane; r < r1; r += lanes) {
+    if (P.left) {
+        constexpr int U = V > 1 ? 4 : 8;
+        const int64_t step = (int64_t)P.lanes * A.xp;
+        const T* p = x + ((int64_t)P.sample * A.s + P.r0 + P.lane) * A.xp + P.c0;
+        unpack<T, V>(load<T, V>(p), k);
+        auto add = [&](const Pack<T, V>& t) {
             float f[V];
-            load<T, V>(x + (n * A.s + r) * A.xp + c0, f);
+            unpack<T, V>(t, f);
+            vsub<V>(f, f, k);
+            vadd<V>(s, s, f);
+            vfma<V>(q, f, f, q);
+        };
+        int i = P.left;
+        for (; i >= U; i -= U, p += U * step) {
+            Pack<T, V> t[U];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (cnt == 0) k[e] = f[e];
-                const float t = f[e] - k[e];
-                s[e] += t;
-                q[e] = fmaf(t, t, q[e]);
-            }
-            ++cnt;
+            for (int u = 0; u < U; ++u) t[u] = load<T, V>(p + u * step);
+#pragma unroll
+            for (int u = 0; u < U; ++u) add(t[u]);
         }
+        for (; i > 0; --i, p += step) add(load<T, V>(p));
+        const float n = (float)P.left, inv = 1.f / n;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const float m = cnt ? s[e] / (float)cnt : 0.f;
-        sm[threadIdx.x * V + e] = k[e] + m;
-        sq[threadIdx.x * V + e] = fmaxf(q[e] - s[e] * m, 0.f);
+        for (int e = 0; e < V; ++e) {
+            const float d = s[e] * inv;
+            k[e] += d;
+            q[e] = fmaxf(fmaf(-s[e], d, q[e]), 0.f);
+        }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < cols * V; i += kThreads) {
-        const int cc = i / V, e = i % V;
-        float mean = 0.f, m2 = 0.f, have = 0.f;
-        for (int l = 0; l < lanes; ++l) {
-            const int64_t left = r1 - r0 - l;
-            const float nb = left > 0 ? (float)((left + lanes - 1) / lanes) : 0.f;
-            if (nb == 0.f) break;
-            const float mb = sm[(l * cols + cc) * V + e], qb = sq[(l * cols + cc) * V + e];
-            const float tot = have + nb, d = mb - mean;
-            mean += d * (nb / tot);
-            m2 += qb + d * d * (have * nb / tot);
-            have = tot;
+    const Span<V> sp(A);
+    // neighbours of equal counts: the mean of their means, and the deviations from it
+#pragma unroll
+    for (int w = 1; w < V; w *= 2)
+        if (w < sp.span) {
+#pragma unroll
+            for (int e = 0; e + w < V; e += 2 * w) {
+                const float d = k[e + w] - k[e];
+                k[e] = fmaf(0.5f, d, k[e]);
+                q[e] += fmaf(0.5f * (float)(w * P.left) * d, d, q[e + w]);
+            }
         }
-        part[(n * A.chunks + blockIdx.x) * A.c + (int)blockIdx.y * kThreads * V + i] = make_float2(mean, m2);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (e % sp.span == 0) {
+            sm[e / sp.span * kThreads + threadIdx.x] = k[e];
+            sq[e / sp.span * kThreads + threadIdx.x] = q[e];
+        }
+    __syncthreads();
+    // a warp to a group: sums about the mean of its first entry
+    const int first = P.tile * A.tile * V, g0 = first / A.cg, g1 = (first + P.cols * V - 1) / A.cg;
+    const int least = P.rows / P.lanes, more = P.rows - least * P.lanes;  // rows of a lane: least, or one more
+    for (int g = g0 + (threadIdx.x >> 5); g <= g1; g += kWarps) {
+        const int q0 = max(g * sp.units - P.tile * A.tile * sp.per, 0);
+        const float about = sm[q0 % sp.per * kThreads + q0 / sp.per];
+        float a = 0.f, b = 0.f;
+        const int units = group_entries<V>(A, P, sp, g, [&](int at, int l) {
+            const float nl = (float)((least + (l < more)) * sp.span), d = sm[at] - about;
+            a = fmaf(nl, d, a);
+            b += nl > 0.f ? fmaf(nl * d, d, sq[at]) : 0.f;
+        });
+        a = warp_sum(a);
+        b = warp_sum(b);
+        const float d = a / ((float)P.rows * (float)(units * sp.span));
+        if ((threadIdx.x & 31) == 0)
+            A.part[((int64_t)blockIdx.x * A.tiles + P.tile) * A.groups + g] = make_float2(about + d, fmaxf(fmaf(-a, d, b), 0.f));
     }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
-    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(~0u, v, o);
+// Channels of group g in column tile t.
+template <int V>
+__device__ __forceinline__ int channels_in(const GnArgs& A, int g, int t) {
+    const int b = t * A.tile * V, e = min(b + A.tile * V, A.c);
+    return max(min((g + 1) * A.cg, e) - max(g * A.cg, b), 0);
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    v = warp_sum(v);
+    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    double t = 0.0;
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) t += red[i];
-    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) t += red[i];
     return t;
 }
 
-// mean and rstd of a group from the chunks' channel statistics.
-__global__ void __launch_bounds__(kThreads) gn_stats_reduce_kernel(GnArgs A, const float2* __restrict__ part,
-                                                                  float* __restrict__ mean, float* __restrict__ rstd) {
-    __shared__ double red[kThreads / 32];
-    const int64_t n = blockIdx.x / A.groups;
-    const int g = blockIdx.x % A.groups;
-    const int items = A.chunks * A.cg;
-    const double count = (double)A.s * A.cg;
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int ch = i / A.cg;
-        const double nb = (double)min(A.rows, A.total - ch * A.rows);
-        sum += nb * (double)part[(n * A.chunks + ch) * A.c + g * A.cg + i % A.cg].x;
+// Mean and rstd of a group from the chunks' statistics, a block to a group, and the coefficients of its channels.
+template <int V>
+__global__ void __launch_bounds__(kThreads) gn_finish_kernel(const GnArgs A, const float* __restrict__ gamma,
+                                                            const float* __restrict__ beta, float* __restrict__ mean,
+                                                            float* __restrict__ rstd) {
+    __shared__ float red[kWarps];
+    const int sample = blockIdx.x / A.groups, g = blockIdx.x - sample * A.groups, items = A.chunks * A.tiles;
+    const float2* p = A.part + (int64_t)sample * items * A.groups + g;
+    const float count = (float)A.s * (float)A.cg;
+    auto weight = [&](int i) {
+        const int ch = A.tiles == 1 ? i : i / A.tiles, nc = A.tiles == 1 ? A.cg : channels_in<V>(A, g, i - ch * A.tiles);
+        return (float)min((int64_t)A.srows, A.s - (int64_t)ch * A.srows) * (float)nc;
+    };
+    // the first pass's values stay in registers for the second where a thread has no more than eight
+    constexpr int kKeep = 8;
+    float2 v[kKeep];
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        v[u] = i < items && weight(i) > 0.f ? p[(int64_t)i * A.groups] : make_float2(0.f, 0.f);
     }
-    const double mu = block_sum(sum, red) / count;
-    double m2 = 0.0;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int ch = i / A.cg;
-        const double nb = (double)min(A.rows, A.total - ch * A.rows);
-        const float2 p = part[(n * A.chunks + ch) * A.c + g * A.cg + i % A.cg];
-        m2 += (double)p.y + nb * ((double)p.x - mu) * ((double)p.x - mu);
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        if (i < items && weight(i) > 0.f) s = fmaf(weight(i), v[u].x, s);
     }
-    const double var = block_sum(m2, red) / count;
+    for (int i = threadIdx.x + kKeep * kThreads; i < items; i += kThreads)
+        if (weight(i) > 0.f) s = fmaf(weight(i), p[(int64_t)i * A.groups].x, s);
+    const float mu = block_sum(s, red) / count;
+    float q = 0.f;
+    auto dev = [&](int i, float2 t) {
+        const float d = t.x - mu;
+        q += fmaf(weight(i) * d, d, t.y);
+    };
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        if (i < items && weight(i) > 0.f) dev(i, v[u]);
+    }
+    for (int i = threadIdx.x + kKeep * kThreads; i < items; i += kThreads)
+        if (weight(i) > 0.f) dev(i, p[(int64_t)i * A.groups]);
+    const float rs = 1.f / sqrtf(block_sum(q, red) / count + A.eps);
     if (threadIdx.x == 0) {
-        mean[blockIdx.x] = (float)mu;
-        rstd[blockIdx.x] = (float)(1.0 / sqrt(var + (double)A.eps));
+        if (mean) mean[blockIdx.x] = mu;
+        if (rstd) rstd[blockIdx.x] = rs;
+    }
+    for (int i = threadIdx.x; i < A.cg; i += kThreads) {
+        const int c = g * A.cg + i;
+        A.coef[(int64_t)sample * A.c + c] = make_float4((gamma ? gamma[c] : 1.f) * rs, mu, beta ? beta[c] : 0.f, rs);
     }
 }
 
-// u = a (x - mean) + b: taking the mean off first keeps u exact to its own size where |mean| is large against the deviation.
 template <int V>
-__device__ __forceinline__ void affine(const GnArgs& A, int64_t n, int c0, const float* __restrict__ gamma,
-                                       const float* __restrict__ beta, const float* __restrict__ mean,
-                                       const float* __restrict__ rstd, float (&a)[V], float (&b)[V], float (&m)[V],
-                                       float (&r)[V]) {
+__device__ __forceinline__ void load_coef(const GnArgs& A, const Place<V>& P, float (&a)[V], float (&m)[V], float (&be)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int g = (c0 + e) / A.cg;
-        m[e] = mean[n * A.groups + g];
-        r[e] = rstd[n * A.groups + g];
-        a[e] = (gamma ? gamma[c0 + e] : 1.f) * r[e];
-        b[e] = beta ? beta[c0 + e] : 0.f;
+        const float4 t = __ldg(&A.coef[(int64_t)P.sample * A.c + P.c0 + e]);
+        a[e] = t.x, m[e] = t.y, be[e] = t.z;
     }
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The value among eight voxels that maximises u = a (x - mean) + beta: the maximum, or for a < 0 the minimum, taken on packed
+// bf16 with the sign bits of such channels flipped.
+template <typename T, int V>
+__device__ __forceinline__ void window_max(const Pack<T, V>* t, const float (&a)[V], float (&best)[V]) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const uint32_t flip = (a[2 * e] < 0.f ? 0x8000u : 0u) | (a[2 * e + 1] < 0.f ? 0x80000000u : 0u);
+            uint32_t m = reinterpret_cast<const uint32_t*>(&t[0])[e] ^ flip;
+#pragma unroll
+            for (int k = 1; k < 8; ++k) m = max_bf16x2(m, reinterpret_cast<const uint32_t*>(&t[k])[e] ^ flip);
+            m ^= flip;
+            best[2 * e] = __uint_as_float(m << 16);
+            best[2 * e + 1] = __uint_as_float(m & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            best[e] = to_f<T>(t[0].v[e]);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {
+                const float f = to_f<T>(t[k].v[e]);
+                best[e] = a[e] < 0.f ? fminf(best[e], f) : fmaxf(best[e], f);
+            }
+        }
+    }
+    // a = 0: every voxel's u is beta, and the first is the maximum
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (a[e] == 0.f) best[e] = to_f<T>(t[0].v[e]);
 }
 
 template <typename T, int V, int POOL, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_apply_kernel(GnArgs A, const T* __restrict__ x, const float* __restrict__ gamma,
-                                                           const float* __restrict__ beta, const float* __restrict__ mean,
-                                                           const float* __restrict__ rstd, T* __restrict__ y) {
-    const int cols = min(A.c / V - (int)blockIdx.y * kThreads, kThreads), lanes = kThreads / cols;
-    const int col = threadIdx.x % cols, lane = threadIdx.x / cols;
-    if (lane >= lanes) return;
-    const int64_t n = blockIdx.z, r0 = blockIdx.x * A.rows, r1 = min(r0 + A.rows, A.total);
-    const int c0 = ((int)blockIdx.y * kThreads + col) * V;
-    float a[V], b[V], m[V], rs[V];
-    affine<V>(A, n, c0, gamma, beta, mean, rstd, a, b, m, rs);
-    for (int64_t r = r0 + lane; r < r1; r += lanes) {
-        float o[V], f[V];
+__global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 4 : 3) gn_apply_kernel(const GnArgs A, const T* __restrict__ x,
+                                                                                       T* __restrict__ y) {
+    const Place<V> P(A, gridDim.x - 1 - blockIdx.x, A.rows, A.total);
+    if (!P.left) return;
+    float a[V], m[V], be[V];
+    load_coef<V>(A, P, a, m, be);
+    const T* xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
+    T* o = y + ((int64_t)P.sample * A.total + P.r0 + P.lane) * A.yp + P.c0;
+    const int64_t ystep = (int64_t)P.lanes * A.yp;
+    auto norm = [&](float (&f)[V]) {
+        vsub<V>(f, f, m);
+        vfma<V>(f, a, f, be);
+    };
+    if constexpr (POOL == CF_POOL_NONE) {
+        constexpr int U = V > 1 ? 4 : 8;
+        const int64_t xstep = (int64_t)P.lanes * A.xp;
+        const T* p = xs + (P.r0 + P.lane) * A.xp;
+        auto one = [&](const Pack<T, V>& t, T* at) {
+            float f[V];
+            unpack<T, V>(t, f);
+            norm(f);
 #pragma unroll
-        for (int k = 0; k < (POOL == CF_POOL_NONE ? 1 : 8); ++k) {
-            load<T, V>(x + voxel_of<POOL>(A, n, r, k) + c0, f);
+            for (int e = 0; e < V; ++e) f[e] = act_of<T, ACT>(f[e], A.slope);
+            store<T, V>(at, f);
+        };
+        int i = P.left;
+        for (; i >= U; i -= U, p += U * xstep, o += U * ystep) {
+            Pack<T, V> t[U];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float u = fmaf(a[e], f[e] - m[e], b[e]);
-                if (POOL == CF_POOL_MAX)
-                    o[e] = k == 0 || u > o[e] ? u : o[e];
-                else if (POOL == CF_POOL_AVG)
-                    o[e] = (k == 0 ? 0.f : o[e]) + act_of<ACT>(u, A.slope);
-                else
-                    o[e] = u;
-            }
+            for (int u = 0; u < U; ++u) t[u] = load<T, V>(p + u * xstep);
+#pragma unroll
+            for (int u = 0; u < U; ++u) one(t[u], o + u * ystep);
         }
+        for (; i > 0; --i, p += xstep, o += ystep) one(load<T, V>(p), o);
+    } else {
+        const Window W(A);
+        int64_t row = P.r0 + P.lane;
+        for (int i = 0; i < P.left; ++i, row += P.lanes, o += ystep) {
+            const T* p = xs + window_at(A, row);
+            Pack<T, V> t[8];
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = POOL == CF_POOL_AVG ? 0.125f * o[e] : act_of<ACT>(o[e], A.slope);
-        store<T, V>(y + (n * A.total + r) * A.yp + c0, o);
+            for (int q = 0; q < 8; ++q) t[q] = load<T, V>(p + W.at(q));
+            float f[V];
+            if (POOL == CF_POOL_MAX) {
+                window_max<T, V>(t, a, f);
+                norm(f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) f[e] = act_of<T, ACT>(f[e], A.slope);
+            } else {
+                float sum[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    unpack<T, V>(t[q], f);
+                    norm(f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sum[e] += act_of<T, ACT>(f[e], A.slope);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) f[e] = 0.125f * sum[e];
+            }
+            store<T, V>(o, f);
+        }
     }
 }
 
-// du of the rows' voxels; PASS 0: channel sums of du and du xh of a chunk (part[n][chunk][c] float2);
-// PASS 1: dx from the groups' means s1, s2 (coef[n][groups] float2).
-template <typename T, int V, int POOL, int ACT, int PASS>
-__global__ void __launch_bounds__(kThreads) gn_bwd_kernel(GnArgs A, const T* __restrict__ x, const float* __restrict__ gamma,
-                                                         const float* __restrict__ beta, const float* __restrict__ mean,
-                                                         const float* __restrict__ rstd, const T* __restrict__ dy,
-                                                         const float2* __restrict__ coef, float2* __restrict__ part,
-                                                         T* __restrict__ dx) {
-    __shared__ float sb[PASS == 0 ? kThreads * V : 1], sg[PASS == 0 ? kThreads * V : 1];
-    const int cols = min(A.c / V - (int)blockIdx.y * kThreads, kThreads), lanes = kThreads / cols;
-    const int col = threadIdx.x % cols, lane = threadIdx.x / cols;
-    const int64_t n = blockIdx.z, r0 = blockIdx.x * A.rows, r1 = min(r0 + A.rows, A.total);
-    const int c0 = ((int)blockIdx.y * kThreads + col) * V;
-    constexpr int K = POOL == CF_POOL_NONE ? 1 : 8;
+// Coefficients of the backward, [n][c], from the forward's statistics.
+__global__ void __launch_bounds__(kThreads) gn_coef_kernel(const GnArgs A, const float* __restrict__ gamma,
+                                                          const float* __restrict__ beta, const float* __restrict__ mean,
+                                                          const float* __restrict__ rstd) {
+    const int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    if (i >= (int64_t)A.n * A.c) return;
+    const int64_t n = i / A.c;
+    const int c = (int)(i - n * A.c);
+    const int64_t g = n * A.groups + c / A.cg;
+    const float rs = rstd[g];
+    A.coef[i] = make_float4((gamma ? gamma[c] : 1.f) * rs, mean[g], beta ? beta[c] : 0.f, rs);
+}
+
+// Channel sums of du and du xh over a chunk: part[sample][chunk][c].
+template <typename T, int V, int POOL, int ACT>
+__global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 3 : 2) gn_bwd_sums_kernel(const GnArgs A, const T* __restrict__ x,
+                                                                                          const T* __restrict__ dy) {
+    __shared__ float sb[kThreads * V], sg[kThreads * V];
+    const Place<V> P(A, blockIdx.x, A.rows, A.total);
     float db[V], dg[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) db[e] = dg[e] = 0.f;
-    if (lane < lanes) {
-        float a[V], b[V], m[V], rs[V], s1[V], s2[V], ga[V];
-        affine<V>(A, n, c0, gamma, beta, mean, rstd, a, b, m, rs);
+    if (P.left) {
+        float a[V], m[V], be[V];
+        load_coef<V>(A, P, a, m, be);
+        const T* xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
+        const T* q = dy + ((int64_t)P.sample * A.total + P.r0 + P.lane) * A.yp + P.c0;
+        const int64_t ystep = (int64_t)P.lanes * A.yp;
+        auto add = [&](float (&f)[V], float (&g)[V]) {
+            float u[V];
+            vsub<V>(f, f, m);
+            vfma<V>(u, a, f, be);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            ga[e] = gamma ? gamma[c0 + e] : 1.f;
-            if (PASS == 1) {
-                const float2 t = coef[n * A.groups + (c0 + e) / A.cg];
-                s1[e] = t.x;
-                s2[e] = t.y;
+            for (int e = 0; e < V; ++e) u[e] = g[e] * act_grad<T, ACT>(u[e], A.slope);
+            vadd<V>(db, db, u);
+            vfma<V>(dg, u, f, dg);
+        };
+        if constexpr (POOL == CF_POOL_NONE) {
+            constexpr int U = V > 1 ? 2 : 4;
+            const int64_t xstep = (int64_t)P.lanes * A.xp;
+            const T* p = xs + (P.r0 + P.lane) * A.xp;
+            auto one = [&](const Pack<T, V>& tx, const Pack<T, V>& td) {
+                float f[V], g[V];
+                unpack<T, V>(tx, f);
+                unpack<T, V>(td, g);
+                add(f, g);
+            };
+            int i = P.left;
+            for (; i >= U; i -= U, p += U * xstep, q += U * ystep) {
+                Pack<T, V> tx[U], td[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) tx[u] = load<T, V>(p + u * xstep), td[u] = load<T, V>(q + u * ystep);
+#pragma unroll
+                for (int u = 0; u < U; ++u) one(tx[u], td[u]);
             }
-        }
-        for (int64_t r = r0 + lane; r < r1; r += lanes) {
-            float g[V], best[V], f[V];
-            int at[V];
-            load<T, V>(dy + (n * A.total + r) * A.yp + c0, g);
-            if (POOL == CF_POOL_MAX) {
+            for (; i > 0; --i, p += xstep, q += ystep) one(load<T, V>(p), load<T, V>(q));
+        } else {
+            const Window W(A);
+            int64_t row = P.r0 + P.lane;
+            for (int i = 0; i < P.left; ++i, row += P.lanes, q += ystep) {
+                const T* p = xs + window_at(A, row);
+                Pack<T, V> t[8];
+                const Pack<T, V> td = load<T, V>(q);
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    load<T, V>(x + voxel_of<POOL>(A, n, r, k) + c0, f);
+                for (int w = 0; w < 8; ++w) t[w] = load<T, V>(p + W.at(w));
+                float f[V], g[V];
+                unpack<T, V>(td, g);
+                if (POOL == CF_POOL_MAX) {
+                    window_max<T, V>(t, a, f);
+                    add(f, g);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float u = fmaf(a[e], f[e] - m[e], b[e]);
-                        if (k == 0 || u > best[e]) {
-                            best[e] = u;
-                            at[e] = k;
-                        }
+                    for (int e = 0; e < V; ++e) g[e] *= 0.125f;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) {
+                        unpack<T, V>(t[w], f);
+                        add(f, g);
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < V; ++e) g[e] *= act_grad<ACT>(best[e], A.slope);
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float o[V];
-                const int64_t vox = voxel_of<POOL>(A, n, r, k) + c0;
-                load<T, V>(x + vox, f);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float du;
-                    if (POOL == CF_POOL_MAX)
-                        du = at[e] == k ? g[e] : 0.f;
-                    else
-                        du = (POOL == CF_POOL_AVG ? 0.125f : 1.f) * g[e] * act_grad<ACT>(fmaf(a[e], f[e] - m[e], b[e]), A.slope);
-                    const float xh = (f[e] - m[e]) * rs[e];
-                    if (PASS == 0) {
-                        db[e] += du;
-                        dg[e] = fmaf(du, xh, dg[e]);
-                    } else {
-                        o[e] = rs[e] * (ga[e] * du - s1[e] - xh * s2[e]);
-                    }
-                }
-                if (PASS == 1) store<T, V>(dx + vox, o);
             }
         }
+#pragma unroll
+        for (int e = 0; e < V; ++e) dg[e] *= __ldg(&A.coef[(int64_t)P.sample * A.c + P.c0 + e]).w;
     }
-    if (PASS == 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            sb[threadIdx.x * V + e] = db[e];
-            sg[threadIdx.x * V + e] = dg[e];
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < cols * V; i += kThreads) {
-            float tb = 0.f, tg = 0.f;
-            for (int l = 0; l < lanes; ++l) {
-                tb += sb[(l * cols) * V + i];
-                tg += sg[(l * cols) * V + i];
+    for (int e = 0; e < V; ++e) {
+        sb[e * kThreads + threadIdx.x] = db[e];
+        sg[e * kThreads + threadIdx.x] = dg[e];
+    }
+    __syncthreads();
+    // a channel's row lanes are added up by as many neighbouring threads as the block has for it
+    const int wide = P.cols * V;
+    float2* part = A.part + (int64_t)blockIdx.x * A.c + P.tile * A.tile * V;
+    int lp = 1;
+    while (2 * lp <= 32 && 2 * lp <= P.lanes && 2 * lp * wide <= kThreads) lp *= 2;
+    for (int i = threadIdx.x / lp; i < (wide + 31) / 32 * 32; i += kThreads / lp) {  // whole warps, for the shuffles
+        float tb = 0.f, tg = 0.f;
+        if (i < wide)
+            for (int l = threadIdx.x & (lp - 1); l < P.lanes; l += lp) {
+                tb += sb[i % V * kThreads + l * P.cols + i / V];
+                tg += sg[i % V * kThreads + l * P.cols + i / V];
             }
-            part[(n * A.chunks + blockIdx.x) * A.c + (int)blockIdx.y * kThreads * V + i] = make_float2(tb, tg);
+        for (int o = lp / 2; o; o >>= 1) {
+            tb += __shfl_xor_sync(~0u, tb, o);
+            tg += __shfl_xor_sync(~0u, tg, o);
         }
+        if (i < wide && (threadIdx.x & (lp - 1)) == 0) part[i] = make_float2(tb, tg);
     }
 }
 
-// Blocks 0 .. n*groups-1: a group's means of gamma du and gamma du xh; the rest: dbeta and dgamma of 256 channels each.
-__global__ void __launch_bounds__(kThreads) gn_bwd_reduce_kernel(GnArgs A, const float2* __restrict__ part,
-                                                                const float* __restrict__ gamma, float2* __restrict__ coef,
-                                                                float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    __shared__ double red[kThreads / 32];
-    const int64_t ng = A.n * A.groups;
-    if (blockIdx.x < ng) {
-        const int64_t n = blockIdx.x / A.groups;
-        const int g = blockIdx.x % A.groups;
-        double s1 = 0.0, s2 = 0.0;
-        for (int i = threadIdx.x; i < A.chunks * A.cg; i += kThreads) {
-            const int ch = i / A.cg, c = g * A.cg + i % A.cg;
-            const float2 p = part[(n * A.chunks + ch) * A.c + c];
-            const double ga = gamma ? gamma[c] : 1.f;
-            s1 += ga * (double)p.x;
-            s2 += ga * (double)p.y;
+// A group's channel sums from the chunks', a block to a group of a sample, and the rest of dx's coefficients:
+// dx = a du + k1 (x - mean) + k0 with k0 = -rstd s1, k1 = -rstd^2 s2, s1 and s2 the group's means of gamma du and gamma du xh.
+__global__ void __launch_bounds__(kThreads) gn_bwd_finish_kernel(const GnArgs A, const float* __restrict__ gamma) {
+    __shared__ float2 red[kThreads];
+    __shared__ float rw[kWarps];
+    const int sample = blockIdx.x / A.groups, g = blockIdx.x - sample * A.groups;
+    const float2* p = A.part + (int64_t)sample * A.chunks * A.c + g * A.cg;
+    const int64_t base = (int64_t)sample * A.c + g * A.cg;
+    float s1 = 0.f, s2 = 0.f;
+    for (int c0 = 0; c0 < A.cg; c0 += kThreads) {
+        const int cols = min(A.cg - c0, kThreads), lanes = kThreads / cols, lane = threadIdx.x / cols, col = threadIdx.x - lane * cols;
+        float tb = 0.f, tg = 0.f;
+        if (lane < lanes) {
+#pragma unroll 8
+            for (int i = lane; i < A.chunks; i += lanes) {
+                const float2 v = p[(int64_t)i * A.c + c0 + col];
+                tb += v.x;
+                tg += v.y;
+            }
         }
-        const double count = (double)A.s * A.cg;
-        s1 = block_sum(s1, red);
-        s2 = block_sum(s2, red);
-        if (threadIdx.x == 0) coef[blockIdx.x] = make_float2((float)(s1 / count), (float)(s2 / count));
+        __syncthreads();
+        red[threadIdx.x] = make_float2(tb, tg);
+        __syncthreads();
+        // the lanes of a column in turn by halves
+        for (int have = lanes; have > 1; have = (have + 1) / 2) {
+            const int half = (have + 1) / 2;
+            float2 t = red[threadIdx.x];
+            if (lane < have - half) {
+                const float2 u = red[threadIdx.x + half * cols];
+                t.x += u.x, t.y += u.y;
+                red[threadIdx.x] = t;
+            }
+            __syncthreads();
+        }
+        if (lane == 0) {
+            const float2 t = red[col];
+            A.chan[base + c0 + col] = t;
+            const float ga = gamma ? gamma[g * A.cg + c0 + col] : 1.f;
+            s1 = fmaf(ga, t.x, s1);
+            s2 = fmaf(ga, t.y, s2);
+        }
+    }
+    const float inv = 1.f / ((float)A.s * (float)A.cg), rs = A.coef[base].w;
+    const float k0 = -rs * (block_sum(s1, rw) * inv), k1 = -rs * rs * (block_sum(s2, rw) * inv);
+    for (int i = threadIdx.x; i < A.cg; i += kThreads) A.lin[base + i] = make_float2(k0, k1);
+}
+
+// dx of a chunk; the blocks from `work` on add up the samples' channel sums instead: dbeta, dgamma.
+template <typename T, int V, int POOL, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs A, const T* __restrict__ x, const T* __restrict__ dy,
+                                                                  T* __restrict__ dx, int work, float* __restrict__ dgamma,
+                                                                  float* __restrict__ dbeta) {
+    if ((int)blockIdx.x >= work) {
+        const int c = ((int)blockIdx.x - work) * kThreads + threadIdx.x;
+        if (blockIdx.y != 0 || c >= A.c) return;
+        float tb = 0.f, tg = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < A.n; ++i) {
+            const float2 v = A.chan[(int64_t)i * A.c + c];
+            tb += v.x;
+            tg += v.y;
+        }
+        if (dbeta) dbeta[c] = tb;
+        if (dgamma) dgamma[c] = tg;
         return;
     }
-    const int c = (int)(blockIdx.x - ng) * kThreads + threadIdx.x;
-    if (c >= A.c) return;
-    double tb = 0.0, tg = 0.0;
-    for (int64_t i = 0; i < A.n * A.chunks; ++i) {
-        const float2 p = part[i * A.c + c];
-        tb += (double)p.x;
-        tg += (double)p.y;
+    const Place<V> P(A, work - 1 - blockIdx.x, A.rows, A.total);
+    if (!P.left) return;
+    float a[V], m[V], be[V], k0[V], k1[V];
+    load_coef<V>(A, P, a, m, be);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float2 t = __ldg(&A.lin[(int64_t)P.sample * A.c + P.c0 + e]);
+        k0[e] = t.x, k1[e] = t.y;
     }
-    if (dbeta) dbeta[c] = (float)tb;
-    if (dgamma) dgamma[c] = (float)tg;
+    const T* xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
+    T* os = dx + (int64_t)P.sample * A.s * A.xp + P.c0;
+    const T* q = dy + ((int64_t)P.sample * A.total + P.r0 + P.lane) * A.yp + P.c0;
+    const int64_t ystep = (int64_t)P.lanes * A.yp;
+    if constexpr (POOL == CF_POOL_NONE) {
+        constexpr int U = V > 1 ? 2 : 4;
+        const int64_t xstep = (int64_t)P.lanes * A.xp;
+        const T* p = xs + (P.r0 + P.lane) * A.xp;
+        T* o = os + (P.r0 + P.lane) * A.xp;
+        auto one = [&](const Pack<T, V>& tx, const Pack<T, V>& td, T* at) {
+            float f[V], g[V], u[V];
+            unpack<T, V>(tx, f);
+            unpack<T, V>(td, g);
+            vsub<V>(f, f, m);
+            vfma<V>(u, a, f, be);
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] *= act_grad<T, ACT>(u[e], A.slope);
+            vfma<V>(f, k1, f, k0);
+            vfma<V>(f, a, g, f);
+            store<T, V>(at, f);
+        };
+        int i = P.left;
+        for (; i >= U; i -= U, p += U * xstep, q += U * ystep, o += U * xstep) {
+            Pack<T, V> tx[U], td[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) tx[u] = load<T, V>(p + u * xstep), td[u] = load<T, V>(q + u * ystep);
+#pragma unroll
+            for (int u = 0; u < U; ++u) one(tx[u], td[u], o + u * xstep);
+        }
+        for (; i > 0; --i, p += xstep, q += ystep, o += xstep) one(load<T, V>(p), load<T, V>(q), o);
+    } else {
+        const Window W(A);
+        int64_t row = P.r0 + P.lane;
+        for (int i = 0; i < P.left; ++i, row += P.lanes, q += ystep) {
+            const int64_t at = window_at(A, row);
+            Pack<T, V> t[8];
+            const Pack<T, V> td = load<T, V>(q);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) t[w] = load<T, V>(xs + at + W.at(w));
+            float g[V], best[V], u[V];
+            unpack<T, V>(td, g);
+            if (POOL == CF_POOL_MAX) {
+                window_max<T, V>(t, a, best);
+                vsub<V>(u, best, m);
+                vfma<V>(u, a, u, be);
+#pragma unroll
+                for (int e = 0; e < V; ++e) g[e] *= a[e] * act_grad<T, ACT>(u[e], A.slope);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) g[e] *= 0.125f;
+            }
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                float f[V], lin[V];
+                unpack<T, V>(t[w], f);
+                vsub<V>(u, f, m);
+                vfma<V>(lin, k1, u, k0);
+                if (POOL == CF_POOL_MAX) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        // the first voxel that has the maximum takes the gradient and leaves none
+                        const bool hit = f[e] == best[e];
+                        lin[e] += hit ? g[e] : 0.f;
+                        g[e] = hit ? 0.f : g[e];
+                    }
+                } else {
+                    vfma<V>(u, a, u, be);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) u[e] = g[e] * act_grad<T, ACT>(u[e], A.slope);
+                    vfma<V>(lin, a, u, lin);
+                }
+                store<T, V>(os + at + W.at(w), lin);
+            }
+        }
+    }
 }
 
 bool desc_ok(const cf_gn_desc* d) {
@@ -359,98 +763,118 @@ cf_status supported(const cf_gn_desc* d) {
     return CF_OK;
 }
 
-// Chunks of a sample: about four blocks of each pass to an SM, at least 32 rows a chunk.
-GnArgs make_args(const cf_gn_desc* d, int num_sms, bool pooled_rows) {
+// Values of a vector access: 16 bytes where channels and pitches allow it, else one value.
+int vec_of(const cf_gn_desc* d) {
+    const int v = d->dtype == CF_DT_F32 ? 4 : 8;
+    const int64_t xp = d->x_pitch ? d->x_pitch : d->c, yp = d->y_pitch ? d->y_pitch : d->c;
+    return d->c % v == 0 && xp % v == 0 && yp % v == 0 ? v : 1;
+}
+
+// Chunks are cut for this many blocks, whatever the device: the workspace's size and the sums' order depend on the
+// descriptor alone.
+constexpr int kPlanBlocks = 4 * 152;
+// Voxels of a thread in a chunk, at most: at 16 bytes each a block reads 64 KB.
+constexpr int kMostRows = 16, kMostRowsScalar = 32;
+
+GnArgs make_args(const cf_gn_desc* d) {
     GnArgs A{};
-    A.n = d->n, A.d = d->d, A.h = d->h, A.w = d->w, A.s = d->d * d->h * d->w;
+    const int v = vec_of(d);
+    A.n = (int)d->n, A.d = (int)d->d, A.h = (int)d->h, A.w = (int)d->w, A.s = d->d * d->h * d->w;
     A.c = d->c, A.groups = d->groups, A.cg = d->c / d->groups;
     A.xp = d->x_pitch ? d->x_pitch : d->c, A.yp = d->y_pitch ? d->y_pitch : d->c;
     A.slope = d->slope, A.eps = d->eps;
-    A.total = pooled_rows && d->pool != CF_POOL_NONE ? A.s / 8 : A.s;
-    const int64_t want = std::max<int64_t>(1, 4 * num_sms / d->n);
-    A.rows = std::max<int64_t>(32, (A.total + want - 1) / want);
+    const int vc = d->c / v;
+    A.tiles = (vc + kThreads - 1) / kThreads;
+    A.tile = (vc + A.tiles - 1) / A.tiles;
+    const int win = d->pool != CF_POOL_NONE ? 8 : 1;
+    A.total = A.s / win;
+    if (win == 8) A.w2 = FastDiv::make((uint32_t)(d->w / 2)), A.h2 = FastDiv::make((uint32_t)(d->h / 2));
+    // voxels of a row lane in a chunk: fewer than the most where there are not enough blocks, but four (a window) at least
+    const int64_t lanes = kThreads / A.tile, most = v > 1 ? kMostRows : kMostRowsScalar;
+    const int64_t share = (A.s * A.n * A.tiles + kPlanBlocks * lanes - 1) / (kPlanBlocks * lanes);
+    const int64_t per = std::max<int64_t>(win == 8 ? 8 : 4, std::min(share, most)) / win * win;
+    A.rows = (int)std::min(A.total, lanes * per / win);
+    A.srows = win * A.rows;
     A.chunks = (int)((A.total + A.rows - 1) / A.rows);
+    A.tdiv = FastDiv::make((uint32_t)A.tile);
+    A.cdiv = FastDiv::make((uint32_t)A.chunks);
     return A;
 }
 
-size_t part_bytes(const GnArgs& A) { return (size_t)A.n * A.chunks * A.c * sizeof(float2); }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Values of a vector access: 16 bytes where channels, pitches and their alignment allow it, else one value.
-int vec_of(const cf_gn_desc* d, const GnArgs& A) {
-    const int v = d->dtype == CF_DT_F32 ? 4 : 8;
-    return A.c % v == 0 && A.xp % v == 0 && A.yp % v == 0 ? v : 1;
-}
-
-dim3 grid_of(const GnArgs& A, int v) { return dim3(A.chunks, (A.c / v + kThreads - 1) / kThreads, (unsigned)A.n); }
-
-template <typename T, int V>
-cf_status forward(const LaunchCtx& ctx, const cf_gn_desc* d, const void* x, const float* gamma, const float* beta, void* y,
-                  float* mean, float* rstd, float2* part) {
-    const GnArgs S = make_args(d, ctx.num_sms, false), P = make_args(d, ctx.num_sms, true);
-    const T* xt = static_cast<const T*>(x);
-    T* yt = static_cast<T*>(y);
-    gn_stats_kernel<T, V><<<grid_of(S, V), kThreads, 0, ctx.stream>>>(S, xt, part);
-    gn_stats_reduce_kernel<<<(unsigned)(S.n * S.groups), kThreads, 0, ctx.stream>>>(S, part, mean, rstd);
-#define CF_GN_APPLY(POOL, ACT) \
-    gn_apply_kernel<T, V, POOL, ACT><<<grid_of(P, V), kThreads, 0, ctx.stream>>>(P, xt, gamma, beta, mean, rstd, yt)
-    if (d->pool == CF_POOL_NONE) {
-        if (d->act == CF_ACT_SILU)
-            CF_GN_APPLY(CF_POOL_NONE, CF_ACT_SILU);
-        else
-            CF_GN_APPLY(CF_POOL_NONE, CF_ACT_LRELU);
-    } else if constexpr (sizeof(T) == 2) {
-        if (d->pool == CF_POOL_MAX)
-            CF_GN_APPLY(CF_POOL_MAX, CF_ACT_LRELU);
-        else if (d->act == CF_ACT_SILU)
-            CF_GN_APPLY(CF_POOL_AVG, CF_ACT_SILU);
-        else
-            CF_GN_APPLY(CF_POOL_AVG, CF_ACT_LRELU);
+// Places the workspace at `base` (NULL: to count) and returns its size.
+size_t place(GnArgs& A, bool backward, char* base) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base + at;
+        at += up256(bytes);
+        return p;
+    };
+    const size_t chunks = (size_t)A.n * A.chunks, nc = (size_t)A.n * A.c;
+    A.part = reinterpret_cast<float2*>(take(chunks * (backward ? (size_t)A.c : (size_t)A.tiles * A.groups) * sizeof(float2)));
+    A.coef = reinterpret_cast<float4*>(take(nc * sizeof(float4)));
+    if (backward) {
+        A.lin = reinterpret_cast<float2*>(take(nc * sizeof(float2)));
+        A.chan = reinterpret_cast<float2*>(take(nc * sizeof(float2)));
     }
-#undef CF_GN_APPLY
-    return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
+    return at;
 }
 
-template <typename T, int V>
-cf_status backward(const LaunchCtx& ctx, const cf_gn_desc* d, const void* x, const float* gamma, const float* beta,
-                   const float* mean, const float* rstd, const void* dy, void* dx, float* dgamma, float* dbeta, float2* part,
-                   float2* coef) {
-    const GnArgs P = make_args(d, ctx.num_sms, true);
+template <typename T, int V, int POOL, int ACT>
+void launch_fwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const float* gamma, const float* beta, void* y, float* mean,
+                float* rstd) {
+    const dim3 grid((unsigned)(A.n * A.chunks), A.tiles);
+    gn_stats_kernel<T, V><<<grid, kThreads, 0, ctx.stream>>>(A, static_cast<const T*>(x));
+    gn_finish_kernel<V><<<A.n * A.groups, kThreads, 0, ctx.stream>>>(A, gamma, beta, mean, rstd);
+    gn_apply_kernel<T, V, POOL, ACT><<<grid, kThreads, 0, ctx.stream>>>(A, static_cast<const T*>(x), static_cast<T*>(y));
+}
+
+template <typename T, int V, int POOL, int ACT>
+void launch_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const float* gamma, const float* beta, const float* mean,
+                const float* rstd, const void* dy, void* dx, float* dgamma, float* dbeta) {
     const T *xt = static_cast<const T*>(x), *dyt = static_cast<const T*>(dy);
-    T* dxt = static_cast<T*>(dx);
-#define CF_GN_BWD(POOL, ACT, PASS)                                                                                        \
-    gn_bwd_kernel<T, V, POOL, ACT, PASS>                                                                                  \
-        <<<grid_of(P, V), kThreads, 0, ctx.stream>>>(P, xt, gamma, beta, mean, rstd, dyt, coef, part, dxt)
-#define CF_GN_PASS(PASS)                                     \
-    if (d->pool == CF_POOL_NONE) {                           \
-        if (d->act == CF_ACT_SILU)                           \
-            CF_GN_BWD(CF_POOL_NONE, CF_ACT_SILU, PASS);      \
-        else                                                 \
-            CF_GN_BWD(CF_POOL_NONE, CF_ACT_LRELU, PASS);     \
-    } else if constexpr (sizeof(T) == 2) {                   \
-        if (d->pool == CF_POOL_MAX)                          \
-            CF_GN_BWD(CF_POOL_MAX, CF_ACT_LRELU, PASS);      \
-        else if (d->act == CF_ACT_SILU)                      \
-            CF_GN_BWD(CF_POOL_AVG, CF_ACT_SILU, PASS);       \
-        else                                                 \
-            CF_GN_BWD(CF_POOL_AVG, CF_ACT_LRELU, PASS);      \
-    }
-    CF_GN_PASS(0)
-    gn_bwd_reduce_kernel<<<(unsigned)(P.n * P.groups + (P.c + kThreads - 1) / kThreads), kThreads, 0, ctx.stream>>>(
-        P, part, gamma, coef, dgamma, dbeta);
-    if (dx != nullptr) {
-        CF_GN_PASS(1)
-    }
-#undef CF_GN_PASS
-#undef CF_GN_BWD
-    return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
+    const int work = A.n * A.chunks, blocks = dx ? work : 0, more = dgamma || dbeta ? (A.c + kThreads - 1) / kThreads : 0;
+    gn_coef_kernel<<<(unsigned)(((int64_t)A.n * A.c + kThreads - 1) / kThreads), kThreads, 0, ctx.stream>>>(A, gamma, beta, mean, rstd);
+    gn_bwd_sums_kernel<T, V, POOL, ACT><<<dim3(work, A.tiles), kThreads, 0, ctx.stream>>>(A, xt, dyt);
+    gn_bwd_finish_kernel<<<A.n * A.groups, kThreads, 0, ctx.stream>>>(A, gamma);
+    if (blocks + more > 0)
+        gn_bwd_apply_kernel<T, V, POOL, ACT>
+            <<<dim3(blocks + more, A.tiles), kThreads, 0, ctx.stream>>>(A, xt, dyt, static_cast<T*>(dx), blocks, dgamma, dbeta);
 }
+
+// Calls f<T, V, POOL, ACT>(...) for the descriptor.
+#define CF_GN_DISPATCH(d, f, ...)                                                     \
+    do {                                                                              \
+        const bool vec = vec_of(d) > 1, silu = (d)->act == CF_ACT_SILU;               \
+        if ((d)->dtype == CF_DT_F32) {                                                \
+            if (vec)                                                                  \
+                silu ? f<float, 4, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)            \
+                     : f<float, 4, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);          \
+            else                                                                      \
+                silu ? f<float, 1, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)            \
+                     : f<float, 1, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);          \
+        } else if ((d)->pool == CF_POOL_NONE) {                                       \
+            if (vec)                                                                  \
+                silu ? f<uint16_t, 8, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)         \
+                     : f<uint16_t, 8, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);       \
+            else                                                                      \
+                silu ? f<uint16_t, 1, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)         \
+                     : f<uint16_t, 1, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);       \
+        } else if ((d)->pool == CF_POOL_MAX) {                                        \
+            vec ? f<uint16_t, 8, CF_POOL_MAX, CF_ACT_LRELU>(__VA_ARGS__)              \
+                : f<uint16_t, 1, CF_POOL_MAX, CF_ACT_LRELU>(__VA_ARGS__);             \
+        } else {                                                                      \
+            if (vec)                                                                  \
+                silu ? f<uint16_t, 8, CF_POOL_AVG, CF_ACT_SILU>(__VA_ARGS__)          \
+                     : f<uint16_t, 8, CF_POOL_AVG, CF_ACT_LRELU>(__VA_ARGS__);        \
+            else                                                                      \
+                silu ? f<uint16_t, 1, CF_POOL_AVG, CF_ACT_SILU>(__VA_ARGS__)          \
+                     : f<uint16_t, 1, CF_POOL_AVG, CF_ACT_LRELU>(__VA_ARGS__);        \
+        }                                                                             \
+    } while (0)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t workspace_bytes(const cf_gn_desc* d, int num_sms, bool backward) {
-    const GnArgs A = make_args(d, num_sms, backward);
-    return (size_t)A.n * A.groups * sizeof(float2) + 256 + part_bytes(A);
-}
 
 }  // namespace
 }  // namespace cf
@@ -461,9 +885,8 @@ extern "C" {
 
 size_t cf_group_norm_workspace_size(const cf_gn_desc* desc, int32_t backward) {
     if (!desc_ok(desc) || supported(desc) != CF_OK) return 0;
-    LaunchCtx ctx;
-    if (!cf_device_ctx(&ctx, nullptr)) return 0;
-    return workspace_bytes(desc, ctx.num_sms, backward != 0);
+    GnArgs A = make_args(desc);
+    return place(A, backward != 0, nullptr);
 }
 
 cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* gamma, const float* beta, void* y,
@@ -473,19 +896,13 @@ cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* 
         !aligned16(ws))
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
+    GnArgs A = make_args(desc);
+    if (ws == nullptr || ws_bytes < place(A, false, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    if (ws == nullptr || ws_bytes < workspace_bytes(desc, ctx.num_sms, false)) return CF_ERR_WORKSPACE;
-    const GnArgs S = make_args(desc, ctx.num_sms, false);
-    const size_t ng = (size_t)S.n * S.groups;
-    if (mean == nullptr) mean = static_cast<float*>(ws);
-    if (rstd == nullptr) rstd = static_cast<float*>(ws) + ng;
-    float2* part = reinterpret_cast<float2*>(static_cast<char*>(ws) + (ng * sizeof(float2) + 255) / 256 * 256);
-    if (desc->dtype == CF_DT_F32)
-        return vec_of(desc, S) > 1 ? forward<float, 4>(ctx, desc, x, gamma, beta, y, mean, rstd, part)
-                                   : forward<float, 1>(ctx, desc, x, gamma, beta, y, mean, rstd, part);
-    return vec_of(desc, S) > 1 ? forward<uint16_t, 8>(ctx, desc, x, gamma, beta, y, mean, rstd, part)
-                               : forward<uint16_t, 1>(ctx, desc, x, gamma, beta, y, mean, rstd, part);
+    place(A, false, static_cast<char*>(ws));
+    CF_GN_DISPATCH(desc, launch_fwd, ctx, A, x, gamma, beta, y, mean, rstd);
+    return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
 }
 
 cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* gamma, const float* beta,
@@ -496,20 +913,13 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
         !aligned16(rstd) || !aligned16(dgamma) || !aligned16(dbeta) || !aligned16(ws))
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
+    GnArgs A = make_args(desc);
+    if (ws == nullptr || ws_bytes < place(A, true, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    if (ws == nullptr || ws_bytes < workspace_bytes(desc, ctx.num_sms, true)) return CF_ERR_WORKSPACE;
-    const GnArgs P = make_args(desc, ctx.num_sms, true);
-    float2* coef = static_cast<float2*>(ws);
-    float2* part =
-        reinterpret_cast<float2*>(static_cast<char*>(ws) + ((size_t)P.n * P.groups * sizeof(float2) + 255) / 256 * 256);
-    if (desc->dtype == CF_DT_F32)
-        return vec_of(desc, P) > 1
-                   ? backward<float, 4>(ctx, desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, part, coef)
-                   : backward<float, 1>(ctx, desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, part, coef);
-    return vec_of(desc, P) > 1
-               ? backward<uint16_t, 8>(ctx, desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, part, coef)
-               : backward<uint16_t, 1>(ctx, desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, part, coef);
+    place(A, true, static_cast<char*>(ws));
+    CF_GN_DISPATCH(desc, launch_bwd, ctx, A, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta);
+    return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
 }
 
 }  // extern "C"
