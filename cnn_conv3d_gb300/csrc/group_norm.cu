@@ -186,6 +186,9 @@ struct Window {
     __device__ __forceinline__ int64_t at(int k) const { return (k & 4 ? d : 0) + (k & 2 ? h : 0) + (k & 1 ? w : 0); }
 };
 
+// A sum of squares less what rounding took below 0; NaN stays NaN.
+__device__ __forceinline__ float nonneg(float v) { return v < 0.f ? 0.f : v; }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
         for (int e = 0; e < V; ++e) {
             const float d = s[e] * inv;
             k[e] += d;
-            q[e] = fmaxf(fmaf(-s[e], d, q[e]), 0.f);
+            q[e] = nonneg(fmaf(-s[e], d, q[e]));
         }
     }
     const Span<V> sp(A);
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
         b = warp_sum(b);
         const float d = a / ((float)P.rows * (float)(units * sp.span));
         if ((threadIdx.x & 31) == 0)
-            A.part[((int64_t)blockIdx.x * A.tiles + P.tile) * A.groups + g] = make_float2(about + d, fmaxf(fmaf(-a, d, b), 0.f));
+            A.part[((int64_t)blockIdx.x * A.tiles + P.tile) * A.groups + g] = make_float2(about + d, nonneg(fmaf(-a, d, b)));
     }
 }
 
@@ -744,6 +747,420 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Small samples: a cluster of blocks holds a sample's channels (or a part of them that is whole groups) in registers, so that
+// one launch reads x (and dy) once; the blocks exchange their group sums through each other's shared memory.
+
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores v at `at` (an address of this block's shared memory) in the block `rank` of the cluster.
+__device__ __forceinline__ void store_remote(const float2* at, uint32_t rank, float2 v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// Where a block of a cluster works: rows r0 .. r0+rows-1 of a sample, columns of tile blockIdx.y.
+template <int V>
+struct SmallPlace {
+    int sample, rank, r0, rows, lanes, col, lane, c0, left;
+    __device__ __forceinline__ SmallPlace(const GnArgs& A) {
+        rank = (int)cluster_rank();
+        sample = blockIdx.x / A.chunks;
+        r0 = rank * A.rows;
+        rows = max(0, min(A.rows, (int)A.total - r0));
+        lane = (int)A.tdiv.div(threadIdx.x);
+        lanes = kSmallThreads / A.tile;
+        col = threadIdx.x - lane * A.tile;
+        c0 = (blockIdx.y * A.tile + col) * V;
+        left = lane < lanes && rows > lane ? (int)((uint32_t)(rows - lane + lanes - 1) / (uint32_t)lanes) : 0;
+    }
+};
+
+// The thread's R items (a voxel's vector, or a window's eight) in registers.
+template <typename T, int V, int POOL, int R>
+struct Held {
+    static constexpr int K = POOL == CF_POOL_NONE ? 1 : 8;
+    Pack<T, V> t[R][K];
+    __device__ __forceinline__ void load_all(const GnArgs& A, const SmallPlace<V>& P, const T* x) {
+        const Window W(A);
+        const T* xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i < P.left) {
+                const int64_t row = P.r0 + P.lane + i * P.lanes;
+                const T* p = xs + (K == 1 ? row * A.xp : window_at(A, row));
+#pragma unroll
+                for (int k = 0; k < K; ++k) t[i][k] = load<T, V>(p + (K == 1 ? 0 : W.at(k)));
+            }
+    }
+};
+
+// Sums of the entries of the tile's group g (numbered from 0), over a warp: f(entry, row lane), an entry at
+// [unit of the vector][thread].
+template <int V, typename F>
+__device__ __forceinline__ void small_entries(const GnArgs& A, int lanes, const Span<V>& sp, int g, F f) {
+    const int lane = threadIdx.x & 31, qb = (g + 1) * sp.units;
+    int lp = 32, sh = 5;
+    while (lp > lanes) lp >>= 1, --sh;
+    for (int q = g * sp.units + (lane >> sh); q < qb; q += 32 >> sh) {
+        const int col = sp.per == 1 ? q : q / sp.per, slot = q - col * sp.per;
+        for (int l = lane & (lp - 1); l < lanes; l += lp) f(slot * kSmallThreads + l * A.tile + col, l);
+    }
+}
+
+template <typename T, int V, int POOL, int ACT, int R>
+__global__ void __launch_bounds__(kSmallThreads, 1) gn_small_fwd_kernel(const GnArgs A, const T* __restrict__ x,
+                                                                       const float* __restrict__ gamma, const float* __restrict__ beta,
+                                                                       T* __restrict__ y, float* __restrict__ mean,
+                                                                       float* __restrict__ rstd) {
+    extern __shared__ float2 ex[];  // [rank][group of the tile], then the tile's (mean, rstd)
+    __shared__ float sm[kSmallThreads * V], sq[kSmallThreads * V];
+    const SmallPlace<V> P(A);
+    const int groups = A.tile * V / A.cg, g0 = blockIdx.y * groups;
+    Held<T, V, POOL, R> H;
+    H.load_all(A, P, x);
+    float k[V], s[V], q[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) k[e] = s[e] = q[e] = 0.f;
+    if (P.left) unpack<T, V>(H.t[0][0], k);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < P.left) {
+#pragma unroll
+            for (int j = 0; j < H.K; ++j) {
+                float f[V];
+                unpack<T, V>(H.t[i][j], f);
+                vsub<V>(f, f, k);
+                vadd<V>(s, s, f);
+                vfma<V>(q, f, f, q);
+            }
+        }
+    const float n = (float)(P.left * H.K), inv = P.left ? 1.f / n : 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float d = s[e] * inv;
+        k[e] += d;
+        q[e] = nonneg(fmaf(-s[e], d, q[e]));
+    }
+    const Span<V> sp(A);
+#pragma unroll
+    for (int w = 1; w < V; w *= 2)
+        if (w < sp.span) {
+#pragma unroll
+            for (int e = 0; e + w < V; e += 2 * w) {
+                const float d = k[e + w] - k[e];
+                k[e] = fmaf(0.5f, d, k[e]);
+                q[e] += fmaf(0.5f * (float)w * n * d, d, q[e + w]);
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (e % sp.span == 0) {
+            sm[e / sp.span * kSmallThreads + threadIdx.x] = k[e];
+            sq[e / sp.span * kSmallThreads + threadIdx.x] = q[e];
+        }
+    __syncthreads();
+    const int least = P.rows / P.lanes, more = P.rows - least * P.lanes;
+    for (int g = threadIdx.x >> 5; g < groups; g += kSmallWarps) {
+        const int q0 = g * sp.units;
+        const float about = sm[q0 % sp.per * kSmallThreads + q0 / sp.per];
+        float a = 0.f, b = 0.f;
+        small_entries<V>(A, P.lanes, sp, g, [&](int at, int l) {
+            const float nl = (float)((least + (l < more)) * H.K * sp.span), d = sm[at] - about;
+            a = fmaf(nl, d, a);
+            b += nl > 0.f ? fmaf(nl * d, d, sq[at]) : 0.f;
+        });
+        a = warp_sum(a);
+        b = warp_sum(b);
+        const float d = P.rows ? a / ((float)(P.rows * H.K) * (float)A.cg) : 0.f;
+        if ((threadIdx.x & 31) < A.chunks)
+            store_remote(&ex[P.rank * groups + g], threadIdx.x & 31, make_float2(about + d, nonneg(fmaf(-a, d, b))));
+    }
+    cluster_sync();
+    float2* stat = ex + A.chunks * groups;
+    for (int g = threadIdx.x; g < groups; g += kSmallThreads) {
+        // the blocks' means and deviations joined about the first's
+        const float about = ex[g].x, per = (float)(H.K * A.cg);
+        float a = 0.f, b = 0.f;
+        for (int r = 0; r < A.chunks; ++r) {
+            const float nr = (float)max(0, min(A.rows, (int)A.total - r * A.rows)) * per;
+            const float2 t = ex[r * groups + g];
+            const float d = t.x - about;
+            if (nr > 0.f) {
+                a = fmaf(nr, d, a);
+                b += fmaf(nr * d, d, t.y);
+            }
+        }
+        const float count = (float)A.s * (float)A.cg, d = a / count;
+        const float mu = about + d, rs = 1.f / sqrtf(nonneg(fmaf(-a, d, b)) / count + A.eps);
+        stat[g] = make_float2(mu, rs);
+        if (P.rank == 0) {
+            if (mean) mean[(int64_t)P.sample * A.groups + g0 + g] = mu;
+            if (rstd) rstd[(int64_t)P.sample * A.groups + g0 + g] = rs;
+        }
+    }
+    __syncthreads();
+    if (!P.left) return;
+    float a[V], m[V], be[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float2 t = stat[(P.col * V + e) / A.cg];
+        m[e] = t.x;
+        a[e] = (gamma ? gamma[P.c0 + e] : 1.f) * t.y;
+        be[e] = beta ? beta[P.c0 + e] : 0.f;
+    }
+    auto norm = [&](float (&f)[V]) {
+        vsub<V>(f, f, m);
+        vfma<V>(f, a, f, be);
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < P.left) {
+            float f[V], o[V];
+            if (POOL == CF_POOL_AVG) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < H.K; ++j) {
+                    unpack<T, V>(H.t[i][j], f);
+                    norm(f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[e] += 0.125f * act_of<T, ACT>(f[e], A.slope);
+                }
+            } else {
+                if constexpr (POOL == CF_POOL_MAX)
+                    window_max<T, V>(H.t[i], a, o);
+                else
+                    unpack<T, V>(H.t[i][0], o);
+                norm(o);
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = act_of<T, ACT>(o[e], A.slope);
+            }
+            store<T, V>(y + ((int64_t)P.sample * A.total + P.r0 + P.lane + i * P.lanes) * A.yp + P.c0, o);
+        }
+}
+
+// dx, and the block's channel sums: part[sample][rank][c].
+template <typename T, int V, int POOL, int ACT, int R>
+__global__ void __launch_bounds__(kSmallThreads, 1) gn_small_bwd_kernel(const GnArgs A, const T* __restrict__ x,
+                                                                       const float* __restrict__ gamma, const float* __restrict__ beta,
+                                                                       const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                                       const T* __restrict__ dy, T* __restrict__ dx) {
+    extern __shared__ float2 ex[];  // [rank][group of the tile], then the tile's (s1, s2)
+    __shared__ float sb[kSmallThreads * V], sg[kSmallThreads * V];
+    const SmallPlace<V> P(A);
+    const int groups = A.tile * V / A.cg;
+    Held<T, V, POOL, R> H;
+    Pack<T, V> D[R];
+    H.load_all(A, P, x);
+    const int64_t yrow = (int64_t)P.sample * A.total + P.r0 + P.lane;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < P.left) D[i] = load<T, V>(dy + (yrow + (int64_t)i * P.lanes) * A.yp + P.c0);
+    float a[V], m[V], be[V], rs[V], db[V], dg[V];
+    if (P.left) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int64_t g = (int64_t)P.sample * A.groups + (P.c0 + e) / A.cg;
+            m[e] = mean[g];
+            rs[e] = rstd[g];
+            a[e] = (gamma ? gamma[P.c0 + e] : 1.f) * rs[e];
+            be[e] = beta ? beta[P.c0 + e] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) db[e] = dg[e] = 0.f;
+    auto grad = [&](float (&f)[V], float (&g)[V]) {  // f: x - mean, g: du
+        float u[V];
+        vsub<V>(f, f, m);
+        vfma<V>(u, a, f, be);
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] *= act_grad<T, ACT>(u[e], A.slope);
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < P.left) {
+            float f[V], g[V], d[V];
+            unpack<T, V>(D[i], d);
+            if (POOL == CF_POOL_AVG) {
+#pragma unroll
+                for (int j = 0; j < H.K; ++j) {
+                    unpack<T, V>(H.t[i][j], f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) g[e] = 0.125f * d[e];
+                    grad(f, g);
+                    vadd<V>(db, db, g);
+                    vfma<V>(dg, g, f, dg);
+                }
+            } else {
+                if constexpr (POOL == CF_POOL_MAX)
+                    window_max<T, V>(H.t[i], a, f);
+                else
+                    unpack<T, V>(H.t[i][0], f);
+                grad(f, d);
+                vadd<V>(db, db, d);
+                vfma<V>(dg, d, f, dg);
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        sb[e * kSmallThreads + threadIdx.x] = db[e];
+        sg[e * kSmallThreads + threadIdx.x] = P.left ? dg[e] * rs[e] : 0.f;
+    }
+    __syncthreads();
+    // a channel's row lanes are added up by as many neighbouring threads as the block has for it; its sums go to slot 0
+    const int wide = A.tile * V, cb = blockIdx.y * wide;
+    int lp = 1;
+    while (2 * lp <= 32 && 2 * lp <= P.lanes && 2 * lp * wide <= kSmallThreads) lp *= 2;
+    float2 sums[V > 1 ? V : 1];  // of the channels this thread takes, in turn: wide <= kSmallThreads V
+    int mine = 0;
+    for (int i = threadIdx.x / lp; i < (wide + 31) / 32 * 32; i += kSmallThreads / lp, ++mine) {
+        float tb = 0.f, tg = 0.f;
+        if (i < wide)
+            for (int l = threadIdx.x & (lp - 1); l < P.lanes; l += lp) {
+                tb += sb[i % V * kSmallThreads + l * A.tile + i / V];
+                tg += sg[i % V * kSmallThreads + l * A.tile + i / V];
+            }
+        for (int o = lp / 2; o; o >>= 1) {
+            tb += __shfl_xor_sync(~0u, tb, o);
+            tg += __shfl_xor_sync(~0u, tg, o);
+        }
+#pragma unroll
+        for (int w = 0; w < V; ++w)
+            if (w == mine) sums[w] = make_float2(tb, tg);
+    }
+    __syncthreads();
+    mine = 0;
+    for (int i = threadIdx.x / lp; i < (wide + 31) / 32 * 32; i += kSmallThreads / lp, ++mine)
+        if (i < wide && (threadIdx.x & (lp - 1)) == 0) {
+            float2 t = sums[0];
+#pragma unroll
+            for (int w = 1; w < V; ++w)
+                if (w == mine) t = sums[w];
+            A.part[((int64_t)P.sample * A.chunks + P.rank) * A.c + cb + i] = t;
+            const float ga = gamma ? gamma[cb + i] : 1.f;
+            sb[i] = t.x * ga;
+            sg[i] = t.y * ga;
+        }
+    if (dx == nullptr) return;  // the same for the whole grid
+    __syncthreads();
+    for (int g = threadIdx.x >> 5; g < groups; g += kSmallWarps) {
+        float s1 = 0.f, s2 = 0.f;
+        for (int i = threadIdx.x & 31; i < A.cg; i += 32) {
+            s1 += sb[g * A.cg + i];
+            s2 += sg[g * A.cg + i];
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if ((threadIdx.x & 31) < A.chunks) store_remote(&ex[P.rank * groups + g], threadIdx.x & 31, make_float2(s1, s2));
+    }
+    cluster_sync();
+    float2* stat = ex + A.chunks * groups;
+    for (int g = threadIdx.x; g < groups; g += kSmallThreads) {
+        float s1 = 0.f, s2 = 0.f;
+        for (int r = 0; r < A.chunks; ++r) {
+            s1 += ex[r * groups + g].x;
+            s2 += ex[r * groups + g].y;
+        }
+        const float inv = 1.f / ((float)A.s * (float)A.cg);
+        stat[g] = make_float2(s1 * inv, s2 * inv);
+    }
+    __syncthreads();
+    if (!P.left) return;
+    float k0[V], k1[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float2 t = stat[(P.col * V + e) / A.cg];
+        k0[e] = -rs[e] * t.x;
+        k1[e] = -rs[e] * rs[e] * t.y;
+    }
+    const Window W(A);
+    T* os = dx + (int64_t)P.sample * A.s * A.xp + P.c0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < P.left) {
+            const int64_t row = P.r0 + P.lane + i * P.lanes;
+            T* o = os + (H.K == 1 ? row * A.xp : window_at(A, row));
+            float f[V], g[V], d[V], lin[V];
+            unpack<T, V>(D[i], d);
+            if constexpr (POOL == CF_POOL_NONE) {
+                unpack<T, V>(H.t[i][0], f);
+                grad(f, d);
+                vfma<V>(lin, k1, f, k0);
+                vfma<V>(lin, a, d, lin);
+                store<T, V>(o, lin);
+            } else {
+                float best[V];
+                if (POOL == CF_POOL_MAX) {
+                    window_max<T, V>(H.t[i], a, best);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) f[e] = best[e];
+                    grad(f, d);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) d[e] *= a[e];
+                }
+#pragma unroll
+                for (int j = 0; j < H.K; ++j) {
+                    unpack<T, V>(H.t[i][j], f);
+                    if (POOL == CF_POOL_MAX) {
+                        float c[V];
+                        vsub<V>(c, f, m);
+                        vfma<V>(lin, k1, c, k0);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const bool hit = f[e] == best[e];
+                            lin[e] += hit ? d[e] : 0.f;
+                            d[e] = hit ? 0.f : d[e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] = 0.125f * d[e];
+                        grad(f, g);
+                        vfma<V>(lin, k1, f, k0);
+                        vfma<V>(lin, a, g, lin);
+                    }
+                    store<T, V>(o + W.at(j), lin);
+                }
+            }
+        }
+}
+
+// dbeta and dgamma from `rows` rows of channel sums: 32 channels a block, a row lane to each warp.
+__global__ void __launch_bounds__(kThreads) gn_channels_kernel(const float2* __restrict__ part, int64_t rows, int c,
+                                                              float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    __shared__ float2 red[kWarps][33];
+    const int ch = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
+    float tb = 0.f, tg = 0.f;
+    if (ch < c) {
+#pragma unroll 4
+        for (int64_t i = l; i < rows; i += kWarps) {
+            const float2 v = part[i * c + ch];
+            tb += v.x;
+            tg += v.y;
+        }
+    }
+    red[l][threadIdx.x & 31] = make_float2(tb, tg);
+    __syncthreads();
+    if (l == 0 && ch < c) {
+        for (int i = 1; i < kWarps; ++i) {
+            tb += red[i][threadIdx.x].x;
+            tg += red[i][threadIdx.x].y;
+        }
+        if (dbeta) dbeta[ch] = tb;
+        if (dgamma) dgamma[ch] = tg;
+    }
+}
+
 bool desc_ok(const cf_gn_desc* d) {
     if (d == nullptr) return false;
     if (d->n <= 0 || d->d <= 0 || d->h <= 0 || d->w <= 0 || d->c <= 0 || d->groups <= 0) return false;
@@ -801,10 +1218,48 @@ GnArgs make_args(const cf_gn_desc* d) {
     return A;
 }
 
+// Items (vectors, or windows of eight) that a thread of the small kernels holds.
+constexpr int kSmallItems = 16, kSmallWindows = 2;
+constexpr int kMaxCluster = 16;
+// Bytes of x up to which a call goes to the small kernels where they take its shape.
+constexpr int64_t kSmallBytes = 16 << 20;
+
+// The small kernels' way to take a call: columns of whole groups, and the blocks of a cluster; false where the sample does not
+// fit.  Sets tile, tiles, chunks (the cluster's blocks) and rows (of a block).
+bool small_args(const cf_gn_desc* d, bool backward, GnArgs& A) {
+    const int v = vec_of(d), win = d->pool != CF_POOL_NONE ? 8 : 1, vc = d->c / v;
+    const int64_t size = d->dtype == CF_DT_F32 ? 4 : 2;
+    if (A.s * A.n * A.c * size > kSmallBytes) return false;
+    int a = A.cg, b = v;
+    while (b) {
+        const int t = a % b;
+        a = b, b = t;
+    }
+    const int least = A.cg / a;  // vectors that are whole groups: lcm(cg, v) / v
+    const int most = win == 8 ? kSmallWindows : backward ? kSmallItems / 2 : kSmallItems;
+    for (int split = 1; split <= vc / least; ++split) {  // the widest columns that fit
+        if ((vc / least) % split) continue;
+        const int tile = vc / split;
+        if (tile > kSmallThreads || tile * v / A.cg > 64) continue;
+        if (split > 1 && (int64_t)tile * v * size < 64) break;
+        const int64_t lanes = kSmallThreads / tile, need = (A.total + lanes * most - 1) / (lanes * most);
+        if (need > kMaxCluster) continue;
+        // more blocks than needed where there are SMs for them, down to a quarter of the items
+        const int64_t want = std::min<int64_t>((A.total + lanes * most / 4 - 1) / (lanes * std::max(1, most / 4)), 152 / (A.n * (int64_t)split));
+        int q = 1;
+        while (q < need || (2 * q <= want && 2 * q <= 8)) q *= 2;
+        A.tile = tile, A.tiles = split, A.chunks = q;
+        A.rows = (int)((A.total + q - 1) / q);
+        A.tdiv = FastDiv::make((uint32_t)tile);
+        return true;
+    }
+    return false;
+}
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Places the workspace at `base` (NULL: to count) and returns its size.
-size_t place(GnArgs& A, bool backward, char* base) {
+size_t place(GnArgs& A, bool backward, bool small, char* base) {
     size_t at = 0;
     auto take = [&](size_t bytes) {
         char* p = base + at;
@@ -812,6 +1267,10 @@ size_t place(GnArgs& A, bool backward, char* base) {
         return p;
     };
     const size_t chunks = (size_t)A.n * A.chunks, nc = (size_t)A.n * A.c;
+    if (small) {
+        if (backward) A.part = reinterpret_cast<float2*>(take(chunks * A.c * sizeof(float2)));
+        return std::max<size_t>(at, 256);
+    }
     A.part = reinterpret_cast<float2*>(take(chunks * (backward ? (size_t)A.c : (size_t)A.tiles * A.groups) * sizeof(float2)));
     A.coef = reinterpret_cast<float4*>(take(nc * sizeof(float4)));
     if (backward) {
@@ -841,6 +1300,56 @@ void launch_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const floa
     if (blocks + more > 0)
         gn_bwd_apply_kernel<T, V, POOL, ACT>
             <<<dim3(blocks + more, A.tiles), kThreads, 0, ctx.stream>>>(A, xt, dyt, static_cast<T*>(dx), blocks, dgamma, dbeta);
+}
+
+// A launch in clusters of A.chunks blocks.
+template <typename K, typename... P>
+cudaError_t launch_small(const LaunchCtx& ctx, const GnArgs& A, int groups, K kern, P... args) {
+    const size_t sm = (size_t)(A.chunks + 1) * groups * sizeof(float2);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(A.n * A.chunks), (unsigned)A.tiles);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = sm;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)A.chunks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (A.chunks > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename T, int V, int POOL, int ACT>
+void launch_small_fwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const float* gamma, const float* beta, void* y, float* mean,
+                      float* rstd) {
+    const int lanes = kSmallThreads / A.tile, items = (A.rows + lanes - 1) / lanes, groups = A.tile * V / A.cg;
+    const T* xt = static_cast<const T*>(x);
+    T* yt = static_cast<T*>(y);
+    constexpr int kMost = POOL == CF_POOL_NONE ? kSmallItems : kSmallWindows, kFew = POOL == CF_POOL_NONE ? kSmallItems / 4 : 1;
+    if (items <= kFew)
+        launch_small(ctx, A, groups, gn_small_fwd_kernel<T, V, POOL, ACT, kFew>, A, xt, gamma, beta, yt, mean, rstd);
+    else
+        launch_small(ctx, A, groups, gn_small_fwd_kernel<T, V, POOL, ACT, kMost>, A, xt, gamma, beta, yt, mean, rstd);
+}
+
+template <typename T, int V, int POOL, int ACT>
+void launch_small_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const float* gamma, const float* beta, const float* mean,
+                      const float* rstd, const void* dy, void* dx, float* dgamma, float* dbeta) {
+    const int lanes = kSmallThreads / A.tile, items = (A.rows + lanes - 1) / lanes, groups = A.tile * V / A.cg;
+    const T *xt = static_cast<const T*>(x), *dyt = static_cast<const T*>(dy);
+    T* dxt = static_cast<T*>(dx);
+    constexpr int kMost = POOL == CF_POOL_NONE ? kSmallItems / 2 : kSmallWindows, kFew = POOL == CF_POOL_NONE ? kSmallItems / 8 : 1;
+    if (items <= kFew)
+        launch_small(ctx, A, groups, gn_small_bwd_kernel<T, V, POOL, ACT, kFew>, A, xt, gamma, beta, mean, rstd, dyt, dxt);
+    else
+        launch_small(ctx, A, groups, gn_small_bwd_kernel<T, V, POOL, ACT, kMost>, A, xt, gamma, beta, mean, rstd, dyt, dxt);
+    if (dgamma || dbeta)
+        gn_channels_kernel<<<(A.c + 31) / 32, kThreads, 0, ctx.stream>>>(A.part, (int64_t)A.n * A.chunks, A.c, dgamma, dbeta);
 }
 
 // Calls f<T, V, POOL, ACT>(...) for the descriptor.
@@ -886,7 +1395,8 @@ extern "C" {
 size_t cf_group_norm_workspace_size(const cf_gn_desc* desc, int32_t backward) {
     if (!desc_ok(desc) || supported(desc) != CF_OK) return 0;
     GnArgs A = make_args(desc);
-    return place(A, backward != 0, nullptr);
+    const bool small = small_args(desc, backward != 0, A);
+    return place(A, backward != 0, small, nullptr);
 }
 
 cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* gamma, const float* beta, void* y,
@@ -897,11 +1407,15 @@ cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* 
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
     GnArgs A = make_args(desc);
-    if (ws == nullptr || ws_bytes < place(A, false, nullptr)) return CF_ERR_WORKSPACE;
+    const bool small = small_args(desc, false, A);
+    if (ws == nullptr || ws_bytes < place(A, false, small, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    place(A, false, static_cast<char*>(ws));
-    CF_GN_DISPATCH(desc, launch_fwd, ctx, A, x, gamma, beta, y, mean, rstd);
+    place(A, false, small, static_cast<char*>(ws));
+    if (small)
+        CF_GN_DISPATCH(desc, launch_small_fwd, ctx, A, x, gamma, beta, y, mean, rstd);
+    else
+        CF_GN_DISPATCH(desc, launch_fwd, ctx, A, x, gamma, beta, y, mean, rstd);
     return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
 }
 
@@ -914,11 +1428,15 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
     GnArgs A = make_args(desc);
-    if (ws == nullptr || ws_bytes < place(A, true, nullptr)) return CF_ERR_WORKSPACE;
+    const bool small = small_args(desc, true, A);
+    if (ws == nullptr || ws_bytes < place(A, true, small, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    place(A, true, static_cast<char*>(ws));
-    CF_GN_DISPATCH(desc, launch_bwd, ctx, A, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta);
+    place(A, true, small, static_cast<char*>(ws));
+    if (small)
+        CF_GN_DISPATCH(desc, launch_small_bwd, ctx, A, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta);
+    else
+        CF_GN_DISPATCH(desc, launch_bwd, ctx, A, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta);
     return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
 }
 
