@@ -30,7 +30,7 @@ struct GnArgs {
     int chunks;              // row chunks of a sample, in both passes
     int srows, rows;         // voxels of a chunk in the statistics pass; voxels or windows of a chunk elsewhere
     int64_t total;           // voxels or windows of a sample
-    FastDiv w2, h2, tdiv, cdiv;  // pooled extents, tile, chunks
+    FastDiv w2, h2, tdiv, cdiv, gdiv;  // pooled extents, tile, chunks, channels of a group
     float2* part;            // sums of a chunk
     float4* coef;            // [n][c]: (a, mean, beta, rstd)
     float2* lin;             // [n][c]: the backward's (k0, k1)
@@ -186,6 +186,10 @@ struct Window {
     __device__ __forceinline__ int64_t at(int k) const { return (k & 4 ? d : 0) + (k & 2 ? h : 0) + (k & 1 ? w : 0); }
 };
 
+// A launch may begin while the one before it ends: it waits for that one's results here, and lets its own successor begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A sum of squares less what rounding took below 0; NaN stays NaN.
 __device__ __forceinline__ float nonneg(float v) { return v < 0.f ? 0.f : v; }
 
@@ -199,10 +203,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // a group is `units` units, a warp takes its units times the row lanes.
 template <int V>
 struct Span {
-    int span, per, units;  // per: units of a vector
+    int span, per, sh, units;  // per = 1 << sh: units of a vector
     __device__ __forceinline__ Span(const GnArgs& A) {
         span = A.cg % V == 0 ? V : V % A.cg == 0 ? A.cg : 1;
         per = V / span;
+        sh = 31 - __clz(per);
         units = A.cg / span;
     }
 };
@@ -216,7 +221,7 @@ __device__ __forceinline__ int group_entries(const GnArgs& A, const Place<V>& P,
     int lp = 32, sh = 5;  // lanes of the warp that take row lanes; the others take further units
     while (lp > P.lanes) lp >>= 1, --sh;
     for (int q = qa + (lane >> sh); q < qb; q += 32 >> sh) {
-        const int col = sp.per == 1 ? q : q / sp.per, slot = q - col * sp.per;
+        const int col = q >> sp.sh, slot = q & (sp.per - 1);
         for (int l = lane & (lp - 1); l < P.lanes; l += lp) f(slot * kThreads + l * P.cols + col, l);
     }
     return qb - qa;
@@ -228,6 +233,7 @@ __device__ __forceinline__ int group_entries(const GnArgs& A, const Place<V>& P,
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, const T* __restrict__ x) {
     __shared__ float sm[kThreads * V], sq[kThreads * V];
+    grid_go();
     const Place<V> P(A, blockIdx.x, A.srows, A.s);
     float k[V], s[V], q[V];
 #pragma unroll
@@ -275,9 +281,10 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
         }
 #pragma unroll
     for (int e = 0; e < V; ++e)
-        if (e % sp.span == 0) {
-            sm[e / sp.span * kThreads + threadIdx.x] = k[e];
-            sq[e / sp.span * kThreads + threadIdx.x] = q[e];
+        if ((e & (sp.span - 1)) == 0) {
+            const int at = (e * sp.per / V) * kThreads + threadIdx.x;
+            sm[at] = k[e];
+            sq[at] = q[e];
         }
     __syncthreads();
     // a warp to a group: sums about the mean of its first entry
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
     const int least = P.rows / P.lanes, more = P.rows - least * P.lanes;  // rows of a lane: least, or one more
     for (int g = g0 + (threadIdx.x >> 5); g <= g1; g += kWarps) {
         const int q0 = max(g * sp.units - P.tile * A.tile * sp.per, 0);
-        const float about = sm[q0 % sp.per * kThreads + q0 / sp.per];
+        const float about = sm[(q0 & (sp.per - 1)) * kThreads + (q0 >> sp.sh)];
         float a = 0.f, b = 0.f;
         const int units = group_entries<V>(A, P, sp, g, [&](int at, int l) {
             const float nl = (float)((least + (l < more)) * sp.span), d = sm[at] - about;
@@ -324,6 +331,8 @@ __global__ void __launch_bounds__(kThreads) gn_finish_kernel(const GnArgs A, con
                                                             const float* __restrict__ beta, float* __restrict__ mean,
                                                             float* __restrict__ rstd) {
     __shared__ float red[kWarps];
+    grid_go();
+    grid_wait();
     const int sample = blockIdx.x / A.groups, g = blockIdx.x - sample * A.groups, items = A.chunks * A.tiles;
     const float2* p = A.part + (int64_t)sample * items * A.groups + g;
     const float count = (float)A.s * (float)A.cg;
@@ -421,6 +430,7 @@ template <typename T, int V, int POOL, int ACT>
 __global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 4 : 3) gn_apply_kernel(const GnArgs A, const T* __restrict__ x,
                                                                                        T* __restrict__ y) {
     const Place<V> P(A, gridDim.x - 1 - blockIdx.x, A.rows, A.total);
+    grid_wait();
     if (!P.left) return;
     float a[V], m[V], be[V];
     load_coef<V>(A, P, a, m, be);
@@ -490,6 +500,7 @@ __global__ void __launch_bounds__(kThreads) gn_coef_kernel(const GnArgs A, const
                                                           const float* __restrict__ beta, const float* __restrict__ mean,
                                                           const float* __restrict__ rstd) {
     const int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    grid_go();
     if (i >= (int64_t)A.n * A.c) return;
     const int64_t n = i / A.c;
     const int c = (int)(i - n * A.c);
@@ -504,6 +515,8 @@ __global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 3 : 2) gn_bwd
                                                                                           const T* __restrict__ dy) {
     __shared__ float sb[kThreads * V], sg[kThreads * V];
     const Place<V> P(A, blockIdx.x, A.rows, A.total);
+    grid_go();
+    grid_wait();
     float db[V], dg[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) db[e] = dg[e] = 0.f;
@@ -600,6 +613,8 @@ __global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 3 : 2) gn_bwd
 __global__ void __launch_bounds__(kThreads) gn_bwd_finish_kernel(const GnArgs A, const float* __restrict__ gamma) {
     __shared__ float2 red[kThreads];
     __shared__ float rw[kWarps];
+    grid_go();
+    grid_wait();
     const int sample = blockIdx.x / A.groups, g = blockIdx.x - sample * A.groups;
     const float2* p = A.part + (int64_t)sample * A.chunks * A.c + g * A.cg;
     const int64_t base = (int64_t)sample * A.c + g * A.cg;
@@ -647,6 +662,7 @@ template <typename T, int V, int POOL, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs A, const T* __restrict__ x, const T* __restrict__ dy,
                                                                   T* __restrict__ dx, int work, float* __restrict__ dgamma,
                                                                   float* __restrict__ dbeta) {
+    grid_wait();
     if ((int)blockIdx.x >= work) {
         const int c = ((int)blockIdx.x - work) * kThreads + threadIdx.x;
         if (blockIdx.y != 0 || c >= A.c) return;
@@ -751,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs 
 // Small samples: a cluster of blocks holds a sample's channels (or a part of them that is whole groups) in registers, so that
 // one launch reads x (and dy) once; the blocks exchange their group sums through each other's shared memory.
 
-constexpr int kSmallThreads = 512;
+constexpr int kSmallThreads = 256;
 constexpr int kSmallWarps = kSmallThreads / 32;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -813,13 +829,13 @@ __device__ __forceinline__ void small_entries(const GnArgs& A, int lanes, const 
     int lp = 32, sh = 5;
     while (lp > lanes) lp >>= 1, --sh;
     for (int q = g * sp.units + (lane >> sh); q < qb; q += 32 >> sh) {
-        const int col = sp.per == 1 ? q : q / sp.per, slot = q - col * sp.per;
+        const int col = q >> sp.sh, slot = q & (sp.per - 1);
         for (int l = lane & (lp - 1); l < lanes; l += lp) f(slot * kSmallThreads + l * A.tile + col, l);
     }
 }
 
 template <typename T, int V, int POOL, int ACT, int R>
-__global__ void __launch_bounds__(kSmallThreads, 1) gn_small_fwd_kernel(const GnArgs A, const T* __restrict__ x,
+__global__ void __launch_bounds__(kSmallThreads, 2) gn_small_fwd_kernel(const GnArgs A, const T* __restrict__ x,
                                                                        const float* __restrict__ gamma, const float* __restrict__ beta,
                                                                        T* __restrict__ y, float* __restrict__ mean,
                                                                        float* __restrict__ rstd) {
@@ -829,6 +845,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_fwd_kernel(const Gn
     const int groups = A.tile * V / A.cg, g0 = blockIdx.y * groups;
     Held<T, V, POOL, R> H;
     H.load_all(A, P, x);
+    float a[V], m[V], be[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        a[e] = gamma && P.left ? gamma[P.c0 + e] : 1.f;
+        be[e] = beta && P.left ? beta[P.c0 + e] : 0.f;
+    }
     float k[V], s[V], q[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) k[e] = s[e] = q[e] = 0.f;
@@ -865,44 +887,45 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_fwd_kernel(const Gn
         }
 #pragma unroll
     for (int e = 0; e < V; ++e)
-        if (e % sp.span == 0) {
-            sm[e / sp.span * kSmallThreads + threadIdx.x] = k[e];
-            sq[e / sp.span * kSmallThreads + threadIdx.x] = q[e];
+        if ((e & (sp.span - 1)) == 0) {
+            const int at = (e * sp.per / V) * kSmallThreads + threadIdx.x;
+            sm[at] = k[e];
+            sq[at] = q[e];
         }
     __syncthreads();
     const int least = P.rows / P.lanes, more = P.rows - least * P.lanes;
     for (int g = threadIdx.x >> 5; g < groups; g += kSmallWarps) {
         const int q0 = g * sp.units;
-        const float about = sm[q0 % sp.per * kSmallThreads + q0 / sp.per];
-        float a = 0.f, b = 0.f;
+        const float about = sm[(q0 & (sp.per - 1)) * kSmallThreads + (q0 >> sp.sh)];
+        float sa = 0.f, sd = 0.f;
         small_entries<V>(A, P.lanes, sp, g, [&](int at, int l) {
             const float nl = (float)((least + (l < more)) * H.K * sp.span), d = sm[at] - about;
-            a = fmaf(nl, d, a);
-            b += nl > 0.f ? fmaf(nl * d, d, sq[at]) : 0.f;
+            sa = fmaf(nl, d, sa);
+            sd += nl > 0.f ? fmaf(nl * d, d, sq[at]) : 0.f;
         });
-        a = warp_sum(a);
-        b = warp_sum(b);
-        const float d = P.rows ? a / ((float)(P.rows * H.K) * (float)A.cg) : 0.f;
+        sa = warp_sum(sa);
+        sd = warp_sum(sd);
+        const float d = P.rows ? sa / ((float)(P.rows * H.K) * (float)A.cg) : 0.f;
         if ((threadIdx.x & 31) < A.chunks)
-            store_remote(&ex[P.rank * groups + g], threadIdx.x & 31, make_float2(about + d, nonneg(fmaf(-a, d, b))));
+            store_remote(&ex[P.rank * groups + g], threadIdx.x & 31, make_float2(about + d, nonneg(fmaf(-sa, d, sd))));
     }
     cluster_sync();
     float2* stat = ex + A.chunks * groups;
     for (int g = threadIdx.x; g < groups; g += kSmallThreads) {
         // the blocks' means and deviations joined about the first's
         const float about = ex[g].x, per = (float)(H.K * A.cg);
-        float a = 0.f, b = 0.f;
+        float sa = 0.f, sd = 0.f;
         for (int r = 0; r < A.chunks; ++r) {
             const float nr = (float)max(0, min(A.rows, (int)A.total - r * A.rows)) * per;
             const float2 t = ex[r * groups + g];
             const float d = t.x - about;
             if (nr > 0.f) {
-                a = fmaf(nr, d, a);
-                b += fmaf(nr * d, d, t.y);
+                sa = fmaf(nr, d, sa);
+                sd += fmaf(nr * d, d, t.y);
             }
         }
-        const float count = (float)A.s * (float)A.cg, d = a / count;
-        const float mu = about + d, rs = 1.f / sqrtf(nonneg(fmaf(-a, d, b)) / count + A.eps);
+        const float count = (float)A.s * (float)A.cg, d = sa / count;
+        const float mu = about + d, rs = 1.f / sqrtf(nonneg(fmaf(-sa, d, sd)) / count + A.eps);
         stat[g] = make_float2(mu, rs);
         if (P.rank == 0) {
             if (mean) mean[(int64_t)P.sample * A.groups + g0 + g] = mu;
@@ -911,13 +934,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_fwd_kernel(const Gn
     }
     __syncthreads();
     if (!P.left) return;
-    float a[V], m[V], be[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float2 t = stat[(P.col * V + e) / A.cg];
+        const float2 t = stat[A.gdiv.div(P.col * V + e)];
         m[e] = t.x;
-        a[e] = (gamma ? gamma[P.c0 + e] : 1.f) * t.y;
-        be[e] = beta ? beta[P.c0 + e] : 0.f;
+        a[e] *= t.y;
     }
     auto norm = [&](float (&f)[V]) {
         vsub<V>(f, f, m);
@@ -952,11 +973,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_fwd_kernel(const Gn
 
 // dx, and the block's channel sums: part[sample][rank][c].
 template <typename T, int V, int POOL, int ACT, int R>
-__global__ void __launch_bounds__(kSmallThreads, 1) gn_small_bwd_kernel(const GnArgs A, const T* __restrict__ x,
+__global__ void __launch_bounds__(kSmallThreads, 2) gn_small_bwd_kernel(const GnArgs A, const T* __restrict__ x,
                                                                        const float* __restrict__ gamma, const float* __restrict__ beta,
                                                                        const float* __restrict__ mean, const float* __restrict__ rstd,
                                                                        const T* __restrict__ dy, T* __restrict__ dx) {
     extern __shared__ float2 ex[];  // [rank][group of the tile], then the tile's (s1, s2)
+    grid_go();
     __shared__ float sb[kSmallThreads * V], sg[kSmallThreads * V];
     const SmallPlace<V> P(A);
     const int groups = A.tile * V / A.cg;
@@ -971,7 +993,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_bwd_kernel(const Gn
     if (P.left) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const int64_t g = (int64_t)P.sample * A.groups + (P.c0 + e) / A.cg;
+            const int64_t g = (int64_t)P.sample * A.groups + A.gdiv.div(P.c0 + e);
             m[e] = mean[g];
             rs[e] = rstd[g];
             a[e] = (gamma ? gamma[P.c0 + e] : 1.f) * rs[e];
@@ -1080,7 +1102,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_bwd_kernel(const Gn
     float k0[V], k1[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float2 t = stat[(P.col * V + e) / A.cg];
+        const float2 t = stat[A.gdiv.div(P.col * V + e)];
         k0[e] = -rs[e] * t.x;
         k1[e] = -rs[e] * rs[e] * t.y;
     }
@@ -1139,6 +1161,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) gn_small_bwd_kernel(const Gn
 __global__ void __launch_bounds__(kThreads) gn_channels_kernel(const float2* __restrict__ part, int64_t rows, int c,
                                                               float* __restrict__ dgamma, float* __restrict__ dbeta) {
     __shared__ float2 red[kWarps][33];
+    grid_wait();
     const int ch = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
     float tb = 0.f, tg = 0.f;
     if (ch < c) {
@@ -1190,10 +1213,10 @@ int vec_of(const cf_gn_desc* d) {
 // Chunks are cut for this many blocks, whatever the device: the workspace's size and the sums' order depend on the
 // descriptor alone.
 constexpr int kPlanBlocks = 4 * 152;
-// Voxels of a thread in a chunk, at most: at 16 bytes each a block reads 64 KB.
-constexpr int kMostRows = 16, kMostRowsScalar = 32;
+// Voxels of a thread in a chunk, at most; the forward's sums allow no more (gn_stats_kernel).
+constexpr int kMostRows = 32, kMostRowsBackward = 64;
 
-GnArgs make_args(const cf_gn_desc* d) {
+GnArgs make_args(const cf_gn_desc* d, bool backward) {
     GnArgs A{};
     const int v = vec_of(d);
     A.n = (int)d->n, A.d = (int)d->d, A.h = (int)d->h, A.w = (int)d->w, A.s = d->d * d->h * d->w;
@@ -1207,7 +1230,7 @@ GnArgs make_args(const cf_gn_desc* d) {
     A.total = A.s / win;
     if (win == 8) A.w2 = FastDiv::make((uint32_t)(d->w / 2)), A.h2 = FastDiv::make((uint32_t)(d->h / 2));
     // voxels of a row lane in a chunk: fewer than the most where there are not enough blocks, but four (a window) at least
-    const int64_t lanes = kThreads / A.tile, most = v > 1 ? kMostRows : kMostRowsScalar;
+    const int64_t lanes = kThreads / A.tile, most = backward ? kMostRowsBackward : kMostRows;
     const int64_t share = (A.s * A.n * A.tiles + kPlanBlocks * lanes - 1) / (kPlanBlocks * lanes);
     const int64_t per = std::max<int64_t>(win == 8 ? 8 : 4, std::min(share, most)) / win * win;
     A.rows = (int)std::min(A.total, lanes * per / win);
@@ -1215,6 +1238,7 @@ GnArgs make_args(const cf_gn_desc* d) {
     A.chunks = (int)((A.total + A.rows - 1) / A.rows);
     A.tdiv = FastDiv::make((uint32_t)A.tile);
     A.cdiv = FastDiv::make((uint32_t)A.chunks);
+    A.gdiv = FastDiv::make((uint32_t)A.cg);
     return A;
 }
 
@@ -1237,23 +1261,30 @@ bool small_args(const cf_gn_desc* d, bool backward, GnArgs& A) {
     }
     const int least = A.cg / a;  // vectors that are whole groups: lcm(cg, v) / v
     const int most = win == 8 ? kSmallWindows : backward ? kSmallItems / 2 : kSmallItems;
-    for (int split = 1; split <= vc / least; ++split) {  // the widest columns that fit
-        if ((vc / least) % split) continue;
+    // of all ways to cut the columns and the rows, the one whose waves of blocks take the fewest steps: a block's start, its
+    // items one after the other, and the exchange where a sample has several blocks
+    int64_t best = INT64_MAX;
+    for (int split = 1; split <= vc / least; ++split) {
         const int tile = vc / split;
-        if (tile > kSmallThreads || tile * v / A.cg > 64) continue;
         if (split > 1 && (int64_t)tile * v * size < 64) break;
-        const int64_t lanes = kSmallThreads / tile, need = (A.total + lanes * most - 1) / (lanes * most);
-        if (need > kMaxCluster) continue;
-        // more blocks than needed where there are SMs for them, down to a quarter of the items
-        const int64_t want = std::min<int64_t>((A.total + lanes * most / 4 - 1) / (lanes * std::max(1, most / 4)), 152 / (A.n * (int64_t)split));
-        int q = 1;
-        while (q < need || (2 * q <= want && 2 * q <= 8)) q *= 2;
-        A.tile = tile, A.tiles = split, A.chunks = q;
-        A.rows = (int)((A.total + q - 1) / q);
-        A.tdiv = FastDiv::make((uint32_t)tile);
-        return true;
+        if ((vc / least) % split || tile > kSmallThreads || tile * v / A.cg > 64) continue;
+        const int64_t lanes = kSmallThreads / tile;
+        for (int q = 1; q <= kMaxCluster; q *= 2) {
+            const int64_t rows = (A.total + q - 1) / q, items = (rows + lanes - 1) / lanes;
+            if (items > most) continue;
+            const int64_t waves = (A.n * (int64_t)split * q + 2 * 152 - 1) / (2 * 152);
+            const int64_t cost = waves * (6 + items * (win == 8 ? 4 : 1) + (q > 1 ? 4 : 0));
+            if (cost < best) {
+                best = cost;
+                A.tile = tile, A.tiles = split, A.chunks = q;
+                A.rows = (int)rows;
+            }
+            if (items == 1) break;
+        }
     }
-    return false;
+    if (best == INT64_MAX) return false;
+    A.tdiv = FastDiv::make((uint32_t)A.tile);
+    return true;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1280,13 +1311,28 @@ size_t place(GnArgs& A, bool backward, bool small, char* base) {
     return at;
 }
 
+// A launch that may begin before the one before it in the stream has ended (its kernel calls grid_wait).
+template <typename K, typename... P>
+void launch_after(const LaunchCtx& ctx, dim3 grid, K kern, P... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <typename T, int V, int POOL, int ACT>
 void launch_fwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const float* gamma, const float* beta, void* y, float* mean,
                 float* rstd) {
     const dim3 grid((unsigned)(A.n * A.chunks), A.tiles);
     gn_stats_kernel<T, V><<<grid, kThreads, 0, ctx.stream>>>(A, static_cast<const T*>(x));
-    gn_finish_kernel<V><<<A.n * A.groups, kThreads, 0, ctx.stream>>>(A, gamma, beta, mean, rstd);
-    gn_apply_kernel<T, V, POOL, ACT><<<grid, kThreads, 0, ctx.stream>>>(A, static_cast<const T*>(x), static_cast<T*>(y));
+    launch_after(ctx, dim3(A.n * A.groups), gn_finish_kernel<V>, A, gamma, beta, mean, rstd);
+    launch_after(ctx, grid, gn_apply_kernel<T, V, POOL, ACT>, A, static_cast<const T*>(x), static_cast<T*>(y));
 }
 
 template <typename T, int V, int POOL, int ACT>
@@ -1295,11 +1341,11 @@ void launch_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const floa
     const T *xt = static_cast<const T*>(x), *dyt = static_cast<const T*>(dy);
     const int work = A.n * A.chunks, blocks = dx ? work : 0, more = dgamma || dbeta ? (A.c + kThreads - 1) / kThreads : 0;
     gn_coef_kernel<<<(unsigned)(((int64_t)A.n * A.c + kThreads - 1) / kThreads), kThreads, 0, ctx.stream>>>(A, gamma, beta, mean, rstd);
-    gn_bwd_sums_kernel<T, V, POOL, ACT><<<dim3(work, A.tiles), kThreads, 0, ctx.stream>>>(A, xt, dyt);
-    gn_bwd_finish_kernel<<<A.n * A.groups, kThreads, 0, ctx.stream>>>(A, gamma);
+    launch_after(ctx, dim3(work, A.tiles), gn_bwd_sums_kernel<T, V, POOL, ACT>, A, xt, dyt);
+    launch_after(ctx, dim3(A.n * A.groups), gn_bwd_finish_kernel, A, gamma);
     if (blocks + more > 0)
-        gn_bwd_apply_kernel<T, V, POOL, ACT>
-            <<<dim3(blocks + more, A.tiles), kThreads, 0, ctx.stream>>>(A, xt, dyt, static_cast<T*>(dx), blocks, dgamma, dbeta);
+        launch_after(ctx, dim3(blocks + more, A.tiles), gn_bwd_apply_kernel<T, V, POOL, ACT>, A, xt, dyt, static_cast<T*>(dx), blocks,
+                     dgamma, dbeta);
 }
 
 // A launch in clusters of A.chunks blocks.
@@ -1349,7 +1395,7 @@ void launch_small_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, cons
     else
         launch_small(ctx, A, groups, gn_small_bwd_kernel<T, V, POOL, ACT, kMost>, A, xt, gamma, beta, mean, rstd, dyt, dxt);
     if (dgamma || dbeta)
-        gn_channels_kernel<<<(A.c + 31) / 32, kThreads, 0, ctx.stream>>>(A.part, (int64_t)A.n * A.chunks, A.c, dgamma, dbeta);
+        launch_after(ctx, dim3((A.c + 31) / 32), gn_channels_kernel, (const float2*)A.part, (int64_t)A.n * A.chunks, A.c, dgamma, dbeta);
 }
 
 // Calls f<T, V, POOL, ACT>(...) for the descriptor.
@@ -1394,7 +1440,7 @@ extern "C" {
 
 size_t cf_group_norm_workspace_size(const cf_gn_desc* desc, int32_t backward) {
     if (!desc_ok(desc) || supported(desc) != CF_OK) return 0;
-    GnArgs A = make_args(desc);
+    GnArgs A = make_args(desc, backward != 0);
     const bool small = small_args(desc, backward != 0, A);
     return place(A, backward != 0, small, nullptr);
 }
@@ -1406,7 +1452,7 @@ cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* 
         !aligned16(ws))
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
-    GnArgs A = make_args(desc);
+    GnArgs A = make_args(desc, false);
     const bool small = small_args(desc, false, A);
     if (ws == nullptr || ws_bytes < place(A, false, small, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
@@ -1427,7 +1473,7 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
         !aligned16(rstd) || !aligned16(dgamma) || !aligned16(dbeta) || !aligned16(ws))
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
-    GnArgs A = make_args(desc);
+    GnArgs A = make_args(desc, true);
     const bool small = small_args(desc, true, A);
     if (ws == nullptr || ws_bytes < place(A, true, small, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
