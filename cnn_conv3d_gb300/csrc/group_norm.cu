@@ -199,6 +199,105 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A thread's own ring of 16-byte slots in shared memory, filled by asynchronous copies: the backward's passes have no registers
+// for as many loads as must be in flight.  No thread waits for another's.
+constexpr uint32_t kSlot = kThreads * 16;  // from a thread's slot to its next
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> slot(uint32_t at) {
+    Pack<T, V> t;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&t);
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    return t;
+}
+
+// A thread's way through its rows of x (WIN: a window's eight voxels each) and dy, f(x's vectors, dy's) for each: through the
+// ring where vectors are 16 bytes, two batches of rows ahead.
+template <typename T, int V, bool WIN>
+struct Rows {
+    static constexpr int K = WIN ? 8 : 1, kBatch = WIN ? 1 : 4, kSlots = 2 * kBatch * (K + 1);
+    static constexpr bool kRing = sizeof(T) * V == 16;
+    static constexpr int kBytes = kRing ? kSlots * (int)kSlot : 0;
+    const T *xs, *px, *pd;
+    int64_t xstep, ystep, row;
+    int step, left, ahead;
+    Window w;
+
+    __device__ __forceinline__ Rows(const GnArgs& A, const Place<V>& P, const T* x, const T* dy) : w(A) {
+        xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
+        row = P.r0 + P.lane;
+        step = P.lanes;
+        left = ahead = P.left;
+        px = xs + (WIN ? window_at(A, row) : row * A.xp);
+        pd = dy + ((int64_t)P.sample * A.total + row) * A.yp + P.c0;
+        xstep = (int64_t)P.lanes * A.xp;
+        ystep = (int64_t)P.lanes * A.yp;
+    }
+    __device__ __forceinline__ void next(const GnArgs& A) {
+        row += step;
+        px = WIN ? xs + window_at(A, row) : px + xstep;
+        pd += ystep;
+    }
+    __device__ __forceinline__ void fetch(const GnArgs& A, uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i < ahead) {
+#pragma unroll
+                for (int j = 0; j < K; ++j) copy16(at + (i * (K + 1) + j) * kSlot, px + (WIN ? w.at(j) : 0));
+                copy16(at + (i * (K + 1) + K) * kSlot, pd);
+                next(A);
+            }
+        copy_commit();
+        ahead -= kBatch;
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(const GnArgs& A, uint32_t ring, F f) {
+        if constexpr (kRing) {
+            constexpr uint32_t kHalf = kBatch * (K + 1) * kSlot;
+            fetch(A, ring);
+            fetch(A, ring + kHalf);
+            uint32_t at = ring;
+            for (int i = 0; i < left; i += kBatch) {
+                copy_wait<1>();
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (i + u < left) {
+                        Pack<T, V> t[K];
+#pragma unroll
+                        for (int j = 0; j < K; ++j) t[j] = slot<T, V>(at + (u * (K + 1) + j) * kSlot);
+                        f(t, slot<T, V>(at + (u * (K + 1) + K) * kSlot));
+                    }
+                fetch(A, at);
+                at = at == ring ? ring + kHalf : ring;
+            }
+            copy_wait<0>();
+        } else {
+            constexpr int U = WIN ? 1 : 4;
+            for (int i = 0; i < left; i += U) {
+                Pack<T, V> t[U][K], d[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u < left) {
+#pragma unroll
+                        for (int j = 0; j < K; ++j) t[u][j] = load<T, V>(px + (WIN ? w.at(j) : 0));
+                        d[u] = load<T, V>(pd);
+                        next(A);
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u < left) f(t[u], d[u]);
+            }
+        }
+    }
+};
+
 // How a block adds up per group: a thread joins `span` neighbouring values of its vector, which are of one group, to a unit;
 // a group is `units` units, a warp takes its units times the row lanes.
 template <int V>
@@ -228,8 +327,8 @@ __device__ __forceinline__ int group_entries(const GnArgs& A, const Place<V>& P,
 }
 
 // Mean and sum of squared deviations of each group over a chunk: part[sample][chunk][tile][group].  A thread sums about its
-// first row: a chunk has at most 32 rows for it, and no more than that factor can be lost in the rounding where the first
-// row is far off.
+// first row, then about the mean of its first few: where the first row is far off, no more than a factor of those few can be
+// lost in the rounding.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, const T* __restrict__ x) {
     __shared__ float sm[kThreads * V], sq[kThreads * V];
@@ -250,6 +349,17 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
             vadd<V>(s, s, f);
             vfma<V>(q, f, f, q);
         };
+        // the sums moved from about k to about the mean of the n rows so far
+        auto recentre = [&](int n) {
+            const float inv = 1.f / (float)n;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float d = s[e] * inv;
+                k[e] += d;
+                q[e] = nonneg(fmaf(-s[e], d, q[e]));
+                s[e] = 0.f;
+            }
+        };
         int i = P.left;
         for (; i >= U; i -= U, p += U * step) {
             Pack<T, V> t[U];
@@ -257,15 +367,10 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
             for (int u = 0; u < U; ++u) t[u] = load<T, V>(p + u * step);
 #pragma unroll
             for (int u = 0; u < U; ++u) add(t[u]);
+            if (i == P.left) recentre(U);
         }
         for (; i > 0; --i, p += step) add(load<T, V>(p));
-        const float n = (float)P.left, inv = 1.f / n;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float d = s[e] * inv;
-            k[e] += d;
-            q[e] = nonneg(fmaf(-s[e], d, q[e]));
-        }
+        recentre(P.left);
     }
     const Span<V> sp(A);
     // neighbours of equal counts: the mean of their means, and the deviations from it
@@ -511,9 +616,9 @@ __global__ void __launch_bounds__(kThreads) gn_coef_kernel(const GnArgs A, const
 
 // Channel sums of du and du xh over a chunk: part[sample][chunk][c].
 template <typename T, int V, int POOL, int ACT>
-__global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 3 : 2) gn_bwd_sums_kernel(const GnArgs A, const T* __restrict__ x,
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_sums_kernel(const GnArgs A, const T* __restrict__ x,
                                                                                           const T* __restrict__ dy) {
-    __shared__ float sb[kThreads * V], sg[kThreads * V];
+    extern __shared__ __align__(16) uint8_t ring[];  // afterwards the threads' sums
     const Place<V> P(A, blockIdx.x, A.rows, A.total);
     grid_go();
     grid_wait();
@@ -523,9 +628,6 @@ __global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 3 : 2) gn_bwd
     if (P.left) {
         float a[V], m[V], be[V];
         load_coef<V>(A, P, a, m, be);
-        const T* xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
-        const T* q = dy + ((int64_t)P.sample * A.total + P.r0 + P.lane) * A.yp + P.c0;
-        const int64_t ystep = (int64_t)P.lanes * A.yp;
         auto add = [&](float (&f)[V], float (&g)[V]) {
             float u[V];
             vsub<V>(f, f, m);
@@ -535,53 +637,32 @@ __global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 3 : 2) gn_bwd
             vadd<V>(db, db, u);
             vfma<V>(dg, u, f, dg);
         };
-        if constexpr (POOL == CF_POOL_NONE) {
-            constexpr int U = V > 1 ? 2 : 4;
-            const int64_t xstep = (int64_t)P.lanes * A.xp;
-            const T* p = xs + (P.r0 + P.lane) * A.xp;
-            auto one = [&](const Pack<T, V>& tx, const Pack<T, V>& td) {
-                float f[V], g[V];
-                unpack<T, V>(tx, f);
-                unpack<T, V>(td, g);
-                add(f, g);
-            };
-            int i = P.left;
-            for (; i >= U; i -= U, p += U * xstep, q += U * ystep) {
-                Pack<T, V> tx[U], td[U];
+        Rows<T, V, POOL != CF_POOL_NONE> W(A, P, x, dy);
+        W.each(A, smem_u32(ring) + threadIdx.x * 16, [&](const auto& t, const Pack<T, V>& td) {
+            float f[V], g[V];
+            unpack<T, V>(td, g);
+            if constexpr (POOL == CF_POOL_AVG) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) tx[u] = load<T, V>(p + u * xstep), td[u] = load<T, V>(q + u * ystep);
-#pragma unroll
-                for (int u = 0; u < U; ++u) one(tx[u], td[u]);
-            }
-            for (; i > 0; --i, p += xstep, q += ystep) one(load<T, V>(p), load<T, V>(q));
-        } else {
-            const Window W(A);
-            int64_t row = P.r0 + P.lane;
-            for (int i = 0; i < P.left; ++i, row += P.lanes, q += ystep) {
-                const T* p = xs + window_at(A, row);
-                Pack<T, V> t[8];
-                const Pack<T, V> td = load<T, V>(q);
-#pragma unroll
-                for (int w = 0; w < 8; ++w) t[w] = load<T, V>(p + W.at(w));
-                float f[V], g[V];
-                unpack<T, V>(td, g);
-                if (POOL == CF_POOL_MAX) {
-                    window_max<T, V>(t, a, f);
-                    add(f, g);
-                } else {
+                for (int j = 0; j < 8; ++j) {
+                    unpack<T, V>(td, g);
 #pragma unroll
                     for (int e = 0; e < V; ++e) g[e] *= 0.125f;
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        unpack<T, V>(t[w], f);
-                        add(f, g);
-                    }
+                    unpack<T, V>(t[j], f);
+                    add(f, g);
                 }
+            } else {
+                if constexpr (POOL == CF_POOL_MAX)
+                    window_max<T, V>(t, a, f);
+                else
+                    unpack<T, V>(t[0], f);
+                add(f, g);
             }
-        }
+        });
 #pragma unroll
         for (int e = 0; e < V; ++e) dg[e] *= __ldg(&A.coef[(int64_t)P.sample * A.c + P.c0 + e]).w;
     }
+    float *sb = reinterpret_cast<float*>(ring), *sg = sb + kThreads * V;
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         sb[e * kThreads + threadIdx.x] = db[e];
@@ -686,47 +767,26 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs 
         const float2 t = __ldg(&A.lin[(int64_t)P.sample * A.c + P.c0 + e]);
         k0[e] = t.x, k1[e] = t.y;
     }
-    const T* xs = x + (int64_t)P.sample * A.s * A.xp + P.c0;
+    extern __shared__ __align__(16) uint8_t ring[];
+    Rows<T, V, POOL != CF_POOL_NONE> W(A, P, x, dy);
     T* os = dx + (int64_t)P.sample * A.s * A.xp + P.c0;
-    const T* q = dy + ((int64_t)P.sample * A.total + P.r0 + P.lane) * A.yp + P.c0;
-    const int64_t ystep = (int64_t)P.lanes * A.yp;
-    if constexpr (POOL == CF_POOL_NONE) {
-        constexpr int U = V > 1 ? 2 : 4;
-        const int64_t xstep = (int64_t)P.lanes * A.xp;
-        const T* p = xs + (P.r0 + P.lane) * A.xp;
-        T* o = os + (P.r0 + P.lane) * A.xp;
-        auto one = [&](const Pack<T, V>& tx, const Pack<T, V>& td, T* at) {
-            float f[V], g[V], u[V];
-            unpack<T, V>(tx, f);
-            unpack<T, V>(td, g);
+    int64_t row = P.r0 + P.lane;
+    W.each(A, smem_u32(ring) + threadIdx.x * 16, [&](const auto& t, const Pack<T, V>& td) {
+        T* o = os + (POOL == CF_POOL_NONE ? row * A.xp : window_at(A, row));
+        row += P.lanes;
+        float f[V], g[V], u[V];
+        unpack<T, V>(td, g);
+        if constexpr (POOL == CF_POOL_NONE) {
+            unpack<T, V>(t[0], f);
             vsub<V>(f, f, m);
             vfma<V>(u, a, f, be);
 #pragma unroll
             for (int e = 0; e < V; ++e) g[e] *= act_grad<T, ACT>(u[e], A.slope);
             vfma<V>(f, k1, f, k0);
             vfma<V>(f, a, g, f);
-            store<T, V>(at, f);
-        };
-        int i = P.left;
-        for (; i >= U; i -= U, p += U * xstep, q += U * ystep, o += U * xstep) {
-            Pack<T, V> tx[U], td[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) tx[u] = load<T, V>(p + u * xstep), td[u] = load<T, V>(q + u * ystep);
-#pragma unroll
-            for (int u = 0; u < U; ++u) one(tx[u], td[u], o + u * xstep);
-        }
-        for (; i > 0; --i, p += xstep, q += ystep, o += xstep) one(load<T, V>(p), load<T, V>(q), o);
-    } else {
-        const Window W(A);
-        int64_t row = P.r0 + P.lane;
-        for (int i = 0; i < P.left; ++i, row += P.lanes, q += ystep) {
-            const int64_t at = window_at(A, row);
-            Pack<T, V> t[8];
-            const Pack<T, V> td = load<T, V>(q);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) t[w] = load<T, V>(xs + at + W.at(w));
-            float g[V], best[V], u[V];
-            unpack<T, V>(td, g);
+            store<T, V>(o, f);
+        } else {
+            float best[V];
             if (POOL == CF_POOL_MAX) {
                 window_max<T, V>(t, a, best);
                 vsub<V>(u, best, m);
@@ -738,9 +798,9 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs 
                 for (int e = 0; e < V; ++e) g[e] *= 0.125f;
             }
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                float f[V], lin[V];
-                unpack<T, V>(t[w], f);
+            for (int j = 0; j < 8; ++j) {
+                float lin[V];
+                unpack<T, V>(t[j], f);
                 vsub<V>(u, f, m);
                 vfma<V>(lin, k1, u, k0);
                 if (POOL == CF_POOL_MAX) {
@@ -757,10 +817,10 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs 
                     for (int e = 0; e < V; ++e) u[e] = g[e] * act_grad<T, ACT>(u[e], A.slope);
                     vfma<V>(lin, a, u, lin);
                 }
-                store<T, V>(os + at + W.at(w), lin);
+                store<T, V>(o + W.w.at(j), lin);
             }
         }
-    }
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -1203,18 +1263,18 @@ cf_status supported(const cf_gn_desc* d) {
     return CF_OK;
 }
 
-// Values of a vector access: 16 bytes where channels and pitches allow it, else one value.
+// Values of a vector access: 16 bytes where channels and pitches allow it, else four values, else one.
 int vec_of(const cf_gn_desc* d) {
-    const int v = d->dtype == CF_DT_F32 ? 4 : 8;
     const int64_t xp = d->x_pitch ? d->x_pitch : d->c, yp = d->y_pitch ? d->y_pitch : d->c;
-    return d->c % v == 0 && xp % v == 0 && yp % v == 0 ? v : 1;
+    for (int v = d->dtype == CF_DT_F32 ? 4 : 8; v >= 4; v /= 2)
+        if (d->c % v == 0 && xp % v == 0 && yp % v == 0) return v;
+    return 1;
 }
-
-// Chunks are cut for this many blocks, whatever the device: the workspace's size and the sums' order depend on the
-// descriptor alone.
-constexpr int kPlanBlocks = 4 * 152;
-// Voxels of a thread in a chunk, at most; the forward's sums allow no more (gn_stats_kernel).
-constexpr int kMostRows = 32, kMostRowsBackward = 64;
+// Chunks are cut for the blocks that fit 152 SMs at once, whatever the device: the workspace's size and the sums' order depend
+// on the descriptor alone.
+int plan_blocks(const cf_gn_desc* d, bool backward) { return 152 * (backward ? 2 : d->pool != CF_POOL_NONE ? 3 : 4); }
+// Voxels of a thread in a chunk, at most.
+constexpr int kMostRows = 64;
 
 GnArgs make_args(const cf_gn_desc* d, bool backward) {
     GnArgs A{};
@@ -1229,11 +1289,12 @@ GnArgs make_args(const cf_gn_desc* d, bool backward) {
     const int win = d->pool != CF_POOL_NONE ? 8 : 1;
     A.total = A.s / win;
     if (win == 8) A.w2 = FastDiv::make((uint32_t)(d->w / 2)), A.h2 = FastDiv::make((uint32_t)(d->h / 2));
-    // voxels of a row lane in a chunk: fewer than the most where there are not enough blocks, but four (a window) at least
-    const int64_t lanes = kThreads / A.tile, most = backward ? kMostRowsBackward : kMostRows;
-    const int64_t share = (A.s * A.n * A.tiles + kPlanBlocks * lanes - 1) / (kPlanBlocks * lanes);
-    const int64_t per = std::max<int64_t>(win == 8 ? 8 : 4, std::min(share, most)) / win * win;
-    A.rows = (int)std::min(A.total, lanes * per / win);
+    // items (voxels, or windows of eight) of a row lane in a chunk: an even share of as many waves of blocks as it takes for
+    // no more than kMostRows voxels, but four (a window) at least
+    const int64_t lanes = kThreads / A.tile, blocks = lanes * plan_blocks(d, backward);
+    const int64_t share = (A.total * A.n * A.tiles + blocks - 1) / blocks, waves = (share * win + kMostRows - 1) / kMostRows;
+    const int64_t per = std::max<int64_t>(win == 8 ? 1 : 4, (share + waves - 1) / waves);
+    A.rows = (int)std::min(A.total, lanes * per);
     A.srows = win * A.rows;
     A.chunks = (int)((A.total + A.rows - 1) / A.rows);
     A.tdiv = FastDiv::make((uint32_t)A.tile);
@@ -1313,10 +1374,12 @@ size_t place(GnArgs& A, bool backward, bool small, char* base) {
 
 // A launch that may begin before the one before it in the stream has ended (its kernel calls grid_wait).
 template <typename K, typename... P>
-void launch_after(const LaunchCtx& ctx, dim3 grid, K kern, P... args) {
+void launch_after(const LaunchCtx& ctx, dim3 grid, int shared, K kern, P... args) {
+    if (shared > (48 << 10)) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1331,8 +1394,8 @@ void launch_fwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const floa
                 float* rstd) {
     const dim3 grid((unsigned)(A.n * A.chunks), A.tiles);
     gn_stats_kernel<T, V><<<grid, kThreads, 0, ctx.stream>>>(A, static_cast<const T*>(x));
-    launch_after(ctx, dim3(A.n * A.groups), gn_finish_kernel<V>, A, gamma, beta, mean, rstd);
-    launch_after(ctx, grid, gn_apply_kernel<T, V, POOL, ACT>, A, static_cast<const T*>(x), static_cast<T*>(y));
+    launch_after(ctx, dim3(A.n * A.groups), 0, gn_finish_kernel<V>, A, gamma, beta, mean, rstd);
+    launch_after(ctx, grid, 0, gn_apply_kernel<T, V, POOL, ACT>, A, static_cast<const T*>(x), static_cast<T*>(y));
 }
 
 template <typename T, int V, int POOL, int ACT>
@@ -1341,11 +1404,12 @@ void launch_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, const floa
     const T *xt = static_cast<const T*>(x), *dyt = static_cast<const T*>(dy);
     const int work = A.n * A.chunks, blocks = dx ? work : 0, more = dgamma || dbeta ? (A.c + kThreads - 1) / kThreads : 0;
     gn_coef_kernel<<<(unsigned)(((int64_t)A.n * A.c + kThreads - 1) / kThreads), kThreads, 0, ctx.stream>>>(A, gamma, beta, mean, rstd);
-    launch_after(ctx, dim3(work, A.tiles), gn_bwd_sums_kernel<T, V, POOL, ACT>, A, xt, dyt);
-    launch_after(ctx, dim3(A.n * A.groups), gn_bwd_finish_kernel, A, gamma);
+    constexpr int kRing = Rows<T, V, POOL != CF_POOL_NONE>::kBytes, kSums = 2 * kThreads * V * (int)sizeof(float);
+    launch_after(ctx, dim3(work, A.tiles), std::max(kRing, kSums), gn_bwd_sums_kernel<T, V, POOL, ACT>, A, xt, dyt);
+    launch_after(ctx, dim3(A.n * A.groups), 0, gn_bwd_finish_kernel, A, gamma);
     if (blocks + more > 0)
-        launch_after(ctx, dim3(blocks + more, A.tiles), gn_bwd_apply_kernel<T, V, POOL, ACT>, A, xt, dyt, static_cast<T*>(dx), blocks,
-                     dgamma, dbeta);
+        launch_after(ctx, dim3(blocks + more, A.tiles), kRing, gn_bwd_apply_kernel<T, V, POOL, ACT>, A, xt, dyt, static_cast<T*>(dx),
+                     blocks, dgamma, dbeta);
 }
 
 // A launch in clusters of A.chunks blocks.
@@ -1395,38 +1459,36 @@ void launch_small_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, cons
     else
         launch_small(ctx, A, groups, gn_small_bwd_kernel<T, V, POOL, ACT, kMost>, A, xt, gamma, beta, mean, rstd, dyt, dxt);
     if (dgamma || dbeta)
-        launch_after(ctx, dim3((A.c + 31) / 32), gn_channels_kernel, (const float2*)A.part, (int64_t)A.n * A.chunks, A.c, dgamma, dbeta);
+        launch_after(ctx, dim3((A.c + 31) / 32), 0, gn_channels_kernel, (const float2*)A.part, (int64_t)A.n * A.chunks, A.c, dgamma, dbeta);
 }
 
 // Calls f<T, V, POOL, ACT>(...) for the descriptor.
-#define CF_GN_DISPATCH(d, f, ...)                                                     \
-    do {                                                                              \
-        const bool vec = vec_of(d) > 1, silu = (d)->act == CF_ACT_SILU;               \
-        if ((d)->dtype == CF_DT_F32) {                                                \
-            if (vec)                                                                  \
-                silu ? f<float, 4, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)            \
-                     : f<float, 4, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);          \
-            else                                                                      \
-                silu ? f<float, 1, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)            \
-                     : f<float, 1, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);          \
-        } else if ((d)->pool == CF_POOL_NONE) {                                       \
-            if (vec)                                                                  \
-                silu ? f<uint16_t, 8, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)         \
-                     : f<uint16_t, 8, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);       \
-            else                                                                      \
-                silu ? f<uint16_t, 1, CF_POOL_NONE, CF_ACT_SILU>(__VA_ARGS__)         \
-                     : f<uint16_t, 1, CF_POOL_NONE, CF_ACT_LRELU>(__VA_ARGS__);       \
-        } else if ((d)->pool == CF_POOL_MAX) {                                        \
-            vec ? f<uint16_t, 8, CF_POOL_MAX, CF_ACT_LRELU>(__VA_ARGS__)              \
-                : f<uint16_t, 1, CF_POOL_MAX, CF_ACT_LRELU>(__VA_ARGS__);             \
-        } else {                                                                      \
-            if (vec)                                                                  \
-                silu ? f<uint16_t, 8, CF_POOL_AVG, CF_ACT_SILU>(__VA_ARGS__)          \
-                     : f<uint16_t, 8, CF_POOL_AVG, CF_ACT_LRELU>(__VA_ARGS__);        \
-            else                                                                      \
-                silu ? f<uint16_t, 1, CF_POOL_AVG, CF_ACT_SILU>(__VA_ARGS__)          \
-                     : f<uint16_t, 1, CF_POOL_AVG, CF_ACT_LRELU>(__VA_ARGS__);        \
-        }                                                                             \
+#define CF_GN_ACT(d, f, T, V, POOL, ...) \
+    ((d)->act == CF_ACT_SILU ? f<T, V, POOL, CF_ACT_SILU>(__VA_ARGS__) : f<T, V, POOL, CF_ACT_LRELU>(__VA_ARGS__))
+#define CF_GN_POOL(d, f, V, ...)                                           \
+    do {                                                                   \
+        if ((d)->pool == CF_POOL_NONE)                                     \
+            CF_GN_ACT(d, f, uint16_t, V, CF_POOL_NONE, __VA_ARGS__);       \
+        else if ((d)->pool == CF_POOL_MAX)                                 \
+            f<uint16_t, V, CF_POOL_MAX, CF_ACT_LRELU>(__VA_ARGS__);        \
+        else                                                               \
+            CF_GN_ACT(d, f, uint16_t, V, CF_POOL_AVG, __VA_ARGS__);        \
+    } while (0)
+#define CF_GN_DISPATCH(d, f, ...)                                          \
+    do {                                                                   \
+        const int vec = vec_of(d);                                         \
+        if ((d)->dtype == CF_DT_F32) {                                     \
+            if (vec > 1)                                                   \
+                CF_GN_ACT(d, f, float, 4, CF_POOL_NONE, __VA_ARGS__);      \
+            else                                                           \
+                CF_GN_ACT(d, f, float, 1, CF_POOL_NONE, __VA_ARGS__);      \
+        } else if (vec == 8) {                                             \
+            CF_GN_POOL(d, f, 8, __VA_ARGS__);                              \
+        } else if (vec == 4) {                                             \
+            CF_GN_POOL(d, f, 4, __VA_ARGS__);                              \
+        } else {                                                           \
+            CF_GN_POOL(d, f, 1, __VA_ARGS__);                              \
+        }                                                                  \
     } while (0)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
