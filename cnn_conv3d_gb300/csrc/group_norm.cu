@@ -330,7 +330,7 @@ __device__ __forceinline__ int group_entries(const GnArgs& A, const Place<V>& P,
 // first row, then about the mean of its first few: where the first row is far off, no more than a factor of those few can be
 // lost in the rounding.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, const T* __restrict__ x) {
+__global__ void __launch_bounds__(kThreads, 3) gn_stats_kernel(const GnArgs A, const T* __restrict__ x) {
     __shared__ float sm[kThreads * V], sq[kThreads * V];
     grid_go();
     const Place<V> P(A, blockIdx.x, A.srows, A.s);
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats_kernel(const GnArgs A, c
 #pragma unroll
     for (int e = 0; e < V; ++e) k[e] = s[e] = q[e] = 0.f;
     if (P.left) {
-        constexpr int U = V > 1 ? 4 : 8;
+        constexpr int U = 8;
         const int64_t step = (int64_t)P.lanes * A.xp;
         const T* p = x + ((int64_t)P.sample * A.s + P.r0 + P.lane) * A.xp + P.c0;
         unpack<T, V>(load<T, V>(p), k);
@@ -1272,7 +1272,7 @@ int vec_of(const cf_gn_desc* d) {
 }
 // Chunks are cut for the blocks that fit 152 SMs at once, whatever the device: the workspace's size and the sums' order depend
 // on the descriptor alone.
-int plan_blocks(const cf_gn_desc* d, bool backward) { return 152 * (backward ? 2 : d->pool != CF_POOL_NONE ? 3 : 4); }
+int plan_blocks(const cf_gn_desc* d, bool backward) { return 152 * (backward ? 2 : 3); }
 // Voxels of a thread in a chunk, at most.
 constexpr int kMostRows = 64;
 
