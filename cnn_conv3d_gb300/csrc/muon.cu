@@ -372,12 +372,12 @@ __device__ __forceinline__ void store_row32(__half* op, int i, int j, int cb, co
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return pack_bf16x2(a, b); }
 
-// The result at row i, columns j .. j+31, from the last iterate (scaled by tau).
-__device__ __forceinline__ void write_result(const Mat& M, int i, int j, float (&y)[32]) {
+// The result at row i, columns j .. j+31, from the last iterate (scaled by tau); the matrix starts `off` values on.
+__device__ __forceinline__ void write_result(const Mat& M, int64_t off, int i, int j, float (&y)[32]) {
     const float inv = 1.f / M.tau;
     const int cnt = min(32, M.n - j);
     if (M.vec && cnt == 32) {
-        const int64_t base = (int64_t)i * M.n + j;
+        const int64_t base = off + (int64_t)i * M.n + j;
         if (M.w) {
             float4 w[8];
 #pragma unroll
@@ -404,7 +404,7 @@ __device__ __forceinline__ void write_result(const Mat& M, int i, int j, float (
         return;
     }
     // transposed: the lanes' rows are consecutive values; else a ragged end or rows that start anywhere
-    const int64_t base = M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j, st = M.tall ? M.k : 1;
+    const int64_t base = off + (M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j), st = M.tall ? M.k : 1;
     if (M.w) {
         float w[32];
 #pragma unroll
@@ -505,7 +505,7 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
 #pragma unroll
                         for (int e = 0; e < 32; ++e) usum = fmaf(y[e], y[e], usum);
                     } else if (i < M.k) {
-                        write_result(M, i, j, y);
+                        write_result(M, 0, i, j, y);
                     }
                 }
             }
@@ -701,6 +701,381 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     }
 }
 
+// ---------------------------------------------------------------------------
+// Matrices of at most 128 rows (the shorter side): a cluster of CTAs to a matrix runs all of it without leaving the chip, each
+// CTA on a slice of the columns.  X's slice is an operand in shared memory and, in fp32, an accumulator in tensor memory, onto
+// which U's product is added in place.  The Gram matrix's parts are exchanged through the CTAs' shared memory: each CTA sums
+// and rounds a slice of its columns for all, and A' A' and B' are then computed by every CTA for itself.
+
+constexpr int kSmallThreads = 256;
+constexpr int kSmallRows = 128, kSmallCols = 384;  // of a CTA: 128 tensor memory columns are left to the Gram matrix
+constexpr int kMaxCluster = 16;
+constexpr uint32_t kMaxShared = 1024 + (2 * kSmallCols / 64 + 8) * kBlkBytes + 4 * kTileF;
+constexpr uint32_t kGram = 384;                    // its tensor memory column
+
+struct SmallJob {
+    Mat mat[kMaxMats];
+    int uniform;       // all matrices are like mat[0], `stride` values apart
+    int64_t stride;
+    int cluster;       // CTAs of a matrix
+    int steps;
+    float a, b, c, eps, mu;
+    int nesterov;
+    int* status;
+    uint64_t wait_ns;
+};
+
+struct SmallShared {
+    uint64_t bar;
+    uint32_t tmem;
+    int abort;
+    float red[16];
+    float2 sums[kMaxCluster];  // of the CTAs: |X|^2, or the two sums of u^2
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* at, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    return a;
+}
+
+// Byte offset of element (r, c) of a 128-row operand in shared memory: 64 x 64 blocks, a column's two blocks in turn.
+__device__ __forceinline__ uint32_t small_at(int r, int c) {
+    return (uint32_t)(((c >> 6) * 2 + (r >> 6)) * (int)kBlkBytes + (r & 63) * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+}
+
+// The two sums of all threads, added to slot `rank` of every CTA of the cluster; visible after the next cluster_sync.
+__device__ __forceinline__ void share_sums(SmallShared& sh, float a, float b, int rank, int cluster) {
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(~0u, a, o);
+        b += __shfl_xor_sync(~0u, b, o);
+    }
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) sh.red[warp] = a, sh.red[8 + warp] = b;
+    __syncthreads();
+    if ((int)threadIdx.x < cluster) {
+        a = b = 0.f;
+        for (int i = 0; i < 8; ++i) a += sh.red[i], b += sh.red[8 + i];
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(&sh.sums[rank], threadIdx.x)), "f"(a), "f"(b) : "memory");
+    }
+}
+__device__ __forceinline__ float2 total_sums(const SmallShared& sh, int cluster) {
+    float2 t = make_float2(0.f, 0.f);
+    for (int i = 0; i < cluster; ++i) {
+        t.x += sh.sums[i].x;
+        t.y += sh.sums[i].y;
+    }
+    return t;
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid_constant__ SmallJob J) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ SmallShared sh;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int id = blockIdx.x / J.cluster, rank = (int)cluster_rank(), Q = J.cluster;
+    const Mat& M = J.mat[J.uniform ? 0 : id];
+    const int64_t off = J.uniform ? id * J.stride : 0;
+    const int kr = (M.k + 31) / 32 * 32;                                     // rows that are worked on
+    const int per = (M.cb + Q - 1) / Q, b0 = min(rank * per, M.cb), nb = min(per, M.cb - b0);  // 64-column blocks of the CTA
+    const int j0 = 64 * b0;
+    uint8_t* xh = smem;                              // 128 rows of X's operand
+    uint8_t* ad = smem + per * 2 * kBlkBytes;        // A', then B': 128 x 128
+    uint8_t* al = ad + 4 * kBlkBytes;                // what rounding left of A'
+    float4* recv = reinterpret_cast<float4*>(al + 4 * kBlkBytes);  // the other CTAs' parts of this one's slice of the Gram matrix
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = warp >> 2;
+    const int i = 32 * q + lane;
+    const bool rows = 32 * q < kr;                   // the warp's rows are worked on
+    uint32_t phase = 0;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&sh.bar, 1);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    // rows beyond those worked on stay zero
+    for (int t = threadIdx.x; t < nb * 2 * (int)kBlkBytes / 16; t += kSmallThreads) reinterpret_cast<uint4*>(xh)[t] = make_uint4(0, 0, 0, 0);
+    for (int t = threadIdx.x; t < 8 * (int)kBlkBytes / 16; t += kSmallThreads) reinterpret_cast<uint4*>(ad)[t] = make_uint4(0, 0, 0, 0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sh.tmem + ((uint32_t)(32 * q) << 16);
+    auto wait = [&]() {
+        mbar_wait(&sh.bar, phase & 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL);
+        ++phase;
+        tc_fence_after();
+    };
+
+    // u into tensor memory, with the momentum step, and the sums of its squares
+    float s = 0.f, s2 = 0.f;
+    if (rows)
+        for (int ch = half; ch < 2 * nb; ch += 2) {
+            uint32_t v[32];
+            const int j = j0 + 32 * ch;
+            const int64_t base = off + (M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j), st = M.tall ? M.k : 1;
+            float u[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const bool in = i < M.k && j + e < M.n;
+                u[e] = !in ? 0.f
+                           : M.f32 ? static_cast<const float*>(M.g)[base + e * st]
+                                   : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[base + e * st]);
+            }
+            if (M.m) {
+                float m[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) m[e] = i < M.k && j + e < M.n ? M.m[base + e * st] : 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    m[e] = fmaf(J.mu, m[e], u[e]);
+                    if (i < M.k && j + e < M.n) M.m[base + e * st] = m[e];
+                    u[e] = J.nesterov ? fmaf(J.mu, m[e], u[e]) : m[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                s = fmaf(u[e], u[e], s);
+                const float t = u[e] * kDown;
+                s2 = fmaf(t, t, s2);
+                v[e] = __float_as_uint(u[e]);
+            }
+            tmem_st32(tm + 32 * ch, v);
+        }
+    tmem_st_wait();
+    cluster_sync();  // every CTA of the cluster has begun
+    share_sums(sh, s, s2, rank, Q);
+    cluster_sync();
+    const float2 uu = total_sums(sh, Q);
+    const float pre = isinf(uu.x) ? kDown : 1.f, nrm = sqrtf(isinf(uu.x) ? uu.y : uu.x), inv = M.tau / (nrm + J.eps * pre);
+    if (rows)
+        for (int ch = half; ch < 2 * nb; ch += 2) {
+            uint32_t v[32];
+            tmem_ld32(tm + 32 * ch, v);
+            tmem_ld_wait();
+            float y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                y[e] = __uint_as_float(v[e]) * pre * inv;
+                v[e] = __float_as_uint(y[e]);
+            }
+            tmem_st32(tm + 32 * ch, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(xh + small_at(i, 32 * ch + e)) = pack8_f16(&y[e]);
+        }
+    tmem_st_wait();
+    float alpha = (nrm * inv) * (nrm * inv);  // |X|^2, scaled by tau^2
+    const float inv2 = 1.f / (M.tau * M.tau);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+
+    const int w = kSmallRows / Q;  // columns of the Gram matrix that a CTA sums
+    for (int step = 0; step < J.steps; ++step) {
+        if (threadIdx.x == 0) {
+            tc_fence_after();
+            const uint32_t xs = smem_u32(xh), id16 = idesc_f16(128, kr, 0);
+            for (int kk = 0; kk < 4 * nb; ++kk) {
+                const uint64_t d = sdesc(xs + (kk >> 2) * 2 * kBlkBytes + (kk & 3) * 32, 16, 1024, SWZ_128B);
+                umma_bf16(sh.tmem + kGram, d, d, id16, kk > 0);
+            }
+            umma_commit(&sh.bar);
+        }
+        __syncwarp();
+        wait();
+        alpha *= inv2 / (float)M.k;
+        if (Q == 1) {
+            if (rows)
+                for (int ch = half; ch < kr / 32; ch += 2) {
+                    uint32_t v[32];
+                    tmem_ld32(tm + kGram + 32 * ch, v);
+                    tmem_ld_wait();
+                    float h[32], l[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float d = __uint_as_float(v[e]) * inv2 - (i == 32 * ch + e && i < M.k ? alpha : 0.f);
+                        h[e] = __half2float(__float2half_rn(d));
+                        l[e] = d - h[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        *reinterpret_cast<uint4*>(ad + small_at(i, 32 * ch + e)) = pack8_f16(&h[e]);
+                        *reinterpret_cast<uint4*>(al + small_at(i, 32 * ch + e)) = pack8_f16(&l[e]);
+                    }
+                }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+        } else {
+            if (rows && nb > 0)
+                for (int ch = half; ch < kr / 32; ch += 2) {
+                    uint32_t v[32];
+                    tmem_ld32(tm + kGram + 32 * ch, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const int c = 32 * ch + e;
+                        const uint32_t at = remote(recv + (rank * (w / 4) + (c % w) / 4) * 128 + i, c / w);
+                        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[e]), "r"(v[e + 1]), "r"(v[e + 2]),
+                                     "r"(v[e + 3])
+                                     : "memory");
+                    }
+                }
+            tc_fence_before();
+            cluster_sync();
+            // the slice of all CTAs that have columns, in turn
+            const int have = (M.cb + per - 1) / per, r = threadIdx.x & 127;
+            if (r < kr && rank * w < kr)
+                for (int c4 = threadIdx.x >> 7; c4 < w / 4; c4 += 2) {
+                    float4 t = recv[c4 * 128 + r];
+                    for (int o = 1; o < have; ++o) {
+                        const float4 x = recv[(o * (w / 4) + c4) * 128 + r];
+                        t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+                    }
+                    const int j = rank * w + 4 * c4;
+                    float d[4] = {t.x * inv2, t.y * inv2, t.z * inv2, t.w * inv2}, h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (r == j + e && r < M.k) d[e] -= alpha;
+                        h[e] = __half2float(__float2half_rn(d[e]));
+                    }
+                    const uint32_t h0 = pack_f16(h[0], h[1]), h1 = pack_f16(h[2], h[3]);
+                    const uint32_t l0 = pack_f16(d[0] - h[0], d[1] - h[1]), l1 = pack_f16(d[2] - h[2], d[3] - h[3]);
+                    const uint32_t at = small_at(r, j);
+                    for (int o = 0; o < have; ++o) {
+                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(remote(ad + at, o)), "r"(h0), "r"(h1) : "memory");
+                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(remote(al + at, o)), "r"(l0), "r"(l1) : "memory");
+                    }
+                }
+            fence_async();
+            cluster_sync();
+        }
+        const float beta = alpha * fmaf(J.c, alpha, J.b), theta = step + 2 >= J.steps ? beta : 0.f;
+        const float wx = J.a + theta, wh = beta - theta, bb = fmaf(2.f * J.c, alpha, J.b);
+        if (threadIdx.x == 0) {
+            tc_fence_after();
+            fence_proxy_async_smem();
+            const uint32_t as = smem_u32(ad), id16 = idesc_f16(128, kr, 0);
+            for (int kk = 0; kk < kr / 16; ++kk) {
+                const uint64_t d = sdesc(as + (kk >> 2) * 2 * kBlkBytes + (kk & 3) * 32, 16, 1024, SWZ_128B);
+                umma_bf16(sh.tmem + kGram, d, d, id16, kk > 0);
+            }
+            umma_commit(&sh.bar);
+        }
+        __syncwarp();
+        // meanwhile what X itself contributes to its successor
+        if (rows)
+            for (int ch = half; ch < 2 * nb; ch += 2) {
+                uint32_t v[32];
+                tmem_ld32(tm + 32 * ch, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float y = __uint_as_float(v[e]);
+                    v[e] = __float_as_uint(fmaf(wx, y, wh * __half2float(__float2half_rn(y))));
+                }
+                tmem_st32(tm + 32 * ch, v);
+            }
+        tmem_st_wait();
+        wait();
+        if (rows)
+            for (int ch = half; ch < kr / 32; ch += 2) {
+                uint32_t v[32];
+                tmem_ld32(tm + kGram + 32 * ch, v);
+                uint4 h4[4], l4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h4[e] = *reinterpret_cast<const uint4*>(ad + small_at(i, 32 * ch + 8 * e));
+                    l4[e] = *reinterpret_cast<const uint4*>(al + small_at(i, 32 * ch + 8 * e));
+                }
+                tmem_ld_wait();
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t hw[4] = {h4[e].x, h4[e].y, h4[e].z, h4[e].w}, lw[4] = {l4[e].x, l4[e].y, l4[e].z, l4[e].w};
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hw[p]));
+                        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lw[p]));
+                        const int f = 8 * e + 2 * p;
+                        o[f] = fmaf(bb, fh.x + fl.x, J.c * __uint_as_float(v[f]));
+                        o[f + 1] = fmaf(bb, fh.y + fl.y, J.c * __uint_as_float(v[f + 1]));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(ad + small_at(i, 32 * ch + e)) = pack8_f16(&o[e]);
+            }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            tc_fence_after();
+            const uint32_t as = smem_u32(ad), xs = smem_u32(xh);
+            for (int kk = 0; kk < kr / 16; ++kk) {
+                const uint64_t da = sdesc(as + (kk >> 2) * 2 * kBlkBytes + (kk & 3) * 32, 16, 1024, SWZ_128B);
+                for (int c = 0; c < nb; c += 4)
+                    umma_bf16(sh.tmem + 64 * c, da,
+                              sdesc(xs + c * 2 * kBlkBytes + (kk >> 2) * kBlkBytes + (kk & 3) * 2048, 2 * kBlkBytes, 1024, SWZ_128B),
+                              idesc_f16(128, 64 * min(4, nb - c), 1), 1u);
+            }
+            umma_commit(&sh.bar);
+        }
+        __syncwarp();
+        wait();
+        const bool last = step + 1 == J.steps;
+        float us = 0.f;
+        if (rows)
+            for (int ch = half; ch < 2 * nb; ch += 2) {
+                uint32_t v[32];
+                tmem_ld32(tm + 32 * ch, v);
+                tmem_ld_wait();
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    y[e] = __uint_as_float(v[e]);
+                    us = fmaf(y[e], y[e], us);
+                }
+                if (!last) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(xh + small_at(i, 32 * ch + e)) = pack8_f16(&y[e]);
+                } else if (i < M.k) {
+                    write_result(M, off, i, j0 + 32 * ch, y);
+                }
+            }
+        if (!last) {
+            // |X|^2 of the next step, seen by all after the exchange of the Gram matrix begins
+            share_sums(sh, us, 0.f, rank, Q);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            if (Q > 1)
+                cluster_sync();
+            else
+                __syncthreads();
+            alpha = total_sums(sh, Q).x;
+        }
+    }
+    if (sh.abort && threadIdx.x == 0) {  // products in flight end before the CTA leaves
+        umma_commit(&sh.bar);
+        mbar_wait_timed(&sh.bar, phase & 1, J.wait_ns);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 512);
+    }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool shape_ok(int64_t rows, int64_t cols) { return rows > 0 && cols > 0; }
 bool shape_supported(int64_t rows, int64_t cols) { return rows <= 65536 && cols <= 65536; }
@@ -774,7 +1149,30 @@ size_t place(Mat* mats, int count, char* base) {
     return at;
 }
 
+// CTAs of a matrix in ns_small_kernel, 0 where it does not take the matrix: as few as hold its columns, but up to four blocks
+// of 64 to a CTA where it has more than one (the steps on X's columns then weigh as much as the exchange).
+int cluster_of(const Mat& M) {
+    const int64_t k = std::min(M.rows, M.cols), cb = (std::max(M.rows, M.cols) + 63) / 64;
+    if (k > kSmallRows || cb > kMaxCluster * (kSmallCols / 64)) return 0;
+    int q = 1;
+    if (cb > kSmallCols / 64)
+        while (q < kMaxCluster && 4 * q < cb) q *= 2;
+    return q;
+}
+
+// Matrices that all fit ns_small_kernel go there: the CTAs of a cluster, else 0.  (Beside larger ones they cost little.)
+int cluster_of(const std::vector<Mat>& mats) {
+    int most = 0;
+    for (const Mat& M : mats) {
+        const int q = cluster_of(M);
+        if (q == 0) return 0;
+        most = std::max(most, q);
+    }
+    return most;
+}
+
 size_t workspace_of(std::vector<Mat>& mats) {
+    if (cluster_of(mats)) return 256;
     size_t most = 0;
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         const int count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
@@ -784,7 +1182,44 @@ size_t workspace_of(std::vector<Mat>& mats) {
     return most;
 }
 
-cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws) {
+cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, int cluster, bool uniform) {
+    if (cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared) != cudaSuccess ||
+        cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return CF_ERR_CUDA;
+    const size_t each = uniform ? mats.size() : kMaxMats;
+    for (size_t b = 0; b < mats.size(); b += each) {
+        SmallJob J{};
+        const int count = (int)std::min(each, mats.size() - b);
+        int per = 1;
+        plan_sizes(&mats[b], uniform ? 1 : count);
+        for (int i = 0; i < (uniform ? 1 : count); ++i) {
+            J.mat[i] = mats[b + i];
+            per = std::max(per, (mats[b + i].cb + cluster - 1) / cluster);
+        }
+        J.uniform = uniform, J.stride = mats[0].rows * mats[0].cols;
+        J.cluster = cluster;
+        J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.mu = mu, J.nesterov = nesterov;
+        J.status = ctx.status;
+        J.wait_ns = ctx.wait_ns;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(count * cluster));
+        cfg.blockDim = dim3(kSmallThreads);
+        cfg.dynamicSmemBytes = 1024 + (2 * per + 8) * kBlkBytes + (cluster > 1 ? 4 * kTileF : 0);
+        cfg.stream = ctx.stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, ns_small_kernel, J) != cudaSuccess) return CF_ERR_CUDA;
+    }
+    return CF_OK;
+}
+
+// uniform: the matrices are of one batch, a matrix apart.
+cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws, bool uniform) {
+    if (const int cluster = cluster_of(mats)) return run_small(ctx, p, mu, nesterov, mats, cluster, uniform);
     if (cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess) return CF_ERR_CUDA;
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         Job J{};
@@ -855,7 +1290,7 @@ cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, v
     if (ws == nullptr || ws_bytes < workspace_of(mats)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    return run(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, 0.f, 0, mats, ws);
+    return run(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, 0.f, 0, mats, ws, true);
 }
 
 static cf_status muon_check(int32_t count, const cf_muon_param* p) {
@@ -906,7 +1341,7 @@ cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon
         mats[i].keep = 1.f - h->lr * h->weight_decay;
         mats[i].step = h->lr * params[i].scale;
     }
-    return run(ctx, p, h->momentum, h->nesterov != 0, mats, ws);
+    return run(ctx, p, h->momentum, h->nesterov != 0, mats, ws, false);
 }
 
 }  // extern "C"
