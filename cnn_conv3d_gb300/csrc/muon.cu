@@ -1,15 +1,12 @@
 // muon.cu -- orthogonalisation of matrices by Newton-Schulz products and the
 // momentum step that uses it, with their entry points.
 //
-// Two launches for all matrices of a call.  ns_input_kernel takes the momentum
-// step and the Frobenius norms' partial sums.  ns_kernel is one cooperative
-// launch of a CTA per SM that runs everything else as phases between grid-wide
-// barriers; a phase's items (tiles of all matrices) are dealt out over the CTAs:
-//   C  X = u / (|u| + eps) in operand form, k x n with k <= n
-//   then for each step
-//   G  partial sums of the Gram matrix X X^T (tiles on and above the diagonal,
-//      the long axis split so that the SMs are filled)
-//   R  A' = X X^T - alpha I, alpha = |X|^2 / k, from the partial sums
+// Matrices with a side of more than 128: three launches for all of a call.  ns_input_kernel takes the momentum step and the
+// Frobenius norms' partial sums, ns_convert_kernel writes X = u / (|u| + eps) in operand form, k x n with k <= n, and
+// ns_kernel is one cooperative launch of a CTA per SM that runs the steps as phases between grid-wide barriers; a phase's
+// items (tiles of all matrices) are dealt out over the CTAs:
+//   G  A' = X X^T - alpha I (tiles on and above the diagonal); where the long axis is split to fill the SMs, its parts' sums
+//   R  A' from the parts, where there are any
 //   S  B' = (b + 2 c alpha) A' + c A' A'     (so b A + c A^2 = beta I + B',
 //                                             beta = b alpha + c alpha^2)
 //   U  X = a X + beta X + B' X; the last step writes the result instead
@@ -19,8 +16,9 @@
 // relative to what is left.  Of beta X, the last two steps take X and the
 // earlier ones its operand: there B' X cancels beta X along directions whose
 // singular value is still small, and has the operand only.
-// Simulated against 64 bits (operands rounded, sums exact): 2e-4 to 1e-3 of the
-// result, where rounding A and B with their diagonals gives up to 4e-3.
+// Any alpha gives the same polynomial; it is where a flat spectrum would be, a^(2 step) / k, up to the value that the
+// polynomial leaves in place.  Simulated against 64 bits (operands rounded, sums exact): 3e-4 to 1.2e-3 of the result, where
+// rounding A and B with their diagonals gives up to 4e-3, and the mean of A's diagonal for alpha 2e-4 to 1e-3.
 // X is scaled by a power of two tau so that its entries stay well inside
 // fp16's normal range for every size.
 //
@@ -43,12 +41,13 @@ namespace {
 constexpr int kNormChunks = 256;          // partial sums of a matrix's norm, at most
 constexpr float kDown = 0x1p-80f;         // scale of the sums that stand in for overflowing ones
 constexpr int kMaxMats = 48;              // matrices of one launch
-constexpr int kThreads = 320;             // producer, issuer, eight epilogue warps
+constexpr int kEpiWarps = 12;             // epilogue warps
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, issuer, epilogue
 constexpr int kBlk = 64 * 64;             // values of an operand block
 constexpr uint32_t kBlkBytes = kBlk * 2;
-constexpr uint32_t kStageA = 4 * kBlkBytes, kStageB = 4 * kBlkBytes, kStage = kStageA + kStageB;
-constexpr int kStages = 3;
-constexpr uint32_t kSmem = kStages * kStage + 1024;
+constexpr uint32_t kRing = 24 * kBlkBytes;  // operand stages: as many as fit, of 4, 6 or 8 blocks
+constexpr int kMostStages = 6;
+constexpr uint32_t kSmem = kRing + 1024;
 constexpr int kTileF = 128 * 128;         // floats of a Gram tile
 
 struct Mat {
@@ -70,15 +69,16 @@ struct Mat {
     int64_t chunk;           // values of each
     int n0, c0, g0, r0, s0, u0;  // first item of each phase
     __half *xh[2], *ad, *bp;
-    float *x, *d, *part, *norm, *unorm, *alpha;
+    float *x, *d, *part, *norm;
 };
 
 struct Job {
     Mat mat[kMaxMats];
     int count, steps;
     int nn, nc, ng, nr, ns, nu;  // items of each phase
-    float a, b, c, eps, mu;
+    float a, b, c, eps, mu, cap;
     int nesterov;
+    int wide;        // some matrix has tiles of 256 rows
     uint32_t* sync;  // arrivals at the grid barrier, abort flag
     int* status;
     uint64_t wait_ns;
@@ -93,6 +93,7 @@ __device__ __forceinline__ float load_u(const Mat& M, const Job& J, int64_t i) {
 // The momentum step of one chunk, and its sums of u^2 and of (kDown u)^2, which stands in where the first overflows.
 __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ Job J) {
     __shared__ float red[16];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x < 2) J.sync[threadIdx.x] = 0;
     int i = 0;
     while (i + 1 < J.count && (int)blockIdx.x >= J.mat[i + 1].n0) ++i;
@@ -123,17 +124,23 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ J
     }
 }
 
-// Sum of v[0 .. count) over the block, the same everywhere and in a fixed order; all threads call it.
+// Sum of v[0 .. count) over a block of 256 threads, the same everywhere and in a fixed order; all threads call it.
 __device__ __forceinline__ float block_sum(const float* v, int count, float* red) {
-    float s = 0.f;
-    for (int i = threadIdx.x; i < count; i += kThreads) s += v[i];
+    float s = (int)threadIdx.x < count ? v[threadIdx.x] : 0.f;  // count <= kNormChunks
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
     __syncthreads();
     s = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) s += red[i];
+    for (int i = 0; i < 8; ++i) s += red[i];
     return s;
+}
+
+// alpha of a step: where a flat spectrum's squared singular values would be, at most what the polynomial leaves in place.
+__device__ __forceinline__ float alpha_of(float a, float cap, int k, int step) {
+    float t = 1.f / (float)k;
+    for (int i = 0; i < step; ++i) t *= a * a;
+    return fminf(t, cap);
 }
 
 // Offset in values of element (r, c) of a blocked operand with cb blocks a row.
@@ -155,38 +162,34 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
 }
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint64_t full[kMostStages], empty[kMostStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort;
-    float red[16];
 };
 
-// All CTAs of the grid: what any of them wrote before is seen by all after, by bulk copies too.
+// All CTAs of the grid: what any of them wrote before is seen by all after, by bulk copies too.  One thread's fences stand for
+// the block's: its barriers order them after, and before, everyone's accesses.
 __device__ bool grid_sync(const Job& J, uint32_t& target, Shared& sh) {
-    fence_async();
     __syncthreads();
     if (threadIdx.x == 0) {
         target += gridDim.x;
         if (*(volatile int*)&sh.abort) atomicExch(&J.sync[1], 1u);
-        __threadfence();
-        atomicAdd(&J.sync[0], 1u);
+        fence_async();
+        asm volatile("red.release.gpu.add.u32 [%0], 1;" ::"l"(&J.sync[0]) : "memory");
         const uint64_t t0 = globaltimer();
-        uint32_t seen, stop;
+        uint32_t seen, stop = 0;
         while (true) {
             asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(seen) : "l"(&J.sync[0]) : "memory");
             if (seen >= target) break;
+            if (globaltimer() - t0 < 50000) continue;  // the abort flag is for waits that are already long
             asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(stop) : "l"(&J.sync[1]) : "memory");
             if (stop == 0 && globaltimer() - t0 > J.wait_ns) {
                 atomicCAS(J.status, 0, (int)WAIT_GRID);
                 atomicExch(&J.sync[1], 1u);
                 stop = 1;
             }
-            if (stop) {
-                sh.abort = 1;
-                break;
-            }
+            if (stop) break;
         }
-        asm volatile("ld.relaxed.gpu.u32 %0, [%1];" : "=r"(stop) : "l"(&J.sync[1]) : "memory");
         if (stop) sh.abort = 1;
         fence_async();
     }
@@ -244,21 +247,28 @@ __device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
     return t;
 }
 
+// A role's way through the ring: each stage's parity, kept over phases that cut the ring differently.
 struct Pipe {
     int stage = 0;
-    uint32_t phase = 0, local = 0;
-    uint32_t issued = 0, par = 0;  // per stage: a copy was issued, parity of the last
-    __device__ __forceinline__ void next() {
-        if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-        }
+    uint32_t bits = 0, local = 0;
+    uint32_t issued = 0;  // stages that a copy was issued for
+    __device__ __forceinline__ uint32_t parity() const { return (bits >> stage) & 1; }
+    __device__ __forceinline__ void next(int stages) {
+        bits ^= 1u << stage;
+        if (++stage == stages) stage = 0;
     }
 };
+// Blocks of a stage in a phase.
+template <int PH>
+__device__ __forceinline__ int stage_blocks(const Job& J) {
+    return PH == PH_S ? 4 : J.wide ? 8 : PH == PH_U ? 6 : 4;
+}
 
 template <int PH>
 __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8_t* ring, Pipe& P) {
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
+    const int sb = stage_blocks<PH>(J), stages = 24 / sb;
+    P.stage = 0;
     int mat = 0;
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
         const Item t = item_of<PH>(J, it, mat);
@@ -270,21 +280,20 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
         const int ab = 2 * t.mr;
         const uint32_t bytes = (ab + (same ? 0 : t.nb)) * kBlkBytes;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
-            if (!mbar_wait(&sh.empty[P.stage], P.phase ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_PRODUCER_EMPTY)) return;
-            uint8_t* s = ring + P.stage * kStage;
+            if (!mbar_wait(&sh.empty[P.stage], P.parity() ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_PRODUCER_EMPTY)) return;
+            uint8_t *s = ring + P.stage * sb * kBlkBytes, *sB = s + ab * kBlkBytes;
             uint64_t* bar = &sh.full[P.stage];
             mbar_arrive_expect_tx(bar, bytes);
             for (int q = 0; q < ab; ++q)
                 bulk_load(s + q * kBlkBytes, a + ((int64_t)(ab * t.i + q) * acb + kb) * kBlk, kBlkBytes, bar);
             if (PH == PH_U) {
-                bulk_load(s + kStageA, M.xh[cur] + ((int64_t)kb * M.cb + 4 * t.j) * kBlk, t.nb * kBlkBytes, bar);
+                bulk_load(sB, M.xh[cur] + ((int64_t)kb * M.cb + 4 * t.j) * kBlk, t.nb * kBlkBytes, bar);
             } else if (!same) {
                 for (int q = 0; q < ab; ++q)
-                    bulk_load(s + kStageA + q * kBlkBytes, a + ((int64_t)(ab * t.j + q) * acb + kb) * kBlk, kBlkBytes, bar);
+                    bulk_load(sB + q * kBlkBytes, a + ((int64_t)(ab * t.j + q) * acb + kb) * kBlk, kBlkBytes, bar);
             }
             P.issued |= 1u << P.stage;
-            P.par = (P.par & ~(1u << P.stage)) | (P.phase << P.stage);
-            P.next();
+            P.next(stages);
         }
     }
 }
@@ -292,6 +301,8 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
 template <int PH>
 __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, Pipe& P) {
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
+    const int sb = stage_blocks<PH>(J), stages = 24 / sb;
+    P.stage = 0;
     int mat = 0;
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
         const Item t = item_of<PH>(J, it, mat);
@@ -306,9 +317,9 @@ __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, P
         const bool same = PH != PH_U && t.i == t.j;
         const uint32_t idesc = idesc_f16(128, 64 * t.nb, PH == PH_U);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
-            if (!mbar_wait(&sh.full[P.stage], P.phase, &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
+            if (!mbar_wait(&sh.full[P.stage], P.parity(), &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
             tc_fence_after();
-            const uint32_t as = smem_u32(ring + P.stage * kStage), bs = same ? as : as + kStageA;
+            const uint32_t as = smem_u32(ring + P.stage * sb * kBlkBytes), bs = same ? as : as + 2 * t.mr * kBlkBytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 // X as [contracted][columns]: 64-column atoms a block apart, 16 contracted rows a step
@@ -319,7 +330,7 @@ __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, P
                     umma_bf16(d[1], sdesc(as + 2 * kBlkBytes + k * 32, 16, 1024, SWZ_128B), bd, idesc, kb > t.kb0 || k > 0);
             }
             umma_commit(&sh.empty[P.stage]);
-            P.next();
+            P.next(stages);
         }
         for (int h = 0; h < t.mr; ++h) umma_commit(&sh.tfull[(P.local + h) & 1]);
         P.local += t.mr;
@@ -344,7 +355,7 @@ struct StepScalars {
 };
 __device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, int step) {
     StepScalars s;
-    s.alpha = *(volatile const float*)M.alpha;
+    s.alpha = alpha_of(J.a, J.cap, M.k, step);
     s.beta = s.alpha * fmaf(J.c, s.alpha, J.b);
     s.theta = step + 2 >= J.steps ? s.beta : 0.f;
     return s;
@@ -353,37 +364,36 @@ __device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, in
 __device__ __forceinline__ uint4 pack8_f16(const float* y) {
     return make_uint4(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
 }
-// 32 values of row i, columns j .. j+31, into a blocked operand: two 32-byte stores of two chunks each, which the XOR keeps
-// side by side.
-__device__ __forceinline__ void store_row32(__half* op, int i, int j, int cb, const float (&y)[32]) {
-#pragma unroll
-    for (int e = 0; e < 32; e += 16) {
-        uint4 p = pack8_f16(&y[e]), q = pack8_f16(&y[e + 8]);
-        if (i & 1) {
-            const uint4 t = p;
-            p = q;
-            q = t;
-        }
-        __half* at = op + (blocked(i, j + e, cb) & ~(int64_t)15);
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(p.x), "r"(p.y), "r"(p.z), "r"(p.w),
-                     "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
-                     : "memory");
+// 16 values of row i, columns j .. j+15, into a blocked operand: a 32-byte store of two chunks, which the XOR keeps side by
+// side.
+__device__ __forceinline__ void store_row16(__half* op, int i, int j, int cb, const float* y) {
+    uint4 p = pack8_f16(y), q = pack8_f16(y + 8);
+    if (i & 1) {
+        const uint4 t = p;
+        p = q;
+        q = t;
     }
+    __half* at = op + (blocked(i, j, cb) & ~(int64_t)15);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(p.x), "r"(p.y), "r"(p.z), "r"(p.w),
+                 "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return pack_bf16x2(a, b); }
 
-// The result at row i, columns j .. j+31, from the last iterate (scaled by tau); the matrix starts `off` values on.
-__device__ __forceinline__ void write_result(const Mat& M, int64_t off, int i, int j, float (&y)[32]) {
+// The result at row i, columns j .. j+C-1, from the last iterate (scaled by tau); the matrix starts `off` values on.
+template <int C>
+__device__ __forceinline__ void write_result(const Mat& M, int64_t off, int i, int j, float (&y)[C]) {
     const float inv = 1.f / M.tau;
-    const int cnt = min(32, M.n - j);
-    if (M.vec && cnt == 32) {
+    const int cnt = min(C, M.n - j);
+    if (cnt <= 0) return;
+    if (M.vec && cnt == C) {
         const int64_t base = off + (int64_t)i * M.n + j;
         if (M.w) {
-            float4 w[8];
+            float4 w[C / 4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const float4*>(M.w + base + 4 * e);
+            for (int e = 0; e < C / 4; ++e) w[e] = *reinterpret_cast<const float4*>(M.w + base + 4 * e);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < C / 4; ++e) {
                 w[e].x = y[4 * e] = M.keep * w[e].x - M.step * (y[4 * e] * inv);
                 w[e].y = y[4 * e + 1] = M.keep * w[e].y - M.step * (y[4 * e + 1] * inv);
                 w[e].z = y[4 * e + 2] = M.keep * w[e].z - M.step * (y[4 * e + 2] * inv);
@@ -392,11 +402,11 @@ __device__ __forceinline__ void write_result(const Mat& M, int64_t off, int i, i
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] *= inv;
+            for (int e = 0; e < C; ++e) y[e] *= inv;
         }
         if (M.o) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
+            for (int e = 0; e < C; e += 8)
                 *reinterpret_cast<uint4*>(M.o + base + e) =
                     make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]), pack_bf16(y[e + 4], y[e + 5]),
                                pack_bf16(y[e + 6], y[e + 7]));
@@ -406,115 +416,136 @@ __device__ __forceinline__ void write_result(const Mat& M, int64_t off, int i, i
     // transposed: the lanes' rows are consecutive values; else a ragged end or rows that start anywhere
     const int64_t base = off + (M.tall ? (int64_t)j * M.k + i : (int64_t)i * M.n + j), st = M.tall ? M.k : 1;
     if (M.w) {
-        float w[32];
+        float w[C];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = e < cnt ? M.w[base + e * st] : 0.f;
+        for (int e = 0; e < C; ++e) w[e] = e < cnt ? M.w[base + e * st] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < C; ++e) {
             y[e] = M.keep * w[e] - M.step * (y[e] * inv);
             if (e < cnt) M.w[base + e * st] = y[e];
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] *= inv;
+        for (int e = 0; e < C; ++e) y[e] *= inv;
     }
     if (M.o) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
+        for (int e = 0; e < C; ++e)
             if (e < cnt) M.o[base + e * st] = __bfloat16_as_ushort(__float2bfloat16_rn(y[e]));
     }
 }
 
+// A' at row i, columns j .. j+15 of the tile d (in fp32): kept in fp32 and as an operand, on both sides of the diagonal.
+__device__ __forceinline__ void store_gram16(const Mat& M, float* d, int r, int c, int i, int j, bool mirror, const float (&o)[16]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *tile_at(d, r, c + 4 * e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+    store_row16(M.ad, i, j, M.rb, o);
+    if (mirror) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) M.ad[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
+    }
+}
+// The 128 x 128 tile (ti, tj), ti <= tj, of A' in fp32.
+__device__ __forceinline__ float* gram_tile(const Mat& M, int ti, int tj) {
+    return M.d + (int64_t)(ti * M.mt - ti * (ti - 1) / 2 + tj - ti) * kTileF;
+}
+
+// 16 columns of the thread's row at a time, the warps of a row quarter in turn.
 template <int PH>
 __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared& sh, Pipe& P) {
+    constexpr int kTurn = kEpiWarps / 4;
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = (warp - 2) >> 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, turn = (warp - 2) >> 2;
     const int r = 32 * q + lane;
     int mat = 0;
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
         const Item t = item_of<PH>(J, it, mat);
         mat = t.mat;
         const Mat& M = J.mat[mat];
-        StepScalars sc{};
-        if (PH != PH_G) sc = scalars_of(J, M, step);
+        const StepScalars sc = scalars_of(J, M, step);
         for (int hh = 0; hh < t.mr; ++hh, ++P.local) {
             const uint32_t acc = P.local & 1, use = P.local >> 1;
             const int i = 128 * (t.mr * t.i + hh) + r;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
-            float4 x[8];
+            float4 x[4];
             float* xt = PH == PH_U ? x_tile(M, i) : nullptr;
             if (PH == PH_U) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = *tile_at(xt, r, 256 * t.j + 32 * half + 4 * e);
+                for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, 256 * t.j + 16 * turn + 4 * e);
             }
             if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
             tc_fence_after();
-            float usum = 0.f;
-            for (int ch = half; ch < 2 * t.nb; ch += 2) {
-                uint32_t v[32];
-                tmem_ld32(tm + 32 * ch, v);
-                const int c = 32 * ch;
+            for (int ch = turn; ch < 4 * t.nb; ch += kTurn) {
+                uint32_t v[32];  // the first 16
+                tmem_ld16(tm + 16 * ch, v);
+                const int c = 16 * ch;
                 if (PH == PH_G) {
-                    // 128 columns at a time, as phase R takes them
-                    float* part = M.part + ((int64_t)(it - M.g0) * t.mr * t.mr + hh * t.mr) * kTileF;
                     tmem_ld_wait();
+                    if (M.splits > 1) {
+                        // 128 columns at a time, as phase R takes them
+                        float* part = M.part + ((int64_t)(it - M.g0) * t.mr * t.mr + hh * t.mr) * kTileF;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                                                               __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                        for (int e = 0; e < 16; e += 4)
+                            *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                                   __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                    } else {
+                        const int ti = t.mr * t.i + hh, tj = t.mr * t.j + (c >> 7);
+                        if (ti <= tj) {
+                            const int j = 128 * tj + (c & 127);
+                            const float inv2 = 1.f / (M.tau * M.tau);
+                            float o[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(v[e]) * inv2 - (i == j + e && i < M.k ? sc.alpha : 0.f);
+                            store_gram16(M, gram_tile(M, ti, tj), r, c & 127, i, j, ti != tj, o);
+                        }
+                    }
                 } else if (PH == PH_S) {
                     const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
                     float* dt = M.d + (int64_t)(it - M.s0) * kTileF;
-                    float4 dd[8];
+                    float4 dd[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dd[e] = *tile_at(dt, r, c + 4 * e);
+                    for (int e = 0; e < 4; ++e) dd[e] = *tile_at(dt, r, c + 4 * e);
                     tmem_ld_wait();
-                    float o[32];
+                    float o[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         o[4 * e] = fmaf(bb, dd[e].x, J.c * __uint_as_float(v[4 * e]));
                         o[4 * e + 1] = fmaf(bb, dd[e].y, J.c * __uint_as_float(v[4 * e + 1]));
                         o[4 * e + 2] = fmaf(bb, dd[e].z, J.c * __uint_as_float(v[4 * e + 2]));
                         o[4 * e + 3] = fmaf(bb, dd[e].w, J.c * __uint_as_float(v[4 * e + 3]));
                     }
                     const int j = 128 * t.j + c;
-                    store_row32(M.bp, i, j, M.rb, o);
+                    store_row16(M.bp, i, j, M.rb, o);
                     if (t.i != t.j) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
+                        for (int e = 0; e < 16; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
                     }
                 } else {
                     const int j = 256 * t.j + c;
                     const float wx = J.a + sc.theta, wh = sc.beta - sc.theta;
-                    float y[32];
+                    float y[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[4 * e] = x[e].x, y[4 * e + 1] = x[e].y, y[4 * e + 2] = x[e].z, y[4 * e + 3] = x[e].w;
-                    if (ch + 2 < 2 * t.nb) {
+                    for (int e = 0; e < 4; ++e) y[4 * e] = x[e].x, y[4 * e + 1] = x[e].y, y[4 * e + 2] = x[e].z, y[4 * e + 3] = x[e].w;
+                    if (ch + kTurn < 4 * t.nb) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = *tile_at(xt, r, j + 64 + 4 * e);
+                        for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, j + 16 * kTurn + 4 * e);
                     }
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 16; ++e)
                         y[e] = fmaf(wx, y[e], fmaf(wh, __half2float(__float2half_rn(y[e])), __uint_as_float(v[e])));
                     if (step + 1 < J.steps) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < 4; ++e)
                             *tile_at(xt, r, j + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                        store_row32(M.xh[cur ^ 1], i, j, M.cb, y);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) usum = fmaf(y[e], y[e], usum);
+                        store_row16(M.xh[cur ^ 1], i, j, M.cb, y);
                     } else if (i < M.k) {
-                        write_result(M, 0, i, j, y);
+                        write_result<16>(M, 0, i, j, y);
                     }
                 }
             }
             tc_fence_before();
             mbar_arrive(&sh.tempty[acc]);
-            if (PH == PH_U && step + 1 < J.steps) {
-                for (int o = 16; o; o >>= 1) usum += __shfl_xor_sync(~0u, usum, o);
-                if (lane == 0) M.unorm[8 * ((it - M.u0) * t.mr + hh) + warp - 2] = usum;
-            }
         }
     }
 }
@@ -532,112 +563,87 @@ __device__ __forceinline__ void product_phase(const Job& J, int cur, int step, S
     __syncwarp();
 }
 
-// X in operand form from u: a thread makes eight values of a row at a time, with its lanes along the stored rows.
-__device__ __forceinline__ void convert_phase(const Job& J, Shared& sh) {
+// X in operand form and in fp32 from u, a 64 x 64 block of a matrix a block: a thread makes eight values of a row at a time,
+// with its lanes along the stored rows.
+__global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__ Job J) {
+    __shared__ float red[8];
     constexpr int kUnits = kBlk / 8;
-    int mat = 0, have = -1;
-    float pre = 0.f, inv = 0.f;
-    for (int it = blockIdx.x; it < J.nc; it += gridDim.x) {
-        while (mat + 1 < J.count && it >= J.mat[mat + 1].c0) ++mat;
-        const Mat& M = J.mat[mat];
-        if (mat != have) {
-            const float s = block_sum(M.norm, M.chunks, sh.red), s2 = block_sum(M.norm + kNormChunks, M.chunks, sh.red);
-            const float nrm = sqrtf(isinf(s) ? s2 : s);
-            // tau u / (|u| + eps) as (u pre) inv
-            pre = isinf(s) ? kDown : 1.f;
-            inv = M.tau / (nrm + J.eps * pre);
-            if (it == M.c0 && threadIdx.x == 0) M.unorm[0] = (nrm * inv) * (nrm * inv);  // |X|^2 of step 0
-            have = mat;
-        }
-        const int e = it - M.c0, bi = e / M.cb, bj = e % M.cb;
-        for (int t = threadIdx.x; t < kUnits; t += kThreads) {
-            const int r = M.tall ? t & 63 : t >> 3, c = 8 * (M.tall ? t >> 6 : t & 7);
-            const int i = 64 * bi + r, j = 64 * bj + c;
-            float y[8];
-            if (M.vec && j < M.n && i < M.k) {  // rows of a multiple of eight values
-                const int64_t at = (int64_t)i * M.n + j;
-                if (M.f32) {
-                    const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(M.g) + at);
-                    const float4 p = g[0], q = g[1];
-                    y[0] = p.x, y[1] = p.y, y[2] = p.z, y[3] = p.w, y[4] = q.x, y[5] = q.y, y[6] = q.z, y[7] = q.w;
-                    if (M.m) {
-                        const float4* m = reinterpret_cast<const float4*>(M.m + at);
-                        const float4 mp = m[0], mq = m[1];
-                        const float f[8] = {mp.x, mp.y, mp.z, mp.w, mq.x, mq.y, mq.z, mq.w};
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) y[x] = J.nesterov ? fmaf(J.mu, f[x], y[x]) : f[x];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int mat = 0;
+    while (mat + 1 < J.count && (int)blockIdx.x >= J.mat[mat + 1].c0) ++mat;
+    const Mat& M = J.mat[mat];
+    const float s = block_sum(M.norm, M.chunks, red), s2 = block_sum(M.norm + kNormChunks, M.chunks, red);
+    // tau u / (|u| + eps) as (u pre) inv
+    const float pre = isinf(s) ? kDown : 1.f, inv = M.tau / (sqrtf(isinf(s) ? s2 : s) + J.eps * pre);
+    const int e = blockIdx.x - M.c0, bi = e / M.cb, bj = e % M.cb;
+            for (int t = threadIdx.x; t < kUnits; t += 256) {
+                const int r = M.tall ? t & 63 : t >> 3, c = 8 * (M.tall ? t >> 6 : t & 7);
+                const int i = 64 * bi + r, j = 64 * bj + c;
+                float y[8];
+                if (M.vec && j < M.n && i < M.k) {  // rows of a multiple of eight values
+                    const int64_t at = (int64_t)i * M.n + j;
+                    if (M.f32) {
+                        const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(M.g) + at);
+                        const float4 p = g[0], q = g[1];
+                        y[0] = p.x, y[1] = p.y, y[2] = p.z, y[3] = p.w, y[4] = q.x, y[5] = q.y, y[6] = q.z, y[7] = q.w;
+                        if (M.m) {
+                            const float4* m = reinterpret_cast<const float4*>(M.m + at);
+                            const float4 mp = m[0], mq = m[1];
+                            const float f[8] = {mp.x, mp.y, mp.z, mp.w, mq.x, mq.y, mq.z, mq.w};
+    #pragma unroll
+                            for (int x = 0; x < 8; ++x) y[x] = J.nesterov ? fmaf(J.mu, f[x], y[x]) : f[x];
+                        }
+                    } else {
+                        const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(M.g) + at);
+                        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+    #pragma unroll
+                        for (int x = 0; x < 4; ++x) y[2 * x] = __uint_as_float(w[x] << 16), y[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
                     }
                 } else {
-                    const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(M.g) + at);
-                    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) y[2 * x] = __uint_as_float(w[x] << 16), y[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
+    #pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        y[x] = i < M.k && j + x < M.n ? load_u(M, J, M.tall ? (int64_t)(j + x) * M.k + i : (int64_t)i * M.n + j + x) : 0.f;
                 }
-            } else {
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    y[x] = i < M.k && j + x < M.n ? load_u(M, J, M.tall ? (int64_t)(j + x) * M.k + i : (int64_t)i * M.n + j + x) : 0.f;
+    #pragma unroll
+                for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
+                *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = pack8_f16(y);
+                float* xt = x_tile(M, i);
+                *tile_at(xt, i & 127, j) = make_float4(y[0], y[1], y[2], y[3]);
+                *tile_at(xt, i & 127, j + 4) = make_float4(y[4], y[5], y[6], y[7]);
             }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
-            *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = pack8_f16(y);
-            float* xt = x_tile(M, i);
-            *tile_at(xt, i & 127, j) = make_float4(y[0], y[1], y[2], y[3]);
-            *tile_at(xt, i & 127, j + 4) = make_float4(y[4], y[5], y[6], y[7]);
-        }
-    }
 }
 
-// A' of a slice of 16 columns and 128 rows of a Gram tile: the sum of its parts, less alpha on the diagonal, in fp32 and as an
-// operand, on both sides of the diagonal.
-__device__ __forceinline__ void reduce_phase(const Job& J, int step, Shared& sh) {
-    int mat = 0, have = -1;
-    float alpha = 0.f;
-    for (int it = blockIdx.x; it < J.nr; it += gridDim.x) {
+// A' of 128 x 128 tiles whose long axis was split: the sum of the parts, less alpha on the diagonal.  A thread takes four
+// columns of a row.
+__device__ __forceinline__ void reduce_phase(const Job& J, int step) {
+    constexpr int kUnits = kTileF / 4;
+    int mat = 0;
+    for (int u = blockIdx.x * kThreads + threadIdx.x; u < J.nr * kUnits; u += gridDim.x * kThreads) {
+        const int it = u / kUnits, in = u % kUnits, r = in & 127, c = 4 * (in >> 7);
         while (mat + 1 < J.count && it >= J.mat[mat + 1].r0) ++mat;
         const Mat& M = J.mat[mat];
-        const float inv2 = 1.f / (M.tau * M.tau);
-        if (mat != have) {
-            alpha = block_sum(M.unorm, step == 0 ? 1 : 8 * M.mt * M.ut, sh.red) * inv2 / (float)M.k;
-            have = mat;
-        }
-        const int slices = 8 * M.mr * M.mr;
-        const int e = it - M.r0, sl = e % slices;
-        if (e == 0 && threadIdx.x == 0) *M.alpha = alpha;
-        int gi, gj;
-        upper_tile(e / slices, M.gt, gi, gj);
-        const int sub = sl / 8;  // 128 x 128 part of the tile
-        const int ti = M.mr * gi + sub / M.mr, tj = M.mr * gj + sub % M.mr;
-        if (ti > tj) continue;
+        int ti, tj;
+        upper_tile(it - M.r0, M.mt, ti, tj);
+        const int gi = ti / M.mr, gj = tj / M.mr, sub = (ti % M.mr) * M.mr + tj % M.mr;
         const int64_t apart = (int64_t)M.mr * M.mr * kTileF;
-        float* part = M.part + (int64_t)(e / slices) * M.splits * apart + sub * kTileF;
-        float* d = M.d + (int64_t)(ti * M.mt - ti * (ti - 1) / 2 + tj - ti) * kTileF;
-        if (threadIdx.x < 256) {
-            const int r = threadIdx.x & 127, c = 16 * (sl % 8) + 4 * (threadIdx.x >> 7);
-            float4 s = *tile_at(part, r, c), u = *tile_at(part, r, c + 8);
-#pragma unroll 4
-            for (int w = 1; w < M.splits; ++w) {
-                const float4 x = *tile_at(part + w * apart, r, c), z = *tile_at(part + w * apart, r, c + 8);
-                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-                u.x += z.x, u.y += z.y, u.z += z.z, u.w += z.w;
-            }
-            float o[8] = {s.x, s.y, s.z, s.w, u.x, u.y, u.z, u.w};
-            const int i = 128 * ti + r, j = 128 * tj + c;
+        float* part = M.part + (int64_t)(gi * M.gt - gi * (gi - 1) / 2 + gj - gi) * M.splits * apart + sub * kTileF;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int w = 0; w < M.splits; ++w) {
+            const float4 x = *tile_at(part + w * apart, r, c);
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+        const float inv2 = 1.f / (M.tau * M.tau), alpha = alpha_of(J.a, J.cap, M.k, step);
+        const int i = 128 * ti + r, j = 128 * tj + c;
+        float o[4] = {s.x * inv2, s.y * inv2, s.z * inv2, s.w * inv2};
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                o[x] *= inv2;
-                if (i == j + x + (x & 4) && i < M.k) o[x] -= alpha;
-            }
+        for (int e = 0; e < 4; ++e)
+            if (i == j + e && i < M.k) o[e] -= alpha;
+        *tile_at(gram_tile(M, ti, tj), r, c) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint2*>(M.ad + blocked(i, j, M.rb)) = make_uint2(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]));
+        if (ti != tj) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float* f = o + 4 * p;
-                *tile_at(d, r, c + 8 * p) = make_float4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<uint2*>(M.ad + blocked(i, j + 8 * p, M.rb)) = make_uint2(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]));
-                if (ti != tj) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) M.ad[blocked(j + 8 * p + x, i, M.rb)] = __float2half_rn(f[x]);
-                }
-            }
+            for (int e = 0; e < 4; ++e) M.ad[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
         }
     }
 }
@@ -648,13 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMostStages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh.tfull[a], 1);
-            mbar_init(&sh.tempty[a], 256);
+            mbar_init(&sh.tempty[a], 32 * kEpiWarps);
         }
         mbar_init(&sh.drain, 1);
         sh.abort = 0;
@@ -670,14 +676,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
 
     Pipe P;
     uint32_t target = 0;
-    convert_phase(J, sh);
-    bool ok = grid_sync(J, target, sh);
+    bool ok = true;
     for (int step = 0; ok && step < J.steps; ++step) {
         const int cur = step & 1;
         product_phase<PH_G>(J, cur, step, sh, ring, P);
         if (!(ok = grid_sync(J, target, sh))) break;
-        reduce_phase(J, step, sh);
-        if (!(ok = grid_sync(J, target, sh))) break;
+        if (J.nr > 0) {
+            reduce_phase(J, step);
+            if (!(ok = grid_sync(J, target, sh))) break;
+        }
         product_phase<PH_S>(J, cur, step, sh, ring, P);
         if (!(ok = grid_sync(J, target, sh))) break;
         product_phase<PH_U>(J, cur, step, sh, ring, P);
@@ -686,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     // after a wait that gave up: copies and products in flight end before the CTA leaves
     if (*(volatile int*)&sh.abort) {
         if (threadIdx.x == 0) {
-            for (int s = 0; s < kStages; ++s)
-                if (P.issued & (1u << s)) mbar_wait_timed(&sh.full[s], (P.par >> s) & 1, J.wait_ns);
+            for (int s = 0; s < kMostStages; ++s)  // bits: the parity after a stage's last copy
+                if (P.issued & (1u << s)) mbar_wait_timed(&sh.full[s], ((P.bits >> s) & 1) ^ 1, J.wait_ns);
         } else if (threadIdx.x == 32) {
             umma_commit(&sh.drain);
             mbar_wait_timed(&sh.drain, 0, J.wait_ns);
@@ -719,7 +726,7 @@ struct SmallJob {
     int64_t stride;
     int cluster;       // CTAs of a matrix
     int steps;
-    float a, b, c, eps, mu;
+    float a, b, c, eps, mu, cap;
     int nesterov;
     int* status;
     uint64_t wait_ns;
@@ -730,7 +737,7 @@ struct SmallShared {
     uint32_t tmem;
     int abort;
     float red[16];
-    float2 sums[kMaxCluster];  // of the CTAs: |X|^2, or the two sums of u^2
+    float2 sums[kMaxCluster];  // of the CTAs: the two sums of u^2
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -874,7 +881,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
             for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(xh + small_at(i, 32 * ch + e)) = pack8_f16(&y[e]);
         }
     tmem_st_wait();
-    float alpha = (nrm * inv) * (nrm * inv);  // |X|^2, scaled by tau^2
     const float inv2 = 1.f / (M.tau * M.tau);
     fence_proxy_async_smem();
     tc_fence_before();
@@ -893,7 +899,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
         }
         __syncwarp();
         wait();
-        alpha *= inv2 / (float)M.k;
+        const float alpha = alpha_of(J.a, J.cap, M.k, step);
         if (Q == 1) {
             if (rows)
                 for (int ch = half; ch < kr / 32; ch += 2) {
@@ -1033,7 +1039,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
         __syncwarp();
         wait();
         const bool last = step + 1 == J.steps;
-        float us = 0.f;
         if (rows)
             for (int ch = half; ch < 2 * nb; ch += 2) {
                 uint32_t v[32];
@@ -1041,27 +1046,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
                 tmem_ld_wait();
                 float y[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    y[e] = __uint_as_float(v[e]);
-                    us = fmaf(y[e], y[e], us);
-                }
+                for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]);
                 if (!last) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(xh + small_at(i, 32 * ch + e)) = pack8_f16(&y[e]);
                 } else if (i < M.k) {
-                    write_result(M, off, i, j0 + 32 * ch, y);
+                    write_result<32>(M, off, i, j0 + 32 * ch, y);
                 }
             }
         if (!last) {
-            // |X|^2 of the next step, seen by all after the exchange of the Gram matrix begins
-            share_sums(sh, us, 0.f, rank, Q);
+            // (a cluster's CTAs write each other's A' only after the next exchange's first barrier)
             fence_proxy_async_smem();
             tc_fence_before();
-            if (Q > 1)
-                cluster_sync();
-            else
-                __syncthreads();
-            alpha = total_sums(sh, Q).x;
+            __syncthreads();
         }
     }
     if (sh.abort && threadIdx.x == 0) {  // products in flight end before the CTA leaves
@@ -1088,6 +1085,24 @@ bool poly_ok(const Poly& p) {
     return p.steps >= 1 && std::isfinite(p.a) && std::isfinite(p.b) && std::isfinite(p.c) && p.eps >= 0.f && std::isfinite(p.eps);
 }
 
+// The squared singular value that the polynomial leaves in place, the smallest root of a + b t + c t^2 = 1 in (0, 2]; 0 (alpha is
+// not used) where there is none.
+float cap_of(const Poly& p) {
+    const double a = p.a - 1.0, b = p.b, c = p.c;
+    double best = 0.0;
+    auto take = [&](double t) {
+        if (t > 0.0 && t <= 2.0 && (best == 0.0 || t < best)) best = t;
+    };
+    if (c == 0.0) {
+        if (b != 0.0) take(-a / b);
+    } else if (b * b >= 4.0 * a * c) {
+        const double r = std::sqrt(b * b - 4.0 * a * c);
+        take((-b - r) / (2.0 * c));
+        take((-b + r) / (2.0 * c));
+    }
+    return (float)best;
+}
+
 // The workspace is laid out for this many CTAs: the sizes do not depend on the device.
 constexpr int kPlanSms = 152;
 
@@ -1111,8 +1126,11 @@ void plan_sizes(Mat* mats, int count) {
         M.gt = (M.k + 128 * M.mr - 1) / (128 * M.mr), M.mt = M.mr * M.gt, M.rb = 2 * M.mt;
         blocks += (int64_t)M.gt * (M.gt + 1) / 2 * M.cb;
     }
-    // a CTA's share of phase G's blocks, at least four to a part (a part costs its sums' round trip through memory)
-    const int64_t share = std::max<int64_t>(4, (blocks + kPlanSms - 1) / kPlanSms);
+    // a CTA's share of phase G's blocks, at least four to a part; but no part at all where the longest axis takes a CTA no longer
+    // than phase R, its barrier and the parts' way through memory do (about 24 blocks)
+    int longest = 0;
+    for (int i = 0; i < count; ++i) longest = std::max(longest, mats[i].cb);
+    const int64_t share = longest <= 24 ? longest : std::max<int64_t>(4, (blocks + kPlanSms - 1) / kPlanSms);
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
         M.per = (int)std::min<int64_t>(share, M.cb);
@@ -1141,10 +1159,8 @@ size_t place(Mat* mats, int count, char* base) {
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
-        M.part = reinterpret_cast<float*>(take((size_t)M.gt * (M.gt + 1) / 2 * M.splits * M.mr * M.mr * kTileF * sizeof(float)));
+        M.part = reinterpret_cast<float*>(take(M.splits > 1 ? (size_t)M.gt * (M.gt + 1) / 2 * M.splits * M.mr * M.mr * kTileF * sizeof(float) : 0));
         M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
-        M.unorm = reinterpret_cast<float*>(take((size_t)M.mt * M.ut * 8 * sizeof(float)));
-        M.alpha = reinterpret_cast<float*>(take(sizeof(float)));
     }
     return at;
 }
@@ -1198,7 +1214,7 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
         }
         J.uniform = uniform, J.stride = mats[0].rows * mats[0].cols;
         J.cluster = cluster;
-        J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.mu = mu, J.nesterov = nesterov;
+        J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.cap = cap_of(p), J.mu = mu, J.nesterov = nesterov;
         J.status = ctx.status;
         J.wait_ns = ctx.wait_ns;
         cudaLaunchConfig_t cfg{};
@@ -1228,20 +1244,31 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         place(&mats[b], J.count, static_cast<char*>(ws));
         for (int i = 0; i < J.count; ++i) {
             Mat& M = J.mat[i] = mats[b + i];
+            J.wide |= M.mr == 2;
             M.n0 = J.nn, M.c0 = J.nc, M.g0 = J.ng, M.r0 = J.nr, M.s0 = J.ns, M.u0 = J.nu;
             const int tiles = M.gt * (M.gt + 1) / 2;
             J.nn += M.chunks;
             J.nc += M.rb * M.cb;
             J.ng += tiles * M.splits;
-            J.nr += tiles * 8 * M.mr * M.mr;
+            J.nr += M.splits > 1 ? M.mt * (M.mt + 1) / 2 : 0;
             J.ns += M.mt * (M.mt + 1) / 2;
             J.nu += M.gt * M.ut;
         }
-        J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.mu = mu, J.nesterov = nesterov;
+        J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.cap = cap_of(p), J.mu = mu, J.nesterov = nesterov;
         J.sync = static_cast<uint32_t*>(ws);
         J.status = ctx.status;
         J.wait_ns = ctx.wait_ns;
         ns_input_kernel<<<J.nn, 256, 0, ctx.stream>>>(J);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)J.nc);
+        cfg.blockDim = dim3(256);
+        cfg.stream = ctx.stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, ns_convert_kernel, J) != cudaSuccess) return CF_ERR_CUDA;
         void* args[] = {&J};
         if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(ns_kernel), dim3(ctx.num_sms), dim3(kThreads), args, kSmem,
                                         ctx.stream) != cudaSuccess)
