@@ -45,7 +45,7 @@ constexpr int kEpiWarps = 12;             // epilogue warps
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, issuer, epilogue
 constexpr int kBlk = 64 * 64;             // values of an operand block
 constexpr uint32_t kBlkBytes = kBlk * 2;
-constexpr uint32_t kRing = 24 * kBlkBytes;  // operand stages: as many as fit, of 4, 6 or 8 blocks
+constexpr uint32_t kRing = 24 * kBlkBytes;  // operand stages: as many as fit, of 4 or 6 blocks
 constexpr int kMostStages = 6;
 constexpr uint32_t kSmem = kRing + 1024;
 constexpr int kTileF = 128 * 128;         // floats of a Gram tile
@@ -61,9 +61,8 @@ struct Mat {
     float keep, step;        // w = keep w - step X
     float tau;
     int vec;                 // rows of the result start at 16 bytes
-    int mr;                  // a tile of phases G and U has mr * 128 rows
-    int rb, cb;              // operand blocks: X is rb x cb, A' and B' rb x rb
-    int mt, gt, ut;          // 128-row tiles, mr * 128-row tiles, 256-column tiles of X
+    int rb, cb, nx;          // operand blocks: X is rb x cb, of which nx have columns, A' and B' rb x rb
+    int mt, gt, ut;          // 128-row tiles, a tile's rows of those (1, in pairs 2) to a tile; 256-column tiles of X
     int splits, per;         // parts of the long axis in phase G, blocks of each
     int chunks;              // norm partials
     int64_t chunk;           // values of each
@@ -78,7 +77,6 @@ struct Job {
     int nn, nc, ng, nr, ns, nu;  // items of each phase
     float a, b, c, eps, mu, cap;
     int nesterov;
-    int wide;        // some matrix has tiles of 256 rows
     uint32_t* sync;  // arrivals at the grid barrier, abort flag
     int* status;
     uint64_t wait_ns;
@@ -199,11 +197,19 @@ __device__ bool grid_sync(const Job& J, uint32_t& target, Shared& sh) {
 
 enum { PH_G, PH_S, PH_U };
 
+// The products run on single CTAs, a tile of 128 rows each, or (PAIR) on pairs that share one of 256 rows: each CTA fetches its
+// own half of the rows and of the other side, and one instruction multiplies for both.  A pair's stages hold half as much for
+// the same products, so that twice as many are in flight.
+template <bool PAIR>
+__device__ __forceinline__ int unit_id() { return PAIR ? blockIdx.x >> 1 : blockIdx.x; }
+template <bool PAIR>
+__device__ __forceinline__ int unit_count() { return PAIR ? gridDim.x >> 1 : gridDim.x; }
+
 // An item of a product phase: which operand blocks, and how many.
 struct Item {
     int mat, i, j, split;  // tile, tile of the other side, part of the long axis
     int kb0, kb1;          // blocks of the contracted axis
-    int mr, nb;            // 128-row parts and 64-column blocks of the tile
+    int nb;                // 64-column blocks of the tile
 };
 
 // Tile e of those on and above the diagonal of t x t tiles, row by row.
@@ -219,7 +225,7 @@ __device__ __forceinline__ void upper_tile(int e, int t, int& i, int& j) {
 template <int PH>
 __device__ __forceinline__ int first_of(const Mat& M) { return PH == PH_G ? M.g0 : PH == PH_S ? M.s0 : M.u0; }
 
-template <int PH>
+template <int PH, bool PAIR>
 __device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
     while (mat + 1 < J.count && it >= first_of<PH>(J.mat[mat + 1])) ++mat;
     const Mat& M = J.mat[mat];
@@ -229,21 +235,20 @@ __device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
     t.split = 0;
     t.kb0 = 0;
     t.kb1 = (M.k + 63) / 64;
-    t.mr = PH == PH_S ? 1 : M.mr;
     if (PH == PH_U) {
         t.i = e % M.gt;
         t.j = e / M.gt;
-        t.nb = min(4, M.cb - 4 * t.j);
+        t.nb = PAIR ? 4 : min(4, M.cb - 4 * t.j);
         return t;
     }
     if (PH == PH_G) {
         t.split = e % M.splits;
         e /= M.splits;
         t.kb0 = t.split * M.per;
-        t.kb1 = min(t.kb0 + M.per, M.cb);
+        t.kb1 = min(t.kb0 + M.per, M.nx);
     }
-    upper_tile(e, PH == PH_G ? M.gt : M.mt, t.i, t.j);
-    t.nb = 2 * t.mr;
+    upper_tile(e, M.gt, t.i, t.j);
+    t.nb = PAIR ? 4 : 2;
     return t;
 }
 
@@ -258,38 +263,72 @@ struct Pipe {
         if (++stage == stages) stage = 0;
     }
 };
-// Blocks of a stage in a phase.
-template <int PH>
-__device__ __forceinline__ int stage_blocks(const Job& J) {
-    return PH == PH_S ? 4 : J.wide ? 8 : PH == PH_U ? 6 : 4;
+// Blocks of a stage in a phase: two of the CTA's rows, and the other side's.
+template <int PH, bool PAIR>
+__host__ __device__ constexpr int stage_blocks() { return PH == PH_U && !PAIR ? 6 : 4; }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* at, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    return a;
+}
+// An arrival at the first CTA's barrier, from either CTA of a pair.  What it announces is in place by then for every reader
+// (copies that have landed in shared memory, tensor memory that has been read): it orders no accesses of its own, and a release
+// for the cluster took the products from 0.25 to 0.7 us a stage.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote(bar, 0)) : "memory");
+}
+// D (both CTAs' tensor memory) (+)= A B: 256 rows, each CTA's shared memory holding half of A's and of B's rows at the same place.
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives at both CTAs' barrier when the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
 // A warp: each lane issues its own copy of a stage (one thread issuing eight took 1.4 us a stage).
-template <int PH>
+template <int PH, bool PAIR>
 __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8_t* ring, Pipe& P) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
-    const int sb = stage_blocks<PH>(J), stages = 24 / sb;
+    constexpr int sb = stage_blocks<PH, PAIR>(), stages = 24 / sb;
     P.stage = 0;
     int mat = 0;
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
-        const Item t = item_of<PH>(J, it, mat);
+    for (int it = unit_id<PAIR>(); it < total; it += unit_count<PAIR>()) {
+        const Item t = item_of<PH, PAIR>(J, it, mat);
         mat = t.mat;
         const Mat& M = J.mat[mat];
         const __half* a = PH == PH_G ? M.xh[cur] : PH == PH_S ? M.ad : M.bp;
         const int acb = PH == PH_G ? M.cb : M.rb;
         const bool same = PH != PH_U && t.i == t.j;
-        const int ab = 2 * t.mr;
-        const uint32_t bytes = (ab + (same ? 0 : t.nb)) * kBlkBytes;
-        // the lane's copy of each stage: a block of the tile's rows, of the other side's rows, or (U) X's row of blocks
-        const bool isb = lane >= ab;
-        const int q = isb ? lane - ab : lane;
-        const bool mine = lane < ab || (!same && q < (PH == PH_U ? 1 : ab));
-        const bool row = PH == PH_U && isb;
-        const __half* src = row ? M.xh[cur] + ((int64_t)t.kb0 * M.cb + 4 * t.j) * kBlk
-                                : a + ((int64_t)(ab * (isb ? t.j : t.i) + q) * acb + t.kb0) * kBlk;
+        const int cols = PH == PH_U ? (PAIR ? 2 : t.nb) : 2;  // blocks of the other side that the CTA fetches
+        const uint32_t bytes = (2 + (same ? 0 : cols)) * kBlkBytes;
+        // the lane's copy of each stage: a block of the tile's rows (lanes 0, 1), of the other side's rows (2, 3), or (U, lane 2)
+        // X's row of blocks
+        const bool isb = lane >= 2, row = PH == PH_U && isb;
+        const int q = lane & 1;
+        const bool mine = lane < 2 || (!same && lane < (PH == PH_U ? 3 : 4));
+        const int tr = (PAIR ? 4 : 2) * (isb ? t.j : t.i) + 2 * rank + q;
+        const __half* src = row ? M.xh[cur] + ((int64_t)t.kb0 * M.cb + 4 * t.j + 2 * rank) * kBlk : a + ((int64_t)tr * acb + t.kb0) * kBlk;
         const int64_t step = row ? (int64_t)M.cb * kBlk : kBlk;
-        const uint32_t size = row ? t.nb * kBlkBytes : kBlkBytes, dst = (isb ? ab + q : q) * kBlkBytes;
+        const uint32_t size = row ? cols * kBlkBytes : kBlkBytes, dst = (isb ? 2 + (row ? 0 : q) : q) * kBlkBytes;
         for (int kb = t.kb0; kb < t.kb1; ++kb, src += step) {
             const bool ok = mbar_wait(&sh.empty[P.stage], P.parity() ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_PRODUCER_EMPTY);
             if (!__all_sync(~0u, ok)) return;
@@ -303,42 +342,55 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
     }
 }
 
-template <int PH>
+// One thread.  In a pair the first CTA's issues for both; the second's tells it of each of its own stages that is full.
+template <int PH, bool PAIR>
 __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, Pipe& P) {
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
-    const int sb = stage_blocks<PH>(J), stages = 24 / sb;
+    constexpr int sb = stage_blocks<PH, PAIR>(), stages = 24 / sb;
+    const bool second = PAIR && cluster_rank() == 1;
     P.stage = 0;
     int mat = 0;
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
-        const Item t = item_of<PH>(J, it, mat);
+    for (int it = unit_id<PAIR>(); it < total; it += unit_count<PAIR>(), ++P.local) {
+        const Item t = item_of<PH, PAIR>(J, it, mat);
         mat = t.mat;
-        uint32_t d[2];
-        for (int h = 0; h < t.mr; ++h) {
-            const uint32_t acc = (P.local + h) & 1, use = (P.local + h) >> 1;
-            if (!mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_TMEM_EMPTY)) return;
-            d[h] = sh.tmem + acc * 256;
+        if (second) {
+            for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                if (!mbar_wait(&sh.full[P.stage], P.parity(), &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
+                arrive_first(&sh.full[P.stage]);
+                P.next(stages);
+            }
+            continue;
         }
+        const uint32_t acc = P.local & 1, use = P.local >> 1, d = sh.tmem + acc * 256;
+        if (!mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_TMEM_EMPTY)) return;
         tc_fence_after();
         const bool same = PH != PH_U && t.i == t.j;
-        const uint32_t idesc = idesc_f16(128, 64 * t.nb, PH == PH_U);
+        const uint32_t idesc = idesc_f16(PAIR ? 256 : 128, 64 * t.nb, PH == PH_U);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
             if (!mbar_wait(&sh.full[P.stage], P.parity(), &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
             tc_fence_after();
-            const uint32_t as = smem_u32(ring + P.stage * sb * kBlkBytes), bs = same ? as : as + 2 * t.mr * kBlkBytes;
+            const uint32_t as = smem_u32(ring + P.stage * sb * kBlkBytes), bs = same ? as : as + 2 * kBlkBytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                const uint64_t ad = sdesc(as + k * 32, 16, 1024, SWZ_128B);
                 // X as [contracted][columns]: 64-column atoms a block apart, 16 contracted rows a step
                 const uint64_t bd = PH == PH_U ? sdesc(bs + k * 2048, kBlkBytes, 1024, SWZ_128B)
                                                : sdesc(bs + k * 32, 16, 1024, SWZ_128B);
-                umma_bf16(d[0], sdesc(as + k * 32, 16, 1024, SWZ_128B), bd, idesc, kb > t.kb0 || k > 0);
-                if (PH != PH_S && t.mr == 2)
-                    umma_bf16(d[1], sdesc(as + 2 * kBlkBytes + k * 32, 16, 1024, SWZ_128B), bd, idesc, kb > t.kb0 || k > 0);
+                if (PAIR)
+                    umma_pair(d, ad, bd, idesc, kb > t.kb0 || k > 0);
+                else
+                    umma_bf16(d, ad, bd, idesc, kb > t.kb0 || k > 0);
             }
-            umma_commit(&sh.empty[P.stage]);
+            if (PAIR)
+                commit_pair(&sh.empty[P.stage]);
+            else
+                umma_commit(&sh.empty[P.stage]);
             P.next(stages);
         }
-        for (int h = 0; h < t.mr; ++h) umma_commit(&sh.tfull[(P.local + h) & 1]);
-        P.local += t.mr;
+        if (PAIR)
+            commit_pair(&sh.tfull[acc]);
+        else
+            umma_commit(&sh.tfull[acc]);
     }
 }
 
@@ -456,61 +508,64 @@ __device__ __forceinline__ float* gram_tile(const Mat& M, int ti, int tj) {
 }
 
 // 16 columns of the thread's row at a time, the warps of a row quarter in turn.
-template <int PH>
+template <int PH, bool PAIR>
 __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared& sh, Pipe& P) {
-    constexpr int kTurn = kEpiWarps / 4;
+    constexpr int kTurn = kEpiWarps / 4, kTile = PAIR ? 2 : 1;  // 128-row tiles of a tile
     const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, turn = (warp - 2) >> 2;
-    const int r = 32 * q + lane;
+    const int r = 32 * q + lane, rank = PAIR ? (int)cluster_rank() : 0;
     int mat = 0;
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
-        const Item t = item_of<PH>(J, it, mat);
+    for (int it = unit_id<PAIR>(); it < total; it += unit_count<PAIR>(), ++P.local) {
+        const Item t = item_of<PH, PAIR>(J, it, mat);
         mat = t.mat;
         const Mat& M = J.mat[mat];
         const StepScalars sc = scalars_of(J, M, step);
-        for (int hh = 0; hh < t.mr; ++hh, ++P.local) {
-            const uint32_t acc = P.local & 1, use = P.local >> 1;
-            const int i = 128 * (t.mr * t.i + hh) + r;
-            const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
-            float4 x[4];
-            float* xt = PH == PH_U ? x_tile(M, i) : nullptr;
-            if (PH == PH_U) {
+        const uint32_t acc = P.local & 1, use = P.local >> 1;
+        const int ti = kTile * t.i + rank, i = 128 * ti + r;
+        const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
+        float4 x[4];
+        float* xt = PH == PH_U ? x_tile(M, i) : nullptr;
+        if (PH == PH_U) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, 256 * t.j + 16 * turn + 4 * e);
-            }
-            if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
-            tc_fence_after();
-            for (int ch = turn; ch < 4 * t.nb; ch += kTurn) {
-                uint32_t v[32];  // the first 16
-                tmem_ld16(tm + 16 * ch, v);
-                const int c = 16 * ch;
-                if (PH == PH_G) {
-                    tmem_ld_wait();
-                    if (M.splits > 1) {
-                        // 128 columns at a time, as phase R takes them
-                        float* part = M.part + ((int64_t)(it - M.g0) * t.mr * t.mr + hh * t.mr) * kTileF;
+            for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, 256 * t.j + 16 * turn + 4 * e);
+        }
+        if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
+        tc_fence_after();
+        for (int ch = turn; ch < 4 * t.nb; ch += kTurn) {
+            uint32_t v[32];  // the first 16
+            tmem_ld16(tm + 16 * ch, v);
+            const int c = 16 * ch;
+            if (PH == PH_G) {
+                tmem_ld_wait();
+                if (M.splits > 1) {
+                    // 128 columns at a time, as phase R takes them
+                    float* part = M.part + ((int64_t)(it - M.g0) * kTile + rank) * kTile * kTileF;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                                                                   __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-                    } else {
-                        const int ti = t.mr * t.i + hh, tj = t.mr * t.j + (c >> 7);
-                        if (ti <= tj) {
-                            const int j = 128 * tj + (c & 127);
-                            const float inv2 = 1.f / (M.tau * M.tau);
-                            float o[16];
+                    for (int e = 0; e < 16; e += 4)
+                        *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                               __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                } else {
+                    const int tj = kTile * t.j + (c >> 7);
+                    if (ti <= tj) {
+                        const int j = 128 * tj + (c & 127);
+                        const float inv2 = 1.f / (M.tau * M.tau);
+                        float o[16];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(v[e]) * inv2 - (i == j + e && i < M.k ? sc.alpha : 0.f);
-                            store_gram16(M, gram_tile(M, ti, tj), r, c & 127, i, j, ti != tj, o);
-                        }
+                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(v[e]) * inv2 - (i == j + e && i < M.k ? sc.alpha : 0.f);
+                        store_gram16(M, gram_tile(M, ti, tj), r, c & 127, i, j, ti != tj, o);
                     }
-                } else if (PH == PH_S) {
-                    const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
-                    float* dt = M.d + (int64_t)(it - M.s0) * kTileF;
-                    float4 dd[4];
+                }
+            } else if (PH == PH_S) {
+                const int tj = kTile * t.j + (c >> 7);
+                const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
+                float4 dd[4];
+                if (ti <= tj) {
+                    float* dt = gram_tile(M, ti, tj);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dd[e] = *tile_at(dt, r, c + 4 * e);
-                    tmem_ld_wait();
+                    for (int e = 0; e < 4; ++e) dd[e] = *tile_at(dt, r, (c & 127) + 4 * e);
+                }
+                tmem_ld_wait();
+                if (ti <= tj) {
                     float o[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -519,51 +574,57 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
                         o[4 * e + 2] = fmaf(bb, dd[e].z, J.c * __uint_as_float(v[4 * e + 2]));
                         o[4 * e + 3] = fmaf(bb, dd[e].w, J.c * __uint_as_float(v[4 * e + 3]));
                     }
-                    const int j = 128 * t.j + c;
+                    const int j = 128 * tj + (c & 127);
                     store_row16(M.bp, i, j, M.rb, o);
-                    if (t.i != t.j) {
+                    if (ti != tj) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) M.bp[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
                     }
-                } else {
-                    const int j = 256 * t.j + c;
-                    const float wx = J.a + sc.theta, wh = sc.beta - sc.theta;
-                    float y[16];
+                }
+            } else {
+                const int j = 256 * t.j + c;
+                const float wx = J.a + sc.theta, wh = sc.beta - sc.theta;
+                float y[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[4 * e] = x[e].x, y[4 * e + 1] = x[e].y, y[4 * e + 2] = x[e].z, y[4 * e + 3] = x[e].w;
-                    if (ch + kTurn < 4 * t.nb) {
+                for (int e = 0; e < 4; ++e) y[4 * e] = x[e].x, y[4 * e + 1] = x[e].y, y[4 * e + 2] = x[e].z, y[4 * e + 3] = x[e].w;
+                if (ch + kTurn < 4 * t.nb) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, j + 16 * kTurn + 4 * e);
-                    }
-                    tmem_ld_wait();
+                    for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, j + 16 * kTurn + 4 * e);
+                }
+                tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        y[e] = fmaf(wx, y[e], fmaf(wh, __half2float(__float2half_rn(y[e])), __uint_as_float(v[e])));
-                    if (step + 1 < J.steps) {
+                for (int e = 0; e < 16; ++e)
+                    y[e] = fmaf(wx, y[e], fmaf(wh, __half2float(__float2half_rn(y[e])), __uint_as_float(v[e])));
+                if (step + 1 < J.steps) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *tile_at(xt, r, j + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                        store_row16(M.xh[cur ^ 1], i, j, M.cb, y);
-                    } else if (i < M.k) {
-                        write_result<16>(M, 0, i, j, y);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        *tile_at(xt, r, j + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                    store_row16(M.xh[cur ^ 1], i, j, M.cb, y);
+                } else if (i < M.k) {
+                    write_result<16>(M, 0, i, j, y);
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&sh.tempty[acc]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (PAIR)
+                arrive_first(&sh.tempty[acc]);
+            else
+                mbar_arrive(&sh.tempty[acc]);
         }
     }
 }
 
-template <int PH>
+template <int PH, bool PAIR>
 __device__ __forceinline__ void product_phase(const Job& J, int cur, int step, Shared& sh, uint8_t* ring, Pipe& P) {
     const int warp = threadIdx.x >> 5;
     if (warp == 0) {
-        produce<PH>(J, cur, sh, ring, P);
+        produce<PH, PAIR>(J, cur, sh, ring, P);
     } else if (warp == 1) {
-        if ((threadIdx.x & 31) == 0) issue<PH>(J, sh, ring, P);
+        if ((threadIdx.x & 31) == 0) issue<PH, PAIR>(J, sh, ring, P);
     } else {
-        epilogue<PH>(J, cur, step, sh, P);
+        epilogue<PH, PAIR>(J, cur, step, sh, P);
     }
     __syncwarp();
 }
@@ -620,8 +681,9 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__
 
 // A' of 128 x 128 tiles whose long axis was split: the sum of the parts, less alpha on the diagonal.  A thread takes four
 // columns of a row.
+template <bool PAIR>
 __device__ __forceinline__ void reduce_phase(const Job& J, int step) {
-    constexpr int kUnits = kTileF / 4;
+    constexpr int kUnits = kTileF / 4, kTile = PAIR ? 2 : 1;
     int mat = 0;
     for (int u = blockIdx.x * kThreads + threadIdx.x; u < J.nr * kUnits; u += gridDim.x * kThreads) {
         const int it = u / kUnits, in = u % kUnits, r = in & 127, c = 4 * (in >> 7);
@@ -629,8 +691,8 @@ __device__ __forceinline__ void reduce_phase(const Job& J, int step) {
         const Mat& M = J.mat[mat];
         int ti, tj;
         upper_tile(it - M.r0, M.mt, ti, tj);
-        const int gi = ti / M.mr, gj = tj / M.mr, sub = (ti % M.mr) * M.mr + tj % M.mr;
-        const int64_t apart = (int64_t)M.mr * M.mr * kTileF;
+        const int gi = ti / kTile, gj = tj / kTile, sub = (ti % kTile) * kTile + tj % kTile;
+        const int64_t apart = (int64_t)kTile * kTile * kTileF;
         float* part = M.part + (int64_t)(gi * M.gt - gi * (gi - 1) / 2 + gj - gi) * M.splits * apart + sub * kTileF;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -653,30 +715,40 @@ __device__ __forceinline__ void reduce_phase(const Job& J, int step) {
     }
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ Job J) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
+    const bool first = !PAIR || cluster_rank() == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMostStages; ++s) {
-            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.full[s], PAIR && first ? 2 : 1);
             mbar_init(&sh.empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh.tfull[a], 1);
-            mbar_init(&sh.tempty[a], 32 * kEpiWarps);
+            mbar_init(&sh.tempty[a], (PAIR ? 2 : 1) * kEpiWarps);
         }
         mbar_init(&sh.drain, 1);
         sh.abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(&sh.tmem, 512);
-        tmem_relinquish();
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(&sh.tmem, 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();  // the barriers of both CTAs are there
+    else
+        __syncthreads();
     tc_fence_after();
 
     Pipe P;
@@ -684,15 +756,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     bool ok = true;
     for (int step = 0; ok && step < J.steps; ++step) {
         const int cur = step & 1;
-        product_phase<PH_G>(J, cur, step, sh, ring, P);
+        product_phase<PH_G, PAIR>(J, cur, step, sh, ring, P);
         if (!(ok = grid_sync(J, target, sh))) break;
         if (J.nr > 0) {
-            reduce_phase(J, step);
+            reduce_phase<PAIR>(J, step);
             if (!(ok = grid_sync(J, target, sh))) break;
         }
-        product_phase<PH_S>(J, cur, step, sh, ring, P);
+        product_phase<PH_S, PAIR>(J, cur, step, sh, ring, P);
         if (!(ok = grid_sync(J, target, sh))) break;
-        product_phase<PH_U>(J, cur, step, sh, ring, P);
+        product_phase<PH_U, PAIR>(J, cur, step, sh, ring, P);
         if (step + 1 < J.steps) ok = grid_sync(J, target, sh);
     }
     // after a wait that gave up: copies and products in flight end before the CTA leaves
@@ -700,16 +772,25 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         if (threadIdx.x == 0) {
             for (int s = 0; s < kMostStages; ++s)  // bits: the parity after a stage's last copy
                 if (P.issued & (1u << s)) mbar_wait_timed(&sh.full[s], ((P.bits >> s) & 1) ^ 1, J.wait_ns);
-        } else if (threadIdx.x == 32) {
-            umma_commit(&sh.drain);
+        } else if (threadIdx.x == 32 && first) {
+            if (PAIR)
+                commit_pair(&sh.drain);
+            else
+                umma_commit(&sh.drain);
             mbar_wait_timed(&sh.drain, 0, J.wait_ns);
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(sh.tmem, 512);
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512) : "memory");
+        else
+            tmem_dealloc(sh.tmem, 512);
     }
 }
 
@@ -745,19 +826,6 @@ struct SmallShared {
     float2 sums[kMaxCluster];  // of the CTAs: the two sums of u^2
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t remote(const void* at, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-    return a;
-}
 
 // Byte offset of element (r, c) of a 128-row operand in shared memory: 64 x 64 blocks, a column's two blocks in turn.
 __device__ __forceinline__ uint32_t small_at(int r, int c) {
@@ -1110,46 +1178,53 @@ float cap_of(const Poly& p) {
 
 // The workspace is laid out for this many CTAs: the sizes do not depend on the device.
 constexpr int kPlanSms = 152;
+// Pairs of CTAs take a launch whose update products have this many tiles of 256 x 256, counted by their blocks of 64 contracted
+// values, or more.
+constexpr int64_t kPairWork = 1000;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Sizes, items and the split of the long axis of matrices that run in one launch.
-void plan_sizes(Mat* mats, int count) {
-    int64_t blocks = 0, tiles = 0;
+// Sizes, and the split of the long axis, of matrices that run in one launch; returns whether on pairs of CTAs.
+bool plan_sizes(Mat* mats, int count) {
+    int64_t blocks = 0, work = 0;
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
         M.tall = M.rows > M.cols;
         M.k = (int)std::min(M.rows, M.cols), M.n = (int)std::max(M.rows, M.cols);
         M.vec = !M.tall && M.n % 8 == 0;
-        M.cb = (M.n + 63) / 64, M.ut = (M.cb + 3) / 4;
-        tiles += (int64_t)((M.k + 127) / 128) * M.ut;
+        M.nx = (M.n + 63) / 64;
+        work += (int64_t)((M.k + 255) / 256) * ((M.nx + 3) / 4) * ((M.k + 63) / 64);
     }
-    for (int i = 0; i < count; ++i) {
-        Mat& M = mats[i];
-        // 256-row tiles fetch a third less for a product than 128-row ones, but there are half as many
-        M.mr = tiles >= 2 * kPlanSms && M.k > 256 ? 2 : 1;
-        M.gt = (M.k + 128 * M.mr - 1) / (128 * M.mr), M.mt = M.mr * M.gt, M.rb = 2 * M.mt;
-        blocks += (int64_t)M.gt * (M.gt + 1) / 2 * M.cb;
-    }
-    // a CTA's share of phase G's blocks, at least four to a part; but no part at all where the longest axis takes a CTA no longer
-    // than phase R, its barrier and the parts' way through memory do (about 24 blocks)
+    const bool pair = work >= kPairWork;
+    const int tile = pair ? 2 : 1;
     int longest = 0;
-    for (int i = 0; i < count; ++i) longest = std::max(longest, mats[i].cb);
-    const int64_t share = longest <= 24 ? longest : std::max<int64_t>(4, (blocks + kPlanSms - 1) / kPlanSms);
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
-        M.per = (int)std::min<int64_t>(share, M.cb);
-        M.splits = (M.cb + M.per - 1) / M.per;
+        M.cb = pair ? (M.nx + 3) / 4 * 4 : M.nx, M.ut = (M.nx + 3) / 4;
+        M.gt = (M.k + 128 * tile - 1) / (128 * tile), M.mt = tile * M.gt, M.rb = 2 * M.mt;
+        blocks += (int64_t)M.gt * (M.gt + 1) / 2 * M.nx;
+        longest = std::max(longest, M.nx);
+    }
+    // a unit's share of phase G's blocks, at least four to a part; but no part at all where the longest axis takes little longer
+    // than a share: phase R, its barrier and the parts' way through memory cost as much as about six blocks
+    const int units = kPlanSms / tile;
+    int64_t share = std::max<int64_t>(4, (blocks + units - 1) / units);
+    if (longest <= share + 6) share = longest;
+    for (int i = 0; i < count; ++i) {
+        Mat& M = mats[i];
+        M.per = (int)std::min<int64_t>(share, M.nx);
+        M.splits = (M.nx + M.per - 1) / M.per;
         const int64_t total = M.rows * M.cols;
         M.chunk = std::max<int64_t>(4096, (total + kNormChunks - 1) / kNormChunks);
         M.chunks = (int)((total + M.chunk - 1) / M.chunk);
         // entries of X are 1 / sqrt(k n) at first and at most about 1.2 / sqrt(n) in the mean later: a quarter of the former's inverse
         M.tau = std::exp2(std::floor(std::log2(std::max(4.0, std::sqrt((double)M.k * M.n)) / 4.0)));
     }
+    return pair;
 }
 
 // Places the matrices' buffers at `base` (which may be NULL, to count) and returns their size.
-size_t place(Mat* mats, int count, char* base) {
+size_t place(Mat* mats, int count, bool pair, char* base) {
     size_t at = 256;
     auto take = [&](size_t bytes) {
         char* p = base + at;
@@ -1164,7 +1239,7 @@ size_t place(Mat* mats, int count, char* base) {
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
-        M.part = reinterpret_cast<float*>(take(M.splits > 1 ? (size_t)M.gt * (M.gt + 1) / 2 * M.splits * M.mr * M.mr * kTileF * sizeof(float) : 0));
+        M.part = reinterpret_cast<float*>(take(M.splits > 1 ? (size_t)M.gt * (M.gt + 1) / 2 * M.splits * (pair ? 4 : 1) * kTileF * sizeof(float) : 0));
         M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
     }
     return at;
@@ -1197,8 +1272,8 @@ size_t workspace_of(std::vector<Mat>& mats) {
     size_t most = 0;
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         const int count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
-        plan_sizes(&mats[b], count);
-        most = std::max(most, place(&mats[b], count, nullptr));
+        const bool pair = plan_sizes(&mats[b], count);
+        most = std::max(most, place(&mats[b], count, pair, nullptr));
     }
     return most;
 }
@@ -1241,22 +1316,23 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
 // uniform: the matrices are of one batch, a matrix apart.
 cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws, bool uniform) {
     if (const int cluster = cluster_of(mats)) return run_small(ctx, p, mu, nesterov, mats, cluster, uniform);
-    if (cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess) return CF_ERR_CUDA;
+    if (cudaFuncSetAttribute(ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+        return CF_ERR_CUDA;
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         Job J{};
         J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
-        plan_sizes(&mats[b], J.count);
-        place(&mats[b], J.count, static_cast<char*>(ws));
+        const bool pair = plan_sizes(&mats[b], J.count);
+        place(&mats[b], J.count, pair, static_cast<char*>(ws));
         for (int i = 0; i < J.count; ++i) {
             Mat& M = J.mat[i] = mats[b + i];
-            J.wide |= M.mr == 2;
             M.n0 = J.nn, M.c0 = J.nc, M.g0 = J.ng, M.r0 = J.nr, M.s0 = J.ns, M.u0 = J.nu;
             const int tiles = M.gt * (M.gt + 1) / 2;
             J.nn += M.chunks;
             J.nc += M.rb * M.cb;
             J.ng += tiles * M.splits;
             J.nr += M.splits > 1 ? M.mt * (M.mt + 1) / 2 : 0;
-            J.ns += M.mt * (M.mt + 1) / 2;
+            J.ns += tiles;
             J.nu += M.gt * M.ut;
         }
         J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.cap = cap_of(p), J.mu = mu, J.nesterov = nesterov;
@@ -1274,10 +1350,20 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         cfg.attrs = at;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, ns_convert_kernel, J) != cudaSuccess) return CF_ERR_CUDA;
-        void* args[] = {&J};
-        if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(ns_kernel), dim3(ctx.num_sms), dim3(kThreads), args, kSmem,
-                                        ctx.stream) != cudaSuccess)
-            return CF_ERR_CUDA;
+        cudaLaunchConfig_t coop{};
+        coop.gridDim = dim3((unsigned)(pair ? ctx.num_sms / 2 * 2 : ctx.num_sms));
+        coop.blockDim = dim3(kThreads);
+        coop.dynamicSmemBytes = kSmem;
+        coop.stream = ctx.stream;
+        cudaLaunchAttribute ca[2];
+        ca[0].id = cudaLaunchAttributeCooperative;
+        ca[0].val.cooperative = 1;
+        ca[1].id = cudaLaunchAttributeClusterDimension;
+        ca[1].val.clusterDim.x = 2;
+        ca[1].val.clusterDim.y = ca[1].val.clusterDim.z = 1;
+        coop.attrs = ca;
+        coop.numAttrs = pair ? 2 : 1;
+        if (cudaLaunchKernelEx(&coop, pair ? ns_kernel<true> : ns_kernel<false>, J) != cudaSuccess) return CF_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
 }
