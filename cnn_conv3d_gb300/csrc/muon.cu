@@ -38,7 +38,7 @@
 namespace cf {
 namespace {
 
-constexpr int kNormChunks = 256;          // partial sums of a matrix's norm, at most
+constexpr int kNormChunks = 1024;         // partial sums of a matrix's norm, at most
 constexpr float kDown = 0x1p-80f;         // scale of the sums that stand in for overflowing ones
 constexpr int kMaxMats = 48;              // matrices of one launch
 constexpr int kEpiWarps = 12;             // epilogue warps
@@ -61,6 +61,7 @@ struct Mat {
     float keep, step;        // w = keep w - step X
     float tau;
     int vec;                 // rows of the result start at 16 bytes
+    int aligned;             // g starts at 16 bytes
     int rb, cb, nx;          // operand blocks: X is rb x cb, of which nx have columns, A' and B' rb x rb
     int mt, gt, ut;          // 128-row tiles, a tile's rows of those (1, in pairs 2) to a tile; 256-column tiles of X
     int splits, per;         // parts of the long axis in phase G, blocks of each
@@ -96,18 +97,39 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ J
     int i = 0;
     while (i + 1 < J.count && (int)blockIdx.x >= J.mat[i + 1].n0) ++i;
     const Mat& M = J.mat[i];
-    const int64_t b = (blockIdx.x - M.n0) * M.chunk, e = min(b + M.chunk, M.rows * M.cols);
+    int64_t b = (blockIdx.x - M.n0) * M.chunk;
+    const int64_t e = min(b + M.chunk, M.rows * M.cols);
     float s = 0.f, s2 = 0.f;
-    for (int64_t j = b + threadIdx.x; j < e; j += 256) {
-        float u = M.f32 ? static_cast<const float*>(M.g)[j] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[j]);
+    auto one = [&](float u, float m, float& mo) {  // returns u, and m's successor
         if (M.m) {
-            const float t = fmaf(J.mu, M.m[j], u);
-            M.m[j] = t;
-            u = J.nesterov ? fmaf(J.mu, t, u) : t;
+            mo = fmaf(J.mu, m, u);
+            u = J.nesterov ? fmaf(J.mu, mo, u) : mo;
         }
         s = fmaf(u, u, s);
         u *= kDown;
         s2 = fmaf(u, u, s2);
+    };
+    if (M.f32 && M.aligned) {
+        // chunks are whole vectors but for the matrix's end
+        const int64_t e4 = b + (e - b) / 4 * 4;
+#pragma unroll 2
+        for (int64_t j = b + 4 * threadIdx.x; j < e4; j += 1024) {
+            const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(M.g) + j);
+            float4 m = M.m ? *reinterpret_cast<const float4*>(M.m + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            one(u.x, m.x, m.x);
+            one(u.y, m.y, m.y);
+            one(u.z, m.z, m.z);
+            one(u.w, m.w, m.w);
+            if (M.m) *reinterpret_cast<float4*>(M.m + j) = m;
+        }
+        b = e4;
+    }
+#pragma unroll 4
+    for (int64_t j = b + threadIdx.x; j < e; j += 256) {
+        const float u = M.f32 ? static_cast<const float*>(M.g)[j] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[j]);
+        float m = M.m ? M.m[j] : 0.f;
+        one(u, m, m);
+        if (M.m) M.m[j] = m;
     }
     for (int o = 16; o; o >>= 1) {
         s += __shfl_down_sync(~0u, s, o);
@@ -124,7 +146,10 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ J
 
 // Sum of v[0 .. count) over a block of 256 threads, the same everywhere and in a fixed order; all threads call it.
 __device__ __forceinline__ float block_sum(const float* v, int count, float* red) {
-    float s = (int)threadIdx.x < count ? v[threadIdx.x] : 0.f;  // count <= kNormChunks
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormChunks / 256; ++i)
+        if ((int)threadIdx.x + 256 * i < count) s += v[threadIdx.x + 256 * i];
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
@@ -680,37 +705,56 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__
 }
 
 // A' of 128 x 128 tiles whose long axis was split: the sum of the parts, less alpha on the diagonal.  A thread takes four
-// columns of a row.
+// columns of a row at a time, kAhead of them at once.
 template <bool PAIR>
 __device__ __forceinline__ void reduce_phase(const Job& J, int step) {
-    constexpr int kUnits = kTileF / 4, kTile = PAIR ? 2 : 1;
-    int mat = 0;
-    for (int u = blockIdx.x * kThreads + threadIdx.x; u < J.nr * kUnits; u += gridDim.x * kThreads) {
-        const int it = u / kUnits, in = u % kUnits, r = in & 127, c = 4 * (in >> 7);
-        while (mat + 1 < J.count && it >= J.mat[mat + 1].r0) ++mat;
-        const Mat& M = J.mat[mat];
-        int ti, tj;
-        upper_tile(it - M.r0, M.mt, ti, tj);
-        const int gi = ti / kTile, gj = tj / kTile, sub = (ti % kTile) * kTile + tj % kTile;
-        const int64_t apart = (int64_t)kTile * kTile * kTileF;
-        float* part = M.part + (int64_t)(gi * M.gt - gi * (gi - 1) / 2 + gj - gi) * M.splits * apart + sub * kTileF;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int w = 0; w < M.splits; ++w) {
-            const float4 x = *tile_at(part + w * apart, r, c);
-            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    constexpr int kUnits = kTileF / 4, kTile = PAIR ? 2 : 1, kAhead = 4;
+    const int stride = gridDim.x * kThreads, total = J.nr * kUnits;
+    for (int u0 = blockIdx.x * kThreads + threadIdx.x; u0 < total; u0 += kAhead * stride) {
+        float4 s[kAhead];
+        auto place = [&](int u, int& mat, int& ti, int& tj, int& r, int& c) {
+            const int it = u / kUnits, in = u % kUnits;
+            r = in & 127, c = 4 * (in >> 7);
+            mat = 0;
+            while (mat + 1 < J.count && it >= J.mat[mat + 1].r0) ++mat;
+            upper_tile(it - J.mat[mat].r0, J.mat[mat].mt, ti, tj);
+        };
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int u = u0 + a * stride;
+            s[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (u >= total) continue;
+            int mat, ti, tj, r, c;
+            place(u, mat, ti, tj, r, c);
+            const Mat& M = J.mat[mat];
+            const int gi = ti / kTile, gj = tj / kTile, sub = (ti % kTile) * kTile + tj % kTile;
+            const int64_t apart = (int64_t)kTile * kTile * kTileF;
+            float* part = M.part + (int64_t)(gi * M.gt - gi * (gi - 1) / 2 + gj - gi) * M.splits * apart + sub * kTileF;
+#pragma unroll 4
+            for (int w = 0; w < M.splits; ++w) {
+                const float4 x = *tile_at(part + w * apart, r, c);
+                s[a].x += x.x, s[a].y += x.y, s[a].z += x.z, s[a].w += x.w;
+            }
         }
-        const float inv2 = 1.f / (M.tau * M.tau), alpha = alpha_of(J.a, J.cap, M.k, step);
-        const int i = 128 * ti + r, j = 128 * tj + c;
-        float o[4] = {s.x * inv2, s.y * inv2, s.z * inv2, s.w * inv2};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (i == j + e && i < M.k) o[e] -= alpha;
-        *tile_at(gram_tile(M, ti, tj), r, c) = make_float4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint2*>(M.ad + blocked(i, j, M.rb)) = make_uint2(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]));
-        if (ti != tj) {
+        for (int a = 0; a < kAhead; ++a) {
+            const int u = u0 + a * stride;
+            if (u >= total) continue;
+            int mat, ti, tj, r, c;
+            place(u, mat, ti, tj, r, c);
+            const Mat& M = J.mat[mat];
+            const float inv2 = 1.f / (M.tau * M.tau), alpha = alpha_of(J.a, J.cap, M.k, step);
+            const int i = 128 * ti + r, j = 128 * tj + c;
+            float o[4] = {s[a].x * inv2, s[a].y * inv2, s[a].z * inv2, s[a].w * inv2};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) M.ad[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
+            for (int e = 0; e < 4; ++e)
+                if (i == j + e && i < M.k) o[e] -= alpha;
+            *tile_at(gram_tile(M, ti, tj), r, c) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint2*>(M.ad + blocked(i, j, M.rb)) = make_uint2(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]));
+            if (ti != tj) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) M.ad[blocked(j + e, i, M.rb)] = __float2half_rn(o[e]);
+            }
         }
     }
 }
@@ -1179,8 +1223,10 @@ float cap_of(const Poly& p) {
 // The workspace is laid out for this many CTAs: the sizes do not depend on the device.
 constexpr int kPlanSms = 152;
 // Pairs of CTAs take a launch whose update products have this many tiles of 256 x 256, counted by their blocks of 64 contracted
-// values, or more.
-constexpr int64_t kPairWork = 1000;
+// values, or more: a pair loads less a product and waits longer at each step of its ring.  Five steps, single CTAs against pairs:
+// 2048 x 2048 (2048 blocks) 229 : 309 us, 1024 x 8192 (2048) 290 : 280, the seven convolutions' filters (2400) 482 : 512,
+// 2048 x 3000 (3072) 456 : 406, 1500 x 8192 (4608) 481 : 426, 2048 x 8192 (8192) 770 : 629.
+constexpr int64_t kPairWork = 2700;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -1192,6 +1238,7 @@ bool plan_sizes(Mat* mats, int count) {
         M.tall = M.rows > M.cols;
         M.k = (int)std::min(M.rows, M.cols), M.n = (int)std::max(M.rows, M.cols);
         M.vec = !M.tall && M.n % 8 == 0;
+        M.aligned = reinterpret_cast<uintptr_t>(M.g) % 16 == 0;
         M.nx = (M.n + 63) / 64;
         work += (int64_t)((M.k + 255) / 256) * ((M.nx + 3) / 4) * ((M.k + 63) / 64);
     }
@@ -1215,7 +1262,7 @@ bool plan_sizes(Mat* mats, int count) {
         M.per = (int)std::min<int64_t>(share, M.nx);
         M.splits = (M.nx + M.per - 1) / M.per;
         const int64_t total = M.rows * M.cols;
-        M.chunk = std::max<int64_t>(4096, (total + kNormChunks - 1) / kNormChunks);
+        M.chunk = std::max<int64_t>(4096, ((total + kNormChunks - 1) / kNormChunks + 3) / 4 * 4);
         M.chunks = (int)((total + M.chunk - 1) / M.chunk);
         // entries of X are 1 / sqrt(k n) at first and at most about 1.2 / sqrt(n) in the mean later: a quarter of the former's inverse
         M.tau = std::exp2(std::floor(std::log2(std::max(4.0, std::sqrt((double)M.k * M.n)) / 4.0)));
