@@ -50,6 +50,8 @@ constexpr int kMostStages = 6;
 constexpr uint32_t kSmem = kRing + 1024;
 constexpr int kTileF = 128 * 128;         // floats of a Gram tile
 
+constexpr int kPlanSms = 152;             // SMs that work is planned for
+
 struct Mat {
     const void* g;
     float* m;
@@ -64,18 +66,28 @@ struct Mat {
     int aligned;             // g starts at 16 bytes
     int rb, cb, nx;          // operand blocks: X is rb x cb, of which nx have columns, A' and B' rb x rb
     int mt, gt, ut;          // 128-row tiles, a tile's rows of those (1, in pairs 2) to a tile; 256-column tiles of X
-    int splits, per;         // parts of the long axis in phase G, blocks of each
     int chunks;              // norm partials
     int64_t chunk;           // values of each
-    int n0, c0, g0, r0, s0, u0;  // first item of each phase
+    int n0, c0, s0, u0;      // first item of each phase
+    int b0;                  // first block of phase G
     __half *xh[2], *ad, *bp;
-    float *x, *d, *part, *norm;
+    float *x, *d, *norm;
+};
+
+// A tile of the Gram matrix whose long axis is cut: the unit that makes its first part, and how many units make one.
+struct Cut {
+    int16_t mat, i, j;
+    uint8_t unit, parts;
 };
 
 struct Job {
     Mat mat[kMaxMats];
+    Cut cut[kPlanSms];
     int count, steps;
-    int nn, nc, ng, nr, ns, nu;  // items of each phase
+    int nn, nc, ns, nu;  // items of each phase; G has S's
+    int share, blocks;   // phase G cut into shares of so many blocks of all its tiles' (0: whole tiles)
+    int cuts;
+    float* part;
     float a, b, c, eps, mu, cap;
     int nesterov;
     uint32_t* sync;  // arrivals at the grid barrier, abort flag
@@ -232,9 +244,10 @@ __device__ __forceinline__ int unit_count() { return PAIR ? gridDim.x >> 1 : gri
 
 // An item of a product phase: which operand blocks, and how many.
 struct Item {
-    int mat, i, j, split;  // tile, tile of the other side, part of the long axis
-    int kb0, kb1;          // blocks of the contracted axis
-    int nb;                // 64-column blocks of the tile
+    int mat, i, j;  // tile, tile of the other side
+    int kb0, kb1;   // blocks of the contracted axis
+    int nb;         // 64-column blocks of the tile
+    int slot;       // where a part of a tile goes, -1 for a whole one
 };
 
 // Tile e of those on and above the diagonal of t x t tiles, row by row.
@@ -247,35 +260,49 @@ __device__ __forceinline__ void upper_tile(int e, int t, int& i, int& j) {
     j = i + e;
 }
 
-template <int PH>
-__device__ __forceinline__ int first_of(const Mat& M) { return PH == PH_G ? M.g0 : PH == PH_S ? M.s0 : M.u0; }
-
+// A unit's way through a phase: items in turn, or in phase G, where it is cut, the tiles of an even share of all blocks.  A share
+// has at most two parts of tiles, one that its tile's other parts come before (the slot 2 unit) and one that they come after.
 template <int PH, bool PAIR>
-__device__ __forceinline__ Item item_of(const Job& J, int it, int mat) {
-    while (mat + 1 < J.count && it >= first_of<PH>(J.mat[mat + 1])) ++mat;
-    const Mat& M = J.mat[mat];
-    Item t;
-    t.mat = mat;
-    int e = it - first_of<PH>(M);
-    t.split = 0;
-    t.kb0 = 0;
-    t.kb1 = (M.k + 63) / 64;
-    if (PH == PH_U) {
-        t.i = e % M.gt;
-        t.j = e / M.gt;
-        t.nb = PAIR ? 4 : min(4, M.cb - 4 * t.j);
-        return t;
+struct Walk {
+    int it, at = 0, end = 0, mat = 0;
+    __device__ __forceinline__ Walk() : it(unit_id<PAIR>()) {}
+    __device__ __forceinline__ bool next(const Job& J, Item& t) {
+        t.kb0 = 0, t.slot = -1;
+        int e;
+        if (PH == PH_G && J.share) {
+            if (at == end) {
+                at = it * J.share, end = min(at + J.share, J.blocks);
+                if (at >= J.blocks) return false;
+                it += unit_count<PAIR>();
+            }
+            while (mat + 1 < J.count && at >= J.mat[mat + 1].b0) ++mat;
+            const Mat& M = J.mat[mat];
+            e = (at - M.b0) / M.nx;
+            t.kb0 = (at - M.b0) - e * M.nx;
+            t.kb1 = min(M.nx, t.kb0 + end - at);
+            at += t.kb1 - t.kb0;
+            if (t.kb1 - t.kb0 < M.nx) t.slot = 2 * (it - unit_count<PAIR>()) + (t.kb0 == 0);
+        } else {
+            if (it >= (PH == PH_U ? J.nu : J.ns)) return false;
+            while (mat + 1 < J.count && it >= (PH == PH_U ? J.mat[mat + 1].u0 : J.mat[mat + 1].s0)) ++mat;
+            const Mat& M = J.mat[mat];
+            e = it - (PH == PH_U ? M.u0 : M.s0);
+            t.kb1 = PH == PH_G ? M.nx : (M.k + 63) / 64;
+            it += unit_count<PAIR>();
+        }
+        const Mat& M = J.mat[mat];
+        t.mat = mat;
+        if (PH == PH_U) {
+            t.i = e % M.gt;
+            t.j = e / M.gt;
+            t.nb = PAIR ? 4 : min(4, M.cb - 4 * t.j);
+        } else {
+            upper_tile(e, M.gt, t.i, t.j);
+            t.nb = PAIR ? 4 : 2;
+        }
+        return true;
     }
-    if (PH == PH_G) {
-        t.split = e % M.splits;
-        e /= M.splits;
-        t.kb0 = t.split * M.per;
-        t.kb1 = min(t.kb0 + M.per, M.nx);
-    }
-    upper_tile(e, M.gt, t.i, t.j);
-    t.nb = PAIR ? 4 : 2;
-    return t;
-}
+};
 
 // A role's way through the ring: each stage's parity, kept over phases that cut the ring differently.
 struct Pipe {
@@ -332,14 +359,12 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 template <int PH, bool PAIR>
 __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8_t* ring, Pipe& P) {
     const int lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
-    const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
     constexpr int sb = stage_blocks<PH, PAIR>(), stages = 24 / sb;
     P.stage = 0;
-    int mat = 0;
-    for (int it = unit_id<PAIR>(); it < total; it += unit_count<PAIR>()) {
-        const Item t = item_of<PH, PAIR>(J, it, mat);
-        mat = t.mat;
-        const Mat& M = J.mat[mat];
+    Walk<PH, PAIR> way;
+    Item t;
+    while (way.next(J, t)) {
+        const Mat& M = J.mat[t.mat];
         const __half* a = PH == PH_G ? M.xh[cur] : PH == PH_S ? M.ad : M.bp;
         const int acb = PH == PH_G ? M.cb : M.rb;
         const bool same = PH != PH_U && t.i == t.j;
@@ -370,14 +395,12 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
 // One thread.  In a pair the first CTA's issues for both; the second's tells it of each of its own stages that is full.
 template <int PH, bool PAIR>
 __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, Pipe& P) {
-    const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
     constexpr int sb = stage_blocks<PH, PAIR>(), stages = 24 / sb;
     const bool second = PAIR && cluster_rank() == 1;
     P.stage = 0;
-    int mat = 0;
-    for (int it = unit_id<PAIR>(); it < total; it += unit_count<PAIR>(), ++P.local) {
-        const Item t = item_of<PH, PAIR>(J, it, mat);
-        mat = t.mat;
+    Walk<PH, PAIR> way;
+    Item t;
+    for (; way.next(J, t); ++P.local) {
         if (second) {
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
                 if (!mbar_wait(&sh.full[P.stage], P.parity(), &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
@@ -536,14 +559,12 @@ __device__ __forceinline__ float* gram_tile(const Mat& M, int ti, int tj) {
 template <int PH, bool PAIR>
 __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared& sh, Pipe& P) {
     constexpr int kTurn = kEpiWarps / 4, kTile = PAIR ? 2 : 1;  // 128-row tiles of a tile
-    const int total = PH == PH_G ? J.ng : PH == PH_S ? J.ns : J.nu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, turn = (warp - 2) >> 2;
     const int r = 32 * q + lane, rank = PAIR ? (int)cluster_rank() : 0;
-    int mat = 0;
-    for (int it = unit_id<PAIR>(); it < total; it += unit_count<PAIR>(), ++P.local) {
-        const Item t = item_of<PH, PAIR>(J, it, mat);
-        mat = t.mat;
-        const Mat& M = J.mat[mat];
+    Walk<PH, PAIR> way;
+    Item t;
+    for (; way.next(J, t); ++P.local) {
+        const Mat& M = J.mat[t.mat];
         const StepScalars sc = scalars_of(J, M, step);
         const uint32_t acc = P.local & 1, use = P.local >> 1;
         const int ti = kTile * t.i + rank, i = 128 * ti + r;
@@ -562,9 +583,9 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
             const int c = 16 * ch;
             if (PH == PH_G) {
                 tmem_ld_wait();
-                if (M.splits > 1) {
+                if (t.slot >= 0) {
                     // 128 columns at a time, as phase R takes them
-                    float* part = M.part + ((int64_t)(it - M.g0) * kTile + rank) * kTile * kTileF;
+                    float* part = J.part + ((int64_t)t.slot * kTile + rank) * kTile * kTileF;
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
                         *tile_at(part, r, c + e) = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
@@ -704,52 +725,44 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__
             }
 }
 
-// A' of 128 x 128 tiles whose long axis was split: the sum of the parts, less alpha on the diagonal.  A thread takes four
-// columns of a row at a time, kAhead of them at once.
-template <bool PAIR>
-__device__ __forceinline__ void reduce_phase(const Job& J, int step) {
-    constexpr int kUnits = kTileF / 4, kTile = PAIR ? 2 : 1, kAhead = 4;
-    const int stride = gridDim.x * kThreads, total = J.nr * kUnits;
-    for (int u0 = blockIdx.x * kThreads + threadIdx.x; u0 < total; u0 += kAhead * stride) {
-        float4 s[kAhead];
-        auto place = [&](int u, int& mat, int& ti, int& tj, int& r, int& c) {
-            const int it = u / kUnits, in = u % kUnits;
-            r = in & 127, c = 4 * (in >> 7);
-            mat = 0;
-            while (mat + 1 < J.count && it >= J.mat[mat + 1].r0) ++mat;
-            upper_tile(it - J.mat[mat].r0, J.mat[mat].mt, ti, tj);
-        };
+// A' of the tiles whose long axis was cut: the sum of the parts, in their order, less alpha on the diagonal.  A warp takes four
+// columns of 32 ROWS rows of a 128 x 128 tile at a time.
+template <bool PAIR, int ROWS>
+__device__ __forceinline__ void join_phase(const Job& J, int step) {
+    constexpr int kTile = PAIR ? 2 : 1, kGroups = kTileF / 4 / (32 * ROWS), kWarps = kThreads / 32;
+    constexpr int64_t kApart = (int64_t)kTile * kTile * kTileF;
+    const int lane = threadIdx.x & 31, total = J.cuts * kTile * kTile * kGroups;
+    for (int it = blockIdx.x * kWarps + (threadIdx.x >> 5); it < total; it += gridDim.x * kWarps) {
+        const int in = it % kGroups, sub = it / kGroups % (kTile * kTile);
+        const Cut& t = J.cut[it / (kTile * kTile * kGroups)];
+        const Mat& M = J.mat[t.mat];
+        const int ti = kTile * t.i + sub / kTile, tj = kTile * t.j + sub % kTile;
+        if (ti > tj) continue;
+        const int r = in * 32 * ROWS % 128 + lane, c = in * 32 * ROWS / 128 * 4;
+        float* part = J.part + (int64_t)(2 * t.unit + 1) * kApart + sub * kTileF;
+        float4 s[ROWS];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            const int u = u0 + a * stride;
-            s[a] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (u >= total) continue;
-            int mat, ti, tj, r, c;
-            place(u, mat, ti, tj, r, c);
-            const Mat& M = J.mat[mat];
-            const int gi = ti / kTile, gj = tj / kTile, sub = (ti % kTile) * kTile + tj % kTile;
-            const int64_t apart = (int64_t)kTile * kTile * kTileF;
-            float* part = M.part + (int64_t)(gi * M.gt - gi * (gi - 1) / 2 + gj - gi) * M.splits * apart + sub * kTileF;
-#pragma unroll 4
-            for (int w = 0; w < M.splits; ++w) {
-                const float4 x = *tile_at(part + w * apart, r, c);
+        for (int a = 0; a < ROWS; ++a) s[a] = *tile_at(part, r + 32 * a, c);
+        part -= kApart;
+#pragma unroll(8 / ROWS)
+        for (int w = 1; w < t.parts; ++w) {
+            part += 2 * kApart;
+#pragma unroll
+            for (int a = 0; a < ROWS; ++a) {
+                const float4 x = *tile_at(part, r + 32 * a, c);
                 s[a].x += x.x, s[a].y += x.y, s[a].z += x.z, s[a].w += x.w;
             }
         }
+        const float inv2 = 1.f / (M.tau * M.tau), alpha = alpha_of(J.a, J.cap, M.k, step);
+        float* d = gram_tile(M, ti, tj);
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            const int u = u0 + a * stride;
-            if (u >= total) continue;
-            int mat, ti, tj, r, c;
-            place(u, mat, ti, tj, r, c);
-            const Mat& M = J.mat[mat];
-            const float inv2 = 1.f / (M.tau * M.tau), alpha = alpha_of(J.a, J.cap, M.k, step);
-            const int i = 128 * ti + r, j = 128 * tj + c;
+        for (int a = 0; a < ROWS; ++a) {
+            const int i = 128 * ti + r + 32 * a, j = 128 * tj + c;
             float o[4] = {s[a].x * inv2, s[a].y * inv2, s[a].z * inv2, s[a].w * inv2};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (i == j + e && i < M.k) o[e] -= alpha;
-            *tile_at(gram_tile(M, ti, tj), r, c) = make_float4(o[0], o[1], o[2], o[3]);
+            *tile_at(d, r + 32 * a, c) = make_float4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint2*>(M.ad + blocked(i, j, M.rb)) = make_uint2(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]));
             if (ti != tj) {
 #pragma unroll
@@ -802,8 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         const int cur = step & 1;
         product_phase<PH_G, PAIR>(J, cur, step, sh, ring, P);
         if (!(ok = grid_sync(J, target, sh))) break;
-        if (J.nr > 0) {
-            reduce_phase<PAIR>(J, step);
+        if (J.cuts > 0) {
+            // four rows to a lane where that leaves items for all warps
+            if (J.cuts * (PAIR ? 128 : 32) >= (int)gridDim.x * kThreads / 32)
+                join_phase<PAIR, 4>(J, step);
+            else
+                join_phase<PAIR, 1>(J, step);
             if (!(ok = grid_sync(J, target, sh))) break;
         }
         product_phase<PH_S, PAIR>(J, cur, step, sh, ring, P);
@@ -1221,7 +1238,6 @@ float cap_of(const Poly& p) {
 }
 
 // The workspace is laid out for this many CTAs: the sizes do not depend on the device.
-constexpr int kPlanSms = 152;
 // Pairs of CTAs take a launch whose update products have this many tiles of 256 x 256, counted by their blocks of 64 contracted
 // values, or more: a pair loads less a product and waits longer at each step of its ring.  Five steps, single CTAs against pairs:
 // 2048 x 2048 (2048 blocks) 229 : 309 us, 1024 x 8192 (2048) 290 : 280, the seven convolutions' filters (2400) 482 : 512,
@@ -1232,7 +1248,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Sizes, and the split of the long axis, of matrices that run in one launch; returns whether on pairs of CTAs.
 bool plan_sizes(Mat* mats, int count) {
-    int64_t blocks = 0, work = 0;
+    int64_t work = 0;
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
         M.tall = M.rows > M.cols;
@@ -1244,23 +1260,10 @@ bool plan_sizes(Mat* mats, int count) {
     }
     const bool pair = work >= kPairWork;
     const int tile = pair ? 2 : 1;
-    int longest = 0;
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
         M.cb = pair ? (M.nx + 3) / 4 * 4 : M.nx, M.ut = (M.nx + 3) / 4;
         M.gt = (M.k + 128 * tile - 1) / (128 * tile), M.mt = tile * M.gt, M.rb = 2 * M.mt;
-        blocks += (int64_t)M.gt * (M.gt + 1) / 2 * M.nx;
-        longest = std::max(longest, M.nx);
-    }
-    // a unit's share of phase G's blocks, at least four to a part; but no part at all where the longest axis takes little longer
-    // than a share: phase R, its barrier and the parts' way through memory cost as much as about six blocks
-    const int units = kPlanSms / tile;
-    int64_t share = std::max<int64_t>(4, (blocks + units - 1) / units);
-    if (longest <= share + 6) share = longest;
-    for (int i = 0; i < count; ++i) {
-        Mat& M = mats[i];
-        M.per = (int)std::min<int64_t>(share, M.nx);
-        M.splits = (M.nx + M.per - 1) / M.per;
         const int64_t total = M.rows * M.cols;
         M.chunk = std::max<int64_t>(4096, ((total + kNormChunks - 1) / kNormChunks + 3) / 4 * 4);
         M.chunks = (int)((total + M.chunk - 1) / M.chunk);
@@ -1270,8 +1273,47 @@ bool plan_sizes(Mat* mats, int count) {
     return pair;
 }
 
-// Places the matrices' buffers at `base` (which may be NULL, to count) and returns their size.
-size_t place(Mat* mats, int count, bool pair, char* base) {
+// A unit's share of phase G's blocks where that is cut, 0 where its units take whole tiles in turn: where the busiest of these
+// has at most ten blocks more than an even share, as phase R, its barrier and the parts' way through memory cost that much.
+int gram_share(const Mat* mats, int count, bool pair) {
+    const int units = kPlanSms / (pair ? 2 : 1);
+    std::vector<int64_t> load((size_t)units, 0);
+    int64_t blocks = 0;
+    size_t u = 0;
+    for (int i = 0; i < count; ++i) {
+        const int64_t tiles = (int64_t)mats[i].gt * (mats[i].gt + 1) / 2;
+        blocks += tiles * mats[i].nx;
+        for (int64_t t = 0; t < tiles; ++t) {
+            load[u] += mats[i].nx;
+            if (++u == load.size()) u = 0;
+        }
+    }
+    const int64_t share = std::max<int64_t>(4, (blocks + units - 1) / units);
+    return *std::max_element(load.begin(), load.end()) <= share + 10 ? 0 : (int)share;
+}
+
+// The tiles that the ends of shares lie in.
+void list_cuts(Job& J) {
+    int last = -1, mat = 0;
+    for (int b = J.share; b < J.blocks; b += J.share) {
+        while (mat + 1 < J.count && b >= J.mat[mat + 1].b0) ++mat;
+        const Mat& M = J.mat[mat];
+        int e = (b - M.b0) / M.nx;
+        const int first = M.b0 + e * M.nx;
+        if (b == first || first == last) continue;  // between tiles, or a tile that is listed
+        last = first;
+        Cut& t = J.cut[J.cuts++];
+        t.mat = (int16_t)mat;
+        t.unit = (uint8_t)(first / J.share);
+        t.parts = (uint8_t)((first + M.nx - 1) / J.share - t.unit + 1);
+        int i = 0;
+        for (; e >= M.gt - i; ++i) e -= M.gt - i;
+        t.i = (int16_t)i, t.j = (int16_t)(i + e);
+    }
+}
+
+// Places the matrices' buffers and the parts at `base` (which may be NULL, to count) and returns their size.
+size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
     size_t at = 256;
     auto take = [&](size_t bytes) {
         char* p = base + at;
@@ -1286,9 +1328,9 @@ size_t place(Mat* mats, int count, bool pair, char* base) {
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
-        M.part = reinterpret_cast<float*>(take(M.splits > 1 ? (size_t)M.gt * (M.gt + 1) / 2 * M.splits * (pair ? 4 : 1) * kTileF * sizeof(float) : 0));
         M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
     }
+    *part = reinterpret_cast<float*>(take(gram_share(mats, count, pair) ? 2 * kPlanSms * (pair ? 2 : 1) * kTileF * sizeof(float) : 0));
     return at;
 }
 
@@ -1320,7 +1362,8 @@ size_t workspace_of(std::vector<Mat>& mats) {
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         const int count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
         const bool pair = plan_sizes(&mats[b], count);
-        most = std::max(most, place(&mats[b], count, pair, nullptr));
+        float* part;
+        most = std::max(most, place(&mats[b], count, pair, nullptr, &part));
     }
     return most;
 }
@@ -1370,18 +1413,19 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         Job J{};
         J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
         const bool pair = plan_sizes(&mats[b], J.count);
-        place(&mats[b], J.count, pair, static_cast<char*>(ws));
+        place(&mats[b], J.count, pair, static_cast<char*>(ws), &J.part);
+        J.share = gram_share(&mats[b], J.count, pair);
         for (int i = 0; i < J.count; ++i) {
             Mat& M = J.mat[i] = mats[b + i];
-            M.n0 = J.nn, M.c0 = J.nc, M.g0 = J.ng, M.r0 = J.nr, M.s0 = J.ns, M.u0 = J.nu;
+            M.n0 = J.nn, M.c0 = J.nc, M.s0 = J.ns, M.u0 = J.nu, M.b0 = J.blocks;
             const int tiles = M.gt * (M.gt + 1) / 2;
             J.nn += M.chunks;
             J.nc += M.rb * M.cb;
-            J.ng += tiles * M.splits;
-            J.nr += M.splits > 1 ? M.mt * (M.mt + 1) / 2 : 0;
+            J.blocks += tiles * M.nx;
             J.ns += tiles;
             J.nu += M.gt * M.ut;
         }
+        if (J.share) list_cuts(J);
         J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.cap = cap_of(p), J.mu = mu, J.nesterov = nesterov;
         J.sync = static_cast<uint32_t*>(ws);
         J.status = ctx.status;
