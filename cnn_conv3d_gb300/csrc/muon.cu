@@ -71,7 +71,8 @@ struct Mat {
     int n0, c0, s0, u0;      // first item of each phase
     int b0;                  // first block of phase G
     __half *xh[2], *ad, *bp;
-    float *x, *d, *norm;
+    uint8_t* x;              // the bytes that X has more than its operand
+    float *d, *norm;
 };
 
 // A tile of the Gram matrix whose long axis is cut: the unit that makes its first part, and how many units make one.
@@ -452,8 +453,34 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 __device__ __forceinline__ float4* tile_at(float* tile, int r, int c) {
     return reinterpret_cast<float4*>(tile) + (c >> 2) * 128 + r;
 }
-// The 128-row tile of X in fp32 that row i is in.
-__device__ __forceinline__ float* x_tile(const Mat& M, int i) { return M.x + (int64_t)(i >> 7) * M.cb * 64 * 128; }
+
+// X beside its operand: a byte a value, (x - h) / (2^-18 e) + 128 with h the operand's value and e the power of two in it, so
+// that the two hold x to 2^-20 of it; a quarter of fp32's bytes, and with the operand, that is read and written anyway, three
+// fifths of the traffic of phase U that X in fp32 took.  16 bytes of a row are together, then those of the tile's next row.
+__device__ __forceinline__ uint4* rest_at(const Mat& M, int i, int j) {
+    return reinterpret_cast<uint4*>(M.x + (int64_t)(i >> 7) * M.cb * 64 * 128) + (j >> 4) * 128 + (i & 127);
+}
+__device__ __forceinline__ float power_of(float h) {
+    return fmaxf(__uint_as_float(__float_as_uint(h) & 0x7F800000u), 0x1p-14f);  // fp16's smallest normal value
+}
+__device__ __forceinline__ uint32_t rest_of(float x, float h) {
+    const float inv = __uint_as_float(0x7F000000u - __float_as_uint(power_of(h)));
+    return __float_as_uint(fminf(fmaf((x - h) * inv, 0x1p18f, 0x1p23f + 128.f), 0x1p23f + 255.f));  // in the lowest byte
+}
+__device__ __forceinline__ uint32_t pack_rest4(const float* x, const float* h) {
+    const uint32_t lo = __byte_perm(rest_of(x[0], h[0]), rest_of(x[1], h[1]), 0x0040);
+    const uint32_t hi = __byte_perm(rest_of(x[2], h[2]), rest_of(x[3], h[3]), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
+// Value e of four: 32 + byte 2^-18 as a float, from which 32 and the bias are taken.
+__device__ __forceinline__ float with_rest(float h, uint32_t bytes, int e) {
+    const float d = __uint_as_float(__byte_perm(bytes, 0x42000000u, 0x7650 | e)) - (32.f + 128.f * 0x1p-18f);
+    return fmaf(d, power_of(h), h);
+}
+__device__ __forceinline__ void unpack2_f16(uint32_t v, float& a, float& b) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    a = f.x, b = f.y;
+}
 
 struct StepScalars {
     float alpha, beta, theta;  // theta: the part of beta that takes X in fp32
@@ -469,10 +496,9 @@ __device__ __forceinline__ StepScalars scalars_of(const Job& J, const Mat& M, in
 __device__ __forceinline__ uint4 pack8_f16(const float* y) {
     return make_uint4(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
 }
-// 16 values of row i, columns j .. j+15, into a blocked operand: a 32-byte store of two chunks, which the XOR keeps side by
-// side.
-__device__ __forceinline__ void store_row16(__half* op, int i, int j, int cb, const float* y) {
-    uint4 p = pack8_f16(y), q = pack8_f16(y + 8);
+// 16 values of row i, columns j .. j+15, into or from a blocked operand: a 32-byte access to two chunks, which the XOR keeps side
+// by side.
+__device__ __forceinline__ void store_row16(__half* op, int i, int j, int cb, uint4 p, uint4 q) {
     if (i & 1) {
         const uint4 t = p;
         p = q;
@@ -482,6 +508,14 @@ __device__ __forceinline__ void store_row16(__half* op, int i, int j, int cb, co
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(p.x), "r"(p.y), "r"(p.z), "r"(p.w),
                  "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
                  : "memory");
+}
+__device__ __forceinline__ void store_row16(__half* op, int i, int j, int cb, const float* y) {
+    store_row16(op, i, j, cb, pack8_f16(y), pack8_f16(y + 8));
+}
+__device__ __forceinline__ void load_row16(const __half* op, int i, int j, int cb, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(op + (blocked(i, j, cb) & ~(int64_t)15)));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return pack_bf16x2(a, b); }
 
@@ -569,11 +603,11 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
         const uint32_t acc = P.local & 1, use = P.local >> 1;
         const int ti = kTile * t.i + rank, i = 128 * ti + r;
         const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
-        float4 x[4];
-        float* xt = PH == PH_U ? x_tile(M, i) : nullptr;
-        if (PH == PH_U) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, 256 * t.j + 16 * turn + 4 * e);
+        uint32_t xh[8];  // the chunk's operand values of X, chunks of eight in stored order, and the rest
+        uint4 xr;
+        if (PH == PH_U && turn < 4 * t.nb) {
+            load_row16(M.xh[cur], i, 256 * t.j + 16 * turn, M.cb, xh);
+            xr = *rest_at(M, i, 256 * t.j + 16 * turn);
         }
         if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
         tc_fence_after();
@@ -630,22 +664,31 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
             } else {
                 const int j = 256 * t.j + c;
                 const float wx = J.a + sc.theta, wh = sc.beta - sc.theta;
-                float y[16];
+                float h[16], y[16];
+                const uint32_t rest[4] = {xr.x, xr.y, xr.z, xr.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[4 * e] = x[e].x, y[4 * e + 1] = x[e].y, y[4 * e + 2] = x[e].z, y[4 * e + 3] = x[e].w;
-                if (ch + kTurn < 4 * t.nb) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = *tile_at(xt, r, j + 16 * kTurn + 4 * e);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t p = i & 1 ? xh[e + 4] : xh[e], q = i & 1 ? xh[e] : xh[e + 4];
+                    unpack2_f16(p, h[2 * e], h[2 * e + 1]);
+                    unpack2_f16(q, h[2 * e + 8], h[2 * e + 9]);
                 }
+                if (ch + kTurn < 4 * t.nb) {
+                    load_row16(M.xh[cur], i, j + 16 * kTurn, M.cb, xh);
+                    xr = *rest_at(M, i, j + 16 * kTurn);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = fmaf(wx, with_rest(h[e], rest[e >> 2], e & 3), wh * h[e]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    y[e] = fmaf(wx, y[e], fmaf(wh, __half2float(__float2half_rn(y[e])), __uint_as_float(v[e])));
+                for (int e = 0; e < 16; ++e) y[e] += __uint_as_float(v[e]);
                 if (step + 1 < J.steps) {
+                    const uint4 p = pack8_f16(y), q = pack8_f16(y + 8);
+                    store_row16(M.xh[cur ^ 1], i, j, M.cb, p, q);
+                    const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *tile_at(xt, r, j + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                    store_row16(M.xh[cur ^ 1], i, j, M.cb, y);
+                    for (int e = 0; e < 8; ++e) unpack2_f16(w[e], h[2 * e], h[2 * e + 1]);
+                    *rest_at(M, i, j) = make_uint4(pack_rest4(y, h), pack_rest4(y + 4, h + 4), pack_rest4(y + 8, h + 8),
+                                                   pack_rest4(y + 12, h + 12));
                 } else if (i < M.k) {
                     write_result<16>(M, 0, i, j, y);
                 }
@@ -718,10 +761,12 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__
                 }
     #pragma unroll
                 for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
-                *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = pack8_f16(y);
-                float* xt = x_tile(M, i);
-                *tile_at(xt, i & 127, j) = make_float4(y[0], y[1], y[2], y[3]);
-                *tile_at(xt, i & 127, j + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                const uint4 p = pack8_f16(y);
+                *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = p;
+                float h[8];
+                unpack2_f16(p.x, h[0], h[1]), unpack2_f16(p.y, h[2], h[3]);
+                unpack2_f16(p.z, h[4], h[5]), unpack2_f16(p.w, h[6], h[7]);
+                reinterpret_cast<uint2*>(rest_at(M, i, j))[(j >> 3) & 1] = make_uint2(pack_rest4(y, h), pack_rest4(y + 4, h + 4));
             }
 }
 
@@ -1324,7 +1369,7 @@ size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
         Mat& M = mats[i];
         const size_t xb = (size_t)M.rb * M.cb * kBlkBytes, ab = (size_t)M.rb * M.rb * kBlkBytes;
         for (int p = 0; p < 2; ++p) M.xh[p] = reinterpret_cast<__half*>(take(xb));
-        M.x = reinterpret_cast<float*>(take(2 * xb));
+        M.x = reinterpret_cast<uint8_t*>(take(xb / 2));
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
