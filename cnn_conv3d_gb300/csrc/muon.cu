@@ -65,7 +65,7 @@ struct Mat {
     int vec;                 // rows of the result start at 16 bytes
     int aligned;             // g starts at 16 bytes
     int rb, cb, nx;          // operand blocks: X is rb x cb, of which nx have columns, A' and B' rb x rb
-    int mt, gt, ut;          // 128-row tiles, a tile's rows of those (1, in pairs 2) to a tile; 256-column tiles of X
+    int mt, gt, ut;          // 128-row tiles, rows of tiles (1, in pairs 2, of those each), columns of tiles of phase U
     int chunks;              // norm partials
     int64_t chunk;           // values of each
     int n0, c0, s0, u0;      // first item of each phase
@@ -88,6 +88,7 @@ struct Job {
     int nn, nc, ns, nu;  // items of each phase; G has S's
     int share, blocks;   // phase G cut into shares of so many blocks of all its tiles' (0: whole tiles)
     int cuts;
+    int half, uw;        // S in tiles of 64 columns; 64-column blocks of a tile of U
     float* part;
     float a, b, c, eps, mu, cap;
     int nesterov;
@@ -247,6 +248,7 @@ __device__ __forceinline__ int unit_count() { return PAIR ? gridDim.x >> 1 : gri
 struct Item {
     int mat, i, j;  // tile, tile of the other side
     int kb0, kb1;   // blocks of the contracted axis
+    int cb0;        // first 64-column block of the tile (S: which half)
     int nb;         // 64-column blocks of the tile
     int slot;       // where a part of a tile goes, -1 for a whole one
 };
@@ -268,7 +270,7 @@ struct Walk {
     int it, at = 0, end = 0, mat = 0;
     __device__ __forceinline__ Walk() : it(unit_id<PAIR>()) {}
     __device__ __forceinline__ bool next(const Job& J, Item& t) {
-        t.kb0 = 0, t.slot = -1;
+        t.kb0 = 0, t.slot = -1, t.cb0 = 0;
         int e;
         if (PH == PH_G && J.share) {
             if (at == end) {
@@ -284,10 +286,12 @@ struct Walk {
             at += t.kb1 - t.kb0;
             if (t.kb1 - t.kb0 < M.nx) t.slot = 2 * (it - unit_count<PAIR>()) + (t.kb0 == 0);
         } else {
-            if (it >= (PH == PH_U ? J.nu : J.ns)) return false;
-            while (mat + 1 < J.count && it >= (PH == PH_U ? J.mat[mat + 1].u0 : J.mat[mat + 1].s0)) ++mat;
+            const int half = PH == PH_S && !PAIR ? J.half : 0, at = it >> half;
+            if (at >= (PH == PH_U ? J.nu : J.ns)) return false;
+            while (mat + 1 < J.count && at >= (PH == PH_U ? J.mat[mat + 1].u0 : J.mat[mat + 1].s0)) ++mat;
             const Mat& M = J.mat[mat];
-            e = it - (PH == PH_U ? M.u0 : M.s0);
+            e = at - (PH == PH_U ? M.u0 : M.s0);
+            t.cb0 = it & half;
             t.kb1 = PH == PH_G ? M.nx : (M.k + 63) / 64;
             it += unit_count<PAIR>();
         }
@@ -296,10 +300,11 @@ struct Walk {
         if (PH == PH_U) {
             t.i = e % M.gt;
             t.j = e / M.gt;
-            t.nb = PAIR ? 4 : min(4, M.cb - 4 * t.j);
+            t.cb0 = J.uw * t.j;
+            t.nb = PAIR ? 4 : min(J.uw, M.cb - t.cb0);
         } else {
             upper_tile(e, M.gt, t.i, t.j);
-            t.nb = PAIR ? 4 : 2;
+            t.nb = PAIR ? 4 : PH == PH_S ? 2 - J.half : 2;
         }
         return true;
     }
@@ -318,7 +323,7 @@ struct Pipe {
 };
 // Blocks of a stage in a phase: two of the CTA's rows, and the other side's.
 template <int PH, bool PAIR>
-__host__ __device__ constexpr int stage_blocks() { return PH == PH_U && !PAIR ? 6 : 4; }
+__device__ __forceinline__ int stage_blocks(const Job& J) { return PH == PH_U && !PAIR && J.uw > 2 ? 6 : 4; }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -360,7 +365,7 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 template <int PH, bool PAIR>
 __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8_t* ring, Pipe& P) {
     const int lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
-    constexpr int sb = stage_blocks<PH, PAIR>(), stages = 24 / sb;
+    const int sb = stage_blocks<PH, PAIR>(J), stages = 24 / sb;
     P.stage = 0;
     Walk<PH, PAIR> way;
     Item t;
@@ -369,15 +374,15 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
         const __half* a = PH == PH_G ? M.xh[cur] : PH == PH_S ? M.ad : M.bp;
         const int acb = PH == PH_G ? M.cb : M.rb;
         const bool same = PH != PH_U && t.i == t.j;
-        const int cols = PH == PH_U ? (PAIR ? 2 : t.nb) : 2;  // blocks of the other side that the CTA fetches
+        const int cols = PAIR ? 2 : t.nb;  // blocks of the other side that the CTA fetches
         const uint32_t bytes = (2 + (same ? 0 : cols)) * kBlkBytes;
         // the lane's copy of each stage: a block of the tile's rows (lanes 0, 1), of the other side's rows (2, 3), or (U, lane 2)
         // X's row of blocks
         const bool isb = lane >= 2, row = PH == PH_U && isb;
         const int q = lane & 1;
-        const bool mine = lane < 2 || (!same && lane < (PH == PH_U ? 3 : 4));
-        const int tr = (PAIR ? 4 : 2) * (isb ? t.j : t.i) + 2 * rank + q;
-        const __half* src = row ? M.xh[cur] + ((int64_t)t.kb0 * M.cb + 4 * t.j + 2 * rank) * kBlk : a + ((int64_t)tr * acb + t.kb0) * kBlk;
+        const bool mine = lane < 2 || (!same && lane < (PH == PH_U ? 3 : 2 + cols));
+        const int tr = (PAIR ? 4 : 2) * (isb ? t.j : t.i) + 2 * rank + q + (isb ? t.cb0 : 0);
+        const __half* src = row ? M.xh[cur] + ((int64_t)t.kb0 * M.cb + t.cb0 + 2 * rank) * kBlk : a + ((int64_t)tr * acb + t.kb0) * kBlk;
         const int64_t step = row ? (int64_t)M.cb * kBlk : kBlk;
         const uint32_t size = row ? cols * kBlkBytes : kBlkBytes, dst = (isb ? 2 + (row ? 0 : q) : q) * kBlkBytes;
         for (int kb = t.kb0; kb < t.kb1; ++kb, src += step) {
@@ -396,7 +401,7 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
 // One thread.  In a pair the first CTA's issues for both; the second's tells it of each of its own stages that is full.
 template <int PH, bool PAIR>
 __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, Pipe& P) {
-    constexpr int sb = stage_blocks<PH, PAIR>(), stages = 24 / sb;
+    const int sb = stage_blocks<PH, PAIR>(J), stages = 24 / sb;
     const bool second = PAIR && cluster_rank() == 1;
     P.stage = 0;
     Walk<PH, PAIR> way;
@@ -418,7 +423,7 @@ __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, P
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
             if (!mbar_wait(&sh.full[P.stage], P.parity(), &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
             tc_fence_after();
-            const uint32_t as = smem_u32(ring + P.stage * sb * kBlkBytes), bs = same ? as : as + 2 * kBlkBytes;
+            const uint32_t as = smem_u32(ring + P.stage * sb * kBlkBytes), bs = as + (same ? t.cb0 : 2) * kBlkBytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint64_t ad = sdesc(as + k * 32, 16, 1024, SWZ_128B);
@@ -603,18 +608,27 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
         const uint32_t acc = P.local & 1, use = P.local >> 1;
         const int ti = kTile * t.i + rank, i = 128 * ti + r;
         const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16);
+        float4 dd[4];    // the chunk's values of A'
+        if (PH == PH_S) {
+            const int c = 64 * t.cb0 + 16 * turn, tj = kTile * t.j + (c >> 7);
+            if (turn < 4 * t.nb && ti <= tj) {
+                float* dt = gram_tile(M, ti, tj);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dd[e] = *tile_at(dt, r, (c & 127) + 4 * e);
+            }
+        }
         uint32_t xh[8];  // the chunk's operand values of X, chunks of eight in stored order, and the rest
         uint4 xr;
         if (PH == PH_U && turn < 4 * t.nb) {
-            load_row16(M.xh[cur], i, 256 * t.j + 16 * turn, M.cb, xh);
-            xr = *rest_at(M, i, 256 * t.j + 16 * turn);
+            load_row16(M.xh[cur], i, 64 * t.cb0 + 16 * turn, M.cb, xh);
+            xr = *rest_at(M, i, 64 * t.cb0 + 16 * turn);
         }
         if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, J.wait_ns, J.status, WAIT_EPI_TMEM_FULL)) return;
         tc_fence_after();
         for (int ch = turn; ch < 4 * t.nb; ch += kTurn) {
             uint32_t v[32];  // the first 16
             tmem_ld16(tm + 16 * ch, v);
-            const int c = 16 * ch;
+            const int c = 64 * t.cb0 + 16 * ch;
             if (PH == PH_G) {
                 tmem_ld_wait();
                 if (t.slot >= 0) {
@@ -638,21 +652,24 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
             } else if (PH == PH_S) {
                 const int tj = kTile * t.j + (c >> 7);
                 const float bb = fmaf(2.f * J.c, sc.alpha, J.b);
-                float4 dd[4];
-                if (ti <= tj) {
-                    float* dt = gram_tile(M, ti, tj);
+                float4 d4[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dd[e] = *tile_at(dt, r, (c & 127) + 4 * e);
+                for (int e = 0; e < 4; ++e) d4[e] = dd[e];
+                const int c2 = c + 16 * kTurn, tj2 = kTile * t.j + (c2 >> 7);
+                if (ch + kTurn < 4 * t.nb && ti <= tj2) {
+                    float* dt = gram_tile(M, ti, tj2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dd[e] = *tile_at(dt, r, (c2 & 127) + 4 * e);
                 }
                 tmem_ld_wait();
                 if (ti <= tj) {
                     float o[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        o[4 * e] = fmaf(bb, dd[e].x, J.c * __uint_as_float(v[4 * e]));
-                        o[4 * e + 1] = fmaf(bb, dd[e].y, J.c * __uint_as_float(v[4 * e + 1]));
-                        o[4 * e + 2] = fmaf(bb, dd[e].z, J.c * __uint_as_float(v[4 * e + 2]));
-                        o[4 * e + 3] = fmaf(bb, dd[e].w, J.c * __uint_as_float(v[4 * e + 3]));
+                        o[4 * e] = fmaf(bb, d4[e].x, J.c * __uint_as_float(v[4 * e]));
+                        o[4 * e + 1] = fmaf(bb, d4[e].y, J.c * __uint_as_float(v[4 * e + 1]));
+                        o[4 * e + 2] = fmaf(bb, d4[e].z, J.c * __uint_as_float(v[4 * e + 2]));
+                        o[4 * e + 3] = fmaf(bb, d4[e].w, J.c * __uint_as_float(v[4 * e + 3]));
                     }
                     const int j = 128 * tj + (c & 127);
                     store_row16(M.bp, i, j, M.rb, o);
@@ -662,7 +679,7 @@ __device__ __forceinline__ void epilogue(const Job& J, int cur, int step, Shared
                     }
                 }
             } else {
-                const int j = 256 * t.j + c;
+                const int j = c;
                 const float wx = J.a + sc.theta, wh = sc.beta - sc.theta;
                 float h[16], y[16];
                 const uint32_t rest[4] = {xr.x, xr.y, xr.z, xr.w};
@@ -1307,7 +1324,7 @@ bool plan_sizes(Mat* mats, int count) {
     const int tile = pair ? 2 : 1;
     for (int i = 0; i < count; ++i) {
         Mat& M = mats[i];
-        M.cb = pair ? (M.nx + 3) / 4 * 4 : M.nx, M.ut = (M.nx + 3) / 4;
+        M.cb = pair ? (M.nx + 3) / 4 * 4 : M.nx;
         M.gt = (M.k + 128 * tile - 1) / (128 * tile), M.mt = tile * M.gt, M.rb = 2 * M.mt;
         const int64_t total = M.rows * M.cols;
         M.chunk = std::max<int64_t>(4096, ((total + kNormChunks - 1) / kNormChunks + 3) / 4 * 4);
@@ -1335,6 +1352,26 @@ int gram_share(const Mat* mats, int count, bool pair) {
     }
     const int64_t share = std::max<int64_t>(4, (blocks + units - 1) / units);
     return *std::max_element(load.begin(), load.end()) <= share + 10 ? 0 : (int)share;
+}
+
+// 64-column blocks of a tile of phase U on single CTAs, which keep the busiest CTA least: a tile takes as long as its blocks'
+// loads (2 + width for each contracted block) and an epilogue that was measured to be worth ten loads a block of width.
+int update_width(const Mat* mats, int count) {
+    int64_t best = INT64_MAX;
+    int width = 4;
+    std::vector<int64_t> load((size_t)kPlanSms);
+    for (int w = 4; w >= 1; --w) {
+        std::fill(load.begin(), load.end(), 0);
+        size_t u = 0;
+        for (int i = 0; i < count; ++i)
+            for (int64_t t = (int64_t)mats[i].gt * ((mats[i].nx + w - 1) / w); t > 0; --t) {
+                load[u] += (int64_t)((mats[i].k + 63) / 64) * (2 + w) + 10 * w + 8;
+                if (++u == load.size()) u = 0;
+            }
+        const int64_t most = *std::max_element(load.begin(), load.end());
+        if (most < best) best = most, width = w;
+    }
+    return width;
 }
 
 // The tiles that the ends of shares lie in.
@@ -1460,8 +1497,10 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         const bool pair = plan_sizes(&mats[b], J.count);
         place(&mats[b], J.count, pair, static_cast<char*>(ws), &J.part);
         J.share = gram_share(&mats[b], J.count, pair);
+        J.uw = pair ? 4 : update_width(&mats[b], J.count);
         for (int i = 0; i < J.count; ++i) {
             Mat& M = J.mat[i] = mats[b + i];
+            M.ut = (M.nx + J.uw - 1) / J.uw;
             M.n0 = J.nn, M.c0 = J.nc, M.s0 = J.ns, M.u0 = J.nu, M.b0 = J.blocks;
             const int tiles = M.gt * (M.gt + 1) / 2;
             J.nn += M.chunks;
@@ -1470,6 +1509,7 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
             J.ns += tiles;
             J.nu += M.gt * M.ut;
         }
+        J.half = !pair && 2 * J.ns <= kPlanSms;
         if (J.share) list_cuts(J);
         J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.cap = cap_of(p), J.mu = mu, J.nesterov = nesterov;
         J.sync = static_cast<uint32_t*>(ws);
