@@ -62,7 +62,7 @@ struct Mat {
     int f32, tall;
     float keep, step;        // w = keep w - step X
     float tau;
-    int vec;                 // rows of the result start at 16 bytes
+    int vec, wide;           // rows start at 16 bytes, those of the result at 32
     int aligned;             // g starts at 16 bytes
     int rb, cb, nx;          // operand blocks: X is rb x cb, of which nx have columns, A' and B' rb x rb
     int mt, gt, ut;          // 128-row tiles, rows of tiles (1, in pairs 2, of those each), columns of tiles of phase U
@@ -530,6 +530,41 @@ __device__ __forceinline__ void write_result(const Mat& M, int64_t off, int i, i
     const float inv = 1.f / M.tau;
     const int cnt = min(C, M.n - j);
     if (cnt <= 0) return;
+    if (M.wide && cnt == C) {
+        // lanes' rows lie apart, so that an access of 32 bytes a lane takes no longer than one of 16
+        const int64_t base = off + (int64_t)i * M.n + j;
+        if (M.w) {
+            float w[C];
+#pragma unroll
+            for (int e = 0; e < C; e += 8)
+                asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=f"(w[e]), "=f"(w[e + 1]), "=f"(w[e + 2]), "=f"(w[e + 3]), "=f"(w[e + 4]), "=f"(w[e + 5]),
+                               "=f"(w[e + 6]), "=f"(w[e + 7])
+                             : "l"(M.w + base + e));
+#pragma unroll
+            for (int e = 0; e < C; ++e) y[e] = M.keep * w[e] - M.step * (y[e] * inv);
+#pragma unroll
+            for (int e = 0; e < C; e += 8)
+                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(M.w + base + e), "f"(y[e]),
+                             "f"(y[e + 1]), "f"(y[e + 2]), "f"(y[e + 3]), "f"(y[e + 4]), "f"(y[e + 5]), "f"(y[e + 6]),
+                             "f"(y[e + 7])
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int e = 0; e < C; ++e) y[e] *= inv;
+        }
+        if (M.o) {
+#pragma unroll
+            for (int e = 0; e < C; e += 16)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(M.o + base + e),
+                             "r"(pack_bf16(y[e], y[e + 1])), "r"(pack_bf16(y[e + 2], y[e + 3])),
+                             "r"(pack_bf16(y[e + 4], y[e + 5])), "r"(pack_bf16(y[e + 6], y[e + 7])),
+                             "r"(pack_bf16(y[e + 8], y[e + 9])), "r"(pack_bf16(y[e + 10], y[e + 11])),
+                             "r"(pack_bf16(y[e + 12], y[e + 13])), "r"(pack_bf16(y[e + 14], y[e + 15]))
+                             : "memory");
+        }
+        return;
+    }
     if (M.vec && cnt == C) {
         const int64_t base = off + (int64_t)i * M.n + j;
         if (M.w) {
@@ -1316,6 +1351,7 @@ bool plan_sizes(Mat* mats, int count) {
         M.tall = M.rows > M.cols;
         M.k = (int)std::min(M.rows, M.cols), M.n = (int)std::max(M.rows, M.cols);
         M.vec = !M.tall && M.n % 8 == 0;
+        M.wide = !M.tall && M.n % 16 == 0 && (reinterpret_cast<uintptr_t>(M.w) | reinterpret_cast<uintptr_t>(M.o)) % 32 == 0;
         M.aligned = reinterpret_cast<uintptr_t>(M.g) % 16 == 0;
         M.nx = (M.n + 63) / 64;
         work += (int64_t)((M.k + 255) / 256) * ((M.nx + 3) / 4) * ((M.k + 63) / 64);
