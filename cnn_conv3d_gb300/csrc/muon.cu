@@ -88,7 +88,8 @@ struct Job {
     int nn, nc, ns, nu;  // items of each phase; G has S's
     int share, blocks;   // phase G cut into shares of so many blocks of all its tiles' (0: whole tiles)
     int cuts;
-    int half, uw;        // S in tiles of 64 columns; 64-column blocks of a tile of U
+    int half, uw;        // S in tiles of half the columns; 64-column blocks of a tile of U
+    int whole;           // tiles of U before those that are taken in halves
     float* part;
     float a, b, c, eps, mu, cap;
     int nesterov;
@@ -248,8 +249,8 @@ __device__ __forceinline__ int unit_count() { return PAIR ? gridDim.x >> 1 : gri
 struct Item {
     int mat, i, j;  // tile, tile of the other side
     int kb0, kb1;   // blocks of the contracted axis
-    int cb0;        // first 64-column block of the tile (S: which half)
-    int nb;         // 64-column blocks of the tile
+    int cb0;        // its first 64-column block (S: within the tile of the other side)
+    int nb;         // 64-column blocks of the item
     int slot;       // where a part of a tile goes, -1 for a whole one
 };
 
@@ -270,7 +271,7 @@ struct Walk {
     int it, at = 0, end = 0, mat = 0;
     __device__ __forceinline__ Walk() : it(unit_id<PAIR>()) {}
     __device__ __forceinline__ bool next(const Job& J, Item& t) {
-        t.kb0 = 0, t.slot = -1, t.cb0 = 0;
+        t.kb0 = 0, t.slot = -1, t.cb0 = 0, t.nb = PAIR ? 4 : 2;
         int e;
         if (PH == PH_G && J.share) {
             if (at == end) {
@@ -286,12 +287,15 @@ struct Walk {
             at += t.kb1 - t.kb0;
             if (t.kb1 - t.kb0 < M.nx) t.slot = 2 * (it - unit_count<PAIR>()) + (t.kb0 == 0);
         } else {
-            const int half = PH == PH_S && !PAIR ? J.half : 0, at = it >> half;
+            const bool half = PH == PH_S ? J.half : PH == PH_U && PAIR && it >= J.whole;
+            const int from = PH == PH_U ? J.whole : 0, which = half ? (it - from) & 1 : 0;
+            const int at = half ? from + ((it - from) >> 1) : it;
             if (at >= (PH == PH_U ? J.nu : J.ns)) return false;
             while (mat + 1 < J.count && at >= (PH == PH_U ? J.mat[mat + 1].u0 : J.mat[mat + 1].s0)) ++mat;
             const Mat& M = J.mat[mat];
             e = at - (PH == PH_U ? M.u0 : M.s0);
-            t.cb0 = it & half;
+            t.nb = (PAIR ? 4 : 2) >> half;
+            t.cb0 = which * t.nb;
             t.kb1 = PH == PH_G ? M.nx : (M.k + 63) / 64;
             it += unit_count<PAIR>();
         }
@@ -300,11 +304,10 @@ struct Walk {
         if (PH == PH_U) {
             t.i = e % M.gt;
             t.j = e / M.gt;
-            t.cb0 = J.uw * t.j;
-            t.nb = PAIR ? 4 : min(J.uw, M.cb - t.cb0);
+            t.cb0 += J.uw * t.j;
+            if (!PAIR) t.nb = min(J.uw, M.cb - t.cb0);
         } else {
             upper_tile(e, M.gt, t.i, t.j);
-            t.nb = PAIR ? 4 : PH == PH_S ? 2 - J.half : 2;
         }
         return true;
     }
@@ -321,6 +324,10 @@ struct Pipe {
         if (++stage == stages) stage = 0;
     }
 };
+// Whether the other side's rows are the tile's, in shared memory at the same place.
+template <int PH, bool PAIR>
+__device__ __forceinline__ bool same_side(const Item& t) { return PH != PH_U && t.i == t.j && !(PAIR && t.nb < 4); }
+
 // Blocks of a stage in a phase: two of the CTA's rows, and the other side's.
 template <int PH, bool PAIR>
 __device__ __forceinline__ int stage_blocks(const Job& J) { return PH == PH_U && !PAIR && J.uw > 2 ? 6 : 4; }
@@ -373,16 +380,16 @@ __device__ __forceinline__ void produce(const Job& J, int cur, Shared& sh, uint8
         const Mat& M = J.mat[t.mat];
         const __half* a = PH == PH_G ? M.xh[cur] : PH == PH_S ? M.ad : M.bp;
         const int acb = PH == PH_G ? M.cb : M.rb;
-        const bool same = PH != PH_U && t.i == t.j;
-        const int cols = PAIR ? 2 : t.nb;  // blocks of the other side that the CTA fetches
+        const bool same = same_side<PH, PAIR>(t);
+        const int cols = PAIR ? t.nb / 2 : t.nb;  // blocks of the other side that the CTA fetches
         const uint32_t bytes = (2 + (same ? 0 : cols)) * kBlkBytes;
         // the lane's copy of each stage: a block of the tile's rows (lanes 0, 1), of the other side's rows (2, 3), or (U, lane 2)
         // X's row of blocks
         const bool isb = lane >= 2, row = PH == PH_U && isb;
         const int q = lane & 1;
         const bool mine = lane < 2 || (!same && lane < (PH == PH_U ? 3 : 2 + cols));
-        const int tr = (PAIR ? 4 : 2) * (isb ? t.j : t.i) + 2 * rank + q + (isb ? t.cb0 : 0);
-        const __half* src = row ? M.xh[cur] + ((int64_t)t.kb0 * M.cb + t.cb0 + 2 * rank) * kBlk : a + ((int64_t)tr * acb + t.kb0) * kBlk;
+        const int tr = (PAIR ? 4 : 2) * (isb ? t.j : t.i) + (isb ? t.cb0 + cols * rank : 2 * rank) + q;
+        const __half* src = row ? M.xh[cur] + ((int64_t)t.kb0 * M.cb + t.cb0 + cols * rank) * kBlk : a + ((int64_t)tr * acb + t.kb0) * kBlk;
         const int64_t step = row ? (int64_t)M.cb * kBlk : kBlk;
         const uint32_t size = row ? cols * kBlkBytes : kBlkBytes, dst = (isb ? 2 + (row ? 0 : q) : q) * kBlkBytes;
         for (int kb = t.kb0; kb < t.kb1; ++kb, src += step) {
@@ -418,7 +425,7 @@ __device__ __forceinline__ void issue(const Job& J, Shared& sh, uint8_t* ring, P
         const uint32_t acc = P.local & 1, use = P.local >> 1, d = sh.tmem + acc * 256;
         if (!mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, J.wait_ns, J.status, WAIT_MMA_TMEM_EMPTY)) return;
         tc_fence_after();
-        const bool same = PH != PH_U && t.i == t.j;
+        const bool same = same_side<PH, PAIR>(t);
         const uint32_t idesc = idesc_f16(PAIR ? 256 : 128, 64 * t.nb, PH == PH_U);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
             if (!mbar_wait(&sh.full[P.stage], P.parity(), &sh.abort, J.wait_ns, J.status, WAIT_MMA_FULL)) return;
@@ -1545,7 +1552,10 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
             J.ns += tiles;
             J.nu += M.gt * M.ut;
         }
-        J.half = !pair && 2 * J.ns <= kPlanSms;
+        // the other side's columns in halves where there are then items enough for one round; U's last round too
+        const int units = kPlanSms / (pair ? 2 : 1), left = J.nu % units;
+        J.half = 2 * J.ns <= units;
+        J.whole = J.nu - (2 * left <= units ? left : 0);
         if (J.share) list_cuts(J);
         J.steps = p.steps, J.a = p.a, J.b = p.b, J.c = p.c, J.eps = p.eps, J.cap = cap_of(p), J.mu = mu, J.nesterov = nesterov;
         J.sync = static_cast<uint32_t*>(ws);
