@@ -959,18 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     }
 }
 
-// ---------------------------------------------------------------------------
-// Matrices of at most 128 rows (the shorter side): a cluster of CTAs to a matrix runs all of it without leaving the chip, each
-// CTA on a slice of the columns.  X's slice is an operand in shared memory and, in fp32, an accumulator in tensor memory, onto
-// which U's product is added in place.  The Gram matrix's parts are exchanged through the CTAs' shared memory: each CTA sums
-// and rounds a slice of its columns for all, and A' A' and B' are then computed by every CTA for itself.
-
-constexpr int kSmallThreads = 256;
-constexpr int kSmallRows = 128, kSmallCols = 384;  // of a CTA: 128 tensor memory columns are left to the Gram matrix
-constexpr int kMaxCluster = 16;
-constexpr uint32_t kMaxShared = 1024 + (2 * kSmallCols / 64 + 8) * kBlkBytes + 4 * kTileF;
-constexpr uint32_t kGram = 384;                    // its tensor memory column
-
+// A launch for matrices that a CTA or a cluster takes whole.
 struct SmallJob {
     Mat mat[kMaxMats];
     int uniform;       // all matrices are like mat[0], `stride` values apart
@@ -982,6 +971,157 @@ struct SmallJob {
     int* status;
     uint64_t wait_ns;
 };
+
+// ---------------------------------------------------------------------------
+// Matrices of at most K = 16 or 32 rows (the shorter side) that a CTA's shared memory holds twice: a CTA to a matrix, all of it
+// in fp32 and without tensor cores, whose way in and out of tensor memory takes longer than these products.
+//   A = X X^T: a group of lanes to a 4 x 4 tile on or above the diagonal, along the columns, then their sums
+//   B = a I + b A + c A A: an entry to a thread
+//   X = B X, into the other buffer: eight rows of a column to a thread
+
+template <int K>
+struct Tiny {
+    static constexpr int kTiles = K / 4 * (K / 4 + 1) / 2, kLanes = K == 16 ? 32 : 16, kThreads = kTiles * kLanes;
+    static constexpr int kLd = K + 4;                                  // a row of A and B in shared memory
+    static constexpr int kCols = K == 16 ? 1536 : 768;                 // of a matrix, at most
+    static constexpr size_t smem(int n) { return sizeof(float) * (2 * (size_t)K * ((n + 3) / 4 * 4 + 4) + 2 * K * kLd + 2 * 32); }
+};
+
+template <int K>
+__global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid_constant__ SmallJob J) {
+    using T = Tiny<K>;
+    extern __shared__ __align__(16) float tiny_smem[];
+    const int id = blockIdx.x, t = threadIdx.x;
+    const Mat& M = J.mat[J.uniform ? 0 : id];
+    const int64_t off = J.uniform ? id * J.stride : 0;
+    const int k = M.k, n = M.n, n4 = (n + 3) / 4, ld = 4 * n4 + 4, count = k * n;
+    float* x0 = tiny_smem;
+    float* x1 = x0 + K * ld;
+    float* A = x1 + K * ld;
+    float* B = A + K * T::kLd;
+    float* red = B + K * T::kLd;
+    auto place = [&](int e) {  // of the stored element e
+        const int r = M.tall ? e % k : e / n, c = M.tall ? e / k : e % n;
+        return r * ld + c;
+    };
+
+    for (int e = t; e < K * ld; e += T::kThreads) x0[e] = 0.f;
+    __syncthreads();
+    float s = 0.f, s2 = 0.f;
+#pragma unroll 4
+    for (int e = t; e < count; e += T::kThreads) {
+        float u = M.f32 ? static_cast<const float*>(M.g)[off + e] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[off + e]);
+        if (M.m) {
+            const float m = fmaf(J.mu, M.m[off + e], u);
+            M.m[off + e] = m;
+            u = J.nesterov ? fmaf(J.mu, m, u) : m;
+        }
+        s = fmaf(u, u, s);
+        const float d = u * kDown;
+        s2 = fmaf(d, d, s2);
+        x0[place(e)] = u;
+    }
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o), s2 += __shfl_xor_sync(~0u, s2, o);
+    if ((t & 31) == 0) red[t >> 5] = s, red[32 + (t >> 5)] = s2;
+    __syncthreads();
+    s = s2 = 0.f;
+    for (int w = 0; w < T::kThreads / 32; ++w) s += red[w], s2 += red[32 + w];
+    const float pre = isinf(s) ? kDown : 1.f, inv = 1.f / (sqrtf(isinf(s) ? s2 : s) + J.eps * pre);
+    for (int e = t; e < K * ld; e += T::kThreads) x0[e] = x0[e] * pre * inv;
+    __syncthreads();
+
+    int ti, tj;  // the tile of the thread's group
+    upper_tile(t / T::kLanes, K / 4, ti, tj);
+    const int in = t % T::kLanes, np = (n + 31) / 32 * 32;
+    for (int step = 0; step < J.steps; ++step) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int c = in; c < n4; c += T::kLanes) {
+            float4 p[4], q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[e] = *reinterpret_cast<const float4*>(x0 + (4 * ti + e) * ld + 4 * c);
+                q[e] = *reinterpret_cast<const float4*>(x0 + (4 * tj + e) * ld + 4 * c);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float4 a = p[e >> 2], b = q[e & 3];
+                v[e] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, v[e]))));
+            }
+        }
+        // each exchange halves the entries that a lane sums on
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+            const bool up = in & o;
+#pragma unroll
+            for (int e = 0; e < o; ++e) {
+                const float give = up ? v[e] : v[e + o], keep = up ? v[e + o] : v[e];
+                v[e] = keep + __shfl_xor_sync(~0u, give, o);
+            }
+        }
+        if (T::kLanes == 32) v[0] += __shfl_xor_sync(~0u, v[0], 16);
+        if (in < 16) {
+            const int i = 4 * ti + (in >> 2), j = 4 * tj + (in & 3);
+            A[i * T::kLd + j] = v[0];
+            A[j * T::kLd + i] = v[0];
+        }
+        __syncthreads();
+        for (int e = t; e < K * K; e += T::kThreads) {
+            const int i = e / K, j = e % K;
+            float d = 0.f;
+#pragma unroll
+            for (int l = 0; l < K; l += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(A + i * T::kLd + l);
+                const float4 b = *reinterpret_cast<const float4*>(A + j * T::kLd + l);
+                d = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, d))));
+            }
+            B[i * T::kLd + j] = fmaf(J.b, A[i * T::kLd + j], fmaf(J.c, d, i == j ? J.a : 0.f));
+        }
+        __syncthreads();
+        for (int e = t; e < np * (K / 8); e += T::kThreads) {
+            const int j = e % np, i = e / np * 8;
+            if (j >= n) continue;
+            float x[K];
+#pragma unroll
+            for (int l = 0; l < K; ++l) x[l] = x0[l * ld + j];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float y = 0.f;
+#pragma unroll
+                for (int l = 0; l < K; l += 4) {
+                    const float4 b = *reinterpret_cast<const float4*>(B + (i + r) * T::kLd + l);
+                    y = fmaf(b.x, x[l], fmaf(b.y, x[l + 1], fmaf(b.z, x[l + 2], fmaf(b.w, x[l + 3], y))));
+                }
+                x1[(i + r) * ld + j] = y;
+            }
+        }
+        if (step == 0)  // what is beyond the columns is zero in both
+            for (int e = t; e < K * (ld - n); e += T::kThreads) x1[e / (ld - n) * ld + n + e % (ld - n)] = 0.f;
+        __syncthreads();
+        float* x = x0;
+        x0 = x1;
+        x1 = x;
+    }
+#pragma unroll 4
+    for (int e = t; e < count; e += T::kThreads) {
+        float y = x0[place(e)];
+        if (M.w) M.w[off + e] = y = M.keep * M.w[off + e] - M.step * y;
+        if (M.o) M.o[off + e] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Matrices of at most 128 rows (the shorter side): a cluster of CTAs to a matrix runs all of it without leaving the chip, each
+// CTA on a slice of the columns.  X's slice is an operand in shared memory and, in fp32, an accumulator in tensor memory, onto
+// which U's product is added in place.  The Gram matrix's parts are exchanged through the CTAs' shared memory: each CTA sums
+// and rounds a slice of its columns for all, and A' A' and B' are then computed by every CTA for itself.
+
+constexpr int kSmallThreads = 256;
+constexpr int kSmallRows = 128, kSmallCols = 384;  // of a CTA: 128 tensor memory columns are left to the Gram matrix
+constexpr int kMaxCluster = 16;
+constexpr uint32_t kMaxShared = 1024 + (2 * kSmallCols / 64 + 8) * kBlkBytes + 4 * kTileF;
+constexpr uint32_t kGram = 384;                    // its tensor memory column
 
 struct SmallShared {
     uint64_t bar;
@@ -1481,6 +1621,13 @@ int cluster_of(const std::vector<Mat>& mats) {
     return most;
 }
 
+// The K of ns_tiny_kernel that takes all of the matrices, or 0.
+int tiny_of(const std::vector<Mat>& mats) {
+    int64_t k = 0, n = 0;
+    for (const Mat& M : mats) k = std::max(k, std::min(M.rows, M.cols)), n = std::max(n, std::max(M.rows, M.cols));
+    return k <= 16 && n <= Tiny<16>::kCols ? 16 : k <= 32 && n <= Tiny<32>::kCols ? 32 : 0;
+}
+
 size_t workspace_of(std::vector<Mat>& mats) {
     if (cluster_of(mats)) return 256;
     size_t most = 0;
@@ -1494,18 +1641,23 @@ size_t workspace_of(std::vector<Mat>& mats) {
 }
 
 cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, int cluster, bool uniform) {
-    if (cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared) != cudaSuccess ||
-        cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    const int tiny = tiny_of(mats);
+    const auto kernel = tiny == 16 ? ns_tiny_kernel<16> : tiny == 32 ? ns_tiny_kernel<32> : ns_small_kernel;
+    if (tiny) cluster = 1;
+    const size_t most = tiny == 16 ? Tiny<16>::smem(Tiny<16>::kCols) : tiny == 32 ? Tiny<32>::smem(Tiny<32>::kCols) : kMaxShared;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
+        (cluster > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
         return CF_ERR_CUDA;
     const size_t each = uniform ? mats.size() : kMaxMats;
     for (size_t b = 0; b < mats.size(); b += each) {
         SmallJob J{};
         const int count = (int)std::min(each, mats.size() - b);
-        int per = 1;
+        int per = 1, longest = 1;
         plan_sizes(&mats[b], uniform ? 1 : count);
         for (int i = 0; i < (uniform ? 1 : count); ++i) {
             J.mat[i] = mats[b + i];
             per = std::max(per, (mats[b + i].cb + cluster - 1) / cluster);
+            longest = std::max(longest, mats[b + i].n);
         }
         J.uniform = uniform, J.stride = mats[0].rows * mats[0].cols;
         J.cluster = cluster;
@@ -1514,8 +1666,9 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
         J.wait_ns = ctx.wait_ns;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(count * cluster));
-        cfg.blockDim = dim3(kSmallThreads);
-        cfg.dynamicSmemBytes = 1024 + (2 * per + 8) * kBlkBytes + (cluster > 1 ? 4 * kTileF : 0);
+        cfg.blockDim = dim3(tiny == 16 ? Tiny<16>::kThreads : tiny == 32 ? Tiny<32>::kThreads : kSmallThreads);
+        cfg.dynamicSmemBytes = tiny == 16 ? Tiny<16>::smem(longest) : tiny == 32 ? Tiny<32>::smem(longest)
+                                                                                : 1024 + (2 * per + 8) * kBlkBytes + (cluster > 1 ? 4 * kTileF : 0);
         cfg.stream = ctx.stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1523,7 +1676,7 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, ns_small_kernel, J) != cudaSuccess) return CF_ERR_CUDA;
+        if (cudaLaunchKernelEx(&cfg, kernel, J) != cudaSuccess) return CF_ERR_CUDA;
     }
     return CF_OK;
 }
