@@ -990,6 +990,7 @@ struct Tiny {
 template <int K>
 __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid_constant__ SmallJob J) {
     using T = Tiny<K>;
+    constexpr int kAhead = 8;  // loads of a thread in flight
     extern __shared__ __align__(16) float tiny_smem[];
     const int id = blockIdx.x, t = threadIdx.x;
     const Mat& M = J.mat[J.uniform ? 0 : id];
@@ -1000,26 +1001,40 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
     float* A = x1 + K * ld;
     float* B = A + K * T::kLd;
     float* red = B + K * T::kLd;
-    auto place = [&](int e) {  // of the stored element e
-        const int r = M.tall ? e % k : e / n, c = M.tall ? e / k : e % n;
-        return r * ld + c;
+    // of the stored element e; the quotient by d is exact while e d < 2^32
+    const uint32_t d = M.tall ? k : n, part = 0xFFFFFFFFu / d + 1;
+    auto place = [&](uint32_t e) {
+        const uint32_t q = part ? __umulhi(e, part) : e, r = e - q * d;
+        return M.tall ? r * ld + q : q * ld + r;
     };
 
     for (int e = t; e < K * ld; e += T::kThreads) x0[e] = 0.f;
     __syncthreads();
     float s = 0.f, s2 = 0.f;
-#pragma unroll 4
-    for (int e = t; e < count; e += T::kThreads) {
-        float u = M.f32 ? static_cast<const float*>(M.g)[off + e] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[off + e]);
-        if (M.m) {
-            const float m = fmaf(J.mu, M.m[off + e], u);
-            M.m[off + e] = m;
-            u = J.nesterov ? fmaf(J.mu, m, u) : m;
+    for (int e0 = t; e0 < count; e0 += kAhead * T::kThreads) {
+        float u[kAhead], m[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int e = e0 + a * T::kThreads;
+            u[a] = m[a] = 0.f;
+            if (e >= count) continue;
+            u[a] = M.f32 ? static_cast<const float*>(M.g)[off + e] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[off + e]);
+            if (M.m) m[a] = M.m[off + e];
         }
-        s = fmaf(u, u, s);
-        const float d = u * kDown;
-        s2 = fmaf(d, d, s2);
-        x0[place(e)] = u;
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int e = e0 + a * T::kThreads;
+            if (e >= count) continue;
+            if (M.m) {
+                m[a] = fmaf(J.mu, m[a], u[a]);
+                M.m[off + e] = m[a];
+                u[a] = J.nesterov ? fmaf(J.mu, m[a], u[a]) : m[a];
+            }
+            s = fmaf(u[a], u[a], s);
+            const float low = u[a] * kDown;
+            s2 = fmaf(low, low, s2);
+            x0[place(e)] = u[a];
+        }
     }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o), s2 += __shfl_xor_sync(~0u, s2, o);
     if ((t & 31) == 0) red[t >> 5] = s, red[32 + (t >> 5)] = s2;
@@ -1079,22 +1094,21 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
             B[i * T::kLd + j] = fmaf(J.b, A[i * T::kLd + j], fmaf(J.c, d, i == j ? J.a : 0.f));
         }
         __syncthreads();
-        for (int e = t; e < np * (K / 8); e += T::kThreads) {
-            const int j = e % np, i = e / np * 8;
+        for (int e = t, j = t, i = 0; e < np * (K / 8); e += T::kThreads, j += T::kThreads) {
+            while (j >= np) j -= np, i += 8;
             if (j >= n) continue;
-            float x[K];
+            float y[8] = {};
 #pragma unroll
-            for (int l = 0; l < K; ++l) x[l] = x0[l * ld + j];
+            for (int l = 0; l < K; l += 4) {
+                const float x[4] = {x0[l * ld + j], x0[(l + 1) * ld + j], x0[(l + 2) * ld + j], x0[(l + 3) * ld + j]};
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                float y = 0.f;
-#pragma unroll
-                for (int l = 0; l < K; l += 4) {
+                for (int r = 0; r < 8; ++r) {
                     const float4 b = *reinterpret_cast<const float4*>(B + (i + r) * T::kLd + l);
-                    y = fmaf(b.x, x[l], fmaf(b.y, x[l + 1], fmaf(b.z, x[l + 2], fmaf(b.w, x[l + 3], y))));
+                    y[r] = fmaf(b.x, x[0], fmaf(b.y, x[1], fmaf(b.z, x[2], fmaf(b.w, x[3], y[r]))));
                 }
-                x1[(i + r) * ld + j] = y;
             }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x1[(i + r) * ld + j] = y[r];
         }
         if (step == 0)  // what is beyond the columns is zero in both
             for (int e = t; e < K * (ld - n); e += T::kThreads) x1[e / (ld - n) * ld + n + e % (ld - n)] = 0.f;
@@ -1103,11 +1117,21 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
         x0 = x1;
         x1 = x;
     }
-#pragma unroll 4
-    for (int e = t; e < count; e += T::kThreads) {
-        float y = x0[place(e)];
-        if (M.w) M.w[off + e] = y = M.keep * M.w[off + e] - M.step * y;
-        if (M.o) M.o[off + e] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    for (int e0 = t; e0 < count; e0 += kAhead * T::kThreads) {
+        float w[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int e = e0 + a * T::kThreads;
+            w[a] = M.w && e < count ? M.w[off + e] : 0.f;
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int e = e0 + a * T::kThreads;
+            if (e >= count) continue;
+            float y = x0[place(e)];
+            if (M.w) M.w[off + e] = y = M.keep * w[a] - M.step * y;
+            if (M.o) M.o[off + e] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        }
     }
 }
 
