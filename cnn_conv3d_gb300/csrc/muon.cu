@@ -977,13 +977,15 @@ struct SmallJob {
 // in fp32 and without tensor cores, whose way in and out of tensor memory takes longer than these products.
 //   A = X X^T: a group of lanes to a 4 x 4 tile on or above the diagonal, along the columns, then their sums
 //   B = a I + b A + c A A: an entry to a thread
-//   X = B X, into the other buffer: eight rows of a column to a thread
+//   X = B X, into the other buffer: 4 x 4 entries to a thread (shared memory's bytes bound this: a column of eight took 1.8 times)
 
 template <int K>
 struct Tiny {
     static constexpr int kTiles = K / 4 * (K / 4 + 1) / 2, kLanes = K == 16 ? 32 : 16, kThreads = kTiles * kLanes;
     static constexpr int kLd = K + 4;                                  // a row of A and B in shared memory
-    static constexpr int kCols = K == 16 ? 1536 : 768;                 // of a matrix, at most
+    // Columns, at most: beyond, the clusters below are faster (five steps, one matrix, here against there: 16 x 108 11 : 37 us,
+    // 16 x 1024 43 : 54, 16 x 1500 59 : 57, 32 x 108 20 : 37, 32 x 432 46 : 60, 32 x 768 72 : 49).
+    static constexpr int kCols = K == 16 ? 1408 : 512;
     static constexpr size_t smem(int n) { return sizeof(float) * (2 * (size_t)K * ((n + 3) / 4 * 4 + 4) + 2 * K * kLd + 2 * 32); }
 };
 
@@ -1047,7 +1049,7 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
 
     int ti, tj;  // the tile of the thread's group
     upper_tile(t / T::kLanes, K / 4, ti, tj);
-    const int in = t % T::kLanes, np = (n + 31) / 32 * 32;
+    const int in = t % T::kLanes;
     for (int step = 0; step < J.steps; ++step) {
         float v[16];
 #pragma unroll
@@ -1094,24 +1096,26 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
             B[i * T::kLd + j] = fmaf(J.b, A[i * T::kLd + j], fmaf(J.c, d, i == j ? J.a : 0.f));
         }
         __syncthreads();
-        for (int e = t, j = t, i = 0; e < np * (K / 8); e += T::kThreads, j += T::kThreads) {
-            while (j >= np) j -= np, i += 8;
-            if (j >= n) continue;
-            float y[8] = {};
+        for (int e = t, c = t, i = 0; e < n4 * (K / 4); e += T::kThreads, c += T::kThreads) {
+            while (c >= n4) c -= n4, i += 4;
+            float4 y[4] = {};
 #pragma unroll
             for (int l = 0; l < K; l += 4) {
-                const float x[4] = {x0[l * ld + j], x0[(l + 1) * ld + j], x0[(l + 2) * ld + j], x0[(l + 3) * ld + j]};
+                float4 x[4];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const float4*>(x0 + (l + r) * ld + 4 * c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
                     const float4 b = *reinterpret_cast<const float4*>(B + (i + r) * T::kLd + l);
-                    y[r] = fmaf(b.x, x[0], fmaf(b.y, x[1], fmaf(b.z, x[2], fmaf(b.w, x[3], y[r]))));
+                    y[r].x = fmaf(b.x, x[0].x, fmaf(b.y, x[1].x, fmaf(b.z, x[2].x, fmaf(b.w, x[3].x, y[r].x))));
+                    y[r].y = fmaf(b.x, x[0].y, fmaf(b.y, x[1].y, fmaf(b.z, x[2].y, fmaf(b.w, x[3].y, y[r].y))));
+                    y[r].z = fmaf(b.x, x[0].z, fmaf(b.y, x[1].z, fmaf(b.z, x[2].z, fmaf(b.w, x[3].z, y[r].z))));
+                    y[r].w = fmaf(b.x, x[0].w, fmaf(b.y, x[1].w, fmaf(b.z, x[2].w, fmaf(b.w, x[3].w, y[r].w))));
                 }
             }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) x1[(i + r) * ld + j] = y[r];
+            for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(x1 + (i + r) * ld + 4 * c) = y[r];
         }
-        if (step == 0)  // what is beyond the columns is zero in both
-            for (int e = t; e < K * (ld - n); e += T::kThreads) x1[e / (ld - n) * ld + n + e % (ld - n)] = 0.f;
         __syncthreads();
         float* x = x0;
         x0 = x1;
