@@ -30,6 +30,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <new>
 #include <vector>
 
 #include "cf_internal.h"
@@ -1627,14 +1628,16 @@ size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
     return at;
 }
 
-// CTAs of a matrix in ns_small_kernel, 0 where it does not take the matrix: as few as hold its columns, but up to four blocks
-// of 64 to a CTA where it has more than one (the steps on X's columns then weigh as much as the exchange).
+// CTAs of a matrix in ns_small_kernel, 0 where it does not take the matrix: as many as leave a CTA about two blocks of 64 columns,
+// or four where there are more than 64 rows (the exchange then weighs as much), and one where it holds them all but for that.
+// Five steps, two blocks against four: 64 x 432 54 : 64 us, 128 x 256 73 : 65.  Long matrices go to ns_kernel, here against there:
+// 64 x 2000 68 : 98, 128 x 432 83 : 88, 128 x 1728 102 : 96, 128 x 3456 132 : 100.
 int cluster_of(const Mat& M) {
-    const int64_t k = std::min(M.rows, M.cols), cb = (std::max(M.rows, M.cols) + 63) / 64;
-    if (k > kSmallRows || cb > kMaxCluster * (kSmallCols / 64)) return 0;
+    const int64_t k = std::min(M.rows, M.cols), n = std::max(M.rows, M.cols), cb = (n + 63) / 64, each = k > 64 ? 4 : 2;
+    if (k > kSmallRows || n > (k > 64 ? 1536 : 4096)) return 0;
     int q = 1;
-    if (cb > kSmallCols / 64)
-        while (q < kMaxCluster && 4 * q < cb) q *= 2;
+    if (cb > (k > 64 ? kSmallCols / 64 : each))
+        while (q < kMaxCluster && each * q < cb) q *= 2;
     return q;
 }
 
@@ -1798,13 +1801,15 @@ static cf_status ns_check(const cf_ns_desc* d) {
     return CF_OK;
 }
 
-size_t cf_orthogonalize_workspace_size(const cf_ns_desc* desc) {
+size_t cf_orthogonalize_workspace_size(const cf_ns_desc* desc) try {
     if (ns_check(desc) != CF_OK) return 0;
     std::vector<Mat> mats = batch_of(desc, nullptr, nullptr);
     return workspace_of(mats);
+} catch (const std::bad_alloc&) {  // the list of matrices
+    return 0;
 }
 
-cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, void* ws, size_t ws_bytes, void* stream) {
+cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, void* ws, size_t ws_bytes, void* stream) try {
     if (const cf_status st = ns_check(desc); st != CF_OK) return st;
     if (g == nullptr || o == nullptr || !aligned16(g) || !aligned16(o) || !aligned16(ws)) return CF_ERR_INVALID_ARG;
     std::vector<Mat> mats = batch_of(desc, g, o);
@@ -1812,6 +1817,8 @@ cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, v
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
     return run(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, 0.f, 0, mats, ws, true);
+} catch (const std::bad_alloc&) {  // the list of matrices
+    return CF_ERR_UNSUPPORTED;
 }
 
 static cf_status muon_check(int32_t count, const cf_muon_param* p) {
@@ -1838,14 +1845,16 @@ static std::vector<Mat> list_of(int32_t count, const cf_muon_param* p) {
     return mats;
 }
 
-size_t cf_muon_workspace_size(int32_t count, const cf_muon_param* params) {
+size_t cf_muon_workspace_size(int32_t count, const cf_muon_param* params) try {
     if (count == 0 || muon_check(count, params) != CF_OK) return 0;
     std::vector<Mat> mats = list_of(count, params);
     return workspace_of(mats);
+} catch (const std::bad_alloc&) {  // the list of matrices
+    return 0;
 }
 
 cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon_hyper* h, void* ws, size_t ws_bytes,
-                       void* stream) {
+                       void* stream) try {
     if (h == nullptr) return CF_ERR_INVALID_ARG;
     const Poly p{h->steps, h->a, h->b, h->c, h->eps};
     if (!poly_ok(p) || !std::isfinite(h->lr) || !std::isfinite(h->momentum) || !std::isfinite(h->weight_decay))
@@ -1863,6 +1872,8 @@ cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon
         mats[i].step = h->lr * params[i].scale;
     }
     return run(ctx, p, h->momentum, h->nesterov != 0, mats, ws, false);
+} catch (const std::bad_alloc&) {  // the list of matrices
+    return CF_ERR_UNSUPPORTED;
 }
 
 }  // extern "C"

@@ -248,3 +248,37 @@ def test_workspace_too_small(cf):
     size = cf.cf_muon_workspace_size(params)
     hyper = cf.cf_muon_hyper(0.01, 0.9, 0.0, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
     assert cf.cf_muon_step(params, hyper, ws, size - 1, check=False) == cf.CF_ERR_WORKSPACE
+
+
+# where one way of taking a matrix ends and the next begins; shares of products that end inside tiles; pairs of CTAs
+@pytest.mark.parametrize("rows,cols", [(16, 1408), (1409, 16), (17, 40), (512, 32), (32, 513), (64, 4096), (64, 4097), (128, 1536),
+                                       (1537, 128), (100, 1500), (1024, 2500), (1200, 1201), (2048, 2600), (2300, 2050)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_orthogonalize_sizes_where_the_way_changes(cf, oracle_mod, rows, cols, dtype):
+    rng = np.random.default_rng(rows * 31 + cols)
+    o, g = _orth(cf, _matrix(rng, (rows, cols), "normal")[None], dtype)
+    _check(oracle_mod, o, g)
+
+
+def test_result_in_rows_that_start_anywhere(cf, oracle_mod):
+    """Outputs whose rows start at 16 bytes, at 32, and at neither."""
+    import torch
+    rng = np.random.default_rng(12)
+    for rows, cols in ((130, 264), (130, 272), (130, 271)):
+        desc = cf.cf_ns_desc(1, rows, cols, cf.CF_DT_F32, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+        size = cf.cf_orthogonalize_workspace_size(desc)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        g = torch.from_numpy(rng.normal(size=(rows, cols)).astype(np.float32)).cuda()
+        for skip in (0, 8, 16):  # 0, 16 and 32 bytes into a buffer
+            buf = torch.full((rows * cols + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+            o = buf[skip:skip + rows * cols].view(rows, cols)
+            cf.cf_orthogonalize(desc, g, o, ws, size)
+            torch.cuda.synchronize()
+            assert bool((buf[:skip] == 9).all()) and bool((buf[skip + rows * cols:] == 9).all())
+            _check(oracle_mod, _f64(o)[None], _f64(g)[None])
+
+
+@pytest.mark.parametrize("shapes", [[(2048, 2600), (130, 270), (7, 9)], [(32, 64), (30, 20), (9, 500)], [(1024, 1024), (512, 512), (256, 2304), (3, 5)]],
+                         ids=["pairs", "tiny", "shares"])
+def test_muon_step_over_the_ways(cf, oracle_mod, shapes):
+    test_muon_step(cf, oracle_mod, shapes, True, 0.01)
