@@ -1,24 +1,26 @@
 // muon.cu -- orthogonalisation of matrices by Newton-Schulz products and the
 // momentum step that uses it, with their entry points.
 //
-// Matrices with a side of more than 128: three launches for all of a call.  ns_input_kernel takes the momentum step and the
-// Frobenius norms' partial sums, ns_convert_kernel writes X = u / (|u| + eps) in operand form, k x n with k <= n, and
+// Of k x n values, k <= n, matrices of a call that all have at most 32 rows go to ns_tiny_kernel, all of at most 128 to
+// ns_small_kernel, each up to a length (tiny_of, cluster_of); the others take three launches for all of a call.  ns_input_kernel
+// takes the momentum step and the Frobenius norms' partial sums, ns_convert_kernel writes X = u / (|u| + eps) in operand form, and
 // ns_kernel is one cooperative launch of a CTA per SM that runs the steps as phases between grid-wide barriers; a phase's
-// items (tiles of all matrices) are dealt out over the CTAs:
-//   G  A' = X X^T - alpha I (tiles on and above the diagonal); where the long axis is split to fill the SMs, its parts' sums
+// items (tiles of all matrices) are dealt out over the CTAs, or over pairs of them:
+//   G  A' = X X^T - alpha I (tiles on and above the diagonal), or parts of the sums where the CTAs take even shares of all
+//      tiles' blocks
 //   R  A' from the parts, where there are any
 //   S  B' = (b + 2 c alpha) A' + c A' A'     (so b A + c A^2 = beta I + B',
 //                                             beta = b alpha + c alpha^2)
 //   U  X = a X + beta X + B' X; the last step writes the result instead
 //
-// Operands are fp16, X beside its operand form in fp32.  Near the end A is
-// close to I: taking alpha and beta off before rounding keeps the rounding
-// relative to what is left.  Of beta X, the last two steps take X and the
-// earlier ones its operand: there B' X cancels beta X along directions whose
+// Operands are fp16 (11 bits; bf16's 8 gave 1e-2 to 3e-1), sums fp32, and X has a byte a value beside its operand (rest_of).
+// Near the end A is close to I: taking alpha and beta off before rounding keeps the rounding relative to what is left.  Of
+// beta X, the last two steps take X and the earlier ones its operand: there B' X cancels beta X along directions whose
 // singular value is still small, and has the operand only.
 // Any alpha gives the same polynomial; it is where a flat spectrum would be, a^(2 step) / k, up to the value that the
 // polynomial leaves in place.  Simulated against 64 bits (operands rounded, sums exact): 3e-4 to 1.2e-3 of the result, where
-// rounding A and B with their diagonals gives up to 4e-3, and the mean of A's diagonal for alpha 2e-4 to 1e-3.
+// rounding A and B with their diagonals gives up to 4e-3, and the mean of A's diagonal for alpha 2e-4 to 1e-3.  Measured:
+// 1.1e-3 for 2048 x 8192, 1.4e-3 for 1511 x 515, both before the result's rounding to bf16.
 // X is scaled by a power of two tau so that its entries stay well inside
 // fp16's normal range for every size.
 //
@@ -105,6 +107,8 @@ __device__ __forceinline__ float load_u(const Mat& M, const Job& J, int64_t i) {
     return u;
 }
 
+// Memory bounds this pass: 2048 x 8192 fp32 in 16 us, 4.0 TB/s, the seven convolutions' g and m (76 MB) in 18 us, 4.3 TB/s and the
+// writes.  256 blocks a matrix and a value a load took 110 us with the next pass, 1024 blocks and four values 48.
 // The momentum step of one chunk, and its sums of u^2 and of (kDown u)^2, which stands in where the first overflows.
 __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ Job J) {
     __shared__ float red[16];
@@ -467,7 +471,8 @@ __device__ __forceinline__ float4* tile_at(float* tile, int r, int c) {
     return reinterpret_cast<float4*>(tile) + (c >> 2) * 128 + r;
 }
 
-// X beside its operand: a byte a value, (x - h) / (2^-18 e) + 128 with h the operand's value and e the power of two in it, so
+// X beside its operand: a byte a value (24 bits in all in place of 32, the products' operands having 11: against fp32 the result
+// is as far from 64 bits as before, 1.1e-3 to 1.4e-3, and five steps of 2048 x 8192 went from 600 to 565 us), (x - h) / (2^-18 e) + 128 with h the operand's value and e the power of two in it, so
 // that the two hold x to 2^-20 of it; a quarter of fp32's bytes, and with the operand, that is read and written anyway, three
 // fifths of the traffic of phase U that X in fp32 took.  16 bytes of a row are together, then those of the tile's next row.
 __device__ __forceinline__ uint4* rest_at(const Mat& M, int i, int j) {
@@ -778,8 +783,8 @@ __device__ __forceinline__ void product_phase(const Job& J, int cur, int step, S
     __syncwarp();
 }
 
-// X in operand form and in fp32 from u, a 64 x 64 block of a matrix a block: a thread makes eight values of a row at a time,
-// with its lanes along the stored rows.
+// X in operand form, with its rest, from u, a 64 x 64 block of a matrix a block: a thread makes eight values of a row at a time,
+// with its lanes along the stored rows.  Instructions and memory about equally: 2048 x 8192 in 23 us (67 MB in, 50 MB out).
 __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__ Job J) {
     __shared__ float red[8];
     constexpr int kUnits = kBlk / 8;
@@ -791,43 +796,43 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__
     // tau u / (|u| + eps) as (u pre) inv
     const float pre = isinf(s) ? kDown : 1.f, inv = M.tau / (sqrtf(isinf(s) ? s2 : s) + J.eps * pre);
     const int e = blockIdx.x - M.c0, bi = e / M.cb, bj = e % M.cb;
-            for (int t = threadIdx.x; t < kUnits; t += 256) {
-                const int r = M.tall ? t & 63 : t >> 3, c = 8 * (M.tall ? t >> 6 : t & 7);
-                const int i = 64 * bi + r, j = 64 * bj + c;
-                float y[8];
-                if (M.vec && j < M.n && i < M.k) {  // rows of a multiple of eight values
-                    const int64_t at = (int64_t)i * M.n + j;
-                    if (M.f32) {
-                        const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(M.g) + at);
-                        const float4 p = g[0], q = g[1];
-                        y[0] = p.x, y[1] = p.y, y[2] = p.z, y[3] = p.w, y[4] = q.x, y[5] = q.y, y[6] = q.z, y[7] = q.w;
-                        if (M.m) {
-                            const float4* m = reinterpret_cast<const float4*>(M.m + at);
-                            const float4 mp = m[0], mq = m[1];
-                            const float f[8] = {mp.x, mp.y, mp.z, mp.w, mq.x, mq.y, mq.z, mq.w};
-    #pragma unroll
-                            for (int x = 0; x < 8; ++x) y[x] = J.nesterov ? fmaf(J.mu, f[x], y[x]) : f[x];
-                        }
-                    } else {
-                        const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(M.g) + at);
-                        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-    #pragma unroll
-                        for (int x = 0; x < 4; ++x) y[2 * x] = __uint_as_float(w[x] << 16), y[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
-                    }
-                } else {
-    #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        y[x] = i < M.k && j + x < M.n ? load_u(M, J, M.tall ? (int64_t)(j + x) * M.k + i : (int64_t)i * M.n + j + x) : 0.f;
+    for (int t = threadIdx.x; t < kUnits; t += 256) {
+        const int r = M.tall ? t & 63 : t >> 3, c = 8 * (M.tall ? t >> 6 : t & 7);
+        const int i = 64 * bi + r, j = 64 * bj + c;
+        float y[8];
+        if (M.vec && j < M.n && i < M.k) {  // rows of a multiple of eight values
+            const int64_t at = (int64_t)i * M.n + j;
+            if (M.f32) {
+                const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(M.g) + at);
+                const float4 p = g[0], q = g[1];
+                y[0] = p.x, y[1] = p.y, y[2] = p.z, y[3] = p.w, y[4] = q.x, y[5] = q.y, y[6] = q.z, y[7] = q.w;
+                if (M.m) {
+                    const float4* m = reinterpret_cast<const float4*>(M.m + at);
+                    const float4 mp = m[0], mq = m[1];
+                    const float f[8] = {mp.x, mp.y, mp.z, mp.w, mq.x, mq.y, mq.z, mq.w};
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) y[x] = J.nesterov ? fmaf(J.mu, f[x], y[x]) : f[x];
                 }
-    #pragma unroll
-                for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
-                const uint4 p = pack8_f16(y);
-                *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = p;
-                float h[8];
-                unpack2_f16(p.x, h[0], h[1]), unpack2_f16(p.y, h[2], h[3]);
-                unpack2_f16(p.z, h[4], h[5]), unpack2_f16(p.w, h[6], h[7]);
-                reinterpret_cast<uint2*>(rest_at(M, i, j))[(j >> 3) & 1] = make_uint2(pack_rest4(y, h), pack_rest4(y + 4, h + 4));
+            } else {
+                const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(M.g) + at);
+                const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) y[2 * x] = __uint_as_float(w[x] << 16), y[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
             }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                y[x] = i < M.k && j + x < M.n ? load_u(M, J, M.tall ? (int64_t)(j + x) * M.k + i : (int64_t)i * M.n + j + x) : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) y[x] = y[x] * pre * inv;
+        const uint4 p = pack8_f16(y);
+        *reinterpret_cast<uint4*>(M.xh[0] + blocked(i, j, M.cb)) = p;
+        float h[8];
+        unpack2_f16(p.x, h[0], h[1]), unpack2_f16(p.y, h[2], h[3]);
+        unpack2_f16(p.z, h[4], h[5]), unpack2_f16(p.w, h[6], h[7]);
+        reinterpret_cast<uint2*>(rest_at(M, i, j))[(j >> 3) & 1] = make_uint2(pack_rest4(y, h), pack_rest4(y + 4, h + 4));
+    }
 }
 
 // A' of the tiles whose long axis was cut: the sum of the parts, in their order, less alpha on the diagonal.  A warp takes four
@@ -877,6 +882,13 @@ __device__ __forceinline__ void join_phase(const Job& J, int step) {
     }
 }
 
+// What bounds it.  On pairs, 2048 x 8192: of a step's 96 us G takes 25 and U 48, at 0.33 and 0.38 us for each 256 x 256 x 64 of a
+// pair where the tensor cores' measured burst rate allows 0.33; the rest is R 10, S 13 and four barriers of 2.5 each.  All five
+// steps and the input passes: 540 us, 1.03 PFLOP/s.  (U's loads come to 113 bytes a nanosecond and SM, of 138 that L2 was measured
+// to give.)  On single CTAs, small sizes: 300 x 2000 is 4.6 + 3.4 + 4.7 + 5.2 us a step, of which 2.5 each are the barrier and
+// most of the rest the latency of loads, products and epilogue one after the other; S's and U's tiles are as narrow as fills the SMs (at 128 and 256 columns 116 us in place of 91).
+// Waiting for a tile's parts in place of R and its barrier was slower (three of 515 x 1511, a step: 12.5 us for G and R against
+// 12.1), as its reads are then a CTA's own and come late.
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ Job J) {
     extern __shared__ uint8_t smem_raw[];
@@ -979,6 +991,8 @@ struct SmallJob {
 //   A = X X^T: a group of lanes to a 4 x 4 tile on or above the diagonal, along the columns, then their sums
 //   B = a I + b A + c A A: an entry to a thread
 //   X = B X, into the other buffer: 4 x 4 entries to a thread (shared memory's bytes bound this: a column of eight took 1.8 times)
+// One of 16 x 108 in 10.5 us (28.7 by the kernel below), of which about three are the loads and the norm; a step's bound is
+// the latency of its three products, their sums over lanes and three block-wide barriers.
 
 template <int K>
 struct Tiny {
@@ -1145,6 +1159,8 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
 // CTA on a slice of the columns.  X's slice is an operand in shared memory and, in fp32, an accumulator in tensor memory, onto
 // which U's product is added in place.  The Gram matrix's parts are exchanged through the CTAs' shared memory: each CTA sums
 // and rounds a slice of its columns for all, and A' A' and B' are then computed by every CTA for itself.
+// Latency bounds it: a step of 64 x 432 takes 10 us, of 128 x 128 10, one after the other three products with their ways in
+// and out of tensor memory and, in clusters, two exchanges.
 
 constexpr int kSmallThreads = 256;
 constexpr int kSmallRows = 128, kSmallCols = 384;  // of a CTA: 128 tensor memory columns are left to the Gram matrix

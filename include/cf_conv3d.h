@@ -400,12 +400,14 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
  * coefficients are (3.4445, -4.7750, 2.0315) with 5 steps: values in about
  * [0.7, 1.2].
  *   g : [batch][rows][cols] bf16 or fp32 (dtype), o : [batch][rows][cols] bf16.
- * Products take fp16 operands (11 bits) with fp32 sums, X is carried between
- * steps in 32 bits, and what the diagonals of A and of the polynomial share is
- * kept out of the rounding: |o - exact| is about 1e-3 |exact| in the Frobenius
- * norm before the rounding to bf16.  A matrix with an entry that is not finite
+ * Products take fp16 operands (11 bits) with fp32 sums (matrices of at most 32
+ * rows: fp32 throughout), X is carried between steps to 2^-20 of its values,
+ * and what the diagonals of A and of the polynomial share is kept out of the
+ * rounding: |o - exact| is about 1e-3 |exact| in the Frobenius norm before the
+ * rounding to bf16.  A matrix with an entry that is not finite
  * gives NaN throughout.
- * Supported: 1 <= steps <= 16; rows, cols up to 65536.
+ * Supported: 1 <= steps <= 16; rows, cols up to 65536; as many matrices as the
+ * host can list (beyond: CF_ERR_UNSUPPORTED).
  *
  * cf_muon_step applies one step of momentum with orthogonalised updates to
  * `count` weight matrices (a conv filter is the matrix [c_out][27 c_in]):
