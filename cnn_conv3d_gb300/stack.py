@@ -636,8 +636,11 @@ class CosmoStack:
         wgrad 2 (split-K + reduce) per block, +1 for a stride-2 block (zero
         insertion); dgrad 2 (filter flip + conv) for blocks 1..L-1 (+1 for
         stride 2), plus the channel sums for a routed or unpooled block below:
-        1 (partials reduction) when fused in the halo-tile epilogue, else 2."""
+        1 (partials reduction) when fused in the halo-tile epilogue, else 2.
+        Group norm 3 forward and 4 backward, where a sample is small 1 and 2
+        (counted as the former)."""
         n = self.L + 3 * sum(1 for l in range(self.L) if self.bn(l))  # BN: sums, reduction, normalisation
+        n += 3 * sum(1 for l in range(self.L) if self.gn(l))
         if self.backward_enabled:
             ch = self.channels
             for l in range(self.L):
@@ -646,11 +649,13 @@ class CosmoStack:
                 pool = self.specs[l][1]
                 if self.bn(l):
                     n += 3  # batch-norm backward: sums, their reduction, dZ
+                elif self.gn(l):
+                    n += 4  # group-norm backward: coefficients, sums, their reduction, dZ
                 elif l == self.L - 1 or not (self.routed(l) or pool == "none" or self.pool_bwd_fused(l)):
                     n += 2  # pool backward
                 if l > 0:
                     n += 2 + s2  # dgrad
-                    if self.bn(l - 1):
+                    if self.normed(l - 1):
                         pass
                     elif self.routed(l - 1) or self.specs[l - 1][1] == "none" or self.pool_bwd_fused(l - 1):
                         fused = (not s2 and ch[l] <= 32 and ch[l] % 16 == 0 and ch[l] in (32, 64, 128)
