@@ -1291,7 +1291,8 @@ int vec_of(const cf_gn_desc* d) {
 // Chunks are cut for the blocks that fit 152 SMs at once, whatever the device: the workspace's size and the sums' order depend
 // on the descriptor alone.
 int plan_blocks(const cf_gn_desc* d, bool backward) { return 152 * (backward ? 2 : 3); }
-// Voxels of a thread in a chunk, at most.
+// Voxels of a thread in a chunk, at most (8 x 128^3 x 32 forward: 329 us; with 32 336, with 16 372, with 256 333; 8 x 64^3 x 64
+// backward 153, 155, 188, 158).
 constexpr int kMostRows = 64;
 
 GnArgs make_args(const cf_gn_desc* d, bool backward) {

@@ -91,7 +91,8 @@ struct Job {
     int nn, nc, ns, nu;  // items of each phase; G has S's
     int share, blocks;   // phase G cut into shares of so many blocks of all its tiles' (0: whole tiles)
     int cuts;
-    int half, uw;        // S in tiles of half the columns; 64-column blocks of a tile of U
+    int half_g, half;    // G (where it is not cut) and S in tiles of half the columns
+    int uw;              // 64-column blocks of a tile of U
     int whole;           // tiles of U before those that are taken in halves
     float* part;
     float a, b, c, eps, mu, cap;
@@ -292,7 +293,7 @@ struct Walk {
             at += t.kb1 - t.kb0;
             if (t.kb1 - t.kb0 < M.nx) t.slot = 2 * (it - unit_count<PAIR>()) + (t.kb0 == 0);
         } else {
-            const bool half = PH == PH_S ? J.half : PH == PH_U && PAIR && it >= J.whole;
+            const bool half = PH == PH_G ? J.half_g : PH == PH_S ? J.half : PH == PH_U && PAIR && it >= J.whole;
             const int from = PH == PH_U ? J.whole : 0, which = half ? (it - from) & 1 : 0;
             const int at = half ? from + ((it - from) >> 1) : it;
             if (at >= (PH == PH_U ? J.nu : J.ns)) return false;
@@ -1563,23 +1564,30 @@ bool plan_sizes(Mat* mats, int count) {
     return pair;
 }
 
-// A unit's share of phase G's blocks where that is cut, 0 where its units take whole tiles in turn: where the busiest of these
-// has at most ten blocks more than an even share, as phase R, its barrier and the parts' way through memory cost that much.
-int gram_share(const Mat* mats, int count, bool pair) {
+// How phase G's tiles are dealt out: whole or in halves of their columns, in turn, or (returns a unit's share) cut into even shares
+// of all blocks.  In loads of an operand block, of which an SM takes one in 0.058 us: a block of the contracted axis takes four, in
+// a half three, and a cut 64 more, phase R and its barrier.  (A step's G and R, cut against halves: three of 515 x 1511 12.1 : 11.1
+// us, 1024 x 1024 11.5 : 8.5; cut, 300 x 2000 takes 8.4 and 512 x 2048 9.3.)
+int gram_share(const Mat* mats, int count, bool pair, int* half) {
     const int units = kPlanSms / (pair ? 2 : 1);
-    std::vector<int64_t> load((size_t)units, 0);
-    int64_t blocks = 0;
-    size_t u = 0;
-    for (int i = 0; i < count; ++i) {
-        const int64_t tiles = (int64_t)mats[i].gt * (mats[i].gt + 1) / 2;
-        blocks += tiles * mats[i].nx;
-        for (int64_t t = 0; t < tiles; ++t) {
-            load[u] += mats[i].nx;
-            if (++u == load.size()) u = 0;
+    std::vector<int64_t> load((size_t)units);
+    int64_t blocks = 0, best = INT64_MAX;
+    for (int h = 0; h < 2; ++h) {
+        std::fill(load.begin(), load.end(), 0);
+        size_t u = 0;
+        for (int i = 0; i < count; ++i) {
+            const int64_t tiles = (int64_t)mats[i].gt * (mats[i].gt + 1) / 2;
+            if (h == 0) blocks += tiles * mats[i].nx;
+            for (int64_t t = 0; t < tiles << h; ++t) {
+                load[u] += mats[i].nx;
+                if (++u == load.size()) u = 0;
+            }
         }
+        const int64_t most = (4 - h) * *std::max_element(load.begin(), load.end());
+        if (most < best) best = most, *half = h;
     }
     const int64_t share = std::max<int64_t>(4, (blocks + units - 1) / units);
-    return *std::max_element(load.begin(), load.end()) <= share + 10 ? 0 : (int)share;
+    return best <= 4 * share + 64 ? 0 : (int)share;
 }
 
 // 64-column blocks of a tile of phase U on single CTAs, which keep the busiest CTA least: a tile takes as long as its blocks'
@@ -1640,7 +1648,8 @@ size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
         M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
     }
-    *part = reinterpret_cast<float*>(take(gram_share(mats, count, pair) ? 2 * kPlanSms * (pair ? 2 : 1) * kTileF * sizeof(float) : 0));
+    int half;
+    *part = reinterpret_cast<float*>(take(gram_share(mats, count, pair, &half) ? 2 * kPlanSms * (pair ? 2 : 1) * kTileF * sizeof(float) : 0));
     return at;
 }
 
@@ -1739,7 +1748,7 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
         const bool pair = plan_sizes(&mats[b], J.count);
         place(&mats[b], J.count, pair, static_cast<char*>(ws), &J.part);
-        J.share = gram_share(&mats[b], J.count, pair);
+        J.share = gram_share(&mats[b], J.count, pair, &J.half_g);
         J.uw = pair ? 4 : update_width(&mats[b], J.count);
         for (int i = 0; i < J.count; ++i) {
             Mat& M = J.mat[i] = mats[b + i];
