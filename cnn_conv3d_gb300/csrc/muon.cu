@@ -885,7 +885,7 @@ __device__ __forceinline__ void join_phase(const Job& J, int step) {
 
 // What bounds it.  On pairs, 2048 x 8192: of a step's 96 us G takes 25 and U 48, at 0.33 and 0.38 us for each 256 x 256 x 64 of a
 // pair where the tensor cores' measured burst rate allows 0.33; the rest is R 10, S 13 and four barriers of 2.5 each.  All five
-// steps and the input passes: 540 us, 1.03 PFLOP/s.  (U's loads come to 113 bytes a nanosecond and SM, of 138 that L2 was measured
+// steps and the input passes: 545 us, 1.02 PFLOP/s.  (U's loads come to 113 bytes a nanosecond and SM, of 138 that L2 was measured
 // to give.)  On single CTAs, small sizes: 300 x 2000 is 4.6 + 3.4 + 4.7 + 5.2 us a step, of which 2.5 each are the barrier and
 // most of the rest the latency of loads, products and epilogue one after the other; S's and U's tiles are as narrow as fills the SMs (at 128 and 256 columns 116 us in place of 91).
 // Waiting for a tile's parts in place of R and its barrier was slower (three of 515 x 1511, a step: 12.5 us for G and R against
@@ -973,9 +973,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     }
 }
 
-// A launch for matrices that a CTA or a cluster takes whole.
+// A launch for matrices that a CTA or a cluster takes whole, of N kinds (arguments with room for 48 take their time: a lone call of
+// 16 x 108 is 23 us with the host's part, with room for one 21.5).
+template <int N>
 struct SmallJob {
-    Mat mat[kMaxMats];
+    Mat mat[N];
     int uniform;       // all matrices are like mat[0], `stride` values apart
     int64_t stride;
     int cluster;       // CTAs of a matrix
@@ -992,7 +994,7 @@ struct SmallJob {
 //   A = X X^T: a group of lanes to a 4 x 4 tile on or above the diagonal, along the columns, then their sums
 //   B = a I + b A + c A A: an entry to a thread
 //   X = B X, into the other buffer: 4 x 4 entries to a thread (shared memory's bytes bound this: a column of eight took 1.8 times)
-// One of 16 x 108 in 10.5 us (28.7 by the kernel below), of which about three are the loads and the norm; a step's bound is
+// One of 16 x 108 in 11 us (28.7 by the kernel below), of which about three are the loads and the norm; a step's bound is
 // the latency of its three products, their sums over lanes and three block-wide barriers.
 
 template <int K>
@@ -1005,8 +1007,8 @@ struct Tiny {
     static constexpr size_t smem(int n) { return sizeof(float) * (2 * (size_t)K * ((n + 3) / 4 * 4 + 4) + 2 * K * kLd + 2 * 32); }
 };
 
-template <int K>
-__global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid_constant__ SmallJob J) {
+template <int K, int N>
+__global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid_constant__ SmallJob<N> J) {
     using T = Tiny<K>;
     constexpr int kAhead = 8;  // loads of a thread in flight
     extern __shared__ __align__(16) float tiny_smem[];
@@ -1207,7 +1209,8 @@ __device__ __forceinline__ float2 total_sums(const SmallShared& sh, int cluster)
     return t;
 }
 
-__global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid_constant__ SmallJob J) {
+template <int N>
+__global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid_constant__ SmallJob<N> J) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ SmallShared sh;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -1696,17 +1699,18 @@ size_t workspace_of(std::vector<Mat>& mats) {
     return most;
 }
 
+template <int N>
 cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, int cluster, bool uniform) {
     const int tiny = tiny_of(mats);
-    const auto kernel = tiny == 16 ? ns_tiny_kernel<16> : tiny == 32 ? ns_tiny_kernel<32> : ns_small_kernel;
+    const auto kernel = tiny == 16 ? ns_tiny_kernel<16, N> : tiny == 32 ? ns_tiny_kernel<32, N> : ns_small_kernel<N>;
     if (tiny) cluster = 1;
     const size_t most = tiny == 16 ? Tiny<16>::smem(Tiny<16>::kCols) : tiny == 32 ? Tiny<32>::smem(Tiny<32>::kCols) : kMaxShared;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
         (cluster > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
         return CF_ERR_CUDA;
-    const size_t each = uniform ? mats.size() : kMaxMats;
+    const size_t each = uniform ? mats.size() : N;
     for (size_t b = 0; b < mats.size(); b += each) {
-        SmallJob J{};
+        SmallJob<N> J{};
         const int count = (int)std::min(each, mats.size() - b);
         int per = 1, longest = 1;
         plan_sizes(&mats[b], uniform ? 1 : count);
@@ -1739,7 +1743,8 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
 
 // uniform: the matrices are of one batch, a matrix apart.
 cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws, bool uniform) {
-    if (const int cluster = cluster_of(mats)) return run_small(ctx, p, mu, nesterov, mats, cluster, uniform);
+    if (const int cluster = cluster_of(mats))
+        return (uniform || mats.size() == 1 ? run_small<1> : run_small<kMaxMats>)(ctx, p, mu, nesterov, mats, cluster, uniform);
     if (cudaFuncSetAttribute(ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
         return CF_ERR_CUDA;
