@@ -282,3 +282,26 @@ def test_result_in_rows_that_start_anywhere(cf, oracle_mod):
                          ids=["pairs", "tiny", "shares"])
 def test_muon_step_over_the_ways(cf, oracle_mod, shapes):
     test_muon_step(cf, oracle_mod, shapes, True, 0.01)
+
+
+@pytest.mark.parametrize("rows,cols", [(2048, 2600), (515, 1511), (128, 700), (16, 108)])
+def test_same_bits_in_a_cuda_graph_and_again(cf, rows, cols):
+    import torch
+    rng = np.random.default_rng(rows)
+    desc = cf.cf_ns_desc(1, rows, cols, cf.CF_DT_F32, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    size = cf.cf_orthogonalize_workspace_size(desc)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    g = torch.from_numpy(rng.normal(size=(rows, cols)).astype(np.float32)).cuda()
+    o = [torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    cf.cf_orthogonalize(desc, g, o[0], ws, size)
+    cf.cf_orthogonalize(desc, g, o[1], ws, size)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cf.cf_orthogonalize(desc, g, o[2], ws, size, torch.cuda.current_stream())
+    ws.fill_(0xFF)
+    o[2].fill_(9.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+    assert torch.equal(o[0], o[1]) and torch.equal(o[0], o[2])
