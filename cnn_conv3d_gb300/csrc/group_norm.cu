@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, POOL == CF_POOL_NONE ? 4 : 3) gn_app
         vfma<V>(f, a, f, be);
     };
     if constexpr (POOL == CF_POOL_NONE) {
-        constexpr int U = V > 1 ? 4 : 8;
+        constexpr int U = V > 2 ? 4 : 8;
         const int64_t xstep = (int64_t)P.lanes * A.xp;
         const T* p = xs + (P.r0 + P.lane) * A.xp;
         auto one = [&](const Pack<T, V>& t, T* at) {
@@ -1281,10 +1281,11 @@ cf_status supported(const cf_gn_desc* d) {
     return CF_OK;
 }
 
-// Values of a vector access: 16 bytes where channels and pitches allow it, else four values, else one.
+// Values of a vector access: 16 bytes where channels and pitches allow it, else four values, in bf16 two, else one.
+// (bf16 in twos against one by one: 2 x 82 95 76 x 58 forward 86 : 103 us, 5 x 89 81 95 x 26 of 90 backward 370 : 409.)
 int vec_of(const cf_gn_desc* d) {
     const int64_t xp = d->x_pitch ? d->x_pitch : d->c, yp = d->y_pitch ? d->y_pitch : d->c;
-    for (int v = d->dtype == CF_DT_F32 ? 4 : 8; v >= 4; v /= 2)
+    for (int v = d->dtype == CF_DT_F32 ? 4 : 8; v >= (d->dtype == CF_DT_F32 ? 4 : 2); v /= 2)
         if (d->c % v == 0 && xp % v == 0 && yp % v == 0) return v;
     return 1;
 }
@@ -1505,6 +1506,8 @@ void launch_small_bwd(const LaunchCtx& ctx, const GnArgs& A, const void* x, cons
             CF_GN_POOL(d, f, 8, __VA_ARGS__);                              \
         } else if (vec == 4) {                                             \
             CF_GN_POOL(d, f, 4, __VA_ARGS__);                              \
+        } else if (vec == 2) {                                             \
+            CF_GN_POOL(d, f, 2, __VA_ARGS__);                              \
         } else {                                                           \
             CF_GN_POOL(d, f, 1, __VA_ARGS__);                              \
         }                                                                  \

@@ -409,3 +409,13 @@ def test_workspace_too_small(cf):
                                                check=False)) if back else \
             (lambda s: cf.cf_group_norm_fwd(desc, x, gamma, beta, torch.empty_like(x), None, None, ws, s, check=False))
         assert call(size - 1) == cf.CF_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("shape,groups,xp,yp", [((2, 6, 4, 10, 10), 5, 0, 0), ((2, 6, 4, 10, 26), 2, 90, 30), ((1, 40, 32, 30, 58), 2, 0, 60),
+                                                ((3, 50, 48, 46, 26), 13, 90, 0), ((1, 8, 8, 8, 1030), 5, 0, 0)])
+@pytest.mark.parametrize("pool", ["none", "max", "avg"])
+def test_channels_in_pairs(cf, oracle_mod, shape, groups, xp, yp, pool):
+    """Channels and pitches that are even and no more."""
+    act = "lrelu" if pool == "max" else "silu"
+    check_forward(cf, oracle_mod, shape, groups, pool=pool, act=act, xp=xp, yp=yp, seed=31)
+    check_backward(cf, oracle_mod, shape, groups, pool=pool, act=act, xp=xp, yp=yp, seed=32)
