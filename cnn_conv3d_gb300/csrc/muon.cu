@@ -1633,9 +1633,12 @@ void list_cuts(Job& J) {
     }
 }
 
-// Places the matrices' buffers and the parts at `base` (which may be NULL, to count) and returns their size.
+// Places the matrices' buffers and the parts after the first 256 bytes of `base` (which may be NULL, to count) and returns the
+// size that this takes of a workspace that starts at any 16 bytes: the operands are accessed 32 bytes at a time, and begin at
+// multiples of 256.
 size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
     size_t at = 256;
+    base += (256 - reinterpret_cast<uintptr_t>(base) % 256) % 256;
     auto take = [&](size_t bytes) {
         char* p = base + at;
         at += up256(bytes);
@@ -1653,7 +1656,7 @@ size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
     }
     int half;
     *part = reinterpret_cast<float*>(take(gram_share(mats, count, pair, &half) ? 2 * kPlanSms * (pair ? 2 : 1) * kTileF * sizeof(float) : 0));
-    return at;
+    return at + 256 - 16;
 }
 
 // CTAs of a matrix in ns_small_kernel, 0 where it does not take the matrix: as many as leave a CTA about two blocks of 64 columns,

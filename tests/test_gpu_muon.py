@@ -305,3 +305,46 @@ def test_same_bits_in_a_cuda_graph_and_again(cf, rows, cols):
     torch.cuda.synchronize()
     assert cf.cf_last_device_status() == cf.CF_OK
     assert torch.equal(o[0], o[1]) and torch.equal(o[0], o[2])
+
+
+@pytest.mark.parametrize("rows,cols", [(130, 300), (515, 1511), (2048, 2600), (64, 864)])
+def test_workspace_that_starts_at_any_16_bytes(cf, rows, cols):
+    """The same bits from a workspace of exactly its size that starts 16, 32 or 240 bytes into a buffer, and nothing beyond its ends
+    is written."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    desc = cf.cf_ns_desc(1, rows, cols, cf.CF_DT_F32, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    size = cf.cf_orthogonalize_workspace_size(desc)
+    g = torch.randn((rows, cols), device="cuda", generator=gen)
+    out = []
+    for skip in (0, 16, 32, 240):
+        buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        o = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+        assert buf.data_ptr() % 256 == 0
+        cf.cf_orthogonalize(desc, g, o, buf[skip:skip + size], size)
+        torch.cuda.synchronize()
+        assert cf.cf_last_device_status() == cf.CF_OK
+        assert bool((buf[:skip] == 0xA5).all()) and bool((buf[skip + size:] == 0xA5).all())
+        out.append(o)
+    assert all(torch.equal(out[0], o) for o in out[1:])
+
+
+def test_muon_workspace_that_starts_at_any_16_bytes(cf):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(40)
+    shapes = [(300, 200), (16, 27), (129, 131), (200, 512)]
+    w0, g, m0 = ([torch.randn(s, device="cuda", generator=gen) for s in shapes] for _ in range(3))
+    hyper = cf.cf_muon_hyper(0.01, 0.9, 0.1, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    got = []
+    for skip in (0, 16, 48):
+        w, m = [t.clone() for t in w0], [t.clone() for t in m0]
+        params = cf.cf_muon_params([(a, None, b, c, 0.5) for a, b, c in zip(w, g, m)])
+        size = cf.cf_muon_workspace_size(params)
+        buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        cf.cf_muon_step(params, hyper, buf[skip:skip + size], size)
+        torch.cuda.synchronize()
+        assert cf.cf_last_device_status() == cf.CF_OK
+        assert bool((buf[:skip] == 0xA5).all()) and bool((buf[skip + size:] == 0xA5).all())
+        got.append(w + m)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
