@@ -852,6 +852,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A block of a cluster may only be written to once it has begun: cluster_begin where a block does, cluster_begun before its first
+// store_remote.  The barrier's time lies under the loads between them.
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Stores v at `at` (an address of this block's shared memory) in the block `rank` of the cluster.
 __device__ __forceinline__ void store_remote(const float2* at, uint32_t rank, float2 v) {
     uint32_t a;
@@ -918,6 +922,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) gn_small_fwd_kernel(const Gn
                                                                        float* __restrict__ rstd) {
     extern __shared__ float2 ex[];  // [rank][group of the tile], then the tile's (mean, rstd)
     __shared__ float sm[kSmallThreads * V], sq[kSmallThreads * V];
+    cluster_begin();
     const SmallPlace<V> P(A);
     const int groups = A.tile * V / A.cg, g0 = blockIdx.y * groups;
     Held<T, V, POOL, R> H;
@@ -970,6 +975,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) gn_small_fwd_kernel(const Gn
             sq[at] = q[e];
         }
     __syncthreads();
+    cluster_begun();
     const int least = P.rows / P.lanes, more = P.rows - least * P.lanes;
     for (int g = threadIdx.x >> 5; g < groups; g += kSmallWarps) {
         const int q0 = g * sp.units;
@@ -1058,6 +1064,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) gn_small_bwd_kernel(const Gn
     extern __shared__ float2 ex[];  // [rank][group of the tile], then the tile's (s1, s2)
     grid_go();
     __shared__ float sb[kSmallThreads * V], sg[kSmallThreads * V];
+    if (dx) cluster_begin();  // the same for the whole grid
     const SmallPlace<V> P(A);
     const int groups = A.tile * V / A.cg;
     Held<T, V, POOL, R> H;
@@ -1152,8 +1159,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) gn_small_bwd_kernel(const Gn
             sb[i] = t.x * ga;
             sg[i] = t.y * ga;
         }
-    if (dx == nullptr) return;  // the same for the whole grid
+    if (dx == nullptr) return;
     __syncthreads();
+    cluster_begun();
     for (int g = threadIdx.x >> 5; g < groups; g += kSmallWarps) {
         float s1 = 0.f, s2 = 0.f;
         for (int i = threadIdx.x & 31; i < A.cg; i += 32) {

@@ -419,3 +419,21 @@ def test_channels_in_pairs(cf, oracle_mod, shape, groups, xp, yp, pool):
     act = "lrelu" if pool == "max" else "silu"
     check_forward(cf, oracle_mod, shape, groups, pool=pool, act=act, xp=xp, yp=yp, seed=31)
     check_backward(cf, oracle_mod, shape, groups, pool=pool, act=act, xp=xp, yp=yp, seed=32)
+
+
+# one group of all channels, so that a cluster of 16 blocks takes a sample: of the blocks 9, 9, 11 and 9 have rows (or windows)
+@pytest.mark.parametrize("shape,pool", [((2, 1, 3, 3, 2048), "none"), ((1, 1, 3, 6, 2048), "none"), ((3, 1, 3, 11, 1024), "none"),
+                                        ((2, 2, 6, 6, 2048), "max")])
+def test_clusters_whose_blocks_have_no_rows(cf, oracle_mod, shape, pool):
+    """And the same bits each time, whatever order the blocks begin in."""
+    import torch
+    act = "lrelu" if pool == "max" else "silu"
+    check_forward(cf, oracle_mod, shape, 1, pool=pool, act=act, seed=41)
+    check_backward(cf, oracle_mod, shape, 1, pool=pool, act=act, seed=42)
+    x, gamma, beta, dy = _inputs(shape, pool, "bf16", 43)
+    first = None
+    for _ in range(20):
+        y, mean, rstd = _run_fwd(cf, shape, 1, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta)
+        got = (y, mean, rstd) + _run_bwd(cf, shape, 1, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta, mean, rstd, dy)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
