@@ -183,7 +183,7 @@ struct Place {
     }
 };
 
-// The offset in x (in values) of a window's first voxel, and of the others from it.
+// The offset in x (in values) of a window's first voxel, and of the others from it.  A sample has fewer than 2^32 windows.
 __device__ __forceinline__ int64_t window_at(const GnArgs& A, int64_t row) {
     const uint32_t m = (uint32_t)row, q = A.w2.div(m), pw = m - q * A.w2.d, pd = A.h2.div(q), ph = q - pd * A.h2.d;
     return (((int64_t)(2 * pd) * A.h + 2 * ph) * A.w + 2 * pw) * A.xp;
@@ -1286,6 +1286,8 @@ bool desc_ok(const cf_gn_desc* d) {
 cf_status supported(const cf_gn_desc* d) {
     if (d->pool != CF_POOL_NONE && (((d->d | d->h | d->w) & 1) || d->dtype != CF_DT_BF16)) return CF_ERR_UNSUPPORTED;
     if (d->pool == CF_POOL_MAX && (d->act != CF_ACT_LRELU || !(d->slope >= 0.f))) return CF_ERR_UNSUPPORTED;
+    // window_at divides a window's number in 32 bits
+    if (d->pool != CF_POOL_NONE && d->d / 2 * (d->h / 2) * (d->w / 2) > (int64_t)UINT32_MAX) return CF_ERR_UNSUPPORTED;
     return CF_OK;
 }
 

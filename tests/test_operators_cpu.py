@@ -180,3 +180,20 @@ def test_muon_refusals(cf):
     assert call([entry()], hyper()) == cf.CF_ERR_WORKSPACE
     p = cf.cf_muon_params([(_Fake(16, 8, 3, 3, 3, 4), None, 48, 64, 0.5)])
     assert (p[0].rows, p[0].cols, p[0].w_bf16, p[0].scale) == (8, 108, None, 0.5)
+
+
+def _refused(cf, desc):
+    """Whether all three entry points refuse the descriptor as unsupported."""
+    status = [cf.cf_group_norm_fwd(desc, 16, None, None, 32, None, None, 48, 1 << 62, check=False),
+              cf.cf_group_norm_bwd(desc, 16, None, None, 48, 48, 32, 64, None, None, 80, 1 << 62, check=False)]
+    sizes = [cf.cf_group_norm_workspace_size(desc, b) for b in (0, 1)]
+    return status == [cf.CF_ERR_UNSUPPORTED] * 2 and sizes == [0, 0]
+
+
+def test_group_norm_refuses_samples_of_2_to_32_windows(cf):
+    """A window's number is divided in 32 bits."""
+    for pool in (cf.CF_POOL_MAX, cf.CF_POOL_AVG):
+        for d, h, w in ((3300, 3300, 3300), (1 << 12, 1 << 12, 1 << 11), (1 << 20, 1 << 15, 2)):
+            assert _refused(cf, _gn(cf, d=d, h=h, w=w, c=1, groups=1, pool=pool)), (d, h, w)
+        assert cf.cf_group_norm_workspace_size(_gn(cf, d=1 << 12, h=1 << 12, w=(1 << 11) - 2, c=1, groups=1, pool=pool), 0) > 0
+    assert cf.cf_group_norm_workspace_size(_gn(cf, d=3300, h=3300, w=3300, c=1, groups=1), 0) > 0
