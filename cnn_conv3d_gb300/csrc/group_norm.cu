@@ -1326,11 +1326,18 @@ GnArgs make_args(const cf_gn_desc* d, bool backward) {
     const int64_t per = std::max<int64_t>(win == 8 ? 1 : 4, (share + waves - 1) / waves);
     A.rows = (int)std::min(A.total, lanes * per);
     A.srows = win * A.rows;
-    A.chunks = (int)((A.total + A.rows - 1) / A.rows);
+    A.chunks = (int)std::min<int64_t>((A.total + A.rows - 1) / A.rows, INT32_MAX);
     A.tdiv = FastDiv::make((uint32_t)A.tile);
     A.cdiv = FastDiv::make((uint32_t)A.chunks);
     A.gdiv = FastDiv::make((uint32_t)A.cg);
     return A;
+}
+
+// Whether the blocks of every launch and the rows of statistics can be counted in 32 bits (what fits the device's memory can).
+bool counts_ok(const GnArgs& A) {
+    const int64_t most = INT32_MAX, n = A.n;
+    return n * A.chunks + A.c / kThreads + 1 <= most && n * A.groups <= most && (int64_t)A.chunks * A.tiles <= most &&
+           n * A.c / kThreads + 1 <= most && A.tiles <= 65535;
 }
 
 // Items (vectors, or windows of eight) that a thread of the small kernels holds.
@@ -1344,7 +1351,7 @@ constexpr int64_t kSmallBytes = 16 << 20;
 bool small_args(const cf_gn_desc* d, bool backward, GnArgs& A) {
     const int v = vec_of(d), win = d->pool != CF_POOL_NONE ? 8 : 1, vc = d->c / v;
     const int64_t size = d->dtype == CF_DT_F32 ? 4 : 2;
-    if (A.s * A.n * A.c * size > kSmallBytes) return false;
+    if (A.s * A.n * A.c > kSmallBytes / size) return false;
     int a = A.cg, b = v;
     while (b) {
         const int t = a % b;
@@ -1535,6 +1542,7 @@ extern "C" {
 size_t cf_group_norm_workspace_size(const cf_gn_desc* desc, int32_t backward) {
     if (!desc_ok(desc) || supported(desc) != CF_OK) return 0;
     GnArgs A = make_args(desc, backward != 0);
+    if (!counts_ok(A)) return 0;
     const bool small = small_args(desc, backward != 0, A);
     return place(A, backward != 0, small, nullptr);
 }
@@ -1547,6 +1555,7 @@ cf_status cf_group_norm_fwd(const cf_gn_desc* desc, const void* x, const float* 
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
     GnArgs A = make_args(desc, false);
+    if (!counts_ok(A)) return CF_ERR_UNSUPPORTED;
     const bool small = small_args(desc, false, A);
     if (ws == nullptr || ws_bytes < place(A, false, small, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
@@ -1568,6 +1577,7 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
         return CF_ERR_INVALID_ARG;
     if (const cf_status st = supported(desc); st != CF_OK) return st;
     GnArgs A = make_args(desc, true);
+    if (!counts_ok(A)) return CF_ERR_UNSUPPORTED;
     const bool small = small_args(desc, true, A);
     if (ws == nullptr || ws_bytes < place(A, true, small, nullptr)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;

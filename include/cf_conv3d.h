@@ -368,7 +368,8 @@ cf_status cf_adam_step(int64_t count, float* w, uint16_t* w_bf16, const float* g
  *           forward (inference), dgamma and dbeta in the backward, dx too.
  * dx must not overlap x or dy.  Supported: any c that groups divides; d, h, w
  * even when pooled, with fewer than 2^32 windows a sample; MAX with LReLU of
- * slope >= 0.
+ * slope >= 0.  (Sizes whose launches would have 2^31 blocks, which no device
+ * holds, are unsupported too.)
  * Workspace: cf_group_norm_workspace_size(desc, 0 forward / 1 backward).
  */
 enum { CF_ACT_LRELU = 0, CF_ACT_SILU = 1 };

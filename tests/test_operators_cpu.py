@@ -197,3 +197,14 @@ def test_group_norm_refuses_samples_of_2_to_32_windows(cf):
             assert _refused(cf, _gn(cf, d=d, h=h, w=w, c=1, groups=1, pool=pool)), (d, h, w)
         assert cf.cf_group_norm_workspace_size(_gn(cf, d=1 << 12, h=1 << 12, w=(1 << 11) - 2, c=1, groups=1, pool=pool), 0) > 0
     assert cf.cf_group_norm_workspace_size(_gn(cf, d=3300, h=3300, w=3300, c=1, groups=1), 0) > 0
+
+
+def test_group_norm_refuses_more_blocks_than_a_launch_has(cf):
+    """2^60 voxels are 2^46 chunks, of which an int held none; 65535 x 65537 groups, and 2^27 chunks of 16 samples, wrapped too."""
+    side = 1 << 20
+    for kw in (dict(d=side, h=side, w=side, c=1, groups=1), dict(n=65535, d=1, h=1, w=1, c=65537, groups=65537),
+               dict(n=16, d=1 << 14, h=1 << 14, w=1 << 13, c=1, groups=1), dict(n=1, d=1, h=1, w=1, c=1 << 30, groups=1)):
+        assert _refused(cf, _gn(cf, **kw)), kw
+    # as much as a device holds
+    assert cf.cf_group_norm_workspace_size(_gn(cf, n=65535, d=128, h=128, w=128, c=1, groups=1), 1) > 0
+    assert cf.cf_group_norm_workspace_size(_gn(cf, n=4096, d=1, h=1, w=1, c=8192, groups=32), 0) > 0
