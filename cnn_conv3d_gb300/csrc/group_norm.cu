@@ -495,11 +495,13 @@ __global__ void __launch_bounds__(kThreads) gn_finish_kernel(const GnArgs A, con
     }
 }
 
+// What the launch before wrote is read by plain loads: the read-only path is for data that nobody writes while the kernel runs, and
+// this one may have begun before.
 template <int V>
 __device__ __forceinline__ void load_coef(const GnArgs& A, const Place<V>& P, float (&a)[V], float (&m)[V], float (&be)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float4 t = __ldg(&A.coef[(int64_t)P.sample * A.c + P.c0 + e]);
+        const float4 t = A.coef[(int64_t)P.sample * A.c + P.c0 + e];
         a[e] = t.x, m[e] = t.y, be[e] = t.z;
     }
 }
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_sums_kernel(const GnArgs A
             }
         });
 #pragma unroll
-        for (int e = 0; e < V; ++e) dg[e] *= __ldg(&A.coef[(int64_t)P.sample * A.c + P.c0 + e]).w;
+        for (int e = 0; e < V; ++e) dg[e] *= A.coef[(int64_t)P.sample * A.c + P.c0 + e].w;
     }
     float *sb = reinterpret_cast<float*>(ring), *sg = sb + kThreads * V;
     __syncthreads();
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const GnArgs 
     load_coef<V>(A, P, a, m, be);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float2 t = __ldg(&A.lin[(int64_t)P.sample * A.c + P.c0 + e]);
+        const float2 t = A.lin[(int64_t)P.sample * A.c + P.c0 + e];
         k0[e] = t.x, k1[e] = t.y;
     }
     extern __shared__ __align__(16) uint8_t ring[];
@@ -1244,8 +1246,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) gn_small_bwd_kernel(const Gn
 }
 
 // dbeta and dgamma from `rows` rows of channel sums: 32 channels a block, a row lane to each warp.
-__global__ void __launch_bounds__(kThreads) gn_channels_kernel(const float2* __restrict__ part, int64_t rows, int c,
-                                                              float* __restrict__ dgamma, float* __restrict__ dbeta) {
+__global__ void __launch_bounds__(kThreads) gn_channels_kernel(const float2* part, int64_t rows, int c, float* dgamma,
+                                                              float* dbeta) {
     __shared__ float2 red[kWarps][33];
     grid_wait();
     const int ch = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
