@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kNormChunks = 1024;         // partial sums of a matrix's norm, at most
 constexpr float kDown = 0x1p-80f;         // scale of the sums that stand in for overflowing ones
+constexpr float kUp = 0x1p100f, kLow = 0x1p-100f;  // scale of those for sums below kLow, of whose squares some or all are lost
 constexpr int kMaxMats = 48;              // matrices of one launch
 constexpr int kEpiWarps = 12;             // epilogue warps
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, issuer, epilogue
@@ -102,6 +103,22 @@ struct Job {
     uint64_t wait_ns;
 };
 
+// The three sums of squares of a matrix's values.
+__device__ __forceinline__ void add_squares(float u, float& s, float& down, float& up) {
+    const float d = u * kDown, p = u * kUp;
+    s = fmaf(u, u, s);
+    down = fmaf(d, d, down);
+    up = fmaf(p, p, up);
+}
+// Which of the three sums gives the norm: 0, 1 (down), 2 (up; beside an eps of 1 or more the values are nothing).
+__device__ __forceinline__ int which_sum(float s, float eps) { return isinf(s) ? 1 : s < kLow && eps < 1.f ? 2 : 0; }
+// tau u / (|u| + eps) as (u pre) inv, from the sum that which_sum names; a zero matrix gives zero whatever eps is.
+__device__ __forceinline__ void scale_of(int which, float sum, float eps, float tau, float& pre, float& inv) {
+    pre = which == 1 ? kDown : which == 2 ? kUp : 1.f;
+    const float den = sqrtf(sum) + eps * pre;
+    inv = den == 0.f ? 0.f : tau / den;
+}
+
 __device__ __forceinline__ float load_u(const Mat& M, const Job& J, int64_t i) {
     float u = M.f32 ? static_cast<const float*>(M.g)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[i]);
     if (M.m) u = J.nesterov ? fmaf(J.mu, M.m[i], u) : M.m[i];
@@ -110,9 +127,10 @@ __device__ __forceinline__ float load_u(const Mat& M, const Job& J, int64_t i) {
 
 // Memory bounds this pass: 2048 x 8192 fp32 in 16 us, 4.0 TB/s, the seven convolutions' g and m (76 MB) in 18 us, 4.3 TB/s and the
 // writes.  256 blocks a matrix and a value a load took 110 us with the next pass, 1024 blocks and four values 48.
-// The momentum step of one chunk, and its sums of u^2 and of (kDown u)^2, which stands in where the first overflows.
+// The momentum step of one chunk, and its sums of u^2, of (kDown u)^2, which stands in where the first overflows, and of (kUp u)^2,
+// which does where it underflows.
 __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ Job J) {
-    __shared__ float red[16];
+    __shared__ float red[24];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x < 2) J.sync[threadIdx.x] = 0;
     int i = 0;
@@ -120,15 +138,13 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ J
     const Mat& M = J.mat[i];
     int64_t b = (blockIdx.x - M.n0) * M.chunk;
     const int64_t e = min(b + M.chunk, M.rows * M.cols);
-    float s = 0.f, s2 = 0.f;
-    auto one = [&](float u, float m, float& mo) {  // returns u, and m's successor
+    float s = 0.f, s2 = 0.f, s3 = 0.f;
+    auto one = [&](float u, float m, float& mo) {  // mo: m's successor
         if (M.m) {
             mo = fmaf(J.mu, m, u);
             u = J.nesterov ? fmaf(J.mu, mo, u) : mo;
         }
-        s = fmaf(u, u, s);
-        u *= kDown;
-        s2 = fmaf(u, u, s2);
+        add_squares(u, s, s2, s3);
     };
     if (M.f32 && M.aligned) {
         // chunks are whole vectors but for the matrix's end
@@ -155,13 +171,15 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ J
     for (int o = 16; o; o >>= 1) {
         s += __shfl_down_sync(~0u, s, o);
         s2 += __shfl_down_sync(~0u, s2, o);
+        s3 += __shfl_down_sync(~0u, s3, o);
     }
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s, red[8 + (threadIdx.x >> 5)] = s2;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s, red[8 + (threadIdx.x >> 5)] = s2, red[16 + (threadIdx.x >> 5)] = s3;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int t = 1; t < 8; ++t) s += red[t], s2 += red[8 + t];
+        for (int t = 1; t < 8; ++t) s += red[t], s2 += red[8 + t], s3 += red[16 + t];
         M.norm[blockIdx.x - M.n0] = s;
         M.norm[kNormChunks + blockIdx.x - M.n0] = s2;
+        M.norm[2 * kNormChunks + blockIdx.x - M.n0] = s3;
     }
 }
 
@@ -793,9 +811,10 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const __grid_constant__
     int mat = 0;
     while (mat + 1 < J.count && (int)blockIdx.x >= J.mat[mat + 1].c0) ++mat;
     const Mat& M = J.mat[mat];
-    const float s = block_sum(M.norm, M.chunks, red), s2 = block_sum(M.norm + kNormChunks, M.chunks, red);
-    // tau u / (|u| + eps) as (u pre) inv
-    const float pre = isinf(s) ? kDown : 1.f, inv = M.tau / (sqrtf(isinf(s) ? s2 : s) + J.eps * pre);
+    float s = block_sum(M.norm, M.chunks, red), pre, inv;
+    const int which = which_sum(s, J.eps);
+    if (which) s = block_sum(M.norm + which * kNormChunks, M.chunks, red);
+    scale_of(which, s, J.eps, M.tau, pre, inv);
     const int e = blockIdx.x - M.c0, bi = e / M.cb, bj = e % M.cb;
     for (int t = threadIdx.x; t < kUnits; t += 256) {
         const int r = M.tall ? t & 63 : t >> 3, c = 8 * (M.tall ? t >> 6 : t & 7);
@@ -1030,7 +1049,7 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
 
     for (int e = t; e < K * ld; e += T::kThreads) x0[e] = 0.f;
     __syncthreads();
-    float s = 0.f, s2 = 0.f;
+    float s = 0.f;
     for (int e0 = t; e0 < count; e0 += kAhead * T::kThreads) {
         float u[kAhead], m[kAhead];
 #pragma unroll
@@ -1051,17 +1070,29 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
                 u[a] = J.nesterov ? fmaf(J.mu, m[a], u[a]) : m[a];
             }
             s = fmaf(u[a], u[a], s);
-            const float low = u[a] * kDown;
-            s2 = fmaf(low, low, s2);
             x0[place(e)] = u[a];
         }
     }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o), s2 += __shfl_xor_sync(~0u, s2, o);
-    if ((t & 31) == 0) red[t >> 5] = s, red[32 + (t >> 5)] = s2;
-    __syncthreads();
-    s = s2 = 0.f;
-    for (int w = 0; w < T::kThreads / 32; ++w) s += red[w], s2 += red[32 + w];
-    const float pre = isinf(s) ? kDown : 1.f, inv = 1.f / (sqrtf(isinf(s) ? s2 : s) + J.eps * pre);
+    auto total = [&](float v, float* to) {
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        if ((t & 31) == 0) to[t >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+        for (int w = 0; w < T::kThreads / 32; ++w) v += to[w];
+        return v;
+    };
+    s = total(s, red);
+    const int which = which_sum(s, J.eps);
+    if (which) {
+        s = 0.f;
+        for (int e = t; e < K * ld; e += T::kThreads) {
+            const float u = x0[e] * (which == 1 ? kDown : kUp);
+            s = fmaf(u, u, s);
+        }
+        s = total(s, red + 32);
+    }
+    float pre, inv;
+    scale_of(which, s, J.eps, 1.f, pre, inv);
     for (int e = t; e < K * ld; e += T::kThreads) x0[e] = x0[e] * pre * inv;
     __syncthreads();
 
@@ -1175,36 +1206,39 @@ struct SmallShared {
     uint64_t bar;
     uint32_t tmem;
     int abort;
-    float red[16];
-    float2 sums[kMaxCluster];  // of the CTAs: the two sums of u^2
+    float red[24];
+    float4 sums[kMaxCluster];  // of the CTAs: the three sums of u^2
 };
-
 
 // Byte offset of element (r, c) of a 128-row operand in shared memory: 64 x 64 blocks, a column's two blocks in turn.
 __device__ __forceinline__ uint32_t small_at(int r, int c) {
     return (uint32_t)(((c >> 6) * 2 + (r >> 6)) * (int)kBlkBytes + (r & 63) * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
 }
 
-// The two sums of all threads, added to slot `rank` of every CTA of the cluster; visible after the next cluster_sync.
-__device__ __forceinline__ void share_sums(SmallShared& sh, float a, float b, int rank, int cluster) {
+// The three sums of all threads, to slot `rank` of every CTA of the cluster; visible after the next cluster_sync.
+__device__ __forceinline__ void share_sums(SmallShared& sh, float a, float b, float c, int rank, int cluster) {
     for (int o = 16; o; o >>= 1) {
         a += __shfl_xor_sync(~0u, a, o);
         b += __shfl_xor_sync(~0u, b, o);
+        c += __shfl_xor_sync(~0u, c, o);
     }
     const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) sh.red[warp] = a, sh.red[8 + warp] = b;
+    if ((threadIdx.x & 31) == 0) sh.red[warp] = a, sh.red[8 + warp] = b, sh.red[16 + warp] = c;
     __syncthreads();
     if ((int)threadIdx.x < cluster) {
-        a = b = 0.f;
-        for (int i = 0; i < 8; ++i) a += sh.red[i], b += sh.red[8 + i];
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(&sh.sums[rank], threadIdx.x)), "f"(a), "f"(b) : "memory");
+        a = b = c = 0.f;
+        for (int i = 0; i < 8; ++i) a += sh.red[i], b += sh.red[8 + i], c += sh.red[16 + i];
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote(&sh.sums[rank], threadIdx.x)), "f"(a), "f"(b),
+                     "f"(c), "f"(0.f)
+                     : "memory");
     }
 }
-__device__ __forceinline__ float2 total_sums(const SmallShared& sh, int cluster) {
-    float2 t = make_float2(0.f, 0.f);
+__device__ __forceinline__ float3 total_sums(const SmallShared& sh, int cluster) {
+    float3 t = make_float3(0.f, 0.f, 0.f);
     for (int i = 0; i < cluster; ++i) {
         t.x += sh.sums[i].x;
         t.y += sh.sums[i].y;
+        t.z += sh.sums[i].z;
     }
     return t;
 }
@@ -1252,7 +1286,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
     };
 
     // u into tensor memory, with the momentum step, and the sums of its squares
-    float s = 0.f, s2 = 0.f;
+    float s = 0.f, s2 = 0.f, s3 = 0.f;
     if (rows)
         for (int ch = half; ch < 2 * nb; ch += 2) {
             uint32_t v[32];
@@ -1279,19 +1313,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                s = fmaf(u[e], u[e], s);
-                const float t = u[e] * kDown;
-                s2 = fmaf(t, t, s2);
+                add_squares(u[e], s, s2, s3);
                 v[e] = __float_as_uint(u[e]);
             }
             tmem_st32(tm + 32 * ch, v);
         }
     tmem_st_wait();
     cluster_sync();  // every CTA of the cluster has begun
-    share_sums(sh, s, s2, rank, Q);
+    share_sums(sh, s, s2, s3, rank, Q);
     cluster_sync();
-    const float2 uu = total_sums(sh, Q);
-    const float pre = isinf(uu.x) ? kDown : 1.f, nrm = sqrtf(isinf(uu.x) ? uu.y : uu.x), inv = M.tau / (nrm + J.eps * pre);
+    const float3 uu = total_sums(sh, Q);
+    const int which = which_sum(uu.x, J.eps);
+    float pre, inv;
+    scale_of(which, which == 1 ? uu.y : which == 2 ? uu.z : uu.x, J.eps, M.tau, pre, inv);
     if (rows)
         for (int ch = half; ch < 2 * nb; ch += 2) {
             uint32_t v[32];
@@ -1652,7 +1686,7 @@ size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
         M.ad = reinterpret_cast<__half*>(take(ab));
         M.bp = reinterpret_cast<__half*>(take(ab));
         M.d = reinterpret_cast<float*>(take((size_t)M.mt * (M.mt + 1) / 2 * kTileF * sizeof(float)));
-        M.norm = reinterpret_cast<float*>(take(2 * kNormChunks * sizeof(float)));
+        M.norm = reinterpret_cast<float*>(take(3 * kNormChunks * sizeof(float)));
     }
     int half;
     *part = reinterpret_cast<float*>(take(gram_share(mats, count, pair, &half) ? 2 * kPlanSms * (pair ? 2 : 1) * kTileF * sizeof(float) : 0));

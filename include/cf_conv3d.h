@@ -398,16 +398,17 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
  * rows x cols and writes, for each, the Newton-Schulz iterate that drives its
  * singular values towards 1: with X the matrix (transposed when rows > cols),
  *   X = u / (|u|_F + eps);  `steps` times: A = X X^T, X = a X + (b A + c A A) X
- * a polynomial of the singular values, so a zero matrix gives zero.  The usual
- * coefficients are (3.4445, -4.7750, 2.0315) with 5 steps: values in about
- * [0.7, 1.2].
+ * a polynomial of the singular values; a zero matrix gives zero, with eps 0 too.
+ * The usual coefficients are (3.4445, -4.7750, 2.0315) with 5 steps: values in
+ * about [0.7, 1.2].
  *   g : [batch][rows][cols] bf16 or fp32 (dtype), o : [batch][rows][cols] bf16.
  * Products take fp16 operands (11 bits) with fp32 sums (matrices of at most 32
  * rows: fp32 throughout), X is carried between steps to 2^-20 of its values,
  * and what the diagonals of A and of the polynomial share is kept out of the
  * rounding: |o - exact| is about 1e-3 |exact| in the Frobenius norm before the
- * rounding to bf16.  A matrix with an entry that is not finite
- * gives NaN throughout.
+ * rounding to bf16 (and 1e-6 where |u|_F is far below eps).  The norm is taken
+ * without overflow or underflow for any finite u and any eps >= 0.  A matrix
+ * with an entry that is not finite gives NaN throughout.
  * Supported: 1 <= steps <= 16; rows, cols up to 65536; as many matrices as the
  * host can list (beyond: CF_ERR_UNSUPPORTED).
  *

@@ -348,3 +348,45 @@ def test_muon_workspace_that_starts_at_any_16_bytes(cf):
         got.append(w + m)
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+# a shape for each way that a matrix goes: one CTA, a cluster of one and of several CTAs, the whole GPU, pairs of CTAs
+WAYS = [(20, 50), (60, 100), (100, 1200), (200, 400), (2048, 2600)]
+
+
+@pytest.mark.parametrize("rows,cols", WAYS)
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-7, 4.0])
+def test_values_whose_squares_underflow_or_overflow(cf, oracle_mod, rows, cols, eps):
+    """The norm of values down to fp32's smallest normal ones and up to 1e30, and of zeros, beside an eps of any size.  Where eps is
+    by far the larger, X is near 0 and its values are held to 2^-33 / tau, sqrt(k n) / tau being 4 to 8: over the steps, each of
+    which passes that on with at most 3.45, sqrt(5) 8 3.45^5 2^-33 = 1e-6 in the Frobenius norm."""
+    rng = np.random.default_rng(rows)
+    base = rng.normal(size=(rows, cols))
+    eps = float(np.float32(eps))
+    scales = [1e-37, 1e-25, 1e-16, 1e30] if rows < 1000 else [1e-25]
+    g = np.stack([np.zeros((rows, cols))] + [base * s for s in scales])
+    o, g = _orth(cf, g, "f32", eps=eps)
+    assert np.all(o[0] == 0)
+    for i in range(1, len(g)):
+        ref = oracle_mod.newton_schulz(g[i], eps=eps)
+        assert np.linalg.norm(o[i] - ref) <= OUT_TOL * np.linalg.norm(ref) + 1e-6, scales[i - 1]
+
+
+@pytest.mark.parametrize("rows,cols", WAYS[:-1])
+def test_muon_step_of_tiny_and_zero_momenta(cf, oracle_mod, rows, cols):
+    import torch
+    rng = np.random.default_rng(cols)
+    m0 = [np.zeros((rows, cols)), rng.normal(size=(rows, cols)) * 1e-26]
+    w = [torch.zeros((rows, cols), device="cuda") for _ in m0]
+    m = [torch.from_numpy(v.astype(np.float32)).cuda() for v in m0]
+    g = [torch.zeros((rows, cols), device="cuda") for _ in m0]
+    params = cf.cf_muon_params([(a, None, b, c, 1.0) for a, b, c in zip(w, g, m)])
+    size = cf.cf_muon_workspace_size(params)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    m64 = _f64(m[1])
+    cf.cf_muon_step(params, cf.cf_muon_hyper(1.0, 0.5, 0.0, 0, 5, 3.4445, -4.7750, 2.0315, 0.0), ws, size)
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+    assert bool((w[0] == 0).all()) and bool((m[0] == 0).all())
+    ref = oracle_mod.newton_schulz(0.5 * m64, eps=0.0)
+    assert np.linalg.norm(_f64(w[1]) + ref) <= NS_TOL * np.linalg.norm(ref)
