@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -1778,6 +1779,47 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
     return CF_OK;
 }
 
+// The cooperative launch.
+struct Coop {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[2];
+    Coop(const LaunchCtx& ctx, bool pair) {
+        cfg.gridDim = dim3((unsigned)(pair ? ctx.num_sms / 2 * 2 : ctx.num_sms));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cfg.stream = ctx.stream;
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = 2;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = pair ? 2 : 1;
+    }
+    Coop(const Coop&) = delete;
+};
+
+// Whether the device holds all of the cooperative launch's blocks at once, asked once for each device: a call that finds out at the
+// launch has taken its momentum steps by then.
+bool coop_fits(const LaunchCtx& ctx, bool pair) {
+    constexpr int kDevices = 64;
+    static std::atomic<int8_t> known[2][kDevices];  // 0: not asked, 1: fits, -1: does not
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
+    int8_t k = known[pair][dev].load(std::memory_order_relaxed);
+    if (k == 0) {
+        int have = 0;
+        Coop coop(ctx, pair);
+        const cudaError_t e =
+            pair ? cudaOccupancyMaxActiveClusters(&have, ns_kernel<true>, &coop.cfg)
+                 : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&have, ns_kernel<false>, kThreads, kSmem);
+        if (e != cudaSuccess) return false;
+        k = have >= (pair ? ctx.num_sms / 2 : 1) ? 1 : -1;
+        known[pair][dev].store(k, std::memory_order_relaxed);
+    }
+    return k > 0;
+}
+
 // uniform: the matrices are of one batch, a matrix apart.
 cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws, bool uniform) {
     if (const int cluster = cluster_of(mats))
@@ -1785,6 +1827,8 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
     if (cudaFuncSetAttribute(ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
         return CF_ERR_CUDA;
+    for (size_t b = 0; b < mats.size(); b += kMaxMats)
+        if (!coop_fits(ctx, plan_sizes(&mats[b], (int)std::min<size_t>(kMaxMats, mats.size() - b)))) return CF_ERR_CUDA;
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         Job J{};
         J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
@@ -1823,20 +1867,8 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         cfg.attrs = at;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, ns_convert_kernel, J) != cudaSuccess) return CF_ERR_CUDA;
-        cudaLaunchConfig_t coop{};
-        coop.gridDim = dim3((unsigned)(pair ? ctx.num_sms / 2 * 2 : ctx.num_sms));
-        coop.blockDim = dim3(kThreads);
-        coop.dynamicSmemBytes = kSmem;
-        coop.stream = ctx.stream;
-        cudaLaunchAttribute ca[2];
-        ca[0].id = cudaLaunchAttributeCooperative;
-        ca[0].val.cooperative = 1;
-        ca[1].id = cudaLaunchAttributeClusterDimension;
-        ca[1].val.clusterDim.x = 2;
-        ca[1].val.clusterDim.y = ca[1].val.clusterDim.z = 1;
-        coop.attrs = ca;
-        coop.numAttrs = pair ? 2 : 1;
-        if (cudaLaunchKernelEx(&coop, pair ? ns_kernel<true> : ns_kernel<false>, J) != cudaSuccess) return CF_ERR_CUDA;
+        Coop coop(ctx, pair);
+        if (cudaLaunchKernelEx(&coop.cfg, pair ? ns_kernel<true> : ns_kernel<false>, J) != cudaSuccess) return CF_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
 }

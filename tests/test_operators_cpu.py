@@ -1,10 +1,17 @@
 """Pins of the 64-bit group norm, Newton-Schulz and momentum step that the GPU tests compare with, and the refusals of their
 entry points (no GPU needed).  Each pin compares with something else: closed forms, invariances, finite differences, the
 singular values."""
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 
 import oracle
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _case(seed, shape, groups):
@@ -208,3 +215,61 @@ def test_group_norm_refuses_more_blocks_than_a_launch_has(cf):
     # as much as a device holds
     assert cf.cf_group_norm_workspace_size(_gn(cf, n=65535, d=128, h=128, w=128, c=1, groups=1), 1) > 0
     assert cf.cf_group_norm_workspace_size(_gn(cf, n=4096, d=1, h=1, w=1, c=8192, groups=32), 0) > 0
+
+
+# ------------------------------------------------------------------------------------------------- launches that fail, by a fake runtime
+# Stands in for the CUDA runtime's calls, with no GPU: counts launches, fails the one of a given number, and says how many blocks
+# a device holds at once.
+FAKE_RUNTIME = """
+static int launches, fail_at, fit = 1, last;
+int fake_launches(void) { return launches; }
+void fake_set(int f, int at) { fit = f; fail_at = at; launches = 0; }
+static int launch(void) { return ++launches == fail_at ? (last = 98) : 0; }
+int cudaGetDevice(int* d) { *d = 0; return 0; }
+int cudaDeviceGetAttribute(int* v, int a, int d) { *v = 152; return 0; }
+int cudaGetSymbolAddress(void** p, const void* s) { static int word; *p = &word; return 0; }
+int cudaGetDriverEntryPointByVersion(const char* s, void** fn, unsigned v, unsigned long long f, int* q) { *fn = (void*)1; *q = 0; return 0; }
+int cudaFuncSetAttribute(const void* f, int a, int v) { return 0; }
+int cudaGetLastError(void) { int e = last; last = 0; return e; }
+int cudaLaunchKernelExC(const void* c, const void* f, void** a) { return launch(); }
+int __cudaLaunchKernel() { return launch(); }
+int __cudaGetKernel(void** k, const void* f) { *k = (void*)f; return 0; }
+unsigned __cudaPushCallConfiguration() { return 0; }
+int __cudaPopCallConfiguration() { return 0; }
+int cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int* n, const void* f, int t, unsigned long s, unsigned g) { *n = fit; return 0; }
+int cudaOccupancyMaxActiveClusters(int* n, const void* f, const void* c) { *n = 76 * fit; return 0; }
+"""
+
+
+def _with_fake_runtime(tmp_path, script):
+    """Runs the script with `cf` (the binding) and `fake` (the fake runtime's controls); returns what it prints."""
+    from cnn_conv3d_gb300 import build
+    build.build()
+    src, lib = tmp_path / "fake.c", tmp_path / "fake.so"
+    src.write_text(FAKE_RUNTIME)
+    subprocess.run(["gcc", "-w", "-shared", "-fPIC", "-o", str(lib), str(src)], check=True)
+    head = f"import ctypes, sys\nsys.path.insert(0, {ROOT!r})\nfake = ctypes.CDLL({str(lib)!r})\nfrom cnn_conv3d_gb300 import cfconv as cf\n"
+    r = subprocess.run([sys.executable, "-c", head + textwrap.dedent(script)], capture_output=True, text=True, timeout=120,
+                       env=dict(os.environ, LD_PRELOAD=str(lib)))
+    assert r.returncode == 0, r.stderr[-2000:]
+    return r.stdout.split()
+
+
+# 200 x 400 on single CTAs, 2048 x 2600 on pairs, the two in one list
+MUON_CALL = """
+def muon(shapes):
+    params = (cf.cf_muon_param * len(shapes))()
+    for p, (p.rows, p.cols) in zip(params, shapes):
+        p.w, p.g, p.m, p.scale = 512, 1024, 2048, 1.0
+    hyper = cf.cf_muon_hyper(1e-3, 0.9, 0.0, 1, 5, 3.4, -4.7, 2.0, 1e-7)
+    return cf.cf_muon_step(params, hyper, 4096, cf.cf_muon_workspace_size(params), check=False)
+"""
+
+
+@pytest.mark.parametrize("shapes,launches", [([(200, 400)], 3), ([(2048, 2600)], 3), ([(200, 400)] * 50 + [(2048, 2600)], 6), ([(16, 108)], 1)])
+def test_muon_step_enqueues_all_or_nothing(tmp_path, shapes, launches):
+    """On a device that does not hold the cooperative launch nothing is enqueued: no momentum without its update."""
+    call = MUON_CALL + f"fake.fake_set(%d, 0)\nprint(muon({shapes!r}), fake.fake_launches())"
+    assert _with_fake_runtime(tmp_path, call % 1) == ["0", str(launches)]
+    if launches > 1:
+        assert _with_fake_runtime(tmp_path, call % 0) == ["4", "0"]
