@@ -1737,6 +1737,12 @@ size_t workspace_of(std::vector<Mat>& mats) {
     return most;
 }
 
+// The runtime's error is taken with its report: the next call is not to find it.
+cf_status cuda_error() {
+    cudaGetLastError();
+    return CF_ERR_CUDA;
+}
+
 template <int N>
 cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, int cluster, bool uniform) {
     const int tiny = tiny_of(mats);
@@ -1745,7 +1751,7 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
     const size_t most = tiny == 16 ? Tiny<16>::smem(Tiny<16>::kCols) : tiny == 32 ? Tiny<32>::smem(Tiny<32>::kCols) : kMaxShared;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
         (cluster > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
-        return CF_ERR_CUDA;
+        return cuda_error();
     const size_t each = uniform ? mats.size() : N;
     for (size_t b = 0; b < mats.size(); b += each) {
         SmallJob<N> J{};
@@ -1774,7 +1780,7 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, kernel, J) != cudaSuccess) return CF_ERR_CUDA;
+        if (cudaLaunchKernelEx(&cfg, kernel, J) != cudaSuccess) return cuda_error();
     }
     return CF_OK;
 }
@@ -1826,9 +1832,9 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         return (uniform || mats.size() == 1 ? run_small<1> : run_small<kMaxMats>)(ctx, p, mu, nesterov, mats, cluster, uniform);
     if (cudaFuncSetAttribute(ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
-        return CF_ERR_CUDA;
+        return cuda_error();
     for (size_t b = 0; b < mats.size(); b += kMaxMats)
-        if (!coop_fits(ctx, plan_sizes(&mats[b], (int)std::min<size_t>(kMaxMats, mats.size() - b)))) return CF_ERR_CUDA;
+        if (!coop_fits(ctx, plan_sizes(&mats[b], (int)std::min<size_t>(kMaxMats, mats.size() - b)))) return cuda_error();
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         Job J{};
         J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
@@ -1856,21 +1862,22 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         J.sync = static_cast<uint32_t*>(ws);
         J.status = ctx.status;
         J.wait_ns = ctx.wait_ns;
-        ns_input_kernel<<<J.nn, 256, 0, ctx.stream>>>(J);
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)J.nc);
+        cfg.gridDim = dim3((unsigned)J.nn);
         cfg.blockDim = dim3(256);
         cfg.stream = ctx.stream;
+        if (cudaLaunchKernelEx(&cfg, ns_input_kernel, J) != cudaSuccess) return cuda_error();
+        cfg.gridDim = dim3((unsigned)J.nc);
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, ns_convert_kernel, J) != cudaSuccess) return CF_ERR_CUDA;
+        if (cudaLaunchKernelEx(&cfg, ns_convert_kernel, J) != cudaSuccess) return cuda_error();
         Coop coop(ctx, pair);
-        if (cudaLaunchKernelEx(&coop.cfg, pair ? ns_kernel<true> : ns_kernel<false>, J) != cudaSuccess) return CF_ERR_CUDA;
+        if (cudaLaunchKernelEx(&coop.cfg, pair ? ns_kernel<true> : ns_kernel<false>, J) != cudaSuccess) return cuda_error();
     }
-    return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA;
+    return CF_OK;
 }
 
 std::vector<Mat> batch_of(const cf_ns_desc* d, const void* g, uint16_t* o) {

@@ -273,3 +273,17 @@ def test_muon_step_enqueues_all_or_nothing(tmp_path, shapes, launches):
     assert _with_fake_runtime(tmp_path, call % 1) == ["0", str(launches)]
     if launches > 1:
         assert _with_fake_runtime(tmp_path, call % 0) == ["4", "0"]
+
+
+@pytest.mark.parametrize("shape,at", [((16, 108), 1), ((64, 864), 1), ((200, 400), 1), ((200, 400), 2), ((200, 400), 3), ((2048, 2600), 3)])
+def test_a_launch_that_fails_is_reported_once(tmp_path, shape, at):
+    """The call says CF_ERR_CUDA and enqueues nothing more, and the error is not left behind for the next one to report as its own."""
+    call = MUON_CALL + f"""
+gn = cf.cf_gn_desc(1, 4, 4, 4, 8, 2, cf.CF_POOL_NONE, cf.CF_ACT_LRELU, 0.3, 1e-5, cf.CF_DT_BF16, 0, 0)
+fake.fake_set(1, {at})
+print(muon([{shape!r}]), fake.fake_launches())
+fake.fake_set(1, 0)
+print(cf.cf_group_norm_fwd(gn, 16, None, None, 32, None, None, 256, 1 << 20, check=False))
+print(muon([{shape!r}]))
+"""
+    assert _with_fake_runtime(tmp_path, call) == ["4", str(at), "0", "0"]
