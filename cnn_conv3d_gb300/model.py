@@ -117,13 +117,18 @@ class CosmoFlowModel:
         return [(self.w32[l], st.w[l], st.dw[l]) for l in range(st.L)] + \
             [(self.fw[i], None, self.dfw[i]) for i in range(len(self.fw) - 1)]
 
+    def _on(self, stream):
+        """Torch's own work of a first step (the optimizer's zeroed state) in the order of the step's stream."""
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
+
     def _muon_update(self, lr, momentum, weight_decay, stream):
         if self._muon is None:
-            ms = [torch.zeros_like(p) for p, _, _ in self.matrices()]
-            params = cf.cf_muon_params([(p, p16, g, m, 0.2 * max(p.shape[0], p.numel() // p.shape[0]) ** 0.5)
-                                        for (p, p16, g), m in zip(self.matrices(), ms)])
-            size = cf.cf_muon_workspace_size(params)
-            self._muon = (ms, params, torch.empty((max(size, 16),), dtype=torch.uint8, device=self.device), size)
+            with self._on(stream):
+                ms = [torch.zeros_like(p) for p, _, _ in self.matrices()]
+                params = cf.cf_muon_params([(p, p16, g, m, 0.2 * max(p.shape[0], p.numel() // p.shape[0]) ** 0.5)
+                                            for (p, p16, g), m in zip(self.matrices(), ms)])
+                size = cf.cf_muon_workspace_size(params)
+                self._muon = (ms, params, torch.empty((max(size, 16),), dtype=torch.uint8, device=self.device), size)
         _, params, ws, size = self._muon
         hyper = cf.cf_muon_hyper(lr, momentum, weight_decay, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
         cf.cf_muon_step(params, hyper, ws, size, stream)
@@ -138,7 +143,8 @@ class CosmoFlowModel:
             taken = {p.data_ptr() for p, _, _ in self.matrices()}
             ps = [t for t in ps if t[0].data_ptr() not in taken]
         if self._adam is None:
-            self._adam = [(torch.zeros_like(p), torch.zeros_like(p)) for p, _, _ in ps]
+            with self._on(s):
+                self._adam = [(torch.zeros_like(p), torch.zeros_like(p)) for p, _, _ in ps]
         self.t += 1
         for (p, p16, g), (m, v) in zip(ps, self._adam):
             cf.cf_adam_step(p.numel(), p, p16, g, m, v, lr, beta1, beta2, eps, self.t, s)

@@ -159,3 +159,30 @@ def test_unknown_optimizer_is_refused(torch_cuda):
     from cnn_conv3d_gb300.model import CosmoFlowModel
     with pytest.raises(ValueError):
         CosmoFlowModel(1, 32, CHANNELS, specs=SPECS, optimizer="sgd")
+
+
+@pytest.mark.parametrize("optimizer", ["muon", "adam"])
+@pytest.mark.parametrize("handle", [False, True])
+def test_first_step_on_a_stream_of_its_own(torch_cuda, optimizer, handle):
+    """The optimizer's state is zeroed in the order of the stream that the step is enqueued on, whatever another stream is busy with."""
+    torch = torch_cuda
+    from cnn_conv3d_gb300 import cfconv as cf
+    runs = []
+    for own in (False, True):
+        m = _model(torch, optimizer, seed=75)
+        m.forward()
+        m.backward()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream() if own else torch.cuda.current_stream()
+        if own:
+            # memory that is handed out again does not hold zeros
+            junk = [torch.full_like(p, 3.0) for p, _, _ in m.params() for _ in range(2)]
+            torch.cuda.synchronize()
+            del junk
+            torch.cuda._sleep(100_000_000)  # the current stream is busy for some 50 ms
+        for _ in range(2):
+            m.update(1e-3, stream=s.cuda_stream if handle and own else s, weight_decay=0.1)
+        torch.cuda.synchronize()
+        assert cf.cf_last_device_status() == cf.CF_OK
+        runs.append([p.clone() for p, _, _ in m.params()])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
