@@ -390,3 +390,41 @@ def test_muon_step_of_tiny_and_zero_momenta(cf, oracle_mod, rows, cols):
     assert bool((w[0] == 0).all()) and bool((m[0] == 0).all())
     ref = oracle_mod.newton_schulz(0.5 * m64, eps=0.0)
     assert np.linalg.norm(_f64(w[1]) + ref) <= NS_TOL * np.linalg.norm(ref)
+
+
+def _precise(cf, shapes, kind, seed):
+    """Orthogonalised matrices as fp32, as the step from weights of zero writes them, and the matrices."""
+    import torch
+    rng = np.random.default_rng(seed)
+    g = [torch.from_numpy(_matrix(rng, s, kind).astype(np.float32)).cuda() for s in shapes]
+    w, m = [torch.zeros_like(t) for t in g], [torch.zeros_like(t) for t in g]
+    params = cf.cf_muon_params([(a, None, b, c, 1.0) for a, b, c in zip(w, g, m)])
+    size = cf.cf_muon_workspace_size(params)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    cf.cf_muon_step(params, cf.cf_muon_hyper(1.0, 0.0, 0.0, 0, 5, 3.4445, -4.7750, 2.0315, 1e-7), ws, size)
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+    return [-_f64(t) for t in w], [_f64(t) for t in g]
+
+
+# The stated precision.  fp16 operands and X to 2^-20: the roundings simulated in 64 bits give 4e-4 to 1.3e-3 over such shapes and
+# kinds of matrices, and 5e-3 to 2e-2 for the third kind where X is carried as its operand alone; half as much again, 2e-3.  fp32
+# throughout: roundings of sums of up to 1408 terms, at most about 2^-19 each, sqrt(3 * 5) * 3.45 * 2^-19 = 2.6e-5 as above, with
+# room for the early steps' that several steps pass on, 1e-4.
+@pytest.mark.parametrize("shape,tol", [((16, 108), 1e-4), ((20, 50), 1e-4), ((1408, 16), 1e-4), ((32, 512), 1e-4), ((32, 513), 2e-3),
+                                       ((64, 864), 2e-3), ((128, 432), 2e-3), ((100, 1200), 2e-3), ((130, 300), 2e-3), ((515, 1511), 2e-3),
+                                       ((2000, 300), 2e-3), ((2048, 2600), 2e-3)])
+@pytest.mark.parametrize("kind", ["normal", "directions", "decay"])
+def test_precision(cf, oracle_mod, shape, tol, kind):
+    (o,), (g,) = _precise(cf, [shape], kind, shape[0] + shape[1])
+    ref = oracle_mod.newton_schulz(g)
+    assert np.linalg.norm(o - ref) <= tol * np.linalg.norm(ref), np.linalg.norm(o - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("shapes,tol", [([(16, 108), (12, 1400)], 1e-4), ([(16, 108), (31, 40), (512, 30)], 1e-4), ([(16, 108), (17, 600)], 2e-3),
+                                        ([(16, 108), (300, 200)], 2e-3)])
+def test_precision_of_a_list(cf, oracle_mod, shapes, tol):
+    """A list is taken as a whole: its largest matrix says how."""
+    for o, g in zip(*_precise(cf, shapes, "directions", len(shapes))):
+        ref = oracle_mod.newton_schulz(g)
+        assert np.linalg.norm(o - ref) <= tol * np.linalg.norm(ref), (o.shape, np.linalg.norm(o - ref) / np.linalg.norm(ref))
