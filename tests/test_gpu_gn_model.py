@@ -186,3 +186,46 @@ def test_first_step_on_a_stream_of_its_own(torch_cuda, optimizer, handle):
         assert cf.cf_last_device_status() == cf.CF_OK
         runs.append([p.clone() for p, _, _ in m.params()])
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_steps_from_host_buffers_give_the_same_bits(torch_cuda):
+    """step_host and step_host_pipelined over group-normalised blocks, and step_host as a CUDA graph, against load + step."""
+    torch = torch_cuda
+    from cnn_conv3d_gb300 import cfconv as cf
+    from cnn_conv3d_gb300.stack import CosmoStack
+    n, spatial = 3, 32
+    inp = synthdata.stack_inputs(n, spatial, CHANNELS, seed=76, with_dy=False)
+    st = CosmoStack(n, spatial, CHANNELS, SLOPE, specs=SPECS)
+    st.load(inp["x"], inp["w"], inp["b"])
+    gen = torch.Generator(device="cuda").manual_seed(76)
+    dy = torch.randn(st.y[-1].shape, device="cuda", generator=gen).to(torch.bfloat16)
+    st.step(dy)
+    torch.cuda.synchronize()
+    outputs, want_dev = st.y + st.dgamma, [t.clone() for t in st.y + st.dgamma]
+    want = [t.cpu() for t in st.dw + st.db]
+    x_host, dy_host = st.x.cpu().pin_memory(), dy.cpu().pin_memory()
+    dw_host, db_host = ([torch.empty(t.shape, dtype=t.dtype).pin_memory() for t in ts] for ts in (st.dw, st.db))
+
+    def clear():
+        torch.cuda.synchronize()
+        for t in [st.x] + outputs + st.dw + st.db + dw_host + db_host:
+            t.fill_(9.0)
+        torch.cuda.synchronize()
+
+    def check():
+        torch.cuda.synchronize()
+        assert cf.cf_last_device_status() == cf.CF_OK
+        assert all(torch.equal(a, b) for a, b in zip(want, dw_host + db_host))
+        assert all(torch.equal(a, b) for a, b in zip(want_dev, outputs))
+
+    clear()
+    st.step_host(x_host, dy_host, dw_host, db_host, chunks=2)
+    check()
+    graph = st.capture(None, host=(x_host, dy_host, dw_host, db_host))
+    clear()
+    graph.replay()
+    check()
+    clear()
+    st.prefetch_host(x_host, dy_host)
+    st.step_host_pipelined(x_host, dy_host, dw_host, db_host)
+    check()

@@ -437,3 +437,133 @@ def test_clusters_whose_blocks_have_no_rows(cf, oracle_mod, shape, pool):
         got = (y, mean, rstd) + _run_bwd(cf, shape, 1, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta, mean, rstd, dy)
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def _windows(t):
+    n, d, h, w, c = t.shape
+    return t.reshape(n, d // 2, 2, h // 2, 2, w // 2, 2, c).permute(0, 1, 3, 5, 2, 4, 6, 7).reshape(n, d // 2, h // 2, w // 2, 8, c)
+
+
+def _unwindows(t):
+    n, d, h, w, _, c = t.shape
+    return t.reshape(n, d, h, w, 2, 2, 2, c).permute(0, 1, 4, 2, 5, 3, 6, 7).reshape(n, 2 * d, 2 * h, 2 * w, c)
+
+
+# more rows than one wave of blocks has in chunks of their longest: 75 million values in eights (forward and backward: two waves),
+# 21 million one by one (three), 43 million in fours
+@pytest.mark.parametrize("shape,groups", [((2, 128, 96, 96, 32), 8), ((3, 96, 82, 70, 13), 13), ((2, 128, 96, 88, 20), 4)])
+@pytest.mark.parametrize("pool,act", [("none", "silu"), ("max", "lrelu"), ("avg", "silu")])
+def test_several_waves_of_chunks(cf, shape, groups, pool, act):
+    """Against the same formulas in 64 bits on the GPU, with the tolerances of the small shapes."""
+    import torch
+    n, c, per, eps = shape[0], shape[-1], shape[-1] // groups, 1e-5
+    x, gamma, beta, dy = _inputs(shape, pool, "bf16", 51)
+    y, mean, rstd = _run_fwd(cf, shape, groups, pool, act, 0.3, eps, "bf16", x, gamma, beta)
+    X, G, B = x.double(), gamma.double(), beta.double()
+    grouped = X.reshape(n, -1, groups, per)
+
+    def wide(t):
+        return t.repeat_interleave(per, 1)[:, None, None, None, :]
+
+    rm = grouped.mean((1, 3))
+    rr = ((grouped - rm[:, None, :, None]) ** 2).mean((1, 3)).add(eps).rsqrt()
+    mabs = grouped.abs().mean((1, 3))
+    assert bool(((mean - rm).abs() <= 2.0 ** -17 * mabs).all())
+    assert bool(((rstd - rr).abs() <= rr * (2.0 ** -17 + (2.0 ** -17 * mabs * rr) ** 2)).all())
+    xh = (X - wide(rm)) * wide(rr)
+    u = G * xh + B
+    ue = 2.0 ** -16 * (G.abs() * wide(rr) * (X.abs() + wide(rm).abs()) + B.abs())
+    act_of = torch.nn.functional.silu if act == "silu" else lambda t: torch.where(t > 0, t, 0.3 * t)
+    if pool == "max":
+        ref = act_of(_windows(u).amax(4))
+    else:
+        ref = act_of(u) if pool == "none" else _windows(act_of(u)).mean(4)
+    tol = 2.0 ** -8 * ref.abs() + 1.1 * (_windows(ue).amax(4) if pool != "none" else ue)
+    assert bool(((y.double() - ref).abs() <= tol).all())
+    del y, ref, tol, ue
+    if pool == "max":  # its gradient may go to either of two voxels that are equal within rounding: small shapes look at that
+        return
+    sm, sr = rm.float(), rr.float()
+    dx, dgamma, dbeta = _run_bwd(cf, shape, groups, pool, act, 0.3, eps, "bf16", x, gamma, beta, sm, sr, dy)
+    xh = (X - wide(sm.double())) * wide(sr.double())
+    u = G * xh + B
+    s = torch.sigmoid(u)
+    full = dy.double() if pool == "none" else _unwindows((dy.double() / 8)[..., None, :].expand(*dy.shape[:4], 8, c))
+    du = full * s * (1 + u * (1 - s))
+    del u, s, full
+
+    def gm(t):
+        return wide(t.reshape(n, -1, groups, per).mean((1, 3)))
+
+    axes = (0, 1, 2, 3)
+    assert bool(((dbeta - du.sum(axes)).abs() <= 2.0 ** -15 * du.abs().sum(axes)).all())
+    assert bool(((dgamma - (du * xh).sum(axes)).abs() <= 2.0 ** -15 * ((du * xh).abs() + du.abs()).sum(axes)).all())
+    r = wide(sr.double())
+    ref = r * (G * du - gm(G * du) - xh * gm(G * du * xh))
+    parts = r * ((G * du).abs() + gm((G * du).abs()) + xh.abs() * gm((G * du * xh).abs())) * (1 + wide(sm.double()).abs() * r)
+    assert bool(((dx.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -14 * parts).all())
+
+
+@pytest.mark.parametrize("pool,dtype", [("none", "bf16"), ("none", "f32"), ("max", "bf16"), ("avg", "bf16")])
+@pytest.mark.parametrize("shape", [(2, 6, 4, 10, 24), (1, 48, 40, 36, 48)])
+def test_slices_that_begin_inside_a_wider_tensor(cf, shape, pool, dtype):
+    """Channels 16 .. 16 + c - 1 of 128, x and dx, and 8 .. of 80, y and dy, have the bits of tensors of their own, and the channels
+    beside them stay as they are."""
+    import torch
+    act, c, groups, xp, yp = "lrelu" if pool == "max" else "silu", shape[-1], 4, 128, 80
+    x, gamma, beta, dy = _inputs(shape, pool, dtype, 52)
+    y, mean, rstd = _run_fwd(cf, shape, groups, pool, act, 0.3, 1e-5, dtype, x, gamma, beta)
+    dx, dgamma, dbeta = _run_bwd(cf, shape, groups, pool, act, 0.3, 1e-5, dtype, x, gamma, beta, mean, rstd, dy)
+    desc = _desc(cf, shape, groups, pool, act, 0.3, 1e-5, dtype, xp, yp)
+    ws = torch.empty(max(cf.cf_group_norm_workspace_size(desc, b) for b in (0, 1)), dtype=torch.uint8, device="cuda")
+
+    def inside(t, pitch, at):
+        buf = torch.full(t.shape[:-1] + (pitch,), 7.0, dtype=t.dtype, device="cuda")
+        return buf, buf[..., at:at + c]
+
+    (_, xs), (yb, ys), (_, dys), (dxb, dxs) = inside(x, xp, 16), inside(y, yp, 8), inside(dy, yp, 8), inside(x, xp, 16)
+    xs.copy_(x)
+    dys.copy_(dy)
+    m2, r2, dg2, db2 = (torch.empty_like(t) for t in (mean, rstd, dgamma, dbeta))
+    cf.cf_group_norm_fwd(desc, xs, gamma, beta, ys, m2, r2, ws, ws.numel())
+    cf.cf_group_norm_bwd(desc, xs, gamma, beta, mean, rstd, dys, dxs, dg2, db2, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+    for a, b in ((y, ys), (mean, m2), (rstd, r2), (dx, dxs), (dgamma, dg2), (dbeta, db2)):
+        assert torch.equal(a, b)
+    for buf, at in ((yb, 8), (dxb, 16)):
+        assert bool((buf[..., :at] == 7).all()) and bool((buf[..., at + c:] == 7).all())
+
+
+@pytest.mark.parametrize("pool", ["none", "max", "avg"])
+def test_large_offsets_both_ways(cf, pool):
+    """The last of three samples, beyond 2^31 values, against the same sample alone: forward and backward.  The chunks of one sample
+    and of three differ, and with them the last bits of sums: 2^-14 of terms of which dx has at most about ten, beside its rounding."""
+    import torch
+    shape, groups, pitch = (3, 64, 64, 64, 8), 2, 3200
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough memory")
+    one = (1,) + shape[1:]
+    act = "lrelu" if pool == "max" else "silu"
+    x, gamma, beta, dy = _inputs(one, pool, "bf16", 53)
+    y, mean, rstd = _run_fwd(cf, one, groups, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta)
+    dx, dgamma, dbeta = _run_bwd(cf, one, groups, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta, mean, rstd, dy)
+    wide = torch.zeros(shape[:-1] + (pitch,), dtype=torch.bfloat16, device="cuda")
+    wide[2, ..., :8] = x[0]
+    desc = _desc(cf, shape, groups, pool, act, 0.3, 1e-5, "bf16", pitch, 0)
+    ws = torch.empty(max(cf.cf_group_norm_workspace_size(desc, b) for b in (0, 1)), dtype=torch.uint8, device="cuda")
+    y3 = torch.empty((3,) + y.shape[1:], dtype=torch.bfloat16, device="cuda")
+    cf.cf_group_norm_fwd(desc, wide, gamma, beta, y3, None, None, ws, ws.numel())
+    m3, r3, dy3 = (torch.zeros((3,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in (mean, rstd, dy))
+    m3[2], r3[2], dy3[2] = mean[0], rstd[0], dy[0]
+    dwide = torch.full_like(wide, 7.0)
+    dg3, db3 = torch.empty_like(dgamma), torch.empty_like(dbeta)
+    cf.cf_group_norm_bwd(desc, wide, gamma, beta, m3, r3, dy3, dwide, dg3, db3, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+    for a, b in ((y[0], y3[2]), (dx[0], dwide[2, ..., :8])):
+        assert bool(((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs() + 1e-3).all())
+    assert bool((dwide[..., 8:] == 7).all()) and bool((dwide[:2, ..., :8] == 0).all())
+    count = dy[..., 0].numel()
+    for a, b in ((dgamma, dg3), (dbeta, db3)):
+        assert bool(((a - b).abs() <= 2.0 ** -14 * count).all())

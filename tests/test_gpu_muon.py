@@ -428,3 +428,40 @@ def test_precision_of_a_list(cf, oracle_mod, shapes, tol):
     for o, g in zip(*_precise(cf, shapes, "directions", len(shapes))):
         ref = oracle_mod.newton_schulz(g)
         assert np.linalg.norm(o - ref) <= tol * np.linalg.norm(ref), (o.shape, np.linalg.norm(o - ref) / np.linalg.norm(ref))
+
+
+def test_more_matrices_than_a_launch_takes(cf, oracle_mod):
+    """A batch of 100 in three launches, whose workspaces follow one another; the same bits as a few of them alone."""
+    rng = np.random.default_rng(50)
+    g = np.stack([_matrix(rng, (130, 140), "directions") for _ in range(100)])
+    o, g = _orth(cf, g, "f32")
+    _check(oracle_mod, o, g)
+    few, _ = _orth(cf, g[46:50], "f32")
+    assert np.array_equal(few, o[46:50])
+
+
+MANY = {"one above 128 rows": [(20 + i, 30 + 2 * i) for i in range(59)] + [(150, 200)], "small": [(3 + i, 10 + 5 * i) for i in range(60)],
+        "tiny": [(1 + i % 16, 16 + i) for i in range(60)], "large last": [(140, 150)] * 48 + [(300, 500), (2, 7)]}
+
+
+@pytest.mark.parametrize("shapes", list(MANY.values()), ids=list(MANY))
+def test_muon_step_of_more_matrices_than_a_launch_takes(cf, oracle_mod, shapes):
+    test_muon_step(cf, oracle_mod, shapes, True, 0.01)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 130, 300), (2, 515, 1511), (1, 2048, 2600), (60, 130, 140)])
+def test_laid_out_workspace_too_small(cf, batch, rows, cols):
+    import torch
+    g = torch.zeros((batch, rows, cols), device="cuda")
+    o = torch.full((batch, rows, cols), 9.0, dtype=torch.bfloat16, device="cuda")
+    desc = cf.cf_ns_desc(batch, rows, cols, cf.CF_DT_F32, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    size = cf.cf_orthogonalize_workspace_size(desc)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert cf.cf_orthogonalize(desc, g, o, ws, size - 1, check=False) == cf.CF_ERR_WORKSPACE
+    entries = [tuple(torch.zeros((rows, cols), device="cuda") for _ in range(3)) for _ in range(batch)]
+    params = cf.cf_muon_params([(w, None, u, m, 1.0) for w, u, m in entries])
+    size = cf.cf_muon_workspace_size(params)
+    hyper = cf.cf_muon_hyper(0.01, 0.9, 0.0, 1, 5, 3.4445, -4.7750, 2.0315, 1e-7)
+    assert cf.cf_muon_step(params, hyper, ws, size - 1, check=False) == cf.CF_ERR_WORKSPACE
+    torch.cuda.synchronize()
+    assert bool((o == 9).all()) and cf.cf_last_device_status() == cf.CF_OK
