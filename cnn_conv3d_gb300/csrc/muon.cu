@@ -55,7 +55,7 @@ constexpr int kMostStages = 6;
 constexpr uint32_t kSmem = kRing + 1024;
 constexpr int kTileF = 128 * 128;         // floats of a Gram tile
 
-constexpr int kPlanSms = 152;             // SMs that work is planned for
+constexpr int kPlanSms = 152;             // SMs that work is planned for: workspaces are laid out without asking the device
 
 struct Mat {
     const void* g;
@@ -905,7 +905,7 @@ __device__ __forceinline__ void join_phase(const Job& J, int step) {
 
 // What bounds it.  On pairs, 2048 x 8192: of a step's 96 us G takes 25 and U 48, at 0.33 and 0.38 us for each 256 x 256 x 64 of a
 // pair where the tensor cores' measured burst rate allows 0.33; the rest is R 10, S 13 and four barriers of 2.5 each.  All five
-// steps and the input passes: 545 us, 1.02 PFLOP/s.  (U's loads come to 113 bytes a nanosecond and SM, of 138 that L2 was measured
+// steps and the input passes: 541 us, 1.03 PFLOP/s.  (U's loads come to 113 bytes a nanosecond and SM, of 138 that L2 was measured
 // to give.)  On single CTAs, small sizes: 300 x 2000 is 4.6 + 3.4 + 4.7 + 5.2 us a step, of which 2.5 each are the barrier and
 // most of the rest the latency of loads, products and epilogue one after the other; S's and U's tiles are as narrow as fills the SMs (at 128 and 256 columns 116 us in place of 91).
 // Waiting for a tile's parts in place of R and its barrier was slower (three of 515 x 1511, a step: 12.5 us for G and R against
@@ -1021,8 +1021,9 @@ template <int K>
 struct Tiny {
     static constexpr int kTiles = K / 4 * (K / 4 + 1) / 2, kLanes = K == 16 ? 32 : 16, kThreads = kTiles * kLanes;
     static constexpr int kLd = K + 4;                                  // a row of A and B in shared memory
-    // Columns, at most: beyond, the clusters below are faster (five steps, one matrix, here against there: 16 x 108 11 : 37 us,
-    // 16 x 1024 43 : 54, 16 x 1500 59 : 57, 32 x 108 20 : 37, 32 x 432 46 : 60, 32 x 768 72 : 49).
+    // Columns, at most.  A call here against the clusters below, which round to fp16: 16 x 108 12 : 29 us, 16 x 1024 42 : 39,
+    // 16 x 1408 53 : 38, 16 x 1500 57 : 41, 32 x 108 20 : 29, 32 x 432 45 : 37, 32 x 512 51 : 37, 32 x 768 71 : 37.  So the last third
+    // of these columns costs up to 15 us for results in fp32.
     static constexpr int kCols = K == 16 ? 1408 : 512;
     static constexpr size_t smem(int n) { return sizeof(float) * (2 * (size_t)K * ((n + 3) / 4 * 4 + 4) + 2 * K * kLd + 2 * 32); }
 };
@@ -1194,8 +1195,8 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
 // CTA on a slice of the columns.  X's slice is an operand in shared memory and, in fp32, an accumulator in tensor memory, onto
 // which U's product is added in place.  The Gram matrix's parts are exchanged through the CTAs' shared memory: each CTA sums
 // and rounds a slice of its columns for all, and A' A' and B' are then computed by every CTA for itself.
-// Latency bounds it: a step of 64 x 432 takes 10 us, of 128 x 128 10, one after the other three products with their ways in
-// and out of tensor memory and, in clusters, two exchanges.
+// Latency bounds it: a call of 64 x 432 takes 45 us and of 128 x 128 43, some 8 a step, one after the other three products with
+// their ways in and out of tensor memory and, in clusters, two exchanges.
 
 constexpr int kSmallThreads = 256;
 constexpr int kSmallRows = 128, kSmallCols = 384;  // of a CTA: 128 tensor memory columns are left to the Gram matrix
@@ -1565,11 +1566,10 @@ float cap_of(const Poly& p) {
     return (float)best;
 }
 
-// The workspace is laid out for this many CTAs: the sizes do not depend on the device.
 // Pairs of CTAs take a launch whose update products have this many tiles of 256 x 256, counted by their blocks of 64 contracted
-// values, or more: a pair loads less a product and waits longer at each step of its ring.  Five steps, single CTAs against pairs:
-// 2048 x 2048 (2048 blocks) 229 : 309 us, 1024 x 8192 (2048) 290 : 280, the seven convolutions' filters (2400) 482 : 512,
-// 2048 x 3000 (3072) 456 : 406, 1500 x 8192 (4608) 481 : 426, 2048 x 8192 (8192) 770 : 629.
+// values, or more: a pair loads less a product and waits longer at each step of its ring.  A whole call, single CTAs against pairs:
+// 2048 x 2048 (2048 blocks) 244 : 241 us, 1024 x 8192 (2048) 264 : 274, the seven convolutions' step (2400) 361 : 376,
+// 2048 x 3000 (3072) 307 : 303, 1500 x 8192 (4608) 410 : 382, 2048 x 8192 (8192) 589 : 545.
 constexpr int64_t kPairWork = 2700;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1696,8 +1696,9 @@ size_t place(Mat* mats, int count, bool pair, char* base, float** part) {
 
 // CTAs of a matrix in ns_small_kernel, 0 where it does not take the matrix: as many as leave a CTA about two blocks of 64 columns,
 // or four where there are more than 64 rows (the exchange then weighs as much), and one where it holds them all but for that.
-// Five steps, two blocks against four: 64 x 432 54 : 64 us, 128 x 256 73 : 65.  Long matrices go to ns_kernel, here against there:
-// 64 x 2000 68 : 98, 128 x 432 83 : 88, 128 x 1728 102 : 96, 128 x 3456 132 : 100.
+// A call, two blocks against four: 64 x 432 45 : 53 us, 64 x 2000 56 : 61, 128 x 432 71 : 72, 128 x 1024 85 : 88, 128 x 1536
+// 123 : 92.  Long matrices go to ns_kernel, here against there: 64 x 2000 56 : 88, 64 x 4096 67 : 94, 128 x 432 72 : 76,
+// 128 x 1024 88 : 86, 128 x 1536 92 : 96, 128 x 1728 94 : 91, 128 x 3456 132 : 92.
 int cluster_of(const Mat& M) {
     const int64_t k = std::min(M.rows, M.cols), n = std::max(M.rows, M.cols), cb = (n + 63) / 64, each = k > 64 ? 4 : 2;
     if (k > kSmallRows || n > (k > 64 ? 1536 : 4096)) return 0;
