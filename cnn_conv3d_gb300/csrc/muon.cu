@@ -2,7 +2,8 @@
 // momentum step that uses it, with their entry points.
 //
 // Of k x n values, k <= n, matrices of a call that all have at most 32 rows go to ns_tiny_kernel, all of at most 128 to
-// ns_small_kernel, each up to a length (tiny_of, cluster_of); the others take three launches for all of a call.  ns_input_kernel
+// ns_small_kernel, each up to a length (tiny_of, cluster_of); the others take three launches for all of a call, but for those of few
+// values, which ns_tiny_kernel takes out of any list (take_few).  ns_input_kernel
 // takes the momentum step and the Frobenius norms' partial sums, ns_convert_kernel writes X = u / (|u| + eps) in operand form, and
 // ns_kernel is one cooperative launch of a CTA per SM that runs the steps as phases between grid-wide barriers; a phase's
 // items (tiles of all matrices) are dealt out over the CTAs, or over pairs of them:
@@ -120,6 +121,9 @@ __device__ __forceinline__ void scale_of(int which, float sum, float eps, float 
     inv = den == 0.f ? 0.f : tau / den;
 }
 
+// A launch that is enqueued under the end of one of its list's small matrices, which it has nothing to do with, still ends after it.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float load_u(const Mat& M, const Job& J, int64_t i) {
     float u = M.f32 ? static_cast<const float*>(M.g)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(M.g)[i]);
     if (M.m) u = J.nesterov ? fmaf(J.mu, M.m[i], u) : M.m[i];
@@ -181,6 +185,7 @@ __global__ void __launch_bounds__(256) ns_input_kernel(const __grid_constant__ J
         M.norm[blockIdx.x - M.n0] = s;
         M.norm[kNormChunks + blockIdx.x - M.n0] = s2;
         M.norm[2 * kNormChunks + blockIdx.x - M.n0] = s3;
+        after_previous();
     }
 }
 
@@ -1044,6 +1049,7 @@ __global__ void __launch_bounds__(Tiny<K>::kThreads) ns_tiny_kernel(const __grid
     float* red = B + K * T::kLd;
     // of the stored element e; the quotient by d is exact while e d < 2^32
     const uint32_t d = M.tall ? k : n, part = 0xFFFFFFFFu / d + 1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // for the rest of a list
     auto place = [&](uint32_t e) {
         const uint32_t q = part ? __umulhi(e, part) : e, r = e - q * d;
         return M.tall ? r * ld + q : q * ld + r;
@@ -1528,6 +1534,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const __grid
         umma_commit(&sh.bar);
         mbar_wait_timed(&sh.bar, phase & 1, J.wait_ns);
     }
+    if (threadIdx.x == 0) after_previous();
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -1568,7 +1575,7 @@ float cap_of(const Poly& p) {
 
 // Pairs of CTAs take a launch whose update products have this many tiles of 256 x 256, counted by their blocks of 64 contracted
 // values, or more: a pair loads less a product and waits longer at each step of its ring.  A whole call, single CTAs against pairs:
-// 2048 x 2048 (2048 blocks) 244 : 241 us, 1024 x 8192 (2048) 264 : 274, the seven convolutions' step (2400) 361 : 376,
+// 2048 x 2048 (2048 blocks) 244 : 241 us, 1024 x 8192 (2048) 264 : 274, the seven convolutions' filters (2400) 361 : 376,
 // 2048 x 3000 (3072) 307 : 303, 1500 x 8192 (4608) 410 : 382, 2048 x 8192 (8192) 589 : 545.
 constexpr int64_t kPairWork = 2700;
 
@@ -1726,6 +1733,20 @@ int tiny_of(const std::vector<Mat>& mats) {
     return k <= 16 && n <= Tiny<16>::kCols ? 16 : k <= 32 && n <= Tiny<32>::kCols ? 32 : 0;
 }
 
+// Takes the matrices of at most 16 rows and 512 columns out of a list that has larger ones: ns_tiny_kernel takes them in fp32.  With
+// fp16 operands what a few values' rounding does depends on the matrix, up to 1e-2 of the result for 3 x 3 and 5e-3 for 4 x 8, where
+// many values' is 1e-3.  Up to 25 us, of which most lie under the other matrices' input pass.
+std::vector<Mat> take_few(std::vector<Mat>& mats) {
+    std::vector<Mat> few;
+    if (tiny_of(mats)) return few;
+    const auto rest = std::stable_partition(mats.begin(), mats.end(), [](const Mat& M) {
+        return std::min(M.rows, M.cols) > 16 || std::max(M.rows, M.cols) > 512;
+    });
+    few.assign(rest, mats.end());
+    mats.erase(rest, mats.end());
+    return few;
+}
+
 size_t workspace_of(std::vector<Mat>& mats) {
     if (cluster_of(mats)) return 256;
     size_t most = 0;
@@ -1744,8 +1765,18 @@ cf_status cuda_error() {
     return CF_ERR_CUDA;
 }
 
+// A launch that may begin before the one before it in the stream has ended.
+cudaLaunchAttribute overlap() {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return at;
+}
+
+// beside: the first launch may run beside the one before it.
 template <int N>
-cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, int cluster, bool uniform) {
+cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, int cluster, bool uniform,
+                    bool beside) {
     const int tiny = tiny_of(mats);
     const auto kernel = tiny == 16 ? ns_tiny_kernel<16, N> : tiny == 32 ? ns_tiny_kernel<32, N> : ns_small_kernel<N>;
     if (tiny) cluster = 1;
@@ -1775,12 +1806,13 @@ cf_status run_small(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov,
         cfg.dynamicSmemBytes = tiny == 16 ? Tiny<16>::smem(longest) : tiny == 32 ? Tiny<32>::smem(longest)
                                                                                 : 1024 + (2 * per + 8) * kBlkBytes + (cluster > 1 ? 4 * kTileF : 0);
         cfg.stream = ctx.stream;
-        cudaLaunchAttribute at[1];
+        cudaLaunchAttribute at[2];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = (unsigned)cluster;
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        at[1] = overlap();
         cfg.attrs = at;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = beside && b == 0 ? 2 : 1;
         if (cudaLaunchKernelEx(&cfg, kernel, J) != cudaSuccess) return cuda_error();
     }
     return CF_OK;
@@ -1827,15 +1859,22 @@ bool coop_fits(const LaunchCtx& ctx, bool pair) {
     return k > 0;
 }
 
-// uniform: the matrices are of one batch, a matrix apart.
-cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, void* ws, bool uniform) {
-    if (const int cluster = cluster_of(mats))
-        return (uniform || mats.size() == 1 ? run_small<1> : run_small<kMaxMats>)(ctx, p, mu, nesterov, mats, cluster, uniform);
-    if (cudaFuncSetAttribute(ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
-        return cuda_error();
-    for (size_t b = 0; b < mats.size(); b += kMaxMats)
-        if (!coop_fits(ctx, plan_sizes(&mats[b], (int)std::min<size_t>(kMaxMats, mats.size() - b)))) return cuda_error();
+// uniform: the matrices are of one batch, a matrix apart.  few: what take_few took out of a list.
+cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::vector<Mat>& mats, std::vector<Mat>& few, void* ws,
+              bool uniform) {
+    const int cluster = cluster_of(mats);
+    if (cluster == 0) {
+        if (cudaFuncSetAttribute(ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+            return cuda_error();
+        for (size_t b = 0; b < mats.size(); b += kMaxMats)
+            if (!coop_fits(ctx, plan_sizes(&mats[b], (int)std::min<size_t>(kMaxMats, mats.size() - b)))) return cuda_error();
+    }
+    if (!few.empty())
+        if (const cf_status st = (few.size() == 1 ? run_small<1> : run_small<kMaxMats>)(ctx, p, mu, nesterov, few, 1, false, false); st != CF_OK)
+            return st;
+    if (cluster)
+        return (uniform || mats.size() == 1 ? run_small<1> : run_small<kMaxMats>)(ctx, p, mu, nesterov, mats, cluster, uniform, !few.empty());
     for (size_t b = 0; b < mats.size(); b += kMaxMats) {
         Job J{};
         J.count = (int)std::min<size_t>(kMaxMats, mats.size() - b);
@@ -1867,12 +1906,11 @@ cf_status run(const LaunchCtx& ctx, const Poly& p, float mu, int nesterov, std::
         cfg.gridDim = dim3((unsigned)J.nn);
         cfg.blockDim = dim3(256);
         cfg.stream = ctx.stream;
+        cudaLaunchAttribute at = overlap();
+        cfg.attrs = &at;
+        cfg.numAttrs = !few.empty() && b == 0 ? 1 : 0;
         if (cudaLaunchKernelEx(&cfg, ns_input_kernel, J) != cudaSuccess) return cuda_error();
         cfg.gridDim = dim3((unsigned)J.nc);
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, ns_convert_kernel, J) != cudaSuccess) return cuda_error();
         Coop coop(ctx, pair);
@@ -1923,7 +1961,8 @@ cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, v
     if (ws == nullptr || ws_bytes < workspace_of(mats)) return CF_ERR_WORKSPACE;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    return run(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, 0.f, 0, mats, ws, true);
+    std::vector<Mat> none;
+    return run(ctx, Poly{desc->steps, desc->a, desc->b, desc->c, desc->eps}, 0.f, 0, mats, none, ws, true);
 } catch (const std::bad_alloc&) {  // the list of matrices
     return CF_ERR_UNSUPPORTED;
 }
@@ -1955,6 +1994,7 @@ static std::vector<Mat> list_of(int32_t count, const cf_muon_param* p) {
 size_t cf_muon_workspace_size(int32_t count, const cf_muon_param* params) try {
     if (count == 0 || muon_check(count, params) != CF_OK) return 0;
     std::vector<Mat> mats = list_of(count, params);
+    take_few(mats);
     return workspace_of(mats);
 } catch (const std::bad_alloc&) {  // the list of matrices
     return 0;
@@ -1971,14 +2011,15 @@ cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon
     if (h->steps > 16) return CF_ERR_UNSUPPORTED;
     if (count == 0) return CF_OK;
     std::vector<Mat> mats = list_of(count, params);
-    if (ws == nullptr || ws_bytes < workspace_of(mats)) return CF_ERR_WORKSPACE;
-    LaunchCtx ctx;
-    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
     for (int32_t i = 0; i < count; ++i) {
         mats[i].keep = 1.f - h->lr * h->weight_decay;
         mats[i].step = h->lr * params[i].scale;
     }
-    return run(ctx, p, h->momentum, h->nesterov != 0, mats, ws, false);
+    std::vector<Mat> few = take_few(mats);
+    if (ws == nullptr || ws_bytes < workspace_of(mats)) return CF_ERR_WORKSPACE;
+    LaunchCtx ctx;
+    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
+    return run(ctx, p, h->momentum, h->nesterov != 0, mats, few, ws, false);
 } catch (const std::bad_alloc&) {  // the list of matrices
     return CF_ERR_UNSUPPORTED;
 }

@@ -405,14 +405,13 @@ cf_status cf_group_norm_bwd(const cf_gn_desc* desc, const void* x, const float* 
  * Products take fp16 operands (11 bits) with fp32 sums, X is carried between
  * steps to 2^-20 of its values, and what the diagonals of A and of the
  * polynomial share is kept out of the rounding: |o - exact| is about 1e-3
- * |exact| in the Frobenius norm before the rounding to bf16 (and 1e-6 where
- * |u|_F is far below eps).  A call whose matrices all have at most 16 rows and
- * 1408 columns, or all at most 32 and 512 (rows: the shorter side), runs in
- * fp32 throughout, to about 3e-5; a list with one larger matrix runs as above
- * in all of it, so that a matrix's last bits depend on what else is in the
- * list.  The norm is taken without overflow or underflow for any finite u and
- * any eps >= 0.  A matrix with an entry that is not finite gives NaN
- * throughout.
+ * |exact| in the Frobenius norm before the rounding to bf16 (up to 3e-3 where a
+ * matrix has eight rows or fewer, and 1e-6 where |u|_F is far below eps).  Calls
+ * whose matrices all have at most 16 rows and 1408 columns, or all at most 32
+ * and 512 (rows: the shorter side), run in fp32 throughout, to about 3e-5, and
+ * so do a list's matrices of at most 16 rows and 512 columns beside larger ones.
+ * The norm is taken without overflow or underflow for any finite u and any
+ * eps >= 0.  A matrix with an entry that is not finite gives NaN throughout.
  * Supported: 1 <= steps <= 16; rows, cols up to 65536; as many matrices as the
  * host can list (beyond: CF_ERR_UNSUPPORTED).
  *

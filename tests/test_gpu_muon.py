@@ -465,3 +465,62 @@ def test_laid_out_workspace_too_small(cf, batch, rows, cols):
     assert cf.cf_muon_step(params, hyper, ws, size - 1, check=False) == cf.CF_ERR_WORKSPACE
     torch.cuda.synchronize()
     assert bool((o == 9).all()) and cf.cf_last_device_status() == cf.CF_OK
+
+
+FEW = [(1, 1), (1, 3), (2, 2), (4, 2), (3, 3), (4, 8), (8, 8), (9, 100), (16, 108), (16, 512), (512, 5), (1, 512)]
+
+
+@pytest.mark.parametrize("larger", [(17, 40), (64, 576), (16, 513), (300, 200), (2048, 2600)])
+def test_matrices_of_few_values_beside_larger_ones(cf, oracle_mod, larger):
+    """They run in fp32 whatever else is in the list: the 1e-4 of test_precision, and the bits of a list of their own."""
+    shapes = FEW * 5 + [larger]
+    o, g = _precise(cf, shapes, "normal", larger[1])
+    for a, b in list(zip(o, g))[:-1]:
+        ref = oracle_mod.newton_schulz(b)
+        assert np.linalg.norm(a - ref) <= 1e-4 * np.linalg.norm(ref), (a.shape, np.linalg.norm(a - ref) / np.linalg.norm(ref))
+    ref = oracle_mod.newton_schulz(g[-1])
+    assert np.linalg.norm(o[-1] - ref) <= 2e-3 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("larger", [(33, 40), (300, 200)])
+def test_matrices_of_few_values_end_with_the_step(cf, larger):
+    """What is enqueued after the step sees them done, on a stream and in a CUDA graph, and they have the bits of a list of their own."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(60)
+    shapes = [(16, 512), (3, 40)] * 30 + [larger]
+    w0, g, m0 = ([torch.randn(s, device="cuda", generator=gen) for s in shapes] for _ in range(3))
+    hyper = cf.cf_muon_hyper(0.01, 0.9, 0.1, 1, 16, 1.5, -0.5, 0.0, 1e-7)
+
+    def entries(w, m, count):
+        return cf.cf_muon_params([(a, None, b, c, 0.5) for a, b, c in zip(w, g, m)][:count])
+
+    def fresh():
+        return [t.clone() for t in w0], [t.clone() for t in m0]
+
+    w, m = fresh()
+    alone = entries(w, m, len(shapes) - 1)
+    size = cf.cf_muon_workspace_size(alone)
+    cf.cf_muon_step(alone, hyper, torch.empty(size, dtype=torch.uint8, device="cuda"), size)
+    want = w[:-1] + m[:-1]
+    torch.cuda.synchronize()
+    w, m = fresh()
+    params = entries(w, m, len(shapes))
+    size = cf.cf_muon_workspace_size(params)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        cf.cf_muon_step(params, hyper, ws, size, s)
+        got = [t.clone() for t in w[:-1] + m[:-1]]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cf.cf_muon_step(params, hyper, ws, size, torch.cuda.current_stream())
+        got = [t.clone() for t in w[:-1] + m[:-1]]
+    for a, b in zip(w + m, w0 + m0):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

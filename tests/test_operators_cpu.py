@@ -287,3 +287,12 @@ print(cf.cf_group_norm_fwd(gn, 16, None, None, 32, None, None, 256, 1 << 20, che
 print(muon([{shape!r}]))
 """
     assert _with_fake_runtime(tmp_path, call) == ["4", str(at), "0", "0"]
+
+
+@pytest.mark.parametrize("shapes,launches", [([(16, 108), (200, 400)], 4), ([(2, 3)] * 50 + [(2048, 2600)], 5), ([(3, 3), (64, 576)], 2),
+                                             ([(16, 512)], 1), ([(16, 512), (30, 30)], 1)])
+def test_muon_step_with_matrices_of_few_values_enqueues_all_or_nothing(tmp_path, shapes, launches):
+    call = MUON_CALL + f"fake.fake_set(%d, 0)\nprint(muon({shapes!r}), fake.fake_launches())"
+    assert _with_fake_runtime(tmp_path, call % 1) == ["0", str(launches)]
+    if max(min(s) for s in shapes) > 128:  # the cooperative launch, on a device that does not hold it
+        assert _with_fake_runtime(tmp_path, call % 0) == ["4", "0"]
