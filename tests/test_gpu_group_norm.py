@@ -567,3 +567,33 @@ def test_large_offsets_both_ways(cf, pool):
     count = dy[..., 0].numel()
     for a, b in ((dgamma, dg3), (dbeta, db3)):
         assert bool(((a - b).abs() <= 2.0 ** -14 * count).all())
+
+
+@pytest.mark.parametrize("shape,groups", [((2, 4, 4, 6, 16), 4), ((3, 48, 48, 48, 64), 8), ((2, 50, 48, 46, 20), 5)])
+@pytest.mark.parametrize("pool", ["none", "max", "avg"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_what_is_not_finite_stays_in_its_group_both_ways(cf, shape, groups, pool, value):
+    """Small and large samples: one value of one group of the last sample; every other group has the bits that it had before."""
+    import torch
+    per, act = shape[-1] // groups, "lrelu" if pool == "max" else "silu"
+    x, gamma, beta, dy = _inputs(shape, pool, "bf16", 54)
+
+    def both(x):
+        y, mean, rstd = _run_fwd(cf, shape, groups, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta)
+        return (y, mean, rstd) + _run_bwd(cf, shape, groups, pool, act, 0.3, 1e-5, "bf16", x, gamma, beta, mean, rstd, dy)
+
+    clean = both(x)
+    x = x.clone()
+    x[-1, -1, 1, 2, per + 1] = value  # the second group
+    got = both(x)
+    for i, (a, b) in enumerate(zip(clean, got)):
+        if i in (1, 2):  # mean, rstd [n][groups]
+            same = torch.ones_like(a, dtype=torch.bool)
+            same[-1, 1] = False
+            assert bool((~torch.isfinite(b[-1, 1])).all())
+        else:  # y, dx of the last sample; dgamma, dbeta of the group's channels
+            same = torch.ones_like(a, dtype=torch.bool)
+            (same[-1] if a.dim() == 5 else same)[..., per:2 * per] = False
+            # (dbeta sums LReLU'(u) dy, and LReLU' is the slope for any u that is not above 0, NaN too)
+            assert bool(torch.isnan(b[~same]).all()) or (i == 5 and act == "lrelu"), i
+        assert torch.equal(a[same], b[same]), i

@@ -524,3 +524,15 @@ def test_matrices_of_few_values_end_with_the_step(cf, larger):
     torch.cuda.synchronize()
     assert cf.cf_last_device_status() == cf.CF_OK
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("rows,cols", WAYS)
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_what_is_not_finite_stays_in_its_matrix(cf, rows, cols, value):
+    rng = np.random.default_rng(70)
+    g = np.stack([_matrix(rng, (rows, cols), "normal") for _ in range(3)])
+    clean, _ = _orth(cf, g, "f32")
+    g[1, rows // 2, cols - 1] = value
+    o, _ = _orth(cf, g, "f32")
+    assert np.array_equal(o[[0, 2]], clean[[0, 2]])
+    assert np.all(np.isnan(o[1]))
