@@ -506,7 +506,8 @@ class CosmoStack:
         the pinned host tensors dw_host[l] / db_host[l].  The copies overlap the
         compute: the input goes over in `chunks` sample ranges (default: one per
         sample, at most 8), the leading blocks running on each range as it
-        lands, and each gradient leaves as soon as it is final.  Same results, bit for
+        lands, and each gradient leaves as soon as it is final (the gammas' of normalised
+        blocks stay on the device, in self.dgamma).  Same results, bit for
         bit, as load + step + copy-back.  The host tensors must stay untouched
         until the caller's stream has passed the step."""
         main = self._main(stream)
