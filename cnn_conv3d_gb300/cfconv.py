@@ -25,8 +25,11 @@ _lib = ctypes.CDLL(LIB_PATH)
 CF_OK, CF_ERR_INVALID_ARG, CF_ERR_UNSUPPORTED, CF_ERR_WORKSPACE, CF_ERR_CUDA, CF_ERR_TIMEOUT = range(6)
 CF_OP_FWD, CF_OP_DGRAD, CF_OP_WGRAD, CF_OP_DGRAD_ROUTED, CF_OP_WGRAD_ROUTED, CF_OP_POOL_BWD, CF_OP_BN = range(7)
 CF_POOL_MAX, CF_POOL_AVG, CF_POOL_NONE = range(3)
-CF_ACT_LRELU, CF_ACT_SILU = range(2)
+CF_ACT_LRELU, CF_ACT_SILU, CF_ACT_GELU = range(3)
 CF_DT_BF16, CF_DT_F32 = range(2)
+CF_LINEAR_FWD, CF_LINEAR_DGRAD, CF_LINEAR_WGRAD = range(3)
+CF_NORM_NONE, CF_NORM_RMS, CF_NORM_LAYER = range(3)
+CF_PER_SAMPLE_GATE, CF_PER_SAMPLE_PRE = 1, 2
 
 
 class cf_conv_desc(ctypes.Structure):
@@ -63,6 +66,40 @@ class cf_muon_hyper(ctypes.Structure):
                 ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class cf_linear_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("k", ctypes.c_int32), ("n", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("slope", ctypes.c_float), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("x_pitch", ctypes.c_int64), ("y_pitch", ctypes.c_int64)]
+
+
+class cf_residual_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int32), ("post", ctypes.c_int32), ("pre", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("f_dtype", ctypes.c_int32), ("per_sample", ctypes.c_int32), ("rows_per_sample", ctypes.c_int64)]
+
+
+class cf_residual_norm_vectors(ctypes.Structure):
+    """Takes tensors, addresses or None.  It holds addresses: keep the tensors."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")]
+
+    def __init__(self, *vectors, **named):
+        super().__init__(*[_ptr(v) for v in vectors], **{name: _ptr(v) for name, v in named.items()})
+
+
+class cf_grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("count", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class cf_adam_param(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("w_bf16", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("count", ctypes.c_int64)]
+
+
+class cf_adam_hyper(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm")] + [
+        ("t", ctypes.c_int64)]
+
+
 class CfError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {cf_status_string(status)} ({status})")
@@ -73,6 +110,8 @@ _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ct
 _DP = ctypes.POINTER(cf_conv_desc)
 _EP = ctypes.POINTER(cf_pool_epi)
 _GP, _NP, _MP, _HP = (ctypes.POINTER(t) for t in (cf_gn_desc, cf_ns_desc, cf_muon_param, cf_muon_hyper))
+_LP, _RP, _VP = (ctypes.POINTER(t) for t in (cf_linear_desc, cf_residual_norm_desc, cf_residual_norm_vectors))
+_GLP, _AP, _AHP = (ctypes.POINTER(t) for t in (cf_grad, cf_adam_param, cf_adam_hyper))
 
 _SIGS = {
     "cf_conv3d_fwd": ([_DP, _vp, _vp, _EP, _vp, _vp, _sz, _vp], ctypes.c_int),
@@ -110,6 +149,19 @@ _SIGS = {
     "cf_orthogonalize": ([_NP, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "cf_muon_workspace_size": ([_i32, _MP], _sz),
     "cf_muon_step": ([_i32, _MP, _HP, _vp, _sz, _vp], ctypes.c_int),
+    "cf_linear_workspace_size": ([_LP, _i32], _sz),
+    "cf_linear_fwd": ([_LP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_linear_act_bwd": ([_LP, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "cf_linear_dgrad": ([_LP, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_linear_wgrad": ([_LP, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp], ctypes.c_int),
+    "cf_residual_norm_workspace_size": ([_RP], _sz),
+    "cf_residual_norm_fwd": ([_RP, _vp, _vp, _VP, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "cf_residual_norm_bwd": ([_RP, _vp, _vp, _VP, _vp, _vp, _vp, _vp, _vp, _VP, _vp, _sz, _vp], ctypes.c_int),
+    "cf_grad_workspace_size": ([_i32, _GLP], _sz),
+    "cf_grad_norm": ([_i32, _GLP, _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_clip_grads": ([_i32, _GLP, _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "cf_clip_adam_workspace_size": ([_i32, _AP], _sz),
+    "cf_clip_adam_step": ([_i32, _AP, _AHP, _vp, _vp, _sz, _vp], ctypes.c_int),
     "cf_workspace_size": ([ctypes.c_int, _DP], _sz),
     "cf_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "cf_last_device_status": ([_vp], ctypes.c_int),
@@ -347,6 +399,89 @@ def cf_muon_workspace_size(params) -> int:
 def cf_muon_step(params, hyper, ws=None, ws_bytes=0, stream=None, check=True):
     st = _lib.cf_muon_step(len(params), params, hyper, _ptr(ws), ws_bytes, _stream(stream))
     return _check(st, "cf_muon_step") if check else st
+
+
+def cf_linear_workspace_size(desc, op: int) -> int:
+    return _lib.cf_linear_workspace_size(desc, int(op))
+
+
+def cf_linear_fwd(desc, x, w, bias, residual, y, pre, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_linear_fwd(desc, _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(pre), _ptr(ws), ws_bytes,
+                            _stream(stream))
+    return _check(st, "cf_linear_fwd") if check else st
+
+
+def cf_linear_act_bwd(desc, dy, pre, dz, stream=None, check=True):
+    st = _lib.cf_linear_act_bwd(desc, _ptr(dy), _ptr(pre), _ptr(dz), _stream(stream))
+    return _check(st, "cf_linear_act_bwd") if check else st
+
+
+def cf_linear_dgrad(desc, dz, w, pre, add, dx, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_linear_dgrad(desc, _ptr(dz), _ptr(w), _ptr(pre), _ptr(add), _ptr(dx), _ptr(ws), ws_bytes,
+                              _stream(stream))
+    return _check(st, "cf_linear_dgrad") if check else st
+
+
+def cf_linear_wgrad(desc, x, dz, dw, db, accumulate=0, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_linear_wgrad(desc, _ptr(x), _ptr(dz), _ptr(dw), _ptr(db), int(accumulate), _ptr(ws), ws_bytes,
+                              _stream(stream))
+    return _check(st, "cf_linear_wgrad") if check else st
+
+
+def cf_residual_norm_workspace_size(desc) -> int:
+    return _lib.cf_residual_norm_workspace_size(desc)
+
+
+def cf_residual_norm_fwd(desc, x, f, vectors, r, h, stats, stream=None, check=True):
+    st = _lib.cf_residual_norm_fwd(desc, _ptr(x), _ptr(f), vectors, _ptr(r), _ptr(h), _ptr(stats), _stream(stream))
+    return _check(st, "cf_residual_norm_fwd") if check else st
+
+
+def cf_residual_norm_bwd(desc, f, r, vectors, stats, dh, dr, dx, df, grads, ws=None, ws_bytes=0, stream=None,
+                         check=True):
+    st = _lib.cf_residual_norm_bwd(desc, _ptr(f), _ptr(r), vectors, _ptr(stats), _ptr(dh), _ptr(dr), _ptr(dx), _ptr(df),
+                                   grads, _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_residual_norm_bwd") if check else st
+
+
+def cf_grads(tensors):
+    """The array of cf_grad for gradients in bf16 or fp32.  The array holds addresses: keep the tensors."""
+    out = (cf_grad * len(tensors))()
+    for p, g in zip(out, tensors):
+        p.g, p.count, p.dtype = _ptr(g), g.numel(), CF_DT_F32 if g.element_size() == 4 else CF_DT_BF16
+    return out
+
+
+def cf_grad_workspace_size(grads) -> int:
+    return _lib.cf_grad_workspace_size(len(grads), grads)
+
+
+def cf_grad_norm(grads, max_norm, out, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_grad_norm(len(grads), grads, float(max_norm), _ptr(out), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_grad_norm") if check else st
+
+
+def cf_clip_grads(grads, max_norm, out, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_clip_grads(len(grads), grads, float(max_norm), _ptr(out), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_clip_grads") if check else st
+
+
+def cf_adam_params(entries):
+    """The array of cf_adam_param for entries (w, w_bf16 or None, g, m, v).  The array holds addresses: keep the
+    tensors."""
+    out = (cf_adam_param * len(entries))()
+    for p, (w, w16, g, m, v) in zip(out, entries):
+        p.w, p.w_bf16, p.g, p.m, p.v, p.count = _ptr(w), _ptr(w16), _ptr(g), _ptr(m), _ptr(v), w.numel()
+    return out
+
+
+def cf_clip_adam_workspace_size(params) -> int:
+    return _lib.cf_clip_adam_workspace_size(len(params), params)
+
+
+def cf_clip_adam_step(params, hyper, out, ws=None, ws_bytes=0, stream=None, check=True):
+    st = _lib.cf_clip_adam_step(len(params), params, hyper, _ptr(out), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "cf_clip_adam_step") if check else st
 
 
 def cf_last_device_status(stream=None) -> int:

@@ -1,0 +1,432 @@
+// residual_norm.cu -- the norms before and after a block with the gated, scaled sum between (r = x + scale gate N_post(f),
+// h = N_pre(r)), forward and backward, with their entry points.
+//
+// Backward, per row, with vh the normalised values, u = gamma_pre dh and dv = scale gate gamma_post dx:
+//   dx = dr + rstd_r (u - mean u - rh mean(u rh))        (the mean of u for the layer norm only)
+//   df = rstd_f (dv - mean dv - fh mean(dv fh))
+// and four sums over rows are enough for all five vectors' gradients: A = sum dx fh, B = sum dx, C = sum dh rh, D = sum dh give
+//   dgate = scale (gamma_post A + beta_post B),  dgamma_post = scale gate A,  dbeta_post = scale gate B,  dgamma_pre = C,
+//   dbeta_pre = D                                 (gate's factor inside the sum over the samples where each has its own)
+#include <algorithm>
+#include <cmath>
+
+#include "cf_internal.h"
+#include "cf_ptx.cuh"
+
+namespace cf {
+namespace {
+
+struct RnArgs {
+    int64_t rows, per;         // per: rows of a sample
+    int c, post, pre;
+    int gate_each, pre_each;   // a vector for each sample
+    float eps, scale, inv_c;
+    int samples, chunks;       // chunks of a sample's rows, `chunk` rows each
+    int64_t chunk;
+    const float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
+};
+
+__device__ __forceinline__ float load(const float* p, int64_t i) { return p[i]; }
+__device__ __forceinline__ float load(const uint16_t* p, int64_t i) { return bf16_bits_to_float(p[i]); }
+__device__ __forceinline__ void store(float* p, int64_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void store(uint16_t* p, int64_t i, float v) { p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ float at_or(const float* p, int64_t i, float other) { return p ? p[i] : other; }
+
+// p = a fh + b with what lies between the norm and the sum.
+__device__ __forceinline__ void post_affine(const RnArgs& A, int64_t sample, int j, float& a, float& b) {
+    const float g = A.scale * at_or(A.gate, A.gate_each ? sample * A.c + j : j, 1.f);
+    a = g * at_or(A.post_gamma, j, 1.f);
+    b = g * at_or(A.post_beta, j, 0.f);
+}
+__device__ __forceinline__ float2 pre_affine(const RnArgs& A, int64_t sample, int j) {
+    const int64_t i = A.pre_each ? sample * A.c + j : j;
+    return make_float2(at_or(A.pre_gamma, i, 1.f), at_or(A.pre_beta, i, 0.f));
+}
+
+constexpr int kThreads = 256;
+
+// Sums over the block, the same in every thread.
+__device__ __forceinline__ float2 block_sum(float a, float b, float2* red) {
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(~0u, a, o);
+        b += __shfl_xor_sync(~0u, b, o);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) a += red[i].x, b += red[i].y;
+    return make_float2(a, b);
+}
+
+// mean and 1 / width of c values, read twice.
+template <typename F>
+__device__ __forceinline__ float2 stats_long(const RnArgs& A, int kind, float2* red, F value) {
+    if (kind == CF_NORM_NONE) return make_float2(0.f, 1.f);
+    float mean = 0.f, s = 0.f;
+    if (kind == CF_NORM_LAYER) {
+        for (int j = threadIdx.x; j < A.c; j += kThreads) s += value(j);
+        mean = block_sum(s, 0.f, red).x * A.inv_c;
+    }
+    s = 0.f;
+    for (int j = threadIdx.x; j < A.c; j += kThreads) {
+        const float t = value(j) - mean;
+        s = fmaf(t, t, s);
+    }
+    return make_float2(mean, rsqrtf(block_sum(s, 0.f, red).x * A.inv_c + A.eps));
+}
+
+// Rows of any length: a block to a row, which is read again for each sum (from L1 or L2).
+template <typename S, typename F>
+__global__ void __launch_bounds__(kThreads) rn_fwd_long_kernel(const RnArgs A, const S* x, const F* f, S* r, F* h, float4* stats) {
+    __shared__ float2 red[kThreads / 32];
+    for (int64_t i = blockIdx.x; i < A.rows; i += gridDim.x) {
+        const int64_t o = i * A.c, sample = i / A.per;
+        const float2 sf = f ? stats_long(A, A.post, red, [&](int j) { return load(f, o + j); }) : make_float2(0.f, 1.f);
+        auto sum = [&](int j) {
+            const float v = load(x, o + j);
+            if (!f) return v;
+            float a, b;
+            post_affine(A, sample, j, a, b);
+            return v + fmaf(a, (load(f, o + j) - sf.x) * sf.y, b);
+        };
+        const float2 sr = stats_long(A, A.pre, red, sum);
+        __syncthreads();  // all have read the row before r, which may be x, is written
+        for (int j = threadIdx.x; j < A.c; j += kThreads) {
+            const float v = sum(j);
+            if (h) {
+                const float2 g = pre_affine(A, sample, j);
+                store(h, o + j, fmaf((v - sr.x) * sr.y, g.x, g.y));
+            }
+            if (r) store(r, o + j, v);
+        }
+        if (stats && threadIdx.x == 0) stats[i] = make_float4(sf.x, sf.y, sr.x, sr.y);
+    }
+}
+
+// dx of value j of a row, from m = (mean u, mean u rh).
+template <typename S, typename F>
+__device__ __forceinline__ float dx_of(const RnArgs& A, int64_t sample, int64_t o, int j, const S* r, const F* dh, const S* dr,
+                                       const float4& st, float2 m) {
+    float d = dr ? load(dr, o + j) : 0.f;
+    if (A.pre != CF_NORM_NONE) {
+        const float u = pre_affine(A, sample, j).x * load(dh, o + j);
+        d = fmaf(st.w, u - m.x - (load(r, o + j) - st.z) * st.w * m.y, d);
+    }
+    return d;
+}
+
+// The means that a row's gradients take.
+template <typename S, typename F>
+__global__ void __launch_bounds__(kThreads) rn_bwd_rows_kernel(const RnArgs A, const F* f, const S* r, const float4* stats, const F* dh,
+                                                               const S* dr, float4* means) {
+    __shared__ float2 red[kThreads / 32];
+    for (int64_t i = blockIdx.x; i < A.rows; i += gridDim.x) {
+        const int64_t o = i * A.c, sample = i / A.per;
+        const float4 st = stats[i];
+        float2 m = make_float2(0.f, 0.f), n = m;
+        if (A.pre != CF_NORM_NONE) {
+            for (int j = threadIdx.x; j < A.c; j += kThreads) {
+                const float u = pre_affine(A, sample, j).x * load(dh, o + j);
+                m.x += u;
+                m.y = fmaf(u, (load(r, o + j) - st.z) * st.w, m.y);
+            }
+            m = block_sum(m.x, m.y, red);
+            m.x = A.pre == CF_NORM_LAYER ? m.x * A.inv_c : 0.f;
+            m.y *= A.inv_c;
+        }
+        if (A.post != CF_NORM_NONE) {
+            for (int j = threadIdx.x; j < A.c; j += kThreads) {
+                float a, b;
+                post_affine(A, sample, j, a, b);
+                const float dv = a * dx_of(A, sample, o, j, r, dh, dr, st, m);
+                n.x += dv;
+                n.y = fmaf(dv, (load(f, o + j) - st.x) * st.y, n.y);
+            }
+            n = block_sum(n.x, n.y, red);
+            n.x = A.post == CF_NORM_LAYER ? n.x * A.inv_c : 0.f;
+            n.y *= A.inv_c;
+        }
+        if (threadIdx.x == 0) means[i] = make_float4(m.x, m.y, n.x, n.y);
+    }
+}
+
+// dx, df and the chunk's sums over rows, from the rows' means: 32 columns to a block, 8 rows at a time.
+template <typename S, typename F>
+__global__ void __launch_bounds__(kThreads) rn_bwd_cols_kernel(const RnArgs A, const F* f, const S* r, const float4* stats, const F* dh,
+                                                               const S* dr, const float4* means, S* dx, F* df, float* part) {
+    __shared__ float4 red[8][32];
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, j = blockIdx.y * 32 + lane;
+    const int sample = blockIdx.x / A.chunks;
+    const int64_t from = sample * A.per + (blockIdx.x - (int64_t)sample * A.chunks) * A.chunk;
+    const int64_t to = min(min(from + A.chunk, (sample + 1) * A.per), A.rows);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < A.c) {
+        float a, b;
+        post_affine(A, sample, j, a, b);
+        for (int64_t i = from + q; i < to; i += 8) {
+            const int64_t o = i * A.c;
+            const float4 st = stats[i], m = means[i];
+            const float d = dx_of(A, sample, o, j, r, dh, dr, st, make_float2(m.x, m.y));
+            const float fh = f ? (load(f, o + j) - st.x) * st.y : 0.f;
+            s.x = fmaf(d, fh, s.x);
+            s.y += d;
+            if (A.pre != CF_NORM_NONE) {
+                const float g = load(dh, o + j);
+                s.z = fmaf(g, (load(r, o + j) - st.z) * st.w, s.z);
+                s.w += g;
+            }
+            if (dx) store(dx, o + j, d);
+            if (df) store(df, o + j, A.post == CF_NORM_NONE ? a * d : st.y * (a * d - m.z - fh * m.w));
+        }
+    }
+    red[q][lane] = s;
+    __syncthreads();
+    if (q == 0 && j < A.c) {
+        for (int i = 1; i < 8; ++i) s.x += red[i][lane].x, s.y += red[i][lane].y, s.z += red[i][lane].z, s.w += red[i][lane].w;
+        float* p = part + (int64_t)blockIdx.x * 4 * A.c + j;
+        p[0] = s.x, p[A.c] = s.y, p[2 * (int64_t)A.c] = s.z, p[3 * (int64_t)A.c] = s.w;
+    }
+}
+
+struct RnGrads {
+    float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
+};
+
+// The sums of 32 columns over rows [0, count) of v [][4][c]; f says what a row counts (per sum): in warp 0.
+template <typename W>
+__device__ __forceinline__ float4 column_sums(const float* v, int64_t count, int c, int j, float4 (*red)[32], W weight) {
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < c) {
+#pragma unroll 4
+        for (int64_t i = q; i < count; i += 8) {
+            const float* p = v + i * 4 * c + j;
+            const float w = weight(i);
+            s.x = fmaf(w, p[0], s.x);
+            s.y = fmaf(w, p[c], s.y);
+            s.z += p[2 * (int64_t)c];
+            s.w += p[3 * (int64_t)c];
+        }
+    }
+    red[q][lane] = s;
+    __syncthreads();
+    if (q == 0)
+        for (int i = 1; i < 8; ++i) s.x += red[i][lane].x, s.y += red[i][lane].y, s.z += red[i][lane].z, s.w += red[i][lane].w;
+    return s;
+}
+
+// Each sample's sums from its chunks' (kept where vectors are shared between samples), and the gradients that are a sample's own.
+__global__ void __launch_bounds__(kThreads) rn_sample_kernel(const RnArgs A, const float* part, float* sums, const RnGrads G) {
+    __shared__ float4 red[8][32];
+    const int j = blockIdx.y * 32 + (threadIdx.x & 31);
+    const int64_t sample = blockIdx.x, c = A.c;
+    const float4 s = column_sums(part + sample * A.chunks * 4 * c, A.chunks, A.c, j, red, [](int64_t) { return 1.f; });
+    if (threadIdx.x >= 32 || j >= A.c) return;
+    const bool one = A.samples == 1;
+    if (!one) {
+        float* p = sums + sample * 4 * c + j;
+        p[0] = s.x, p[c] = s.y, p[2 * c] = s.z, p[3 * c] = s.w;
+    }
+    if (G.gate && (one || A.gate_each))
+        G.gate[sample * c + j] = A.scale * (at_or(A.post_gamma, j, 1.f) * s.x + at_or(A.post_beta, j, 0.f) * s.y);
+    if (one || A.pre_each) {
+        if (G.pre_gamma) G.pre_gamma[sample * c + j] = s.z;
+        if (G.pre_beta) G.pre_beta[sample * c + j] = s.w;
+    }
+    if (one) {
+        const float g = A.scale * at_or(A.gate, j, 1.f);
+        if (G.post_gamma) G.post_gamma[j] = g * s.x;
+        if (G.post_beta) G.post_beta[j] = g * s.y;
+    }
+}
+
+// The gradients of vectors that samples share.
+__global__ void __launch_bounds__(kThreads) rn_shared_kernel(const RnArgs A, const float* sums, const RnGrads G) {
+    __shared__ float4 red[8][32];
+    const int j = blockIdx.x * 32 + (threadIdx.x & 31), c = A.c;
+    const float4 s = column_sums(sums, A.samples, c, j, red, [&](int64_t i) { return A.gate_each ? at_or(A.gate, i * c + j, 1.f) : 1.f; });
+    if (threadIdx.x >= 32 || j >= A.c) return;
+    const float g = A.scale * (A.gate_each ? 1.f : at_or(A.gate, j, 1.f));
+    if (G.post_gamma) G.post_gamma[j] = g * s.x;
+    if (G.post_beta) G.post_beta[j] = g * s.y;
+    if (G.gate && !A.gate_each) G.gate[j] = A.scale * (at_or(A.post_gamma, j, 1.f) * s.x + at_or(A.post_beta, j, 0.f) * s.y);
+    if (!A.pre_each) {
+        if (G.pre_gamma) G.pre_gamma[j] = s.z;
+        if (G.pre_beta) G.pre_beta[j] = s.w;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) rn_zero_kernel(float* p, int64_t count) {
+    const int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    if (i < count) p[i] = 0.f;
+}
+
+// --------------------------------------------------------------------------------------------------------------------------- host
+constexpr int kPlanSms = 152;  // work is cut for so many SMs: workspaces are laid out without asking the device
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+cf_status status_of() { return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA; }
+
+RnArgs args_of(const cf_residual_norm_desc* d) {
+    RnArgs A{};
+    A.rows = d->rows, A.c = d->c, A.post = d->post, A.pre = d->pre;
+    A.eps = d->eps, A.scale = d->scale, A.inv_c = 1.f / (float)d->c;
+    A.per = d->rows_per_sample ? d->rows_per_sample : std::max<int64_t>(d->rows, 1);
+    A.gate_each = (d->per_sample & CF_PER_SAMPLE_GATE) != 0, A.pre_each = (d->per_sample & CF_PER_SAMPLE_PRE) != 0;
+    if (!d->per_sample) A.per = std::max<int64_t>(d->rows, 1);
+    A.samples = (int)((d->rows + A.per - 1) / A.per);
+    return A;
+}
+void vectors_of(RnArgs& A, const cf_residual_norm_vectors* v) {
+    if (v == nullptr) return;
+    A.post_gamma = v->post_gamma, A.post_beta = v->post_beta, A.gate = v->gate, A.pre_gamma = v->pre_gamma, A.pre_beta = v->pre_beta;
+}
+// Chunks of a sample's rows for about `blocks` blocks, of at least `least` rows.
+void cut(RnArgs& A, int64_t blocks, int64_t least) {
+    const int64_t per = std::min(A.per, A.rows);
+    int64_t chunks = std::max<int64_t>(1, std::min((blocks + A.samples - 1) / std::max(A.samples, 1), per / least));
+    A.chunk = (per + chunks - 1) / chunks;
+    A.chunks = (int)((per + A.chunk - 1) / A.chunk);
+}
+
+struct Layout {
+    float4* means;
+    float *part, *sums;
+    size_t bytes;
+};
+Layout layout_of(const RnArgs& A, void* ws) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        void* p = static_cast<char*>(ws) + at;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    Layout L;
+    L.means = static_cast<float4*>(take((size_t)A.rows * sizeof(float4)));
+    L.part = static_cast<float*>(take((size_t)A.samples * A.chunks * 4 * A.c * sizeof(float)));
+    L.sums = static_cast<float*>(take(A.samples > 1 ? (size_t)A.samples * 4 * A.c * sizeof(float) : 0));
+    L.bytes = std::max<size_t>(at, 256);
+    return L;
+}
+RnArgs plan_bwd(const cf_residual_norm_desc* d) {
+    RnArgs A = args_of(d);
+    if (A.rows) cut(A, std::max(1, kPlanSms * 8 * 32 / A.c), 8);
+    return A;
+}
+
+cf_status check(const cf_residual_norm_desc* d) {
+    if (d == nullptr || d->rows < 0 || d->c <= 0) return CF_ERR_INVALID_ARG;
+    if (d->post < CF_NORM_NONE || d->post > CF_NORM_LAYER || d->pre < CF_NORM_NONE || d->pre > CF_NORM_LAYER) return CF_ERR_INVALID_ARG;
+    if (!(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->scale)) return CF_ERR_INVALID_ARG;
+    if ((d->dtype != CF_DT_BF16 && d->dtype != CF_DT_F32) || (d->f_dtype != CF_DT_BF16 && d->f_dtype != CF_DT_F32)) return CF_ERR_INVALID_ARG;
+    if ((d->per_sample & ~(CF_PER_SAMPLE_GATE | CF_PER_SAMPLE_PRE)) || d->rows_per_sample < 0) return CF_ERR_INVALID_ARG;
+    if (d->dtype == CF_DT_BF16 && d->f_dtype == CF_DT_F32) return CF_ERR_UNSUPPORTED;
+    if (d->c > 65536 || d->rows >= (int64_t)1 << 31) return CF_ERR_UNSUPPORTED;
+    const int64_t per = d->rows_per_sample ? d->rows_per_sample : std::max<int64_t>(d->rows, 1);
+    if (d->per_sample && (d->rows + per - 1) / per >= 1 << 24) return CF_ERR_UNSUPPORTED;
+    return CF_OK;
+}
+bool vectors_ok(const cf_residual_norm_desc* d, const cf_residual_norm_vectors* v) {
+    if (v == nullptr) return true;
+    for (const float* p : {v->post_gamma, v->post_beta, v->gate, v->pre_gamma, v->pre_beta})
+        if (!aligned16(p)) return false;
+    if (d->post == CF_NORM_NONE && v->post_gamma) return false;
+    if (d->pre == CF_NORM_NONE && v->pre_gamma) return false;
+    return !(d->post != CF_NORM_LAYER && v->post_beta) && !(d->pre != CF_NORM_LAYER && v->pre_beta);
+}
+
+// f with the stream's and the blocks' types.
+template <typename Fn>
+cf_status with_types(const cf_residual_norm_desc* d, Fn f) {
+    if (d->f_dtype == CF_DT_F32) return f(float{}, float{});
+    if (d->dtype == CF_DT_F32) return f(float{}, uint16_t{});
+    return f(uint16_t{}, uint16_t{});
+}
+
+}  // namespace
+}  // namespace cf
+
+using namespace cf;
+
+extern "C" {
+
+size_t cf_residual_norm_workspace_size(const cf_residual_norm_desc* desc) {
+    if (check(desc) != CF_OK) return 0;
+    return layout_of(plan_bwd(desc), nullptr).bytes;
+}
+
+cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x, const void* f, const cf_residual_norm_vectors* vectors,
+                               void* r, void* h, float* stats, void* stream) {
+    if (const cf_status st = check(desc); st != CF_OK) return st;
+    const bool pre = desc->pre != CF_NORM_NONE;
+    if (!vectors_ok(desc, vectors) || (f == nullptr && (desc->post != CF_NORM_NONE || (vectors && vectors->gate)))) return CF_ERR_INVALID_ARG;
+    if (desc->rows == 0) return CF_OK;
+    if (!x || (h != nullptr) != pre || (!r && !h)) return CF_ERR_INVALID_ARG;
+    for (const void* p : {x, f, (const void*)r, (const void*)h, (const void*)stats})
+        if (!aligned16(p)) return CF_ERR_INVALID_ARG;
+    LaunchCtx ctx;
+    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
+    RnArgs A = args_of(desc);
+    vectors_of(A, vectors);
+    return with_types(desc, [&](auto s, auto t) {
+        using S = decltype(s);
+        using F = decltype(t);
+        rn_fwd_long_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(
+            A, static_cast<const S*>(x), static_cast<const F*>(f), static_cast<S*>(r), static_cast<F*>(h), reinterpret_cast<float4*>(stats));
+        return status_of();
+    });
+}
+
+cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f, const void* r, const cf_residual_norm_vectors* vectors,
+                               const float* stats, const void* dh, const void* dr, void* dx, void* df,
+                               const cf_residual_norm_vectors* grads, void* ws, size_t ws_bytes, void* stream) {
+    if (const cf_status st = check(desc); st != CF_OK) return st;
+    const bool pre = desc->pre != CF_NORM_NONE;
+    if (!vectors_ok(desc, vectors) || !vectors_ok(desc, grads)) return CF_ERR_INVALID_ARG;
+    const bool sums = grads && (grads->post_gamma || grads->post_beta || grads->gate || grads->pre_gamma || grads->pre_beta);
+    if (desc->rows) {
+        if (!stats || (dh != nullptr) != pre || (pre && !r) || (!dh && !dr) || (!dx && !df && !sums)) return CF_ERR_INVALID_ARG;
+        if (!f && (desc->post != CF_NORM_NONE || df || (vectors && vectors->gate) || (grads && grads->gate))) return CF_ERR_INVALID_ARG;
+        for (const void* p : {f, r, (const void*)stats, dh, dr, (const void*)dx, (const void*)df, (const void*)ws})
+            if (!aligned16(p)) return CF_ERR_INVALID_ARG;
+    }
+    RnArgs A = plan_bwd(desc);
+    vectors_of(A, vectors);
+    RnGrads G{};
+    if (grads) G = RnGrads{grads->post_gamma, grads->post_beta, grads->gate, grads->pre_gamma, grads->pre_beta};
+    const Layout L = layout_of(A, ws);
+    if (desc->rows && (ws == nullptr || ws_bytes < L.bytes)) return CF_ERR_WORKSPACE;
+    LaunchCtx ctx;
+    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
+    if (desc->rows == 0) {
+        // no samples either: a vector for each of them has no values
+        const bool ge = A.gate_each, pe = A.pre_each;
+        for (float* p : {G.post_gamma, G.post_beta, ge ? nullptr : G.gate, pe ? nullptr : G.pre_gamma, pe ? nullptr : G.pre_beta})
+            if (p) {
+                rn_zero_kernel<<<(A.c + kThreads - 1) / kThreads, kThreads, 0, ctx.stream>>>(p, A.c);
+                if (const cf_status st = status_of(); st != CF_OK) return st;
+            }
+        return CF_OK;
+    }
+    return with_types(desc, [&](auto s, auto t) {
+        using S = decltype(s);
+        using F = decltype(t);
+        const S *rs = static_cast<const S*>(r), *drs = static_cast<const S*>(dr);
+        const F *fs = static_cast<const F*>(f), *dhs = static_cast<const F*>(dh);
+        const float4* st4 = reinterpret_cast<const float4*>(stats);
+        const unsigned tiles = (A.c + 31) / 32;
+        rn_bwd_rows_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(A, fs, rs, st4, dhs, drs,
+                                                                                                                   L.means);
+        if (const cf_status st = status_of(); st != CF_OK) return st;
+        rn_bwd_cols_kernel<S, F><<<dim3((unsigned)(A.samples * A.chunks), tiles), kThreads, 0, ctx.stream>>>(
+            A, fs, rs, st4, dhs, drs, L.means, static_cast<S*>(dx), static_cast<F*>(df), L.part);
+        if (const cf_status st = status_of(); st != CF_OK || !sums) return st;
+        rn_sample_kernel<<<dim3((unsigned)A.samples, tiles), kThreads, 0, ctx.stream>>>(A, L.part, L.sums, G);
+        if (const cf_status st = status_of(); st != CF_OK || A.samples == 1) return st;
+        rn_shared_kernel<<<tiles, kThreads, 0, ctx.stream>>>(A, L.sums, G);
+        return status_of();
+    });
+}
+
+}  // extern "C"

@@ -372,7 +372,7 @@ cf_status cf_adam_step(int64_t count, float* w, uint16_t* w_bf16, const float* g
  * holds, are unsupported too.)
  * Workspace: cf_group_norm_workspace_size(desc, 0 forward / 1 backward).
  */
-enum { CF_ACT_LRELU = 0, CF_ACT_SILU = 1 };
+enum { CF_ACT_LRELU = 0, CF_ACT_SILU = 1, CF_ACT_GELU = 2 /* cf_linear_* only */ };
 enum { CF_DT_BF16 = 0, CF_DT_F32 = 1 };
 
 typedef struct {
@@ -456,6 +456,156 @@ cf_status cf_orthogonalize(const cf_ns_desc* desc, const void* g, uint16_t* o, v
 size_t cf_muon_workspace_size(int32_t count, const cf_muon_param* params);
 cf_status cf_muon_step(int32_t count, const cf_muon_param* params, const cf_muon_hyper* hyper, void* ws,
                        size_t ws_bytes, void* stream);
+
+/*
+ * Matrix products with bias, activation and residual: a 1x1x1 convolution of
+ * NDHWC voxels, or a fully connected layer on the tensor cores.
+ *   fwd     z = x w^T + b;  y = residual + scale act(z)
+ *   act_bwd dz = scale dy act'(pre)
+ *   dgrad   dx = add + scale (dz w) act'(pre)
+ *   wgrad   dw = scale dz^T x,  db = scale sum over the rows of dz
+ *   act: LReLU(slope) (slope 1: none, 0: ReLU; LReLU'(0) = slope), SiLU
+ *        z / (1 + exp(-z)), or GELU z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3)))
+ *   x [rows][k], w [n][k], dz [rows][n] bf16; bias [n] fp32 or NULL.
+ *   y, residual, dy [rows][n] and dx, add [rows][k]: bf16 or fp32 (dtype);
+ *        residual and add may be NULL, and may be y and dx themselves.
+ *   pre: z rounded to bf16.  Of the forward [rows][n], or NULL; act_bwd takes
+ *        that.  The backward data takes the layer below's, [rows][k] with its
+ *        act and slope in the descriptor: dx is then that layer's dz (NULL: no
+ *        activation).  A dz from act_bwd has the scale in it already.
+ *   dw [n][k], db [n] fp32 (db may be NULL); accumulate != 0 adds to both.
+ *   x_pitch: values from a row to the next of x, dx, add and the backward
+ *        data's pre; y_pitch: of y, residual, dy, dz and the forward's pre; 0 =
+ *        dense.  w, dw are dense.
+ * Products of bf16 values are summed in fp32 (wgrad: over parts of the rows, the
+ * parts joined in an order fixed by the sizes), and each output is rounded once.
+ * y must not overlap x or w, nor dx dz, w or pre, other than as said.  rows 0 does
+ * nothing but to zero dw and db.
+ * Supported: rows < 2^31, k, n <= 2^20, pitches < 2^28, any alignment of rows;
+ * faster where k, n and the pitches are multiples of 8.
+ * Workspace: cf_linear_workspace_size(desc, CF_LINEAR_*); act_bwd takes none.
+ */
+enum { CF_LINEAR_FWD = 0, CF_LINEAR_DGRAD = 1, CF_LINEAR_WGRAD = 2 };
+
+typedef struct {
+    int64_t rows;
+    int32_t k, n;
+    int32_t act;              /* CF_ACT_* */
+    float slope;              /* of CF_ACT_LRELU */
+    float scale;
+    int32_t dtype;            /* CF_DT_* of y, residual, dy, dx, add */
+    int64_t x_pitch, y_pitch; /* 0 = k, n */
+} cf_linear_desc;
+
+size_t cf_linear_workspace_size(const cf_linear_desc* desc, int32_t op);
+cf_status cf_linear_fwd(const cf_linear_desc* desc, const uint16_t* x, const uint16_t* w, const float* bias,
+                        const void* residual, void* y, uint16_t* pre, void* ws, size_t ws_bytes, void* stream);
+cf_status cf_linear_act_bwd(const cf_linear_desc* desc, const void* dy, const uint16_t* pre, uint16_t* dz,
+                            void* stream);
+cf_status cf_linear_dgrad(const cf_linear_desc* desc, const uint16_t* dz, const uint16_t* w, const uint16_t* pre,
+                          const void* add, void* dx, void* ws, size_t ws_bytes, void* stream);
+cf_status cf_linear_wgrad(const cf_linear_desc* desc, const uint16_t* x, const uint16_t* dz, float* dw, float* db,
+                          int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The norms before and after a block, with its gate and residual scale: what
+ * lies between a block's output f and the next block's input h on a residual
+ * stream, in one pass.  Rows of c values (voxels' channels):
+ *   N(v) = gamma (v - mean) rstd + beta, rstd = 1 / sqrt(mean (v - mean)^2 + eps)
+ *          over the row's values; CF_NORM_RMS: mean 0; CF_NORM_NONE: v itself
+ *   r = x + scale gate N_post(f)        the stream after the block
+ *   h = N_pre(r)                        the next block's input
+ * f NULL (post CF_NORM_NONE, no gate): h = N_pre(x), the first block's input.
+ * Backward, from dr (what comes to r from later in the stream, or NULL) and dh:
+ *   dx = dr + N_pre'(r) dh;  df = N_post'(f) (scale gate dx); the vectors' sums
+ * over their rows.  dx is also the gradient at x; it is rounded only where stored.
+ *   x, r, dr, dx [rows][c] of dtype; f, h, dh, df [rows][c] of f_dtype.  Both
+ *          bf16, both fp32, or an fp32 stream with bf16 blocks.  r may be x, dx
+ *          dr, and df dh.
+ *   gate, gamma, beta: fp32 [c], NULL for 1, 1 and 0.  per_sample: gate, or
+ *          N_pre's gamma and beta, or both have a vector for each sample, [samples][c],
+ *          a sample being rows_per_sample rows (0: all), the last one what is left.
+ *          beta is CF_NORM_LAYER's only.
+ *   stats  [rows][4] fp32: mean and rstd of f, then of r (0 and 1 where there is
+ *          no norm); NULL in the forward for inference.  h is taken from r before
+ *          r's rounding, and the statistics are that r's.
+ *   r may be NULL in the forward, dx, df and any gradient in the backward.
+ * Sums are fp32 in an order fixed by the sizes.  rows 0 zeroes the gradients.
+ * Supported: c <= 65536, rows < 2^31, samples < 2^24.
+ * Workspace: cf_residual_norm_workspace_size (backward; the forward takes none).
+ */
+enum { CF_NORM_NONE = 0, CF_NORM_RMS = 1, CF_NORM_LAYER = 2 };
+enum { CF_PER_SAMPLE_GATE = 1, CF_PER_SAMPLE_PRE = 2 };
+
+typedef struct {
+    int64_t rows;
+    int32_t c;
+    int32_t post, pre;       /* CF_NORM_* */
+    float eps, scale;
+    int32_t dtype, f_dtype;  /* CF_DT_* */
+    int32_t per_sample;      /* CF_PER_SAMPLE_* */
+    int64_t rows_per_sample;
+} cf_residual_norm_desc;
+
+/* The vectors (in the backward also their gradients). */
+typedef struct {
+    float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
+} cf_residual_norm_vectors;
+
+size_t cf_residual_norm_workspace_size(const cf_residual_norm_desc* desc);
+cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x, const void* f,
+                               const cf_residual_norm_vectors* vectors, void* r, void* h, float* stats, void* stream);
+cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f, const void* r,
+                               const cf_residual_norm_vectors* vectors, const float* stats, const void* dh,
+                               const void* dr, void* dx, void* df, const cf_residual_norm_vectors* grads, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * The global norm of a list of gradients, and clipping by it:
+ *   norm = sqrt(sum of all tensors' squares),  factor = min(1, max_norm / (norm + 1e-6))
+ *   cf_grad_norm      : out [2] fp32 (device) = norm, factor
+ *   cf_clip_grads     : and g = factor g in place, untouched where the factor is 1
+ *   cf_clip_adam_step : and an Adam step of the list with factor g, which itself stays as
+ *       it is:  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+ *       w = (1 - lr weight_decay) w - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps),
+ *       w_bf16 = w rounded (or NULL).  max_norm 0 (here only): no clipping, no norm, and
+ *       out (which may then be NULL) is not written.
+ * Squares are summed so that none is lost to overflow or underflow, in an order
+ * fixed by the list.  A norm that is infinite gives a factor of 0 (and NaN in place
+ * of infinite entries), one that is NaN NaN everywhere: a caller that skips such
+ * steps looks at out[0] of cf_grad_norm first.
+ *   grads, params: host arrays, read during the call; g bf16 or fp32 (cf_grad),
+ *       w, g, m, v fp32 (cf_adam_param); they may begin at any value.  count 0 gives norm 0.  Entries of
+ *       no values are skipped; tensors that are written must not overlap others.
+ * Workspaces: cf_grad_workspace_size, cf_clip_adam_workspace_size.
+ */
+typedef struct {
+    void* g;
+    int64_t count;
+    int32_t dtype; /* CF_DT_* */
+} cf_grad;
+
+typedef struct {
+    float* w;
+    uint16_t* w_bf16;
+    const float* g;
+    float *m, *v;
+    int64_t count;
+} cf_adam_param;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, max_norm;
+    int64_t t; /* step, >= 1 */
+} cf_adam_hyper;
+
+size_t cf_grad_workspace_size(int32_t count, const cf_grad* grads);
+cf_status cf_grad_norm(int32_t count, const cf_grad* grads, float max_norm, float* out, void* ws, size_t ws_bytes,
+                       void* stream);
+cf_status cf_clip_grads(int32_t count, const cf_grad* grads, float max_norm, float* out, void* ws, size_t ws_bytes,
+                        void* stream);
+size_t cf_clip_adam_workspace_size(int32_t count, const cf_adam_param* params);
+cf_status cf_clip_adam_step(int32_t count, const cf_adam_param* params, const cf_adam_hyper* hyper, float* out,
+                            void* ws, size_t ws_bytes, void* stream);
 
 /*
  * cf_bias_lrelu_pool_bwd without a workspace argument, for callers that

@@ -733,3 +733,107 @@ def muon_step(w, g, m, lr, scale, momentum=0.95, nesterov=True, weight_decay=0.0
     m = momentum * m + g
     u = g + momentum * m if nesterov else m
     return w * (1.0 - lr * weight_decay) - lr * scale * newton_schulz(u, steps, coef, eps), m
+
+
+# ------------------------------------------------- products with an epilogue, residual norms, clipping (64 bits)
+def linear_act(z, act="none", slope=1.0):
+    if act == "gelu":
+        return 0.5 * z * (1 + np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)))
+    if act == "silu":
+        return z / (1 + np.exp(-z))
+    return np.where(z > 0, z, slope * z) if act == "lrelu" else z
+
+
+def linear_act_grad(z, act="none", slope=1.0):
+    if act == "gelu":
+        t = np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3))
+        return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * z ** 2)
+    if act == "silu":
+        e = 1 / (1 + np.exp(-z))
+        return e * (1 + z * (1 - e))
+    return np.where(z > 0, 1.0, slope) if act == "lrelu" else np.ones_like(z)
+
+
+def linear_fwd(x, w, bias=None, residual=None, act="none", slope=1.0, scale=1.0):
+    """(y, z) of z = x w^T + b, y = residual + scale act(z)."""
+    z = x @ w.T + (0.0 if bias is None else bias)
+    return scale * linear_act(z, act, slope) + (0.0 if residual is None else residual), z
+
+
+def linear_dgrad(dz, w, pre=None, add=None, act="none", slope=1.0, scale=1.0):
+    """dx = add + scale (dz w) act'(pre)."""
+    return scale * (dz @ w) * (1.0 if pre is None else linear_act_grad(pre, act, slope)) + (0.0 if add is None else add)
+
+
+def linear_wgrad(x, dz, scale=1.0):
+    return scale * dz.T @ x, scale * dz.sum(0)
+
+
+def _row_norm(v, kind, eps):
+    """(normalised values, mean, rstd) of each row; kind "none", "rms" or "layer"."""
+    mean = v.mean(1) if kind == "layer" else np.zeros(len(v))
+    rstd = 1 / np.sqrt(((v - mean[:, None]) ** 2).mean(1) + eps) if kind != "none" else np.ones(len(v))
+    return (v - mean[:, None]) * rstd[:, None], mean, rstd
+
+
+def _rows_of(v, rows, per):
+    """A vector beside rows: [c], or [samples][c] with `per` rows a sample; None for None."""
+    return v if v is None or v.ndim == 1 else np.repeat(v, per, 0)[:rows]
+
+
+def _apply(vh, gamma, beta):
+    return vh * (1.0 if gamma is None else gamma) + (0.0 if beta is None else beta)
+
+
+def residual_norm_fwd(x, f, vec, post="none", pre="none", scale=1.0, eps=1e-5, per=0):
+    """r = x + scale gate N_post(f), h = N_pre(r) (None without a norm) and the rows' statistics [rows][4]; vec: a dict of
+    post_gamma, post_beta, gate, pre_gamma, pre_beta ([c], or [samples][c] of `per` rows each)."""
+    rows = len(x)
+    v = {k: _rows_of(vec.get(k), rows, per) for k in ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")}
+    r, mf, sf = x, np.zeros(rows), np.ones(rows)
+    if f is not None:
+        fh, mf, sf = _row_norm(f, post, eps)
+        r = x + scale * (1.0 if v["gate"] is None else v["gate"]) * _apply(fh, v["post_gamma"], v["post_beta"])
+    rh, mr, sr = _row_norm(r, pre, eps)
+    return r, None if pre == "none" else _apply(rh, v["pre_gamma"], v["pre_beta"]), np.stack((mf, sf, mr, sr), 1)
+
+
+def residual_norm_bwd(f, r, vec, dh, dr, post="none", pre="none", scale=1.0, eps=1e-5, per=0):
+    """dx, df and a dict of the vectors' gradients, from r itself (h = N_pre(r)) and f."""
+    rows = len(r)
+    v = {k: _rows_of(vec.get(k), rows, per) for k in ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")}
+
+    def back(u, vh, rstd, kind):
+        d = u - vh * (u * vh).mean(1, keepdims=True)
+        return rstd[:, None] * (d - u.mean(1, keepdims=True) if kind == "layer" else d) if kind != "none" else u
+
+    def total(t, name):
+        o = vec.get(name)
+        if o is None or o.ndim == 1:
+            return t.sum(0)
+        return np.stack([t[i * per:(i + 1) * per].sum(0) for i in range(len(o))])
+
+    grads, dx = {}, np.zeros_like(r) if dr is None else dr
+    if pre != "none":
+        rh, _, sr = _row_norm(r, pre, eps)
+        grads["pre_gamma"], grads["pre_beta"] = total(dh * rh, "pre_gamma"), total(dh, "pre_beta")
+        dx = dx + back(dh * (1.0 if v["pre_gamma"] is None else v["pre_gamma"]), rh, sr, pre)
+    if f is None:
+        return dx, None, grads
+    fh, _, sf = _row_norm(f, post, eps)
+    grads["gate"] = total(scale * dx * _apply(fh, v["post_gamma"], v["post_beta"]), "gate")
+    dp = scale * dx * (1.0 if v["gate"] is None else v["gate"])
+    grads["post_gamma"], grads["post_beta"] = (dp * fh).sum(0), dp.sum(0)
+    return dx, back(dp * (1.0 if v["post_gamma"] is None else v["post_gamma"]), fh, sf, post), grads
+
+
+def clip_factor(grads, max_norm):
+    """(norm, factor) of a list of gradients."""
+    norm = np.sqrt(sum(float((g.astype(np.longdouble) ** 2).sum()) for g in grads))
+    return norm, min(1.0, max_norm / (norm + 1e-6))
+
+
+def adam_decay_step(w, g, m, v, lr, t, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0):
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    return (1 - lr * weight_decay) * w - lr * (m / (1 - beta1 ** t)) / (np.sqrt(v / (1 - beta2 ** t)) + eps), m, v
