@@ -1,128 +1,26 @@
 // linear.cu -- matrix products of bf16 rows with bias, activation and residual in the epilogue (forward), with the activation's
 // derivative in it (backward data), and summed over the rows (backward weight), with their entry points.
+//
+// The products run in linear_gemm.cuh's kernel; here are its plans, the copies of operands whose rows TMA cannot fetch (they start
+// at no multiple of 16 bytes), the activation's own backward and the checks.
 #include <algorithm>
 #include <cmath>
 
-#include "cf_internal.h"
-#include "cf_ptx.cuh"
+#include "linear_gemm.cuh"
 
 namespace cf {
 namespace {
 
-enum { ACT_LRELU = CF_ACT_LRELU, ACT_SILU = CF_ACT_SILU, ACT_GELU = CF_ACT_GELU };
-
-constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
-constexpr float kGeluB = 0.044715f;
-
-// 1 / (1 + exp(-t))
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
-
-__device__ __forceinline__ float act_of(int act, float slope, float z) {
-    if (act == ACT_LRELU) return z > 0.f ? z : slope * z;
-    return z * sigmoid(act == ACT_SILU ? z : kGeluA * fmaf(kGeluB * z, z * z, z));
-}
-__device__ __forceinline__ float act_grad(int act, float slope, float z) {
-    if (act == ACT_LRELU) return z > 0.f ? 1.f : slope;
-    z = z > 100.f ? 100.f : z < -100.f ? -100.f : z;  // 1 and 0 beyond, where products with 1 - e would be inf times 0
-    if (act == ACT_SILU) {
-        const float e = sigmoid(z);
-        return fmaf(z * e, 1.f - e, e);
-    }
-    const float e = sigmoid(kGeluA * fmaf(kGeluB * z, z * z, z));
-    return fmaf(z * e * (1.f - e), kGeluA * fmaf(3.f * kGeluB * z, z, 1.f), e);
-}
-
-// What the epilogue of a product needs: D [m][n], pitch values a row.
-struct Epi {
-    const float* bias;
-    const void* add;        // residual
-    const uint16_t* pre_in; // backward data: the derivative's argument
-    uint16_t* pre_out;
-    void* out;
-    int64_t pitch;
-    int act, f32, accumulate;
-    float slope, scale;
-};
-
-enum { OP_FWD = CF_LINEAR_FWD, OP_DGRAD = CF_LINEAR_DGRAD, OP_WGRAD = CF_LINEAR_WGRAD };
-
-template <int OP>
-__device__ __forceinline__ void finish(const Epi& E, int64_t i, int j, float acc) {
-    const int64_t o = i * E.pitch + j;
-    float v;
-    if (OP == OP_FWD) {
-        const float z = acc + (E.bias ? E.bias[j] : 0.f);
-        if (E.pre_out) E.pre_out[o] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-        v = E.scale * act_of(E.act, E.slope, z);
-    } else {
-        v = E.scale * acc;
-        if (OP == OP_DGRAD && E.pre_in) v *= act_grad(E.act, E.slope, bf16_bits_to_float(E.pre_in[o]));
-    }
-    if (OP == OP_WGRAD) {
-        float* d = static_cast<float*>(E.out) + o;
-        *d = E.accumulate ? *d + v : v;
-        return;
-    }
-    if (E.f32) {
-        if (E.add) v += static_cast<const float*>(E.add)[o];
-        static_cast<float*>(E.out)[o] = v;
-    } else {
-        if (E.add) v += bf16_bits_to_float(static_cast<const uint16_t*>(E.add)[o]);
-        static_cast<uint16_t*>(E.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
-}
-
-// A(i, k) and B(j, k) at their strides.
-struct Operands {
-    const uint16_t *a, *b;
-    int64_t ai, ak, bj, bk, m, k;
-    int n;
-};
-
-// 64 x 64 outputs to a block, 4 x 4 to a thread, 16 of the contracted axis at a time.
-template <int OP>
-__global__ void __launch_bounds__(256) linear_kernel(const Operands P, const Epi E) {
-    __shared__ float as[16][65], bs[16][65];
-    const int64_t i0 = (int64_t)blockIdx.x * 64;
-    const int j0 = blockIdx.y * 64, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < P.k; k0 += 16) {
-        for (int e = threadIdx.x; e < 1024; e += 256) {
-            // along the axis that is contiguous
-            const int ka = P.ak == 1 ? e & 15 : e >> 6, ia = P.ak == 1 ? e >> 4 : e & 63;
-            const int kb = P.bk == 1 ? e & 15 : e >> 6, jb = P.bk == 1 ? e >> 4 : e & 63;
-            as[ka][ia] = i0 + ia < P.m && k0 + ka < P.k ? bf16_bits_to_float(P.a[(i0 + ia) * P.ai + (k0 + ka) * P.ak]) : 0.f;
-            bs[kb][jb] = j0 + jb < P.n && k0 + kb < P.k ? bf16_bits_to_float(P.b[(j0 + jb) * P.bj + (k0 + kb) * P.bk]) : 0.f;
-        }
-        __syncthreads();
+// [rows][width] at any pitch as rows of `to` values, a multiple of 8; what is behind a row's end is not read by anyone.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const uint16_t* src, int64_t rows, int width, int64_t pitch, uint16_t* dst, int to) {
+    const int per = to / 8;
+    for (int64_t e = blockIdx.x * (int64_t)256 + threadIdx.x; e < rows * per; e += (int64_t)gridDim.x * 256) {
+        const int64_t i = e / per;
+        const int j = (int)(e - i * per) * 8;
+        uint32_t u[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(as[k][ty + 16 * a], bs[k][tx + 16 * b], acc[a][b]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            if (i0 + ty + 16 * a < P.m && j0 + tx + 16 * b < P.n) finish<OP>(E, i0 + ty + 16 * a, j0 + tx + 16 * b, acc[a][b]);
-}
-
-// db = scale sum of the rows of dz: 32 columns to a block.
-__global__ void __launch_bounds__(256) linear_bias_kernel(const uint16_t* dz, int64_t rows, int n, int64_t pitch, float scale, int accumulate,
-                                                          float* db) {
-    __shared__ float red[8][32];
-    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (j < n)
-        for (int64_t i = q; i < rows; i += 8) s += bf16_bits_to_float(dz[i * pitch + j]);
-    red[q][lane] = s;
-    __syncthreads();
-    if (q == 0 && j < n) {
-        for (int i = 1; i < 8; ++i) s += red[i][lane];
-        db[j] = accumulate ? db[j] + scale * s : scale * s;
+        for (int x = 0; x < 8; ++x) u[x] = j + x < width ? src[i * pitch + j + x] : 0;
+        *reinterpret_cast<uint4*>(dst + i * to + j) = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
     }
 }
 
@@ -151,10 +49,111 @@ cf_status check(const cf_linear_desc* d) {
 int64_t x_pitch(const cf_linear_desc* d) { return d->x_pitch ? d->x_pitch : d->k; }
 int64_t y_pitch(const cf_linear_desc* d) { return d->y_pitch ? d->y_pitch : d->n; }
 
-template <int OP>
-cf_status product(const LaunchCtx& ctx, const Operands& P, const Epi& E) {
-    linear_kernel<OP><<<dim3((unsigned)((P.m + 63) / 64), (unsigned)((P.n + 63) / 64)), 256, 0, ctx.stream>>>(P, E);
+constexpr int kPlanSms = 152;  // work is cut for so many SMs: workspaces are laid out without asking the device
+
+// An operand as it lies in memory: `rows` rows of `width` values, the contracted axis along them (K-major) or across.
+struct Side {
+    int64_t rows, width, pitch;
+    bool mn;
+    bool packed() const { return pitch % 8 != 0; }
+    int64_t kept() const { return packed() ? (width + 7) / 8 * 8 : pitch; }
+    size_t bytes() const { return packed() ? ((size_t)rows * kept() * 2 + 255) / 256 * 256 : 0; }
+};
+struct Product {
+    LinPlan plan;
+    Side a, b;
+    size_t part, dpart;  // bytes
+    size_t bytes() const { return a.bytes() + b.bytes() + part + dpart; }
+};
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t over(int64_t v, int64_t by) { return (v + by - 1) / by; }
+
+// Rows that fill a tile's 128 lanes no more than once go to its columns, and the other side to the lanes: twice as many tiles, each
+// with as little of the rows as there is.  Likewise a k of at most 128 in the backward weight beside a wider n.
+bool exchanged(int op, int64_t rows, int64_t k, int64_t n) { return op == OP_WGRAD ? k <= 128 && n > 128 : rows <= 128; }
+
+Product plan_of(const cf_linear_desc* d, int op) {
+    const Side x{d->rows, d->k, x_pitch(d), op == OP_WGRAD}, w{d->n, d->k, d->k, op == OP_DGRAD}, dz{d->rows, d->n, y_pitch(d), op == OP_WGRAD};
+    Product P{};
+    LinGemm& G = P.plan.g;
+    P.plan.swap = exchanged(op, d->rows, d->k, d->n);
+    P.a = op == OP_FWD ? x : dz;
+    P.b = op == OP_WGRAD ? x : w;
+    G.m = op == OP_WGRAD ? d->n : d->rows;
+    G.n = op == OP_FWD ? d->n : d->k;
+    G.nkb = over(op == OP_FWD ? d->k : op == OP_DGRAD ? d->n : d->rows, 64);
+    if (P.plan.swap) std::swap(P.a, P.b), std::swap(G.m, G.n);
+    G.a_mn = P.a.mn, G.b_mn = P.b.mn;
+
+    // pairs where there are 256 x 256 tiles, and products enough
+    const int64_t wide = over(G.m, 256) * over(G.n, 256) * G.nkb;
+    P.plan.pair = !P.plan.swap && G.m > 128 && G.n > 128 && wide >= 8 * (kPlanSms / 2);
+    const int units = P.plan.pair ? kPlanSms / 2 : kPlanSms, step = P.plan.pair ? 32 : 16;
+    G.tm = over(G.m, P.plan.pair ? 256 : 128);
+    G.bn = (int)up(over(G.n, over(G.n, 256)), step);
+    if (!P.plan.pair && G.nkb <= 16)
+        while (G.bn > 64 && G.tm * over(G.n, G.bn / 2) <= units) G.bn = (int)up(G.bn / 2, 16);
+    G.tn = over(G.n, G.bn);
+    const int half = P.plan.pair ? G.bn / 2 : G.bn;
+    G.a_box = 128, G.b_box = half;
+    G.stage_bytes = (int)(16384 + (G.b_mn ? up(half, 64) * 128 : up(half * 128, 1024)));
+    G.stages = std::min<int>(kLinMostStages, kLinRing / G.stage_bytes);
+
+    // tiles over a whole number of rounds are cut where that saves more than the second launch and the parts take
+    const int64_t tiles = G.tm * G.tn, rounds = tiles / units, rem = tiles - rounds * units;
+    const double block = G.stage_bytes / 100e3, join = 4.0;  // us
+    const int64_t share = std::max<int64_t>(2, over(rem * G.nkb, units));
+    G.whole = tiles, G.rest = 0, G.share = 1;
+    if (rem && (G.nkb - share) * block > join) G.whole = tiles - rem, G.rest = rem * G.nkb, G.share = share;
+    G.units = (int)(G.whole ? std::min<int64_t>(units, tiles) : over(G.rest, G.share));
+    P.plan.cut = G.rest && share < G.nkb;
+    if (P.plan.cut) {
+        const size_t slots = 2 * (size_t)over(G.rest, G.share);
+        P.part = slots * (P.plan.pair ? 2 : 1) * 128 * G.bn * sizeof(float);
+        P.dpart = op == OP_WGRAD ? slots * 256 * sizeof(float) : 0;
+    }
+    return P;
+}
+
+cf_status pack(const LaunchCtx& ctx, const Side& s, const uint16_t*& at, char*& ws) {
+    if (!s.packed()) return CF_OK;
+    uint16_t* to = reinterpret_cast<uint16_t*>(ws);
+    const int64_t blocks = std::min<int64_t>(over(s.rows * s.kept() / 8, 256), 16 * ctx.num_sms);
+    linear_pack_kernel<<<(unsigned)blocks, 256, 0, ctx.stream>>>(at, s.rows, (int)s.width, s.pitch, to, (int)s.kept());
+    at = to;
+    ws += s.bytes();
     return status_of();
+}
+bool map_of(CUtensorMap* m, const Side& s, const uint16_t* at, int box) {
+    const uint64_t dims[2] = {(uint64_t)s.width, (uint64_t)s.rows}, strides[1] = {(uint64_t)s.kept() * 2};
+    const uint32_t boxes[2] = {64, (uint32_t)(s.mn ? 64 : box)};
+    return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, at, dims, strides, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int OP>
+cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b, LinEpi E, void* ws, size_t ws_bytes, void* stream) {
+    Product P = plan_of(d, OP);
+    if (P.bytes() && (ws == nullptr || ws_bytes < P.bytes())) return CF_ERR_WORKSPACE;
+    LaunchCtx ctx;
+    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
+    if (P.plan.swap) std::swap(a, b);
+    char* at = static_cast<char*>(ws);
+    if (const cf_status st = pack(ctx, P.a, a, at); st != CF_OK) return st;
+    if (const cf_status st = pack(ctx, P.b, b, at); st != CF_OK) return st;
+    LinGemm& G = P.plan.g;
+    G.part = reinterpret_cast<float*>(at);
+    G.dpart = reinterpret_cast<float*>(at + P.part);
+    G.status = ctx.status, G.wait_ns = ctx.wait_ns;
+    auto starts = [](const void* p, uintptr_t at) { return reinterpret_cast<uintptr_t>(p) % at == 0; };
+    E.wide = E.pitch % 16 == 0 && starts(E.out, 32) && starts(E.add, 32) && starts(E.pre_in, 32) && starts(E.pre_out, 32) ? 2 : E.pitch % 8 == 0;
+    CUtensorMap ta, tb;
+    if (!map_of(&ta, P.a, a, G.a_box) || !map_of(&tb, P.b, b, G.b_box)) return CF_ERR_CUDA;
+    return launch_linear<OP>(ctx, P.plan, ta, tb, E);
+}
+
+__global__ void __launch_bounds__(256) linear_zero_kernel(float* p, int64_t count) {
+    for (int64_t e = blockIdx.x * (int64_t)256 + threadIdx.x; e < count; e += (int64_t)gridDim.x * 256) p[e] = 0.f;
 }
 
 }  // namespace
@@ -165,8 +164,8 @@ using namespace cf;
 extern "C" {
 
 size_t cf_linear_workspace_size(const cf_linear_desc* desc, int32_t op) {
-    if (check(desc) != CF_OK || op < CF_LINEAR_FWD || op > CF_LINEAR_WGRAD) return 0;
-    return 0;
+    if (check(desc) != CF_OK || op < CF_LINEAR_FWD || op > CF_LINEAR_WGRAD || desc->rows == 0) return 0;
+    return plan_of(desc, op).bytes();
 }
 
 cf_status cf_linear_fwd(const cf_linear_desc* desc, const uint16_t* x, const uint16_t* w, const float* bias, const void* residual, void* y,
@@ -176,11 +175,10 @@ cf_status cf_linear_fwd(const cf_linear_desc* desc, const uint16_t* x, const uin
     if (!x || !w || !y) return CF_ERR_INVALID_ARG;
     for (const void* p : {(const void*)x, (const void*)w, (const void*)bias, residual, (const void*)y, (const void*)pre, (const void*)ws})
         if (!aligned16(p)) return CF_ERR_INVALID_ARG;
-    if (ws_bytes < cf_linear_workspace_size(desc, CF_LINEAR_FWD)) return CF_ERR_WORKSPACE;
-    LaunchCtx ctx;
-    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    const Operands P{x, w, x_pitch(desc), 1, desc->k, 1, desc->rows, desc->k, desc->n};
-    return product<OP_FWD>(ctx, P, Epi{bias, residual, nullptr, pre, y, y_pitch(desc), desc->act, desc->dtype == CF_DT_F32, 0, desc->slope, desc->scale});
+    return product<OP_FWD>(desc, x, w,
+                           LinEpi{bias, residual, nullptr, pre, y, nullptr, y_pitch(desc), desc->rows, desc->n, desc->act, desc->dtype == CF_DT_F32, 0,
+                                  0, desc->slope, desc->scale},
+                           ws, ws_bytes, stream);
 }
 
 cf_status cf_linear_act_bwd(const cf_linear_desc* desc, const void* dy, const uint16_t* pre, uint16_t* dz, void* stream) {
@@ -202,11 +200,10 @@ cf_status cf_linear_dgrad(const cf_linear_desc* desc, const uint16_t* dz, const 
     if (!dz || !w || !dx) return CF_ERR_INVALID_ARG;
     for (const void* p : {(const void*)dz, (const void*)w, (const void*)pre, add, (const void*)dx, (const void*)ws})
         if (!aligned16(p)) return CF_ERR_INVALID_ARG;
-    if (ws_bytes < cf_linear_workspace_size(desc, CF_LINEAR_DGRAD)) return CF_ERR_WORKSPACE;
-    LaunchCtx ctx;
-    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    const Operands P{dz, w, y_pitch(desc), 1, 1, desc->k, desc->rows, desc->n, desc->k};
-    return product<OP_DGRAD>(ctx, P, Epi{nullptr, add, pre, nullptr, dx, x_pitch(desc), desc->act, desc->dtype == CF_DT_F32, 0, desc->slope, desc->scale});
+    return product<OP_DGRAD>(desc, dz, w,
+                             LinEpi{nullptr, add, pre, nullptr, dx, nullptr, x_pitch(desc), desc->rows, desc->k, desc->act, desc->dtype == CF_DT_F32,
+                                    0, 0, desc->slope, desc->scale},
+                             ws, ws_bytes, stream);
 }
 
 cf_status cf_linear_wgrad(const cf_linear_desc* desc, const uint16_t* x, const uint16_t* dz, float* dw, float* db, int32_t accumulate, void* ws,
@@ -215,15 +212,20 @@ cf_status cf_linear_wgrad(const cf_linear_desc* desc, const uint16_t* x, const u
     if ((desc->rows && (!x || !dz)) || !dw) return CF_ERR_INVALID_ARG;
     for (const void* p : {(const void*)x, (const void*)dz, (const void*)dw, (const void*)db, (const void*)ws})
         if (!aligned16(p)) return CF_ERR_INVALID_ARG;
-    if (ws_bytes < cf_linear_workspace_size(desc, CF_LINEAR_WGRAD)) return CF_ERR_WORKSPACE;
-    LaunchCtx ctx;
-    if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    const Operands P{dz, x, 1, y_pitch(desc), 1, x_pitch(desc), desc->n, desc->rows, desc->k};
-    if (db) {
-        linear_bias_kernel<<<(desc->n + 31) / 32, 256, 0, ctx.stream>>>(dz, desc->rows, desc->n, y_pitch(desc), desc->scale, accumulate, db);
-        if (const cf_status st = status_of(); st != CF_OK) return st;
+    if (desc->rows == 0) {
+        LaunchCtx ctx;
+        if (accumulate) return CF_OK;
+        if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
+        const int64_t count = (int64_t)desc->n * desc->k;
+        linear_zero_kernel<<<(unsigned)std::min<int64_t>(over(count, 256), 16 * ctx.num_sms), 256, 0, ctx.stream>>>(dw, count);
+        if (const cf_status st = status_of(); st != CF_OK || !db) return st;
+        linear_zero_kernel<<<(unsigned)std::min<int64_t>(over(desc->n, 256), 16 * ctx.num_sms), 256, 0, ctx.stream>>>(db, desc->n);
+        return status_of();
     }
-    return product<OP_WGRAD>(ctx, P, Epi{nullptr, nullptr, nullptr, nullptr, dw, desc->k, CF_ACT_LRELU, 1, accumulate, 1.f, desc->scale});
+    return product<OP_WGRAD>(desc, dz, x,
+                             LinEpi{nullptr, nullptr, nullptr, nullptr, dw, db, desc->k, desc->n, desc->k, CF_ACT_LRELU, 1, accumulate != 0, 0, 1.f,
+                                    desc->scale},
+                             ws, ws_bytes, stream);
 }
 
 }  // extern "C"

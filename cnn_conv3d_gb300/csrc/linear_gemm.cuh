@@ -1,0 +1,677 @@
+// linear_gemm.cuh -- the product of linear.cu on the tensor cores: D [m][n] = sum over K of A [m][K] B [n][K] with an epilogue,
+// one kernel template for the three directions, instantiated by a translation unit each.
+//
+//   forward          A = x [rows][k],       B = w [n][k]                both with the contracted axis contiguous (K-major)
+//   backward data    A = dz [rows][n],      B = w as [K = n][k]         B with its rows contiguous (MN-major)
+//   backward weight  A = dz as [K = rows][n], B = x as [K = rows][k]    both MN-major
+// or the two exchanged (SWAP) where that side is narrow: few rows in the forward and the backward data, so that the weights' rows
+// fill the 128 lanes of a tile and the rows are its columns, and a narrow k in the backward weight.
+//
+// A CTA is a TMA warp, an issuing thread and eight epilogue warps.  Operands come in stages of 64 of the contracted axis (128-byte
+// rows, swizzled); tiles are 128 rows by up to 256 columns, or 256 by 256 on a pair of CTAs with one instruction for both, each CTA
+// fetching half of either side: then a stage costs 64 bytes of L2 a cycle and SM, where a lone CTA's would cost 96 of the about 70
+// that it gives.  The accumulator is double: the epilogue of a tile runs under the products of the next.
+//
+// Tiles are dealt out whole, and what is left over for a last, uneven round (or all of it, where there are fewer tiles than CTAs) in
+// even shares of 64-blocks of the contracted axis; tiles that are cut leave fp32 parts, joined in order by a second launch.
+#pragma once
+
+#include "cf_internal.h"
+#include "cf_pair.cuh"
+
+namespace cf {
+
+enum { OP_FWD = CF_LINEAR_FWD, OP_DGRAD = CF_LINEAR_DGRAD, OP_WGRAD = CF_LINEAR_WGRAD };
+
+// What the epilogue needs.  Rows and columns are the output's, not the tile's, whatever SWAP.
+struct LinEpi {
+    const float* bias;
+    const void* add;         // forward: residual
+    const uint16_t* pre_in;  // backward data: the derivative's argument
+    uint16_t* pre_out;       // forward
+    void* out;
+    float* db;               // backward weight: sums of dz's rows, or NULL
+    int64_t pitch, rows;
+    int cols;
+    int act, f32, accumulate;
+    int wide;                // 2: 16 values from a multiple of 16 on start at 32 bytes, 1: at 16, 0: anywhere
+    float slope, scale;
+};
+
+struct LinGemm {
+    int64_t m, n, nkb;       // D's sizes, 64-blocks of the contracted axis
+    int64_t tm, tn;          // tiles
+    int bn;                  // columns of a tile
+    int a_mn, b_mn;          // operands with their rows contiguous
+    int a_box, b_box;        // K-major: rows of a copy
+    int stages, stage_bytes;
+    int64_t whole;           // tiles that are dealt out whole
+    int64_t rest, share;     // blocks of the others, and a unit's of them
+    int units;               // CTAs or pairs
+    float *part, *dpart;     // parts of cut tiles: a unit's two slots of 128 x bn values a CTA; of db, 256 values a slot
+    int* status;
+    uint64_t wait_ns;
+};
+
+constexpr int kLinEpiWarps = 8;
+constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
+constexpr int kLinMostStages = 10;
+constexpr uint32_t kLinRing = 192 << 10;
+constexpr uint32_t kLinOnes = 16 << 10;                     // 128 rows of 64 ones (backward weight)
+constexpr uint32_t kLinSmem = kLinRing + kLinOnes + 1024;  // and alignment
+
+// ------------------------------------------------------------------------------------------------------------------ activations
+constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float t) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+    return r;
+}
+__device__ __forceinline__ float rcp(float t) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+    return r;
+}
+// 1 / (1 + exp(-t)), t = z for SiLU, kGeluA (z + kGeluB z^3) for GELU; infinities give 0 and 1.
+__device__ __forceinline__ float silu_gate(float z) { return rcp(1.f + ex2(-kLog2e * z)); }
+__device__ __forceinline__ float gelu_gate(float z) { return rcp(1.f + ex2(z * fmaf(z * z, -kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA))); }
+
+__device__ __forceinline__ float act_of(int act, float slope, float z) {
+    if (act == CF_ACT_LRELU) return z > 0.f ? z : slope * z;
+    return z * (act == CF_ACT_SILU ? silu_gate(z) : gelu_gate(z));
+}
+__device__ __forceinline__ float act_grad(int act, float slope, float z) {
+    if (act == CF_ACT_LRELU) return z > 0.f ? 1.f : slope;
+    z = z > 100.f ? 100.f : z < -100.f ? -100.f : z;  // 1 and 0 beyond, where products with 1 - e would be inf times 0
+    if (act == CF_ACT_SILU) {
+        const float e = silu_gate(z);
+        return fmaf(z * e, 1.f - e, e);
+    }
+    const float e = gelu_gate(z);
+    return fmaf(z * e * (1.f - e), kGeluA * fmaf(3.f * kGeluB * z, z, 1.f), e);
+}
+// The activation of all, with one branch.
+template <int N>
+__device__ __forceinline__ void activate(const LinEpi& E, float (&v)[N]) {
+    if (E.act == CF_ACT_LRELU) {
+        if (E.slope == 1.f) return;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = v[e] > 0.f ? v[e] : E.slope * v[e];
+    } else if (E.act == CF_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] *= silu_gate(v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] *= gelu_gate(v[e]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void times_grad(const LinEpi& E, const float (&z)[N], float (&v)[N]) {
+    if (E.act == CF_ACT_LRELU) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] *= z[e] > 0.f ? 1.f : E.slope;
+    } else if (E.act == CF_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] *= act_grad(CF_ACT_SILU, 0.f, z[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] *= act_grad(CF_ACT_GELU, 0.f, z[e]);
+    }
+}
+
+// --------------------------------------------------------------------------------------------------------- rows of the epilogue
+// 16 values of a row from o on, `cnt` of which there are.
+__device__ __forceinline__ void load16(const void* p, int f32, int64_t o, int wide, int cnt, float (&v)[16]) {
+    if (wide && cnt == 16) {
+        uint32_t u[16];
+        if (f32) {
+            const float* f = static_cast<const float*>(p) + o;
+            if (wide == 2) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 8)
+                    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                                 : "=r"(u[e]), "=r"(u[e + 1]), "=r"(u[e + 2]), "=r"(u[e + 3]), "=r"(u[e + 4]), "=r"(u[e + 5]), "=r"(u[e + 6]),
+                                   "=r"(u[e + 7])
+                                 : "l"(f + e));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(f + e);
+                    u[e] = q.x, u[e + 1] = q.y, u[e + 2] = q.z, u[e + 3] = q.w;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
+            return;
+        }
+        const uint16_t* h = static_cast<const uint16_t*>(p) + o;
+        if (wide == 2) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                         : "l"(h));
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(h), b = *reinterpret_cast<const uint4*>(h + 8);
+            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[2 * e] = __uint_as_float(u[e] << 16), v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        v[e] = e >= cnt ? 0.f : f32 ? static_cast<const float*>(p)[o + e] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[o + e]);
+}
+__device__ __forceinline__ void store16(void* p, int f32, int64_t o, int wide, int cnt, const float (&v)[16]) {
+    if (wide && cnt == 16) {
+        if (f32) {
+            float* f = static_cast<float*>(p) + o;
+            if (wide == 2) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 8)
+                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(f + e), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]),
+                                 "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]), "f"(v[e + 6]), "f"(v[e + 7])
+                                 : "memory");
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(f + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+            return;
+        }
+        uint16_t* h = static_cast<uint16_t*>(p) + o;
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        if (wide == 2) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(h), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
+                         "r"(u[5]), "r"(u[6]), "r"(u[7])
+                         : "memory");
+        } else {
+            *reinterpret_cast<uint4*>(h) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(h + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < cnt) {
+            if (f32)
+                static_cast<float*>(p)[o + e] = v[e];
+            else
+                static_cast<uint16_t*>(p)[o + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+        }
+}
+
+// 16 columns of row i from column j on.
+template <int OP>
+__device__ __forceinline__ void finish_row(const LinEpi& E, int64_t i, int j, float (&v)[16]) {
+    const int cnt = min(16, E.cols - j);
+    if (cnt <= 0) return;
+    const int64_t o = i * E.pitch + j;
+    float t[16];
+    if (OP == OP_FWD) {
+        if (E.bias) {
+            load16(E.bias, 1, j, 1, cnt, t);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += t[e];
+        }
+        if (E.pre_out) store16(E.pre_out, 0, o, E.wide, cnt, v);
+        activate(E, v);
+    } else if (OP == OP_DGRAD && E.pre_in) {
+        load16(E.pre_in, 0, o, E.wide, cnt, t);
+        times_grad(E, t, v);
+    }
+    const void* add = OP == OP_WGRAD ? (E.accumulate ? E.out : nullptr) : E.add;
+    if (add) {
+        load16(add, E.f32, o, E.wide, cnt, t);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = fmaf(E.scale, v[e], t[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] *= E.scale;
+    }
+    store16(E.out, E.f32, o, E.wide, cnt, v);
+}
+// N rows of column j from row i on (neighbouring threads have neighbouring columns).
+template <int OP, int N>
+__device__ __forceinline__ void finish_column(const LinEpi& E, int64_t i, int j, float (&v)[N]) {
+    if (j >= E.cols) return;
+    const int cnt = (int)min((int64_t)N, E.rows - i);
+    const int64_t o = i * E.pitch + j;
+    float t[N];
+    auto load = [&](const void* p, int f32) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            t[e] = e >= cnt ? 0.f
+                   : f32    ? static_cast<const float*>(p)[o + e * E.pitch]
+                            : bf16_bits_to_float(static_cast<const uint16_t*>(p)[o + e * E.pitch]);
+    };
+    if (OP == OP_FWD) {
+        const float b = E.bias ? E.bias[j] : 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            v[e] += b;
+            if (E.pre_out && e < cnt) E.pre_out[o + e * E.pitch] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+        }
+        activate(E, v);
+    } else if (OP == OP_DGRAD && E.pre_in) {
+        load(E.pre_in, 0);
+        times_grad(E, t, v);
+    }
+    const void* add = OP == OP_WGRAD ? (E.accumulate ? E.out : nullptr) : E.add;
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = 0.f;
+    if (add) load(add, E.f32);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float r = add ? fmaf(E.scale, v[e], t[e]) : E.scale * v[e];
+        if (e < cnt) {
+            if (E.f32)
+                static_cast<float*>(E.out)[o + e * E.pitch] = r;
+            else
+                static_cast<uint16_t*>(E.out)[o + e * E.pitch] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------------------------------- work
+struct LinItem {
+    int64_t mt, nt, kb0, kb1;
+    int slot;  // where a part goes, -1 for a whole tile
+};
+// Tiles in bands of eight rows of tiles, so that what runs at one time shares operands in L2.
+__device__ __forceinline__ void tile_of(const LinGemm& G, int64_t t, int64_t& mt, int64_t& nt) {
+    const int64_t band = t / (8 * G.tn), r = t - band * 8 * G.tn, high = min((int64_t)8, G.tm - 8 * band);
+    nt = r / high;
+    mt = 8 * band + r - nt * high;
+}
+struct LinWalk {
+    int unit;
+    int64_t t, at, end;
+    __device__ __forceinline__ LinWalk(const LinGemm& G, int u) : unit(u), t(u) {
+        at = min(u * G.share, G.rest), end = min(at + G.share, G.rest);
+    }
+    __device__ __forceinline__ bool next(const LinGemm& G, LinItem& s) {
+        if (t < G.whole) {
+            tile_of(G, t, s.mt, s.nt);
+            s.kb0 = 0, s.kb1 = G.nkb, s.slot = -1;
+            t += G.units;
+            return true;
+        }
+        if (at >= end) return false;
+        const int64_t e = at / G.nkb;
+        tile_of(G, G.whole + e, s.mt, s.nt);
+        s.kb0 = at - e * G.nkb;
+        s.kb1 = min(G.nkb, s.kb0 + end - at);
+        at += s.kb1 - s.kb0;
+        s.slot = s.kb1 - s.kb0 == G.nkb ? -1 : 2 * unit + (s.kb0 == 0);
+        return true;
+    }
+};
+
+struct LinShared {
+    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+struct LinRing {
+    int stage = 0;
+    uint32_t bits = 0, issued = 0;
+    __device__ __forceinline__ uint32_t parity() const { return (bits >> stage) & 1; }
+    __device__ __forceinline__ void next(int stages) {
+        bits ^= 1u << stage;
+        if (++stage == stages) stage = 0;
+    }
+};
+
+// The sums of dz's rows come from products with ones: they are taken with the first tile across the other side, into the
+// accumulator that is not the tile's, which therefore has to be free, and is only free again when the tile's epilogue is through.
+template <int OP, bool SWAP>
+__device__ __forceinline__ bool takes_sums(const LinEpi& E, const LinItem& s) {
+    return OP == OP_WGRAD && E.db && (SWAP ? s.mt : s.nt) == 0;
+}
+
+template <bool PAIR, int OP, bool SWAP>
+__global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                                                                     const __grid_constant__ LinGemm G, const __grid_constant__ LinEpi E) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ LinShared sh;
+    uint8_t* ones = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* ring = ones + kLinOnes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
+    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&ta);
+        tma_prefetch_desc(&tb);
+        for (int s = 0; s < kLinMostStages; ++s) {
+            mbar_init(&sh.full[s], PAIR && rank == 0 ? 2 : 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sh.tfull[a], 1);
+            mbar_init(&sh.tempty[a], (PAIR ? 2 : 1) * kLinEpiWarps);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (OP == OP_WGRAD) {
+        for (int e = threadIdx.x; e < (int)kLinOnes / 4; e += kLinThreads) reinterpret_cast<uint32_t*>(ones)[e] = 0x3F803F80u;
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(&sh.tmem, 512);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+
+    LinWalk way(G, unit);
+    LinItem s;
+    LinRing R;
+    if (warp == 0) {
+        // a lane for each copy of a stage: one of A's (two where it is MN-major), the others of B's
+        const int bhalf = PAIR ? G.bn / 2 : G.bn;
+        const bool isb = lane >= 2;
+        const int q = isb ? lane - 2 : lane;
+        bool ok = true;
+        while (ok && way.next(G, s)) {
+            const int64_t m0 = s.mt * (PAIR ? 256 : 128) + 128 * rank, n0 = s.nt * G.bn + bhalf * rank;
+            const int na = G.a_mn ? (int)min((int64_t)2, max((int64_t)0, (G.m - m0 + 63) / 64)) : 1;
+            const int nb = G.b_mn ? (int)min((int64_t)(bhalf + 63) / 64, max((int64_t)0, (G.n - n0 + 63) / 64)) : 1;
+            const uint32_t bytes = (G.a_mn ? na * 8192 : 16384) + (G.b_mn ? nb * 8192 : G.b_box * 128);
+            const bool mn = isb ? G.b_mn : G.a_mn, mine = q < (isb ? nb : na);
+            const int64_t r0 = isb ? n0 : m0;
+            const uint32_t dst = (isb ? 16384 : 0) + q * 8192;
+            const CUtensorMap* map = isb ? &tb : &ta;
+            for (int64_t kb = s.kb0; kb < s.kb1; ++kb) {
+                ok = __all_sync(~0u, mbar_wait(&sh.empty[R.stage], R.parity() ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_PRODUCER_EMPTY));
+                if (!ok) break;
+                uint64_t* bar = &sh.full[R.stage];
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+                if (mine) {
+                    uint8_t* to = ring + R.stage * G.stage_bytes + dst;
+                    if (mn)
+                        tma_load_2d(to, map, bar, (int)(r0 + 64 * q), (int)(64 * kb));
+                    else
+                        tma_load_2d(to, map, bar, (int)(64 * kb), (int)r0);
+                }
+                R.issued |= 1u << R.stage;
+                R.next(G.stages);
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        const bool second = PAIR && rank == 1;
+        const uint32_t idesc = idesc_bf16(PAIR ? 256 : 128, G.bn, G.a_mn, G.b_mn);
+        // A's rows times ones [K][N]: 16 (32 for a pair) equal columns; exchanged, ones [128][K] times B: equal rows
+        const uint32_t idesc1 = SWAP ? idesc_bf16(128, G.bn, 0, G.b_mn) : idesc_bf16(PAIR ? 256 : 128, PAIR ? 32 : 16, G.a_mn, 0);
+        const uint64_t one = sdesc(smem_u32(ones), 16, 1024, SWZ_128B);
+        const uint32_t astep = G.a_mn ? 2048 : 32, bstep = G.b_mn ? 2048 : 32;
+        const uint32_t alead = G.a_mn ? 8192 : 16, blead = G.b_mn ? 8192 : 16;
+        bool alone = false;  // the tile before took sums
+        bool ok = true;
+        for (uint32_t local = 0; ok && way.next(G, s); ++local) {
+            if (second) {
+                for (int64_t kb = s.kb0; ok && kb < s.kb1; ++kb) {
+                    ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
+                    if (!ok) break;
+                    arrive_first(&sh.full[R.stage]);
+                    R.next(G.stages);
+                }
+                continue;
+            }
+            const uint32_t acc = local & 1, use = local >> 1, d = sh.tmem + acc * 256, d1 = sh.tmem + (acc ^ 1) * 256;
+            ok = mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
+            const bool sums = takes_sums<OP, SWAP>(E, s);
+            if (ok && (sums || alone) && local)  // the tile before is through: accumulator acc ^ 1, its use (local - 1) / 2
+                ok = mbar_wait(&sh.tempty[acc ^ 1], ((local - 1) >> 1) & 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
+            alone = sums;
+            tc_fence_after();
+            for (int64_t kb = s.kb0; ok && kb < s.kb1; ++kb) {
+                ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t as = smem_u32(ring + R.stage * G.stage_bytes), bs = as + 16384;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t ad = sdesc(as + k * astep, alead, 1024, SWZ_128B), bd = sdesc(bs + k * bstep, blead, 1024, SWZ_128B);
+                    const uint32_t more = kb > s.kb0 || k > 0;
+                    if (PAIR)
+                        umma_pair(d, ad, bd, idesc, more);
+                    else
+                        umma_bf16(d, ad, bd, idesc, more);
+                    if (OP == OP_WGRAD && sums) {
+                        if (PAIR)
+                            umma_pair(d1, ad, one, idesc1, more);
+                        else
+                            umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, more);
+                    }
+                }
+                if (PAIR)
+                    commit_pair(&sh.empty[R.stage]);
+                else
+                    umma_commit(&sh.empty[R.stage]);
+                R.next(G.stages);
+            }
+            if (!ok) break;
+            if (PAIR)
+                commit_pair(&sh.tfull[acc]);
+            else
+                umma_commit(&sh.tfull[acc]);
+        }
+    } else if (warp >= 2) {
+        // 16 columns of the thread's lane at a time, the two warps of a lane quarter in turn
+        const int q = warp & 3, turn = (warp - 2) >> 2, r = 32 * q + lane;
+        for (uint32_t local = 0; way.next(G, s); ++local) {
+            const uint32_t acc = local & 1, use = local >> 1;
+            const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
+            const int64_t i = s.mt * (PAIR ? 256 : 128) + 128 * rank + r, j0 = s.nt * G.bn;
+            float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
+            if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL)) break;
+            tc_fence_after();
+            for (int c = 16 * turn; c < G.bn; c += 32) {
+                uint32_t u[32];
+                tmem_ld16(tm + c, u);
+                tmem_ld_wait();
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
+                if (part) {
+                    if (SWAP) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            reinterpret_cast<float4*>(part)[((c + e) >> 2) * 128 + r] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    } else {
+                        store16(part, 1, (int64_t)r * G.bn + c, 2, 16, v);
+                    }
+                } else if (SWAP) {
+                    if (i < G.m) finish_column<OP>(E, j0 + c, (int)i, v);
+                } else if (i < G.m) {
+                    finish_row<OP>(E, i, (int)(j0 + c), v);
+                }
+                if (OP == OP_WGRAD && SWAP && takes_sums<OP, SWAP>(E, s)) {
+                    tmem_ld16(tm1 + c, u);
+                    tmem_ld_wait();
+                    if (r == 0) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int64_t j = j0 + c + e;
+                            const float b = __uint_as_float(u[e]);
+                            if (part)
+                                G.dpart[(int64_t)s.slot * 256 + c + e] = b;
+                            else if (j < G.n)
+                                E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
+                        }
+                    }
+                }
+            }
+            if (OP == OP_WGRAD && !SWAP && turn == 0 && takes_sums<OP, SWAP>(E, s)) {
+                uint32_t u[32];
+                tmem_ld16(tm1, u);
+                tmem_ld_wait();
+                const float b = __uint_as_float(u[0]);
+                if (part)
+                    G.dpart[(int64_t)s.slot * 256 + 128 * rank + r] = b;
+                else if (i < G.m)
+                    E.db[i] = E.accumulate ? fmaf(E.scale, b, E.db[i]) : E.scale * b;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR)
+                    arrive_first(&sh.tempty[acc]);
+                else
+                    mbar_arrive(&sh.tempty[acc]);
+            }
+        }
+    }
+    __syncwarp();
+    // after a wait that gave up: copies and products in flight end before the CTA leaves
+    if (*(volatile int*)&sh.abort) {
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < kLinMostStages; ++k)  // bits: the parity after a stage's last copy
+                if (R.issued & (1u << k)) mbar_wait_timed(&sh.full[k], ((R.bits >> k) & 1) ^ 1, G.wait_ns);
+        } else if (threadIdx.x == 32 && rank == 0) {
+            if (PAIR)
+                commit_pair(&sh.drain);
+            else
+                umma_commit(&sh.drain);
+            mbar_wait_timed(&sh.drain, 0, G.wait_ns);
+        }
+    }
+    tc_fence_before();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512) : "memory");
+        else
+            tmem_dealloc(sh.tmem, 512);
+    }
+}
+
+// The tiles that were cut, from their parts in order.  `ways` threads add a share of the parts of four values each; the values of
+// neighbouring threads are neighbours in a part (SWAP: along its rows).
+template <int OP, bool SWAP>
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinGemm G, const __grid_constant__ LinEpi E, int pair, int ways) {
+    __shared__ float4 red[256];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int values = pair ? 2 : 1, per = 256 / ways;                       // CTAs of a tile; float4s of a block
+    const int quads = values * 128 * G.bn / 4, blocks = (quads + per - 1) / per;  // of a tile
+    const int64_t e = blockIdx.x / blocks;
+    const int f = (int)(blockIdx.x - e * blocks) * per + (int)threadIdx.x % per, way = threadIdx.x / per;
+    const int64_t u0 = e * G.nkb / G.share, u1 = ((e + 1) * G.nkb - 1) / G.share;
+    if (u0 == u1) return;  // this tile was a unit's alone
+    int64_t mt, nt;
+    tile_of(G, G.whole + e, mt, nt);
+    const int64_t apart = (int64_t)values * 128 * G.bn / 4;
+    const float4* p = reinterpret_cast<const float4*>(G.part) + f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (f < quads) {
+#pragma unroll 8
+        for (int64_t u = u0 + way; u <= u1; u += ways) {
+            const float4 x = __ldcg(p + (2 * u + (u == u0)) * apart);
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+    }
+    red[threadIdx.x] = s;
+    __syncthreads();
+    if (way == 0 && f < quads) {
+        for (int w = 1; w < ways; ++w) {
+            const float4 x = red[w * per + threadIdx.x];
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+        const int cta = f / (32 * G.bn), in = f - cta * 32 * G.bn;
+        float v[4] = {s.x, s.y, s.z, s.w};
+        if (SWAP) {
+            finish_column<OP>(E, nt * G.bn + 4 * (in >> 7), (int)(mt * 128 + (in & 127)), v);
+        } else {
+            const int row = in / (G.bn / 4), c = 4 * (in - row * (G.bn / 4));
+            const int64_t i = mt * 128 * values + 128 * cta + row;
+            if (i < G.m) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float one[1] = {v[x]};
+                    finish_column<OP>(E, i, (int)(nt * G.bn) + c + x, one);
+                }
+            }
+        }
+    }
+    // db of the tile: 256 values, by the tile's first block
+    if (OP == OP_WGRAD && E.db && (SWAP ? mt : nt) == 0 && blockIdx.x == e * blocks) {
+        float b = 0.f;
+        for (int64_t u = u0; u <= u1; ++u) b += __ldcg(G.dpart + (2 * u + (u == u0)) * 256 + threadIdx.x);
+        const int64_t j = SWAP ? nt * G.bn + threadIdx.x : mt * 128 * values + threadIdx.x;
+        const bool there = SWAP ? (int)threadIdx.x < G.bn && j < G.n : (int)threadIdx.x < 128 * values && j < G.m;
+        if (there) E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
+    }
+}
+
+struct LinPlan {
+    LinGemm g;
+    bool pair, swap;
+    bool cut;  // some tile is in parts
+};
+
+// Both launches of a product; instantiated for each direction in a file of its own.
+template <int OP>
+cf_status launch_linear(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& ta, const CUtensorMap& tb, const LinEpi& E);
+
+#ifdef CF_LINEAR_OP
+namespace {
+template <bool PAIR, bool SWAP>
+cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& ta, const CUtensorMap& tb, const LinEpi& E) {
+    auto kernel = linear_gemm_kernel<PAIR, CF_LINEAR_OP, SWAP>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(P.g.units * (PAIR ? 2 : 1)));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kLinSmem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = PAIR ? 2 : 1;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, P.g, E) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
+    if (!P.cut) return CF_OK;
+    const int64_t tiles = P.g.rest / P.g.nkb, parts = (P.g.nkb + P.g.share - 1) / P.g.share + 1;
+    int ways = 1;
+    while (ways < 8 && 4 * ways < parts) ways *= 2;
+    const int quads = (PAIR ? 2 : 1) * 32 * P.g.bn, per = 256 / ways;
+    cfg.gridDim = dim3((unsigned)(tiles * ((quads + per - 1) / per)));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, linear_join_kernel<CF_LINEAR_OP, SWAP>, P.g, E, PAIR ? 1 : 0, ways) != cudaSuccess)
+        return cudaGetLastError(), CF_ERR_CUDA;
+    return CF_OK;
+}
+}  // namespace
+
+template <>
+cf_status launch_linear<CF_LINEAR_OP>(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& ta, const CUtensorMap& tb, const LinEpi& E) {
+    if (P.pair) return run_linear<true, false>(ctx, P, ta, tb, E);
+    return P.swap ? run_linear<false, true>(ctx, P, ta, tb, E) : run_linear<false, false>(ctx, P, ta, tb, E);
+}
+#endif
+
+}  // namespace cf

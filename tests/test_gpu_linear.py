@@ -149,6 +149,20 @@ def test_backward_weight_sizes(cf, rows, k, n):
     check_wgrad(cf, np.random.default_rng(rows + k + n), rows, k, n)
 
 
+# tiles of pairs, whole and cut, ends that fill neither half of a pair; many tiles of lone CTAs
+LARGE = [(1500, 3000, 1000), (5000, 520, 1290), (700, 9000, 400), (2048, 2048, 2048), (300, 20000, 272), (9000, 1032, 160), (50000, 64, 250),
+         (150, 5000, 2600)]
+
+
+@pytest.mark.parametrize("rows,k,n", LARGE)
+def test_large_products(cf, rows, k, n):
+    rng = np.random.default_rng(rows)
+    check_fwd(cf, rng, rows, k, n, "silu", pre=False)
+    check_dgrad(cf, rng, rows, n, k, "gelu", dtype=F32)
+    check_wgrad(cf, rng, n, k, rows)
+    check_wgrad(cf, rng, k, rows, n)
+
+
 @pytest.mark.parametrize("act,slope", [("none", 1.0), ("lrelu", 0.3), ("lrelu", 0.0), ("silu", 1.0), ("gelu", 1.0)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows", [4, 300])
