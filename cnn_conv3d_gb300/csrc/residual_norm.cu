@@ -189,6 +189,340 @@ __global__ void __launch_bounds__(kThreads) rn_bwd_cols_kernel(const RnArgs A, c
     }
 }
 
+// ------------------------------------------------------------------------------------------------ rows that registers hold at once
+// Eight values of a row to a thread: T threads of a warp to a row of up to 256 values (T a power of two, 32 / T rows of a warp at
+// once), or all of a block's (WIDE, up to 4096).  Where c is a multiple of eight a thread has neighbouring columns in 16-byte
+// accesses, otherwise columns T apart.  A block has the rows of a chunk of one sample, keeps the vectors in registers over them and
+// fetches a row's values while the one before is worked on.
+constexpr int kMostWide = 4096;
+
+template <bool VEC>
+struct Cols {
+    static constexpr bool vec = VEC;
+    int t, T, c;
+    __device__ __forceinline__ int at(int e) const { return vec ? 8 * t + e : t + T * e; }
+    __device__ __forceinline__ bool has(int e) const { return vec ? 8 * t < c : t + T * e < c; }
+};
+
+template <typename S>
+struct Raw {  // eight values as they are stored
+    uint32_t u[sizeof(S) * 2];
+};
+template <typename C_>
+__device__ __forceinline__ Raw<uint16_t> load8(const uint16_t* p, int64_t o, const C_& C) {
+    Raw<uint16_t> r;
+    if (C.vec) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (C.has(0)) v = __ldcg(reinterpret_cast<const uint4*>(p + o + 8 * C.t));
+        r.u[0] = v.x, r.u[1] = v.y, r.u[2] = v.z, r.u[3] = v.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a = C.has(2 * e) ? p[o + C.at(2 * e)] : 0, b = C.has(2 * e + 1) ? p[o + C.at(2 * e + 1)] : 0;
+            r.u[e] = a | b << 16;
+        }
+    }
+    return r;
+}
+template <typename C_>
+__device__ __forceinline__ Raw<float> load8(const float* p, int64_t o, const C_& C) {
+    Raw<float> r;
+    if (C.vec) {
+        uint4 v = make_uint4(0, 0, 0, 0), w = v;
+        if (C.has(0)) {
+            const uint4* q = reinterpret_cast<const uint4*>(p + o + 8 * C.t);
+            v = __ldcg(q), w = __ldcg(q + 1);
+        }
+        r.u[0] = v.x, r.u[1] = v.y, r.u[2] = v.z, r.u[3] = v.w, r.u[4] = w.x, r.u[5] = w.y, r.u[6] = w.z, r.u[7] = w.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.u[e] = C.has(e) ? __float_as_uint(p[o + C.at(e)]) : 0;
+    }
+    return r;
+}
+__device__ __forceinline__ void unpack(const Raw<uint16_t>& r, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[2 * e] = __uint_as_float(r.u[e] << 16), v[2 * e + 1] = __uint_as_float(r.u[e] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.u[e]);
+}
+template <typename C_>
+__device__ __forceinline__ void store8(uint16_t* p, int64_t o, const C_& C, const float (&v)[8]) {
+    if (C.vec) {
+        if (C.has(0))
+            *reinterpret_cast<uint4*>(p + o + 8 * C.t) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (C.has(e)) store(p, o + C.at(e), v[e]);
+    }
+}
+template <typename C_>
+__device__ __forceinline__ void store8(float* p, int64_t o, const C_& C, const float (&v)[8]) {
+    if (C.vec) {
+        if (C.has(0)) {
+            float4* q = reinterpret_cast<float4*>(p + o + 8 * C.t);
+            q[0] = make_float4(v[0], v[1], v[2], v[3]), q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (C.has(e)) p[o + C.at(e)] = v[e];
+    }
+}
+// A vector's eight values, `other` where there is none.
+template <typename C_>
+__device__ __forceinline__ void vector8(const float* p, int64_t o, const C_& C, float other, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = other;
+    if (p == nullptr) return;
+    if (C.vec) {
+        if (C.has(0)) {
+            const float4* q = reinterpret_cast<const float4*>(p + o + 8 * C.t);
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (C.has(e)) v[e] = p[o + C.at(e)];
+    }
+}
+
+// Sums over a row's threads, the same in each of them.  WIDE: one barrier, the buffers in turn.
+template <bool WIDE>
+struct RowSum {
+    float2 (*red)[32];
+    int turn = 0, T;
+    __device__ __forceinline__ float2 operator()(float a, float b) {
+        for (int o = (WIDE ? 32 : T) >> 1; o; o >>= 1) {
+            a += __shfl_xor_sync(~0u, a, o);
+            b += __shfl_xor_sync(~0u, b, o);
+        }
+        if (WIDE) {
+            float2* r = red[turn];
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
+            __syncthreads();
+            a = b = 0.f;
+            for (int i = 0; i < (int)(blockDim.x >> 5); ++i) a += r[i].x, b += r[i].y;
+        }
+        return make_float2(a, b);
+    }
+};
+
+// (mean, 1 / width) of a row that its threads hold eight values of each.
+template <bool WIDE, typename C_>
+__device__ __forceinline__ float2 stats8(const RnArgs& A, int kind, const C_& C, RowSum<WIDE>& sum, const float (&v)[8]) {
+    if (kind == CF_NORM_NONE) return make_float2(0.f, 1.f);
+    float mean = 0.f, s = 0.f;
+    if (kind == CF_NORM_LAYER) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[e];  // values that a thread does not have are 0
+        mean = sum(s, 0.f).x * A.inv_c;
+    }
+    s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = C.has(e) ? v[e] - mean : 0.f;
+        s = fmaf(t, t, s);
+    }
+    return make_float2(mean, rsqrtf(sum(s, 0.f).x * A.inv_c + A.eps));
+}
+
+// A block's chunk of rows, and the thread's place in them.
+struct Place {
+    int64_t from, to, sample;
+    int step;  // rows at once
+};
+template <bool WIDE, typename C_>
+__device__ __forceinline__ Place place_of(const RnArgs& A, int T, C_& C) {
+    Place P;
+    C.c = A.c, C.T = T;
+    C.t = WIDE ? threadIdx.x : threadIdx.x & (T - 1);
+    P.sample = blockIdx.x / A.chunks;
+    const int64_t first = P.sample * A.per + (blockIdx.x - P.sample * A.chunks) * A.chunk;
+    P.to = min(min(first + A.chunk, (P.sample + 1) * A.per), A.rows);
+    P.step = WIDE ? 1 : kThreads / T;
+    P.from = first + (WIDE ? 0 : (int)threadIdx.x / T);
+    return P;
+}
+
+template <typename S, typename F, bool WIDE, bool VEC>
+__global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 3) rn_fwd_kernel(const RnArgs A, int T, const S* x, const F* f, S* r, F* h,
+                                                                                     float4* stats) {
+    __shared__ float2 red[2][32];
+    Cols<VEC> C;
+    const Place P = place_of<WIDE>(A, T, C);
+    RowSum<WIDE> sum{red, 0, T};
+    float a[8], b[8], g[8], beta[8];
+    {
+        float gate[8];
+        vector8(A.gate, A.gate_each ? P.sample * A.c : 0, C, 1.f, gate);
+        vector8(A.post_gamma, 0, C, 1.f, a);
+        vector8(A.post_beta, 0, C, 0.f, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] *= A.scale * gate[e], b[e] *= A.scale * gate[e];
+        vector8(A.pre_gamma, A.pre_each ? P.sample * A.c : 0, C, 1.f, g);
+        vector8(A.pre_beta, A.pre_each ? P.sample * A.c : 0, C, 0.f, beta);
+    }
+    // all threads of a warp go round as often, for the shuffles
+    const int64_t rounds = (P.to - (P.from - (WIDE ? 0 : (int)threadIdx.x / T)) + P.step - 1) / P.step;
+    Raw<S> xn{};
+    Raw<F> fn{};
+    if (P.from < P.to) {
+        xn = load8(x, P.from * A.c, C);
+        if (f) fn = load8(f, P.from * A.c, C);
+    }
+    for (int64_t k = 0; k < rounds; ++k) {
+        const int64_t i = P.from + k * P.step, o = i * A.c;
+        const bool mine = i < P.to;
+        float v[8], w[8];
+        unpack(xn, v);
+        unpack(fn, w);
+        if (i + P.step < P.to) {
+            xn = load8(x, o + P.step * (int64_t)A.c, C);
+            if (f) fn = load8(f, o + P.step * (int64_t)A.c, C);
+        }
+        const float2 sf = f ? stats8<WIDE>(A, A.post, C, sum, w) : make_float2(0.f, 1.f);
+        if (f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = C.has(e) ? v[e] + fmaf(a[e], (w[e] - sf.x) * sf.y, b[e]) : 0.f;
+        }
+        if (r && mine) store8(r, o, C, v);
+        const float2 sr = stats8<WIDE>(A, A.pre, C, sum, v);
+        if (h && mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - sr.x) * sr.y, g[e], beta[e]);
+            store8(h, o, C, v);
+        }
+        if (stats && mine && C.t == 0) stats[i] = make_float4(sf.x, sf.y, sr.x, sr.y);
+    }
+}
+
+template <typename S, typename F, bool WIDE, bool VEC>
+__global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2) rn_bwd_kernel(const RnArgs A, int T, const F* f, const S* r, const float4* stats,
+                                                                                     const F* dh, const S* dr, S* dx, F* df, float* part) {
+    __shared__ float2 red[2][32];
+    Cols<VEC> C;
+    const Place P = place_of<WIDE>(A, T, C);
+    RowSum<WIDE> sum{red, 0, T};
+    float a[8], g[8];
+    {
+        float gate[8];
+        vector8(A.gate, A.gate_each ? P.sample * A.c : 0, C, 1.f, gate);
+        vector8(A.post_gamma, 0, C, 1.f, a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] *= A.scale * gate[e];
+        vector8(A.pre_gamma, A.pre_each ? P.sample * A.c : 0, C, 1.f, g);
+    }
+    float sa[8] = {}, sb[8] = {}, sc[8] = {}, sd[8] = {};
+    const int64_t rounds = (P.to - (P.from - (WIDE ? 0 : (int)threadIdx.x / T)) + P.step - 1) / P.step;
+    Raw<F> fn{}, dhn{};
+    Raw<S> rn{}, drn{};
+    float4 stn = make_float4(0.f, 1.f, 0.f, 1.f);
+    auto fetch = [&](int64_t i) {
+        const int64_t o = i * A.c;
+        stn = __ldcg(stats + i);
+        if (dh) rn = load8(r, o, C), dhn = load8(dh, o, C);
+        if (dr) drn = load8(dr, o, C);
+        if (f) fn = load8(f, o, C);
+    };
+    if (P.from < P.to) fetch(P.from);
+    for (int64_t k = 0; k < rounds; ++k) {
+        const int64_t i = P.from + k * P.step, o = i * A.c;
+        const bool mine = i < P.to;
+        float d[8], w[8];
+        float4 st = stn;
+        unpack(drn, d);
+        unpack(fn, w);
+        if (A.pre != CF_NORM_NONE) {
+            float rh[8], u[8];
+            unpack(rn, rh);
+            unpack(dhn, u);
+            if (i + P.step < P.to) fetch(i + P.step);
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                rh[e] = C.has(e) ? (rh[e] - st.z) * st.w : 0.f;
+                if (mine) sc[e] = fmaf(u[e], rh[e], sc[e]), sd[e] += u[e];
+                u[e] *= g[e];
+                m0 += u[e];
+                m1 = fmaf(u[e], rh[e], m1);
+            }
+            float2 m = sum(m0, m1);
+            m.x = A.pre == CF_NORM_LAYER ? m.x * A.inv_c : 0.f;
+            m.y *= A.inv_c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = C.has(e) ? fmaf(st.w, u[e] - m.x - rh[e] * m.y, d[e]) : 0.f;
+        } else if (i + P.step < P.to) {
+            fetch(i + P.step);
+        }
+        if (dx && mine) store8(dx, o, C, d);
+        if (f) {
+            float n0 = 0.f, n1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[e] = C.has(e) ? (w[e] - st.x) * st.y : 0.f;
+                if (mine) sa[e] = fmaf(d[e], w[e], sa[e]), sb[e] += d[e];
+                d[e] *= a[e];
+                n0 += d[e];
+                n1 = fmaf(d[e], w[e], n1);
+            }
+            if (A.post != CF_NORM_NONE) {
+                float2 n = sum(n0, n1);
+                n.x = A.post == CF_NORM_LAYER ? n.x * A.inv_c : 0.f;
+                n.y *= A.inv_c;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] = st.y * (d[e] - n.x - w[e] * n.y);
+            }
+            if (df && mine) store8(df, o, C, d);
+        } else if (mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sb[e] += d[e];
+        }
+    }
+    if (part == nullptr) return;
+    float* to = part + (int64_t)blockIdx.x * 4 * A.c;
+    auto put = [&](float (&v)[8], int which) {
+        float* p = to + (int64_t)which * A.c;
+        if (WIDE) {
+            if (C.vec) {
+                if (C.has(0)) {
+                    float4* q = reinterpret_cast<float4*>(p + 8 * C.t);
+                    q[0] = make_float4(v[0], v[1], v[2], v[3]), q[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (C.has(e)) p[C.at(e)] = v[e];
+            }
+        } else {
+            // the rows of a warp, then its warps in order
+            __shared__ float all[kThreads / 32][256];
+            for (int o = T; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(~0u, v[e], o);
+            __syncthreads();
+            if ((int)(threadIdx.x & 31) < T)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (C.has(e)) all[threadIdx.x >> 5][C.at(e)] = v[e];
+            __syncthreads();
+            if ((int)threadIdx.x < A.c) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < kThreads / 32; ++w) s += all[w][threadIdx.x];
+                p[threadIdx.x] = s;
+            }
+        }
+    };
+    put(sa, 0), put(sb, 1), put(sc, 2), put(sd, 3);
+}
+
 struct RnGrads {
     float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
 };
@@ -290,6 +624,17 @@ void cut(RnArgs& A, int64_t blocks, int64_t least) {
     A.chunks = (int)((per + A.chunk - 1) / A.chunk);
 }
 
+// Threads of a row: up to 256 values a part of a warp, up to kMostWide a block, beyond 0.
+int threads_of(int c) {
+    if (c > kMostWide) return 0;
+    if (c > 256) return (c + 255) / 256 * 32;
+    int T = 1;
+    while (8 * T < c) T *= 2;
+    return T;
+}
+// Blocks that the device holds, as many as the kernels' registers let it: of rows in warps `narrow` an SM, else 512 threads.
+int64_t resident(int T, int narrow) { return (int64_t)kPlanSms * (T <= 32 ? narrow : 512 / T); }
+
 struct Layout {
     float4* means;
     float *part, *sums;
@@ -303,7 +648,7 @@ Layout layout_of(const RnArgs& A, void* ws) {
         return p;
     };
     Layout L;
-    L.means = static_cast<float4*>(take((size_t)A.rows * sizeof(float4)));
+    L.means = static_cast<float4*>(take(A.c > kMostWide ? (size_t)A.rows * sizeof(float4) : 0));
     L.part = static_cast<float*>(take((size_t)A.samples * A.chunks * 4 * A.c * sizeof(float)));
     L.sums = static_cast<float*>(take(A.samples > 1 ? (size_t)A.samples * 4 * A.c * sizeof(float) : 0));
     L.bytes = std::max<size_t>(at, 256);
@@ -311,7 +656,12 @@ Layout layout_of(const RnArgs& A, void* ws) {
 }
 RnArgs plan_bwd(const cf_residual_norm_desc* d) {
     RnArgs A = args_of(d);
-    if (A.rows) cut(A, std::max(1, kPlanSms * 8 * 32 / A.c), 8);
+    if (A.rows == 0) return A;
+    const int T = threads_of(A.c);
+    if (T)
+        cut(A, resident(T, 2), T <= 32 ? kThreads / T : 1);
+    else
+        cut(A, std::max(1, kPlanSms * 8 * 32 / A.c), 8);
     return A;
 }
 
@@ -372,6 +722,14 @@ cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x,
     return with_types(desc, [&](auto s, auto t) {
         using S = decltype(s);
         using F = decltype(t);
+        if (const int T = threads_of(A.c); T) {
+            cut(A, resident(T, 3), T <= 32 ? kThreads / T : 1);
+            auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_fwd_kernel<S, F, false, true> : rn_fwd_kernel<S, F, true, true>)
+                                       : (T <= 32 ? rn_fwd_kernel<S, F, false, false> : rn_fwd_kernel<S, F, true, false>);
+            kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? kThreads : T, 0, ctx.stream>>>(
+                A, T, static_cast<const S*>(x), static_cast<const F*>(f), static_cast<S*>(r), static_cast<F*>(h), reinterpret_cast<float4*>(stats));
+            return status_of();
+        }
         rn_fwd_long_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(
             A, static_cast<const S*>(x), static_cast<const F*>(f), static_cast<S*>(r), static_cast<F*>(h), reinterpret_cast<float4*>(stats));
         return status_of();
@@ -416,11 +774,18 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
         const F *fs = static_cast<const F*>(f), *dhs = static_cast<const F*>(dh);
         const float4* st4 = reinterpret_cast<const float4*>(stats);
         const unsigned tiles = (A.c + 31) / 32;
-        rn_bwd_rows_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(A, fs, rs, st4, dhs, drs,
-                                                                                                                   L.means);
-        if (const cf_status st = status_of(); st != CF_OK) return st;
-        rn_bwd_cols_kernel<S, F><<<dim3((unsigned)(A.samples * A.chunks), tiles), kThreads, 0, ctx.stream>>>(
-            A, fs, rs, st4, dhs, drs, L.means, static_cast<S*>(dx), static_cast<F*>(df), L.part);
+        if (const int T = threads_of(A.c); T) {
+            auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_bwd_kernel<S, F, false, true> : rn_bwd_kernel<S, F, true, true>)
+                                       : (T <= 32 ? rn_bwd_kernel<S, F, false, false> : rn_bwd_kernel<S, F, true, false>);
+            kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? kThreads : T, 0, ctx.stream>>>(A, T, fs, rs, st4, dhs, drs, static_cast<S*>(dx),
+                                                                                               static_cast<F*>(df), sums ? L.part : nullptr);
+        } else {
+            rn_bwd_rows_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(A, fs, rs, st4, dhs, drs,
+                                                                                                                       L.means);
+            if (const cf_status st = status_of(); st != CF_OK) return st;
+            rn_bwd_cols_kernel<S, F><<<dim3((unsigned)(A.samples * A.chunks), tiles), kThreads, 0, ctx.stream>>>(
+                A, fs, rs, st4, dhs, drs, L.means, static_cast<S*>(dx), static_cast<F*>(df), L.part);
+        }
         if (const cf_status st = status_of(); st != CF_OK || !sums) return st;
         rn_sample_kernel<<<dim3((unsigned)A.samples, tiles), kThreads, 0, ctx.stream>>>(A, L.part, L.sums, G);
         if (const cf_status st = status_of(); st != CF_OK || A.samples == 1) return st;
