@@ -91,14 +91,14 @@ Product plan_of(const cf_linear_desc* d, int op) {
     P.plan.pair = !P.plan.swap && G.m > 128 && G.n > 128 && wide >= 8 * (kPlanSms / 2);
     const int units = P.plan.pair ? kPlanSms / 2 : kPlanSms, step = P.plan.pair ? 32 : 16;
     G.tm = over(G.m, P.plan.pair ? 256 : 128);
-    G.bn = (int)up(over(G.n, over(G.n, 256)), step);
+    // the epilogue's passes of 64 columns end with a tile where another follows
+    G.bn = (int)up(over(G.n, over(G.n, 256)), G.n > 256 ? 64 : step);
     if (!P.plan.pair && G.nkb <= 16)
-        while (G.bn > 64 && G.tm * over(G.n, G.bn / 2) <= units) G.bn = (int)up(G.bn / 2, 16);
+        while (G.bn > 64 && G.tm * over(G.n, up(G.bn / 2, 64)) <= units) G.bn = (int)up(G.bn / 2, 64);
     G.tn = over(G.n, G.bn);
     const int half = P.plan.pair ? G.bn / 2 : G.bn;
     G.a_box = 128, G.b_box = half;
     G.stage_bytes = (int)(16384 + (G.b_mn ? up(half, 64) * 128 : up(half * 128, 1024)));
-    G.stages = std::min<int>(kLinMostStages, kLinRing / G.stage_bytes);
 
     // tiles over a whole number of rounds are cut where that saves more than the second launch and the parts take
     const int64_t tiles = G.tm * G.tn, rounds = tiles / units, rem = tiles - rounds * units;
@@ -142,14 +142,37 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
     if (const cf_status st = pack(ctx, P.a, a, at); st != CF_OK) return st;
     if (const cf_status st = pack(ctx, P.b, b, at); st != CF_OK) return st;
     LinGemm& G = P.plan.g;
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    LinMaps M{};
+    uint32_t room = kLinRoom - (OP == OP_WGRAD ? kLinOnes : 0);
+    if (!P.plan.swap) {
+        LinStage& S = G.st;
+        if (OP == OP_WGRAD && E.accumulate) E.add = E.out;
+        const bool aux = E.pre_in || E.pre_out;
+        S.load_add = E.add != nullptr, S.load_aux = E.pre_in != nullptr;
+        // a stored row that ends inside 16 bytes would fill them up
+        S.tma = E.pitch % 8 == 0 && E.cols % 8 == 0;
+        S.gw = E.f32 && !aux ? 32 : 64;
+        S.out_bytes = S.gw * (E.f32 ? 128 : 64), S.aux_bytes = aux ? 4096 : 0;
+        // two buffers where the epilogue is most of a tile's time, and two stages fit beside them
+        const uint32_t pass = kLinEpiWarps * (S.out_bytes + S.aux_bytes);
+        S.buffers = G.nkb <= 8 && room - 2 * pass >= 2u * G.stage_bytes ? 2 : 1;
+        room -= S.buffers * pass;
+        auto rows_map = [&](CUtensorMap* m, const void* p, bool f32) {
+            const uint64_t dims[2] = {(uint64_t)E.cols, (uint64_t)E.rows}, strides[1] = {(uint64_t)E.pitch * (f32 ? 4 : 2)};
+            const uint32_t box[2] = {f32 ? 32u : 64u, 32};
+            return encode_tmap(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        const void* pre = OP == OP_FWD ? E.pre_out : E.pre_in;
+        if (S.tma && (!rows_map(&M.out, E.out, E.f32) || (E.add && !rows_map(&M.add, E.add, E.f32)) || (aux && !rows_map(&M.aux, pre, false))))
+            return CF_ERR_CUDA;
+    }
+    G.stages = std::min<int>(kLinMostStages, room / G.stage_bytes);
     G.part = reinterpret_cast<float*>(at);
     G.dpart = reinterpret_cast<float*>(at + P.part);
     G.status = ctx.status, G.wait_ns = ctx.wait_ns;
-    auto starts = [](const void* p, uintptr_t at) { return reinterpret_cast<uintptr_t>(p) % at == 0; };
-    E.wide = E.pitch % 16 == 0 && starts(E.out, 32) && starts(E.add, 32) && starts(E.pre_in, 32) && starts(E.pre_out, 32) ? 2 : E.pitch % 8 == 0;
-    CUtensorMap ta, tb;
-    if (!map_of(&ta, P.a, a, G.a_box) || !map_of(&tb, P.b, b, G.b_box)) return CF_ERR_CUDA;
-    return launch_linear<OP>(ctx, P.plan, ta, tb, E);
+    if (!map_of(&M.a, P.a, a, G.a_box) || !map_of(&M.b, P.b, b, G.b_box)) return CF_ERR_CUDA;
+    return launch_linear<OP>(ctx, P.plan, M, E);
 }
 
 __global__ void __launch_bounds__(256) linear_zero_kernel(float* p, int64_t count) {
@@ -177,7 +200,7 @@ cf_status cf_linear_fwd(const cf_linear_desc* desc, const uint16_t* x, const uin
         if (!aligned16(p)) return CF_ERR_INVALID_ARG;
     return product<OP_FWD>(desc, x, w,
                            LinEpi{bias, residual, nullptr, pre, y, nullptr, y_pitch(desc), desc->rows, desc->n, desc->act, desc->dtype == CF_DT_F32, 0,
-                                  0, desc->slope, desc->scale},
+                                  desc->slope, desc->scale},
                            ws, ws_bytes, stream);
 }
 
@@ -202,7 +225,7 @@ cf_status cf_linear_dgrad(const cf_linear_desc* desc, const uint16_t* dz, const 
         if (!aligned16(p)) return CF_ERR_INVALID_ARG;
     return product<OP_DGRAD>(desc, dz, w,
                              LinEpi{nullptr, add, pre, nullptr, dx, nullptr, x_pitch(desc), desc->rows, desc->k, desc->act, desc->dtype == CF_DT_F32,
-                                    0, 0, desc->slope, desc->scale},
+                                    0, desc->slope, desc->scale},
                              ws, ws_bytes, stream);
 }
 
@@ -223,7 +246,7 @@ cf_status cf_linear_wgrad(const cf_linear_desc* desc, const uint16_t* x, const u
         return status_of();
     }
     return product<OP_WGRAD>(desc, dz, x,
-                             LinEpi{nullptr, nullptr, nullptr, nullptr, dw, db, desc->k, desc->n, desc->k, CF_ACT_LRELU, 1, accumulate != 0, 0, 1.f,
+                             LinEpi{nullptr, nullptr, nullptr, nullptr, dw, db, desc->k, desc->n, desc->k, CF_ACT_LRELU, 1, accumulate != 0, 1.f,
                                     desc->scale},
                              ws, ws_bytes, stream);
 }

@@ -34,11 +34,22 @@ struct LinEpi {
     int64_t pitch, rows;
     int cols;
     int act, f32, accumulate;
-    int wide;                // 2: 16 values from a multiple of 16 on start at 32 bytes, 1: at 16, 0: anywhere
     float slope, scale;
 };
 
+// The epilogue's way to rows in memory: a warp's 32 rows x `gw` columns pass through shared memory (128-byte rows, swizzled, in
+// slabs of 4 KB), from and to which TMA copies them.  A lane owns a row, so that its own accesses to memory would be 32 lines an
+// instruction: stores that way took the data pipe 57 cycles a kilobyte and 64 -> 256 on 2.1M voxels 731 us.
+struct LinStage {
+    int tma;                   // rows begin and end at 16 bytes; otherwise a warp copies value by value along the rows
+    int gw;                    // columns of a pass: 64, or 32 of fp32 with no pre-activation beside them
+    int buffers;               // 1, or 2: what is loaded of the next pass comes under the present one
+    int out_bytes, aux_bytes;  // of a buffer: the output (and what is added to it, in the same place), the pre-activation
+    int load_add, load_aux;
+};
+
 struct LinGemm {
+    LinStage st;
     int64_t m, n, nkb;       // D's sizes, 64-blocks of the contracted axis
     int64_t tm, tn;          // tiles
     int bn;                  // columns of a tile
@@ -56,9 +67,9 @@ struct LinGemm {
 constexpr int kLinEpiWarps = 8;
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
 constexpr int kLinMostStages = 10;
-constexpr uint32_t kLinRing = 192 << 10;
-constexpr uint32_t kLinOnes = 16 << 10;                     // 128 rows of 64 ones (backward weight)
-constexpr uint32_t kLinSmem = kLinRing + kLinOnes + 1024;  // and alignment
+constexpr uint32_t kLinOnes = 16 << 10;             // 128 rows of 64 ones (backward weight)
+constexpr uint32_t kLinSmem = 232448 - 1024;        // dynamic: all but the barriers
+constexpr uint32_t kLinRoom = kLinSmem - 1024;      // stages, passes and ones, from a multiple of 1024 on
 
 // ------------------------------------------------------------------------------------------------------------------ activations
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -123,116 +134,104 @@ __device__ __forceinline__ void times_grad(const LinEpi& E, const float (&z)[N],
 }
 
 // --------------------------------------------------------------------------------------------------------- rows of the epilogue
-// 16 values of a row from o on, `cnt` of which there are.
-__device__ __forceinline__ void load16(const void* p, int f32, int64_t o, int wide, int cnt, float (&v)[16]) {
-    if (wide && cnt == 16) {
-        uint32_t u[16];
-        if (f32) {
-            const float* f = static_cast<const float*>(p) + o;
-            if (wide == 2) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 8)
-                    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                                 : "=r"(u[e]), "=r"(u[e + 1]), "=r"(u[e + 2]), "=r"(u[e + 3]), "=r"(u[e + 4]), "=r"(u[e + 5]), "=r"(u[e + 6]),
-                                   "=r"(u[e + 7])
-                                 : "l"(f + e));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(f + e);
-                    u[e] = q.x, u[e + 1] = q.y, u[e + 2] = q.z, u[e + 3] = q.w;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
-            return;
-        }
-        const uint16_t* h = static_cast<const uint16_t*>(p) + o;
-        if (wide == 2) {
-            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                         : "l"(h));
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(h), b = *reinterpret_cast<const uint4*>(h + 8);
-            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[2 * e] = __uint_as_float(u[e] << 16), v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        v[e] = e >= cnt ? 0.f : f32 ? static_cast<const float*>(p)[o + e] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[o + e]);
-}
-__device__ __forceinline__ void store16(void* p, int f32, int64_t o, int wide, int cnt, const float (&v)[16]) {
-    if (wide && cnt == 16) {
-        if (f32) {
-            float* f = static_cast<float*>(p) + o;
-            if (wide == 2) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 8)
-                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(f + e), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]),
-                                 "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]), "f"(v[e + 6]), "f"(v[e + 7])
-                                 : "memory");
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(f + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-            }
-            return;
-        }
-        uint16_t* h = static_cast<uint16_t*>(p) + o;
-        uint32_t u[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-        if (wide == 2) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(h), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
-                         "r"(u[5]), "r"(u[6]), "r"(u[7])
-                         : "memory");
-        } else {
-            *reinterpret_cast<uint4*>(h) = make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(h + 8) = make_uint4(u[4], u[5], u[6], u[7]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (e < cnt) {
-            if (f32)
-                static_cast<float*>(p)[o + e] = v[e];
-            else
-                static_cast<uint16_t*>(p)[o + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
-        }
-}
+// Byte `at` of row r (at most 64 fp32 columns) in a buffer of slabs.
+__device__ __forceinline__ uint32_t slab_at(int r, int at) { return (at >> 7) * 4096 + r * 128 + ((((at & 127) >> 4) ^ (r & 7)) << 4) + (at & 15); }
 
-// 16 columns of row i from column j on.
+// 16 columns of the thread's row from column c of the pass on.
+__device__ __forceinline__ void slab_load16(const uint8_t* buf, int f32, int r, int c, float (&v)[16]) {
+    if (f32) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(buf + slab_at(r, 4 * (c + e)));
+            v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+            const uint4 q = *reinterpret_cast<const uint4*>(buf + slab_at(r, 2 * (c + e)));
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[e + 2 * x] = __uint_as_float(u[x] << 16), v[e + 2 * x + 1] = __uint_as_float(u[x] & 0xFFFF0000u);
+        }
+    }
+}
+__device__ __forceinline__ void slab_store16(uint8_t* buf, int f32, int r, int c, const float (&v)[16]) {
+    if (f32) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(buf + slab_at(r, 4 * (c + e))) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(buf + slab_at(r, 2 * (c + e))) =
+                make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+    }
+}
+// A warp's copies between a buffer and rows that begin anywhere: rows [i, i + 32) of `rows`, columns [j, j + width) of `cols`.
+template <bool IN>
+__device__ __forceinline__ void slab_copy(uint8_t* buf, void* p, int f32, int64_t i, int64_t rows, int j, int cols, int width, int64_t pitch) {
+    const int lane = threadIdx.x & 31, high = (int)min((int64_t)32, rows - i);
+    for (int c = lane; c < width && j + c < cols; c += 32) {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            if (r >= high) continue;
+            const int64_t o = (i + r) * pitch + j + c;
+            if (f32) {
+                float* at = reinterpret_cast<float*>(buf + slab_at(r, 4 * c));
+                if (IN)
+                    *at = static_cast<float*>(p)[o];
+                else
+                    static_cast<float*>(p)[o] = *at;
+            } else {
+                uint16_t* at = reinterpret_cast<uint16_t*>(buf + slab_at(r, 2 * c));
+                if (IN)
+                    *at = static_cast<uint16_t*>(p)[o];
+                else
+                    static_cast<uint16_t*>(p)[o] = *at;
+            }
+        }
+    }
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// 16 columns of a row, from column c of the pass, column j of D, on: what is added and the derivative's argument lie in the buffers.
 template <int OP>
-__device__ __forceinline__ void finish_row(const LinEpi& E, int64_t i, int j, float (&v)[16]) {
-    const int cnt = min(16, E.cols - j);
-    if (cnt <= 0) return;
-    const int64_t o = i * E.pitch + j;
+__device__ __forceinline__ void finish_row(const LinEpi& E, const LinStage& S, uint8_t* out, uint8_t* aux, int r, int c, int j, float (&v)[16]) {
     float t[16];
     if (OP == OP_FWD) {
         if (E.bias) {
-            load16(E.bias, 1, j, 1, cnt, t);
+            if (j + 16 <= E.cols) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += t[e];
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 q = __ldg(reinterpret_cast<const float4*>(E.bias + j + e));
+                    v[e] += q.x, v[e + 1] += q.y, v[e + 2] += q.z, v[e + 3] += q.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += j + e < E.cols ? E.bias[j + e] : 0.f;
+            }
         }
-        if (E.pre_out) store16(E.pre_out, 0, o, E.wide, cnt, v);
+        if (S.aux_bytes) slab_store16(aux, 0, r, c, v);
         activate(E, v);
-    } else if (OP == OP_DGRAD && E.pre_in) {
-        load16(E.pre_in, 0, o, E.wide, cnt, t);
+    } else if (OP == OP_DGRAD && S.load_aux) {
+        slab_load16(aux, 0, r, c, t);
         times_grad(E, t, v);
     }
-    const void* add = OP == OP_WGRAD ? (E.accumulate ? E.out : nullptr) : E.add;
-    if (add) {
-        load16(add, E.f32, o, E.wide, cnt, t);
+    if (S.load_add) {
+        slab_load16(out, E.f32, r, c, t);
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = fmaf(E.scale, v[e], t[e]);
     } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] *= E.scale;
     }
-    store16(E.out, E.f32, o, E.wide, cnt, v);
+    slab_store16(out, E.f32, r, c, v);
 }
 // N rows of column j from row i on (neighbouring threads have neighbouring columns).
 template <int OP, int N>
@@ -312,7 +311,7 @@ struct LinWalk {
 };
 
 struct LinShared {
-    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain;
+    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain, in[kLinEpiWarps][2];
     uint32_t tmem;
     int abort;
 };
@@ -333,18 +332,43 @@ __device__ __forceinline__ bool takes_sums(const LinEpi& E, const LinItem& s) {
     return OP == OP_WGRAD && E.db && (SWAP ? s.mt : s.nt) == 0;
 }
 
+// The passes of an epilogue warp over the tiles that it finishes itself, in the order that it takes them.
+template <bool PAIR>
+struct LinPasses {
+    LinWalk way;
+    LinItem s;
+    int c;  // first column of the pass in its tile
+    bool more;
+    __device__ __forceinline__ LinPasses(const LinGemm& G, int unit, int turn) : way(G, unit), c(G.bn), more(true) { next(G, turn); }
+    __device__ __forceinline__ void next(const LinGemm& G, int turn) {
+        c += 2 * G.st.gw;
+        while (more && c >= G.bn) {
+            do more = way.next(G, s);
+            while (more && s.slot >= 0);
+            c = turn * G.st.gw;
+        }
+    }
+};
+
+struct LinMaps {
+    CUtensorMap a, b;      // operands
+    CUtensorMap out, add;  // the output's rows and what is added
+    CUtensorMap aux;       // the pre-activation
+};
+
 template <bool PAIR, int OP, bool SWAP>
-__global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                                                                     const __grid_constant__ LinGemm G, const __grid_constant__ LinEpi E) {
+__global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ LinMaps M, const __grid_constant__ LinGemm G,
+                                                                     const __grid_constant__ LinEpi E) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ LinShared sh;
     uint8_t* ones = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* ring = ones + kLinOnes;
+    uint8_t* passes = ones + (OP == OP_WGRAD ? kLinOnes : 0);
+    uint8_t* ring = passes + (SWAP ? 0 : kLinEpiWarps * G.st.buffers * (G.st.out_bytes + G.st.aux_bytes));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
     const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&ta);
-        tma_prefetch_desc(&tb);
+        tma_prefetch_desc(&M.a);
+        tma_prefetch_desc(&M.b);
         for (int s = 0; s < kLinMostStages; ++s) {
             mbar_init(&sh.full[s], PAIR && rank == 0 ? 2 : 1);
             mbar_init(&sh.empty[s], 1);
@@ -354,6 +378,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             mbar_init(&sh.tempty[a], (PAIR ? 2 : 1) * kLinEpiWarps);
         }
         mbar_init(&sh.drain, 1);
+        for (int w = 0; w < kLinEpiWarps; ++w) mbar_init(&sh.in[w][0], 1), mbar_init(&sh.in[w][1], 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -394,7 +419,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             const bool mn = isb ? G.b_mn : G.a_mn, mine = q < (isb ? nb : na);
             const int64_t r0 = isb ? n0 : m0;
             const uint32_t dst = (isb ? 16384 : 0) + q * 8192;
-            const CUtensorMap* map = isb ? &tb : &ta;
+            const CUtensorMap* map = isb ? &M.b : &M.a;
             for (int64_t kb = s.kb0; kb < s.kb1; ++kb) {
                 ok = __all_sync(~0u, mbar_wait(&sh.empty[R.stage], R.parity() ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_PRODUCER_EMPTY));
                 if (!ok) break;
@@ -472,8 +497,34 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 umma_commit(&sh.tfull[acc]);
         }
     } else if (warp >= 2) {
-        // 16 columns of the thread's lane at a time, the two warps of a lane quarter in turn
+        // a pass of columns at a time, the two warps of a lane quarter in turn, 16 columns of the thread's lane at once
         const int q = warp & 3, turn = (warp - 2) >> 2, r = 32 * q + lane;
+        const LinStage& S = G.st;
+        uint8_t* mine = passes + (warp - 2) * S.buffers * (S.out_bytes + S.aux_bytes);
+        const uint32_t in_bytes = (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
+        uint32_t done = 0, asked = 0;  // passes finished, and those whose loads were issued
+        LinPasses<PAIR> ahead(G, unit, turn);
+        // loads of the next pass that has none yet, into the buffer that its turn is; lane 0, once that buffer's store has been read
+        auto ask = [&]() {
+            if (!ahead.more) return;
+            const int b = asked % S.buffers;
+            uint8_t* out = mine + b * (S.out_bytes + S.aux_bytes);
+            const int row = (int)(ahead.s.mt * (PAIR ? 256 : 128) + 128 * rank + 32 * q), col = (int)(ahead.s.nt * G.bn) + ahead.c;
+            if (S.tma && in_bytes && lane == 0) {
+                uint64_t* bar = &sh.in[warp - 2][b];
+                mbar_arrive_expect_tx(bar, in_bytes);
+                const int step = E.f32 ? 32 : 64;
+                if (S.load_add)
+                    for (int x = 0; x < S.out_bytes / 4096; ++x) tma_load_2d(out + x * 4096, &M.add, bar, col + x * step, row);
+                if (S.load_aux) tma_load_2d(out + S.out_bytes, &M.aux, bar, col, row);
+            }
+            ++asked;
+            ahead.next(G, turn);
+        };
+        if (!SWAP && S.tma && in_bytes) {
+            ask();
+            __syncwarp();
+        }
         for (uint32_t local = 0; way.next(G, s); ++local) {
             const uint32_t acc = local & 1, use = local >> 1;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
@@ -481,41 +532,104 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
             if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL)) break;
             tc_fence_after();
-            for (int c = 16 * turn; c < G.bn; c += 32) {
-                uint32_t u[32];
-                tmem_ld16(tm + c, u);
-                tmem_ld_wait();
-                float v[16];
+            if (SWAP || part) {
+                for (int c = 16 * turn; c < G.bn; c += 32) {
+                    uint32_t u[32];
+                    tmem_ld16(tm + c, u);
+                    tmem_ld_wait();
+                    float v[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
-                if (part) {
-                    if (SWAP) {
+                    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
+                    if (part) {
+                        // four columns of all 128 rows in turn
 #pragma unroll
                         for (int e = 0; e < 16; e += 4)
                             reinterpret_cast<float4*>(part)[((c + e) >> 2) * 128 + r] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    } else {
-                        store16(part, 1, (int64_t)r * G.bn + c, 2, 16, v);
+                    } else if (i < G.m) {
+                        finish_column<OP>(E, j0 + c, (int)i, v);
                     }
-                } else if (SWAP) {
-                    if (i < G.m) finish_column<OP>(E, j0 + c, (int)i, v);
-                } else if (i < G.m) {
-                    finish_row<OP>(E, i, (int)(j0 + c), v);
-                }
-                if (OP == OP_WGRAD && SWAP && takes_sums<OP, SWAP>(E, s)) {
-                    tmem_ld16(tm1 + c, u);
-                    tmem_ld_wait();
-                    if (r == 0) {
+                    if (OP == OP_WGRAD && SWAP && takes_sums<OP, SWAP>(E, s)) {
+                        tmem_ld16(tm1 + c, u);
+                        tmem_ld_wait();
+                        if (r == 0) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int64_t j = j0 + c + e;
-                            const float b = __uint_as_float(u[e]);
-                            if (part)
-                                G.dpart[(int64_t)s.slot * 256 + c + e] = b;
-                            else if (j < G.n)
-                                E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
+                            for (int e = 0; e < 16; ++e) {
+                                const int64_t j = j0 + c + e;
+                                const float b = __uint_as_float(u[e]);
+                                if (part)
+                                    G.dpart[(int64_t)s.slot * 256 + c + e] = b;
+                                else if (j < G.n)
+                                    E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
+                            }
                         }
                     }
                 }
+            } else {
+                bool ok = true;
+                for (int c0 = turn * S.gw; ok && c0 < G.bn; c0 += 2 * S.gw, ++done) {
+                    const int b = done % S.buffers;
+                    uint8_t *out = mine + b * (S.out_bytes + S.aux_bytes), *aux = out + S.out_bytes;
+                    const int64_t row = i - lane;
+                    const int col = (int)j0 + c0;
+                    if (S.tma && in_bytes) {
+                        if (S.buffers == 1 && done) {  // the next pass's loads go where this warp's last store was
+                            if (lane == 0) bulk_wait_read<0>();
+                            __syncwarp();
+                            ask();
+                        }
+                        ok = mbar_wait(&sh.in[warp - 2][b], (done / S.buffers) & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
+                        if (!ok) break;
+                    } else if (S.tma) {
+                        if (lane == 0) {
+                            if (S.buffers == 1)
+                                bulk_wait_read<0>();
+                            else
+                                bulk_wait_read<1>();
+                        }
+                        __syncwarp();
+                    } else if (row < E.rows) {
+                        if (S.load_add) slab_copy<true>(out, const_cast<void*>(E.add), E.f32, row, E.rows, col, E.cols, S.gw, E.pitch);
+                        if (S.load_aux) slab_copy<true>(aux, const_cast<uint16_t*>(E.pre_in), 0, row, E.rows, col, E.cols, S.gw, E.pitch);
+                        __syncwarp();
+                    }
+                    for (int c = 0; c < S.gw && c0 + c < G.bn; c += 32) {
+                        uint32_t u[32];
+                        tmem_ld32(tm + c0 + c, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            float v[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[h + e]);
+                            if (col + c + h < E.cols) finish_row<OP>(E, S, out, aux, lane, c + h, col + c + h, v);
+                        }
+                        if (c == 0 && S.tma && in_bytes && S.buffers == 2) {  // the other buffer's store has had time to be read
+                            if (lane == 0) bulk_wait_read<0>();
+                            __syncwarp();
+                            ask();
+                        }
+                    }
+                    const bool pre = OP == OP_FWD && S.aux_bytes;
+                    if (S.tma) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            const int step = E.f32 ? 32 : 64;
+                            for (int x = 0; row < E.rows && x < S.out_bytes / 4096; ++x)
+                                if (col + x * step < E.cols) tma_store_2d(&M.out, out + x * 4096, col + x * step, (int)row);
+                            if (pre && row < E.rows && col < E.cols) tma_store_2d(&M.aux, aux, col, (int)row);
+                            bulk_commit();  // a group to each pass, an empty one too: they are counted
+                        }
+                    } else {
+                        __syncwarp();
+                        if (row < E.rows) {
+                            slab_copy<false>(out, E.out, E.f32, row, E.rows, col, E.cols, S.gw, E.pitch);
+                            if (pre) slab_copy<false>(aux, E.pre_out, 0, row, E.rows, col, E.cols, S.gw, E.pitch);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (!ok) break;
             }
             if (OP == OP_WGRAD && !SWAP && turn == 0 && takes_sums<OP, SWAP>(E, s)) {
                 uint32_t u[32];
@@ -536,6 +650,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     mbar_arrive(&sh.tempty[acc]);
             }
         }
+        if (lane == 0) bulk_wait();
+        if (!SWAP && lane == 0 && *(volatile int*)&sh.abort)  // loads in flight end before the CTA leaves
+            for (uint32_t k = done; k < asked; ++k) mbar_wait_timed(&sh.in[warp - 2][k % S.buffers], (k / S.buffers) & 1, G.wait_ns);
     }
     __syncwarp();
     // after a wait that gave up: copies and products in flight end before the CTA leaves
@@ -565,24 +682,25 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
     }
 }
 
-// The tiles that were cut, from their parts in order.  `ways` threads add a share of the parts of four values each; the values of
-// neighbouring threads are neighbours in a part (SWAP: along its rows).
+// The tiles that were cut, from their parts in order: a block has 32 columns of so many rows that `ways` threads share the parts of
+// four values of a row; the sums go through shared memory to rows of 32 columns (SWAP: are columns of rows already).
 template <int OP, bool SWAP>
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinGemm G, const __grid_constant__ LinEpi E, int pair, int ways) {
     __shared__ float4 red[256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int values = pair ? 2 : 1, per = 256 / ways;                       // CTAs of a tile; float4s of a block
-    const int quads = values * 128 * G.bn / 4, blocks = (quads + per - 1) / per;  // of a tile
-    const int64_t e = blockIdx.x / blocks;
-    const int f = (int)(blockIdx.x - e * blocks) * per + (int)threadIdx.x % per, way = threadIdx.x / per;
+    const int ctas = pair ? 2 : 1, high = 32 / ways;                      // rows of a block
+    const int across = (G.bn + 31) / 32, down = ctas * 128 / high;        // blocks of a tile
+    const int64_t e = blockIdx.x / (across * down);
     const int64_t u0 = e * G.nkb / G.share, u1 = ((e + 1) * G.nkb - 1) / G.share;
     if (u0 == u1) return;  // this tile was a unit's alone
     int64_t mt, nt;
     tile_of(G, G.whole + e, mt, nt);
-    const int64_t apart = (int64_t)values * 128 * G.bn / 4;
-    const float4* p = reinterpret_cast<const float4*>(G.part) + f;
+    const int block = (int)(blockIdx.x - e * across * down), c0 = block / down * 32, r0 = block % down * high;
+    const int way = threadIdx.x / (8 * high), in = threadIdx.x % (8 * high), row = r0 + in % high, quad = in / high;
+    const int64_t apart = (int64_t)ctas * 32 * G.bn;
+    const float4* p = reinterpret_cast<const float4*>(G.part) + (int64_t)(row >> 7) * 32 * G.bn + (c0 / 4 + quad) * 128 + (row & 127);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (f < quads) {
+    if (c0 + 4 * quad < G.bn) {
 #pragma unroll 8
         for (int64_t u = u0 + way; u <= u1; u += ways) {
             const float4 x = __ldcg(p + (2 * u + (u == u0)) * apart);
@@ -591,33 +709,31 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     }
     red[threadIdx.x] = s;
     __syncthreads();
-    if (way == 0 && f < quads) {
-        for (int w = 1; w < ways; ++w) {
-            const float4 x = red[w * per + threadIdx.x];
-            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-        }
-        const int cta = f / (32 * G.bn), in = f - cta * 32 * G.bn;
-        float v[4] = {s.x, s.y, s.z, s.w};
-        if (SWAP) {
-            finish_column<OP>(E, nt * G.bn + 4 * (in >> 7), (int)(mt * 128 + (in & 127)), v);
-        } else {
-            const int row = in / (G.bn / 4), c = 4 * (in - row * (G.bn / 4));
-            const int64_t i = mt * 128 * values + 128 * cta + row;
-            if (i < G.m) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float one[1] = {v[x]};
-                    finish_column<OP>(E, i, (int)(nt * G.bn) + c + x, one);
-                }
+    if (SWAP) {
+        if (way == 0) {
+            for (int w = 1; w < ways; ++w) {
+                const float4 x = red[w * 8 * high + in];
+                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
             }
+            float v[4] = {s.x, s.y, s.z, s.w};
+            if (c0 + 4 * quad < G.bn) finish_column<OP>(E, nt * G.bn + c0 + 4 * quad, (int)(mt * 128 + row), v);
+        }
+    } else {
+        const int lane = threadIdx.x & 31;
+        for (int r = threadIdx.x >> 5; r < high; r += 8) {
+            const float* at = reinterpret_cast<const float*>(red + lane / 4 * high + r) + (lane & 3);
+            float v[1] = {0.f};
+            for (int w = 0; w < ways; ++w) v[0] += at[w * 8 * high * 4];
+            const int64_t i = mt * 128 * ctas + r0 + r;
+            if (i < G.m && c0 + lane < G.bn) finish_column<OP>(E, i, (int)(nt * G.bn) + c0 + lane, v);
         }
     }
     // db of the tile: 256 values, by the tile's first block
-    if (OP == OP_WGRAD && E.db && (SWAP ? mt : nt) == 0 && blockIdx.x == e * blocks) {
+    if (OP == OP_WGRAD && E.db && (SWAP ? mt : nt) == 0 && block == 0) {
         float b = 0.f;
         for (int64_t u = u0; u <= u1; ++u) b += __ldcg(G.dpart + (2 * u + (u == u0)) * 256 + threadIdx.x);
-        const int64_t j = SWAP ? nt * G.bn + threadIdx.x : mt * 128 * values + threadIdx.x;
-        const bool there = SWAP ? (int)threadIdx.x < G.bn && j < G.n : (int)threadIdx.x < 128 * values && j < G.m;
+        const int64_t j = SWAP ? nt * G.bn + threadIdx.x : mt * 128 * ctas + threadIdx.x;
+        const bool there = SWAP ? (int)threadIdx.x < G.bn && j < G.n : (int)threadIdx.x < 128 * ctas && j < G.m;
         if (there) E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
     }
 }
@@ -630,12 +746,12 @@ struct LinPlan {
 
 // Both launches of a product; instantiated for each direction in a file of its own.
 template <int OP>
-cf_status launch_linear(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& ta, const CUtensorMap& tb, const LinEpi& E);
+cf_status launch_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E);
 
 #ifdef CF_LINEAR_OP
 namespace {
 template <bool PAIR, bool SWAP>
-cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& ta, const CUtensorMap& tb, const LinEpi& E) {
+cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
     auto kernel = linear_gemm_kernel<PAIR, CF_LINEAR_OP, SWAP>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
@@ -649,13 +765,12 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = PAIR ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, P.g, E) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, M, P.g, E) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
     if (!P.cut) return CF_OK;
     const int64_t tiles = P.g.rest / P.g.nkb, parts = (P.g.nkb + P.g.share - 1) / P.g.share + 1;
     int ways = 1;
     while (ways < 8 && 4 * ways < parts) ways *= 2;
-    const int quads = (PAIR ? 2 : 1) * 32 * P.g.bn, per = 256 / ways;
-    cfg.gridDim = dim3((unsigned)(tiles * ((quads + per - 1) / per)));
+    cfg.gridDim = dim3((unsigned)(tiles * ((P.g.bn + 31) / 32) * ((PAIR ? 2 : 1) * 4 * ways)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -668,9 +783,9 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& 
 }  // namespace
 
 template <>
-cf_status launch_linear<CF_LINEAR_OP>(const LaunchCtx& ctx, const LinPlan& P, const CUtensorMap& ta, const CUtensorMap& tb, const LinEpi& E) {
-    if (P.pair) return run_linear<true, false>(ctx, P, ta, tb, E);
-    return P.swap ? run_linear<false, true>(ctx, P, ta, tb, E) : run_linear<false, false>(ctx, P, ta, tb, E);
+cf_status launch_linear<CF_LINEAR_OP>(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
+    if (P.pair) return run_linear<true, false>(ctx, P, M, E);
+    return P.swap ? run_linear<false, true>(ctx, P, M, E) : run_linear<false, false>(ctx, P, M, E);
 }
 #endif
 
