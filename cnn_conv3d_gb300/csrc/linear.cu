@@ -82,7 +82,7 @@ Product plan_of(const cf_linear_desc* d, int op) {
     P.b = op == OP_WGRAD ? x : w;
     G.m = op == OP_WGRAD ? d->n : d->rows;
     G.n = op == OP_FWD ? d->n : d->k;
-    G.nkb = over(op == OP_FWD ? d->k : op == OP_DGRAD ? d->n : d->rows, 64);
+    G.nkb = (int)over(op == OP_FWD ? d->k : op == OP_DGRAD ? d->n : d->rows, 64);
     if (P.plan.swap) std::swap(P.a, P.b), std::swap(G.m, G.n);
     G.a_mn = P.a.mn, G.b_mn = P.b.mn;
 
@@ -90,22 +90,22 @@ Product plan_of(const cf_linear_desc* d, int op) {
     const int64_t wide = over(G.m, 256) * over(G.n, 256) * G.nkb;
     P.plan.pair = !P.plan.swap && G.m > 128 && G.n > 128 && wide >= 8 * (kPlanSms / 2);
     const int units = P.plan.pair ? kPlanSms / 2 : kPlanSms, step = P.plan.pair ? 32 : 16;
-    G.tm = over(G.m, P.plan.pair ? 256 : 128);
+    G.tm = (int)over(G.m, P.plan.pair ? 256 : 128);
     // the epilogue's passes of 64 columns end with a tile where another follows
     G.bn = (int)up(over(G.n, over(G.n, 256)), G.n > 256 ? 64 : step);
     if (!P.plan.pair && G.nkb <= 16)
-        while (G.bn > 64 && G.tm * over(G.n, up(G.bn / 2, 64)) <= units) G.bn = (int)up(G.bn / 2, 64);
-    G.tn = over(G.n, G.bn);
+        while (G.bn > 64 && (int64_t)G.tm * over(G.n, up(G.bn / 2, 64)) <= units) G.bn = (int)up(G.bn / 2, 64);
+    G.tn = (int)over(G.n, G.bn);
     const int half = P.plan.pair ? G.bn / 2 : G.bn;
     G.a_box = 128, G.b_box = half;
     G.stage_bytes = (int)(16384 + (G.b_mn ? up(half, 64) * 128 : up(half * 128, 1024)));
 
     // tiles over a whole number of rounds are cut where that saves more than the second launch and the parts take
-    const int64_t tiles = G.tm * G.tn, rounds = tiles / units, rem = tiles - rounds * units;
+    const int64_t tiles = (int64_t)G.tm * G.tn, rounds = tiles / units, rem = tiles - rounds * units;
     const double block = G.stage_bytes / 100e3, join = 4.0;  // us
     const int64_t share = std::max<int64_t>(2, over(rem * G.nkb, units));
-    G.whole = tiles, G.rest = 0, G.share = 1;
-    if (rem && (G.nkb - share) * block > join) G.whole = tiles - rem, G.rest = rem * G.nkb, G.share = share;
+    G.whole = (int)tiles, G.rest = 0, G.share = 1;
+    if (rem && (G.nkb - share) * block > join) G.whole = (int)(tiles - rem), G.rest = rem * G.nkb, G.share = (int)share;
     G.units = (int)(G.whole ? std::min<int64_t>(units, tiles) : over(G.rest, G.share));
     P.plan.cut = G.rest && share < G.nkb;
     if (P.plan.cut) {
@@ -154,10 +154,10 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
         S.tma = E.pitch % 8 == 0 && E.cols % 8 == 0;
         S.gw = E.f32 && !aux ? 32 : 64;
         S.out_bytes = S.gw * (E.f32 ? 128 : 64), S.aux_bytes = aux ? 4096 : 0;
-        // two buffers where the epilogue is most of a tile's time, and two stages fit beside them
+        // both sets where the epilogue is most of a tile's time, if two stages fit beside their room
         const uint32_t pass = kLinEpiWarps * (S.out_bytes + S.aux_bytes);
-        S.buffers = G.nkb <= 8 && room - 2 * pass >= 2u * G.stage_bytes ? 2 : 1;
-        room -= S.buffers * pass;
+        S.sets = G.nkb <= 16 && room >= 2 * pass + 2 * G.stage_bytes ? 2 : 1;
+        room -= S.sets * pass;
         auto rows_map = [&](CUtensorMap* m, const void* p, bool f32) {
             const uint64_t dims[2] = {(uint64_t)E.cols, (uint64_t)E.rows}, strides[1] = {(uint64_t)E.pitch * (f32 ? 4 : 2)};
             const uint32_t box[2] = {f32 ? 32u : 64u, 32};

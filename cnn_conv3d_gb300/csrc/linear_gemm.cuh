@@ -7,7 +7,7 @@
 // or the two exchanged (SWAP) where that side is narrow: few rows in the forward and the backward data, so that the weights' rows
 // fill the 128 lanes of a tile and the rows are its columns, and a narrow k in the backward weight.
 //
-// A CTA is a TMA warp, an issuing thread and eight epilogue warps.  Operands come in stages of 64 of the contracted axis (128-byte
+// A CTA is a TMA warp, an issuing thread and two sets of eight epilogue warps.  Operands come in stages of 64 of the contracted axis (128-byte
 // rows, swizzled); tiles are 128 rows by up to 256 columns, or 256 by 256 on a pair of CTAs with one instruction for both, each CTA
 // fetching half of either side: then a stage costs 64 bytes of L2 a cycle and SM, where a lone CTA's would cost 96 of the about 70
 // that it gives.  The accumulator is double: the epilogue of a tile runs under the products of the next.
@@ -43,29 +43,31 @@ struct LinEpi {
 struct LinStage {
     int tma;                   // rows begin and end at 16 bytes; otherwise a warp copies value by value along the rows
     int gw;                    // columns of a pass: 64, or 32 of fp32 with no pre-activation beside them
-    int buffers;               // 1, or 2: what is loaded of the next pass comes under the present one
-    int out_bytes, aux_bytes;  // of a buffer: the output (and what is added to it, in the same place), the pre-activation
+    int sets;                  // 2: sets of epilogue warps take the tiles in turn; 1: one takes all
+    int out_bytes, aux_bytes;  // a warp's room: the output (and what is added to it, in the same place), the pre-activation
     int load_add, load_aux;
 };
 
 struct LinGemm {
     LinStage st;
-    int64_t m, n, nkb;       // D's sizes, 64-blocks of the contracted axis
-    int64_t tm, tn;          // tiles
+    int64_t m, n;            // D's sizes
+    int nkb;                 // 64-blocks of the contracted axis
+    int tm, tn;              // tiles
     int bn;                  // columns of a tile
     int a_mn, b_mn;          // operands with their rows contiguous
     int a_box, b_box;        // K-major: rows of a copy
     int stages, stage_bytes;
-    int64_t whole;           // tiles that are dealt out whole
-    int64_t rest, share;     // blocks of the others, and a unit's of them
+    int whole;               // tiles that are dealt out whole
+    int share;               // a unit's blocks of the others
+    int64_t rest;            // all blocks of the others
     int units;               // CTAs or pairs
     float *part, *dpart;     // parts of cut tiles: a unit's two slots of 128 x bn values a CTA; of db, 256 values a slot
     int* status;
     uint64_t wait_ns;
 };
 
-constexpr int kLinEpiWarps = 8;
-constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
+constexpr int kLinEpiWarps = 8;  // of a set
+constexpr int kLinThreads = 64 + 2 * 32 * kLinEpiWarps;
 constexpr int kLinMostStages = 10;
 constexpr uint32_t kLinOnes = 16 << 10;             // 128 rows of 64 ones (backward weight)
 constexpr uint32_t kLinSmem = 232448 - 1024;        // dynamic: all but the barriers
@@ -86,24 +88,65 @@ __device__ __forceinline__ float rcp(float t) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
     return r;
 }
+// Two values at a time: one instruction for both.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 1 / (1 + 2^t)
+__device__ __forceinline__ uint64_t gate2(uint64_t t) {
+    float a, b;
+    apart(t, a, b);
+    apart(add2(two(ex2(a), ex2(b)), two(1.f, 1.f)), a, b);
+    return two(rcp(a), rcp(b));
+}
 // 1 / (1 + exp(-t)), t = z for SiLU, kGeluA (z + kGeluB z^3) for GELU; infinities give 0 and 1.
-__device__ __forceinline__ float silu_gate(float z) { return rcp(1.f + ex2(-kLog2e * z)); }
-__device__ __forceinline__ float gelu_gate(float z) { return rcp(1.f + ex2(z * fmaf(z * z, -kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA))); }
-
-__device__ __forceinline__ float act_of(int act, float slope, float z) {
-    if (act == CF_ACT_LRELU) return z > 0.f ? z : slope * z;
-    return z * (act == CF_ACT_SILU ? silu_gate(z) : gelu_gate(z));
+__device__ __forceinline__ uint64_t silu_gate(uint64_t z) { return gate2(mul2(z, two(-kLog2e, -kLog2e))); }
+__device__ __forceinline__ uint64_t gelu_gate(uint64_t z) {
+    constexpr float a = -kLog2e * kGeluA, b = -kLog2e * kGeluA * kGeluB;
+    return gate2(mul2(z, fma2(mul2(z, z), two(b, b), two(a, a))));
+}
+// z within +-100, where the derivatives are 1 and 0 already and no product of theirs is inf times 0; a NaN stays.
+__device__ __forceinline__ float bounded(float z) {
+    asm("{min.NaN.f32 %0, %0, 0f42C80000;\n\tmax.NaN.f32 %0, %0, 0fC2C80000;}" : "+f"(z));
+    return z;
+}
+__device__ __forceinline__ uint64_t smooth_grad(int act, uint64_t z) {
+    float a, b;
+    apart(z, a, b);
+    z = two(bounded(a), bounded(b));
+    const uint64_t e = act == CF_ACT_SILU ? silu_gate(z) : gelu_gate(z);
+    uint64_t t = mul2(mul2(z, e), fma2(e, two(-1.f, -1.f), two(1.f, 1.f)));
+    if (act == CF_ACT_GELU) {
+        constexpr float c = 3.f * kGeluA * kGeluB;
+        t = mul2(t, fma2(mul2(z, z), two(c, c), two(kGeluA, kGeluA)));
+    }
+    return add2(e, t);
 }
 __device__ __forceinline__ float act_grad(int act, float slope, float z) {
     if (act == CF_ACT_LRELU) return z > 0.f ? 1.f : slope;
-    z = z > 100.f ? 100.f : z < -100.f ? -100.f : z;  // 1 and 0 beyond, where products with 1 - e would be inf times 0
-    if (act == CF_ACT_SILU) {
-        const float e = silu_gate(z);
-        return fmaf(z * e, 1.f - e, e);
-    }
-    const float e = gelu_gate(z);
-    return fmaf(z * e * (1.f - e), kGeluA * fmaf(3.f * kGeluB * z, z, 1.f), e);
+    float a, b;
+    apart(smooth_grad(act, two(z, z)), a, b);
+    return a;
 }
+
 // The activation of all, with one branch.
 template <int N>
 __device__ __forceinline__ void activate(const LinEpi& E, float (&v)[N]) {
@@ -111,12 +154,14 @@ __device__ __forceinline__ void activate(const LinEpi& E, float (&v)[N]) {
         if (E.slope == 1.f) return;
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = v[e] > 0.f ? v[e] : E.slope * v[e];
-    } else if (E.act == CF_ACT_SILU) {
+        return;
+    }
+    const bool silu = E.act == CF_ACT_SILU;
+    constexpr int kStep = N > 1 ? 2 : 1;
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= silu_gate(v[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= gelu_gate(v[e]);
+    for (int e = 0; e < N; e += kStep) {
+        const uint64_t z = two(v[e], v[e + kStep - 1]);
+        apart(mul2(z, silu ? silu_gate(z) : gelu_gate(z)), v[e], v[e + kStep - 1]);
     }
 }
 template <int N>
@@ -124,13 +169,13 @@ __device__ __forceinline__ void times_grad(const LinEpi& E, const float (&z)[N],
     if (E.act == CF_ACT_LRELU) {
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] *= z[e] > 0.f ? 1.f : E.slope;
-    } else if (E.act == CF_ACT_SILU) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= act_grad(CF_ACT_SILU, 0.f, z[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= act_grad(CF_ACT_GELU, 0.f, z[e]);
+        return;
     }
+    const int act = E.act;
+    constexpr int kStep = N > 1 ? 2 : 1;
+#pragma unroll
+    for (int e = 0; e < N; e += kStep)
+        apart(mul2(two(v[e], v[e + kStep - 1]), smooth_grad(act, two(z[e], z[e + kStep - 1]))), v[e], v[e + kStep - 1]);
 }
 
 // --------------------------------------------------------------------------------------------------------- rows of the epilogue
@@ -196,8 +241,7 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 16 columns of a row, from column c of the pass, column j of D, on: what is added and the derivative's argument lie in the buffers.
@@ -210,7 +254,8 @@ __device__ __forceinline__ void finish_row(const LinEpi& E, const LinStage& S, u
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 q = __ldg(reinterpret_cast<const float4*>(E.bias + j + e));
-                    v[e] += q.x, v[e + 1] += q.y, v[e + 2] += q.z, v[e + 3] += q.w;
+                    apart(add2(two(v[e], v[e + 1]), two(q.x, q.y)), v[e], v[e + 1]);
+                    apart(add2(two(v[e + 2], v[e + 3]), two(q.z, q.w)), v[e + 2], v[e + 3]);
                 }
             } else {
 #pragma unroll
@@ -226,10 +271,10 @@ __device__ __forceinline__ void finish_row(const LinEpi& E, const LinStage& S, u
     if (S.load_add) {
         slab_load16(out, E.f32, r, c, t);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = fmaf(E.scale, v[e], t[e]);
-    } else {
+        for (int e = 0; e < 16; e += 2) apart(fma2(two(v[e], v[e + 1]), two(E.scale, E.scale), two(t[e], t[e + 1])), v[e], v[e + 1]);
+    } else if (E.scale != 1.f) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] *= E.scale;
+        for (int e = 0; e < 16; e += 2) apart(mul2(two(v[e], v[e + 1]), two(E.scale, E.scale)), v[e], v[e + 1]);
     }
     slab_store16(out, E.f32, r, c, v);
 }
@@ -277,41 +322,42 @@ __device__ __forceinline__ void finish_column(const LinEpi& E, int64_t i, int j,
 
 // ------------------------------------------------------------------------------------------------------------------------- work
 struct LinItem {
-    int64_t mt, nt, kb0, kb1;
+    int mt, nt, kb0, kb1;
     int slot;  // where a part goes, -1 for a whole tile
 };
 // Tiles in bands of eight rows of tiles, so that what runs at one time shares operands in L2.
-__device__ __forceinline__ void tile_of(const LinGemm& G, int64_t t, int64_t& mt, int64_t& nt) {
-    const int64_t band = t / (8 * G.tn), r = t - band * 8 * G.tn, high = min((int64_t)8, G.tm - 8 * band);
+__device__ __forceinline__ void tile_of(const LinGemm& G, int t, int& mt, int& nt) {
+    const int band = t / (8 * G.tn), r = t - band * 8 * G.tn, high = min(8, G.tm - 8 * band);
     nt = r / high;
     mt = 8 * band + r - nt * high;
 }
 struct LinWalk {
-    int unit;
-    int64_t t, at, end;
-    __device__ __forceinline__ LinWalk(const LinGemm& G, int u) : unit(u), t(u) {
-        at = min(u * G.share, G.rest), end = min(at + G.share, G.rest);
+    int t, e, kb, left;  // the next whole tile; the next of the others, its block, and how many the unit still takes
+    __device__ __forceinline__ LinWalk(const LinGemm& G, int unit) : t(unit), e(0), kb(0), left(0) {
+        const int64_t at = (int64_t)unit * G.share;
+        if (at >= G.rest) return;
+        e = (int)(at / G.nkb), kb = (int)(at - (int64_t)e * G.nkb);
+        left = (int)min((int64_t)G.share, G.rest - at);
     }
-    __device__ __forceinline__ bool next(const LinGemm& G, LinItem& s) {
+    __device__ __forceinline__ bool next(const LinGemm& G, int unit, LinItem& s) {
         if (t < G.whole) {
             tile_of(G, t, s.mt, s.nt);
             s.kb0 = 0, s.kb1 = G.nkb, s.slot = -1;
             t += G.units;
             return true;
         }
-        if (at >= end) return false;
-        const int64_t e = at / G.nkb;
+        if (left == 0) return false;
         tile_of(G, G.whole + e, s.mt, s.nt);
-        s.kb0 = at - e * G.nkb;
-        s.kb1 = min(G.nkb, s.kb0 + end - at);
-        at += s.kb1 - s.kb0;
-        s.slot = s.kb1 - s.kb0 == G.nkb ? -1 : 2 * unit + (s.kb0 == 0);
+        const int take = min(left, G.nkb - kb);
+        s.kb0 = kb, s.kb1 = kb + take;
+        s.slot = take == G.nkb ? -1 : 2 * unit + (kb == 0);
+        left -= take, kb = 0, ++e;
         return true;
     }
 };
 
 struct LinShared {
-    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain, in[kLinEpiWarps][2];
+    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain, in[2 * kLinEpiWarps];
     uint32_t tmem;
     int abort;
 };
@@ -333,18 +379,23 @@ __device__ __forceinline__ bool takes_sums(const LinEpi& E, const LinItem& s) {
 }
 
 // The passes of an epilogue warp over the tiles that it finishes itself, in the order that it takes them.
-template <bool PAIR>
 struct LinPasses {
     LinWalk way;
     LinItem s;
-    int c;  // first column of the pass in its tile
+    int c, local;  // first column of the pass in its tile; the unit's tiles and parts so far
     bool more;
-    __device__ __forceinline__ LinPasses(const LinGemm& G, int unit, int turn) : way(G, unit), c(G.bn), more(true) { next(G, turn); }
-    __device__ __forceinline__ void next(const LinGemm& G, int turn) {
+    __device__ __forceinline__ LinPasses(const LinGemm& G, int unit, int set, int turn) : way(G, unit), c(G.bn), local(0), more(true) {
+        next(G, unit, set, turn);
+    }
+    __device__ __forceinline__ void next(const LinGemm& G, int unit, int set, int turn) {
         c += 2 * G.st.gw;
         while (more && c >= G.bn) {
-            do more = way.next(G, s);
-            while (more && s.slot >= 0);
+            bool mine;
+            do {
+                more = way.next(G, unit, s);
+                mine = s.slot < 0 && (G.st.sets == 1 || (local & 1) == set);
+                ++local;
+            } while (more && !mine);
             c = turn * G.st.gw;
         }
     }
@@ -363,7 +414,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
     __shared__ LinShared sh;
     uint8_t* ones = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* passes = ones + (OP == OP_WGRAD ? kLinOnes : 0);
-    uint8_t* ring = passes + (SWAP ? 0 : kLinEpiWarps * G.st.buffers * (G.st.out_bytes + G.st.aux_bytes));
+    uint8_t* ring = passes + (SWAP ? 0 : G.st.sets * kLinEpiWarps * (G.st.out_bytes + G.st.aux_bytes));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
     const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
     if (threadIdx.x == 0) {
@@ -378,7 +429,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             mbar_init(&sh.tempty[a], (PAIR ? 2 : 1) * kLinEpiWarps);
         }
         mbar_init(&sh.drain, 1);
-        for (int w = 0; w < kLinEpiWarps; ++w) mbar_init(&sh.in[w][0], 1), mbar_init(&sh.in[w][1], 1);
+        for (int w = 0; w < 2 * kLinEpiWarps; ++w) mbar_init(&sh.in[w], 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -411,8 +462,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         const bool isb = lane >= 2;
         const int q = isb ? lane - 2 : lane;
         bool ok = true;
-        while (ok && way.next(G, s)) {
-            const int64_t m0 = s.mt * (PAIR ? 256 : 128) + 128 * rank, n0 = s.nt * G.bn + bhalf * rank;
+        while (ok && way.next(G, unit, s)) {
+            const int64_t m0 = (int64_t)s.mt * (PAIR ? 256 : 128) + 128 * rank, n0 = (int64_t)s.nt * G.bn + bhalf * rank;
             const int na = G.a_mn ? (int)min((int64_t)2, max((int64_t)0, (G.m - m0 + 63) / 64)) : 1;
             const int nb = G.b_mn ? (int)min((int64_t)(bhalf + 63) / 64, max((int64_t)0, (G.n - n0 + 63) / 64)) : 1;
             const uint32_t bytes = (G.a_mn ? na * 8192 : 16384) + (G.b_mn ? nb * 8192 : G.b_box * 128);
@@ -420,7 +471,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             const int64_t r0 = isb ? n0 : m0;
             const uint32_t dst = (isb ? 16384 : 0) + q * 8192;
             const CUtensorMap* map = isb ? &M.b : &M.a;
-            for (int64_t kb = s.kb0; kb < s.kb1; ++kb) {
+            for (int kb = s.kb0; kb < s.kb1; ++kb) {
                 ok = __all_sync(~0u, mbar_wait(&sh.empty[R.stage], R.parity() ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_PRODUCER_EMPTY));
                 if (!ok) break;
                 uint64_t* bar = &sh.full[R.stage];
@@ -447,9 +498,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         const uint32_t alead = G.a_mn ? 8192 : 16, blead = G.b_mn ? 8192 : 16;
         bool alone = false;  // the tile before took sums
         bool ok = true;
-        for (uint32_t local = 0; ok && way.next(G, s); ++local) {
+        for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
             if (second) {
-                for (int64_t kb = s.kb0; ok && kb < s.kb1; ++kb) {
+                for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
                     ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
                     if (!ok) break;
                     arrive_first(&sh.full[R.stage]);
@@ -464,7 +515,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 ok = mbar_wait(&sh.tempty[acc ^ 1], ((local - 1) >> 1) & 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
             alone = sums;
             tc_fence_after();
-            for (int64_t kb = s.kb0; ok && kb < s.kb1; ++kb) {
+            for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
                 ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
                 if (!ok) break;
                 tc_fence_after();
@@ -497,40 +548,38 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 umma_commit(&sh.tfull[acc]);
         }
     } else if (warp >= 2) {
-        // a pass of columns at a time, the two warps of a lane quarter in turn, 16 columns of the thread's lane at once
-        const int q = warp & 3, turn = (warp - 2) >> 2, r = 32 * q + lane;
+        // a pass of columns at a time, the two warps of a set's lane quarter in turn, 32 columns of the thread's lane at once
+        const int q = warp & 3, set = (warp - 2) >> 3, turn = ((warp - 2) >> 2) & 1, r = 32 * q + lane;
         const LinStage& S = G.st;
-        uint8_t* mine = passes + (warp - 2) * S.buffers * (S.out_bytes + S.aux_bytes);
-        const uint32_t in_bytes = (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
+        uint8_t *out = passes + (warp - 2) * (S.out_bytes + S.aux_bytes), *aux = out + S.out_bytes;
+        const uint32_t in_bytes = SWAP || !S.tma ? 0 : (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
         uint32_t done = 0, asked = 0;  // passes finished, and those whose loads were issued
-        LinPasses<PAIR> ahead(G, unit, turn);
-        // loads of the next pass that has none yet, into the buffer that its turn is; lane 0, once that buffer's store has been read
+        bool ok = set < S.sets || SWAP;
+        LinPasses ahead(G, unit, set, turn);
+        // the next pass's loads, once the present one's store has been read
         auto ask = [&]() {
-            if (!ahead.more) return;
-            const int b = asked % S.buffers;
-            uint8_t* out = mine + b * (S.out_bytes + S.aux_bytes);
-            const int row = (int)(ahead.s.mt * (PAIR ? 256 : 128) + 128 * rank + 32 * q), col = (int)(ahead.s.nt * G.bn) + ahead.c;
-            if (S.tma && in_bytes && lane == 0) {
-                uint64_t* bar = &sh.in[warp - 2][b];
-                mbar_arrive_expect_tx(bar, in_bytes);
-                const int step = E.f32 ? 32 : 64;
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+            if (!in_bytes || !ahead.more) return;
+            if (lane == 0) {
+                const int row = ahead.s.mt * (PAIR ? 256 : 128) + 128 * rank + 32 * q, col = ahead.s.nt * G.bn + ahead.c;
+                mbar_arrive_expect_tx(&sh.in[warp - 2], in_bytes);
                 if (S.load_add)
-                    for (int x = 0; x < S.out_bytes / 4096; ++x) tma_load_2d(out + x * 4096, &M.add, bar, col + x * step, row);
-                if (S.load_aux) tma_load_2d(out + S.out_bytes, &M.aux, bar, col, row);
+                    for (int x = 0; x < S.out_bytes / 4096; ++x) tma_load_2d(out + x * 4096, &M.add, &sh.in[warp - 2], col + x * (E.f32 ? 32 : 64), row);
+                if (S.load_aux) tma_load_2d(aux, &M.aux, &sh.in[warp - 2], col, row);
             }
             ++asked;
-            ahead.next(G, turn);
+            ahead.next(G, unit, set, turn);
         };
-        if (!SWAP && S.tma && in_bytes) {
-            ask();
-            __syncwarp();
-        }
-        for (uint32_t local = 0; way.next(G, s); ++local) {
+        if (ok && !SWAP && S.tma) ask();
+        for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
             const uint32_t acc = local & 1, use = local >> 1;
+            if ((SWAP ? 2 : S.sets) == 2 && (int)acc != set) continue;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
-            const int64_t i = s.mt * (PAIR ? 256 : 128) + 128 * rank + r, j0 = s.nt * G.bn;
+            const int64_t i = (int64_t)s.mt * (PAIR ? 256 : 128) + 128 * rank + r, j0 = (int64_t)s.nt * G.bn;
             float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
-            if (!mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL)) break;
+            ok = mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
+            if (!ok) break;
             tc_fence_after();
             if (SWAP || part) {
                 for (int c = 16 * turn; c < G.bn; c += 32) {
@@ -565,29 +614,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     }
                 }
             } else {
-                bool ok = true;
-                for (int c0 = turn * S.gw; ok && c0 < G.bn; c0 += 2 * S.gw, ++done) {
-                    const int b = done % S.buffers;
-                    uint8_t *out = mine + b * (S.out_bytes + S.aux_bytes), *aux = out + S.out_bytes;
+                for (int c0 = turn * S.gw; c0 < G.bn; c0 += 2 * S.gw, ++done) {
                     const int64_t row = i - lane;
                     const int col = (int)j0 + c0;
-                    if (S.tma && in_bytes) {
-                        if (S.buffers == 1 && done) {  // the next pass's loads go where this warp's last store was
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
-                            ask();
-                        }
-                        ok = mbar_wait(&sh.in[warp - 2][b], (done / S.buffers) & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
+                    if (in_bytes) {
+                        ok = mbar_wait(&sh.in[warp - 2], done & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
                         if (!ok) break;
-                    } else if (S.tma) {
-                        if (lane == 0) {
-                            if (S.buffers == 1)
-                                bulk_wait_read<0>();
-                            else
-                                bulk_wait_read<1>();
-                        }
-                        __syncwarp();
-                    } else if (row < E.rows) {
+                    } else if (!S.tma && row < E.rows) {
                         if (S.load_add) slab_copy<true>(out, const_cast<void*>(E.add), E.f32, row, E.rows, col, E.cols, S.gw, E.pitch);
                         if (S.load_aux) slab_copy<true>(aux, const_cast<uint16_t*>(E.pre_in), 0, row, E.rows, col, E.cols, S.gw, E.pitch);
                         __syncwarp();
@@ -603,11 +636,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                             for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[h + e]);
                             if (col + c + h < E.cols) finish_row<OP>(E, S, out, aux, lane, c + h, col + c + h, v);
                         }
-                        if (c == 0 && S.tma && in_bytes && S.buffers == 2) {  // the other buffer's store has had time to be read
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
-                            ask();
-                        }
                     }
                     const bool pre = OP == OP_FWD && S.aux_bytes;
                     if (S.tma) {
@@ -618,8 +646,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                             for (int x = 0; row < E.rows && x < S.out_bytes / 4096; ++x)
                                 if (col + x * step < E.cols) tma_store_2d(&M.out, out + x * 4096, col + x * step, (int)row);
                             if (pre && row < E.rows && col < E.cols) tma_store_2d(&M.aux, aux, col, (int)row);
-                            bulk_commit();  // a group to each pass, an empty one too: they are counted
+                            bulk_commit();
                         }
+                        ask();
                     } else {
                         __syncwarp();
                         if (row < E.rows) {
@@ -652,7 +681,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         }
         if (lane == 0) bulk_wait();
         if (!SWAP && lane == 0 && *(volatile int*)&sh.abort)  // loads in flight end before the CTA leaves
-            for (uint32_t k = done; k < asked; ++k) mbar_wait_timed(&sh.in[warp - 2][k % S.buffers], (k / S.buffers) & 1, G.wait_ns);
+            for (uint32_t k = done; k < asked; ++k) mbar_wait_timed(&sh.in[warp - 2], k & 1, G.wait_ns);
     }
     __syncwarp();
     // after a wait that gave up: copies and products in flight end before the CTA leaves
@@ -690,10 +719,10 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int ctas = pair ? 2 : 1, high = 32 / ways;                      // rows of a block
     const int across = (G.bn + 31) / 32, down = ctas * 128 / high;        // blocks of a tile
-    const int64_t e = blockIdx.x / (across * down);
-    const int64_t u0 = e * G.nkb / G.share, u1 = ((e + 1) * G.nkb - 1) / G.share;
+    const int e = blockIdx.x / (across * down);
+    const int64_t u0 = (int64_t)e * G.nkb / G.share, u1 = ((int64_t)(e + 1) * G.nkb - 1) / G.share;
     if (u0 == u1) return;  // this tile was a unit's alone
-    int64_t mt, nt;
+    int mt, nt;
     tile_of(G, G.whole + e, mt, nt);
     const int block = (int)(blockIdx.x - e * across * down), c0 = block / down * 32, r0 = block % down * high;
     const int way = threadIdx.x / (8 * high), in = threadIdx.x % (8 * high), row = r0 + in % high, quad = in / high;
@@ -716,7 +745,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
                 s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
             }
             float v[4] = {s.x, s.y, s.z, s.w};
-            if (c0 + 4 * quad < G.bn) finish_column<OP>(E, nt * G.bn + c0 + 4 * quad, (int)(mt * 128 + row), v);
+            if (c0 + 4 * quad < G.bn) finish_column<OP>(E, (int64_t)nt * G.bn + c0 + 4 * quad, mt * 128 + row, v);
         }
     } else {
         const int lane = threadIdx.x & 31;
@@ -724,15 +753,15 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
             const float* at = reinterpret_cast<const float*>(red + lane / 4 * high + r) + (lane & 3);
             float v[1] = {0.f};
             for (int w = 0; w < ways; ++w) v[0] += at[w * 8 * high * 4];
-            const int64_t i = mt * 128 * ctas + r0 + r;
-            if (i < G.m && c0 + lane < G.bn) finish_column<OP>(E, i, (int)(nt * G.bn) + c0 + lane, v);
+            const int64_t i = (int64_t)mt * 128 * ctas + r0 + r;
+            if (i < G.m && c0 + lane < G.bn) finish_column<OP>(E, i, nt * G.bn + c0 + lane, v);
         }
     }
     // db of the tile: 256 values, by the tile's first block
     if (OP == OP_WGRAD && E.db && (SWAP ? mt : nt) == 0 && block == 0) {
         float b = 0.f;
         for (int64_t u = u0; u <= u1; ++u) b += __ldcg(G.dpart + (2 * u + (u == u0)) * 256 + threadIdx.x);
-        const int64_t j = SWAP ? nt * G.bn + threadIdx.x : mt * 128 * ctas + threadIdx.x;
+        const int64_t j = SWAP ? (int64_t)nt * G.bn + threadIdx.x : (int64_t)mt * 128 * ctas + threadIdx.x;
         const bool there = SWAP ? (int)threadIdx.x < G.bn && j < G.n : (int)threadIdx.x < 128 * ctas && j < G.m;
         if (there) E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
     }
@@ -767,7 +796,7 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, c
     cfg.numAttrs = PAIR ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kernel, M, P.g, E) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
     if (!P.cut) return CF_OK;
-    const int64_t tiles = P.g.rest / P.g.nkb, parts = (P.g.nkb + P.g.share - 1) / P.g.share + 1;
+    const int64_t tiles = P.g.rest / P.g.nkb, parts = ((int64_t)P.g.nkb + P.g.share - 1) / P.g.share + 1;
     int ways = 1;
     while (ways < 8 && 4 * ways < parts) ways *= 2;
     cfg.gridDim = dim3((unsigned)(tiles * ((P.g.bn + 31) / 32) * ((PAIR ? 2 : 1) * 4 * ways)));
