@@ -211,30 +211,35 @@ __device__ __forceinline__ void slab_store16(uint8_t* buf, int f32, int r, int c
                 make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
     }
 }
-// A warp's copies between a buffer and rows that begin anywhere: rows [i, i + 32) of `rows`, columns [j, j + width) of `cols`.
-template <bool IN>
-__device__ __forceinline__ void slab_copy(uint8_t* buf, void* p, int f32, int64_t i, int64_t rows, int j, int cols, int width, int64_t pitch) {
+// A warp's copies between a buffer and rows that begin anywhere: rows [i, i + 32) of `rows`, columns [j, j + width) of `cols`; eight
+// accesses of a lane in flight.
+template <bool IN, typename T>
+__device__ __forceinline__ void slab_copy(uint8_t* buf, T* p, int64_t i, int64_t rows, int j, int cols, int width, int64_t pitch) {
     const int lane = threadIdx.x & 31, high = (int)min((int64_t)32, rows - i);
     for (int c = lane; c < width && j + c < cols; c += 32) {
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r) {
-            if (r >= high) continue;
-            const int64_t o = (i + r) * pitch + j + c;
-            if (f32) {
-                float* at = reinterpret_cast<float*>(buf + slab_at(r, 4 * c));
+        T* at = p + i * pitch + j + c;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+            T v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                v[r] = !IN ? *reinterpret_cast<const T*>(buf + slab_at(r0 + r, (int)sizeof(T) * c)) : r0 + r < high ? at[(r0 + r) * pitch] : T(0);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
                 if (IN)
-                    *at = static_cast<float*>(p)[o];
-                else
-                    static_cast<float*>(p)[o] = *at;
-            } else {
-                uint16_t* at = reinterpret_cast<uint16_t*>(buf + slab_at(r, 2 * c));
-                if (IN)
-                    *at = static_cast<uint16_t*>(p)[o];
-                else
-                    static_cast<uint16_t*>(p)[o] = *at;
+                    *reinterpret_cast<T*>(buf + slab_at(r0 + r, (int)sizeof(T) * c)) = v[r];
+                else if (r0 + r < high)
+                    at[(r0 + r) * pitch] = v[r];
             }
         }
     }
+}
+template <bool IN>
+__device__ __forceinline__ void slab_copy(uint8_t* buf, void* p, int f32, int64_t i, int64_t rows, int j, int cols, int width, int64_t pitch) {
+    if (f32)
+        slab_copy<IN>(buf, static_cast<float*>(p), i, rows, j, cols, width, pitch);
+    else
+        slab_copy<IN>(buf, static_cast<uint16_t*>(p), i, rows, j, cols, width, pitch);
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(smem_u32(src)), "r"(c0), "r"(c1)
@@ -407,7 +412,8 @@ struct LinMaps {
     CUtensorMap aux;       // the pre-activation
 };
 
-template <bool PAIR, int OP, bool SWAP>
+// TMA: S.tma, which a kernel of both would pay for with registers.
+template <bool PAIR, int OP, bool SWAP, bool TMA>
 __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ LinMaps M, const __grid_constant__ LinGemm G,
                                                                      const __grid_constant__ LinEpi E) {
     extern __shared__ uint8_t smem_raw[];
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         const int q = warp & 3, set = (warp - 2) >> 3, turn = ((warp - 2) >> 2) & 1, r = 32 * q + lane;
         const LinStage& S = G.st;
         uint8_t *out = passes + (warp - 2) * (S.out_bytes + S.aux_bytes), *aux = out + S.out_bytes;
-        const uint32_t in_bytes = SWAP || !S.tma ? 0 : (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
+        const uint32_t in_bytes = SWAP || !TMA ? 0 : (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
         uint32_t done = 0, asked = 0;  // passes finished, and those whose loads were issued
         bool ok = set < S.sets || SWAP;
         LinPasses ahead(G, unit, set, turn);
@@ -571,7 +577,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             ++asked;
             ahead.next(G, unit, set, turn);
         };
-        if (ok && !SWAP && S.tma) ask();
+        if (ok && !SWAP && TMA) ask();
         for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
             const uint32_t acc = local & 1, use = local >> 1;
             if ((SWAP ? 2 : S.sets) == 2 && (int)acc != set) continue;
@@ -617,10 +623,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 for (int c0 = turn * S.gw; c0 < G.bn; c0 += 2 * S.gw, ++done) {
                     const int64_t row = i - lane;
                     const int col = (int)j0 + c0;
-                    if (in_bytes) {
+                    if (TMA && in_bytes) {
                         ok = mbar_wait(&sh.in[warp - 2], done & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
                         if (!ok) break;
-                    } else if (!S.tma && row < E.rows) {
+                    } else if (!TMA && row < E.rows) {
                         if (S.load_add) slab_copy<true>(out, const_cast<void*>(E.add), E.f32, row, E.rows, col, E.cols, S.gw, E.pitch);
                         if (S.load_aux) slab_copy<true>(aux, const_cast<uint16_t*>(E.pre_in), 0, row, E.rows, col, E.cols, S.gw, E.pitch);
                         __syncwarp();
@@ -638,7 +644,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                         }
                     }
                     const bool pre = OP == OP_FWD && S.aux_bytes;
-                    if (S.tma) {
+                    if (TMA) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -779,9 +785,9 @@ cf_status launch_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M
 
 #ifdef CF_LINEAR_OP
 namespace {
-template <bool PAIR, bool SWAP>
+template <bool PAIR, bool SWAP, bool TMA>
 cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
-    auto kernel = linear_gemm_kernel<PAIR, CF_LINEAR_OP, SWAP>;
+    auto kernel = linear_gemm_kernel<PAIR, CF_LINEAR_OP, SWAP, TMA>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(P.g.units * (PAIR ? 2 : 1)));
@@ -813,8 +819,10 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, c
 
 template <>
 cf_status launch_linear<CF_LINEAR_OP>(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
-    if (P.pair) return run_linear<true, false>(ctx, P, M, E);
-    return P.swap ? run_linear<false, true>(ctx, P, M, E) : run_linear<false, false>(ctx, P, M, E);
+    const bool tma = P.g.st.tma;
+    if (P.pair) return tma ? run_linear<true, false, true>(ctx, P, M, E) : run_linear<true, false, false>(ctx, P, M, E);
+    if (P.swap) return run_linear<false, true, true>(ctx, P, M, E);
+    return tma ? run_linear<false, false, true>(ctx, P, M, E) : run_linear<false, false, false>(ctx, P, M, E);
 }
 #endif
 
