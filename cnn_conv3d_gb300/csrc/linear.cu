@@ -144,7 +144,7 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
     LinGemm& G = P.plan.g;
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     LinMaps M{};
-    uint32_t room = kLinRoom - (OP == OP_WGRAD ? kLinOnes : 0);
+    uint32_t room = kLinSmem - (uint32_t)sizeof(LinShared) - (OP == OP_WGRAD ? kLinOnes : 0);
     if (!P.plan.swap) {
         LinStage& S = G.st;
         if (OP == OP_WGRAD && E.accumulate) E.add = E.out;
@@ -155,7 +155,7 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
         S.gw = E.f32 && !aux ? 32 : 64;
         S.out_bytes = S.gw * (E.f32 ? 128 : 64), S.aux_bytes = aux ? 4096 : 0;
         // both sets where the epilogue is most of a tile's time, if two stages fit beside their room
-        const uint32_t pass = kLinEpiWarps * (S.out_bytes + S.aux_bytes);
+        const uint32_t pass = kLinEpiWarps * (S.out_bytes + S.aux_bytes) + (OP == OP_FWD ? kLinBias : 0);
         S.sets = G.nkb <= 16 && room >= 2 * pass + 2 * G.stage_bytes ? 2 : 1;
         room -= S.sets * pass;
         auto rows_map = [&](CUtensorMap* m, const void* p, bool f32) {

@@ -70,8 +70,8 @@ constexpr int kLinEpiWarps = 8;  // of a set
 constexpr int kLinThreads = 64 + 2 * 32 * kLinEpiWarps;
 constexpr int kLinMostStages = 10;
 constexpr uint32_t kLinOnes = 16 << 10;             // 128 rows of 64 ones (backward weight)
-constexpr uint32_t kLinSmem = 232448 - 1024;        // dynamic: all but the barriers
-constexpr uint32_t kLinRoom = kLinSmem - 1024;      // stages, passes and ones, from a multiple of 1024 on
+constexpr uint32_t kLinSmem = 232448;               // all of it: ones, passes and stages, then LinShared
+constexpr uint32_t kLinBias = kLinEpiWarps * 64 * 4;  // of a set
 
 // ------------------------------------------------------------------------------------------------------------------ activations
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -247,24 +247,18 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// 16 columns of a row, from column c of the pass, column j of D, on: what is added and the derivative's argument lie in the buffers.
+// 16 columns of a row from column c of the pass on: the pass's bias, what is added and the derivative's argument are in shared memory.
 template <int OP>
-__device__ __forceinline__ void finish_row(const LinEpi& E, const LinStage& S, uint8_t* out, uint8_t* aux, int r, int c, int j, float (&v)[16]) {
+__device__ __forceinline__ void finish_row(const LinEpi& E, const LinStage& S, uint8_t* out, uint8_t* aux, const float* bias, int r, int c, float (&v)[16]) {
     float t[16];
     if (OP == OP_FWD) {
         if (E.bias) {
-            if (j + 16 <= E.cols) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 q = __ldg(reinterpret_cast<const float4*>(E.bias + j + e));
-                    apart(add2(two(v[e], v[e + 1]), two(q.x, q.y)), v[e], v[e + 1]);
-                    apart(add2(two(v[e + 2], v[e + 3]), two(q.z, q.w)), v[e + 2], v[e + 3]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += j + e < E.cols ? E.bias[j + e] : 0.f;
+            for (int e = 0; e < 16; e += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(bias + c + e);
+                apart(add2(two(v[e], v[e + 1]), two(q.x, q.y)), v[e], v[e + 1]);
+                apart(add2(two(v[e + 2], v[e + 3]), two(q.z, q.w)), v[e + 2], v[e + 3]);
             }
         }
         if (S.aux_bytes) slab_store16(aux, 0, r, c, v);
@@ -362,10 +356,11 @@ struct LinWalk {
 };
 
 struct LinShared {
-    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain, in[2 * kLinEpiWarps];
+    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], in[2 * kLinEpiWarps], drain;
     uint32_t tmem;
     int abort;
 };
+static_assert(sizeof(LinShared) % 16 == 0, "the bias is before it");
 struct LinRing {
     int stage = 0;
     uint32_t bits = 0, issued = 0;
@@ -416,28 +411,36 @@ struct LinMaps {
 template <bool PAIR, int OP, bool SWAP, bool TMA>
 __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ LinMaps M, const __grid_constant__ LinGemm G,
                                                                      const __grid_constant__ LinEpi E) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ LinShared sh;
-    uint8_t* ones = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if (smem_u32(smem_raw) & 1023) {  // the swizzle goes by the address, and there is no room to move in
+        if (threadIdx.x == 0) atomicCAS(G.status, 0, (int)WAIT_PROBE);
+        return;
+    }
+    uint8_t* ones = smem_raw;
+    LinShared& sh = *reinterpret_cast<LinShared*>(smem_raw + kLinSmem - sizeof(LinShared));
     uint8_t* passes = ones + (OP == OP_WGRAD ? kLinOnes : 0);
     uint8_t* ring = passes + (SWAP ? 0 : G.st.sets * kLinEpiWarps * (G.st.out_bytes + G.st.aux_bytes));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
     const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-    if (threadIdx.x == 0) {
-        tma_prefetch_desc(&M.a);
-        tma_prefetch_desc(&M.b);
-        for (int s = 0; s < kLinMostStages; ++s) {
-            mbar_init(&sh.full[s], PAIR && rank == 0 ? 2 : 1);
-            mbar_init(&sh.empty[s], 1);
+    if (warp == 0) {
+        // a lane to each barrier
+        if (lane == 0) {
+            tma_prefetch_desc(&M.a);
+            tma_prefetch_desc(&M.b);
+            sh.abort = 0;
         }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(&sh.tfull[a], 1);
-            mbar_init(&sh.tempty[a], (PAIR ? 2 : 1) * kLinEpiWarps);
+        if (lane < kLinMostStages) {
+            mbar_init(&sh.full[lane], PAIR && rank == 0 ? 2 : 1);
+            mbar_init(&sh.empty[lane], 1);
+        } else if (lane < kLinMostStages + 2) {
+            mbar_init(&sh.tfull[lane - kLinMostStages], 1);
+            mbar_init(&sh.tempty[lane - kLinMostStages], (PAIR ? 2 : 1) * kLinEpiWarps);
+        } else if (lane == kLinMostStages + 2) {
+            mbar_init(&sh.drain, 1);
         }
-        mbar_init(&sh.drain, 1);
-        for (int w = 0; w < 2 * kLinEpiWarps; ++w) mbar_init(&sh.in[w], 1);
-        sh.abort = 0;
+        if (lane >= 32 - 2 * kLinEpiWarps) mbar_init(&sh.in[lane - (32 - 2 * kLinEpiWarps)], 1);
         fence_barrier_init();
+        __syncwarp();
     }
     if (OP == OP_WGRAD) {
         for (int e = threadIdx.x; e < (int)kLinOnes / 4; e += kLinThreads) reinterpret_cast<uint32_t*>(ones)[e] = 0x3F803F80u;
@@ -453,11 +456,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         }
     }
     tc_fence_before();
+    // the barriers are the first warp's own, so that a lone CTA's loads need not wait for the others
     if (PAIR)
         cluster_sync();
+    else if (warp == 0)
+        asm volatile("bar.arrive 1, %0;" ::"n"(kLinThreads) : "memory");
     else
-        __syncthreads();
+        named_bar_sync(1, kLinThreads);
     tc_fence_after();
+    // begun under the end of the launch before.  (Letting the joining launch begin under this one's end took 1.3 us longer.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     LinWalk way(G, unit);
     LinItem s;
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 umma_commit(&sh.tfull[acc]);
         }
     } else if (warp >= 2) {
-        // a pass of columns at a time, the two warps of a set's lane quarter in turn, 32 columns of the thread's lane at once
+        // a pass of columns at a time, the two warps of a set's lane quarter in turn, 16 columns of the thread's lane at once
         const int q = warp & 3, set = (warp - 2) >> 3, turn = ((warp - 2) >> 2) & 1, r = 32 * q + lane;
         const LinStage& S = G.st;
         uint8_t *out = passes + (warp - 2) * (S.out_bytes + S.aux_bytes), *aux = out + S.out_bytes;
@@ -578,12 +586,20 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             ahead.next(G, unit, set, turn);
         };
         if (ok && !SWAP && TMA) ask();
+        // the pass's bias, loaded before its products are there
+        float *biases = reinterpret_cast<float*>(&sh) - S.sets * kLinBias / 4 + (warp - 2) * 64, b0 = 0.f, b1 = 0.f;
+        auto ask_bias = [&](int64_t j) {
+            if (OP != OP_FWD || SWAP || !E.bias) return;
+            b0 = j + lane < E.cols ? E.bias[j + lane] : 0.f;
+            b1 = j + 32 + lane < E.cols ? E.bias[j + 32 + lane] : 0.f;
+        };
         for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
             const uint32_t acc = local & 1, use = local >> 1;
             if ((SWAP ? 2 : S.sets) == 2 && (int)acc != set) continue;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
             const int64_t i = (int64_t)s.mt * (PAIR ? 256 : 128) + 128 * rank + r, j0 = (int64_t)s.nt * G.bn;
             float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
+            ask_bias(j0 + turn * S.gw);
             ok = mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
             if (!ok) break;
             tc_fence_after();
@@ -631,17 +647,20 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                         if (S.load_aux) slab_copy<true>(aux, const_cast<uint16_t*>(E.pre_in), 0, row, E.rows, col, E.cols, S.gw, E.pitch);
                         __syncwarp();
                     }
-                    for (int c = 0; c < S.gw && c0 + c < G.bn; c += 32) {
-                        uint32_t u[32];
-                        tmem_ld32(tm + c0 + c, u);
+                    if (OP == OP_FWD && E.bias) {
+                        biases[lane] = b0, biases[32 + lane] = b1;
+                        __syncwarp();
+                        ask_bias(col + 2 * S.gw);
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < S.gw && c0 + c < G.bn; c += 16) {
+                        uint32_t u[32];  // the first 16
+                        tmem_ld16(tm + c0 + c, u);
                         tmem_ld_wait();
+                        float v[16];
 #pragma unroll
-                        for (int h = 0; h < 32; h += 16) {
-                            float v[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[h + e]);
-                            if (col + c + h < E.cols) finish_row<OP>(E, S, out, aux, lane, c + h, col + c + h, v);
-                        }
+                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
+                        if (col + c < E.cols) finish_row<OP>(E, S, out, aux, biases, lane, c, v);
                     }
                     const bool pre = OP == OP_FWD && S.aux_bytes;
                     if (TMA) {
@@ -685,7 +704,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     mbar_arrive(&sh.tempty[acc]);
             }
         }
-        if (lane == 0) bulk_wait();
+        if (lane == 0) bulk_wait_read();  // shared memory outlives the stores' reads; the stores end with the grid
         if (!SWAP && lane == 0 && *(volatile int*)&sh.abort)  // loads in flight end before the CTA leaves
             for (uint32_t k = done; k < asked; ++k) mbar_wait_timed(&sh.in[warp - 2], k & 1, G.wait_ns);
     }
@@ -794,12 +813,14 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, c
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = kLinSmem;
     cfg.stream = ctx.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = PAIR ? 2 : 1;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = PAIR ? 2 : 1;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 1 : 0;
+    cfg.numAttrs = PAIR ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, M, P.g, E) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
     if (!P.cut) return CF_OK;
     const int64_t tiles = P.g.rest / P.g.nkb, parts = ((int64_t)P.g.nkb + P.g.share - 1) / P.g.share + 1;
@@ -808,8 +829,6 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, c
     cfg.gridDim = dim3((unsigned)(tiles * ((P.g.bn + 31) / 32) * ((PAIR ? 2 : 1) * 4 * ways)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, linear_join_kernel<CF_LINEAR_OP, SWAP>, P.g, E, PAIR ? 1 : 0, ways) != cudaSuccess)
         return cudaGetLastError(), CF_ERR_CUDA;
