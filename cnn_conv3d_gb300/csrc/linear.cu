@@ -73,6 +73,41 @@ int64_t over(int64_t v, int64_t by) { return (v + by - 1) / by; }
 // with as little of the rows as there is.  Likewise a k of at most 128 in the backward weight beside a wider n.
 bool exchanged(int op, int64_t rows, int64_t k, int64_t n) { return op == OP_WGRAD ? k <= 128 && n > 128 : rows <= 128; }
 
+// A way to cut a product, and about how long it takes.
+struct Shape {
+    bool pair;
+    int bn, units, stage_bytes;
+    int64_t tm, tn, whole, share;  // tiles dealt out whole; a unit's blocks of the others
+    double ns;
+};
+
+// What a call's time is made of, in ns, as measured on its parts: 2000 until the first stage is there; a stage as its bytes come from
+// L2 (105 a ns and SM, 118 at best) or its products run, whichever is longer; an epilogue of 1000 and 700 for each 128 columns, under
+// the next tile's products if there is one; and where tiles are cut, writing parts at 50 bytes a ns and SM, and a second launch that
+// reads them all at 4000.  A pair's launch and barriers take 700 more; over many rounds its tiles' epilogues go better (64 -> 256 on
+// 2.1M rows 416 us on pairs, 562 on lone CTAs, whose stages are half as large again and only two fit).
+bool shape(const LinGemm& G, bool pair, int bn, bool cut, Shape& t) {
+    t.pair = pair, t.bn = bn;
+    t.units = pair ? kPlanSms / 2 : kPlanSms;
+    t.tm = over(G.m, pair ? 256 : 128), t.tn = over(G.n, bn);
+    const int half = pair ? bn / 2 : bn;
+    t.stage_bytes = (int)(16384 + (G.b_mn ? up(half, 64) * 128 : up(half * 128, 1024)));
+    const double products = 4 / 1.9 * std::max(bn / 2.0, (4096 + 32.0 * bn) / 128), block = std::max(t.stage_bytes / 105.0, products);
+    const double epilogue = 1000 + 700 * over(bn, 128), start = pair ? 2700 : 2000, round = pair ? epilogue : 1.3 * epilogue;
+    const int64_t tiles = t.tm * t.tn, rounds = tiles / t.units, rem = tiles - rounds * t.units;
+    t.whole = tiles, t.share = 1;
+    if (!cut) {
+        const int64_t most = rounds + (rem > 0);
+        t.ns = start + std::max(most * G.nkb * block, (most - 1) * round) + epilogue;
+        return true;
+    }
+    t.whole = tiles - rem, t.share = std::max<int64_t>(2, over(rem * G.nkb, t.units));
+    if (rem == 0 || t.share >= G.nkb) return false;
+    const double bytes = 512.0 * bn, parts = over(rem * G.nkb, t.share) * (pair ? 2 : 1) * bytes;
+    t.ns = start + std::max((rounds * G.nkb + t.share) * block, rounds * round) + 500 + bytes / 50 + 3000 + parts / 4000;
+    return true;
+}
+
 Product plan_of(const cf_linear_desc* d, int op) {
     const Side x{d->rows, d->k, x_pitch(d), op == OP_WGRAD}, w{d->n, d->k, d->k, op == OP_DGRAD}, dz{d->rows, d->n, y_pitch(d), op == OP_WGRAD};
     Product P{};
@@ -86,26 +121,28 @@ Product plan_of(const cf_linear_desc* d, int op) {
     if (P.plan.swap) std::swap(P.a, P.b), std::swap(G.m, G.n);
     G.a_mn = P.a.mn, G.b_mn = P.b.mn;
 
-    // pairs where there are 256 x 256 tiles, and products enough
-    const int64_t wide = over(G.m, 256) * over(G.n, 256) * G.nkb;
-    P.plan.pair = !P.plan.swap && G.m > 128 && G.n > 128 && wide >= 8 * (kPlanSms / 2);
-    const int units = P.plan.pair ? kPlanSms / 2 : kPlanSms, step = P.plan.pair ? 32 : 16;
-    G.tm = (int)over(G.m, P.plan.pair ? 256 : 128);
-    // the epilogue's passes of 64 columns end with a tile where another follows
-    G.bn = (int)up(over(G.n, over(G.n, 256)), G.n > 256 ? 64 : step);
-    if (!P.plan.pair && G.nkb <= 16)
-        while (G.bn > 64 && (int64_t)G.tm * over(G.n, up(G.bn / 2, 64)) <= units) G.bn = (int)up(G.bn / 2, 64);
-    G.tn = (int)over(G.n, G.bn);
-    const int half = P.plan.pair ? G.bn / 2 : G.bn;
-    G.a_box = 128, G.b_box = half;
-    G.stage_bytes = (int)(16384 + (G.b_mn ? up(half, 64) * 128 : up(half * 128, 1024)));
-
-    // tiles over a whole number of rounds are cut where that saves more than the second launch and the parts take
-    const int64_t tiles = (int64_t)G.tm * G.tn, rounds = tiles / units, rem = tiles - rounds * units;
-    const double block = G.stage_bytes / 100e3, join = 4.0;  // us
-    const int64_t share = std::max<int64_t>(2, over(rem * G.nkb, units));
-    G.whole = (int)tiles, G.rest = 0, G.share = 1;
-    if (rem && (G.nkb - share) * block > join) G.whole = (int)(tiles - rem), G.rest = rem * G.nkb, G.share = (int)share;
+    // The tile and the cut that should be quickest.
+    Shape best{}, t;
+    for (const bool pair : {true, false}) {
+        if (pair && (P.plan.swap || G.m <= 128 || G.n <= 128)) continue;
+        for (const int at : {256, 192, 128, 64}) {
+            if (P.plan.swap && at < 256) break;
+            // the epilogue's passes of 64 columns end with a tile where another follows
+            const int64_t tn = over(G.n, at);
+            const int bn = (int)up(over(G.n, tn), tn > 1 ? 64 : pair ? 32 : 16);
+            if (bn > 256) continue;
+            for (const bool cut : {false, true})
+                if (shape(G, pair, bn, cut, t) && (best.ns == 0 || t.ns < best.ns)) best = t;
+        }
+    }
+    P.plan.pair = best.pair;
+    const int units = best.units;
+    G.tm = (int)best.tm, G.tn = (int)best.tn, G.bn = best.bn;
+    G.stage_bytes = best.stage_bytes;
+    G.a_box = 128, G.b_box = best.pair ? best.bn / 2 : best.bn;
+    const int64_t tiles = best.tm * best.tn;
+    G.whole = (int)best.whole, G.share = (int)best.share, G.rest = (tiles - best.whole) * G.nkb;
+    const int64_t share = best.share;
     G.units = (int)(G.whole ? std::min<int64_t>(units, tiles) : over(G.rest, G.share));
     P.plan.cut = G.rest && share < G.nkb;
     if (P.plan.cut) {
@@ -145,8 +182,10 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     LinMaps M{};
     uint32_t room = kLinSmem - (uint32_t)sizeof(LinShared) - (OP == OP_WGRAD ? kLinOnes : 0);
+    const bool few = (int64_t)G.tm * G.tn <= 2 * G.units && G.bn > 128;
+    LinStage& S = G.st;
+    S.sets = few ? 1 : 2, S.turns = few ? 4 : 2;
     if (!P.plan.swap) {
-        LinStage& S = G.st;
         if (OP == OP_WGRAD && E.accumulate) E.add = E.out;
         const bool aux = E.pre_in || E.pre_out;
         S.load_add = E.add != nullptr, S.load_aux = E.pre_in != nullptr;
@@ -154,10 +193,12 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
         S.tma = E.pitch % 8 == 0 && E.cols % 8 == 0;
         S.gw = E.f32 && !aux ? 32 : 64;
         S.out_bytes = S.gw * (E.f32 ? 128 : 64), S.aux_bytes = aux ? 4096 : 0;
-        // both sets where the epilogue is most of a tile's time, if two stages fit beside their room
-        const uint32_t pass = kLinEpiWarps * (S.out_bytes + S.aux_bytes) + (OP == OP_FWD ? kLinBias : 0);
-        S.sets = G.nkb <= 16 && room >= 2 * pass + 2 * G.stage_bytes ? 2 : 1;
-        room -= S.sets * pass;
+        // All warps, on one tile or on two in turn, where the epilogue is much of a tile's time and two stages fit beside their room;
+        // else half of them, and more stages.
+        const uint32_t pass = S.out_bytes + S.aux_bytes + (OP == OP_FWD ? kLinBias : 0);
+        const bool all = G.nkb <= 16 && room >= kLinEpiWarps * pass + 2 * G.stage_bytes;
+        S.sets = all && !few ? 2 : 1, S.turns = all && few ? 4 : 2;
+        room -= 4 * S.sets * S.turns * pass;
         auto rows_map = [&](CUtensorMap* m, const void* p, bool f32) {
             const uint64_t dims[2] = {(uint64_t)E.cols, (uint64_t)E.rows}, strides[1] = {(uint64_t)E.pitch * (f32 ? 4 : 2)};
             const uint32_t box[2] = {f32 ? 32u : 64u, 32};

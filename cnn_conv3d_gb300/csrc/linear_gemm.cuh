@@ -7,7 +7,7 @@
 // or the two exchanged (SWAP) where that side is narrow: few rows in the forward and the backward data, so that the weights' rows
 // fill the 128 lanes of a tile and the rows are its columns, and a narrow k in the backward weight.
 //
-// A CTA is a TMA warp, an issuing thread and two sets of eight epilogue warps.  Operands come in stages of 64 of the contracted axis (128-byte
+// A CTA is a TMA warp, an issuing thread and sixteen epilogue warps.  Operands come in stages of 64 of the contracted axis (128-byte
 // rows, swizzled); tiles are 128 rows by up to 256 columns, or 256 by 256 on a pair of CTAs with one instruction for both, each CTA
 // fetching half of either side: then a stage costs 64 bytes of L2 a cycle and SM, where a lone CTA's would cost 96 of the about 70
 // that it gives.  The accumulator is double: the epilogue of a tile runs under the products of the next.
@@ -43,7 +43,7 @@ struct LinEpi {
 struct LinStage {
     int tma;                   // rows begin and end at 16 bytes; otherwise a warp copies value by value along the rows
     int gw;                    // columns of a pass: 64, or 32 of fp32 with no pre-activation beside them
-    int sets;                  // 2: sets of epilogue warps take the tiles in turn; 1: one takes all
+    int sets, turns;           // sets of epilogue warps that take the tiles in turn; a set's warps for each quarter of the lanes
     int out_bytes, aux_bytes;  // a warp's room: the output (and what is added to it, in the same place), the pre-activation
     int load_add, load_aux;
 };
@@ -66,12 +66,12 @@ struct LinGemm {
     uint64_t wait_ns;
 };
 
-constexpr int kLinEpiWarps = 8;  // of a set
-constexpr int kLinThreads = 64 + 2 * 32 * kLinEpiWarps;
+constexpr int kLinEpiWarps = 16;
+constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
 constexpr int kLinMostStages = 10;
 constexpr uint32_t kLinOnes = 16 << 10;             // 128 rows of 64 ones (backward weight)
 constexpr uint32_t kLinSmem = 232448;               // all of it: ones, passes and stages, then LinShared
-constexpr uint32_t kLinBias = kLinEpiWarps * 64 * 4;  // of a set
+constexpr uint32_t kLinBias = 64 * 4;               // of a warp's pass
 
 // ------------------------------------------------------------------------------------------------------------------ activations
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -356,7 +356,7 @@ struct LinWalk {
 };
 
 struct LinShared {
-    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], in[2 * kLinEpiWarps], drain;
+    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], in[kLinEpiWarps], drain;
     uint32_t tmem;
     int abort;
 };
@@ -388,7 +388,7 @@ struct LinPasses {
         next(G, unit, set, turn);
     }
     __device__ __forceinline__ void next(const LinGemm& G, int unit, int set, int turn) {
-        c += 2 * G.st.gw;
+        c += G.st.turns * G.st.gw;
         while (more && c >= G.bn) {
             bool mine;
             do {
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
     uint8_t* ones = smem_raw;
     LinShared& sh = *reinterpret_cast<LinShared*>(smem_raw + kLinSmem - sizeof(LinShared));
     uint8_t* passes = ones + (OP == OP_WGRAD ? kLinOnes : 0);
-    uint8_t* ring = passes + (SWAP ? 0 : G.st.sets * kLinEpiWarps * (G.st.out_bytes + G.st.aux_bytes));
+    uint8_t* ring = passes + (SWAP ? 0 : 4 * G.st.sets * G.st.turns * (G.st.out_bytes + G.st.aux_bytes));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = PAIR ? (int)cluster_rank() : 0;
     const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
     if (warp == 0) {
@@ -434,11 +434,11 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             mbar_init(&sh.empty[lane], 1);
         } else if (lane < kLinMostStages + 2) {
             mbar_init(&sh.tfull[lane - kLinMostStages], 1);
-            mbar_init(&sh.tempty[lane - kLinMostStages], (PAIR ? 2 : 1) * kLinEpiWarps);
+            mbar_init(&sh.tempty[lane - kLinMostStages], (PAIR ? 2 : 1) * 4 * G.st.turns);
         } else if (lane == kLinMostStages + 2) {
             mbar_init(&sh.drain, 1);
         }
-        if (lane >= 32 - 2 * kLinEpiWarps) mbar_init(&sh.in[lane - (32 - 2 * kLinEpiWarps)], 1);
+        if (lane >= 32 - kLinEpiWarps) mbar_init(&sh.in[lane - (32 - kLinEpiWarps)], 1);
         fence_barrier_init();
         __syncwarp();
     }
@@ -562,13 +562,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 umma_commit(&sh.tfull[acc]);
         }
     } else if (warp >= 2) {
-        // a pass of columns at a time, the two warps of a set's lane quarter in turn, 16 columns of the thread's lane at once
-        const int q = warp & 3, set = (warp - 2) >> 3, turn = ((warp - 2) >> 2) & 1, r = 32 * q + lane;
+        // a pass of columns at a time, a set's warps of a quarter of the lanes in turn, 16 columns of the thread's lane at once
         const LinStage& S = G.st;
+        const int q = warp & 3, group = (warp - 2) >> 2, set = S.turns == 4 ? 0 : group >> 1, turn = S.turns == 4 ? group : group & 1;
+        const int r = 32 * q + lane;
         uint8_t *out = passes + (warp - 2) * (S.out_bytes + S.aux_bytes), *aux = out + S.out_bytes;
         const uint32_t in_bytes = SWAP || !TMA ? 0 : (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
         uint32_t done = 0, asked = 0;  // passes finished, and those whose loads were issued
-        bool ok = set < S.sets || SWAP;
+        bool ok = set < S.sets;
         LinPasses ahead(G, unit, set, turn);
         // the next pass's loads, once the present one's store has been read
         auto ask = [&]() {
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         };
         if (ok && !SWAP && TMA) ask();
         // the pass's bias, loaded before its products are there
-        float *biases = reinterpret_cast<float*>(&sh) - S.sets * kLinBias / 4 + (warp - 2) * 64, b0 = 0.f, b1 = 0.f;
+        float *biases = reinterpret_cast<float*>(&sh) - 4 * S.sets * S.turns * kLinBias / 4 + (warp - 2) * 64, b0 = 0.f, b1 = 0.f;
         auto ask_bias = [&](int64_t j) {
             if (OP != OP_FWD || SWAP || !E.bias) return;
             b0 = j + lane < E.cols ? E.bias[j + lane] : 0.f;
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         };
         for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
             const uint32_t acc = local & 1, use = local >> 1;
-            if ((SWAP ? 2 : S.sets) == 2 && (int)acc != set) continue;
+            if (S.sets == 2 && (int)acc != set) continue;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
             const int64_t i = (int64_t)s.mt * (PAIR ? 256 : 128) + 128 * rank + r, j0 = (int64_t)s.nt * G.bn;
             float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             if (!ok) break;
             tc_fence_after();
             if (SWAP || part) {
-                for (int c = 16 * turn; c < G.bn; c += 32) {
+                for (int c = 16 * turn; c < G.bn; c += 16 * S.turns) {
                     uint32_t u[32];
                     tmem_ld16(tm + c, u);
                     tmem_ld_wait();
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     }
                 }
             } else {
-                for (int c0 = turn * S.gw; c0 < G.bn; c0 += 2 * S.gw, ++done) {
+                for (int c0 = turn * S.gw; c0 < G.bn; c0 += S.turns * S.gw, ++done) {
                     const int64_t row = i - lane;
                     const int col = (int)j0 + c0;
                     if (TMA && in_bytes) {
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     if (OP == OP_FWD && E.bias) {
                         biases[lane] = b0, biases[32 + lane] = b1;
                         __syncwarp();
-                        ask_bias(col + 2 * S.gw);
+                        ask_bias(col + S.turns * S.gw);
                     }
 #pragma unroll 1
                     for (int c = 0; c < S.gw && c0 + c < G.bn; c += 16) {
