@@ -292,45 +292,73 @@ __device__ __forceinline__ void vector8(const float* p, int64_t o, const C_& C, 
     }
 }
 
-// Sums over a row's threads, the same in each of them.  WIDE: one barrier, the buffers in turn.
+// Sums over the threads of B rows, the same in each of them.  WIDE: one barrier of the rows' T threads, the buffers in turn; it also
+// tells all of them of a thread that has failed.
+constexpr int kMostRows = 2;
 template <bool WIDE>
 struct RowSum {
-    float2 (*red)[32];
+    float (*red)[16][2 * kMostRows];
     int turn = 0, T;
-    __device__ __forceinline__ float2 operator()(float a, float b) {
-        for (int o = (WIDE ? 32 : T) >> 1; o; o >>= 1) {
-            a += __shfl_xor_sync(~0u, a, o);
-            b += __shfl_xor_sync(~0u, b, o);
-        }
+    int failed = 0;
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&v)[N]) {
+        for (int o = (WIDE ? 32 : T) >> 1; o; o >>= 1)
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] += __shfl_xor_sync(~0u, v[e], o);
         if (WIDE) {
-            float2* r = red[turn];
+            float(*r)[2 * kMostRows] = red[turn];
             turn ^= 1;
-            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
-            __syncthreads();
-            a = b = 0.f;
-            for (int i = 0; i < (int)(blockDim.x >> 5); ++i) a += r[i].x, b += r[i].y;
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int e = 0; e < N; ++e) r[threadIdx.x >> 5][e] = v[e];
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.s32 p, %0, 0;\n\t"
+                "barrier.cta.red.or.pred q, 1, %1, p;\n\t"
+                "selp.s32 %0, 1, 0, q;\n\t}\n"
+                : "+r"(failed)
+                : "r"(T)
+                : "memory");
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < T >> 5; ++i)
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] += r[i][e];
         }
-        return make_float2(a, b);
     }
 };
 
-// (mean, 1 / width) of a row that its threads hold eight values of each.
-template <bool WIDE, typename C_>
-__device__ __forceinline__ float2 stats8(const RnArgs& A, int kind, const C_& C, RowSum<WIDE>& sum, const float (&v)[8]) {
-    if (kind == CF_NORM_NONE) return make_float2(0.f, 1.f);
-    float mean = 0.f, s = 0.f;
+// (mean, 1 / width) of B rows that their threads hold eight values of each.
+template <bool WIDE, int B, typename C_>
+__device__ __forceinline__ void stats8(const RnArgs& A, int kind, const C_& C, RowSum<WIDE>& sum, const float (&v)[B][8], float2 (&st)[B]) {
+#pragma unroll
+    for (int k = 0; k < B; ++k) st[k] = make_float2(0.f, 1.f);
+    if (kind == CF_NORM_NONE) return;
+    float s[B];
     if (kind == CF_NORM_LAYER) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[e];  // values that a thread does not have are 0
-        mean = sum(s, 0.f).x * A.inv_c;
-    }
-    s = 0.f;
+        for (int k = 0; k < B; ++k) {
+            s[k] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float t = C.has(e) ? v[e] - mean : 0.f;
-        s = fmaf(t, t, s);
+            for (int e = 0; e < 8; ++e) s[k] += v[k][e];  // values that a thread does not have are 0
+        }
+        sum(s);
+#pragma unroll
+        for (int k = 0; k < B; ++k) st[k].x = s[k] * A.inv_c;
     }
-    return make_float2(mean, rsqrtf(sum(s, 0.f).x * A.inv_c + A.eps));
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+        s[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float t = C.has(e) ? v[k][e] - st[k].x : 0.f;
+            s[k] = fmaf(t, t, s[k]);
+        }
+    }
+    sum(s);
+#pragma unroll
+    for (int k = 0; k < B; ++k) st[k].y = rsqrtf(s[k] * A.inv_c + A.eps);
 }
 
 // A block's chunk of rows, and the thread's place in them.
@@ -351,24 +379,58 @@ __device__ __forceinline__ Place place_of(const RnArgs& A, int T, C_& C) {
     return P;
 }
 
-template <typename S, typename F, bool WIDE, bool VEC>
-__global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 3) rn_fwd_kernel(const RnArgs A, int T, const S* x, const F* f, S* r, F* h,
-                                                                                     float4* stats) {
-    __shared__ float2 red[2][32];
-    Cols<VEC> C;
-    const Place P = place_of<WIDE>(A, T, C);
-    RowSum<WIDE> sum{red, 0, T};
+// The vectors of a thread's columns: p = a fh + b, h = g rh + beta.
+struct FwdVectors {
     float a[8], b[8], g[8], beta[8];
-    {
+    template <typename C_>
+    __device__ __forceinline__ FwdVectors(const RnArgs& A, const C_& C, int64_t sample) {
         float gate[8];
-        vector8(A.gate, A.gate_each ? P.sample * A.c : 0, C, 1.f, gate);
+        vector8(A.gate, A.gate_each ? sample * A.c : 0, C, 1.f, gate);
         vector8(A.post_gamma, 0, C, 1.f, a);
         vector8(A.post_beta, 0, C, 0.f, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] *= A.scale * gate[e], b[e] *= A.scale * gate[e];
-        vector8(A.pre_gamma, A.pre_each ? P.sample * A.c : 0, C, 1.f, g);
-        vector8(A.pre_beta, A.pre_each ? P.sample * A.c : 0, C, 0.f, beta);
+        vector8(A.pre_gamma, A.pre_each ? sample * A.c : 0, C, 1.f, g);
+        vector8(A.pre_beta, A.pre_each ? sample * A.c : 0, C, 0.f, beta);
     }
+};
+// B rows, `step` apart from row i on, from their values v of x and w of f; rows that are not `mine` are zeros.
+template <typename S, typename F, bool WIDE, int B, typename C_>
+__device__ __forceinline__ void fwd_rows(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, const FwdVectors& V, bool with_f, int64_t i, int step,
+                                         const bool (&mine)[B], float (&v)[B][8], float (&w)[B][8], S* r, F* h, float4* stats) {
+    float2 sf[B], sr[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) sf[k] = make_float2(0.f, 1.f);
+    if (with_f) {
+        stats8<WIDE>(A, A.post, C, sum, w, sf);
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] = C.has(e) ? v[k][e] + fmaf(V.a[e], (w[k][e] - sf[k].x) * sf[k].y, V.b[e]) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+        if (r && mine[k]) store8(r, (i + k * step) * A.c, C, v[k]);
+    stats8<WIDE>(A, A.pre, C, sum, v, sr);
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+        if (h && mine[k]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] = fmaf((v[k][e] - sr[k].x) * sr[k].y, V.g[e], V.beta[e]);
+            store8(h, (i + k * step) * A.c, C, v[k]);
+        }
+        if (stats && mine[k] && C.t == 0) stats[i + k * step] = make_float4(sf[k].x, sf[k].y, sr[k].x, sr[k].y);
+    }
+}
+
+template <typename S, typename F, bool WIDE, bool VEC>
+__global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 3) rn_fwd_kernel(const RnArgs A, int T, const S* x, const F* f, S* r,
+                                                                                              F* h, float4* stats) {
+    __shared__ float red[2][16][2 * kMostRows];
+    Cols<VEC> C;
+    const Place P = place_of<WIDE>(A, T, C);
+    RowSum<WIDE> sum{red, 0, T};
+    const FwdVectors V(A, C, P.sample);
     // all threads of a warp go round as often, for the shuffles
     const int64_t rounds = (P.to - (P.from - (WIDE ? 0 : (int)threadIdx.x / T)) + P.step - 1) / P.step;
     Raw<S> xn{};
@@ -378,114 +440,87 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 3)
         if (f) fn = load8(f, P.from * A.c, C);
     }
     for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t i = P.from + k * P.step, o = i * A.c;
-        const bool mine = i < P.to;
-        float v[8], w[8];
-        unpack(xn, v);
-        unpack(fn, w);
+        const int64_t i = P.from + k * P.step;
+        float v[1][8], w[1][8];
+        unpack(xn, v[0]);
+        unpack(fn, w[0]);
         if (i + P.step < P.to) {
-            xn = load8(x, o + P.step * (int64_t)A.c, C);
-            if (f) fn = load8(f, o + P.step * (int64_t)A.c, C);
+            xn = load8(x, (i + P.step) * A.c, C);
+            if (f) fn = load8(f, (i + P.step) * A.c, C);
         }
-        const float2 sf = f ? stats8<WIDE>(A, A.post, C, sum, w) : make_float2(0.f, 1.f);
-        if (f) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = C.has(e) ? v[e] + fmaf(a[e], (w[e] - sf.x) * sf.y, b[e]) : 0.f;
-        }
-        if (r && mine) store8(r, o, C, v);
-        const float2 sr = stats8<WIDE>(A, A.pre, C, sum, v);
-        if (h && mine) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - sr.x) * sr.y, g[e], beta[e]);
-            store8(h, o, C, v);
-        }
-        if (stats && mine && C.t == 0) stats[i] = make_float4(sf.x, sf.y, sr.x, sr.y);
+        const bool mine[1] = {i < P.to};
+        fwd_rows(A, C, sum, V, f != nullptr, i, 0, mine, v, w, r, h, stats);
     }
 }
 
-template <typename S, typename F, bool WIDE, bool VEC>
-__global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2) rn_bwd_kernel(const RnArgs A, int T, const F* f, const S* r, const float4* stats,
-                                                                                     const F* dh, const S* dr, S* dx, F* df, float* part) {
-    __shared__ float2 red[2][32];
-    Cols<VEC> C;
-    const Place P = place_of<WIDE>(A, T, C);
-    RowSum<WIDE> sum{red, 0, T};
-    float a[8], g[8];
-    {
+// Backward: du = a dx, u = g dh, and the sums over the thread's rows.
+struct BwdVectors {
+    float a[8], g[8], sa[8] = {}, sb[8] = {}, sc[8] = {}, sd[8] = {};
+    template <typename C_>
+    __device__ __forceinline__ BwdVectors(const RnArgs& A, const C_& C, int64_t sample) {
         float gate[8];
-        vector8(A.gate, A.gate_each ? P.sample * A.c : 0, C, 1.f, gate);
+        vector8(A.gate, A.gate_each ? sample * A.c : 0, C, 1.f, gate);
         vector8(A.post_gamma, 0, C, 1.f, a);
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] *= A.scale * gate[e];
-        vector8(A.pre_gamma, A.pre_each ? P.sample * A.c : 0, C, 1.f, g);
+        vector8(A.pre_gamma, A.pre_each ? sample * A.c : 0, C, 1.f, g);
     }
-    float sa[8] = {}, sb[8] = {}, sc[8] = {}, sd[8] = {};
-    const int64_t rounds = (P.to - (P.from - (WIDE ? 0 : (int)threadIdx.x / T)) + P.step - 1) / P.step;
-    Raw<F> fn{}, dhn{};
-    Raw<S> rn{}, drn{};
-    float4 stn = make_float4(0.f, 1.f, 0.f, 1.f);
-    auto fetch = [&](int64_t i) {
-        const int64_t o = i * A.c;
-        stn = __ldcg(stats + i);
-        if (dh) rn = load8(r, o, C), dhn = load8(dh, o, C);
-        if (dr) drn = load8(dr, o, C);
-        if (f) fn = load8(f, o, C);
-    };
-    if (P.from < P.to) fetch(P.from);
-    for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t i = P.from + k * P.step, o = i * A.c;
-        const bool mine = i < P.to;
-        float d[8], w[8];
-        float4 st = stn;
-        unpack(drn, d);
-        unpack(fn, w);
-        if (A.pre != CF_NORM_NONE) {
-            float rh[8], u[8];
-            unpack(rn, rh);
-            unpack(dhn, u);
-            if (i + P.step < P.to) fetch(i + P.step);
-            float m0 = 0.f, m1 = 0.f;
+};
+// dx of B rows from the values d of dr, rh of r and u of dh; rows that are not there are zeros.
+template <bool WIDE, int B, typename C_>
+__device__ __forceinline__ void bwd_stream(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, BwdVectors& V, const float4 (&st)[B], float (&d)[B][8],
+                                           float (&rh)[B][8], float (&u)[B][8]) {
+    float m[2 * B];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                rh[e] = C.has(e) ? (rh[e] - st.z) * st.w : 0.f;
-                if (mine) sc[e] = fmaf(u[e], rh[e], sc[e]), sd[e] += u[e];
-                u[e] *= g[e];
-                m0 += u[e];
-                m1 = fmaf(u[e], rh[e], m1);
-            }
-            float2 m = sum(m0, m1);
-            m.x = A.pre == CF_NORM_LAYER ? m.x * A.inv_c : 0.f;
-            m.y *= A.inv_c;
+    for (int k = 0; k < B; ++k) {
+        m[2 * k] = m[2 * k + 1] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = C.has(e) ? fmaf(st.w, u[e] - m.x - rh[e] * m.y, d[e]) : 0.f;
-        } else if (i + P.step < P.to) {
-            fetch(i + P.step);
-        }
-        if (dx && mine) store8(dx, o, C, d);
-        if (f) {
-            float n0 = 0.f, n1 = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                w[e] = C.has(e) ? (w[e] - st.x) * st.y : 0.f;
-                if (mine) sa[e] = fmaf(d[e], w[e], sa[e]), sb[e] += d[e];
-                d[e] *= a[e];
-                n0 += d[e];
-                n1 = fmaf(d[e], w[e], n1);
-            }
-            if (A.post != CF_NORM_NONE) {
-                float2 n = sum(n0, n1);
-                n.x = A.post == CF_NORM_LAYER ? n.x * A.inv_c : 0.f;
-                n.y *= A.inv_c;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = st.y * (d[e] - n.x - w[e] * n.y);
-            }
-            if (df && mine) store8(df, o, C, d);
-        } else if (mine) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sb[e] += d[e];
+        for (int e = 0; e < 8; ++e) {
+            rh[k][e] = C.has(e) ? (rh[k][e] - st[k].z) * st[k].w : 0.f;
+            V.sc[e] = fmaf(u[k][e], rh[k][e], V.sc[e]), V.sd[e] += u[k][e];
+            u[k][e] *= V.g[e];
+            m[2 * k] += u[k][e];
+            m[2 * k + 1] = fmaf(u[k][e], rh[k][e], m[2 * k + 1]);
         }
     }
-    if (part == nullptr) return;
+    sum(m);
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+        const float m0 = A.pre == CF_NORM_LAYER ? m[2 * k] * A.inv_c : 0.f, m1 = m[2 * k + 1] * A.inv_c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[k][e] = C.has(e) ? fmaf(st[k].w, u[k][e] - m0 - rh[k][e] * m1, d[k][e]) : 0.f;
+    }
+}
+// df (in d) from dx (in d) and the values w of f.
+template <bool WIDE, int B, typename C_>
+__device__ __forceinline__ void bwd_block(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, BwdVectors& V, const float4 (&st)[B], float (&d)[B][8],
+                                          float (&w)[B][8]) {
+    float n[2 * B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+        n[2 * k] = n[2 * k + 1] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[k][e] = C.has(e) ? (w[k][e] - st[k].x) * st[k].y : 0.f;
+            V.sa[e] = fmaf(d[k][e], w[k][e], V.sa[e]), V.sb[e] += d[k][e];
+            d[k][e] *= V.a[e];
+            n[2 * k] += d[k][e];
+            n[2 * k + 1] = fmaf(d[k][e], w[k][e], n[2 * k + 1]);
+        }
+    }
+    if (A.post == CF_NORM_NONE) return;
+    sum(n);
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+        const float n0 = A.post == CF_NORM_LAYER ? n[2 * k] * A.inv_c : 0.f, n1 = n[2 * k + 1] * A.inv_c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[k][e] = st[k].y * (d[k][e] - n0 - w[k][e] * n1);
+    }
+}
+
+// The block's sums to its part, in the order of its warps; `all` has room for 256 floats of each of `warps` warps.
+template <bool WIDE, typename C_>
+__device__ __forceinline__ void put_sums(const RnArgs& A, const C_& C, int T, BwdVectors& V, float* part, float* all, int warps) {
     float* to = part + (int64_t)blockIdx.x * 4 * A.c;
     auto put = [&](float (&v)[8], int which) {
         float* p = to + (int64_t)which * A.c;
@@ -500,27 +535,278 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2)
                 for (int e = 0; e < 8; ++e)
                     if (C.has(e)) p[C.at(e)] = v[e];
             }
-        } else {
-            // the rows of a warp, then its warps in order
-            __shared__ float all[kThreads / 32][256];
-            for (int o = T; o < 32; o <<= 1)
+            return;
+        }
+        const int warp = threadIdx.x >> 5;
+        for (int o = T; o < 32; o <<= 1)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(~0u, v[e], o);
-            __syncthreads();
-            if ((int)(threadIdx.x & 31) < T)
+            for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(~0u, v[e], o);
+        __syncthreads();
+        if (warp < warps && (int)(threadIdx.x & 31) < T)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (C.has(e)) all[threadIdx.x >> 5][C.at(e)] = v[e];
-            __syncthreads();
-            if ((int)threadIdx.x < A.c) {
-                float s = 0.f;
-#pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) s += all[w][threadIdx.x];
-                p[threadIdx.x] = s;
-            }
+            for (int e = 0; e < 8; ++e)
+                if (C.has(e)) all[warp * 256 + C.at(e)] = v[e];
+        __syncthreads();
+        if ((int)threadIdx.x < A.c) {
+            float s = 0.f;
+            for (int w = 0; w < warps; ++w) s += all[w * 256 + threadIdx.x];
+            p[threadIdx.x] = s;
         }
     };
-    put(sa, 0), put(sb, 1), put(sc, 2), put(sd, 3);
+    put(V.sa, 0), put(V.sb, 1), put(V.sc, 2), put(V.sd, 3);
+}
+
+template <typename S, typename F, bool WIDE, bool VEC>
+__global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2) rn_bwd_kernel(const RnArgs A, int T, const F* f, const S* r,
+                                                                                              const float4* stats, const F* dh, const S* dr, S* dx,
+                                                                                              F* df, float* part) {
+    __shared__ float red[2][16][2 * kMostRows];
+    __shared__ float all[WIDE ? 1 : kThreads / 32 * 256];
+    Cols<VEC> C;
+    const Place P = place_of<WIDE>(A, T, C);
+    RowSum<WIDE> sum{red, 0, T};
+    BwdVectors V(A, C, P.sample);
+    const int64_t rounds = (P.to - (P.from - (WIDE ? 0 : (int)threadIdx.x / T)) + P.step - 1) / P.step;
+    Raw<F> fn{}, dhn{};
+    Raw<S> rn{}, drn{};
+    float4 stn = make_float4(0.f, 1.f, 0.f, 1.f);
+    auto fetch = [&](int64_t i) {
+        const int64_t o = i * A.c;
+        stn = make_float4(0.f, 1.f, 0.f, 1.f);
+        fn = dhn = Raw<F>{}, rn = drn = Raw<S>{};  // zeros for what is not there
+        if (i >= P.to) return;
+        stn = __ldcg(stats + i);
+        if (dh) rn = load8(r, o, C), dhn = load8(dh, o, C);
+        if (dr) drn = load8(dr, o, C);
+        if (f) fn = load8(f, o, C);
+    };
+    fetch(P.from);
+    for (int64_t k = 0; k < rounds; ++k) {
+        const int64_t i = P.from + k * P.step, o = i * A.c;
+        const bool mine = i < P.to;
+        float d[1][8], w[1][8];
+        const float4 st[1] = {stn};
+        unpack(drn, d[0]);
+        unpack(fn, w[0]);
+        if (A.pre != CF_NORM_NONE) {
+            float rh[1][8], u[1][8];
+            unpack(rn, rh[0]);
+            unpack(dhn, u[0]);
+            fetch(i + P.step);
+            bwd_stream(A, C, sum, V, st, d, rh, u);
+        } else {
+            fetch(i + P.step);
+        }
+        if (dx && mine) store8(dx, o, C, d[0]);
+        if (f) {
+            bwd_block(A, C, sum, V, st, d, w);
+            if (df && mine) store8(df, o, C, d[0]);
+        }
+    }
+    if (part) put_sums<WIDE>(A, C, T, V, part, all, kThreads / 32);
+}
+
+// ------------------------------------------------------------------------------------------------ the same, fed by bulk copies
+// A block's rows are one stretch of memory of each tensor, copied into stages of `high` rows: what is on its way does not depend on what
+// registers hold.  Threads work on two rows at a time, whose sums go together: a row's time is mostly the latency of those.  Rows of
+// warps have a warp that copies; where all threads have a row, the first of them does, for the stage before, once all are through with it.
+// Rows of a multiple of eight values.
+constexpr int kRingWarps = 15;
+constexpr int kMostRing = 8;
+
+struct RnRing {
+    int high, stages;  // rows of a stage
+    uint32_t stage_bytes;
+    int* status;
+    uint64_t wait_ns;
+};
+struct RnShared {
+    uint64_t full[kMostRing], empty[kMostRing];
+    int abort;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// What a stage holds, one after another: a row's bytes of each (0: not there).
+struct RnTensors {
+    const char* at[5];
+    int bytes[5];
+};
+// The copies of one stage after another, by one thread.
+struct RingFill {
+    int64_t i;
+    int stage = 0;
+    uint32_t parity = 1, issued = 0;
+    __device__ __forceinline__ bool next(const RnRing& R, const RnTensors& X, RnShared& sh, uint8_t* ring, int64_t to) {
+        if (!mbar_wait(&sh.empty[stage], parity, &sh.abort, R.wait_ns, R.status, WAIT_PRODUCER_EMPTY)) return false;
+        const int rows = (int)min((int64_t)R.high, to - i);
+        mbar_arrive_expect_tx(&sh.full[stage], rows * (X.bytes[0] + X.bytes[1] + X.bytes[2] + X.bytes[3] + X.bytes[4]));
+        uint8_t* dst = ring + stage * R.stage_bytes;
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            if (X.bytes[k]) bulk_load(dst, X.at[k] + i * X.bytes[k], rows * X.bytes[k], &sh.full[stage]);
+            dst += R.high * X.bytes[k];
+        }
+        ++issued;
+        i += R.high;
+        if (++stage == R.stages) stage = 0, parity ^= 1;
+        return true;
+    }
+    // after a wait that gave up: copies in flight end before the block leaves
+    __device__ __forceinline__ void drain(const RnRing& R, RnShared& sh) const {
+        if (*(volatile int*)&sh.abort)
+            for (uint32_t k = issued > (uint32_t)R.stages ? issued - R.stages : 0; k < issued; ++k)
+                mbar_wait_timed(&sh.full[k % R.stages], (k / R.stages) & 1, R.wait_ns);
+    }
+};
+
+// Sets the block up; the rows of its chunk.
+template <bool WIDE, typename C_>
+__device__ __forceinline__ Place ring_begin(const RnArgs& A, int T, C_& C, const RnRing& R, RnShared& sh) {
+    const int compute = WIDE ? T : 32 * kRingWarps;
+    C.c = A.c, C.T = T, C.t = WIDE ? threadIdx.x : threadIdx.x & (T - 1);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < R.stages; ++k) mbar_init(&sh.full[k], 1), mbar_init(&sh.empty[k], compute / 32);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    Place P;
+    P.sample = blockIdx.x / A.chunks;
+    P.from = P.sample * A.per + (blockIdx.x - P.sample * A.chunks) * A.chunk;
+    P.to = min(min(P.from + A.chunk, (P.sample + 1) * A.per), A.rows);
+    P.step = WIDE ? 1 : kRingWarps * 32 / T;
+    return P;
+}
+template <typename T_>
+__device__ __forceinline__ void from_stage(const uint8_t* p, bool there, int c, int row, int t, float (&v)[8]) {
+    Raw<T_> raw{};
+    if (there) {
+        const uint4* q = reinterpret_cast<const uint4*>(p + ((int64_t)row * c + 8 * t) * sizeof(T_));
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(T_) / 2; ++e) {
+            const uint4 x = q[e];
+            raw.u[4 * e] = x.x, raw.u[4 * e + 1] = x.y, raw.u[4 * e + 2] = x.z, raw.u[4 * e + 3] = x.w;
+        }
+    }
+    unpack(raw, v);
+}
+
+// All threads' way through the stages: body(stage's bytes, first row of the stage that is the thread's, how many the stage has, the
+// block's row that the stage begins with).  WIDE, where all threads meet in a row's sums, they leave together when one has given a
+// wait up.
+template <bool WIDE, typename B>
+__device__ __forceinline__ void ring_run(const RnRing& R, const RnTensors& X, const Place& P, int T, RowSum<WIDE>& sum, RnShared& sh, uint8_t* ring,
+                                         B body) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = WIDE ? 0 : warp * (32 / T), in = WIDE ? 0 : lane / T;
+    RingFill fill{P.from};
+    if (!WIDE && warp == kRingWarps) {
+        if (lane == 0) {
+            while (fill.i < P.to && fill.next(R, X, sh, ring, P.to)) {}
+            fill.drain(R, sh);
+        }
+        return;
+    }
+    if (WIDE && threadIdx.x == 0)
+        for (int k = 0; k + 1 < R.stages && fill.i < P.to; ++k)
+            if (!fill.next(R, X, sh, ring, P.to)) sum.failed = 1;
+    int stage = 0;
+    uint32_t parity = 0;
+    for (int64_t i = P.from; i < P.to; i += R.high) {
+        if (WIDE && threadIdx.x == 0 && fill.i < P.to && !fill.next(R, X, sh, ring, P.to)) sum.failed = 1;
+        const int rows = (int)min((int64_t)R.high, P.to - i);
+        const bool ok = mbar_wait(&sh.full[stage], parity, &sh.abort, R.wait_ns, R.status, WAIT_MMA_FULL);
+        if (!WIDE && !__all_sync(~0u, ok)) break;
+        if (!ok) sum.failed = 1;
+        for (int k = at; k < rows; k += kMostRows * P.step) {
+            body(ring + stage * R.stage_bytes, k + in, rows, i);
+            if (WIDE && sum.failed) break;
+        }
+        if (WIDE && sum.failed) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        if (++stage == R.stages) stage = 0, parity ^= 1;
+    }
+    if (WIDE && threadIdx.x == 0) fill.drain(R, sh);
+}
+
+template <typename S, typename F, bool WIDE>
+__global__ void __launch_bounds__(512, 1) rn_fwd_ring_kernel(const RnArgs A, int T, const RnRing R, const S* x, const F* f, S* r, F* h, float4* stats) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RnShared sh;
+    __shared__ float red[2][16][2 * kMostRows];
+    Cols<true> C;
+    const Place P = ring_begin<WIDE>(A, T, C, R, sh);
+    const int row = A.c * (int)sizeof(S);
+    const RnTensors X{{reinterpret_cast<const char*>(x), reinterpret_cast<const char*>(f)}, {row, f ? A.c * (int)sizeof(F) : 0}};
+    RowSum<WIDE> sum{red, 0, T};
+    const FwdVectors V(A, C, P.sample);
+    ring_run<WIDE>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
+        float v[kMostRows][8], w[kMostRows][8];
+        bool mine[kMostRows];
+#pragma unroll
+        for (int b = 0; b < kMostRows; ++b) {
+            mine[b] = k + b * P.step < rows;
+            from_stage<S>(stage, mine[b] && C.has(0), A.c, k + b * P.step, C.t, v[b]);
+            from_stage<F>(stage + R.high * row, f && mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
+        }
+        fwd_rows(A, C, sum, V, f != nullptr, i + k, P.step, mine, v, w, r, h, stats);
+    });
+}
+
+template <typename S, typename F, bool WIDE>
+__global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int T, const RnRing R, const F* f, const S* r, const float4* stats,
+                                                           const F* dh, const S* dr, S* dx, F* df, float* part) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RnShared sh;
+    __shared__ float red[2][16][2 * kMostRows];
+    Cols<true> C;
+    const Place P = ring_begin<WIDE>(A, T, C, R, sh);
+    const int rs = A.c * (int)sizeof(S), rf = A.c * (int)sizeof(F);
+    const RnTensors X{{reinterpret_cast<const char*>(r), reinterpret_cast<const char*>(dr), reinterpret_cast<const char*>(dh),
+                       reinterpret_cast<const char*>(f), reinterpret_cast<const char*>(stats)},
+                      {dh ? rs : 0, dr ? rs : 0, dh ? rf : 0, f ? rf : 0, 16}};
+    const int o1 = R.high * X.bytes[0], o2 = o1 + R.high * X.bytes[1], o3 = o2 + R.high * X.bytes[2], o4 = o3 + R.high * X.bytes[3];
+    BwdVectors V(A, C, P.sample);
+    RowSum<WIDE> sum{red, 0, T};
+    ring_run<WIDE>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
+        float d[kMostRows][8];
+        float4 st[kMostRows];
+        bool mine[kMostRows];
+#pragma unroll
+        for (int b = 0; b < kMostRows; ++b) {
+            mine[b] = k + b * P.step < rows;
+            st[b] = mine[b] ? *reinterpret_cast<const float4*>(stage + o4 + 16 * (k + b * P.step)) : make_float4(0.f, 1.f, 0.f, 1.f);
+            from_stage<S>(stage + o1, dr && mine[b] && C.has(0), A.c, k + b * P.step, C.t, d[b]);
+        }
+        if (A.pre != CF_NORM_NONE) {
+            float rh[kMostRows][8], u[kMostRows][8];
+#pragma unroll
+            for (int b = 0; b < kMostRows; ++b) {
+                from_stage<S>(stage, mine[b] && C.has(0), A.c, k + b * P.step, C.t, rh[b]);
+                from_stage<F>(stage + o2, mine[b] && C.has(0), A.c, k + b * P.step, C.t, u[b]);
+            }
+            bwd_stream(A, C, sum, V, st, d, rh, u);
+        }
+#pragma unroll
+        for (int b = 0; b < kMostRows; ++b)
+            if (dx && mine[b]) store8(dx, (i + k + b * P.step) * A.c, C, d[b]);
+        if (f) {
+            float w[kMostRows][8];
+#pragma unroll
+            for (int b = 0; b < kMostRows; ++b) from_stage<F>(stage + o3, mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
+            bwd_block(A, C, sum, V, st, d, w);
+#pragma unroll
+            for (int b = 0; b < kMostRows; ++b)
+                if (df && mine[b]) store8(df, (i + k + b * P.step) * A.c, C, d[b]);
+        }
+    });
+    if (part == nullptr) return;
+    __syncthreads();  // the stages are read, and hold the sums now
+    put_sums<WIDE>(A, C, T, V, part, reinterpret_cast<float*>(ring), kRingWarps);
 }
 
 struct RnGrads {
@@ -624,7 +910,7 @@ void cut(RnArgs& A, int64_t blocks, int64_t least) {
     A.chunks = (int)((per + A.chunk - 1) / A.chunk);
 }
 
-// Threads of a row: up to 256 values a part of a warp, up to kMostWide a block, beyond 0.
+// Threads of a row: up to 256 values a part of a warp, up to kMostWide a block, beyond that 0.
 int threads_of(int c) {
     if (c > kMostWide) return 0;
     if (c > 256) return (c + 255) / 256 * 32;
@@ -632,8 +918,36 @@ int threads_of(int c) {
     while (8 * T < c) T *= 2;
     return T;
 }
-// Blocks that the device holds, as many as the kernels' registers let it: of rows in warps `narrow` an SM, else 512 threads.
-int64_t resident(int T, int narrow) { return (int64_t)kPlanSms * (T <= 32 ? narrow : 512 / T); }
+// Blocks of the kernels without a ring that an SM holds, as many as their registers let it.
+int per_sm(int T, int narrow) { return T <= 32 ? narrow : std::max(1, 512 / T); }
+// And of those with one: a block of 15 warps and one that copies, or of T threads.
+int ring_per_sm(int T) { return T <= 32 ? 1 : 512 / T; }
+
+// Whether rows go through the ring: whole vectors, and at least two rounds of rows to a block.  Fewer are quicker without (64 x 256
+// forward 2.2 us without, 3.4 with it), more with it (8 x 32^3 x 128 forward 74 without, 55 with it).
+bool ringed(const RnArgs& A, int T) {
+    const int64_t step = kMostRows * (T <= 32 ? kRingWarps * 32 / T : 1);
+    return T && A.c % 8 == 0 && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms;
+}
+// A's rows cut for the kernel that takes them.
+void cut_rows(RnArgs& A, int T, int narrow) {
+    if (ringed(A, T))
+        cut(A, (int64_t)kPlanSms * ring_per_sm(T), T <= 32 ? kRingWarps * 32 / T : 1);
+    else
+        cut(A, (int64_t)kPlanSms * per_sm(T, narrow), T <= 32 ? kThreads / T : 1);
+}
+RnRing ring_of(const LaunchCtx& ctx, const RnArgs& A, int T, int per_row, int& shared) {
+    RnRing R{};
+    const int n = ring_per_sm(T), step = kMostRows * (T <= 32 ? kRingWarps * 32 / T : 1);
+    const int room = 228 * 1024 / n - 1024 - 1024;  // what the system keeps of a block's, and the barriers
+    R.high = std::max(1, room / 4 / (per_row * step)) * step;  // four stages, or as many as fit of one round of rows
+    R.high = (int)std::min<int64_t>(R.high, (A.chunk + step - 1) / step * step);
+    R.stage_bytes = (uint32_t)((R.high * per_row + 127) / 128 * 128);
+    R.stages = std::min(kMostRing, room / (int)R.stage_bytes);
+    R.status = ctx.status, R.wait_ns = ctx.wait_ns;
+    shared = std::max<int>(R.stages * R.stage_bytes, kRingWarps * 256 * 4);
+    return R;
+}
 
 struct Layout {
     float4* means;
@@ -659,7 +973,7 @@ RnArgs plan_bwd(const cf_residual_norm_desc* d) {
     if (A.rows == 0) return A;
     const int T = threads_of(A.c);
     if (T)
-        cut(A, resident(T, 2), T <= 32 ? kThreads / T : 1);
+        cut_rows(A, T, 2);
     else
         cut(A, std::max(1, kPlanSms * 8 * 32 / A.c), 8);
     return A;
@@ -722,12 +1036,23 @@ cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x,
     return with_types(desc, [&](auto s, auto t) {
         using S = decltype(s);
         using F = decltype(t);
+        const S* xs = static_cast<const S*>(x);
+        const F* fs = static_cast<const F*>(f);
+        float4* st4 = reinterpret_cast<float4*>(stats);
         if (const int T = threads_of(A.c); T) {
-            cut(A, resident(T, 3), T <= 32 ? kThreads / T : 1);
+            cut_rows(A, T, 3);
+            const unsigned blocks = (unsigned)(A.samples * A.chunks);
+            if (ringed(A, T)) {
+                int shared;
+                const RnRing R = ring_of(ctx, A, T, A.c * (int)(sizeof(S) + (f ? sizeof(F) : 0)), shared);
+                auto kernel = T <= 32 ? rn_fwd_ring_kernel<S, F, false> : rn_fwd_ring_kernel<S, F, true>;
+                if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
+                kernel<<<blocks, T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(A, T, R, xs, fs, static_cast<S*>(r), static_cast<F*>(h), st4);
+                return status_of();
+            }
             auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_fwd_kernel<S, F, false, true> : rn_fwd_kernel<S, F, true, true>)
                                        : (T <= 32 ? rn_fwd_kernel<S, F, false, false> : rn_fwd_kernel<S, F, true, false>);
-            kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? kThreads : T, 0, ctx.stream>>>(
-                A, T, static_cast<const S*>(x), static_cast<const F*>(f), static_cast<S*>(r), static_cast<F*>(h), reinterpret_cast<float4*>(stats));
+            kernel<<<blocks, T <= 32 ? kThreads : T, 0, ctx.stream>>>(A, T, xs, fs, static_cast<S*>(r), static_cast<F*>(h), st4);
             return status_of();
         }
         rn_fwd_long_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(
@@ -774,7 +1099,15 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
         const F *fs = static_cast<const F*>(f), *dhs = static_cast<const F*>(dh);
         const float4* st4 = reinterpret_cast<const float4*>(stats);
         const unsigned tiles = (A.c + 31) / 32;
-        if (const int T = threads_of(A.c); T) {
+        if (const int T = threads_of(A.c); T && ringed(A, T)) {
+            int shared;
+            const int per_row = A.c * (int)((dh ? sizeof(S) + sizeof(F) : 0) + (dr ? sizeof(S) : 0) + (f ? sizeof(F) : 0)) + 16;
+            const RnRing R = ring_of(ctx, A, T, per_row, shared);
+            auto kernel = T <= 32 ? rn_bwd_ring_kernel<S, F, false> : rn_bwd_ring_kernel<S, F, true>;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
+            kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(
+                A, T, R, fs, rs, st4, dhs, drs, static_cast<S*>(dx), static_cast<F*>(df), sums ? L.part : nullptr);
+        } else if (T) {
             auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_bwd_kernel<S, F, false, true> : rn_bwd_kernel<S, F, true, true>)
                                        : (T <= 32 ? rn_bwd_kernel<S, F, false, false> : rn_bwd_kernel<S, F, true, false>);
             kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? kThreads : T, 0, ctx.stream>>>(A, T, fs, rs, st4, dhs, drs, static_cast<S*>(dx),

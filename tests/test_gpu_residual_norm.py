@@ -209,6 +209,36 @@ def test_many_rows(cf, rows, c):
     case.check_backward()
 
 
+# enough rows for the kernels that copies feed: ends inside a stage, in a round of rows, samples that end inside a block's
+@pytest.mark.parametrize("post,pre", [("layer", "layer"), ("rms", "none"), ("none", "rms")])
+@pytest.mark.parametrize("dtype,f_dtype", TYPES)
+@pytest.mark.parametrize("rows,c,each,per", [(19001, 128, 0, 0), (10007, 256, 3, 1000), (2003, 1000, 2, 333), (1300, 2048, 0, 0), (701, 4096, 1, 100)])
+def test_rows_in_stages(cf, rows, c, each, per, post, pre, dtype, f_dtype):
+    case = Case(cf, rows, rows, c, post, pre, dtype, f_dtype, each=each, per=per)
+    case.check_forward()
+    case.check_backward()
+
+
+@pytest.mark.parametrize("rows,c", [(300001, 8), (80003, 32), (38000, 56)])
+def test_narrow_rows_in_stages(cf, rows, c):
+    case = Case(cf, rows, rows, c, "layer", "rms", BF, BF, each=1, per=rows // 3)
+    case.check_forward()
+    case.check_backward()
+
+
+@pytest.mark.parametrize("rows,c", [(20000, 128), (1300, 2048)])
+def test_stages_without_some_tensors(cf, rows, c):
+    case = Case(cf, c, rows, c, "none", "layer", gate=False, with_f=False, with_dr=False)
+    case.check_forward()
+    case.check_backward()
+    case = Case(cf, c, rows, c, "rms", "rms", F32, BF)
+    dx, df, g = case.backward()
+    dr, dh = case.dr, case.dh
+    case.dr = dr.clone()
+    dx2, df2, g2 = case.backward(dx=case.dr)
+    assert torch.equal(dx, dx2) and torch.equal(df, df2) and all(torch.equal(g[k], g2[k]) for k in g)
+
+
 @pytest.mark.parametrize("c", [48, 300, 9000])
 def test_first_norm_and_parts_left_out(cf, c):
     case = Case(cf, c, 33, c, "none", "layer", gate=False, with_f=False, with_dr=False)
