@@ -12,6 +12,7 @@
 
 #include "cf_internal.h"
 #include "cf_ptx.cuh"
+#include "cf_two.cuh"
 
 namespace cf {
 namespace {
@@ -240,16 +241,23 @@ __device__ __forceinline__ Raw<float> load8(const float* p, int64_t o, const C_&
     }
     return r;
 }
-__device__ __forceinline__ void unpack(const Raw<uint16_t>& r, float (&v)[8]) {
+// As four pairs, with which all arithmetic is done.
+__device__ __forceinline__ void unpack(const Raw<uint16_t>& r, uint64_t (&v)[4]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[2 * e] = __uint_as_float(r.u[e] << 16), v[2 * e + 1] = __uint_as_float(r.u[e] & 0xFFFF0000u);
+    for (int e = 0; e < 4; ++e) v[e] = two(__uint_as_float(r.u[e] << 16), __uint_as_float(r.u[e] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack(const Raw<float>& r, float (&v)[8]) {
+__device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&v)[4]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.u[e]);
+    for (int e = 0; e < 4; ++e) v[e] = two(__uint_as_float(r.u[2 * e]), __uint_as_float(r.u[2 * e + 1]));
+}
+__device__ __forceinline__ void spread(const uint64_t (&p)[4], float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) apart(p[e], v[2 * e], v[2 * e + 1]);
 }
 template <typename C_>
-__device__ __forceinline__ void store8(uint16_t* p, int64_t o, const C_& C, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, int64_t o, const C_& C, const uint64_t (&q)[4]) {
+    float v[8];
+    spread(q, v);
     if (C.vec) {
         if (C.has(0))
             *reinterpret_cast<uint4*>(p + o + 8 * C.t) =
@@ -261,11 +269,13 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t o, const C_& C, cons
     }
 }
 template <typename C_>
-__device__ __forceinline__ void store8(float* p, int64_t o, const C_& C, const float (&v)[8]) {
+__device__ __forceinline__ void store8(float* p, int64_t o, const C_& C, const uint64_t (&q)[4]) {
+    float v[8];
+    spread(q, v);
     if (C.vec) {
         if (C.has(0)) {
-            float4* q = reinterpret_cast<float4*>(p + o + 8 * C.t);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]), q[1] = make_float4(v[4], v[5], v[6], v[7]);
+            float4* to = reinterpret_cast<float4*>(p + o + 8 * C.t);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]), to[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     } else {
 #pragma unroll
@@ -273,23 +283,28 @@ __device__ __forceinline__ void store8(float* p, int64_t o, const C_& C, const f
             if (C.has(e)) p[o + C.at(e)] = v[e];
     }
 }
-// A vector's eight values, `other` where there is none.
+// A vector's eight values, `other` where there is no vector, and 0 in columns that the thread does not have: what it makes of those
+// adds nothing to a row's sums.
 template <typename C_>
-__device__ __forceinline__ void vector8(const float* p, int64_t o, const C_& C, float other, float (&v)[8]) {
+__device__ __forceinline__ void vector8(const float* p, int64_t o, const C_& C, float other, uint64_t (&q)[4]) {
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = other;
-    if (p == nullptr) return;
-    if (C.vec) {
-        if (C.has(0)) {
-            const float4* q = reinterpret_cast<const float4*>(p + o + 8 * C.t);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    for (int e = 0; e < 8; ++e) v[e] = C.has(e) ? other : 0.f;
+    if (p != nullptr) {
+        if (C.vec) {
+            if (C.has(0)) {
+                const float4* from = reinterpret_cast<const float4*>(p + o + 8 * C.t);
+                const float4 a = from[0], b = from[1];
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (C.has(e)) v[e] = p[o + C.at(e)];
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (C.has(e)) v[e] = p[o + C.at(e)];
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = two(v[2 * e], v[2 * e + 1]);
 }
 
 // Sums over the threads of B rows, the same in each of them.  WIDE: one barrier of the rows' T threads, the buffers in turn; it also
@@ -329,32 +344,35 @@ struct RowSum {
     }
 };
 
-// (mean, 1 / width) of B rows that their threads hold eight values of each.
+// (mean, 1 / width) of B rows that their threads hold eight values of each (0 in columns that they do not have).
 template <bool WIDE, int B, typename C_>
-__device__ __forceinline__ void stats8(const RnArgs& A, int kind, const C_& C, RowSum<WIDE>& sum, const float (&v)[B][8], float2 (&st)[B]) {
+__device__ __forceinline__ void stats8(const RnArgs& A, int kind, const C_& C, RowSum<WIDE>& sum, const uint64_t (&v)[B][4], float2 (&st)[B]) {
 #pragma unroll
     for (int k = 0; k < B; ++k) st[k] = make_float2(0.f, 1.f);
     if (kind == CF_NORM_NONE) return;
     float s[B];
     if (kind == CF_NORM_LAYER) {
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-            s[k] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[k] += v[k][e];  // values that a thread does not have are 0
-        }
+        for (int k = 0; k < B; ++k) s[k] = total(add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
         sum(s);
 #pragma unroll
         for (int k = 0; k < B; ++k) st[k].x = s[k] * A.inv_c;
     }
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-        s[k] = 0.f;
+        uint64_t q = 0;
+        const uint64_t less = both(-st[k].x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = C.has(e) ? v[k][e] - st[k].x : 0.f;
-            s[k] = fmaf(t, t, s[k]);
+        for (int e = 0; e < 4; ++e) {
+            uint64_t t = add2(v[k][e], less);
+            if (!C.vec) {
+                float a, b;
+                apart(t, a, b);
+                t = two(C.has(2 * e) ? a : 0.f, C.has(2 * e + 1) ? b : 0.f);
+            }
+            q = fma2(t, t, q);
         }
+        s[k] = C.vec && !C.has(0) ? 0.f : total(q);
     }
     sum(s);
 #pragma unroll
@@ -381,23 +399,26 @@ __device__ __forceinline__ Place place_of(const RnArgs& A, int T, C_& C) {
 
 // The vectors of a thread's columns: p = a fh + b, h = g rh + beta.
 struct FwdVectors {
-    float a[8], b[8], g[8], beta[8];
+    uint64_t a[4], b[4], g[4], beta[4];
     template <typename C_>
     __device__ __forceinline__ FwdVectors(const RnArgs& A, const C_& C, int64_t sample) {
-        float gate[8];
+        uint64_t gate[4];
         vector8(A.gate, A.gate_each ? sample * A.c : 0, C, 1.f, gate);
         vector8(A.post_gamma, 0, C, 1.f, a);
         vector8(A.post_beta, 0, C, 0.f, b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= A.scale * gate[e], b[e] *= A.scale * gate[e];
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t s = mul2(both(A.scale), gate[e]);
+            a[e] = mul2(a[e], s), b[e] = mul2(b[e], s);
+        }
         vector8(A.pre_gamma, A.pre_each ? sample * A.c : 0, C, 1.f, g);
         vector8(A.pre_beta, A.pre_each ? sample * A.c : 0, C, 0.f, beta);
     }
 };
-// B rows, `step` apart from row i on, from their values v of x and w of f; rows that are not `mine` are zeros.
+// B rows, `step` apart from row i on, from their values v of x and w of f (0 where the thread has none).
 template <typename S, typename F, bool WIDE, int B, typename C_>
 __device__ __forceinline__ void fwd_rows(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, const FwdVectors& V, bool with_f, int64_t i, int step,
-                                         const bool (&mine)[B], float (&v)[B][8], float (&w)[B][8], S* r, F* h, float4* stats) {
+                                         const bool (&mine)[B], uint64_t (&v)[B][4], uint64_t (&w)[B][4], S* r, F* h, float4* stats) {
     float2 sf[B], sr[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) sf[k] = make_float2(0.f, 1.f);
@@ -406,7 +427,8 @@ __device__ __forceinline__ void fwd_rows(const RnArgs& A, const C_& C, RowSum<WI
 #pragma unroll
         for (int k = 0; k < B; ++k)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[k][e] = C.has(e) ? v[k][e] + fmaf(V.a[e], (w[k][e] - sf[k].x) * sf[k].y, V.b[e]) : 0.f;
+            for (int e = 0; e < 4; ++e)
+                v[k][e] = add2(v[k][e], fma2(V.a[e], mul2(add2(w[k][e], both(-sf[k].x)), both(sf[k].y)), V.b[e]));
     }
 #pragma unroll
     for (int k = 0; k < B; ++k)
@@ -416,7 +438,7 @@ __device__ __forceinline__ void fwd_rows(const RnArgs& A, const C_& C, RowSum<WI
     for (int k = 0; k < B; ++k) {
         if (h && mine[k]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[k][e] = fmaf((v[k][e] - sr[k].x) * sr[k].y, V.g[e], V.beta[e]);
+            for (int e = 0; e < 4; ++e) v[k][e] = fma2(mul2(add2(v[k][e], both(-sr[k].x)), both(sr[k].y)), V.g[e], V.beta[e]);
             store8(h, (i + k * step) * A.c, C, v[k]);
         }
         if (stats && mine[k] && C.t == 0) stats[i + k * step] = make_float4(sf[k].x, sf[k].y, sr[k].x, sr[k].y);
@@ -441,7 +463,7 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 3)
     }
     for (int64_t k = 0; k < rounds; ++k) {
         const int64_t i = P.from + k * P.step;
-        float v[1][8], w[1][8];
+        uint64_t v[1][4], w[1][4];
         unpack(xn, v[0]);
         unpack(fn, w[0]);
         if (i + P.step < P.to) {
@@ -453,68 +475,73 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 3)
     }
 }
 
-// Backward: du = a dx, u = g dh, and the sums over the thread's rows.
+// Backward: dv = a dx, u = g dh, and the sums over the thread's rows.  In columns that a thread does not have a and g are 0, so that
+// what it makes there of the means adds nothing to a row's sums (its own, of those columns, go nowhere).
 struct BwdVectors {
-    float a[8], g[8], sa[8] = {}, sb[8] = {}, sc[8] = {}, sd[8] = {};
+    uint64_t a[4], g[4], sa[4] = {}, sb[4] = {}, sc[4] = {}, sd[4] = {};
     template <typename C_>
     __device__ __forceinline__ BwdVectors(const RnArgs& A, const C_& C, int64_t sample) {
-        float gate[8];
+        uint64_t gate[4];
         vector8(A.gate, A.gate_each ? sample * A.c : 0, C, 1.f, gate);
         vector8(A.post_gamma, 0, C, 1.f, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= A.scale * gate[e];
+        for (int e = 0; e < 4; ++e) a[e] = mul2(a[e], mul2(both(A.scale), gate[e]));
         vector8(A.pre_gamma, A.pre_each ? sample * A.c : 0, C, 1.f, g);
     }
 };
 // dx of B rows from the values d of dr, rh of r and u of dh; rows that are not there are zeros.
 template <bool WIDE, int B, typename C_>
-__device__ __forceinline__ void bwd_stream(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, BwdVectors& V, const float4 (&st)[B], float (&d)[B][8],
-                                           float (&rh)[B][8], float (&u)[B][8]) {
+__device__ __forceinline__ void bwd_stream(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, BwdVectors& V, const float4 (&st)[B], uint64_t (&d)[B][4],
+                                           uint64_t (&rh)[B][4], uint64_t (&u)[B][4]) {
     float m[2 * B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-        m[2 * k] = m[2 * k + 1] = 0.f;
+        uint64_t m0 = 0, m1 = 0;
+        const uint64_t less = both(-st[k].z), wide = both(st[k].w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            rh[k][e] = C.has(e) ? (rh[k][e] - st[k].z) * st[k].w : 0.f;
-            V.sc[e] = fmaf(u[k][e], rh[k][e], V.sc[e]), V.sd[e] += u[k][e];
-            u[k][e] *= V.g[e];
-            m[2 * k] += u[k][e];
-            m[2 * k + 1] = fmaf(u[k][e], rh[k][e], m[2 * k + 1]);
+        for (int e = 0; e < 4; ++e) {
+            rh[k][e] = mul2(add2(rh[k][e], less), wide);
+            V.sc[e] = fma2(u[k][e], rh[k][e], V.sc[e]), V.sd[e] = add2(V.sd[e], u[k][e]);
+            u[k][e] = mul2(u[k][e], V.g[e]);
+            m0 = add2(m0, u[k][e]);
+            m1 = fma2(u[k][e], rh[k][e], m1);
         }
+        m[2 * k] = total(m0), m[2 * k + 1] = total(m1);
     }
     sum(m);
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-        const float m0 = A.pre == CF_NORM_LAYER ? m[2 * k] * A.inv_c : 0.f, m1 = m[2 * k + 1] * A.inv_c;
+        const uint64_t m0 = both(A.pre == CF_NORM_LAYER ? -m[2 * k] * A.inv_c : 0.f), m1 = both(-m[2 * k + 1] * A.inv_c), wide = both(st[k].w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[k][e] = C.has(e) ? fmaf(st[k].w, u[k][e] - m0 - rh[k][e] * m1, d[k][e]) : 0.f;
+        for (int e = 0; e < 4; ++e) d[k][e] = fma2(wide, fma2(rh[k][e], m1, add2(u[k][e], m0)), d[k][e]);
     }
 }
 // df (in d) from dx (in d) and the values w of f.
 template <bool WIDE, int B, typename C_>
-__device__ __forceinline__ void bwd_block(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, BwdVectors& V, const float4 (&st)[B], float (&d)[B][8],
-                                          float (&w)[B][8]) {
+__device__ __forceinline__ void bwd_block(const RnArgs& A, const C_& C, RowSum<WIDE>& sum, BwdVectors& V, const float4 (&st)[B], uint64_t (&d)[B][4],
+                                          uint64_t (&w)[B][4]) {
     float n[2 * B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-        n[2 * k] = n[2 * k + 1] = 0.f;
+        uint64_t n0 = 0, n1 = 0;
+        const uint64_t less = both(-st[k].x), wide = both(st[k].y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[k][e] = C.has(e) ? (w[k][e] - st[k].x) * st[k].y : 0.f;
-            V.sa[e] = fmaf(d[k][e], w[k][e], V.sa[e]), V.sb[e] += d[k][e];
-            d[k][e] *= V.a[e];
-            n[2 * k] += d[k][e];
-            n[2 * k + 1] = fmaf(d[k][e], w[k][e], n[2 * k + 1]);
+        for (int e = 0; e < 4; ++e) {
+            w[k][e] = mul2(add2(w[k][e], less), wide);
+            V.sa[e] = fma2(d[k][e], w[k][e], V.sa[e]), V.sb[e] = add2(V.sb[e], d[k][e]);
+            d[k][e] = mul2(d[k][e], V.a[e]);
+            n0 = add2(n0, d[k][e]);
+            n1 = fma2(d[k][e], w[k][e], n1);
         }
+        n[2 * k] = total(n0), n[2 * k + 1] = total(n1);
     }
     if (A.post == CF_NORM_NONE) return;
     sum(n);
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-        const float n0 = A.post == CF_NORM_LAYER ? n[2 * k] * A.inv_c : 0.f, n1 = n[2 * k + 1] * A.inv_c;
+        const uint64_t n0 = both(A.post == CF_NORM_LAYER ? -n[2 * k] * A.inv_c : 0.f), n1 = both(-n[2 * k + 1] * A.inv_c), wide = both(st[k].y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[k][e] = st[k].y * (d[k][e] - n0 - w[k][e] * n1);
+        for (int e = 0; e < 4; ++e) d[k][e] = mul2(wide, fma2(w[k][e], n1, add2(d[k][e], n0)));
     }
 }
 
@@ -522,13 +549,15 @@ __device__ __forceinline__ void bwd_block(const RnArgs& A, const C_& C, RowSum<W
 template <bool WIDE, typename C_>
 __device__ __forceinline__ void put_sums(const RnArgs& A, const C_& C, int T, BwdVectors& V, float* part, float* all, int warps) {
     float* to = part + (int64_t)blockIdx.x * 4 * A.c;
-    auto put = [&](float (&v)[8], int which) {
+    auto put = [&](uint64_t (&q)[4], int which) {
+        float v[8];
+        spread(q, v);
         float* p = to + (int64_t)which * A.c;
         if (WIDE) {
             if (C.vec) {
                 if (C.has(0)) {
-                    float4* q = reinterpret_cast<float4*>(p + 8 * C.t);
-                    q[0] = make_float4(v[0], v[1], v[2], v[3]), q[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    float4* at = reinterpret_cast<float4*>(p + 8 * C.t);
+                    at[0] = make_float4(v[0], v[1], v[2], v[3]), at[1] = make_float4(v[4], v[5], v[6], v[7]);
                 }
             } else {
 #pragma unroll
@@ -584,12 +613,12 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2)
     for (int64_t k = 0; k < rounds; ++k) {
         const int64_t i = P.from + k * P.step, o = i * A.c;
         const bool mine = i < P.to;
-        float d[1][8], w[1][8];
+        uint64_t d[1][4], w[1][4];
         const float4 st[1] = {stn};
         unpack(drn, d[0]);
         unpack(fn, w[0]);
         if (A.pre != CF_NORM_NONE) {
-            float rh[1][8], u[1][8];
+            uint64_t rh[1][4], u[1][4];
             unpack(rn, rh[0]);
             unpack(dhn, u[0]);
             fetch(i + P.step);
@@ -608,8 +637,9 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2)
 
 // ------------------------------------------------------------------------------------------------ the same, fed by bulk copies
 // A block's rows are one stretch of memory of each tensor, copied into stages of `high` rows: what is on its way does not depend on what
-// registers hold.  Threads work on two rows at a time, whose sums go together: a row's time is mostly the latency of those.  Rows of
-// warps have a warp that copies; where all threads have a row, the first of them does, for the stage before, once all are through with it.
+// registers hold.  Threads work on two rows at a time (ROWS), whose sums go together: a row's time is mostly the latency of those; but for the backward
+// of rows that all threads share, which has the registers for one.  Rows of warps have a warp that copies; where all threads have a row,
+// the first does, for the stage before, once all are through with it.
 // Rows of a multiple of eight values.
 constexpr int kRingWarps = 15;
 constexpr int kMostRing = 8;
@@ -635,21 +665,29 @@ struct RnTensors {
     const char* at[5];
     int bytes[5];
 };
-// The copies of one stage after another, by one thread.
+// The copies of one stage after another, by a warp: a lane to each tensor.
 struct RingFill {
     int64_t i;
+    const char* at = nullptr;
+    int mine = 0, per_row = 0, before = 0;
     int stage = 0;
     uint32_t parity = 1, issued = 0;
-    __device__ __forceinline__ bool next(const RnRing& R, const RnTensors& X, RnShared& sh, uint8_t* ring, int64_t to) {
-        if (!mbar_wait(&sh.empty[stage], parity, &sh.abort, R.wait_ns, R.status, WAIT_PRODUCER_EMPTY)) return false;
-        const int rows = (int)min((int64_t)R.high, to - i);
-        mbar_arrive_expect_tx(&sh.full[stage], rows * (X.bytes[0] + X.bytes[1] + X.bytes[2] + X.bytes[3] + X.bytes[4]));
-        uint8_t* dst = ring + stage * R.stage_bytes;
+    __device__ __forceinline__ RingFill(const RnTensors& X, int64_t from) : i(from) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
-            if (X.bytes[k]) bulk_load(dst, X.at[k] + i * X.bytes[k], rows * X.bytes[k], &sh.full[stage]);
-            dst += R.high * X.bytes[k];
+            if (k < lane) before += X.bytes[k];
+            if (k == lane) at = X.at[k], mine = X.bytes[k];
+            per_row += X.bytes[k];
         }
+    }
+    __device__ __forceinline__ bool next(const RnRing& R, RnShared& sh, uint8_t* ring, int64_t to) {
+        const bool ok = mbar_wait(&sh.empty[stage], parity, &sh.abort, R.wait_ns, R.status, WAIT_PRODUCER_EMPTY);
+        if (!__all_sync(~0u, ok)) return false;
+        const int rows = (int)min((int64_t)R.high, to - i);
+        if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&sh.full[stage], rows * per_row);
+        __syncwarp();
+        if (mine) bulk_load(ring + stage * R.stage_bytes + R.high * before, at + i * mine, rows * mine, &sh.full[stage]);
         ++issued;
         i += R.high;
         if (++stage == R.stages) stage = 0, parity ^= 1;
@@ -657,7 +695,7 @@ struct RingFill {
     }
     // after a wait that gave up: copies in flight end before the block leaves
     __device__ __forceinline__ void drain(const RnRing& R, RnShared& sh) const {
-        if (*(volatile int*)&sh.abort)
+        if (*(volatile int*)&sh.abort && (threadIdx.x & 31) == 0)
             for (uint32_t k = issued > (uint32_t)R.stages ? issued - R.stages : 0; k < issued; ++k)
                 mbar_wait_timed(&sh.full[k % R.stages], (k / R.stages) & 1, R.wait_ns);
     }
@@ -682,7 +720,7 @@ __device__ __forceinline__ Place ring_begin(const RnArgs& A, int T, C_& C, const
     return P;
 }
 template <typename T_>
-__device__ __forceinline__ void from_stage(const uint8_t* p, bool there, int c, int row, int t, float (&v)[8]) {
+__device__ __forceinline__ void from_stage(const uint8_t* p, bool there, int c, int row, int t, uint64_t (&v)[4]) {
     Raw<T_> raw{};
     if (there) {
         const uint4* q = reinterpret_cast<const uint4*>(p + ((int64_t)row * c + 8 * t) * sizeof(T_));
@@ -698,30 +736,28 @@ __device__ __forceinline__ void from_stage(const uint8_t* p, bool there, int c, 
 // All threads' way through the stages: body(stage's bytes, first row of the stage that is the thread's, how many the stage has, the
 // block's row that the stage begins with).  WIDE, where all threads meet in a row's sums, they leave together when one has given a
 // wait up.
-template <bool WIDE, typename B>
+template <bool WIDE, int ROWS, typename B>
 __device__ __forceinline__ void ring_run(const RnRing& R, const RnTensors& X, const Place& P, int T, RowSum<WIDE>& sum, RnShared& sh, uint8_t* ring,
                                          B body) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = WIDE ? 0 : warp * (32 / T), in = WIDE ? 0 : lane / T;
-    RingFill fill{P.from};
+    RingFill fill(X, P.from);
     if (!WIDE && warp == kRingWarps) {
-        if (lane == 0) {
-            while (fill.i < P.to && fill.next(R, X, sh, ring, P.to)) {}
-            fill.drain(R, sh);
-        }
+        while (fill.i < P.to && fill.next(R, sh, ring, P.to)) {}
+        fill.drain(R, sh);
         return;
     }
-    if (WIDE && threadIdx.x == 0)
+    if (WIDE && warp == 0)
         for (int k = 0; k + 1 < R.stages && fill.i < P.to; ++k)
-            if (!fill.next(R, X, sh, ring, P.to)) sum.failed = 1;
+            if (!fill.next(R, sh, ring, P.to)) sum.failed = 1;
     int stage = 0;
     uint32_t parity = 0;
     for (int64_t i = P.from; i < P.to; i += R.high) {
-        if (WIDE && threadIdx.x == 0 && fill.i < P.to && !fill.next(R, X, sh, ring, P.to)) sum.failed = 1;
+        if (WIDE && warp == 0 && fill.i < P.to && !fill.next(R, sh, ring, P.to)) sum.failed = 1;
         const int rows = (int)min((int64_t)R.high, P.to - i);
         const bool ok = mbar_wait(&sh.full[stage], parity, &sh.abort, R.wait_ns, R.status, WAIT_MMA_FULL);
         if (!WIDE && !__all_sync(~0u, ok)) break;
         if (!ok) sum.failed = 1;
-        for (int k = at; k < rows; k += kMostRows * P.step) {
+        for (int k = at; k < rows; k += ROWS * P.step) {
             body(ring + stage * R.stage_bytes, k + in, rows, i);
             if (WIDE && sum.failed) break;
         }
@@ -730,10 +766,10 @@ __device__ __forceinline__ void ring_run(const RnRing& R, const RnTensors& X, co
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
         if (++stage == R.stages) stage = 0, parity ^= 1;
     }
-    if (WIDE && threadIdx.x == 0) fill.drain(R, sh);
+    if (WIDE && warp == 0) fill.drain(R, sh);
 }
 
-template <typename S, typename F, bool WIDE>
+template <typename S, typename F, bool WIDE, int ROWS>
 __global__ void __launch_bounds__(512, 1) rn_fwd_ring_kernel(const RnArgs A, int T, const RnRing R, const S* x, const F* f, S* r, F* h, float4* stats) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RnShared sh;
@@ -744,11 +780,11 @@ __global__ void __launch_bounds__(512, 1) rn_fwd_ring_kernel(const RnArgs A, int
     const RnTensors X{{reinterpret_cast<const char*>(x), reinterpret_cast<const char*>(f)}, {row, f ? A.c * (int)sizeof(F) : 0}};
     RowSum<WIDE> sum{red, 0, T};
     const FwdVectors V(A, C, P.sample);
-    ring_run<WIDE>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
-        float v[kMostRows][8], w[kMostRows][8];
-        bool mine[kMostRows];
+    ring_run<WIDE, ROWS>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
+        uint64_t v[ROWS][4], w[ROWS][4];
+        bool mine[ROWS];
 #pragma unroll
-        for (int b = 0; b < kMostRows; ++b) {
+        for (int b = 0; b < ROWS; ++b) {
             mine[b] = k + b * P.step < rows;
             from_stage<S>(stage, mine[b] && C.has(0), A.c, k + b * P.step, C.t, v[b]);
             from_stage<F>(stage + R.high * row, f && mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
@@ -757,7 +793,7 @@ __global__ void __launch_bounds__(512, 1) rn_fwd_ring_kernel(const RnArgs A, int
     });
 }
 
-template <typename S, typename F, bool WIDE>
+template <typename S, typename F, bool WIDE, int ROWS>
 __global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int T, const RnRing R, const F* f, const S* r, const float4* stats,
                                                            const F* dh, const S* dr, S* dx, F* df, float* part) {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -772,35 +808,35 @@ __global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int
     const int o1 = R.high * X.bytes[0], o2 = o1 + R.high * X.bytes[1], o3 = o2 + R.high * X.bytes[2], o4 = o3 + R.high * X.bytes[3];
     BwdVectors V(A, C, P.sample);
     RowSum<WIDE> sum{red, 0, T};
-    ring_run<WIDE>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
-        float d[kMostRows][8];
-        float4 st[kMostRows];
-        bool mine[kMostRows];
+    ring_run<WIDE, ROWS>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
+        uint64_t d[ROWS][4];
+        float4 st[ROWS];
+        bool mine[ROWS];
 #pragma unroll
-        for (int b = 0; b < kMostRows; ++b) {
+        for (int b = 0; b < ROWS; ++b) {
             mine[b] = k + b * P.step < rows;
             st[b] = mine[b] ? *reinterpret_cast<const float4*>(stage + o4 + 16 * (k + b * P.step)) : make_float4(0.f, 1.f, 0.f, 1.f);
             from_stage<S>(stage + o1, dr && mine[b] && C.has(0), A.c, k + b * P.step, C.t, d[b]);
         }
         if (A.pre != CF_NORM_NONE) {
-            float rh[kMostRows][8], u[kMostRows][8];
+            uint64_t rh[ROWS][4], u[ROWS][4];
 #pragma unroll
-            for (int b = 0; b < kMostRows; ++b) {
+            for (int b = 0; b < ROWS; ++b) {
                 from_stage<S>(stage, mine[b] && C.has(0), A.c, k + b * P.step, C.t, rh[b]);
                 from_stage<F>(stage + o2, mine[b] && C.has(0), A.c, k + b * P.step, C.t, u[b]);
             }
             bwd_stream(A, C, sum, V, st, d, rh, u);
         }
 #pragma unroll
-        for (int b = 0; b < kMostRows; ++b)
+        for (int b = 0; b < ROWS; ++b)
             if (dx && mine[b]) store8(dx, (i + k + b * P.step) * A.c, C, d[b]);
         if (f) {
-            float w[kMostRows][8];
+            uint64_t w[ROWS][4];
 #pragma unroll
-            for (int b = 0; b < kMostRows; ++b) from_stage<F>(stage + o3, mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
+            for (int b = 0; b < ROWS; ++b) from_stage<F>(stage + o3, mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
             bwd_block(A, C, sum, V, st, d, w);
 #pragma unroll
-            for (int b = 0; b < kMostRows; ++b)
+            for (int b = 0; b < ROWS; ++b)
                 if (df && mine[b]) store8(df, (i + k + b * P.step) * A.c, C, d[b]);
         }
     });
@@ -926,7 +962,7 @@ int ring_per_sm(int T) { return T <= 32 ? 1 : 512 / T; }
 // Whether rows go through the ring: whole vectors, and at least two rounds of rows to a block.  Fewer are quicker without (64 x 256
 // forward 2.2 us without, 3.4 with it), more with it (8 x 32^3 x 128 forward 74 without, 55 with it).
 bool ringed(const RnArgs& A, int T) {
-    const int64_t step = kMostRows * (T <= 32 ? kRingWarps * 32 / T : 1);
+    const int64_t step = T <= 32 ? kMostRows * (kRingWarps * 32 / T) : 2;
     return T && A.c % 8 == 0 && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms;
 }
 // A's rows cut for the kernel that takes them.
@@ -936,11 +972,11 @@ void cut_rows(RnArgs& A, int T, int narrow) {
     else
         cut(A, (int64_t)kPlanSms * per_sm(T, narrow), T <= 32 ? kThreads / T : 1);
 }
-RnRing ring_of(const LaunchCtx& ctx, const RnArgs& A, int T, int per_row, int& shared) {
+RnRing ring_of(const LaunchCtx& ctx, const RnArgs& A, int T, int at_once, int per_row, int& shared) {
     RnRing R{};
-    const int n = ring_per_sm(T), step = kMostRows * (T <= 32 ? kRingWarps * 32 / T : 1);
+    const int n = ring_per_sm(T), step = at_once * (T <= 32 ? kRingWarps * 32 / T : 1);
     const int room = 228 * 1024 / n - 1024 - 1024;  // what the system keeps of a block's, and the barriers
-    R.high = std::max(1, room / 4 / (per_row * step)) * step;  // four stages, or as many as fit of one round of rows
+    R.high = std::max(1, room / 5 / (per_row * step)) * step;  // five stages, or as many as fit of one round of rows
     R.high = (int)std::min<int64_t>(R.high, (A.chunk + step - 1) / step * step);
     R.stage_bytes = (uint32_t)((R.high * per_row + 127) / 128 * 128);
     R.stages = std::min(kMostRing, room / (int)R.stage_bytes);
@@ -1044,8 +1080,8 @@ cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x,
             const unsigned blocks = (unsigned)(A.samples * A.chunks);
             if (ringed(A, T)) {
                 int shared;
-                const RnRing R = ring_of(ctx, A, T, A.c * (int)(sizeof(S) + (f ? sizeof(F) : 0)), shared);
-                auto kernel = T <= 32 ? rn_fwd_ring_kernel<S, F, false> : rn_fwd_ring_kernel<S, F, true>;
+                const RnRing R = ring_of(ctx, A, T, 2, A.c * (int)(sizeof(S) + (f ? sizeof(F) : 0)), shared);
+                auto kernel = T <= 32 ? rn_fwd_ring_kernel<S, F, false, 2> : rn_fwd_ring_kernel<S, F, true, 2>;
                 if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
                 kernel<<<blocks, T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(A, T, R, xs, fs, static_cast<S*>(r), static_cast<F*>(h), st4);
                 return status_of();
@@ -1102,8 +1138,8 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
         if (const int T = threads_of(A.c); T && ringed(A, T)) {
             int shared;
             const int per_row = A.c * (int)((dh ? sizeof(S) + sizeof(F) : 0) + (dr ? sizeof(S) : 0) + (f ? sizeof(F) : 0)) + 16;
-            const RnRing R = ring_of(ctx, A, T, per_row, shared);
-            auto kernel = T <= 32 ? rn_bwd_ring_kernel<S, F, false> : rn_bwd_ring_kernel<S, F, true>;
+            const RnRing R = ring_of(ctx, A, T, T <= 32 ? 2 : 1, per_row, shared);
+            auto kernel = T <= 32 ? rn_bwd_ring_kernel<S, F, false, 2> : rn_bwd_ring_kernel<S, F, true, 1>;
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
             kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(
                 A, T, R, fs, rs, st4, dhs, drs, static_cast<S*>(dx), static_cast<F*>(df), sums ? L.part : nullptr);
