@@ -140,6 +140,14 @@ Product plan_of(const cf_linear_desc* d, int op) {
     G.tm = (int)best.tm, G.tn = (int)best.tn, G.bn = best.bn;
     G.stage_bytes = best.stage_bytes;
     G.a_box = 128, G.b_box = best.pair ? best.bn / 2 : best.bn;
+    // Narrow tiles of many rows: as many side by side as the accumulator holds, so that what a tile takes besides its products and
+    // stores is taken less often; with rounds enough left to even out.
+    G.sub = 1;
+    if (!best.pair && !P.plan.swap && op != OP_WGRAD && best.tn == 1 && best.whole == best.tm) {
+        while (2 * G.sub * best.bn <= 256 && best.tm >= 8 * G.sub * best.units) G.sub *= 2;
+        best.tm = over(G.m, 128 * G.sub), best.whole = best.tm;
+        G.tm = (int)best.tm;
+    }
     const int64_t tiles = best.tm * best.tn;
     G.whole = (int)best.whole, G.share = (int)best.share, G.rest = (tiles - best.whole) * G.nkb;
     const int64_t share = best.share;

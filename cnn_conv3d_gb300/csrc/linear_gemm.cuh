@@ -55,6 +55,7 @@ struct LinGemm {
     int nkb;                 // 64-blocks of the contracted axis
     int tm, tn;              // tiles
     int bn;                  // columns of a tile
+    int sub;                 // a narrow tile has so many times 128 rows, side by side in the accumulator
     int a_mn, b_mn;          // operands with their rows contiguous
     int a_box, b_box;        // K-major: rows of a copy
     int stages, stage_bytes;
@@ -357,26 +358,35 @@ __device__ __forceinline__ bool takes_sums(const LinEpi& E, const LinItem& s) {
     return OP == OP_WGRAD && E.db && (SWAP ? s.mt : s.nt) == 0;
 }
 
+// Rows of a tile's parts of 128 (of one CTA) that there are.
+template <bool PAIR>
+__device__ __forceinline__ int parts_of(const LinGemm& G, const LinItem& s) {
+    return PAIR || G.sub == 1 ? 1 : (int)min((int64_t)G.sub, (G.m - (int64_t)s.mt * 128 * G.sub + 127) / 128);
+}
 // The passes of an epilogue warp over the tiles that it finishes itself, in the order that it takes them.
+template <bool PAIR>
 struct LinPasses {
     LinWalk way;
     LinItem s;
-    int c, local;  // first column of the pass in its tile; the unit's tiles and parts so far
+    int pass, part, c, local;  // pass of the tile: its 128 rows, and first column; the unit's tiles and parts so far
     bool more;
-    __device__ __forceinline__ LinPasses(const LinGemm& G, int unit, int set, int turn) : way(G, unit), c(G.bn), local(0), more(true) {
+    __device__ __forceinline__ LinPasses(const LinGemm& G, int unit, int set, int turn) : way(G, unit), pass(1 << 20), local(0), more(true) {
         next(G, unit, set, turn);
     }
     __device__ __forceinline__ void next(const LinGemm& G, int unit, int set, int turn) {
-        c += G.st.turns * G.st.gw;
-        while (more && c >= G.bn) {
+        const int across = (G.bn + G.st.gw - 1) / G.st.gw;
+        pass += G.st.turns;
+        while (more && (pass >= 1 << 20 || pass >= across * parts_of<PAIR>(G, s))) {
             bool mine;
             do {
                 more = way.next(G, unit, s);
                 mine = s.slot < 0 && (G.st.sets == 1 || (local & 1) == set);
                 ++local;
             } while (more && !mine);
-            c = turn * G.st.gw;
+            pass = turn;
         }
+        part = pass / across;
+        c = (pass - part * across) * G.st.gw;
     }
 };
 
@@ -456,29 +466,33 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         const int q = isb ? lane - 2 : lane;
         bool ok = true;
         while (ok && way.next(G, unit, s)) {
-            const int64_t m0 = (int64_t)s.mt * (PAIR ? 256 : 128) + 128 * rank, n0 = (int64_t)s.nt * G.bn + bhalf * rank;
+            int64_t m0 = (int64_t)s.mt * (PAIR ? 256 : 128 * G.sub) + 128 * rank;
+            const int64_t n0 = (int64_t)s.nt * G.bn + bhalf * rank;
+            const int parts = parts_of<PAIR>(G, s);
             const int na = G.a_mn ? (int)min((int64_t)2, max((int64_t)0, (G.m - m0 + 63) / 64)) : 1;
             const int nb = G.b_mn ? (int)min((int64_t)(bhalf + 63) / 64, max((int64_t)0, (G.n - n0 + 63) / 64)) : 1;
             const uint32_t bytes = (G.a_mn ? na * 8192 : 16384) + (G.b_mn ? nb * 8192 : G.b_box * 128);
             const bool mn = isb ? G.b_mn : G.a_mn, mine = q < (isb ? nb : na);
-            const int64_t r0 = isb ? n0 : m0;
             const uint32_t dst = (isb ? 16384 : 0) + q * 8192;
             const CUtensorMap* map = isb ? &M.b : &M.a;
-            for (int kb = s.kb0; kb < s.kb1; ++kb) {
-                ok = __all_sync(~0u, mbar_wait(&sh.empty[R.stage], R.parity() ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_PRODUCER_EMPTY));
-                if (!ok) break;
-                uint64_t* bar = &sh.full[R.stage];
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                __syncwarp();
-                if (mine) {
-                    uint8_t* to = ring + R.stage * G.stage_bytes + dst;
-                    if (mn)
-                        tma_load_2d(to, map, bar, (int)(r0 + 64 * q), (int)(64 * kb));
-                    else
-                        tma_load_2d(to, map, bar, (int)(64 * kb), (int)r0);
+            for (int part = 0; ok && part < parts; ++part, m0 += 128) {
+                const int64_t r0 = isb ? n0 : m0;
+                for (int kb = s.kb0; kb < s.kb1; ++kb) {
+                    ok = __all_sync(~0u, mbar_wait(&sh.empty[R.stage], R.parity() ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_PRODUCER_EMPTY));
+                    if (!ok) break;
+                    uint64_t* bar = &sh.full[R.stage];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (mine) {
+                        uint8_t* to = ring + R.stage * G.stage_bytes + dst;
+                        if (mn)
+                            tma_load_2d(to, map, bar, (int)(r0 + 64 * q), (int)(64 * kb));
+                        else
+                            tma_load_2d(to, map, bar, (int)(64 * kb), (int)r0);
+                    }
+                    R.issued |= 1u << R.stage;
+                    R.next(G.stages);
                 }
-                R.issued |= 1u << R.stage;
-                R.next(G.stages);
             }
         }
     } else if (warp == 1 && lane == 0) {
@@ -508,31 +522,35 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 ok = mbar_wait(&sh.tempty[acc ^ 1], ((local - 1) >> 1) & 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
             alone = sums;
             tc_fence_after();
-            for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
-                ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t as = smem_u32(ring + R.stage * G.stage_bytes), bs = as + 16384;
+            const int parts = parts_of<PAIR>(G, s);
+            for (int part = 0; ok && part < parts; ++part) {
+                const uint32_t dp = d + part * G.bn;
+                for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
+                    ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t as = smem_u32(ring + R.stage * G.stage_bytes), bs = as + 16384;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t ad = sdesc(as + k * astep, alead, 1024, SWZ_128B), bd = sdesc(bs + k * bstep, blead, 1024, SWZ_128B);
-                    const uint32_t more = kb > s.kb0 || k > 0;
-                    if (PAIR)
-                        umma_pair(d, ad, bd, idesc, more);
-                    else
-                        umma_bf16(d, ad, bd, idesc, more);
-                    if (OP == OP_WGRAD && sums) {
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t ad = sdesc(as + k * astep, alead, 1024, SWZ_128B), bd = sdesc(bs + k * bstep, blead, 1024, SWZ_128B);
+                        const uint32_t more = kb > s.kb0 || k > 0;
                         if (PAIR)
-                            umma_pair(d1, ad, one, idesc1, more);
+                            umma_pair(dp, ad, bd, idesc, more);
                         else
-                            umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, more);
+                            umma_bf16(dp, ad, bd, idesc, more);
+                        if (OP == OP_WGRAD && sums) {
+                            if (PAIR)
+                                umma_pair(d1, ad, one, idesc1, more);
+                            else
+                                umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, more);
+                        }
                     }
+                    if (PAIR)
+                        commit_pair(&sh.empty[R.stage]);
+                    else
+                        umma_commit(&sh.empty[R.stage]);
+                    R.next(G.stages);
                 }
-                if (PAIR)
-                    commit_pair(&sh.empty[R.stage]);
-                else
-                    umma_commit(&sh.empty[R.stage]);
-                R.next(G.stages);
             }
             if (!ok) break;
             if (PAIR)
@@ -549,14 +567,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         const uint32_t in_bytes = SWAP || !TMA ? 0 : (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
         uint32_t done = 0, asked = 0;  // passes finished, and those whose loads were issued
         bool ok = set < S.sets;
-        LinPasses ahead(G, unit, set, turn);
+        LinPasses<PAIR> ahead(G, unit, set, turn);
         // the next pass's loads, once the present one's store has been read
         auto ask = [&]() {
             if (lane == 0) bulk_wait_read();
             __syncwarp();
             if (!in_bytes || !ahead.more) return;
             if (lane == 0) {
-                const int row = ahead.s.mt * (PAIR ? 256 : 128) + 128 * rank + 32 * q, col = ahead.s.nt * G.bn + ahead.c;
+                const int row = ahead.s.mt * (PAIR ? 256 : 128 * G.sub) + 128 * (rank + ahead.part) + 32 * q, col = ahead.s.nt * G.bn + ahead.c;
                 mbar_arrive_expect_tx(&sh.in[warp - 2], in_bytes);
                 if (S.load_add)
                     for (int x = 0; x < S.out_bytes / 4096; ++x) tma_load_2d(out + x * 4096, &M.add, &sh.in[warp - 2], col + x * (E.f32 ? 32 : 64), row);
@@ -577,9 +595,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             const uint32_t acc = local & 1, use = local >> 1;
             if (S.sets == 2 && (int)acc != set) continue;
             const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
-            const int64_t i = (int64_t)s.mt * (PAIR ? 256 : 128) + 128 * rank + r, j0 = (int64_t)s.nt * G.bn;
+            const int64_t i = (int64_t)s.mt * (PAIR ? 256 : 128 * G.sub) + 128 * rank + r, j0 = (int64_t)s.nt * G.bn;
+            const int across = (G.bn + S.gw - 1) / S.gw, most = across * parts_of<PAIR>(G, s);  // passes
             float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
-            ask_bias(j0 + turn * S.gw);
+            ask_bias(j0 + turn % across * S.gw);
             ok = mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
             if (!ok) break;
             tc_fence_after();
@@ -616,8 +635,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     }
                 }
             } else {
-                for (int c0 = turn * S.gw; c0 < G.bn; c0 += S.turns * S.gw, ++done) {
-                    const int64_t row = i - lane;
+                for (int pass = turn; pass < most; pass += S.turns, ++done) {
+                    const int sub = pass / across, c0 = (pass - sub * across) * S.gw;
+                    const int64_t row = i - lane + 128 * sub;
                     const int col = (int)j0 + c0;
                     if (TMA && in_bytes) {
                         ok = mbar_wait(&sh.in[warp - 2], done & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
@@ -630,12 +650,12 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     if (OP == OP_FWD && E.bias) {
                         biases[lane] = b0, biases[32 + lane] = b1;
                         __syncwarp();
-                        ask_bias(col + S.turns * S.gw);
+                        ask_bias(j0 + (pass + S.turns) % across * S.gw);
                     }
 #pragma unroll 1
                     for (int c = 0; c < S.gw && c0 + c < G.bn; c += 16) {
                         uint32_t u[32];  // the first 16
-                        tmem_ld16(tm + c0 + c, u);
+                        tmem_ld16(tm + sub * G.bn + c0 + c, u);
                         tmem_ld_wait();
                         float v[16];
 #pragma unroll

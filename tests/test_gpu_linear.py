@@ -163,6 +163,14 @@ def test_large_products(cf, rows, k, n):
     check_wgrad(cf, rng, k, rows, n)
 
 
+@pytest.mark.parametrize("rows,k,n", [(160001, 32, 32), (400100, 64, 16), (170000, 40, 48), (330000, 16, 128), (200003, 24, 21)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_narrow_products_of_many_rows(cf, rows, k, n, dtype):
+    rng = np.random.default_rng(rows)
+    check_fwd(cf, rng, rows, k, n, "gelu", dtype=dtype)
+    check_dgrad(cf, rng, rows, n, k, "silu", dtype=dtype)
+
+
 @pytest.mark.parametrize("act,slope", [("none", 1.0), ("lrelu", 0.3), ("lrelu", 0.0), ("silu", 1.0), ("gelu", 1.0)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows", [4, 300])
