@@ -640,7 +640,8 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2)
 // registers hold.  Threads work on two rows at a time (ROWS), whose sums go together: a row's time is mostly the latency of those; but for the backward
 // of rows that all threads share, which has the registers for one.  Rows of warps have a warp that copies; where all threads have a row,
 // the first does, for the stage before, once all are through with it.
-// Rows of a multiple of eight values.
+// Bulk copies begin and end at multiples of 16 bytes: where rows do not, a stage's first row lies up to 15 bytes into its room, and what
+// is left of a tensor behind its last whole 16 bytes is copied value by value.
 constexpr int kRingWarps = 15;
 constexpr int kMostRing = 8;
 
@@ -660,34 +661,46 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-// What a stage holds, one after another: a row's bytes of each (0: not there).
+// What a stage holds, one after another: a row's bytes of each (0: not there), a multiple of 16 or `size` times so many values.
 struct RnTensors {
     const char* at[5];
-    int bytes[5];
+    int bytes[5], size[5];
+    int64_t rows;
 };
+// A tensor's room in a stage.
+__host__ __device__ inline int room_of(int high, int bytes) { return bytes ? (high * bytes + 30) & ~15 : 0; }
 // The copies of one stage after another, by a warp: a lane to each tensor.
 struct RingFill {
-    int64_t i;
+    int64_t i, end = 0;  // the next row; the tensor's bytes
     const char* at = nullptr;
-    int mine = 0, per_row = 0, before = 0;
+    int mine = 0, size = 0, before = 0;
     int stage = 0;
     uint32_t parity = 1, issued = 0;
-    __device__ __forceinline__ RingFill(const RnTensors& X, int64_t from) : i(from) {
+    __device__ __forceinline__ RingFill(const RnTensors& X, int high, int64_t from) : i(from) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
-            if (k < lane) before += X.bytes[k];
-            if (k == lane) at = X.at[k], mine = X.bytes[k];
-            per_row += X.bytes[k];
+            if (k < lane) before += room_of(high, X.bytes[k]);
+            if (k == lane) at = X.at[k], mine = X.bytes[k], size = X.size[k];
         }
+        end = X.rows * mine;
     }
     __device__ __forceinline__ bool next(const RnRing& R, RnShared& sh, uint8_t* ring, int64_t to) {
         const bool ok = mbar_wait(&sh.empty[stage], parity, &sh.abort, R.wait_ns, R.status, WAIT_PRODUCER_EMPTY);
         if (!__all_sync(~0u, ok)) return false;
-        const int rows = (int)min((int64_t)R.high, to - i);
-        if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&sh.full[stage], rows * per_row);
+        const int64_t first = i * mine, last = min(i + R.high, to) * mine, low = first & ~(int64_t)15;
+        const int64_t high = min((last + 15) & ~(int64_t)15, end & ~(int64_t)15);
+        uint8_t* dst = ring + stage * R.stage_bytes + before;
+        for (int64_t b = high; b < last; b += size) {
+            if (size == 4)
+                *reinterpret_cast<float*>(dst + (b - low)) = *reinterpret_cast<const float*>(at + b);
+            else
+                *reinterpret_cast<uint16_t*>(dst + (b - low)) = *reinterpret_cast<const uint16_t*>(at + b);
+        }
+        const uint32_t bytes = __reduce_add_sync(~0u, (uint32_t)(high - low));
+        if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&sh.full[stage], bytes);
         __syncwarp();
-        if (mine) bulk_load(ring + stage * R.stage_bytes + R.high * before, at + i * mine, rows * mine, &sh.full[stage]);
+        if (high > low) bulk_load(dst, at + low, (uint32_t)(high - low), &sh.full[stage]);
         ++issued;
         i += R.high;
         if (++stage == R.stages) stage = 0, parity ^= 1;
@@ -719,15 +732,29 @@ __device__ __forceinline__ Place ring_begin(const RnArgs& A, int T, C_& C, const
     P.step = WIDE ? 1 : kRingWarps * 32 / T;
     return P;
 }
-template <typename T_>
-__device__ __forceinline__ void from_stage(const uint8_t* p, bool there, int c, int row, int t, uint64_t (&v)[4]) {
+// The thread's values of row k of a tensor's room, in a stage that begins with row i.
+template <typename T_, typename C_>
+__device__ __forceinline__ void from_stage(const uint8_t* room, bool there, const C_& C, int64_t i, int k, uint64_t (&v)[4]) {
     Raw<T_> raw{};
-    if (there) {
-        const uint4* q = reinterpret_cast<const uint4*>(p + ((int64_t)row * c + 8 * t) * sizeof(T_));
+    if (C.vec) {
+        if (there && C.has(0)) {
+            const uint4* q = reinterpret_cast<const uint4*>(room + (k * C.c + 8 * C.t) * (int)sizeof(T_));
 #pragma unroll
-        for (int e = 0; e < (int)sizeof(T_) / 2; ++e) {
-            const uint4 x = q[e];
-            raw.u[4 * e] = x.x, raw.u[4 * e + 1] = x.y, raw.u[4 * e + 2] = x.z, raw.u[4 * e + 3] = x.w;
+            for (int e = 0; e < (int)sizeof(T_) / 2; ++e) {
+                const uint4 x = q[e];
+                raw.u[4 * e] = x.x, raw.u[4 * e + 1] = x.y, raw.u[4 * e + 2] = x.z, raw.u[4 * e + 3] = x.w;
+            }
+        }
+    } else if (there) {
+        const T_* q = reinterpret_cast<const T_*>(room + ((int)(i * C.c * (int)sizeof(T_)) & 15)) + k * C.c;
+        if (sizeof(T_) == 4) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (C.has(e)) raw.u[e % (2 * sizeof(T_))] = *reinterpret_cast<const uint32_t*>(q + C.at(e));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (C.has(e)) raw.u[e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(q + C.at(e)) << 16 * (e & 1);
         }
     }
     unpack(raw, v);
@@ -740,7 +767,7 @@ template <bool WIDE, int ROWS, typename B>
 __device__ __forceinline__ void ring_run(const RnRing& R, const RnTensors& X, const Place& P, int T, RowSum<WIDE>& sum, RnShared& sh, uint8_t* ring,
                                          B body) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = WIDE ? 0 : warp * (32 / T), in = WIDE ? 0 : lane / T;
-    RingFill fill(X, P.from);
+    RingFill fill(X, R.high, P.from);
     if (!WIDE && warp == kRingWarps) {
         while (fill.i < P.to && fill.next(R, sh, ring, P.to)) {}
         fill.drain(R, sh);
@@ -769,15 +796,17 @@ __device__ __forceinline__ void ring_run(const RnRing& R, const RnTensors& X, co
     if (WIDE && warp == 0) fill.drain(R, sh);
 }
 
-template <typename S, typename F, bool WIDE, int ROWS>
+template <typename S, typename F, bool WIDE, int ROWS, bool VEC>
 __global__ void __launch_bounds__(512, 1) rn_fwd_ring_kernel(const RnArgs A, int T, const RnRing R, const S* x, const F* f, S* r, F* h, float4* stats) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RnShared sh;
     __shared__ float red[2][16][2 * kMostRows];
-    Cols<true> C;
+    Cols<VEC> C;
     const Place P = ring_begin<WIDE>(A, T, C, R, sh);
     const int row = A.c * (int)sizeof(S);
-    const RnTensors X{{reinterpret_cast<const char*>(x), reinterpret_cast<const char*>(f)}, {row, f ? A.c * (int)sizeof(F) : 0}};
+    const RnTensors X{{reinterpret_cast<const char*>(x), reinterpret_cast<const char*>(f)}, {row, f ? A.c * (int)sizeof(F) : 0},
+                      {sizeof(S), sizeof(F)}, A.rows};
+    const int of_f = room_of(R.high, row);
     RowSum<WIDE> sum{red, 0, T};
     const FwdVectors V(A, C, P.sample);
     ring_run<WIDE, ROWS>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
@@ -786,26 +815,27 @@ __global__ void __launch_bounds__(512, 1) rn_fwd_ring_kernel(const RnArgs A, int
 #pragma unroll
         for (int b = 0; b < ROWS; ++b) {
             mine[b] = k + b * P.step < rows;
-            from_stage<S>(stage, mine[b] && C.has(0), A.c, k + b * P.step, C.t, v[b]);
-            from_stage<F>(stage + R.high * row, f && mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
+            from_stage<S>(stage, mine[b], C, i, k + b * P.step, v[b]);
+            from_stage<F>(stage + of_f, f && mine[b], C, i, k + b * P.step, w[b]);
         }
         fwd_rows(A, C, sum, V, f != nullptr, i + k, P.step, mine, v, w, r, h, stats);
     });
 }
 
-template <typename S, typename F, bool WIDE, int ROWS>
+template <typename S, typename F, bool WIDE, int ROWS, bool VEC>
 __global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int T, const RnRing R, const F* f, const S* r, const float4* stats,
                                                            const F* dh, const S* dr, S* dx, F* df, float* part) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RnShared sh;
     __shared__ float red[2][16][2 * kMostRows];
-    Cols<true> C;
+    Cols<VEC> C;
     const Place P = ring_begin<WIDE>(A, T, C, R, sh);
     const int rs = A.c * (int)sizeof(S), rf = A.c * (int)sizeof(F);
     const RnTensors X{{reinterpret_cast<const char*>(r), reinterpret_cast<const char*>(dr), reinterpret_cast<const char*>(dh),
                        reinterpret_cast<const char*>(f), reinterpret_cast<const char*>(stats)},
-                      {dh ? rs : 0, dr ? rs : 0, dh ? rf : 0, f ? rf : 0, 16}};
-    const int o1 = R.high * X.bytes[0], o2 = o1 + R.high * X.bytes[1], o3 = o2 + R.high * X.bytes[2], o4 = o3 + R.high * X.bytes[3];
+                      {dh ? rs : 0, dr ? rs : 0, dh ? rf : 0, f ? rf : 0, 16}, {sizeof(S), sizeof(S), sizeof(F), sizeof(F), 4}, A.rows};
+    const int o1 = room_of(R.high, X.bytes[0]), o2 = o1 + room_of(R.high, X.bytes[1]), o3 = o2 + room_of(R.high, X.bytes[2]);
+    const int o4 = o3 + room_of(R.high, X.bytes[3]);
     BwdVectors V(A, C, P.sample);
     RowSum<WIDE> sum{red, 0, T};
     ring_run<WIDE, ROWS>(R, X, P, T, sum, sh, ring, [&](const uint8_t* stage, int k, int rows, int64_t i) {
@@ -816,14 +846,14 @@ __global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int
         for (int b = 0; b < ROWS; ++b) {
             mine[b] = k + b * P.step < rows;
             st[b] = mine[b] ? *reinterpret_cast<const float4*>(stage + o4 + 16 * (k + b * P.step)) : make_float4(0.f, 1.f, 0.f, 1.f);
-            from_stage<S>(stage + o1, dr && mine[b] && C.has(0), A.c, k + b * P.step, C.t, d[b]);
+            from_stage<S>(stage + o1, dr && mine[b], C, i, k + b * P.step, d[b]);
         }
         if (A.pre != CF_NORM_NONE) {
             uint64_t rh[ROWS][4], u[ROWS][4];
 #pragma unroll
             for (int b = 0; b < ROWS; ++b) {
-                from_stage<S>(stage, mine[b] && C.has(0), A.c, k + b * P.step, C.t, rh[b]);
-                from_stage<F>(stage + o2, mine[b] && C.has(0), A.c, k + b * P.step, C.t, u[b]);
+                from_stage<S>(stage, mine[b], C, i, k + b * P.step, rh[b]);
+                from_stage<F>(stage + o2, mine[b], C, i, k + b * P.step, u[b]);
             }
             bwd_stream(A, C, sum, V, st, d, rh, u);
         }
@@ -833,7 +863,7 @@ __global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int
         if (f) {
             uint64_t w[ROWS][4];
 #pragma unroll
-            for (int b = 0; b < ROWS; ++b) from_stage<F>(stage + o3, mine[b] && C.has(0), A.c, k + b * P.step, C.t, w[b]);
+            for (int b = 0; b < ROWS; ++b) from_stage<F>(stage + o3, mine[b], C, i, k + b * P.step, w[b]);
             bwd_block(A, C, sum, V, st, d, w);
 #pragma unroll
             for (int b = 0; b < ROWS; ++b)
@@ -959,11 +989,11 @@ int per_sm(int T, int narrow) { return T <= 32 ? narrow : std::max(1, 512 / T); 
 // And of those with one: a block of 15 warps and one that copies, or of T threads.
 int ring_per_sm(int T) { return T <= 32 ? 1 : 512 / T; }
 
-// Whether rows go through the ring: whole vectors, and at least two rounds of rows to a block.  Fewer are quicker without (64 x 256
+// Whether rows go through the ring: at least two rounds of rows to a block.  Fewer are quicker without (64 x 256
 // forward 2.2 us without, 3.4 with it), more with it (8 x 32^3 x 128 forward 74 without, 55 with it).
 bool ringed(const RnArgs& A, int T) {
     const int64_t step = T <= 32 ? kMostRows * (kRingWarps * 32 / T) : 2;
-    return T && A.c % 8 == 0 && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms;
+    return T && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms;
 }
 // A's rows cut for the kernel that takes them.
 void cut_rows(RnArgs& A, int T, int narrow) {
@@ -976,9 +1006,10 @@ RnRing ring_of(const LaunchCtx& ctx, const RnArgs& A, int T, int at_once, int pe
     RnRing R{};
     const int n = ring_per_sm(T), step = at_once * (T <= 32 ? kRingWarps * 32 / T : 1);
     const int room = 228 * 1024 / n - 1024 - 1024;  // what the system keeps of a block's, and the barriers
-    R.high = std::max(1, room / 5 / (per_row * step)) * step;  // five stages, or as many as fit of one round of rows
+    R.high = std::max(1, (room / 5 - 288) / (per_row * step)) * step;  // five stages, or as many as fit of one round of rows
+    if (3 * (R.high * per_row + 288) > room) R.high = step / at_once;
     R.high = (int)std::min<int64_t>(R.high, (A.chunk + step - 1) / step * step);
-    R.stage_bytes = (uint32_t)((R.high * per_row + 127) / 128 * 128);
+    R.stage_bytes = (uint32_t)((R.high * per_row + 5 * 32 + 127) / 128 * 128);
     R.stages = std::min(kMostRing, room / (int)R.stage_bytes);
     R.status = ctx.status, R.wait_ns = ctx.wait_ns;
     shared = std::max<int>(R.stages * R.stage_bytes, kRingWarps * 256 * 4);
@@ -1081,7 +1112,8 @@ cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x,
             if (ringed(A, T)) {
                 int shared;
                 const RnRing R = ring_of(ctx, A, T, 2, A.c * (int)(sizeof(S) + (f ? sizeof(F) : 0)), shared);
-                auto kernel = T <= 32 ? rn_fwd_ring_kernel<S, F, false, 2> : rn_fwd_ring_kernel<S, F, true, 2>;
+                auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_fwd_ring_kernel<S, F, false, 2, true> : rn_fwd_ring_kernel<S, F, true, 2, true>)
+                                           : (T <= 32 ? rn_fwd_ring_kernel<S, F, false, 2, false> : rn_fwd_ring_kernel<S, F, true, 2, false>);
                 if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
                 kernel<<<blocks, T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(A, T, R, xs, fs, static_cast<S*>(r), static_cast<F*>(h), st4);
                 return status_of();
@@ -1139,7 +1171,8 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
             int shared;
             const int per_row = A.c * (int)((dh ? sizeof(S) + sizeof(F) : 0) + (dr ? sizeof(S) : 0) + (f ? sizeof(F) : 0)) + 16;
             const RnRing R = ring_of(ctx, A, T, T <= 32 ? 2 : 1, per_row, shared);
-            auto kernel = T <= 32 ? rn_bwd_ring_kernel<S, F, false, 2> : rn_bwd_ring_kernel<S, F, true, 1>;
+            auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_bwd_ring_kernel<S, F, false, 2, true> : rn_bwd_ring_kernel<S, F, true, 1, true>)
+                                       : (T <= 32 ? rn_bwd_ring_kernel<S, F, false, 2, false> : rn_bwd_ring_kernel<S, F, true, 1, false>);
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
             kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(
                 A, T, R, fs, rs, st4, dhs, drs, static_cast<S*>(dx), static_cast<F*>(df), sums ? L.part : nullptr);

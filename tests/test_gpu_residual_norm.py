@@ -219,6 +219,16 @@ def test_rows_in_stages(cf, rows, c, each, per, post, pre, dtype, f_dtype):
     case.check_backward()
 
 
+# rows that begin inside 16 bytes, whose tensors end inside 16 bytes too
+@pytest.mark.parametrize("dtype,f_dtype", TYPES)
+@pytest.mark.parametrize("rows,c,each,per", [(20003, 130, 0, 0), (10007, 255, 3, 1001), (2003, 1001, 2, 333), (1301, 2045, 0, 0), (701, 4095, 1, 101),
+                                             (600001, 3, 0, 0), (400003, 1, 0, 0), (2437, 515, 0, 0)])
+def test_rows_that_begin_anywhere_in_stages(cf, rows, c, each, per, dtype, f_dtype):
+    case = Case(cf, rows, rows, c, "layer" if c > 3 else "rms", "rms", dtype, f_dtype, each=each, per=per)
+    case.check_forward()
+    case.check_backward()
+
+
 @pytest.mark.parametrize("rows,c", [(300001, 8), (80003, 32), (38000, 56)])
 def test_narrow_rows_in_stages(cf, rows, c):
     case = Case(cf, rows, rows, c, "layer", "rms", BF, BF, each=1, per=rows // 3)
@@ -226,7 +236,7 @@ def test_narrow_rows_in_stages(cf, rows, c):
     case.check_backward()
 
 
-@pytest.mark.parametrize("rows,c", [(20000, 128), (1300, 2048)])
+@pytest.mark.parametrize("rows,c", [(20000, 128), (1300, 2048), (20001, 129), (1301, 2047)])
 def test_stages_without_some_tensors(cf, rows, c):
     case = Case(cf, c, rows, c, "none", "layer", gate=False, with_f=False, with_dr=False)
     case.check_forward()
