@@ -27,22 +27,8 @@ struct RnArgs {
     const float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
 };
 
-__device__ __forceinline__ float load(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float load(const uint16_t* p, int64_t i) { return bf16_bits_to_float(p[i]); }
-__device__ __forceinline__ void store(float* p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void store(uint16_t* p, int64_t i, float v) { p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 __device__ __forceinline__ float at_or(const float* p, int64_t i, float other) { return p ? p[i] : other; }
-
-// p = a fh + b with what lies between the norm and the sum.
-__device__ __forceinline__ void post_affine(const RnArgs& A, int64_t sample, int j, float& a, float& b) {
-    const float g = A.scale * at_or(A.gate, A.gate_each ? sample * A.c + j : j, 1.f);
-    a = g * at_or(A.post_gamma, j, 1.f);
-    b = g * at_or(A.post_beta, j, 0.f);
-}
-__device__ __forceinline__ float2 pre_affine(const RnArgs& A, int64_t sample, int j) {
-    const int64_t i = A.pre_each ? sample * A.c + j : j;
-    return make_float2(at_or(A.pre_gamma, i, 1.f), at_or(A.pre_beta, i, 0.f));
-}
 
 constexpr int kThreads = 256;
 
@@ -58,136 +44,6 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2* red) {
     a = b = 0.f;
     for (int i = 0; i < (int)(blockDim.x >> 5); ++i) a += red[i].x, b += red[i].y;
     return make_float2(a, b);
-}
-
-// mean and 1 / width of c values, read twice.
-template <typename F>
-__device__ __forceinline__ float2 stats_long(const RnArgs& A, int kind, float2* red, F value) {
-    if (kind == CF_NORM_NONE) return make_float2(0.f, 1.f);
-    float mean = 0.f, s = 0.f;
-    if (kind == CF_NORM_LAYER) {
-        for (int j = threadIdx.x; j < A.c; j += kThreads) s += value(j);
-        mean = block_sum(s, 0.f, red).x * A.inv_c;
-    }
-    s = 0.f;
-    for (int j = threadIdx.x; j < A.c; j += kThreads) {
-        const float t = value(j) - mean;
-        s = fmaf(t, t, s);
-    }
-    return make_float2(mean, rsqrtf(block_sum(s, 0.f, red).x * A.inv_c + A.eps));
-}
-
-// Rows of any length: a block to a row, which is read again for each sum (from L1 or L2).
-template <typename S, typename F>
-__global__ void __launch_bounds__(kThreads) rn_fwd_long_kernel(const RnArgs A, const S* x, const F* f, S* r, F* h, float4* stats) {
-    __shared__ float2 red[kThreads / 32];
-    for (int64_t i = blockIdx.x; i < A.rows; i += gridDim.x) {
-        const int64_t o = i * A.c, sample = i / A.per;
-        const float2 sf = f ? stats_long(A, A.post, red, [&](int j) { return load(f, o + j); }) : make_float2(0.f, 1.f);
-        auto sum = [&](int j) {
-            const float v = load(x, o + j);
-            if (!f) return v;
-            float a, b;
-            post_affine(A, sample, j, a, b);
-            return v + fmaf(a, (load(f, o + j) - sf.x) * sf.y, b);
-        };
-        const float2 sr = stats_long(A, A.pre, red, sum);
-        __syncthreads();  // all have read the row before r, which may be x, is written
-        for (int j = threadIdx.x; j < A.c; j += kThreads) {
-            const float v = sum(j);
-            if (h) {
-                const float2 g = pre_affine(A, sample, j);
-                store(h, o + j, fmaf((v - sr.x) * sr.y, g.x, g.y));
-            }
-            if (r) store(r, o + j, v);
-        }
-        if (stats && threadIdx.x == 0) stats[i] = make_float4(sf.x, sf.y, sr.x, sr.y);
-    }
-}
-
-// dx of value j of a row, from m = (mean u, mean u rh).
-template <typename S, typename F>
-__device__ __forceinline__ float dx_of(const RnArgs& A, int64_t sample, int64_t o, int j, const S* r, const F* dh, const S* dr,
-                                       const float4& st, float2 m) {
-    float d = dr ? load(dr, o + j) : 0.f;
-    if (A.pre != CF_NORM_NONE) {
-        const float u = pre_affine(A, sample, j).x * load(dh, o + j);
-        d = fmaf(st.w, u - m.x - (load(r, o + j) - st.z) * st.w * m.y, d);
-    }
-    return d;
-}
-
-// The means that a row's gradients take.
-template <typename S, typename F>
-__global__ void __launch_bounds__(kThreads) rn_bwd_rows_kernel(const RnArgs A, const F* f, const S* r, const float4* stats, const F* dh,
-                                                               const S* dr, float4* means) {
-    __shared__ float2 red[kThreads / 32];
-    for (int64_t i = blockIdx.x; i < A.rows; i += gridDim.x) {
-        const int64_t o = i * A.c, sample = i / A.per;
-        const float4 st = stats[i];
-        float2 m = make_float2(0.f, 0.f), n = m;
-        if (A.pre != CF_NORM_NONE) {
-            for (int j = threadIdx.x; j < A.c; j += kThreads) {
-                const float u = pre_affine(A, sample, j).x * load(dh, o + j);
-                m.x += u;
-                m.y = fmaf(u, (load(r, o + j) - st.z) * st.w, m.y);
-            }
-            m = block_sum(m.x, m.y, red);
-            m.x = A.pre == CF_NORM_LAYER ? m.x * A.inv_c : 0.f;
-            m.y *= A.inv_c;
-        }
-        if (A.post != CF_NORM_NONE) {
-            for (int j = threadIdx.x; j < A.c; j += kThreads) {
-                float a, b;
-                post_affine(A, sample, j, a, b);
-                const float dv = a * dx_of(A, sample, o, j, r, dh, dr, st, m);
-                n.x += dv;
-                n.y = fmaf(dv, (load(f, o + j) - st.x) * st.y, n.y);
-            }
-            n = block_sum(n.x, n.y, red);
-            n.x = A.post == CF_NORM_LAYER ? n.x * A.inv_c : 0.f;
-            n.y *= A.inv_c;
-        }
-        if (threadIdx.x == 0) means[i] = make_float4(m.x, m.y, n.x, n.y);
-    }
-}
-
-// dx, df and the chunk's sums over rows, from the rows' means: 32 columns to a block, 8 rows at a time.
-template <typename S, typename F>
-__global__ void __launch_bounds__(kThreads) rn_bwd_cols_kernel(const RnArgs A, const F* f, const S* r, const float4* stats, const F* dh,
-                                                               const S* dr, const float4* means, S* dx, F* df, float* part) {
-    __shared__ float4 red[8][32];
-    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, j = blockIdx.y * 32 + lane;
-    const int sample = blockIdx.x / A.chunks;
-    const int64_t from = sample * A.per + (blockIdx.x - (int64_t)sample * A.chunks) * A.chunk;
-    const int64_t to = min(min(from + A.chunk, (sample + 1) * A.per), A.rows);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < A.c) {
-        float a, b;
-        post_affine(A, sample, j, a, b);
-        for (int64_t i = from + q; i < to; i += 8) {
-            const int64_t o = i * A.c;
-            const float4 st = stats[i], m = means[i];
-            const float d = dx_of(A, sample, o, j, r, dh, dr, st, make_float2(m.x, m.y));
-            const float fh = f ? (load(f, o + j) - st.x) * st.y : 0.f;
-            s.x = fmaf(d, fh, s.x);
-            s.y += d;
-            if (A.pre != CF_NORM_NONE) {
-                const float g = load(dh, o + j);
-                s.z = fmaf(g, (load(r, o + j) - st.z) * st.w, s.z);
-                s.w += g;
-            }
-            if (dx) store(dx, o + j, d);
-            if (df) store(df, o + j, A.post == CF_NORM_NONE ? a * d : st.y * (a * d - m.z - fh * m.w));
-        }
-    }
-    red[q][lane] = s;
-    __syncthreads();
-    if (q == 0 && j < A.c) {
-        for (int i = 1; i < 8; ++i) s.x += red[i][lane].x, s.y += red[i][lane].y, s.z += red[i][lane].z, s.w += red[i][lane].w;
-        float* p = part + (int64_t)blockIdx.x * 4 * A.c + j;
-        p[0] = s.x, p[A.c] = s.y, p[2 * (int64_t)A.c] = s.z, p[3 * (int64_t)A.c] = s.w;
-    }
 }
 
 // ------------------------------------------------------------------------------------------------ rows that registers hold at once
@@ -875,6 +731,202 @@ __global__ void __launch_bounds__(512, 1) rn_bwd_ring_kernel(const RnArgs A, int
     put_sums<WIDE>(A, C, T, V, part, reinterpret_cast<float*>(ring), kRingWarps);
 }
 
+// ------------------------------------------------------------------------------------------------ longer rows
+// Rows of any length, a block's threads with eight values each at a time, read again for each sum (from L1 or L2).
+template <bool VEC>
+__device__ __forceinline__ Cols<VEC> cols_at(int c, int first, int lanes, int lane) {
+    Cols<VEC> C;
+    C.c = c, C.T = lanes, C.t = VEC ? first / 8 + lane : first + lane;
+    return C;
+}
+__device__ __forceinline__ void normed(uint64_t (&v)[4], float mean, float rstd) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul2(add2(v[e], both(-mean)), both(rstd));
+}
+template <bool VEC>
+__device__ __forceinline__ void keep_own(const Cols<VEC>& C, uint64_t (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a, b;
+        apart(v[e], a, b);
+        v[e] = two(C.has(2 * e) ? a : 0.f, C.has(2 * e + 1) ? b : 0.f);
+    }
+}
+
+template <typename S, typename F, bool VEC>
+__global__ void __launch_bounds__(kThreads) rn_fwd_long_kernel(const RnArgs A, const S* x, const F* f, S* r, F* h, float4* stats) {
+    __shared__ float2 red[kThreads / 32];
+    constexpr int kStep = 8 * kThreads;
+    for (int64_t i = blockIdx.x; i < A.rows; i += gridDim.x) {
+        const int64_t o = i * A.c, sample = i / A.per;
+        float2 sf = make_float2(0.f, 1.f), sr = sf;
+        // r's values from column j0 on, f's normalised with sf
+        auto value = [&](const Cols<VEC>& C, uint64_t (&v)[4]) {
+            unpack(load8(x, o, C), v);
+            if (!f) return;
+            uint64_t w[4];
+            unpack(load8(f, o, C), w);
+            normed(w, sf.x, sf.y);
+            const FwdVectors V(A, C, sample);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = add2(v[e], fma2(V.a[e], w[e], V.b[e]));
+        };
+        auto stats_of = [&](int kind, auto get, float2& st) {
+            if (kind == CF_NORM_NONE) return;
+            float mean = 0.f, s = 0.f;
+            for (int pass = kind == CF_NORM_LAYER ? 0 : 1; pass < 2; ++pass) {
+                s = 0.f;
+                for (int j0 = 0; j0 < A.c; j0 += kStep) {
+                    const Cols<VEC> C = cols_at<VEC>(A.c, j0, kThreads, threadIdx.x);
+                    uint64_t v[4], q = 0;
+                    get(C, v);
+                    if (pass == 0) {
+                        s += total(add2(add2(v[0], v[1]), add2(v[2], v[3])));
+                        continue;
+                    }
+                    normed(v, mean, 1.f);
+                    keep_own(C, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q = fma2(v[e], v[e], q);
+                    s += total(q);
+                }
+                s = block_sum(s, 0.f, red).x * A.inv_c;
+                if (pass == 0) mean = s;
+            }
+            st = make_float2(mean, rsqrtf(s + A.eps));
+        };
+        if (f) stats_of(A.post, [&](const Cols<VEC>& C, uint64_t (&v)[4]) { unpack(load8(f, o, C), v); }, sf);
+        stats_of(A.pre, value, sr);
+        __syncthreads();  // all have read the row before r, which may be x, is written
+        for (int j0 = 0; j0 < A.c; j0 += kStep) {
+            const Cols<VEC> C = cols_at<VEC>(A.c, j0, kThreads, threadIdx.x);
+            uint64_t v[4];
+            value(C, v);
+            if (r) store8(r, o, C, v);
+            if (h) {
+                const FwdVectors V(A, C, sample);
+                normed(v, sr.x, sr.y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], V.g[e], V.beta[e]);
+                store8(h, o, C, v);
+            }
+        }
+        if (stats && threadIdx.x == 0) stats[i] = make_float4(sf.x, sf.y, sr.x, sr.y);
+    }
+}
+
+// dx of eight values of a row, from m = (mean u, mean u rh) (0, 0 and no norm: dr).
+template <typename S, typename F, bool VEC>
+__device__ __forceinline__ void dx8(const RnArgs& A, const Cols<VEC>& C, int64_t o, const S* r, const F* dh, const S* dr, const float4& st, float2 m,
+                                    const uint64_t (&g)[4], uint64_t (&d)[4], uint64_t (&rh)[4], uint64_t (&u)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = rh[e] = u[e] = 0;
+    if (dr) unpack(load8(dr, o, C), d);
+    if (A.pre == CF_NORM_NONE) return;
+    unpack(load8(r, o, C), rh);
+    unpack(load8(dh, o, C), u);
+    normed(rh, st.z, st.w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = fma2(both(st.w), fma2(rh[e], both(-m.y), fma2(u[e], g[e], both(-m.x))), d[e]);
+}
+
+// The means that a row's gradients take.
+template <typename S, typename F, bool VEC>
+__global__ void __launch_bounds__(kThreads) rn_bwd_rows_kernel(const RnArgs A, const F* f, const S* r, const float4* stats, const F* dh, const S* dr,
+                                                               float4* means) {
+    __shared__ float2 red[kThreads / 32];
+    constexpr int kStep = 8 * kThreads;
+    for (int64_t i = blockIdx.x; i < A.rows; i += gridDim.x) {
+        const int64_t o = i * A.c, sample = i / A.per;
+        const float4 st = stats[i];
+        float2 m = make_float2(0.f, 0.f), n = m;
+        uint64_t d[4], rh[4], u[4];
+        if (A.pre != CF_NORM_NONE) {
+            for (int j0 = 0; j0 < A.c; j0 += kStep) {
+                const Cols<VEC> C = cols_at<VEC>(A.c, j0, kThreads, threadIdx.x);
+                const BwdVectors V(A, C, sample);
+                dx8(A, C, o, r, dh, static_cast<const S*>(nullptr), st, m, V.g, d, rh, u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t t = mul2(u[e], V.g[e]);
+                    m.x += total(t), m.y += total(mul2(t, rh[e]));
+                }
+            }
+            m = block_sum(m.x, m.y, red);
+            m.x = A.pre == CF_NORM_LAYER ? m.x * A.inv_c : 0.f;
+            m.y *= A.inv_c;
+        }
+        if (A.post != CF_NORM_NONE) {
+            for (int j0 = 0; j0 < A.c; j0 += kStep) {
+                const Cols<VEC> C = cols_at<VEC>(A.c, j0, kThreads, threadIdx.x);
+                const BwdVectors V(A, C, sample);
+                uint64_t w[4];
+                dx8(A, C, o, r, dh, dr, st, m, V.g, d, rh, u);
+                unpack(load8(f, o, C), w);
+                normed(w, st.x, st.y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t t = mul2(d[e], V.a[e]);
+                    n.x += total(t), n.y += total(mul2(t, w[e]));
+                }
+            }
+            n = block_sum(n.x, n.y, red);
+            n.x = A.post == CF_NORM_LAYER ? n.x * A.inv_c : 0.f;
+            n.y *= A.inv_c;
+        }
+        if (threadIdx.x == 0) means[i] = make_float4(m.x, m.y, n.x, n.y);
+    }
+}
+
+// dx, df and the chunk's sums over rows, from the rows' means: 256 columns to a block, a row to a warp.
+template <typename S, typename F, bool VEC>
+__global__ void __launch_bounds__(kThreads) rn_bwd_cols_kernel(const RnArgs A, const F* f, const S* r, const float4* stats, const F* dh, const S* dr,
+                                                               const float4* means, S* dx, F* df, float* part) {
+    __shared__ float all[kThreads / 32][256];
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const Cols<VEC> C = cols_at<VEC>(A.c, blockIdx.y * 256, 32, lane);
+    const int64_t sample = blockIdx.x / A.chunks;
+    const int64_t from = sample * A.per + (blockIdx.x - sample * A.chunks) * A.chunk;
+    const int64_t to = min(min(from + A.chunk, (sample + 1) * A.per), A.rows);
+    BwdVectors V(A, C, sample);
+    for (int64_t i = from + q; i < to; i += kThreads / 32) {
+        const int64_t o = i * A.c;
+        const float4 st = stats[i], m = means[i];
+        uint64_t d[4], rh[4], u[4], w[4] = {};
+        if (f) unpack(load8(f, o, C), w);
+        dx8(A, C, o, r, dh, dr, st, make_float2(m.x, m.y), V.g, d, rh, u);
+        normed(w, st.x, st.y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            V.sc[e] = fma2(u[e], rh[e], V.sc[e]), V.sd[e] = add2(V.sd[e], u[e]);
+            V.sa[e] = fma2(d[e], w[e], V.sa[e]), V.sb[e] = add2(V.sb[e], d[e]);
+        }
+        if (dx) store8(dx, o, C, d);
+        if (df) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[e] = mul2(d[e], V.a[e]);
+                if (A.post != CF_NORM_NONE) d[e] = mul2(both(st.y), fma2(w[e], both(-m.w), add2(d[e], both(-m.z))));
+            }
+            store8(df, o, C, d);
+        }
+    }
+    auto put = [&](const uint64_t (&p)[4], int which) {
+        float v[8];
+        spread(p, v);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) all[q][VEC ? 8 * lane + e : lane + 32 * e] = v[e];
+        __syncthreads();
+        const int j = blockIdx.y * 256 + threadIdx.x;
+        if (j >= A.c) return;
+        float s = 0.f;
+        for (int k = 0; k < kThreads / 32; ++k) s += all[k][threadIdx.x];
+        part[(int64_t)blockIdx.x * 4 * A.c + (int64_t)which * A.c + j] = s;
+    };
+    put(V.sa, 0), put(V.sb, 1), put(V.sc, 2), put(V.sd, 3);
+}
+
 struct RnGrads {
     float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
 };
@@ -1042,7 +1094,7 @@ RnArgs plan_bwd(const cf_residual_norm_desc* d) {
     if (T)
         cut_rows(A, T, 2);
     else
-        cut(A, std::max(1, kPlanSms * 8 * 32 / A.c), 8);
+        cut(A, std::max(1, kPlanSms * 4 * 256 / A.c), 8);
     return A;
 }
 
@@ -1123,8 +1175,8 @@ cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x,
             kernel<<<blocks, T <= 32 ? kThreads : T, 0, ctx.stream>>>(A, T, xs, fs, static_cast<S*>(r), static_cast<F*>(h), st4);
             return status_of();
         }
-        rn_fwd_long_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(
-            A, static_cast<const S*>(x), static_cast<const F*>(f), static_cast<S*>(r), static_cast<F*>(h), reinterpret_cast<float4*>(stats));
+        auto kernel = A.c % 8 == 0 ? rn_fwd_long_kernel<S, F, true> : rn_fwd_long_kernel<S, F, false>;
+        kernel<<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(A, xs, fs, static_cast<S*>(r), static_cast<F*>(h), st4);
         return status_of();
     });
 }
@@ -1182,10 +1234,12 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
             kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? kThreads : T, 0, ctx.stream>>>(A, T, fs, rs, st4, dhs, drs, static_cast<S*>(dx),
                                                                                                static_cast<F*>(df), sums ? L.part : nullptr);
         } else {
-            rn_bwd_rows_kernel<S, F><<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(A, fs, rs, st4, dhs, drs,
-                                                                                                                       L.means);
+            const bool vec = A.c % 8 == 0;
+            auto rows = vec ? rn_bwd_rows_kernel<S, F, true> : rn_bwd_rows_kernel<S, F, false>;
+            auto cols = vec ? rn_bwd_cols_kernel<S, F, true> : rn_bwd_cols_kernel<S, F, false>;
+            rows<<<(unsigned)std::min<int64_t>(A.rows, 8 * ctx.num_sms), kThreads, 0, ctx.stream>>>(A, fs, rs, st4, dhs, drs, L.means);
             if (const cf_status st = status_of(); st != CF_OK) return st;
-            rn_bwd_cols_kernel<S, F><<<dim3((unsigned)(A.samples * A.chunks), tiles), kThreads, 0, ctx.stream>>>(
+            cols<<<dim3((unsigned)(A.samples * A.chunks), (A.c + 255) / 256), kThreads, 0, ctx.stream>>>(
                 A, fs, rs, st4, dhs, drs, L.means, static_cast<S*>(dx), static_cast<F*>(df), L.part);
         }
         if (const cf_status st = status_of(); st != CF_OK || !sums) return st;

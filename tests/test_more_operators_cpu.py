@@ -243,3 +243,47 @@ def test_clip_refusals(cf):
         assert adam(params(), **kw) == bad, kw
     assert cf.cf_clip_adam_step(params(), None, 32, 64, 1 << 30, check=False) == bad
     assert adam(params(), size=cf.cf_clip_adam_workspace_size(params()) - 1) == cf.CF_ERR_WORKSPACE
+
+
+# ------------------------------------------------------------------------------------------------- launches that fail, by a fake runtime
+CALLS = """
+def grads(n):
+    out = (cf.cf_grad * n)()
+    for p in out:
+        p.g, p.count, p.dtype = 4096, 5000, cf.CF_DT_F32
+    return out
+def norm(n=3):
+    g = grads(n)
+    return cf.cf_grad_norm(g, 1.0, 256, 512, cf.cf_grad_workspace_size(g), check=False)
+def clip(n=3):
+    g = grads(n)
+    return cf.cf_clip_grads(g, 1.0, 256, 512, cf.cf_grad_workspace_size(g), check=False)
+def adam(n=3, max_norm=1.0):
+    out = (cf.cf_adam_param * n)()
+    for p in out:
+        p.w, p.g, p.m, p.v, p.count = 4096, 8192, 12288, 16384, 3000
+    h = cf.cf_adam_hyper(1e-3, 0.9, 0.999, 1e-8, 0.0, max_norm, 1)
+    return cf.cf_clip_adam_step(out, h, 256, 512, cf.cf_clip_adam_workspace_size(out), check=False)
+def rn(rows, c, back, each=0, per=0, sums=True):
+    d = cf.cf_residual_norm_desc(rows, c, cf.CF_NORM_RMS, cf.CF_NORM_RMS, 1e-5, 1.0, 0, 0, each, per)
+    if not back:
+        return cf.cf_residual_norm_fwd(d, 256, 512, None, 768, 1024, None, check=False)
+    g = cf.cf_residual_norm_vectors(gate=2048) if sums else None
+    return cf.cf_residual_norm_bwd(d, 256, 512, None, 768, 1024, 1280, 1536, 1792, g, 4096, cf.cf_residual_norm_workspace_size(d), check=False)
+"""
+
+
+@pytest.mark.parametrize("call,launches", [("norm()", 2), ("clip()", 2), ("adam()", 2), ("adam(3, 0.0)", 1), ("norm(2000)", 3), ("clip(2000)", 4),
+                                           ("adam(1000)", 4), ("norm(0)", 1), ("rn(64, 256, 0)", 1), ("rn(64, 256, 1)", 2), ("rn(64, 256, 1, sums=False)", 1),
+                                           ("rn(64, 256, 1, 1, 32)", 3), ("rn(100000, 128, 0)", 1), ("rn(100000, 128, 1)", 2), ("rn(64, 9000, 0)", 1),
+                                           ("rn(64, 9000, 1)", 3)])
+def test_a_launch_that_fails_ends_the_call_and_is_reported_once(tmp_path, call, launches):
+    """The call says CF_ERR_CUDA, enqueues nothing more, and does not leave the error behind for the next one."""
+    from test_operators_cpu import _with_fake_runtime
+    script = CALLS + f"fake.fake_set(1, 0)\nprint({call}, fake.fake_launches())\n"
+    for at in range(1, launches + 1):
+        script += f"fake.fake_set(1, {at})\nprint({call}, fake.fake_launches())\nfake.fake_set(1, 0)\nprint({call})\n"
+    want = ["0", str(launches)]
+    for at in range(1, launches + 1):
+        want += ["4", str(at), "0"]
+    assert _with_fake_runtime(tmp_path, script) == want
