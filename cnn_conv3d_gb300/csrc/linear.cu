@@ -140,10 +140,14 @@ Product plan_of(const cf_linear_desc* d, int op) {
     G.tm = (int)best.tm, G.tn = (int)best.tn, G.bn = best.bn;
     G.stage_bytes = best.stage_bytes;
     G.a_box = 128, G.b_box = best.pair ? best.bn / 2 : best.bn;
+    // fp32 results of more blocks than the tensor cores may sum
+    G.seg = 24;
+    const int64_t most = std::max<int64_t>(best.whole ? G.nkb : 0, best.whole < best.tm * best.tn ? std::min<int64_t>(best.share, G.nkb) : 0);
+    P.plan.sums = (op == OP_WGRAD || d->dtype == CF_DT_F32) && most > G.seg;
     // Narrow tiles of many rows: as many side by side as the accumulator holds, so that what a tile takes besides its products and
     // stores is taken less often; with rounds enough left to even out.
     G.sub = 1;
-    if (!best.pair && !P.plan.swap && op != OP_WGRAD && best.tn == 1 && best.whole == best.tm) {
+    if (!best.pair && !P.plan.swap && !P.plan.sums && best.tn == 1 && best.whole == best.tm) {
         while (2 * G.sub * best.bn <= 256 && best.tm >= 8 * G.sub * best.units) G.sub *= 2;
         best.tm = over(G.m, 128 * G.sub), best.whole = best.tm;
         G.tm = (int)best.tm;
@@ -190,9 +194,9 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     LinMaps M{};
     uint32_t room = kLinSmem - (uint32_t)sizeof(LinShared) - (OP == OP_WGRAD ? kLinOnes : 0);
-    const bool few = (int64_t)G.tm * G.tn <= 2 * G.units && G.bn > 128;
+    const bool sums = P.plan.sums, few = (int64_t)G.tm * G.tn <= 2 * G.units && G.bn > 128;
     LinStage& S = G.st;
-    S.sets = few ? 1 : 2, S.turns = few ? 4 : 2;
+    S.sets = few || sums ? 1 : 2, S.turns = few && !sums ? 4 : 2, S.gw = 32;
     if (!P.plan.swap) {
         if (OP == OP_WGRAD && E.accumulate) E.add = E.out;
         const bool aux = E.pre_in || E.pre_out;
@@ -204,7 +208,7 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
         // All warps, on one tile or on two in turn, where the epilogue is much of a tile's time and two stages fit beside their room;
         // else half of them, and more stages.
         const uint32_t pass = S.out_bytes + S.aux_bytes + (OP == OP_FWD ? kLinBias : 0);
-        const bool all = G.nkb <= 16 && room >= kLinEpiWarps * pass + 2 * G.stage_bytes;
+        const bool all = !sums && G.nkb <= 16 && room >= kLinEpiWarps * pass + 2 * G.stage_bytes;
         S.sets = all && !few ? 2 : 1, S.turns = all && few ? 4 : 2;
         room -= 4 * S.sets * S.turns * pass;
         auto rows_map = [&](CUtensorMap* m, const void* p, bool f32) {

@@ -7,14 +7,21 @@
 // or the two exchanged (SWAP) where that side is narrow: few rows in the forward and the backward data, so that the weights' rows
 // fill the 128 lanes of a tile and the rows are its columns, and a narrow k in the backward weight.
 //
-// A CTA is a TMA warp, an issuing thread and sixteen epilogue warps.  Operands come in stages of 64 of the contracted axis (128-byte
+// A CTA is a TMA warp, an issuing thread and sixteen epilogue warps (eight, see below).  Operands come in stages of 64 of the contracted axis (128-byte
 // rows, swizzled); tiles are 128 rows by up to 256 columns, or 256 by 256 on a pair of CTAs with one instruction for both, each CTA
 // fetching half of either side: then a stage costs 64 bytes of L2 a cycle and SM, where a lone CTA's would cost 96 of the about 70
 // that it gives.  The accumulator is double: the epilogue of a tile runs under the products of the next.
 //
+// The tensor cores cut off what an fp32 sum cannot hold: about 1.7e-8 of the result for each step of 16 of the contracted axis where
+// the values' signs are mixed (weights of 2048 x 8192 from 16384 rows: 1.7e-5 off, where sums in fp32 that round are 1.4e-6).  Where the
+// result is fp32 they therefore sum 24 blocks of the axis at a time, and the epilogue warps, then eight with the registers for it, add
+// these sums up, rounding, under the next blocks' products (SUMS): 1.5e-6, and 393 us in place of 362; 16 blocks took 406, 32 390.
+//
 // Tiles are dealt out whole, and what is left over for a last, uneven round (or all of it, where there are fewer tiles than CTAs) in
 // even shares of 64-blocks of the contracted axis; tiles that are cut leave fp32 parts, joined in order by a second launch.
 #pragma once
+
+#include <type_traits>
 
 #include "cf_internal.h"
 #include "cf_pair.cuh"
@@ -63,13 +70,15 @@ struct LinGemm {
     int share;               // a unit's blocks of the others
     int64_t rest;            // all blocks of the others
     int units;               // CTAs or pairs
+    int seg;                 // SUMS: blocks that the tensor cores sum
     float *part, *dpart;     // parts of cut tiles: a unit's two slots of 128 x bn values a CTA; of db, 256 values a slot
     int* status;
     uint64_t wait_ns;
 };
 
 constexpr int kLinEpiWarps = 16;
-constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
+constexpr int kLinSumWarps = 8;  // with SUMS
+constexpr int threads_of_linear(bool sums) { return 64 + 32 * (sums ? kLinSumWarps : kLinEpiWarps); }
 constexpr int kLinMostStages = 10;
 constexpr uint32_t kLinOnes = 16 << 10;             // 128 rows of 64 ones (backward weight)
 constexpr uint32_t kLinSmem = 232448;               // all of it: ones, passes and stages, then LinShared
@@ -359,6 +368,16 @@ struct LinShared {
     int abort;
 };
 static_assert(sizeof(LinShared) % 16 == 0, "the bias is before it");
+// The accumulators in turn, and how often each has been filled.
+struct Accumulators {
+    uint32_t uses[2] = {0, 0};
+    int flip = 0;
+    __device__ __forceinline__ int next(bool sums) const { return sums ? 0 : flip; }
+    __device__ __forceinline__ void used(int acc, bool sums) {
+        ++uses[acc];
+        if (!sums) flip ^= 1;
+    }
+};
 struct LinRing {
     int stage = 0;
     uint32_t bits = 0, issued = 0;
@@ -369,8 +388,8 @@ struct LinRing {
     }
 };
 
-// The sums of dz's rows come from products with ones: they are taken with the first tile across the other side, into the
-// accumulator that is not the tile's, which therefore has to be free, and is only free again when the tile's epilogue is through.
+// The sums of dz's rows come from products with ones: they are taken with the first tile across the other side, into the second
+// accumulator, while all of the tile's own products go to the first.
 template <int OP, bool SWAP>
 __device__ __forceinline__ bool takes_sums(const LinEpi& E, const LinItem& s) {
     return OP == OP_WGRAD && E.db && (SWAP ? s.mt : s.nt) == 0;
@@ -415,10 +434,11 @@ struct LinMaps {
 };
 
 // TMA: S.tma, which a kernel of both would pay for with registers.
-template <bool PAIR, int OP, bool SWAP, bool TMA>
-__global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ LinMaps M, const __grid_constant__ LinGemm G,
+template <bool PAIR, int OP, bool SWAP, bool TMA, bool SUMS>
+__global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel(const __grid_constant__ LinMaps M, const __grid_constant__ LinGemm G,
                                                                      const __grid_constant__ LinEpi E) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
+    constexpr int kLinThreads = threads_of_linear(SUMS);
     if (smem_u32(smem_raw) & 1023) {  // the swizzle goes by the address, and there is no room to move in
         if (threadIdx.x == 0) atomicCAS(G.status, 0, (int)WAIT_PROBE);
         return;
@@ -521,9 +541,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         const uint64_t one = sdesc(smem_u32(ones), 16, 1024, SWZ_128B);
         const uint32_t astep = G.a_mn ? 2048 : 32, bstep = G.b_mn ? 2048 : 32;
         const uint32_t alead = G.a_mn ? 8192 : 16, blead = G.b_mn ? 8192 : 16;
+        Accumulators A;
         bool alone = false;  // the tile before took sums
         bool ok = true;
-        for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
+        auto free_of = [&](int acc) {
+            return A.uses[acc] == 0 || mbar_wait(&sh.tempty[acc], (A.uses[acc] - 1) & 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
+        };
+        while (ok && way.next(G, unit, s)) {
             if (second) {
                 for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
                     ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
@@ -533,48 +557,51 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 }
                 continue;
             }
-            const uint32_t acc = local & 1, use = local >> 1, d = sh.tmem + acc * 256, d1 = sh.tmem + (acc ^ 1) * 256;
-            ok = mbar_wait(&sh.tempty[acc], (use & 1) ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
             const bool sums = takes_sums<OP, SWAP>(E, s);
-            if (ok && (sums || alone) && local)  // the tile before is through: accumulator acc ^ 1, its use (local - 1) / 2
-                ok = mbar_wait(&sh.tempty[acc ^ 1], ((local - 1) >> 1) & 1, &sh.abort, G.wait_ns, G.status, WAIT_MMA_TMEM_EMPTY);
+            if (sums || alone) ok = free_of(0) && free_of(1);
             alone = sums;
-            tc_fence_after();
-            const int parts = parts_of<PAIR>(G, s);
-            for (int part = 0; ok && part < parts; ++part) {
-                const uint32_t dp = d + part * G.bn;
-                for (int kb = s.kb0; ok && kb < s.kb1; ++kb) {
-                    ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t as = smem_u32(ring + R.stage * G.stage_bytes), bs = as + 16384;
+            const int parts = parts_of<PAIR>(G, s), seg = SUMS ? G.seg : s.kb1 - s.kb0;
+            for (int k0 = s.kb0; ok && k0 < s.kb1; k0 += seg) {
+                const int acc = A.next(sums), k1 = min(k0 + seg, s.kb1);
+                const uint32_t d = sh.tmem + acc * 256, d1 = sh.tmem + 256;
+                ok = free_of(acc);
+                tc_fence_after();
+                for (int part = 0; ok && part < parts; ++part) {
+                    const uint32_t dp = d + part * G.bn;
+                    for (int kb = k0; ok && kb < k1; ++kb) {
+                        ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t as = smem_u32(ring + R.stage * G.stage_bytes), bs = as + 16384;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t ad = sdesc(as + k * astep, alead, 1024, SWZ_128B), bd = sdesc(bs + k * bstep, blead, 1024, SWZ_128B);
-                        const uint32_t more = kb > s.kb0 || k > 0;
-                        if (PAIR)
-                            umma_pair(dp, ad, bd, idesc, more);
-                        else
-                            umma_bf16(dp, ad, bd, idesc, more);
-                        if (OP == OP_WGRAD && sums) {
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t ad = sdesc(as + k * astep, alead, 1024, SWZ_128B), bd = sdesc(bs + k * bstep, blead, 1024, SWZ_128B);
+                            const uint32_t more = kb > k0 || k > 0;
                             if (PAIR)
-                                umma_pair(d1, ad, one, idesc1, more);
+                                umma_pair(dp, ad, bd, idesc, more);
                             else
-                                umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, more);
+                                umma_bf16(dp, ad, bd, idesc, more);
+                            if (OP == OP_WGRAD && sums) {
+                                if (PAIR)
+                                    umma_pair(d1, ad, one, idesc1, kb > s.kb0 || k > 0);
+                                else
+                                    umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, kb > s.kb0 || k > 0);
+                            }
                         }
+                        if (PAIR)
+                            commit_pair(&sh.empty[R.stage]);
+                        else
+                            umma_commit(&sh.empty[R.stage]);
+                        R.next(G.stages);
                     }
-                    if (PAIR)
-                        commit_pair(&sh.empty[R.stage]);
-                    else
-                        umma_commit(&sh.empty[R.stage]);
-                    R.next(G.stages);
                 }
+                if (!ok) break;
+                if (PAIR)
+                    commit_pair(&sh.tfull[acc]);
+                else
+                    umma_commit(&sh.tfull[acc]);
+                A.used(acc, sums);
             }
-            if (!ok) break;
-            if (PAIR)
-                commit_pair(&sh.tfull[acc]);
-            else
-                umma_commit(&sh.tfull[acc]);
         }
     } else if (warp >= 2) {
         // a pass of columns at a time, a set's warps of a quarter of the lanes in turn, 16 columns of the thread's lane at once
@@ -609,10 +636,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
             b0 = j + lane < E.cols ? E.bias[j + lane] : 0.f;
             b1 = j + 32 + lane < E.cols ? E.bias[j + 32 + lane] : 0.f;
         };
-        for (uint32_t local = 0; ok && way.next(G, unit, s); ++local) {
-            const uint32_t acc = local & 1, use = local >> 1;
-            if (S.sets == 2 && (int)acc != set) continue;
-            const uint32_t tm = sh.tmem + acc * 256 + ((uint32_t)(32 * q) << 16), tm1 = sh.tmem + (acc ^ 1) * 256 + ((uint32_t)(32 * q) << 16);
+        // SUMS: the warp's group g of 32 columns, of four
+        auto group_of = [&](int g) { return S.gw == 64 ? 64 * (turn + 2 * (g >> 1)) + 32 * (g & 1) : 32 * (turn + 2 * g); };
+        Accumulators A;
+        while (ok && way.next(G, unit, s)) {
+            const bool sums = takes_sums<OP, SWAP>(E, s);
+            int acc = A.next(sums);
+            if (S.sets == 2 && acc != set) {
+                A.used(acc, sums);
+                continue;
+            }
             const int64_t i = (int64_t)s.mt * (PAIR ? 256 : 128 * G.sub) + 128 * rank + r, j0 = (int64_t)s.nt * G.bn;
             const int across = (G.bn + S.gw - 1) / S.gw, most = across * parts_of<PAIR>(G, s);  // passes
             float* part = s.slot < 0 ? nullptr : G.part + ((int64_t)s.slot * (PAIR ? 2 : 1) + rank) * 128 * G.bn;
@@ -625,11 +658,72 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 __syncwarp();
             };
             if (!part && turn < most) copy_in(i - lane + 128 * (turn / across), (int)j0 + turn % across * S.gw);
-            ok = mbar_wait(&sh.tfull[acc], use & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
-            if (!ok) break;
-            tc_fence_after();
+            const uint32_t lanes = (uint32_t)(32 * q) << 16, tm1 = sh.tmem + 256 + lanes;
+            uint32_t tm = 0;
+            auto filled = [&]() {
+                acc = A.next(sums);
+                tm = sh.tmem + acc * 256 + lanes;
+                ok = mbar_wait(&sh.tfull[acc], A.uses[acc] & 1, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL);
+                tc_fence_after();
+                return ok;
+            };
+            auto emptied = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR)
+                        arrive_first(&sh.tempty[acc]);
+                    else
+                        mbar_arrive(&sh.tempty[acc]);
+                }
+                A.used(acc, sums);
+            };
+            if (SUMS && s.kb1 - s.kb0 > G.seg) {
+                // all blocks' sums, the last written back to where the epilogue finds a tile's
+                uint64_t v[4][16];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[g][e] = 0;
+                for (int k0 = s.kb0; k0 < s.kb1; k0 += G.seg) {
+                    if (!filled()) break;
+                    const bool last = k0 + G.seg >= s.kb1;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int c = group_of(g);
+                        if (c >= G.bn) continue;
+#pragma unroll
+                        for (int h = 0; h < 16; h += 8) {
+                            uint32_t u[32];  // the first 16
+                            tmem_ld16(tm + c + 2 * h, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                v[g][h + e] = add2(v[g][h + e], two(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])));
+                            if (!last) continue;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float a, b;
+                                apart(v[g][h + e], a, b);
+                                u[2 * e] = __float_as_uint(a), u[2 * e + 1] = __float_as_uint(b);
+                            }
+                            tmem_st16(tm + c + 2 * h, u);
+                        }
+                    }
+                    if (last)
+                        tmem_st_wait();
+                    else
+                        emptied();
+                }
+                if (!ok) break;
+            } else if (!filled()) {
+                break;
+            }
             if (SWAP || part) {
-                for (int c = 16 * turn; c < G.bn; c += 16 * S.turns) {
+                for (int k = 0;; ++k) {
+                    const int c = SUMS ? group_of(k >> 1) + 16 * (k & 1) : 16 * (turn + S.turns * k);
+                    if (SUMS ? k == 8 : c >= G.bn) break;
+                    if (c >= G.bn) continue;
                     uint32_t u[32];
                     tmem_ld16(tm + c, u);
                     tmem_ld_wait();
@@ -644,7 +738,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                     } else if (i < G.m) {
                         finish_column<OP>(E, j0 + c, (int)i, v);
                     }
-                    if (OP == OP_WGRAD && SWAP && takes_sums<OP, SWAP>(E, s)) {
+                    if (OP == OP_WGRAD && SWAP && sums) {
                         tmem_ld16(tm1 + c, u);
                         tmem_ld_wait();
                         if (r == 0) {
@@ -709,7 +803,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 }
                 if (!ok) break;
             }
-            if (OP == OP_WGRAD && !SWAP && turn == 0 && takes_sums<OP, SWAP>(E, s)) {
+            if (OP == OP_WGRAD && !SWAP && turn == 0 && sums) {
                 uint32_t u[32];
                 tmem_ld16(tm1, u);
                 tmem_ld_wait();
@@ -719,14 +813,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
                 else if (i < G.m)
                     E.db[i] = E.accumulate ? fmaf(E.scale, b, E.db[i]) : E.scale * b;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR)
-                    arrive_first(&sh.tempty[acc]);
-                else
-                    mbar_arrive(&sh.tempty[acc]);
-            }
+            emptied();
         }
         if (lane == 0) bulk_wait_read();  // shared memory outlives the stores' reads; the stores end with the grid
         if (!SWAP && lane == 0 && *(volatile int*)&sh.abort)  // loads in flight end before the CTA leaves
@@ -819,7 +906,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 struct LinPlan {
     LinGemm g;
     bool pair, swap;
-    bool cut;  // some tile is in parts
+    bool cut;   // some tile is in parts
+    bool sums;  // SUMS
 };
 
 // Both launches of a product; instantiated for each direction in a file of its own.
@@ -828,13 +916,13 @@ cf_status launch_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M
 
 #ifdef CF_LINEAR_OP
 namespace {
-template <bool PAIR, bool SWAP, bool TMA>
+template <bool PAIR, bool SWAP, bool TMA, bool SUMS>
 cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
-    auto kernel = linear_gemm_kernel<PAIR, CF_LINEAR_OP, SWAP, TMA>;
+    auto kernel = linear_gemm_kernel<PAIR, CF_LINEAR_OP, SWAP, TMA, SUMS>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(P.g.units * (PAIR ? 2 : 1)));
-    cfg.blockDim = dim3(kLinThreads);
+    cfg.blockDim = dim3(threads_of_linear(SUMS));
     cfg.dynamicSmemBytes = kLinSmem;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute at[2];
@@ -862,10 +950,13 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, c
 
 template <>
 cf_status launch_linear<CF_LINEAR_OP>(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
-    const bool tma = P.g.st.tma;
-    if (P.pair) return tma ? run_linear<true, false, true>(ctx, P, M, E) : run_linear<true, false, false>(ctx, P, M, E);
-    if (P.swap) return run_linear<false, true, true>(ctx, P, M, E);
-    return tma ? run_linear<false, false, true>(ctx, P, M, E) : run_linear<false, false, false>(ctx, P, M, E);
+    auto run = [&](auto sums) {
+        constexpr bool kSums = decltype(sums)::value;
+        if (P.swap) return run_linear<false, true, true, kSums>(ctx, P, M, E);
+        if (P.pair) return P.g.st.tma ? run_linear<true, false, true, kSums>(ctx, P, M, E) : run_linear<true, false, false, kSums>(ctx, P, M, E);
+        return P.g.st.tma ? run_linear<false, false, true, kSums>(ctx, P, M, E) : run_linear<false, false, false, kSums>(ctx, P, M, E);
+    };
+    return P.sums ? run(std::true_type{}) : run(std::false_type{});
 }
 #endif
 
