@@ -190,12 +190,15 @@ struct RowSum {
                 : "+r"(failed)
                 : "r"(T)
                 : "memory");
+            // up to 16 warps' sums: a lane to each
+            const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < T >> 5; ++i)
+            for (int e = 0; e < N; ++e) v[e] = lane < T >> 5 ? r[lane][e] : 0.f;
+            for (int o = T > 256 ? 8 : T > 128 ? 4 : T > 64 ? 2 : 1; o; o >>= 1)
 #pragma unroll
-                for (int e = 0; e < N; ++e) v[e] += r[i][e];
+                for (int e = 0; e < N; ++e) v[e] += __shfl_xor_sync(~0u, v[e], o);
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = __shfl_sync(~0u, v[e], 0);
         }
     }
 };

@@ -180,6 +180,28 @@ def test_activations_and_types(cf, act, slope, dtype, rows):
     check_dgrad(cf, rng, rows, 96, 136, act, slope, 0.7, dtype)
 
 
+@pytest.mark.parametrize("rows,k,n,op", [(200000, 64, 72, "wgrad"), (9000, 520, 264, "wgrad"), (300, 12000, 264, "fwd"), (40, 12000, 264, "fwd"),
+                                         (700, 136, 9000, "dgrad")])
+def test_long_sums_keep_fp32s_precision(cf, rows, k, n, op):
+    """The tensor cores cut sums off, on average by 2^-24 of them, at each of at most 96 steps of 16 before they are added up in fp32
+    that rounds; a sum of values of mixed signs is on average at most 0.7 of its end: 96 0.7 2^-24 = 4.0e-6 of the result."""
+    rng = np.random.default_rng(20)
+    x, w, dz = rows_of(rng, rows, k), rows_of(rng, n, k), rows_of(rng, rows, n)
+    out = torch.empty({"wgrad": (n, k), "fwd": (rows, n), "dgrad": (rows, k)}[op], device="cuda")
+    d = desc_of(cf, rows, k, n, dtype=F32)
+    ws = workspace(cf, d, {"fwd": 0, "dgrad": 1, "wgrad": 2}[op])
+    if op == "wgrad":
+        cf.cf_linear_wgrad(d, x, dz, out, None, 0, *ws)
+        ref = f64(dz).T @ f64(x)
+    elif op == "fwd":
+        cf.cf_linear_fwd(d, x, w, None, None, out, None, *ws)
+        ref = f64(x) @ f64(w).T
+    else:
+        cf.cf_linear_dgrad(d, dz, w, None, None, out, *ws)
+        ref = f64(dz) @ f64(w)
+    assert np.linalg.norm(f64(out) - ref) <= 4.0e-6 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("residual,pre,bias", [(0, 0, 0), (1, 0, 1), (0, 1, 0), (0, 0, 1)])
 @pytest.mark.parametrize("rows,k,n", [(3, 256, 200), (520, 256, 200)])
 @pytest.mark.parametrize("dtype", [BF, F32])
