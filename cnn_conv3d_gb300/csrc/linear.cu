@@ -49,6 +49,7 @@ cf_status check(const cf_linear_desc* d) {
 int64_t x_pitch(const cf_linear_desc* d) { return d->x_pitch ? d->x_pitch : d->k; }
 int64_t y_pitch(const cf_linear_desc* d) { return d->y_pitch ? d->y_pitch : d->n; }
 
+constexpr int kMostSummed = 24;  // blocks whose sum the tensor cores take for an fp32 result
 constexpr int kPlanSms = 152;  // work is cut for so many SMs: workspaces are laid out without asking the device
 
 // An operand as it lies in memory: `rows` rows of `width` values, the contracted axis along them (K-major) or across.
@@ -76,7 +77,7 @@ bool exchanged(int op, int64_t rows, int64_t k, int64_t n) { return op == OP_WGR
 // A way to cut a product, and about how long it takes.
 struct Shape {
     bool pair;
-    int bn, units, stage_bytes;
+    int bn, units, stage_bytes, split;
     int64_t tm, tn, whole, share;  // tiles dealt out whole; a unit's blocks of the others
     double ns;
 };
@@ -95,7 +96,7 @@ bool shape(const LinGemm& G, bool pair, int bn, bool cut, Shape& t) {
     const double products = 4 / 1.9 * std::max(bn / 2.0, (4096 + 32.0 * bn) / 128), block = std::max(t.stage_bytes / 105.0, products);
     const double epilogue = 1000 + 700 * over(bn, 128), start = pair ? 2700 : 2000, round = pair ? epilogue : 1.3 * epilogue;
     const int64_t tiles = t.tm * t.tn, rounds = tiles / t.units, rem = tiles - rounds * t.units;
-    t.whole = tiles, t.share = 1;
+    t.whole = tiles, t.share = 1, t.split = 0;
     if (!cut) {
         const int64_t most = rounds + (rem > 0);
         t.ns = start + std::max(most * G.nkb * block, (most - 1) * round) + epilogue;
@@ -105,6 +106,19 @@ bool shape(const LinGemm& G, bool pair, int bn, bool cut, Shape& t) {
     if (rem == 0 || t.share >= G.nkb) return false;
     const double bytes = 512.0 * bn, parts = over(rem * G.nkb, t.share) * (pair ? 2 : 1) * bytes;
     t.ns = start + std::max((rounds * G.nkb + t.share) * block, rounds * round) + 500 + bytes / 50 + 3000 + parts / 4000;
+    return true;
+}
+
+// A tile to a cluster of `split` CTAs.  Clusters of four leave some of an SM group idle, so that about 128 CTAs run at a time.
+// 2300 until the first stage is there; 2000, and 4 for each of a tile's columns, to add up; and the epilogue, which where rows are not on
+// the columns goes by 32 columns with their loads' latency.
+bool shape_split(const LinGemm& G, int op, bool swap, int bn, int split, Shape& t) {
+    shape(G, false, bn, false, t);
+    const int64_t tiles = t.tm * t.tn;
+    if (split > G.nkb || tiles * split > (split > 2 ? 128 : 144)) return false;
+    t.split = split;
+    t.ns = 2300 + over(G.nkb, split) * std::max(t.stage_bytes / 105.0, 4 / 1.9 * std::max(bn / 2.0, (4096 + 32.0 * bn) / 128)) + 2000 + 4 * bn +
+           (swap ? 500 : (op == OP_DGRAD ? 1000 : 600) * over(bn / split, 32));
     return true;
 }
 
@@ -133,6 +147,10 @@ Product plan_of(const cf_linear_desc* d, int op) {
             if (bn > 256) continue;
             for (const bool cut : {false, true})
                 if (shape(G, pair, bn, cut, t) && (best.ns == 0 || t.ns < best.ns)) best = t;
+            // of more blocks than the tensor cores may sum for an fp32 result there is no such kernel
+            if (pair || op == OP_WGRAD) continue;
+            for (const int split : {2, 4})
+                if ((d->dtype != CF_DT_F32 || over(G.nkb, split) <= kMostSummed) && shape_split(G, op, P.plan.swap, bn, split, t) && t.ns < best.ns) best = t;
         }
     }
     P.plan.pair = best.pair;
@@ -141,13 +159,14 @@ Product plan_of(const cf_linear_desc* d, int op) {
     G.stage_bytes = best.stage_bytes;
     G.a_box = 128, G.b_box = best.pair ? best.bn / 2 : best.bn;
     // fp32 results of more blocks than the tensor cores may sum
-    G.seg = 24;
+    G.seg = kMostSummed;
+    G.split = best.split;
     const int64_t most = std::max<int64_t>(best.whole ? G.nkb : 0, best.whole < best.tm * best.tn ? std::min<int64_t>(best.share, G.nkb) : 0);
     P.plan.sums = (op == OP_WGRAD || d->dtype == CF_DT_F32) && most > G.seg;
     // Narrow tiles of many rows: as many side by side as the accumulator holds, so that what a tile takes besides its products and
     // stores is taken less often; with rounds enough left to even out.
     G.sub = 1;
-    if (!best.pair && !P.plan.swap && !P.plan.sums && best.tn == 1 && best.whole == best.tm) {
+    if (!best.pair && !best.split && !P.plan.swap && !P.plan.sums && best.tn == 1 && best.whole == best.tm) {
         while (2 * G.sub * best.bn <= 256 && best.tm >= 8 * G.sub * best.units) G.sub *= 2;
         best.tm = over(G.m, 128 * G.sub), best.whole = best.tm;
         G.tm = (int)best.tm;
@@ -197,7 +216,7 @@ cf_status product(const cf_linear_desc* d, const uint16_t* a, const uint16_t* b,
     const bool sums = P.plan.sums, few = (int64_t)G.tm * G.tn <= 2 * G.units && G.bn > 128;
     LinStage& S = G.st;
     S.sets = few || sums ? 1 : 2, S.turns = few && !sums ? 4 : 2, S.gw = 32;
-    if (!P.plan.swap) {
+    if (!P.plan.swap && !G.split) {
         if (OP == OP_WGRAD && E.accumulate) E.add = E.out;
         const bool aux = E.pre_in || E.pre_out;
         S.load_add = E.add != nullptr, S.load_aux = E.pre_in != nullptr;

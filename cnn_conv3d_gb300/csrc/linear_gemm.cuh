@@ -17,7 +17,9 @@
 // result is fp32 they therefore sum 24 blocks of the axis at a time, and the epilogue warps, then eight with the registers for it, add
 // these sums up, rounding, under the next blocks' products (SUMS): 1.5e-6, and 393 us in place of 362; 16 blocks took 406, 32 390.
 //
-// Tiles are dealt out whole, and what is left over for a last, uneven round (or all of it, where there are fewer tiles than CTAs) in
+// Where there are fewer tiles than CTAs, a cluster may take each, its CTAs even shares of the contracted axis, whose sums they add up
+// through distributed shared memory, each CTA of some columns (linear_split_kernel).  Otherwise
+// tiles are dealt out whole, and what is left over for a last, uneven round (or all of it, where there are fewer tiles than CTAs) in
 // even shares of 64-blocks of the contracted axis; tiles that are cut leave fp32 parts, joined in order by a second launch.
 #pragma once
 
@@ -71,6 +73,7 @@ struct LinGemm {
     int64_t rest;            // all blocks of the others
     int units;               // CTAs or pairs
     int seg;                 // SUMS: blocks that the tensor cores sum
+    int split;               // CTAs of a cluster that share a tile (linear_split_kernel), or 0
     float *part, *dpart;     // parts of cut tiles: a unit's two slots of 128 x bn values a CTA; of db, 256 values a slot
     int* status;
     uint64_t wait_ns;
@@ -847,6 +850,160 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
     }
 }
 
+// A tile to a cluster of two or four CTAs, which share the blocks of the contracted axis: each leaves its sums in its shared memory, four
+// columns of all 128 rows in turn, and of some of the columns adds all CTAs', in their order, and takes the epilogue.  8 x 2048 -> 2048
+// takes 6.8 us so, and 7.7 with parts in memory and a second launch (10.6 in clusters of eight, which are late to be placed);
+// 128 x 4096 -> 4096 11.9 and 16.7; 200 x 4096 -> 4096 17.4 and 23.
+constexpr int kSplitThreads = 64 + 32 * 8;
+constexpr int kMostSplit = 4;
+template <int OP, bool SWAP>
+__global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __grid_constant__ LinMaps M, const __grid_constant__ LinGemm G,
+                                                                       const __grid_constant__ LinEpi E) {
+    extern __shared__ __align__(1024) uint8_t ring[];
+    LinShared& sh = *reinterpret_cast<LinShared*>(ring + kLinSmem - sizeof(LinShared));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cluster_rank(), C = G.split;
+    // the swizzle goes by the address: all CTAs' are alike, and leave alike
+    if (smem_u32(ring) & 1023) {
+        if (threadIdx.x == 0) atomicCAS(G.status, 0, (int)WAIT_PROBE);
+        return;
+    }
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&M.a);
+            tma_prefetch_desc(&M.b);
+            sh.abort = 0;
+            mbar_init(&sh.tfull[0], 1);
+            mbar_init(&sh.drain, 1);
+        }
+        if (lane < kLinMostStages) mbar_init(&sh.full[lane], 1), mbar_init(&sh.empty[lane], 1);
+        fence_barrier_init();
+        __syncwarp();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    int mt, nt;
+    tile_of(G, blockIdx.x / C, mt, nt);
+    const int kb0 = (int)((int64_t)G.nkb * rank / C), kb1 = (int)((int64_t)G.nkb * (rank + 1) / C);
+    const int64_t m0 = (int64_t)mt * 128, n0 = (int64_t)nt * G.bn;
+    LinRing R;
+    if (warp == 0) {
+        const bool isb = lane >= 2;
+        const int q = isb ? lane - 2 : lane;
+        const int na = G.a_mn ? (int)min((int64_t)2, (G.m - m0 + 63) / 64) : 1, nb = G.b_mn ? (int)min((int64_t)(G.bn + 63) / 64, (G.n - n0 + 63) / 64) : 1;
+        const uint32_t bytes = (G.a_mn ? na * 8192 : 16384) + (G.b_mn ? nb * 8192 : G.b_box * 128);
+        const bool mn = isb ? G.b_mn : G.a_mn, mine = q < (isb ? nb : na);
+        const int64_t r0 = isb ? n0 : m0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const bool ok = mbar_wait(&sh.empty[R.stage], R.parity() ^ 1, &sh.abort, G.wait_ns, G.status, WAIT_PRODUCER_EMPTY);
+            if (!__all_sync(~0u, ok)) break;
+            uint64_t* bar = &sh.full[R.stage];
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (mine) {
+                uint8_t* to = ring + R.stage * G.stage_bytes + (isb ? 16384 : 0) + q * 8192;
+                if (mn)
+                    tma_load_2d(to, isb ? &M.b : &M.a, bar, (int)(r0 + 64 * q), 64 * kb);
+                else
+                    tma_load_2d(to, isb ? &M.b : &M.a, bar, 64 * kb, (int)r0);
+            }
+            R.issued |= 1u << R.stage;
+            R.next(G.stages);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(128, G.bn, G.a_mn, G.b_mn);
+            const uint32_t astep = G.a_mn ? 2048 : 32, bstep = G.b_mn ? 2048 : 32, alead = G.a_mn ? 8192 : 16, blead = G.b_mn ? 8192 : 16;
+            bool ok = true;
+            for (int kb = kb0; ok && kb < kb1; ++kb) {
+                ok = mbar_wait(&sh.full[R.stage], R.parity(), &sh.abort, G.wait_ns, G.status, WAIT_MMA_FULL);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t as = smem_u32(ring + R.stage * G.stage_bytes), bs = as + 16384;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_bf16(sh.tmem, sdesc(as + k * astep, alead, 1024, SWZ_128B), sdesc(bs + k * bstep, blead, 1024, SWZ_128B), idesc, kb > kb0 || k > 0);
+                umma_commit(&sh.empty[R.stage]);
+                R.next(G.stages);
+            }
+            if (ok) umma_commit(&sh.tfull[0]);
+        }
+    } else {
+        // all operands are read when the products are done, and their place is the sums'
+        const int q = warp & 3, turn = (warp - 2) >> 2;
+        if (mbar_wait(&sh.tfull[0], 0, &sh.abort, G.wait_ns, G.status, WAIT_EPI_TMEM_FULL)) {
+            tc_fence_after();
+            float4* to = reinterpret_cast<float4*>(ring) + 32 * q + lane;
+            for (int c = 16 * turn; c < G.bn; c += 32) {
+                uint32_t u[32];
+                tmem_ld16(sh.tmem + ((uint32_t)(32 * q) << 16) + c, u);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    to[((c + e) >> 2) * 128] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    // after a wait that gave up: copies and products in flight end before the CTA leaves
+    if (*(volatile int*)&sh.abort) {
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < kLinMostStages; ++k)
+                if (R.issued & (1u << k)) mbar_wait_timed(&sh.full[k], ((R.bits >> k) & 1) ^ 1, G.wait_ns);
+        } else if (threadIdx.x == 32) {
+            umma_commit(&sh.drain);
+            mbar_wait_timed(&sh.drain, 0, G.wait_ns);
+        }
+    }
+    cluster_sync();  // all CTAs' sums are there
+    const int quads = G.bn / 4, from = quads * rank / C, to = quads * (rank + 1) / C;
+    float4* mine = reinterpret_cast<float4*>(ring) + quads * 128;  // behind the sums: the CTA's own columns, row by row
+    if (warp >= 2) {
+        for (int f = threadIdx.x - 64; f < (to - from) * 128; f += 256) {
+            const int row = f & 127, c4 = from + (f >> 7);
+            float4 x[kMostSplit];
+#pragma unroll
+            for (int k = 0; k < kMostSplit; ++k) {
+                if (k >= C) continue;
+                const uint32_t at = remote(reinterpret_cast<const float4*>(ring) + c4 * 128 + row, k);
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w) : "r"(at));
+            }
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kMostSplit; ++k)
+                if (k < C) v[0] += x[k].x, v[1] += x[k].y, v[2] += x[k].z, v[3] += x[k].w;
+            if (SWAP)
+                finish_column<OP>(E, n0 + 4 * c4, (int)m0 + row, v);
+            else  // a row's quads, turned by the row so that both ways are without conflicts
+                mine[row * (to - from) + ((f >> 7) + row) % (to - from)] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (!SWAP) {
+            named_bar_sync(2, 256);
+            const int wide = to - from;
+            const int row = 16 * (warp - 2);
+            if (m0 + row < G.m)
+                for (int c = lane; c < 4 * wide; c += 32) {
+                    float v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = reinterpret_cast<const float*>(mine + (row + e) * wide + ((c >> 2) + row + e) % wide)[c & 3];
+                    finish_column<OP>(E, m0 + row, (int)n0 + 4 * from + c, v);
+                }
+        }
+    }
+    cluster_sync();  // and read
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 256);
+    }
+}
+
 // The tiles that were cut, from their parts in order: a block has 32 columns of so many rows that `ways` threads share the parts of
 // four values of a row; the sums go through shared memory to rows of 32 columns (SWAP: are columns of rows already).
 template <int OP, bool SWAP>
@@ -885,13 +1042,25 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         }
     } else {
         const int lane = threadIdx.x & 31;
-        for (int r = threadIdx.x >> 5; r < high; r += 8) {
-            const float* at = reinterpret_cast<const float*>(red + lane / 4 * high + r) + (lane & 3);
-            float v[1] = {0.f};
-            for (int w = 0; w < ways; ++w) v[0] += at[w * 8 * high * 4];
-            const int64_t i = (int64_t)mt * 128 * ctas + r0 + r;
-            if (i < G.m && c0 + lane < G.bn) finish_column<OP>(E, i, nt * G.bn + c0 + lane, v);
-        }
+        // a warp's rows are neighbours: four, or one where the parts are shared
+        auto rows = [&](auto count) {
+            constexpr int N = decltype(count)::value;
+            for (int r = N * (threadIdx.x >> 5); r < high; r += 8 * N) {
+                float v[N];
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float* at = reinterpret_cast<const float*>(red + lane / 4 * high + r + e) + (lane & 3);
+                    v[e] = 0.f;
+                    for (int w = 0; w < ways; ++w) v[e] += at[w * 8 * high * 4];
+                }
+                const int64_t i = (int64_t)mt * 128 * ctas + r0 + r;
+                if (i < G.m && c0 + lane < G.bn) finish_column<OP>(E, i, nt * G.bn + c0 + lane, v);
+            }
+        };
+        if (high == 32)
+            rows(std::integral_constant<int, 4>{});
+        else
+            rows(std::integral_constant<int, 1>{});
     }
     // db of the tile: 256 values, by the tile's first block
     if (OP == OP_WGRAD && E.db && (SWAP ? mt : nt) == 0 && block == 0) {
@@ -946,10 +1115,32 @@ cf_status run_linear(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, c
         return cudaGetLastError(), CF_ERR_CUDA;
     return CF_OK;
 }
+template <bool SWAP>
+cf_status run_split(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
+    auto kernel = linear_split_kernel<CF_LINEAR_OP, SWAP>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(P.g.tm * P.g.tn * P.g.split));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = kLinSmem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)P.g.split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, M, P.g, E) != cudaSuccess) return cudaGetLastError(), CF_ERR_CUDA;
+    return CF_OK;
+}
 }  // namespace
 
 template <>
 cf_status launch_linear<CF_LINEAR_OP>(const LaunchCtx& ctx, const LinPlan& P, const LinMaps& M, const LinEpi& E) {
+    if constexpr (CF_LINEAR_OP != OP_WGRAD)
+        if (P.g.split) return P.swap ? run_split<true>(ctx, P, M, E) : run_split<false>(ctx, P, M, E);
     auto run = [&](auto sums) {
         constexpr bool kSums = decltype(sums)::value;
         if (P.swap) return run_linear<false, true, true, kSums>(ctx, P, M, E);

@@ -131,7 +131,9 @@ def check_wgrad(cf, rng, rows, k, n, scale=1.0, xp=0, yp=0, bias=True, accumulat
 
 
 SIZES = [(1, 8, 8), (1, 1, 1), (2, 2048, 96), (8, 512, 2048), (33, 64, 40), (128, 64, 256), (129, 72, 264), (300, 32, 32), (257, 1000, 130),
-         (5, 3, 7), (640, 515, 77), (1000, 130, 33), (2000, 256, 512), (77, 4100, 520), (16, 4096, 1024), (64, 96, 4096), (4096, 16, 48)]
+         (5, 3, 7), (640, 515, 77), (1000, 130, 33), (2000, 256, 512), (77, 4100, 520), (16, 4096, 1024), (64, 96, 4096), (4096, 16, 48),
+         # tiles that clusters of two, four and eight share, more blocks than CTAs or as many, ends inside a tile
+         (20, 200, 1000), (100, 1030, 500), (200, 2000, 1000), (260, 700, 150), (500, 4000, 520), (1000, 640, 320), (3, 130, 40)]
 
 
 @pytest.mark.parametrize("rows,k,n", SIZES)
@@ -150,7 +152,7 @@ def test_backward_weight_sizes(cf, rows, k, n):
 
 
 # tiles of pairs, whole and cut, ends that fill neither half of a pair; many tiles of lone CTAs
-LARGE = [(1500, 3000, 1000), (5000, 520, 1290), (700, 9000, 400), (2048, 2048, 2048), (300, 20000, 272), (9000, 1032, 160), (50000, 64, 250),
+LARGE = [(40, 3000, 10000), (1500, 3000, 1000), (5000, 520, 1290), (700, 9000, 400), (2048, 2048, 2048), (300, 20000, 272), (9000, 1032, 160), (50000, 64, 250),
          (150, 5000, 2600)]
 
 
