@@ -24,12 +24,49 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const uint16_t* src, i
     }
 }
 
-__global__ void __launch_bounds__(256) linear_act_bwd_kernel(const void* dy, int f32, const uint16_t* pre, uint16_t* dz, int64_t rows, int n,
-                                                             int64_t pitch, int act, float slope, float scale) {
-    for (int64_t e = blockIdx.x * (int64_t)256 + threadIdx.x; e < rows * n; e += (int64_t)gridDim.x * 256) {
-        const int64_t i = e / n, o = i * pitch + (e - i * n);
-        const float d = f32 ? static_cast<const float*>(dy)[o] : bf16_bits_to_float(static_cast<const uint16_t*>(dy)[o]);
-        dz[o] = __bfloat16_as_ushort(__float2bfloat16_rn(scale * d * act_grad(act, slope, bf16_bits_to_float(pre[o]))));
+// dz = scale dy act'(pre), eight values of a row at a time (VEC: which begin at 16 bytes).  Memory bounds it.
+template <bool VEC>
+__global__ void __launch_bounds__(256) linear_act_bwd_kernel(const void* dy, const uint16_t* pre, uint16_t* dz, int64_t rows, int n, int64_t pitch,
+                                                             const __grid_constant__ LinEpi E) {
+    const int per = (n + 7) / 8;
+    for (int64_t e = blockIdx.x * (int64_t)256 + threadIdx.x; e < rows * per; e += (int64_t)gridDim.x * 256) {
+        const int64_t i = e / per;
+        const int j = (int)(e - i * per) * 8;
+        const int64_t o = i * pitch + j;
+        float d[8], z[8];
+        if (VEC) {
+            const uint4 q = *reinterpret_cast<const uint4*>(pre + o);
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) z[2 * x] = __uint_as_float(u[x] << 16), z[2 * x + 1] = __uint_as_float(u[x] & 0xFFFF0000u);
+            if (E.f32) {
+                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(dy) + o);
+                const float4 a = p[0], b = p[1];
+                d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+            } else {
+                const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dy) + o);
+                const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) d[2 * x] = __uint_as_float(w[x] << 16), d[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const bool in = j + x < n;
+                z[x] = in ? bf16_bits_to_float(pre[o + x]) : 0.f;
+                d[x] = !in ? 0.f : E.f32 ? static_cast<const float*>(dy)[o + x] : bf16_bits_to_float(static_cast<const uint16_t*>(dy)[o + x]);
+            }
+        }
+        times_grad(E, z, d);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) d[x] *= E.scale;
+        if (VEC) {
+            *reinterpret_cast<uint4*>(dz + o) = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7]));
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (j + x < n) dz[o + x] = __bfloat16_as_ushort(__float2bfloat16_rn(d[x]));
+        }
     }
 }
 
@@ -282,9 +319,11 @@ cf_status cf_linear_act_bwd(const cf_linear_desc* desc, const void* dy, const ui
     if (!dy || !pre || !dz || !aligned16(dy) || !aligned16(pre) || !aligned16(dz)) return CF_ERR_INVALID_ARG;
     LaunchCtx ctx;
     if (!cf_device_ctx(&ctx, stream)) return CF_ERR_CUDA;
-    const int64_t blocks = std::min<int64_t>((desc->rows * desc->n + 255) / 256, 8 * ctx.num_sms);
-    linear_act_bwd_kernel<<<(unsigned)blocks, 256, 0, ctx.stream>>>(dy, desc->dtype == CF_DT_F32, pre, dz, desc->rows, desc->n, y_pitch(desc),
-                                                                    desc->act, desc->slope, desc->scale);
+    LinEpi E{};
+    E.act = desc->act, E.f32 = desc->dtype == CF_DT_F32, E.slope = desc->slope, E.scale = desc->scale;
+    const int64_t pitch = y_pitch(desc), blocks = std::min<int64_t>(over(desc->rows * over(desc->n, 8), 256), 16 * ctx.num_sms);
+    auto kernel = desc->n % 8 == 0 && pitch % 8 == 0 ? linear_act_bwd_kernel<true> : linear_act_bwd_kernel<false>;
+    kernel<<<(unsigned)blocks, 256, 0, ctx.stream>>>(dy, pre, dz, desc->rows, desc->n, pitch, E);
     return status_of();
 }
 

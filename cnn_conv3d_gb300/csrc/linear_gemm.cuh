@@ -132,13 +132,6 @@ __device__ __forceinline__ uint64_t smooth_grad(int act, uint64_t z) {
     }
     return add2(e, t);
 }
-__device__ __forceinline__ float act_grad(int act, float slope, float z) {
-    if (act == CF_ACT_LRELU) return z > 0.f ? 1.f : slope;
-    float a, b;
-    apart(smooth_grad(act, two(z, z)), a, b);
-    return a;
-}
-
 // The activation of all, with one branch.
 template <int N>
 __device__ __forceinline__ void activate(const LinEpi& E, float (&v)[N]) {
