@@ -9,6 +9,7 @@
 //   dbeta_pre = D                                 (gate's factor inside the sum over the samples where each has its own)
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "cf_internal.h"
 #include "cf_ptx.cuh"
@@ -934,32 +935,36 @@ struct RnGrads {
     float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
 };
 
-// The sums of 32 columns over rows [0, count) of v [][4][c]; f says what a row counts (per sum): in warp 0.
+// The sums of 32 columns over rows [0, count) of v [][4][c], of the first two weighted by a row's weight: in warp 0.
+constexpr int kSumWarps = 32;
 template <typename W>
 __device__ __forceinline__ float4 column_sums(const float* v, int64_t count, int c, int j, float4 (*red)[32], W weight) {
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (j < c) {
 #pragma unroll 4
-        for (int64_t i = q; i < count; i += 8) {
+        for (int64_t i = q; i < count; i += kSumWarps) {
             const float* p = v + i * 4 * c + j;
             const float w = weight(i);
-            s.x = fmaf(w, p[0], s.x);
-            s.y = fmaf(w, p[c], s.y);
-            s.z += p[2 * (int64_t)c];
-            s.w += p[3 * (int64_t)c];
+            s.x = fmaf(w, __ldcg(p), s.x);
+            s.y = fmaf(w, __ldcg(p + c), s.y);
+            s.z += __ldcg(p + 2 * (int64_t)c);
+            s.w += __ldcg(p + 3 * (int64_t)c);
         }
     }
     red[q][lane] = s;
     __syncthreads();
     if (q == 0)
-        for (int i = 1; i < 8; ++i) s.x += red[i][lane].x, s.y += red[i][lane].y, s.z += red[i][lane].z, s.w += red[i][lane].w;
+        for (int i = 1; i < kSumWarps; ++i) s.x += red[i][lane].x, s.y += red[i][lane].y, s.z += red[i][lane].z, s.w += red[i][lane].w;
     return s;
 }
+// These launches begin under the end of the one before.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Each sample's sums from its chunks' (kept where vectors are shared between samples), and the gradients that are a sample's own.
-__global__ void __launch_bounds__(kThreads) rn_sample_kernel(const RnArgs A, const float* part, float* sums, const RnGrads G) {
-    __shared__ float4 red[8][32];
+__global__ void __launch_bounds__(32 * kSumWarps) rn_sample_kernel(const RnArgs A, const float* part, float* sums, const RnGrads G) {
+    __shared__ float4 red[kSumWarps][32];
+    wait_previous();
     const int j = blockIdx.y * 32 + (threadIdx.x & 31);
     const int64_t sample = blockIdx.x, c = A.c;
     const float4 s = column_sums(part + sample * A.chunks * 4 * c, A.chunks, A.c, j, red, [](int64_t) { return 1.f; });
@@ -983,8 +988,9 @@ __global__ void __launch_bounds__(kThreads) rn_sample_kernel(const RnArgs A, con
 }
 
 // The gradients of vectors that samples share.
-__global__ void __launch_bounds__(kThreads) rn_shared_kernel(const RnArgs A, const float* sums, const RnGrads G) {
-    __shared__ float4 red[8][32];
+__global__ void __launch_bounds__(32 * kSumWarps) rn_shared_kernel(const RnArgs A, const float* sums, const RnGrads G) {
+    __shared__ float4 red[kSumWarps][32];
+    wait_previous();
     const int j = blockIdx.x * 32 + (threadIdx.x & 31), c = A.c;
     const float4 s = column_sums(sums, A.samples, c, j, red, [&](int64_t i) { return A.gate_each ? at_or(A.gate, i * c + j, 1.f) : 1.f; });
     if (threadIdx.x >= 32 || j >= A.c) return;
@@ -1008,6 +1014,21 @@ constexpr int kPlanSms = 152;  // work is cut for so many SMs: workspaces are la
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 cf_status status_of() { return cudaGetLastError() == cudaSuccess ? CF_OK : CF_ERR_CUDA; }
+
+// A launch that begins under the end of the one before it in the stream.
+template <typename... P>
+cf_status launch_after(const LaunchCtx& ctx, dim3 grid, void (*kernel)(P...), const std::common_type_t<P>&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * kSumWarps);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? CF_OK : (cudaGetLastError(), CF_ERR_CUDA);
+}
 
 RnArgs args_of(const cf_residual_norm_desc* d) {
     RnArgs A{};
@@ -1044,11 +1065,11 @@ int per_sm(int T, int narrow) { return T <= 32 ? narrow : std::max(1, 512 / T); 
 // And of those with one: a block of 15 warps and one that copies, or of T threads.
 int ring_per_sm(int T) { return T <= 32 ? 1 : 512 / T; }
 
-// Whether rows go through the ring: at least two rounds of rows to a block.  Fewer are quicker without (64 x 256
+// Whether rows go through the ring: at least two rounds of rows to a block, and of a sample.  Fewer are quicker without (64 x 256
 // forward 2.2 us without, 3.4 with it), more with it (8 x 32^3 x 128 forward 74 without, 55 with it).
 bool ringed(const RnArgs& A, int T) {
     const int64_t step = T <= 32 ? kMostRows * (kRingWarps * 32 / T) : 2;
-    return T && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms;
+    return T && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms && A.per >= 2 * step;
 }
 // A's rows cut for the kernel that takes them.
 void cut_rows(RnArgs& A, int T, int narrow) {
@@ -1221,7 +1242,7 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
         const S *rs = static_cast<const S*>(r), *drs = static_cast<const S*>(dr);
         const F *fs = static_cast<const F*>(f), *dhs = static_cast<const F*>(dh);
         const float4* st4 = reinterpret_cast<const float4*>(stats);
-        const unsigned tiles = (A.c + 31) / 32;
+        const unsigned tiles = (A.c + 31) / 32;  // of the sums' columns
         if (const int T = threads_of(A.c); T && ringed(A, T)) {
             int shared;
             const int per_row = A.c * (int)((dh ? sizeof(S) + sizeof(F) : 0) + (dr ? sizeof(S) : 0) + (f ? sizeof(F) : 0)) + 16;
@@ -1246,10 +1267,9 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
                 A, fs, rs, st4, dhs, drs, L.means, static_cast<S*>(dx), static_cast<F*>(df), L.part);
         }
         if (const cf_status st = status_of(); st != CF_OK || !sums) return st;
-        rn_sample_kernel<<<dim3((unsigned)A.samples, tiles), kThreads, 0, ctx.stream>>>(A, L.part, L.sums, G);
-        if (const cf_status st = status_of(); st != CF_OK || A.samples == 1) return st;
-        rn_shared_kernel<<<tiles, kThreads, 0, ctx.stream>>>(A, L.sums, G);
-        return status_of();
+        if (const cf_status st = launch_after(ctx, dim3((unsigned)A.samples, tiles), rn_sample_kernel, A, L.part, L.sums, G); st != CF_OK || A.samples == 1)
+            return st;
+        return launch_after(ctx, dim3(tiles), rn_shared_kernel, A, L.sums, G);
     });
 }
 
