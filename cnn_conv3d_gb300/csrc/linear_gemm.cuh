@@ -7,8 +7,8 @@
 // or the two exchanged (SWAP) where that side is narrow: few rows in the forward and the backward data, so that the weights' rows
 // fill the 128 lanes of a tile and the rows are its columns, and a narrow k in the backward weight.
 //
-// A CTA is a TMA warp, an issuing thread and sixteen epilogue warps (eight, see below).  Operands come in stages of 64 of the contracted axis (128-byte
-// rows, swizzled); tiles are 128 rows by up to 256 columns, or 256 by 256 on a pair of CTAs with one instruction for both, each CTA
+// A CTA is a TMA warp, an issuing thread and sixteen epilogue warps (eight, see below).  Operands come in stages of 64 of the contracted
+// axis (128-byte rows, swizzled); tiles are 128 rows by up to 256 columns, or 256 by 256 on a pair of CTAs with one instruction for both, each CTA
 // fetching half of either side: then a stage costs 64 bytes of L2 a cycle and SM, where a lone CTA's would cost 96 of the about 70
 // that it gives.  The accumulator is double: the epilogue of a tile runs under the products of the next.
 //

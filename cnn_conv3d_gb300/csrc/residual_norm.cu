@@ -7,6 +7,12 @@
 // and four sums over rows are enough for all five vectors' gradients: A = sum dx fh, B = sum dx, C = sum dh rh, D = sum dh give
 //   dgate = scale (gamma_post A + beta_post B),  dgamma_post = scale gate A,  dbeta_post = scale gate B,  dgamma_pre = C,
 //   dbeta_pre = D                                 (gate's factor inside the sum over the samples where each has its own)
+//
+// Every tensor is read and written once, so memory is the bound, and what keeps from it is the latency of the rows' sums.  A row is held
+// by as many threads as give each eight of its values: part of a warp up to 256 values, a block up to 4096; longer rows are read again
+// for each sum.  Columns' sums stay in registers over a block's rows, whose chunks depend on the sizes alone: results do not change
+// from run to run.  bf16 RMS norms of 67M values, cold (8 us of it measuring), forward and backward: rows of 256 values 95 and 153 us
+// (5.6 and 5.3 TB/s), of 1024 107 and 198 us (5.0 and 4.1), of 4096 119 and 216 us (4.5 and 3.7), of 8192 178 and 400 us (3.0 and 2.0).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -497,9 +503,10 @@ __global__ void __launch_bounds__(WIDE ? kMostWide / 8 : kThreads, WIDE ? 1 : 2)
 
 // ------------------------------------------------------------------------------------------------ the same, fed by bulk copies
 // A block's rows are one stretch of memory of each tensor, copied into stages of `high` rows: what is on its way does not depend on what
-// registers hold.  Threads work on two rows at a time (ROWS), whose sums go together: a row's time is mostly the latency of those; but for the backward
-// of rows that all threads share, which has the registers for one.  Rows of warps have a warp that copies; where all threads have a row,
-// the first does, for the stage before, once all are through with it.
+// registers hold.  Threads work on two rows at a time (ROWS), whose sums go together: a row's time is mostly the latency of those; but for
+// the backward of rows that all threads share, which has the registers for one.  Rows of warps have a warp that copies; where all threads
+// have a row, the first does, for the stage before, once all are through with it.  A row's sums of one barrier instead of two (of dv with
+// the next row's of u) were slower: 302 us in place of 213 at 131072 x 512.
 // Bulk copies begin and end at multiples of 16 bytes: where rows do not, a stage's first row lies up to 15 bytes into its room, and what
 // is left of a tensor behind its last whole 16 bytes is copied value by value.
 constexpr int kRingWarps = 15;
@@ -1065,15 +1072,20 @@ int per_sm(int T, int narrow) { return T <= 32 ? narrow : std::max(1, 512 / T); 
 // And of those with one: a block of 15 warps and one that copies, or of T threads.
 int ring_per_sm(int T) { return T <= 32 ? 1 : 512 / T; }
 
-// Whether rows go through the ring: at least two rounds of rows to a block, and of a sample.  Fewer are quicker without (64 x 256
-// forward 2.2 us without, 3.4 with it), more with it (8 x 32^3 x 128 forward 74 without, 55 with it).
-bool ringed(const RnArgs& A, int T) {
+// Whether rows go through the ring: at least two rounds of rows to a block, and of a sample.  Fewer are quicker without (64 x 256,
+// warm, forward 2.4 us without and 3.9 with it, backward 5.8 and 8.1); at the bound both take the same (9120 x 256 forward 5.8 and 6.0,
+// backward 15.0 and 14.5); long ones, cold, are quicker with it (262144 x 256 forward 101 and 95, backward 183 and 153; 131072 x 512
+// forward 117 and 107; 65536 x 515 203 and 132, 351 and 226).  The backward of rows that all threads of a block share, in whole words of
+// eight, is not: its time is that of the block's sums (131072 x 512 195 us without and 213 with it, 16384 x 4096 218 and 220, of an fp32
+// stream 246 and 243; warm 1216 x 4096 23 and 27).
+bool ringed(const RnArgs& A, int T, bool backward) {
+    if (backward && T > 32 && A.c % 8 == 0) return false;
     const int64_t step = T <= 32 ? kMostRows * (kRingWarps * 32 / T) : 2;
     return T && A.rows >= 2 * step * ring_per_sm(T) * kPlanSms && A.per >= 2 * step;
 }
 // A's rows cut for the kernel that takes them.
-void cut_rows(RnArgs& A, int T, int narrow) {
-    if (ringed(A, T))
+void cut_rows(RnArgs& A, int T, int narrow, bool backward) {
+    if (ringed(A, T, backward))
         cut(A, (int64_t)kPlanSms * ring_per_sm(T), T <= 32 ? kRingWarps * 32 / T : 1);
     else
         cut(A, (int64_t)kPlanSms * per_sm(T, narrow), T <= 32 ? kThreads / T : 1);
@@ -1116,7 +1128,7 @@ RnArgs plan_bwd(const cf_residual_norm_desc* d) {
     if (A.rows == 0) return A;
     const int T = threads_of(A.c);
     if (T)
-        cut_rows(A, T, 2);
+        cut_rows(A, T, 2, true);
     else
         cut(A, std::max(1, kPlanSms * 4 * 256 / A.c), 8);
     return A;
@@ -1183,9 +1195,9 @@ cf_status cf_residual_norm_fwd(const cf_residual_norm_desc* desc, const void* x,
         const F* fs = static_cast<const F*>(f);
         float4* st4 = reinterpret_cast<float4*>(stats);
         if (const int T = threads_of(A.c); T) {
-            cut_rows(A, T, 3);
+            cut_rows(A, T, 3, false);
             const unsigned blocks = (unsigned)(A.samples * A.chunks);
-            if (ringed(A, T)) {
+            if (ringed(A, T, false)) {
                 int shared;
                 const RnRing R = ring_of(ctx, A, T, 2, A.c * (int)(sizeof(S) + (f ? sizeof(F) : 0)), shared);
                 auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_fwd_ring_kernel<S, F, false, 2, true> : rn_fwd_ring_kernel<S, F, true, 2, true>)
@@ -1243,12 +1255,13 @@ cf_status cf_residual_norm_bwd(const cf_residual_norm_desc* desc, const void* f,
         const F *fs = static_cast<const F*>(f), *dhs = static_cast<const F*>(dh);
         const float4* st4 = reinterpret_cast<const float4*>(stats);
         const unsigned tiles = (A.c + 31) / 32;  // of the sums' columns
-        if (const int T = threads_of(A.c); T && ringed(A, T)) {
+        if (const int T = threads_of(A.c); T && ringed(A, T, true)) {
             int shared;
             const int per_row = A.c * (int)((dh ? sizeof(S) + sizeof(F) : 0) + (dr ? sizeof(S) : 0) + (f ? sizeof(F) : 0)) + 16;
             const RnRing R = ring_of(ctx, A, T, T <= 32 ? 2 : 1, per_row, shared);
-            auto kernel = A.c % 8 == 0 ? (T <= 32 ? rn_bwd_ring_kernel<S, F, false, 2, true> : rn_bwd_ring_kernel<S, F, true, 1, true>)
-                                       : (T <= 32 ? rn_bwd_ring_kernel<S, F, false, 2, false> : rn_bwd_ring_kernel<S, F, true, 1, false>);
+            auto kernel = T > 32         ? rn_bwd_ring_kernel<S, F, true, 1, false>
+                          : A.c % 8 == 0 ? rn_bwd_ring_kernel<S, F, false, 2, true>
+                                         : rn_bwd_ring_kernel<S, F, false, 2, false>;
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared) != cudaSuccess) return status_of(), CF_ERR_CUDA;
             kernel<<<(unsigned)(A.samples * A.chunks), T <= 32 ? 32 * kRingWarps + 32 : T, shared, ctx.stream>>>(
                 A, T, R, fs, rs, st4, dhs, drs, static_cast<S*>(dx), static_cast<F*>(df), sums ? L.part : nullptr);
