@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
 
 // A tile to a cluster of two or four CTAs, which share the blocks of the contracted axis: each leaves its sums in its shared memory, four
 // columns of all 128 rows in turn, and of some of the columns adds all CTAs', in their order, and takes the epilogue.  8 x 2048 -> 2048
-// takes 6.8 us so, and 7.7 with parts in memory and a second launch (10.6 in clusters of eight, which are late to be placed);
+// takes 6.8 us so, and 7.7 with parts in memory and a second launch (10.6 in clusters of eight);
 // 128 x 4096 -> 4096 11.9 and 16.7; 200 x 4096 -> 4096 17.4 and 23.
 constexpr int kSplitThreads = 64 + 32 * 8;
 constexpr int kMostSplit = 4;

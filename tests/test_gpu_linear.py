@@ -132,7 +132,7 @@ def check_wgrad(cf, rng, rows, k, n, scale=1.0, xp=0, yp=0, bias=True, accumulat
 
 SIZES = [(1, 8, 8), (1, 1, 1), (2, 2048, 96), (8, 512, 2048), (33, 64, 40), (128, 64, 256), (129, 72, 264), (300, 32, 32), (257, 1000, 130),
          (5, 3, 7), (640, 515, 77), (1000, 130, 33), (2000, 256, 512), (77, 4100, 520), (16, 4096, 1024), (64, 96, 4096), (4096, 16, 48),
-         # tiles that clusters of two, four and eight share, more blocks than CTAs or as many, ends inside a tile
+         # tiles that clusters share, more blocks than CTAs or as many, ends inside a tile
          (20, 200, 1000), (100, 1030, 500), (200, 2000, 1000), (260, 700, 150), (500, 4000, 520), (1000, 640, 320), (3, 130, 40)]
 
 
