@@ -396,26 +396,29 @@ template <bool PAIR>
 __device__ __forceinline__ int parts_of(const LinGemm& G, const LinItem& s) {
     return PAIR || G.sub == 1 ? 1 : (int)min((int64_t)G.sub, (G.m - (int64_t)s.mt * 128 * G.sub + 127) / 128);
 }
-// The passes of an epilogue warp over the tiles that it finishes itself, in the order that it takes them.
-template <bool PAIR>
+// The passes of an epilogue warp over the tiles that it finishes itself, in the order that it takes them: of two sets, those whose
+// accumulator is the set's, by the rule of all other warps (a tile that takes sums turns the accumulators no further).
+template <int OP, bool SWAP, bool PAIR>
 struct LinPasses {
     LinWalk way;
     LinItem s;
-    int pass, part, c, local;  // pass of the tile: its 128 rows, and first column; the unit's tiles and parts so far
+    Accumulators A;
+    int pass, part, c;  // pass of the tile: its 128 rows, and first column
     bool more;
-    __device__ __forceinline__ LinPasses(const LinGemm& G, int unit, int set, int turn) : way(G, unit), pass(1 << 20), local(0), more(true) {
-        next(G, unit, set, turn);
+    __device__ __forceinline__ LinPasses(const LinGemm& G, const LinEpi& E, int unit, int set, int turn) : way(G, unit), pass(1 << 20), more(true) {
+        next(G, E, unit, set, turn);
     }
-    __device__ __forceinline__ void next(const LinGemm& G, int unit, int set, int turn) {
+    __device__ __forceinline__ void next(const LinGemm& G, const LinEpi& E, int unit, int set, int turn) {
         const int across = (G.bn + G.st.gw - 1) / G.st.gw;
         pass += G.st.turns;
         while (more && (pass >= 1 << 20 || pass >= across * parts_of<PAIR>(G, s))) {
-            bool mine;
-            do {
-                more = way.next(G, unit, s);
-                mine = s.slot < 0 && (G.st.sets == 1 || (local & 1) == set);
-                ++local;
-            } while (more && !mine);
+            bool mine = false;
+            while (!mine && (more = way.next(G, unit, s))) {
+                const bool sums = takes_sums<OP, SWAP>(E, s);
+                const int acc = A.next(sums);
+                mine = s.slot < 0 && (G.st.sets == 1 || acc == set);
+                A.used(acc, sums);
+            }
             pass = turn;
         }
         part = pass / across;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
         const uint32_t in_bytes = SWAP || !TMA ? 0 : (S.load_add ? S.out_bytes : 0) + (S.load_aux ? S.aux_bytes : 0);
         uint32_t done = 0, asked = 0;  // passes finished, and those whose loads were issued
         bool ok = set < S.sets;
-        LinPasses<PAIR> ahead(G, unit, set, turn);
+        LinPasses<OP, SWAP, PAIR> ahead(G, E, unit, set, turn);
         // the next pass's loads, once the present one's store has been read
         auto ask = [&]() {
             if (lane == 0) bulk_wait_read();
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                 if (S.load_aux) tma_load_2d(aux, &M.aux, &sh.in[warp - 2], col, row);
             }
             ++asked;
-            ahead.next(G, unit, set, turn);
+            ahead.next(G, E, unit, set, turn);
         };
         if (ok && !SWAP && TMA) ask();
         // the pass's bias, loaded before its products are there

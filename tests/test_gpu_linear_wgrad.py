@@ -1,0 +1,59 @@
+"""The backward weight of the products (cf_linear_wgrad) where its sums are taken in many pieces: by CTAs with several tiles each, and
+over many rows."""
+import numpy as np
+import pytest
+
+from gpu_util import guarded
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def cf():
+    from cnn_conv3d_gb300 import build
+    build.build()
+    from cnn_conv3d_gb300 import cfconv
+    return cfconv
+
+
+def call(cf, x, dz, dw, db, scale=1.0, accumulate=0):
+    (rows, k), n = x.shape, dz.shape[1]
+    d = cf.cf_linear_desc(rows, k, n, cf.CF_ACT_LRELU, 1.0, scale, cf.CF_DT_BF16, x.stride(0), dz.stride(0))
+    size = cf.cf_linear_workspace_size(d, cf.CF_LINEAR_WGRAD)
+    ws = torch.full((max(size, 16),), 0xA5, dtype=torch.uint8, device="cuda")
+    cf.cf_linear_wgrad(d, x, dz, dw, db, accumulate, ws, size)
+    torch.cuda.synchronize()
+    assert cf.cf_last_device_status() == cf.CF_OK
+
+
+def whole(g, shape, most):
+    """Whole numbers from -most to most."""
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda", dtype=torch.int32)
+
+
+# more tiles than CTAs or pairs take at once, of few rows: what is added comes ahead of the products (pairs with several tiles of which
+# some take the sums of dz, lone CTAs, tiles one across, ends inside a tile, rows that TMA does not take); the last: cut tiles
+SEVERAL = [(8, 16384, 2048), (512, 2048, 8192), (1000, 4096, 4096), (256, 1024, 4096), (1000, 136, 40000), (512, 4096, 4096), (256, 2048, 11008),
+           (300, 200, 20000), (40, 264, 30000), (1024, 8192, 8192), (70, 1001, 9000), (64, 20000, 136), (1100, 2056, 4100), (30000, 520, 264)]
+
+
+@pytest.mark.parametrize("rows,k,n", SEVERAL)
+@pytest.mark.parametrize("with_db", [True, False])
+@pytest.mark.parametrize("accumulate", [1, 0])
+def test_sums_of_whole_numbers_are_exact(cf, rows, k, n, with_db, accumulate):
+    """Products of whole numbers up to 3 stay below 2^24 over all rows, so that every fp32 sum holds them and no order or cut rounds; the
+    gradients that are there differ from value to value."""
+    g = torch.Generator("cuda").manual_seed(rows + k + n)
+    x, dz = whole(g, (rows, k), 3).to(BF), whole(g, (rows, n), 3).to(BF)
+    (dw, ok_w), (db, ok_b) = guarded((n, k), F32, fill=0.0), guarded((n,), F32, fill=0.0)
+    dw.copy_(whole(g, (n, k), 1000)), db.copy_(whole(g, (n,), 1000))
+    want_w, want_b = (0.5 * dz.double().T @ x.double(), 0.5 * dz.double().sum(0)) if not accumulate else \
+        (dw.double() + 0.5 * dz.double().T @ x.double(), db.double() + 0.5 * dz.double().sum(0))
+    left = db.clone()
+    call(cf, x, dz, dw, db if with_db else None, 0.5, accumulate)
+    ok_w(), ok_b()
+    assert torch.equal(dw.double(), want_w)
+    assert torch.equal(db.double(), want_b) if with_db else torch.equal(db, left)
