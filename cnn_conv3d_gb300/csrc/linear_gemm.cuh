@@ -16,6 +16,8 @@
 // the values' signs are mixed (weights of 2048 x 8192 from 16384 rows: 1.7e-5 off, where sums in fp32 that round are 1.4e-6).  Where the
 // result is fp32 they therefore sum 24 blocks of the axis at a time, and the epilogue warps, then eight with the registers for it, add
 // these sums up, rounding, under the next blocks' products (SUMS): 1.5e-6, and 393 us in place of 362; 16 blocks took 406, 32 390.
+// Bias gradients likewise, a thread or a lane to each: of rows whose sizes differ by e^3 each way 1.5e-5 and 1.8e-5 off (16384 rows of 4096,
+// 20000 of 38912) with one sum over all of a tile's rows, 5e-7 so, at the same times.
 //
 // Where there are fewer tiles than CTAs, a cluster may take each, its CTAs even shares of the contracted axis, whose sums they add up
 // through distributed shared memory, each CTA of some columns (linear_split_kernel).  Otherwise
@@ -582,9 +584,9 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                                 umma_bf16(dp, ad, bd, idesc, more);
                             if (OP == OP_WGRAD && sums) {
                                 if (PAIR)
-                                    umma_pair(d1, ad, one, idesc1, kb > s.kb0 || k > 0);
+                                    umma_pair(d1, ad, one, idesc1, more);
                                 else
-                                    umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, kb > s.kb0 || k > 0);
+                                    umma_bf16(d1, SWAP ? one : ad, SWAP ? bd : one, idesc1, more);
                             }
                         }
                         if (PAIR)
@@ -677,6 +679,31 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                 }
                 A.used(acc, sums);
             };
+            // SUMS: db of the tile, as the blocks' sums come: the thread's row's, or (SWAP, where all rows are alike) column `lane`'s of a
+            // group of 32 to each warp
+            float b = 0.f;
+            auto add_db = [&]() {
+                if (!SUMS || OP != OP_WGRAD || !sums || (!SWAP && turn != 0) || (SWAP && group_of(q) >= G.bn)) return;
+                uint32_t u[32];
+                if (SWAP) {
+                    uint32_t low = 0;
+#pragma unroll
+                    for (int h = 0; h < 32; h += 16) {
+                        tmem_ld16(tm1 + group_of(q) + h, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int o = 8; o; o >>= 1)
+#pragma unroll
+                            for (int e = 0; e < o; ++e) u[e] = lane & o ? u[e + o] : u[e];
+                        if (h == 0) low = u[0];
+                    }
+                    u[0] = lane & 16 ? u[0] : low;
+                } else {
+                    tmem_ld16(tm1, u);
+                    tmem_ld_wait();
+                }
+                b += __uint_as_float(u[0]);
+            };
             if (SUMS && s.kb1 - s.kb0 > G.seg) {
                 // all blocks' sums, the last written back to where the epilogue finds a tile's
                 uint64_t v[4][16];
@@ -686,6 +713,7 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                     for (int e = 0; e < 16; ++e) v[g][e] = 0;
                 for (int k0 = s.kb0; k0 < s.kb1; k0 += G.seg) {
                     if (!filled()) break;
+                    add_db();
                     const bool last = k0 + G.seg >= s.kb1;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -717,6 +745,8 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                 if (!ok) break;
             } else if (!filled()) {
                 break;
+            } else {
+                add_db();
             }
             if (SWAP || part) {
                 for (int k = 0;; ++k) {
@@ -737,7 +767,7 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                     } else if (i < G.m) {
                         finish_column<OP>(E, j0 + c, (int)i, v);
                     }
-                    if (OP == OP_WGRAD && SWAP && sums) {
+                    if (OP == OP_WGRAD && SWAP && !SUMS && sums) {
                         tmem_ld16(tm1 + c, u);
                         tmem_ld_wait();
                         if (r == 0) {
@@ -803,14 +833,26 @@ __global__ void __launch_bounds__(threads_of_linear(SUMS), 1) linear_gemm_kernel
                 if (!ok) break;
             }
             if (OP == OP_WGRAD && !SWAP && turn == 0 && sums) {
-                uint32_t u[32];
-                tmem_ld16(tm1, u);
-                tmem_ld_wait();
-                const float b = __uint_as_float(u[0]);
+                if (!SUMS) {
+                    uint32_t u[32];
+                    tmem_ld16(tm1, u);
+                    tmem_ld_wait();
+                    b = __uint_as_float(u[0]);
+                }
                 if (part)
                     G.dpart[(int64_t)s.slot * 256 + 128 * rank + r] = b;
                 else if (i < G.m)
                     E.db[i] = E.accumulate ? fmaf(E.scale, b, E.db[i]) : E.scale * b;
+            }
+            if (OP == OP_WGRAD && SWAP && SUMS && sums) {
+                const int c = group_of(q) + lane;
+                const int64_t j = j0 + c;
+                if (c < G.bn) {
+                    if (part)
+                        G.dpart[(int64_t)s.slot * 256 + c] = b;
+                    else if (j < G.n)
+                        E.db[j] = E.accumulate ? fmaf(E.scale, b, E.db[j]) : E.scale * b;
+                }
             }
             emptied();
         }

@@ -57,3 +57,25 @@ def test_sums_of_whole_numbers_are_exact(cf, rows, k, n, with_db, accumulate):
     ok_w(), ok_b()
     assert torch.equal(dw.double(), want_w)
     assert torch.equal(db.double(), want_b) if with_db else torch.equal(db, left)
+
+
+# tiles of pairs, whole and cut, of lone CTAs with rows that TMA takes and does not, sides exchanged, cut and whole
+@pytest.mark.parametrize("rows,k,n", [(16384, 4096, 4096), (16384, 2048, 2048), (9000, 1040, 4100), (16384, 200, 136), (100000, 64, 4096),
+                                      (20000, 128, 38912), (200000, 72, 1000)])
+def test_bias_sums_keep_fp32s_precision(cf, rows, k, n):
+    """Sums of dz whose rows differ in size by e^3 each way, with a mean of their own.  The tensor cores cut sums off, on average by 2^-24 of
+    them, at each of at most 96 steps of 16 rows before they are added up in fp32 that rounds, once for each 1536 rows and a few times where
+    a tile is cut; on average a sum is at most 0.7 of its end on the way: (96 + rows / 1536 + 8) 0.7 2^-24 of the result."""
+    g = torch.Generator("cuda").manual_seed(rows + k + n)
+    size = torch.exp(6 * torch.rand((rows, 1), generator=g, device="cuda") - 3)
+    dz = ((torch.randn((rows, n), generator=g, device="cuda") + 0.25) * size).to(BF)
+    x = torch.randn((rows, k), generator=g, device="cuda").to(BF)
+    dw, db = torch.empty((n, k), device="cuda"), torch.empty(n, device="cuda")
+    call(cf, x, dz, dw, db)
+    want = sum(dz[i:i + 8192].double().sum(0) for i in range(0, rows, 8192))
+    error = float((db.double() - want).norm() / want.norm())
+    assert error <= (96 + rows / 1536 + 8) * 0.7 * 2.0 ** -24, f"{error:.2e}"
+    # and added to what is there, with the same bits before the addition
+    again = torch.full_like(db, 3.0)
+    call(cf, x, dz, dw, again, 1.0, 1)
+    assert torch.equal(again, db + 3.0)
