@@ -565,6 +565,7 @@ struct RingFill {
                 *reinterpret_cast<uint16_t*>(dst + (b - low)) = *reinterpret_cast<const uint16_t*>(at + b);
         }
         const uint32_t bytes = __reduce_add_sync(~0u, (uint32_t)(high - low));
+        __syncwarp();  // the arrival announces all lanes' values: a reduction orders no memory
         if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&sh.full[stage], bytes);
         __syncwarp();
         if (high > low) bulk_load(dst, at + low, (uint32_t)(high - low), &sh.full[stage]);
