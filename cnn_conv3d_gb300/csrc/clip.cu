@@ -164,7 +164,7 @@ __device__ __forceinline__ float2 join(const double* part, int parts, float max_
     if (threadIdx.x == 0) red[0] = s;
     __syncthreads();
     const float norm = (float)sqrt(red[0]);
-    const float f = max_norm / (norm + kClipEps);
+    const float f = isinf(norm) ? 0.f : max_norm / (norm + kClipEps);  // also where max_norm is infinite
     return make_float2(norm, f < 1.f || f != f ? f : 1.f);
 }
 
