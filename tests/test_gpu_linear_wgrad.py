@@ -38,9 +38,12 @@ def whole(g, shape, most):
 # some take the sums of dz, lone CTAs, tiles one across, ends inside a tile, rows that TMA does not take); the last: cut tiles
 SEVERAL = [(8, 16384, 2048), (512, 2048, 8192), (1000, 4096, 4096), (256, 1024, 4096), (1000, 136, 40000), (512, 4096, 4096), (256, 2048, 11008),
            (300, 200, 20000), (40, 264, 30000), (1024, 8192, 8192), (70, 1001, 9000), (64, 20000, 136), (1100, 2056, 4100), (30000, 520, 264)]
+# and long sums: cut and whole tiles of pairs and lone CTAs in segments, sides exchanged, rows that TMA does not take
+LONG = [(16384, 2048, 2048), (9000, 4096, 4096), (9000, 1041, 4100), (100000, 64, 4096), (20000, 128, 38912), (200000, 64, 72), (50001, 40, 24),
+        (200003, 33, 300)]
 
 
-@pytest.mark.parametrize("rows,k,n", SEVERAL)
+@pytest.mark.parametrize("rows,k,n", SEVERAL + LONG)
 @pytest.mark.parametrize("with_db", [True, False])
 @pytest.mark.parametrize("accumulate", [1, 0])
 def test_sums_of_whole_numbers_are_exact(cf, rows, k, n, with_db, accumulate):
