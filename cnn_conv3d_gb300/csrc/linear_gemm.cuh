@@ -404,23 +404,22 @@ template <int OP, bool SWAP, bool PAIR>
 struct LinPasses {
     LinWalk way;
     LinItem s;
-    Accumulators A;
-    int pass, part, c;  // pass of the tile: its 128 rows, and first column
+    int pass, part, c, local;  // pass of the tile: its 128 rows, and first column; the unit's tiles so far that turned the accumulators
     bool more;
-    __device__ __forceinline__ LinPasses(const LinGemm& G, const LinEpi& E, int unit, int set, int turn) : way(G, unit), pass(1 << 20), more(true) {
+    __device__ __forceinline__ LinPasses(const LinGemm& G, const LinEpi& E, int unit, int set, int turn) : way(G, unit), pass(1 << 20), local(0), more(true) {
         next(G, E, unit, set, turn);
     }
     __device__ __forceinline__ void next(const LinGemm& G, const LinEpi& E, int unit, int set, int turn) {
         const int across = (G.bn + G.st.gw - 1) / G.st.gw;
         pass += G.st.turns;
         while (more && (pass >= 1 << 20 || pass >= across * parts_of<PAIR>(G, s))) {
-            bool mine = false;
-            while (!mine && (more = way.next(G, unit, s))) {
+            bool mine;
+            do {
+                more = way.next(G, unit, s);
                 const bool sums = takes_sums<OP, SWAP>(E, s);
-                const int acc = A.next(sums);
-                mine = s.slot < 0 && (G.st.sets == 1 || acc == set);
-                A.used(acc, sums);
-            }
+                mine = s.slot < 0 && (G.st.sets == 1 || (sums ? 0 : local & 1) == set);  // Accumulators::next
+                if (!sums) ++local;
+            } while (more && !mine);
             pass = turn;
         }
         part = pass / across;
